@@ -187,8 +187,9 @@ def _to_eight(values, at_least_one):
     """Blocks of values as e4m3 numbers and the scale of each block."""
     top = values.abs().amax(1, keepdim=True)
     used = ~(top < 2.0 ** -96)
-    scale = torch.where(used, top / 448.0, 0.0)
-    inverse = torch.where(used, 448.0 / top, 0.0)
+    most = torch.full_like(top, 448.0)  # a tensor: torch divides by, or into, a number through a reciprocal
+    scale = torch.where(used, top / most, 0.0)
+    inverse = torch.where(used, most / top, 0.0)
     code = (values * inverse).to(torch.float8_e4m3fn)
     if at_least_one:
         code = torch.where((values > 0) & (code.float() == 0), 2.0 ** -9, code.float()).to(torch.float8_e4m3fn)
@@ -221,8 +222,7 @@ def _tensor_inputs(case, seed):
 
 def prepare(case, seed):
     op = case["op"]
-    make = _norm_inputs if op.startswith("norm") else _recurrence_inputs if op.startswith("recurrence") else _tensor_inputs
-    s = make(case, seed)
+    s = {"norm": _norm_inputs, "recurrence": _recurrence_inputs}.get(op.split("_")[0], _tensor_inputs)(case, seed)
     s["case"] = case
     if own:
         s["plan"] = _plan(s)
