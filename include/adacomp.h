@@ -350,6 +350,154 @@ adacomp_status adacomp_materialize(adacomp_layer_t h, float* residue, void* ws, 
 adacomp_status adacomp_materialize_group(adacomp_layer_t h, float* const* residue, void* ws, size_t ws_bytes,
                                          cudaStream_t stream);
 
+/* ------------------------------------------------------------------------------
+ * Training operators around the compressor: what makes the gradients that are
+ * compressed (layer norm, a gated linear recurrence) and what is done with the
+ * decoded ones (their common norm, an AdamW step over all tensors). The pages name
+ * the nets and the optimisers (Claims > Application
+ * #r629-conv-40x-and-fc-lstm-200x-compression-across-optimizers) without giving these
+ * operators; they are read as defined below.
+ *
+ * The conventions above hold, with these differences: tensors of layer norm and the
+ * recurrence are strided (strides count elements; the last axis is contiguous) and
+ * aligned to their element type only (ADACOMP_ERR_ALIGNMENT otherwise); aligned to
+ * 16 bytes, with strides that keep every row so, they are read and written faster.
+ * Outputs may not overlap inputs or each other unless a call says so. Sums, statistics
+ * and states are fp32 or wider; results are rounded to the output's type once. Calls
+ * are deterministic. Non-finite inputs reach only the results that depend on them.
+ * A handle holds sizes and types only and may be used by several host threads.
+ * ------------------------------------------------------------------------------ */
+
+/* Layer norm over rows of dim elements (dim >= 1) of type x_dtype, with a weight and
+ * a bias of type w_dtype (both dtypes ADACOMP_F32 or ADACOMP_BF16):
+ *     mean = sum(x) / dim,  var = sum((x - mean)^2) / dim,  rstd = 1 / sqrt(var + eps),
+ *     y = (x - mean) * rstd * w + b.
+ * eps >= 0 and finite. Host only. */
+typedef struct adacomp_layer_norm* adacomp_layer_norm_t;
+adacomp_status adacomp_layer_norm_init(adacomp_layer_norm_t* out, int64_t dim, adacomp_dtype x_dtype,
+                                       adacomp_dtype w_dtype, float eps);
+
+/* y = norm of each of `rows` rows (0 does nothing). w and b are w_dtype[dim], b may be
+ * NULL (no bias). mean and rstd, fp32[rows] each, are what the backward pass needs;
+ * either may be NULL. y may be x itself with the same stride. x_stride >= 0 (0: one row
+ * read for all), y_stride >= dim unless rows < 2. */
+adacomp_status adacomp_layer_norm_forward(adacomp_layer_norm_t h, int64_t rows, const void* x, int64_t x_stride,
+                                          const void* w, const void* b, void* y, int64_t y_stride, float* mean,
+                                          float* rstd, cudaStream_t stream);
+
+/* Workspace bytes of a backward pass over `rows` rows (the partial sums of dw and db;
+ * needs no initialisation). */
+size_t adacomp_layer_norm_backward_ws_bytes(adacomp_layer_norm_t h, int64_t rows);
+
+/* From dy and the forward pass's x, mean and rstd, with xh = (x - mean) * rstd and g = dy * w:
+ *     dx = rstd * (g - sum(g)/dim - xh * sum(g * xh)/dim),
+ *     dw = sum over rows of dy * xh,   db = sum over rows of dy.
+ * dw and db are w_dtype[dim] and are overwritten (zeros for 0 rows); db may be NULL. dx
+ * may be dy or x itself with the same stride. ws: 16-byte aligned, of at least
+ * adacomp_layer_norm_backward_ws_bytes(h, rows) bytes. */
+adacomp_status adacomp_layer_norm_backward(adacomp_layer_norm_t h, int64_t rows, const void* dy, int64_t dy_stride,
+                                           const void* x, int64_t x_stride, const void* w, const float* mean,
+                                           const float* rstd, void* dx, int64_t dx_stride, void* dw, void* db,
+                                           void* ws, size_t ws_bytes, cudaStream_t stream);
+void adacomp_layer_norm_free(adacomp_layer_norm_t h);
+
+/* A gated linear recurrence over `channels` independent channels (>= 1) of sequences
+ * [batch, steps, channels] in `dtype`: with the gate a_t = 1 / (1 + exp(-z_t)),
+ *     h_t = a_t * h_{t-1} + (1 - a_t) * x_t,   y_t = h_t,   t = 0 .. length-1.
+ * The state is fp32 throughout; y is it rounded once. steps = 1 is the form for one new
+ * token. Host only. */
+typedef struct adacomp_recurrence* adacomp_recurrence_t;
+adacomp_status adacomp_recurrence_init(adacomp_recurrence_t* out, int64_t channels, adacomp_dtype dtype);
+
+/* Bytes of the fp32 states that a forward pass keeps for the backward pass: one every
+ * ADACOMP_RECURRENCE_CHUNK steps, [batch][ceil(steps / chunk)][channels]. */
+#define ADACOMP_RECURRENCE_CHUNK 128
+size_t adacomp_recurrence_carry_bytes(adacomp_recurrence_t h, int64_t batch, int64_t steps);
+
+/* The forward pass. z, x and y each have a stride between sequences and one between
+ * steps (z and x may be the two halves of one buffer).
+ *   h0       device fp32[batch][channels], the state before the first step; NULL: zeros
+ *   lengths  device int32[batch], each sequence's steps, clamped to 0..steps; NULL: all
+ *            of them. z and x past the length are not read (they may hold anything), and
+ *            y is zero there.
+ *   h_last   device fp32[batch][channels], the state after the last step (h0 for a
+ *            sequence without steps); may be NULL, may be h0 itself
+ *   carry    as adacomp_recurrence_carry_bytes; NULL when no backward pass follows
+ * batch = 0 does nothing; steps = 0 copies the state. */
+adacomp_status adacomp_recurrence_forward(adacomp_recurrence_t h, int64_t batch, int64_t steps, const void* z,
+                                          int64_t z_batch, int64_t z_step, const void* x, int64_t x_batch,
+                                          int64_t x_step, const float* h0, const int32_t* lengths, void* y,
+                                          int64_t y_batch, int64_t y_step, float* h_last, float* carry,
+                                          cudaStream_t stream);
+
+/* The backward pass, from the gradients dy of y and dh_last of h_last (NULL: zeros), the
+ * forward pass's inputs and its carry. With G_t = dy_t + a_{t+1} * G_{t+1} (dh_last in
+ * place of the last product):
+ *     dx_t = (1 - a_t) * G_t,  dz_t = a_t * (1 - a_t) * (h_{t-1} - x_t) * G_t,
+ *     dh0 = a_0 * G_0.
+ * h_{t-1} is computed again in fp32 from the carry. dz and dx are zero past a sequence's
+ * length, where dy is not read; dh0 (fp32[batch][channels]) may be NULL or dh_last itself.
+ * z, x, dz and dx: a stride pair each, as in the forward pass. */
+adacomp_status adacomp_recurrence_backward(adacomp_recurrence_t h, int64_t batch, int64_t steps, const void* z,
+                                           int64_t z_batch, int64_t z_step, const void* x, int64_t x_batch,
+                                           int64_t x_step, const void* dy, int64_t dy_batch, int64_t dy_step,
+                                           const float* carry, const int32_t* lengths, const float* dh_last,
+                                           void* dz, int64_t dz_batch, int64_t dz_step, void* dx, int64_t dx_batch,
+                                           int64_t dx_step, float* dh0, cudaStream_t stream);
+void adacomp_recurrence_free(adacomp_recurrence_t h);
+
+/* AdamW over many tensors at once, and the norm of their gradients. Tensor i has n[i]
+ * elements (>= 1), weights of w_dtype[i], gradients of g_dtype[i] (ADACOMP_F32 or
+ * ADACOMP_BF16) and a decoupled weight decay weight_decay[i] (the array may be NULL: none
+ * decays). state_bits is 32 (m and v are fp32[n]) or 8: m and the root of v are then
+ * e4m3[n] numbers, each block of ADACOMP_ADAMW_BLOCK elements with an fp32 scale, so that
+ * the block's largest magnitude is 448 * scale. num_tensors is 1..ADACOMP_MAX_TENSORS.
+ * norm_ws_bytes (may be NULL) receives the workspace size of adacomp_grad_norm. Host only. */
+typedef struct adacomp_adamw* adacomp_adamw_t;
+#define ADACOMP_ADAMW_BLOCK 256
+#define ADACOMP_MAX_TENSORS 65536
+adacomp_status adacomp_adamw_init(adacomp_adamw_t* out, int32_t num_tensors, const int64_t* n,
+                                  const int32_t* w_dtype, const int32_t* g_dtype, const float* weight_decay,
+                                  int32_t state_bits, size_t* norm_ws_bytes);
+
+/* norm = grad_scale * sqrt(sum of the squares of all gradients), and the coefficient that
+ * adacomp_adamw_step multiplies the gradients by:
+ *     result[0] = norm,
+ *     result[1] = grad_scale * min(1, max_norm / (norm + 1e-6))   (grad_scale if max_norm <= 0),
+ * or NaN in result[1] when the norm is not finite. Squares whose fp32 sums would overflow
+ * or vanish are summed in fp64. grad is a host array of num_tensors device pointers,
+ * 16-byte aligned; result is device fp32[2]; ws is 16-byte aligned and zero-filled before
+ * its first use (every call leaves it ready for the next). grad_scale must be finite and
+ * positive. */
+adacomp_status adacomp_grad_norm(adacomp_adamw_t h, const void* const* grad, float grad_scale, float max_norm,
+                                 float* result, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* One AdamW step. With c = *coefficient (or grad_scale where that is NULL), every operation
+ * fp32, rounded once, without fused multiply-adds:
+ *     g = c * g_j,  m = beta1 * m + (1 - beta1) * g,  v = beta2 * v + (1 - beta2) * (g * g),
+ *     u = sqrt(v),
+ *     w = fl32(1 - lr * weight_decay) * w
+ *         - fl32(lr / bias_correction1) * (m / (u * fl32(1 / sqrt(bias_correction2)) + eps)).
+ * The three constants are formed in fp64 and rounded once. With 8-bit states m and v enter
+ * as (e4m3 * scale) and (e4m3 * scale)^2, and leave as the block's new scale = max/448 and
+ * the e4m3 nearest to value * (448/max) (to even; a positive u never becomes 0 but the
+ * smallest e4m3; a block whose max is below 2^-96 becomes zeros with scale 0).
+ *   weight, grad, m, v   host arrays of num_tensors device pointers, 16-byte aligned;
+ *                        weight, m and v are in/out. State starts as zeros.
+ *   m_scale, v_scale     8-bit states: device fp32[ceil(n/256)] per tensor; otherwise NULL
+ *   copy                 NULL, or per tensor a bf16[n] buffer that receives the new weight
+ *                        rounded (for weights held in fp32 next to a bf16 model), 16-byte
+ *                        aligned, or NULL for none
+ *   coefficient          device fp32 (e.g. result + 1 of adacomp_grad_norm) or NULL. When it
+ *                        is not finite the call leaves weights, states and copies as they are.
+ * beta1, beta2 in [0, 1), eps > 0 and bias corrections > 0, or ADACOMP_ERR_INVALID_ARG. */
+adacomp_status adacomp_adamw_step(adacomp_adamw_t h, void* const* weight, const void* const* grad, void* const* m,
+                                  void* const* v, float* const* m_scale, float* const* v_scale, void* const* copy,
+                                  float lr, float beta1, float beta2, float eps, float bias_correction1,
+                                  float bias_correction2, float grad_scale, const float* coefficient,
+                                  cudaStream_t stream);
+void adacomp_adamw_free(adacomp_adamw_t h);
+
 /* Releases the handle. adacomp_free(NULL) does nothing. */
 void adacomp_free(adacomp_layer_t h);
 

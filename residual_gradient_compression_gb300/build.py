@@ -1,6 +1,6 @@
 """Builds libadacomp.so in-tree for GB300 (sm_103a) with nvcc.
 
-One nvcc invocation compiles the three translation units in parallel; the result is
+One nvcc invocation compiles the translation units in parallel; the result is
 placed next to this file and loaded by the package's ctypes binding. With
 ADACOMP_DEBUG_CHECKS=1 in the environment, the build and the binding use the debug
 library instead, libadacomp_debug.so beside it, built with -DADACOMP_DEBUG_CHECKS:
@@ -52,7 +52,7 @@ def up_to_date(debug: bool | None = None) -> bool:
 def command(out: str, debug: bool = False, verbose: bool = False) -> list:
     nvcc = os.environ.get("NVCC", "nvcc")
     cmd = [nvcc, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "--threads", "4", *(["-DADACOMP_DEBUG_CHECKS"] if debug else []),
+           "--threads", "8", *(["-DADACOMP_DEBUG_CHECKS"] if debug else []),
            "-I", os.path.join(ROOT, "include"), "-o", out, *sources()]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

@@ -1,0 +1,437 @@
+// The norm of many gradients and an AdamW step over many tensors, with the moments in
+// 32 or in 8 bits: kernels and C entry points (adacomp.h).
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "train_common.cuh"
+
+namespace adacomp {
+namespace {
+
+constexpr int kAwThreads = 256;
+constexpr int kAwWarps = kAwThreads / 32;
+constexpr int kAwBlock = ADACOMP_ADAMW_BLOCK;      // elements per scale, and per warp and turn
+constexpr int kAwTile = kAwWarps * kAwBlock;       // elements per CTA
+constexpr int kAwTensors = 400;                    // tensors per launch (a by-value kernel parameter)
+constexpr int kNormTensors = 1300;
+constexpr int kNormGrid = 608;                     // CTAs per launch at most: partial sums, in an order of their own
+
+struct AwTensor {
+    void *w, *m, *v, *copy;
+    const void* g;
+    float *ms, *vs;
+    int64_t n;
+    uint32_t tile_begin;
+    float decay;  // 1 - lr * weight_decay
+};
+
+struct AwTable {
+    AwTensor t[kAwTensors];
+    int32_t count;
+    float beta1, beta2, rest1, rest2, step, root, eps, scale;
+    const float* coefficient;
+};
+static_assert(sizeof(AwTable) <= 32764, "kernel parameters");
+
+struct NormTensor {
+    const void* g;
+    int64_t n;
+    uint32_t tile_begin;
+};
+
+struct NormTable {
+    NormTensor t[kNormTensors];
+    int32_t count;
+    uint32_t tiles;        // of this launch
+    uint32_t first_part;   // where its partial sums start
+    uint32_t all_parts;    // partial sums of all launches of the call
+    float scale, max_norm;
+    float* result;
+    uint32_t* ticket;
+    double* part;
+};
+static_assert(sizeof(NormTable) <= 32764, "kernel parameters");
+
+// The last tensor whose first tile is at or before `tile`.
+template <typename Table> __device__ __forceinline__ int owner_of(const Table& tab, uint32_t tile)
+{
+    int lo = 0, hi = tab.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.t[mid].tile_begin <= tile) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------- e4m3
+__device__ __forceinline__ uint32_t to_e4m3(float v)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
+    return r & 0xffu;
+}
+
+__device__ __forceinline__ float from_e4m3(uint32_t c)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+    float f;
+    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.f32.f16 %0, lo; }" : "=f"(f) : "r"(h));
+    return f;
+}
+
+struct Scales {
+    float scale, inverse;
+};
+
+// The scale of a block whose largest magnitude is `top`, given as its bits (NaN is the
+// largest of all). Below 2^-96, where 448 / top would come near overflow, there is none.
+__device__ __forceinline__ Scales scales_of(uint32_t bits)
+{
+    const float top = __uint_as_float(bits);
+    Scales s = {0.0f, 0.0f};
+    if (!(top < 0x1p-96f)) {
+        s.scale = __fdiv_rn(top, 448.0f);
+        s.inverse = __fdiv_rn(448.0f, top);
+    }
+    return s;
+}
+
+// ---------------------------------------------------------------- step
+// One warp per block of 256 elements, a tile of eight blocks per CTA.
+template <typename W, typename G, bool kEight>
+__global__ void __launch_bounds__(kAwThreads) adamw_kernel(const __grid_constant__ AwTable tab)
+{
+    ptx::griddep_wait();
+    const float c = tab.coefficient ? *tab.coefficient : tab.scale;
+    if (!isfinite(c)) return;
+    const AwTensor& t = tab.t[owner_of(tab, blockIdx.x)];
+    const int lane = threadIdx.x & 31;
+    const int64_t block = (int64_t)(blockIdx.x - t.tile_begin) * kAwWarps + (threadIdx.x >> 5);
+    const int64_t first = block * kAwBlock;
+    if (first >= t.n) return;
+    W* w = static_cast<W*>(t.w);
+    const G* g = static_cast<const G*>(t.g);
+    bf16* copy = static_cast<bf16*>(t.copy);
+    float mv[kAwBlock / 32], uv[kAwBlock / 32];
+    uint32_t mtop = 0, utop = 0;
+    float ms = 0.0f, us = 0.0f;
+    if (kEight) {
+        ms = t.ms[block];
+        us = t.vs[block];
+    }
+#pragma unroll
+    for (int k = 0; k < kAwBlock / 32; ++k) {
+        const int64_t i = first + k * 32 + lane;
+        mv[k] = uv[k] = 0.0f;
+        if (i >= t.n) continue;
+        float m, v;
+        if (kEight) {
+            m = __fmul_rn(from_e4m3(static_cast<uint8_t*>(t.m)[i]), ms);
+            const float u = __fmul_rn(from_e4m3(static_cast<uint8_t*>(t.v)[i]), us);
+            v = __fmul_rn(u, u);
+        } else {
+            m = static_cast<float*>(t.m)[i];
+            v = static_cast<float*>(t.v)[i];
+        }
+        const float d = __fmul_rn(c, to_f32(g[i]));
+        m = __fadd_rn(__fmul_rn(tab.beta1, m), __fmul_rn(tab.rest1, d));
+        v = __fadd_rn(__fmul_rn(tab.beta2, v), __fmul_rn(tab.rest2, __fmul_rn(d, d)));
+        const float u = __fsqrt_rn(v);
+        const float q = __fdiv_rn(m, __fadd_rn(__fmul_rn(u, tab.root), tab.eps));
+        const float x = __fsub_rn(__fmul_rn(t.decay, to_f32(w[i])), __fmul_rn(tab.step, q));
+        w[i] = from_f32<W>(x);
+        if (copy) copy[i] = from_f32<bf16>(x);
+        if (kEight) {
+            mv[k] = m;
+            uv[k] = u;
+            mtop = max(mtop, __float_as_uint(m) & 0x7fffffffu);
+            utop = max(utop, __float_as_uint(u) & 0x7fffffffu);
+        } else {
+            static_cast<float*>(t.m)[i] = m;
+            static_cast<float*>(t.v)[i] = v;
+        }
+    }
+    if (!kEight) return;
+    const Scales a = scales_of(__reduce_max_sync(0xffffffffu, mtop));
+    const Scales b = scales_of(__reduce_max_sync(0xffffffffu, utop));
+#pragma unroll
+    for (int k = 0; k < kAwBlock / 32; ++k) {
+        const int64_t i = first + k * 32 + lane;
+        if (i >= t.n) continue;
+        static_cast<uint8_t*>(t.m)[i] = (uint8_t)to_e4m3(__fmul_rn(mv[k], a.inverse));
+        const uint32_t r = to_e4m3(__fmul_rn(uv[k], b.inverse));
+        static_cast<uint8_t*>(t.v)[i] = (uint8_t)(r == 0 && uv[k] > 0.0f ? 1u : r);
+    }
+    if (lane == 0) {
+        t.ms[block] = a.scale;
+        t.vs[block] = b.scale;
+    }
+}
+
+// ---------------------------------------------------------------- norm
+__device__ __forceinline__ double block_sum(double v, double* shared)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double s = 0.0;
+    for (int i = 0; i < kAwWarps; ++i) s += shared[i];
+    return s;
+}
+
+// A CTA sums its tiles and leaves one fp64 partial sum; the last CTA of the call adds
+// the partial sums in their order.
+template <typename G>
+__global__ void __launch_bounds__(kAwThreads) grad_norm_kernel(const __grid_constant__ NormTable tab)
+{
+    ptx::griddep_wait();
+    __shared__ double shared[kAwWarps];
+    __shared__ bool last;
+    double sum = 0.0;
+    for (uint32_t tile = blockIdx.x; tile < tab.tiles; tile += gridDim.x) {
+        const NormTensor& t = tab.t[owner_of(tab, tile)];
+        const G* g = static_cast<const G*>(t.g);
+        const int64_t first = (int64_t)(tile - t.tile_begin) * kAwTile + threadIdx.x;
+        float s = 0.0f;
+        uint32_t any = 0;
+#pragma unroll
+        for (int k = 0; k < kAwTile / kAwThreads; ++k) {
+            const int64_t i = first + k * kAwThreads;
+            const float v = i < t.n ? to_f32(g[i]) : 0.0f;
+            s = fmaf(v, v, s);
+            any |= __float_as_uint(v) << 1;
+        }
+        if (!(s >= 0x1p-90f && s < 0x1p+127f) && any != 0) {  // squares that overflow or vanish in fp32
+            for (int k = 0; k < kAwTile / kAwThreads; ++k) {
+                const int64_t i = first + k * kAwThreads;
+                const double v = i < t.n ? (double)to_f32(g[i]) : 0.0;
+                sum = fma(v, v, sum);
+            }
+        } else {
+            sum += (double)s;
+        }
+    }
+    sum = block_sum(sum, shared);
+    if (threadIdx.x == 0) {
+        tab.part[tab.first_part + blockIdx.x] = sum;
+        __threadfence();
+        last = atomicAdd(tab.ticket, 1u) == tab.all_parts - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    sum = 0.0;
+    for (uint32_t i = threadIdx.x; i < tab.all_parts; i += kAwThreads) sum += __ldcg(tab.part + i);
+    __syncthreads();
+    sum = block_sum(sum, shared);
+    if (threadIdx.x == 0) {
+        const float norm = (float)(sqrt(sum) * (double)tab.scale);
+        float k = 1.0f;
+        if (tab.max_norm > 0.0f) k = fminf(__fdiv_rn(tab.max_norm, __fadd_rn(norm, 1e-6f)), 1.0f);
+        tab.result[0] = norm;
+        tab.result[1] = isfinite(norm) ? __fmul_rn(tab.scale, k) : __uint_as_float(0x7fc00000u);
+        *tab.ticket = 0;
+    }
+}
+
+uint32_t tiles_of(int64_t n) { return (uint32_t)((n + kAwTile - 1) / kAwTile); }
+
+}  // namespace
+}  // namespace adacomp
+
+struct adacomp_adamw {
+    std::vector<int64_t> n;
+    std::vector<uint8_t> w_bf16, g_bf16;
+    std::vector<float> weight_decay;
+    std::vector<int32_t> by_g[2];     // tensors by gradient type, as the norm's launches take them
+    std::vector<int32_t> by_wg[4];    // and by weight and gradient type
+    int32_t state_bits = 32;
+    uint32_t norm_parts = 0;
+    size_t norm_ws = 0;
+};
+
+namespace {
+
+using namespace adacomp;
+
+// The launches of one call: runs of at most `cap` tensors and 2^31 - 1 tiles.
+template <typename F> adacomp_status for_runs(const adacomp_adamw* h, const std::vector<int32_t>& list, int cap, F&& f)
+{
+    size_t i = 0;
+    while (i < list.size()) {
+        size_t j = i;
+        uint64_t tiles = 0;
+        while (j < list.size() && (int)(j - i) < cap) {
+            const uint64_t more = tiles_of(h->n[(size_t)list[j]]);
+            if (j > i && tiles + more > 0x7fffffffull) break;
+            tiles += more;
+            ++j;
+        }
+        const adacomp_status st = f(i, j, (uint32_t)tiles);
+        if (st != ADACOMP_OK) return st;
+        i = j;
+    }
+    return ADACOMP_OK;
+}
+
+template <typename W, typename G> cudaError_t step_launch(const AwTable* tab, uint32_t tiles, bool eight, cudaStream_t s)
+{
+    return launch_after(eight ? adamw_kernel<W, G, true> : adamw_kernel<W, G, false>, dim3(tiles), dim3(kAwThreads), 0,
+                        s, *tab);
+}
+
+}  // namespace
+
+extern "C" {
+
+adacomp_status adacomp_adamw_init(adacomp_adamw_t* out, int32_t num_tensors, const int64_t* n,
+                                  const int32_t* w_dtype, const int32_t* g_dtype, const float* weight_decay,
+                                  int32_t state_bits, size_t* norm_ws_bytes)
+{
+    if (!out) return ADACOMP_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (num_tensors < 1 || num_tensors > ADACOMP_MAX_TENSORS || !n || !w_dtype || !g_dtype ||
+        (state_bits != 8 && state_bits != 32))
+        return ADACOMP_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < num_tensors; ++i)
+        if (n[i] < 1 || n[i] > (int64_t)1 << 40 || !known_dtype(w_dtype[i]) || !known_dtype(g_dtype[i]) ||
+            (weight_decay && !std::isfinite(weight_decay[i])))
+            return ADACOMP_ERR_INVALID_ARG;
+    adacomp_adamw* h = nullptr;
+    try {
+        h = new adacomp_adamw;
+        for (int32_t i = 0; i < num_tensors; ++i) {
+            h->n.push_back(n[i]);
+            h->w_bf16.push_back(w_dtype[i] == ADACOMP_BF16);
+            h->g_bf16.push_back(g_dtype[i] == ADACOMP_BF16);
+            h->weight_decay.push_back(weight_decay ? weight_decay[i] : 0.0f);
+            h->by_g[h->g_bf16.back()].push_back(i);
+            h->by_wg[h->w_bf16.back() * 2 + h->g_bf16.back()].push_back(i);
+        }
+    } catch (...) {
+        delete h;
+        return ADACOMP_ERR_INVALID_ARG;
+    }
+    h->state_bits = state_bits;
+    for (int k = 0; k < 2; ++k)
+        for_runs(h, h->by_g[k], kNormTensors, [&](size_t, size_t, uint32_t tiles) {
+            h->norm_parts += tiles < (uint32_t)kNormGrid ? tiles : (uint32_t)kNormGrid;
+            return ADACOMP_OK;
+        });
+    h->norm_ws = 16 + 8 * (size_t)h->norm_parts;
+    if (norm_ws_bytes) *norm_ws_bytes = h->norm_ws;
+    *out = h;
+    return ADACOMP_OK;
+}
+
+adacomp_status adacomp_grad_norm(adacomp_adamw_t h, const void* const* grad, float grad_scale, float max_norm,
+                                 float* result, void* ws, size_t ws_bytes, cudaStream_t stream)
+{
+    TrainRange range("adacomp_grad_norm");
+    if (!h || !grad || !result || !ws || !(grad_scale > 0.0f) || !std::isfinite(grad_scale) || std::isnan(max_norm))
+        return ADACOMP_ERR_INVALID_ARG;
+    if (!is_aligned(ws, 16) || !is_aligned(result, 4)) return ADACOMP_ERR_ALIGNMENT;
+    if (ws_bytes < h->norm_ws) return ADACOMP_ERR_WORKSPACE;
+    for (size_t i = 0; i < h->n.size(); ++i) {
+        if (!grad[i]) return ADACOMP_ERR_INVALID_ARG;
+        if (!is_aligned(grad[i], 16)) return ADACOMP_ERR_ALIGNMENT;
+    }
+    NormTable* tab = new (std::nothrow) NormTable;
+    if (!tab) return ADACOMP_ERR_INVALID_ARG;
+    tab->all_parts = h->norm_parts;
+    tab->scale = grad_scale;
+    tab->max_norm = max_norm;
+    tab->result = result;
+    tab->ticket = static_cast<uint32_t*>(ws);
+    tab->part = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + 16);
+    uint32_t parts = 0;
+    adacomp_status st = ADACOMP_OK;
+    for (int k = 0; k < 2 && st == ADACOMP_OK; ++k)
+        st = for_runs(h, h->by_g[k], kNormTensors, [&](size_t i, size_t j, uint32_t tiles) {
+            uint32_t tile = 0;
+            for (size_t q = i; q < j; ++q) {
+                const size_t id = (size_t)h->by_g[k][q];
+                tab->t[q - i] = {grad[id], h->n[id], tile};
+                tile += tiles_of(h->n[id]);
+            }
+            const uint32_t grid = tiles < (uint32_t)kNormGrid ? tiles : (uint32_t)kNormGrid;
+            tab->count = (int32_t)(j - i);
+            tab->tiles = tiles;
+            tab->first_part = parts;
+            parts += grid;
+            return launch_result(launch_after(k ? grad_norm_kernel<bf16> : grad_norm_kernel<float>, dim3(grid),
+                                              dim3(kAwThreads), 0, stream, *tab), stream);
+        });
+    delete tab;
+    return st;
+}
+
+adacomp_status adacomp_adamw_step(adacomp_adamw_t h, void* const* weight, const void* const* grad, void* const* m,
+                                  void* const* v, float* const* m_scale, float* const* v_scale, void* const* copy,
+                                  float lr, float beta1, float beta2, float eps, float bias_correction1,
+                                  float bias_correction2, float grad_scale, const float* coefficient,
+                                  cudaStream_t stream)
+{
+    TrainRange range("adacomp_adamw_step");
+    if (!h || !weight || !grad || !m || !v) return ADACOMP_ERR_INVALID_ARG;
+    const bool eight = h->state_bits == 8;
+    if (eight != (m_scale != nullptr) || eight != (v_scale != nullptr)) return ADACOMP_ERR_INVALID_ARG;
+    if (!std::isfinite(lr) || !(beta1 >= 0.0f && beta1 < 1.0f) || !(beta2 >= 0.0f && beta2 < 1.0f) || !(eps > 0.0f) ||
+        !std::isfinite(eps) || !(bias_correction1 > 0.0f) || !(bias_correction2 > 0.0f))
+        return ADACOMP_ERR_INVALID_ARG;
+    if (!is_aligned(coefficient, 4)) return ADACOMP_ERR_ALIGNMENT;
+    for (size_t i = 0; i < h->n.size(); ++i) {
+        if (!weight[i] || !grad[i] || !m[i] || !v[i] || (eight && (!m_scale[i] || !v_scale[i])))
+            return ADACOMP_ERR_INVALID_ARG;
+        if (!is_aligned(weight[i], 16) || !is_aligned(grad[i], 16) || !is_aligned(m[i], 16) || !is_aligned(v[i], 16) ||
+            (eight && (!is_aligned(m_scale[i], 4) || !is_aligned(v_scale[i], 4))) || (copy && !is_aligned(copy[i], 16)))
+            return ADACOMP_ERR_ALIGNMENT;
+    }
+    AwTable* tab = new (std::nothrow) AwTable;
+    if (!tab) return ADACOMP_ERR_INVALID_ARG;
+    tab->beta1 = beta1;
+    tab->beta2 = beta2;
+    tab->rest1 = 1.0f - beta1;
+    tab->rest2 = 1.0f - beta2;
+    tab->step = (float)((double)lr / (double)bias_correction1);
+    tab->root = (float)(1.0 / std::sqrt((double)bias_correction2));
+    tab->eps = eps;
+    tab->scale = grad_scale;
+    tab->coefficient = coefficient;
+    adacomp_status st = ADACOMP_OK;
+    for (int k = 0; k < 4 && st == ADACOMP_OK; ++k)
+        st = for_runs(h, h->by_wg[k], kAwTensors, [&](size_t i, size_t j, uint32_t tiles) {
+            uint32_t tile = 0;
+            for (size_t q = i; q < j; ++q) {
+                const size_t id = (size_t)h->by_wg[k][q];
+                AwTensor& t = tab->t[q - i];
+                t.w = weight[id];
+                t.g = grad[id];
+                t.m = m[id];
+                t.v = v[id];
+                t.ms = eight ? m_scale[id] : nullptr;
+                t.vs = eight ? v_scale[id] : nullptr;
+                t.copy = copy ? copy[id] : nullptr;
+                t.n = h->n[id];
+                t.tile_begin = tile;
+                t.decay = (float)(1.0 - (double)lr * (double)h->weight_decay[id]);
+                tile += tiles_of(t.n);
+            }
+            tab->count = (int32_t)(j - i);
+            const cudaError_t e = k == 0   ? step_launch<float, float>(tab, tiles, eight, stream)
+                                  : k == 1 ? step_launch<float, bf16>(tab, tiles, eight, stream)
+                                  : k == 2 ? step_launch<bf16, float>(tab, tiles, eight, stream)
+                                           : step_launch<bf16, bf16>(tab, tiles, eight, stream);
+            return launch_result(e, stream);
+        });
+    delete tab;
+    return st;
+}
+
+void adacomp_adamw_free(adacomp_adamw_t h) { delete h; }
+
+}  // extern "C"

@@ -1,0 +1,67 @@
+// Shared by the training operators' kernels (layer norm, recurrence, AdamW): element
+// types, loads and stores of short vectors, warp sums, and host-side checks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "adacomp.h"
+#include "adacomp_internal.cuh"
+
+namespace adacomp {
+
+adacomp_status launch_result(cudaError_t e, cudaStream_t stream);  // abi.cu
+
+namespace {
+
+// ---------------------------------------------------------------- host
+struct TrainRange {  // a named range on the host timeline, as for the compressor's calls
+    explicit TrainRange(const char* name) { nvtxRangePushA(name); }
+    ~TrainRange() { nvtxRangePop(); }
+    TrainRange(const TrainRange&) = delete;
+    TrainRange& operator=(const TrainRange&) = delete;
+};
+
+inline bool is_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool known_dtype(int32_t t) { return t == ADACOMP_F32 || t == ADACOMP_BF16; }
+inline int dtype_bytes(int32_t t) { return t == ADACOMP_BF16 ? 2 : 4; }
+
+// Multiprocessors of the current device, looked up once per device.
+inline cudaError_t sm_count(int* out)
+{
+    static int known[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (known[dev] == 0) {
+        int n = 0;
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        known[dev] = n;
+    }
+    *out = known[dev];
+    return cudaSuccess;
+}
+
+// ---------------------------------------------------------------- device
+using bf16 = __nv_bfloat16;
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ bf16 from_f32<bf16>(float v) { return __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+}  // namespace
+}  // namespace adacomp

@@ -1,0 +1,277 @@
+"""The gated linear recurrence, forward and backward, against the plain form in 64 bits
+(GPU): step by step, with worst-case bounds that follow the recurrence (tests/_train.py).
+Steps cross the edges of the chunks that a kernel splits the sequence into."""
+import pytest
+import torch
+
+import residual_gradient_compression_gb300 as ac
+from _gpu import ensure_built
+from _train import U, assert_within, recurrence
+
+pytestmark = pytest.mark.gpu
+F, B = torch.float32, torch.bfloat16
+CODE = {F: ac.F32, B: ac.BF16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_built()
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _rand(gen, *shape, dtype=F, scale=1.0, offset=0.0):
+    return (torch.randn(*shape, generator=gen, device="cuda") * scale + offset).to(dtype)
+
+
+def _inputs(seed, batch, steps, ch, dt, gate=2.0):
+    gen = _gen(seed)
+    return (_rand(gen, batch, steps, ch, dtype=dt, offset=gate), _rand(gen, batch, steps, ch, dtype=dt),
+            _rand(gen, batch, ch), _rand(gen, batch, steps, ch, dtype=dt), _rand(gen, batch, ch))
+
+
+def _carry(h, batch, steps):
+    n = ac.adacomp_recurrence_carry_bytes(h, batch, steps) // 4
+    return torch.full((n,), float("nan"), device="cuda")
+
+
+def _run(z, x, h0, lengths, dy, dh_last, dz=None, dx=None, y=None):
+    batch, steps, ch = z.shape
+    h = ac.adacomp_recurrence_init(ch, CODE[z.dtype])
+    new = lambda: torch.full((batch, steps, ch), -9.0, dtype=z.dtype, device="cuda")  # noqa: E731
+    y = new() if y is None else y
+    dz = new() if dz is None else dz
+    dx = new() if dx is None else dx
+    h_last, dh0 = torch.empty(batch, ch, device="cuda"), torch.empty(batch, ch, device="cuda")
+    carry = _carry(h, batch, steps)
+    ac.adacomp_recurrence_forward(h, z, x, y, h0=h0, lengths=lengths, h_last=h_last, carry=carry)
+    ac.adacomp_recurrence_backward(h, z, x, dy, carry, dz, dx, lengths=lengths, dh_last=dh_last, dh0=dh0)
+    return y, h_last, dz, dx, dh0
+
+
+def _check(got, z, x, h0, lengths, dy, dh_last):
+    ref, bound = recurrence(z, x, h0, lengths, dy, dh_last)
+    for name, g, r, e in zip(("y", "h_last", "dz", "dx", "dh0"), got, ref, bound):
+        assert_within(g, r, e, f"{name} {tuple(z.shape)} {z.dtype}")
+
+
+SIZES = [(1, 1, 1), (3, 1, 70), (64, 1, 1024), (2, 2, 3), (1, 7, 33), (5, 15, 64), (2, 16, 65), (3, 17, 2), (1, 31, 130),
+         (2, 63, 32), (2, 64, 64), (1, 65, 66), (2, 127, 5), (2, 128, 96), (1, 129, 63), (1, 255, 64), (3, 257, 40),
+         (1, 512, 31), (1, 1000, 129), (1, 1023, 64), (2, 1025, 68), (1, 2049, 7), (1, 4500, 1), (20, 300, 200),
+         (300, 40, 33), (2, 130, 4096)]
+
+
+@pytest.mark.parametrize("dt", [F, B])
+@pytest.mark.parametrize("batch,steps,ch", SIZES)
+def test_forward_and_backward(batch, steps, ch, dt):
+    z, x, h0, dy, dh = _inputs(batch + steps * 7 + ch, batch, steps, ch, dt)
+    _check(_run(z, x, h0, None, dy, dh), z, x, h0, None, dy, dh)
+
+
+@pytest.mark.parametrize("dt", [F, B])
+@pytest.mark.parametrize("batch,steps,ch", [(7, 200, 37), (6, 1300, 64), (9, 20, 130)])
+def test_lengths_and_what_lies_past_them(batch, steps, ch, dt):
+    """Whole, empty, negative and overlong lengths; NaN past the end reaches nothing."""
+    z, x, h0, dy, dh = _inputs(batch, batch, steps, ch, dt)
+    lengths = torch.tensor(([steps, 0, 1, steps - 1, steps // 2, -3, steps + 100, 129, 128] * 2)[:batch],
+                           dtype=torch.int32, device="cuda")
+    ends = lengths.clamp(0, steps)
+    gone = torch.arange(steps, device="cuda")[None, :] >= ends[:, None]
+    for t in (z, x, dy):
+        t[gone] = float("nan")
+    got = _run(z, x, h0, lengths, dy, dh)
+    _check(got, z, x, h0, lengths, dy, dh)
+    for k in (0, 2, 3):
+        assert not got[k][gone].any() and not torch.signbit(got[k][gone]).any()
+    assert torch.equal(got[1][1], h0[1]) and torch.equal(got[4][1], dh[1])  # the empty sequence
+
+
+def _strided(layout, batch, steps, ch, dt, fill):
+    """Tensors of one layout: whether the halves of one buffer, time before batch, or apart
+    from a base that is aligned to its element alone."""
+    if layout == "halves":
+        return fill(torch.empty(batch, steps, 2 * ch, dtype=dt, device="cuda"))
+    if layout == "time first":
+        return fill(torch.empty(steps, batch, 2 * ch, dtype=dt, device="cuda").transpose(0, 1))
+    flat = torch.empty(1 + batch * (steps + 1) * (2 * ch + 3), dtype=dt, device="cuda")
+    return fill(flat[1:].view(batch, steps + 1, 2 * ch + 3)[:, :steps, :2 * ch])
+
+
+@pytest.mark.parametrize("dt", [F, B])
+@pytest.mark.parametrize("ch", [64, 50, 33])
+@pytest.mark.parametrize("layout", ["halves", "time first", "odd"])
+def test_layouts(layout, ch, dt):
+    batch, steps = 3, 150
+    z, x, h0, dy, dh = _inputs(ch, batch, steps, ch, dt)
+    plain = _run(z, x, h0, None, dy, dh)
+
+    def fill(t):
+        t[..., :ch], t[..., ch:] = z, x
+        return t
+
+    zx = _strided(layout, batch, steps, ch, dt, fill)
+    dzx = _strided(layout, batch, steps, ch, dt, lambda t: t)
+    dy2 = _strided(layout, batch, steps, ch, dt, lambda t: t)[..., :ch]
+    dy2.copy_(dy)
+    y = _strided(layout, batch, steps, ch, dt, lambda t: t)[..., ch:]
+    got = _run(zx[..., :ch], zx[..., ch:], h0, None, dy2, dh, dzx[..., :ch], dzx[..., ch:], y)
+    _check(got, z, x, h0, None, dy, dh)
+    for g, p in zip(got, plain):  # the split of the steps does not depend on the layout
+        assert torch.equal(g, p)
+
+
+def test_what_lies_between_the_rows_is_kept():
+    batch, steps, ch = 2, 40, 21
+    z, x, h0, dy, dh = _inputs(1, batch, steps, ch, B)
+    outs = [torch.full((batch, steps + 2, ch + 5), -7.0, dtype=B, device="cuda") for _ in range(3)]
+    views = [o[:, 1:steps + 1, 2:ch + 2] for o in outs]
+    _run(z, x, h0, None, dy, dh, views[0], views[1], views[2])
+    for o, v in zip(outs, views):
+        assert not (v == -7.0).all()
+        v.fill_(-7.0)
+        assert bool((o == -7.0).all())
+
+
+def test_optional_inputs_and_outputs():
+    z, x, h0, dy, dh = _inputs(8, 2, 140, 48, F)
+    full = _run(z, x, torch.zeros_like(h0), None, dy, torch.zeros_like(dh))
+    h = ac.adacomp_recurrence_init(48, ac.F32)
+    y, dz, dx = torch.empty_like(z), torch.empty_like(z), torch.empty_like(z)
+    ac.adacomp_recurrence_forward(h, z, x, y)
+    assert torch.equal(y, full[0])
+    carry = _carry(h, 2, 140)
+    state = h0.clone()
+    ac.adacomp_recurrence_forward(h, z, x, y, h0=state, h_last=state, carry=carry)  # the state in place
+    assert torch.equal(state, _run(z, x, h0, None, dy, dh)[1])
+    ac.adacomp_recurrence_forward(h, z, x, y, carry=carry)
+    ac.adacomp_recurrence_backward(h, z, x, dy, carry, dz, dx)
+    assert torch.equal(dz, full[2]) and torch.equal(dx, full[3])
+    grad = dh.clone()
+    ac.adacomp_recurrence_backward(h, z, x, dy, carry, dz, dx, dh_last=grad, dh0=grad)
+    ref = _run(z, x, torch.zeros_like(h0), None, dy, dh)
+    assert torch.equal(grad, ref[4]) and torch.equal(dz, ref[2])
+
+
+def test_no_steps_and_no_sequences():
+    h = ac.adacomp_recurrence_init(10, ac.F32)
+    empty = torch.empty(3, 0, 10, device="cuda")
+    h0, last = torch.randn(3, 10, device="cuda"), torch.empty(3, 10, device="cuda")
+    carry = torch.empty(0, device="cuda")
+    ac.adacomp_recurrence_forward(h, empty, empty, empty, h0=h0, h_last=last, carry=carry)
+    assert torch.equal(last, h0)
+    ac.adacomp_recurrence_forward(h, empty, empty, empty, h_last=last)
+    assert not last.any()
+    ac.adacomp_recurrence_backward(h, empty, empty, empty, carry, empty, empty, dh_last=h0, dh0=last)
+    assert torch.equal(last, h0)
+    none = torch.empty(0, 5, 10, device="cuda")
+    ac.adacomp_recurrence_forward(h, none, none, none)
+
+
+def test_steps_one_by_one_carry_the_state():
+    """Single-token calls that hand the state on, against the whole sequence at once."""
+    batch, steps, ch = 4, 40, 96
+    z, x, h0, _, _ = _inputs(6, batch, steps, ch, F)
+    ref, bound = recurrence(z, x, h0)
+    h = ac.adacomp_recurrence_init(ch, ac.F32)
+    state, y = h0.clone(), torch.empty_like(z)
+    for t in range(steps):
+        ac.adacomp_recurrence_forward(h, z[:, t:t + 1], x[:, t:t + 1], y[:, t:t + 1], h0=state, h_last=state)
+    assert_within(y, ref[0], bound[0], "y")
+    assert_within(state, ref[1], bound[1], "state")
+
+
+@pytest.mark.parametrize("dt", [F, B])
+def test_closed_open_and_infinite_gates(dt):
+    """Gates far out on both sides: a state that is kept for good, or forgotten at once."""
+    batch, steps, ch = 2, 300, 40
+    z, x, h0, dy, dh = _inputs(11, batch, steps, ch, dt)
+    z[:, :, 0:8] = 80.0
+    z[:, :, 8:16] = -80.0
+    z[:, :, 16:20] = float("inf")
+    z[:, :, 20:24] = -float("inf")
+    z[:, ::3, 24:32] = 30.0
+    _check(_run(z, x, h0, None, dy, dh), z.clamp(-1e3, 1e3), x, h0, None, dy, dh)
+
+
+def test_non_finite_values_stay_in_their_channel_and_after_their_step():
+    z, x, h0, dy, dh = _inputs(12, 2, 300, 70, F)
+    clean = _run(z, x, h0, None, dy, dh)
+    x[1, 137, 3] = float("nan")
+    z[0, 200, 69] = float("nan")
+    got = _run(z, x, h0, None, dy, dh)
+    y = clean[0].clone()
+    assert torch.isnan(got[0][1, 137:, 3]).all() and torch.isnan(got[0][0, 200:, 69]).all()
+    ok = torch.ones_like(y, dtype=torch.bool)
+    ok[1, 137:, 3] = False
+    ok[0, 200:, 69] = False
+    assert torch.isfinite(got[0][ok]).all()
+    others = torch.ones(2, 300, 70, dtype=torch.bool, device="cuda")
+    others[1, :, 3] = False
+    others[0, :, 69] = False
+    for k in (0, 2, 3):
+        assert torch.equal(got[k][others], clean[k][others])
+
+
+def test_gradients_against_differences():
+    """Directional derivatives of the kernel's own forward pass in 32 bits; the bound is the
+    central difference's (a third derivative of order one per element) and the rounding's."""
+    batch, steps, ch = 2, 200, 33
+    z, x, h0, dy, dh = _inputs(5, batch, steps, ch, F, gate=1.0)
+    h = ac.adacomp_recurrence_init(ch, ac.F32)
+    grads = _run(z, x, h0, None, dy, dh)[2:]
+    gen, e = _gen(50), 2.0 ** -7
+
+    def loss(z, x, h0):
+        y, last = torch.empty_like(z), torch.empty_like(h0)
+        ac.adacomp_recurrence_forward(h, z, x, y, h0=h0, h_last=last)
+        return float((y.double() * dy.double()).sum() + (last.double() * dh.double()).sum())
+
+    for k, grad in enumerate(grads):
+        args = [z, x, h0]
+        v = _rand(gen, *args[k].shape)
+        ends = []
+        for s in (e, -e):
+            moved = list(args)
+            moved[k] = args[k] + s * v
+            ends.append(loss(*moved))
+        got, want = (ends[0] - ends[1]) / (2 * e), float((grad.double() * v.double()).sum())
+        scale = float((batch * steps * ch) ** 0.5)
+        assert abs(got - want) <= scale * (4 * e * e + 64 * U / e), (k, got, want)
+
+
+def test_offsets_past_32_bits():
+    """Sequences 2^31 + 64 elements apart."""
+    batch, steps, ch, gap = 2, 150, 40, 2 ** 31 + 64
+    z, x, h0, dy, dh = _inputs(21, batch, steps, ch, B)
+    flat = torch.empty(gap + steps * 2 * ch, dtype=B, device="cuda")
+    zx = flat.as_strided((batch, steps, 2 * ch), (gap, 2 * ch, 1))
+    zx[..., :ch], zx[..., ch:] = z, x
+    out = torch.empty(gap + steps * 2 * ch, dtype=B, device="cuda").as_strided((batch, steps, 2 * ch), (gap, 2 * ch, 1))
+    ref = _run(z, x, h0, None, dy, dh)
+    got = _run(zx[..., :ch], zx[..., ch:], h0, None, dy, dh, out[..., :ch], out[..., ch:])
+    assert all(torch.equal(a, r) for a, r in zip(got, ref))
+
+
+def test_same_bits_on_another_stream_and_in_a_graph():
+    z, x, h0, dy, dh = _inputs(31, 3, 1500, 200, B)
+    ref = _run(z, x, h0, None, dy, dh)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            assert all(torch.equal(a, r) for a, r in zip(_run(z, x, h0, None, dy, dh), ref))
+    side.synchronize()
+    h = ac.adacomp_recurrence_init(200, ac.BF16)
+    out = [torch.zeros_like(t) for t in ref]
+    carry = _carry(h, 3, 1500)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ac.adacomp_recurrence_forward(h, z, x, out[0], h0=h0, h_last=out[1], carry=carry)
+        ac.adacomp_recurrence_backward(h, z, x, dy, carry, out[2], out[3], dh_last=dh, dh0=out[4])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, r) for a, r in zip(out, ref))
