@@ -4,6 +4,8 @@
 #include <new>
 #include <vector>
 
+#include <cuda_fp16.h>
+
 #include "train_common.cuh"
 
 namespace adacomp {
@@ -15,7 +17,8 @@ constexpr int kAwBlock = ADACOMP_ADAMW_BLOCK;      // elements per scale, and pe
 constexpr int kAwTile = kAwWarps * kAwBlock;       // elements per CTA
 constexpr int kAwTensors = 400;                    // tensors per launch (a by-value kernel parameter)
 constexpr int kNormTensors = 1300;
-constexpr int kNormGrid = 608;                     // CTAs per launch at most: partial sums, in an order of their own
+constexpr int kNormGrid = 912;                     // CTAs per launch at most (six per SM), each with a partial sum
+constexpr int kNormVectors = 4;                    // 16-byte vectors per thread and tile
 
 struct AwTensor {
     void *w, *m, *v, *copy;
@@ -66,20 +69,19 @@ template <typename Table> __device__ __forceinline__ int owner_of(const Table& t
 }
 
 // ---------------------------------------------------------------- e4m3
-__device__ __forceinline__ uint32_t to_e4m3(float v)
+// Two values as two e4m3 numbers, the first in the low byte.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
 {
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
-    return r & 0xffu;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
-__device__ __forceinline__ float from_e4m3(uint32_t c)
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c)
 {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-    float f;
-    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.f32.f16 %0, lo; }" : "=f"(f) : "r"(h));
-    return f;
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 struct Scales {
@@ -100,74 +102,176 @@ __device__ __forceinline__ Scales scales_of(uint32_t bits)
 }
 
 // ---------------------------------------------------------------- step
-// One warp per block of 256 elements, a tile of eight blocks per CTA.
+struct Adam {
+    float c, beta1, beta2, rest1, rest2, step, root, eps, decay;
+};
+
+// One element: the new m, v's root u and the weight, from m, v, the gradient and the weight.
+__device__ __forceinline__ void adam(const Adam& k, float g, float& m, float& v, float& u, float& w)
+{
+    g = __fmul_rn(k.c, g);
+    m = __fadd_rn(__fmul_rn(k.beta1, m), __fmul_rn(k.rest1, g));
+    v = __fadd_rn(__fmul_rn(k.beta2, v), __fmul_rn(k.rest2, __fmul_rn(g, g)));
+    u = __fsqrt_rn(v);
+    const float q = __fdiv_rn(m, __fadd_rn(__fmul_rn(u, k.root), k.eps));
+    w = __fsub_rn(__fmul_rn(k.decay, w), __fmul_rn(k.step, q));
+}
+
+// Four consecutive elements. Past a tensor's end they read as zero and are not written.
+__device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, float (&v)[4])
+{
+    if (i + 4 <= n) {
+        const float4 q = *reinterpret_cast<const float4*>(p + i);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = i + j < n ? p[i + j] : 0.0f;
+}
+
+__device__ __forceinline__ void load4(const bf16* p, int64_t i, int64_t n, float (&v)[4])
+{
+    if (i + 4 <= n) {
+        const uint2 q = *reinterpret_cast<const uint2*>(p + i);
+        v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
+        v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = i + j < n ? to_f32(p[i + j]) : 0.0f;
+}
+
+__device__ __forceinline__ uint32_t load4(const uint8_t* p, int64_t i, int64_t n)
+{
+    if (i + 4 <= n) return *reinterpret_cast<const uint32_t*>(p + i);
+    uint32_t r = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (i + j < n) r |= (uint32_t)p[i + j] << (8 * j);
+    return r;
+}
+
+__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const float (&v)[4])
+{
+    if (i + 4 <= n) {
+        *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (i + j < n) p[i + j] = v[j];
+}
+
+__device__ __forceinline__ void store4(bf16* p, int64_t i, int64_t n, const float (&v)[4])
+{
+    if (i + 4 <= n) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(p + i) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (i + j < n) p[i + j] = from_f32<bf16>(v[j]);
+}
+
+__device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, uint32_t v)
+{
+    if (i + 4 <= n) {
+        *reinterpret_cast<uint32_t*>(p + i) = v;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (i + j < n) p[i + j] = (uint8_t)(v >> (8 * j));
+}
+
+// One warp per block of 256 elements, a tile of eight blocks per CTA; a lane has four
+// elements of either half of its block, so that every access of a warp is contiguous.
 template <typename W, typename G, bool kEight>
 __global__ void __launch_bounds__(kAwThreads) adamw_kernel(const __grid_constant__ AwTable tab)
 {
+    constexpr int kParts = kAwBlock / 128;
     ptx::griddep_wait();
-    const float c = tab.coefficient ? *tab.coefficient : tab.scale;
-    if (!isfinite(c)) return;
     const AwTensor& t = tab.t[owner_of(tab, blockIdx.x)];
-    const int lane = threadIdx.x & 31;
     const int64_t block = (int64_t)(blockIdx.x - t.tile_begin) * kAwWarps + (threadIdx.x >> 5);
-    const int64_t first = block * kAwBlock;
-    if (first >= t.n) return;
+    const int64_t n = t.n, first = block * kAwBlock + (threadIdx.x & 31) * 4;
+    if (block * kAwBlock >= n) return;
     W* w = static_cast<W*>(t.w);
     const G* g = static_cast<const G*>(t.g);
     bf16* copy = static_cast<bf16*>(t.copy);
-    float mv[kAwBlock / 32], uv[kAwBlock / 32];
-    uint32_t mtop = 0, utop = 0;
-    float ms = 0.0f, us = 0.0f;
+    float wv[kParts][4], gv[kParts][4], mv[kParts][4], vv[kParts][4], ms, us;
+    uint32_t mc[kParts], uc[kParts];
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+        const int64_t i = first + k * 128;
+        load4(w, i, n, wv[k]);
+        load4(g, i, n, gv[k]);
+        if (kEight) {
+            mc[k] = load4(static_cast<const uint8_t*>(t.m), i, n);
+            uc[k] = load4(static_cast<const uint8_t*>(t.v), i, n);
+        } else {
+            load4(static_cast<const float*>(t.m), i, n, mv[k]);
+            load4(static_cast<const float*>(t.v), i, n, vv[k]);
+        }
+    }
     if (kEight) {
         ms = t.ms[block];
         us = t.vs[block];
     }
+    Adam a = {tab.scale, tab.beta1, tab.beta2, tab.rest1, tab.rest2, tab.step, tab.root, tab.eps, t.decay};
+    if (tab.coefficient) a.c = *tab.coefficient;
+    if (!isfinite(a.c)) return;
+    uint32_t mtop = 0, utop = 0;
 #pragma unroll
-    for (int k = 0; k < kAwBlock / 32; ++k) {
-        const int64_t i = first + k * 32 + lane;
-        mv[k] = uv[k] = 0.0f;
-        if (i >= t.n) continue;
-        float m, v;
+    for (int k = 0; k < kParts; ++k) {
+        const int64_t i = first + k * 128;
         if (kEight) {
-            m = __fmul_rn(from_e4m3(static_cast<uint8_t*>(t.m)[i]), ms);
-            const float u = __fmul_rn(from_e4m3(static_cast<uint8_t*>(t.v)[i]), us);
-            v = __fmul_rn(u, u);
-        } else {
-            m = static_cast<float*>(t.m)[i];
-            v = static_cast<float*>(t.v)[i];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float2 m = from_e4m3x2(mc[k] >> (16 * j)), u = from_e4m3x2(uc[k] >> (16 * j));
+                mv[k][2 * j] = __fmul_rn(m.x, ms), mv[k][2 * j + 1] = __fmul_rn(m.y, ms);
+                const float x = __fmul_rn(u.x, us), y = __fmul_rn(u.y, us);
+                vv[k][2 * j] = __fmul_rn(x, x), vv[k][2 * j + 1] = __fmul_rn(y, y);
+            }
         }
-        const float d = __fmul_rn(c, to_f32(g[i]));
-        m = __fadd_rn(__fmul_rn(tab.beta1, m), __fmul_rn(tab.rest1, d));
-        v = __fadd_rn(__fmul_rn(tab.beta2, v), __fmul_rn(tab.rest2, __fmul_rn(d, d)));
-        const float u = __fsqrt_rn(v);
-        const float q = __fdiv_rn(m, __fadd_rn(__fmul_rn(u, tab.root), tab.eps));
-        const float x = __fsub_rn(__fmul_rn(t.decay, to_f32(w[i])), __fmul_rn(tab.step, q));
-        w[i] = from_f32<W>(x);
-        if (copy) copy[i] = from_f32<bf16>(x);
-        if (kEight) {
-            mv[k] = m;
-            uv[k] = u;
-            mtop = max(mtop, __float_as_uint(m) & 0x7fffffffu);
-            utop = max(utop, __float_as_uint(u) & 0x7fffffffu);
-        } else {
-            static_cast<float*>(t.m)[i] = m;
-            static_cast<float*>(t.v)[i] = v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float u;
+            adam(a, gv[k][j], mv[k][j], vv[k][j], u, wv[k][j]);
+            if (kEight) {
+                vv[k][j] = u;
+                mtop = max(mtop, __float_as_uint(mv[k][j]) & 0x7fffffffu);
+                utop = max(utop, __float_as_uint(u) & 0x7fffffffu);
+            }
+        }
+        store4(w, i, n, wv[k]);
+        if (copy) store4(copy, i, n, wv[k]);
+        if (!kEight) {
+            store4(static_cast<float*>(t.m), i, n, mv[k]);
+            store4(static_cast<float*>(t.v), i, n, vv[k]);
         }
     }
     if (!kEight) return;
-    const Scales a = scales_of(__reduce_max_sync(0xffffffffu, mtop));
-    const Scales b = scales_of(__reduce_max_sync(0xffffffffu, utop));
+    const Scales p = scales_of(__reduce_max_sync(0xffffffffu, mtop));
+    const Scales q = scales_of(__reduce_max_sync(0xffffffffu, utop));
 #pragma unroll
-    for (int k = 0; k < kAwBlock / 32; ++k) {
-        const int64_t i = first + k * 32 + lane;
-        if (i >= t.n) continue;
-        static_cast<uint8_t*>(t.m)[i] = (uint8_t)to_e4m3(__fmul_rn(mv[k], a.inverse));
-        const uint32_t r = to_e4m3(__fmul_rn(uv[k], b.inverse));
-        static_cast<uint8_t*>(t.v)[i] = (uint8_t)(r == 0 && uv[k] > 0.0f ? 1u : r);
+    for (int k = 0; k < kParts; ++k) {
+        uint32_t m = 0, u = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            m |= to_e4m3x2(__fmul_rn(mv[k][2 * j], p.inverse), __fmul_rn(mv[k][2 * j + 1], p.inverse)) << (16 * j);
+            u |= to_e4m3x2(__fmul_rn(vv[k][2 * j], q.inverse), __fmul_rn(vv[k][2 * j + 1], q.inverse)) << (16 * j);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if ((u >> (8 * j) & 0xffu) == 0 && vv[k][j] > 0.0f) u |= 1u << (8 * j);
+        store4(static_cast<uint8_t*>(t.m), first + k * 128, n, m);
+        store4(static_cast<uint8_t*>(t.v), first + k * 128, n, u);
     }
-    if (lane == 0) {
-        t.ms[block] = a.scale;
-        t.vs[block] = b.scale;
+    if ((threadIdx.x & 31) == 0) {
+        t.ms[block] = p.scale;
+        t.vs[block] = q.scale;
     }
 }
 
@@ -183,31 +287,73 @@ __device__ __forceinline__ double block_sum(double v, double* shared)
     return s;
 }
 
-// A CTA sums its tiles and leaves one fp64 partial sum; the last CTA of the call adds
-// the partial sums in their order.
-template <typename G>
-__global__ void __launch_bounds__(kAwThreads) grad_norm_kernel(const __grid_constant__ NormTable tab)
+// One 16-byte vector of a gradient, zeros past its end.
+template <typename G> __device__ __forceinline__ uint4 load_vector(const G* g, int64_t i, int64_t n)
 {
+    constexpr int kPer = 16 / (int)sizeof(G);
+    if (i + kPer <= n) return *reinterpret_cast<const uint4*>(g + i);
+    uint32_t r[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+        if (i + j < n) r[j * (int)sizeof(G) / 4] |= sizeof(G) == 4 ? reinterpret_cast<const uint32_t*>(g)[i + j]
+                         : (uint32_t)reinterpret_cast<const uint16_t*>(g)[i + j] << (16 * (j & 1));
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <typename G> __device__ __forceinline__ int values_of(uint32_t word, float (&v)[2])
+{
+    if (sizeof(G) == 4) {
+        v[0] = __uint_as_float(word);
+        return 1;
+    }
+    v[0] = __uint_as_float(word << 16);
+    v[1] = __uint_as_float(word & 0xffff0000u);
+    return 2;
+}
+
+// A CTA sums a run of consecutive tiles and leaves one fp64 partial sum; the last CTA of
+// the call adds the partial sums in their order.
+template <typename G>
+__global__ void __launch_bounds__(kAwThreads, 6) grad_norm_kernel(const __grid_constant__ NormTable tab)
+{
+    constexpr int kPer = 16 / (int)sizeof(G);
     ptx::griddep_wait();
     __shared__ double shared[kAwWarps];
     __shared__ bool last;
     double sum = 0.0;
-    for (uint32_t tile = blockIdx.x; tile < tab.tiles; tile += gridDim.x) {
-        const NormTensor& t = tab.t[owner_of(tab, tile)];
+    uint32_t tile = (uint32_t)((uint64_t)tab.tiles * blockIdx.x / gridDim.x);
+    const uint32_t end = (uint32_t)((uint64_t)tab.tiles * (blockIdx.x + 1) / gridDim.x);
+    int id = owner_of(tab, tile);
+    uint32_t next = id + 1 < tab.count ? tab.t[id + 1].tile_begin : tab.tiles;
+    for (; tile < end; ++tile) {
+        if (tile >= next) {
+            ++id;
+            next = id + 1 < tab.count ? tab.t[id + 1].tile_begin : tab.tiles;
+        }
+        const NormTensor& t = tab.t[id];
         const G* g = static_cast<const G*>(t.g);
-        const int64_t first = (int64_t)(tile - t.tile_begin) * kAwTile + threadIdx.x;
+        const int64_t first = (int64_t)(tile - t.tile_begin) * (kNormVectors * kAwThreads * kPer) + threadIdx.x * kPer;
+        uint32_t word[kNormVectors][4];
+#pragma unroll
+        for (int k = 0; k < kNormVectors; ++k) {
+            const uint4 q = load_vector(g, first + k * (kAwThreads * kPer), t.n);
+            word[k][0] = q.x, word[k][1] = q.y, word[k][2] = q.z, word[k][3] = q.w;
+        }
         float s = 0.0f;
         uint32_t any = 0;
 #pragma unroll
-        for (int k = 0; k < kAwTile / kAwThreads; ++k) {
-            const int64_t i = first + k * kAwThreads;
-            const float v = i < t.n ? to_f32(g[i]) : 0.0f;
-            s = fmaf(v, v, s);
-            any |= __float_as_uint(v) << 1;
+        for (int k = 0; k < kNormVectors * 4; ++k) {
+            float v[2];
+            const int c = values_of<G>(word[k / 4][k % 4], v);
+            for (int j = 0; j < c; ++j) {
+                s = fmaf(v[j], v[j], s);
+                any |= __float_as_uint(v[j]) << 1;
+            }
         }
         if (!(s >= 0x1p-90f && s < 0x1p+127f) && any != 0) {  // squares that overflow or vanish in fp32
-            for (int k = 0; k < kAwTile / kAwThreads; ++k) {
-                const int64_t i = first + k * kAwThreads;
+#pragma unroll 1
+            for (int k = 0; k < kNormVectors * kPer; ++k) {
+                const int64_t i = first + k / kPer * (kAwThreads * kPer) + k % kPer;
                 const double v = i < t.n ? (double)to_f32(g[i]) : 0.0;
                 sum = fma(v, v, sum);
             }
@@ -238,7 +384,13 @@ __global__ void __launch_bounds__(kAwThreads) grad_norm_kernel(const __grid_cons
     }
 }
 
-uint32_t tiles_of(int64_t n) { return (uint32_t)((n + kAwTile - 1) / kAwTile); }
+uint32_t step_tiles(int64_t n) { return (uint32_t)((n + kAwTile - 1) / kAwTile); }
+
+uint32_t norm_tiles(int64_t n, bool is_bf16)
+{
+    const int64_t per = (int64_t)kNormVectors * kAwThreads * (is_bf16 ? 8 : 4);
+    return (uint32_t)((n + per - 1) / per);
+}
 
 }  // namespace
 }  // namespace adacomp
@@ -259,14 +411,14 @@ namespace {
 using namespace adacomp;
 
 // The launches of one call: runs of at most `cap` tensors and 2^31 - 1 tiles.
-template <typename F> adacomp_status for_runs(const adacomp_adamw* h, const std::vector<int32_t>& list, int cap, F&& f)
+template <typename T, typename F> adacomp_status for_runs(const std::vector<int32_t>& list, int cap, T&& tiles_of, F&& f)
 {
     size_t i = 0;
     while (i < list.size()) {
         size_t j = i;
         uint64_t tiles = 0;
         while (j < list.size() && (int)(j - i) < cap) {
-            const uint64_t more = tiles_of(h->n[(size_t)list[j]]);
+            const uint64_t more = tiles_of((size_t)list[j]);
             if (j > i && tiles + more > 0x7fffffffull) break;
             tiles += more;
             ++j;
@@ -318,10 +470,11 @@ adacomp_status adacomp_adamw_init(adacomp_adamw_t* out, int32_t num_tensors, con
     }
     h->state_bits = state_bits;
     for (int k = 0; k < 2; ++k)
-        for_runs(h, h->by_g[k], kNormTensors, [&](size_t, size_t, uint32_t tiles) {
-            h->norm_parts += tiles < (uint32_t)kNormGrid ? tiles : (uint32_t)kNormGrid;
-            return ADACOMP_OK;
-        });
+        for_runs(h->by_g[k], kNormTensors, [&](size_t id) { return norm_tiles(h->n[id], k); },
+                 [&](size_t, size_t, uint32_t tiles) {
+                     h->norm_parts += tiles < (uint32_t)kNormGrid ? tiles : (uint32_t)kNormGrid;
+                     return ADACOMP_OK;
+                 });
     h->norm_ws = 16 + 8 * (size_t)h->norm_parts;
     if (norm_ws_bytes) *norm_ws_bytes = h->norm_ws;
     *out = h;
@@ -350,13 +503,14 @@ adacomp_status adacomp_grad_norm(adacomp_adamw_t h, const void* const* grad, flo
     tab->part = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + 16);
     uint32_t parts = 0;
     adacomp_status st = ADACOMP_OK;
-    for (int k = 0; k < 2 && st == ADACOMP_OK; ++k)
-        st = for_runs(h, h->by_g[k], kNormTensors, [&](size_t i, size_t j, uint32_t tiles) {
+    for (int k = 0; k < 2 && st == ADACOMP_OK; ++k) {
+        const auto tiles_of = [&](size_t id) { return norm_tiles(h->n[id], k); };
+        st = for_runs(h->by_g[k], kNormTensors, tiles_of, [&](size_t i, size_t j, uint32_t tiles) {
             uint32_t tile = 0;
             for (size_t q = i; q < j; ++q) {
                 const size_t id = (size_t)h->by_g[k][q];
                 tab->t[q - i] = {grad[id], h->n[id], tile};
-                tile += tiles_of(h->n[id]);
+                tile += tiles_of(id);
             }
             const uint32_t grid = tiles < (uint32_t)kNormGrid ? tiles : (uint32_t)kNormGrid;
             tab->count = (int32_t)(j - i);
@@ -366,6 +520,7 @@ adacomp_status adacomp_grad_norm(adacomp_adamw_t h, const void* const* grad, flo
             return launch_result(launch_after(k ? grad_norm_kernel<bf16> : grad_norm_kernel<float>, dim3(grid),
                                               dim3(kAwThreads), 0, stream, *tab), stream);
         });
+    }
     delete tab;
     return st;
 }
@@ -403,8 +558,9 @@ adacomp_status adacomp_adamw_step(adacomp_adamw_t h, void* const* weight, const 
     tab->scale = grad_scale;
     tab->coefficient = coefficient;
     adacomp_status st = ADACOMP_OK;
+    const auto tiles_of = [&](size_t id) { return step_tiles(h->n[id]); };
     for (int k = 0; k < 4 && st == ADACOMP_OK; ++k)
-        st = for_runs(h, h->by_wg[k], kAwTensors, [&](size_t i, size_t j, uint32_t tiles) {
+        st = for_runs(h->by_wg[k], kAwTensors, tiles_of, [&](size_t i, size_t j, uint32_t tiles) {
             uint32_t tile = 0;
             for (size_t q = i; q < j; ++q) {
                 const size_t id = (size_t)h->by_wg[k][q];
@@ -419,7 +575,7 @@ adacomp_status adacomp_adamw_step(adacomp_adamw_t h, void* const* weight, const 
                 t.n = h->n[id];
                 t.tile_begin = tile;
                 t.decay = (float)(1.0 - (double)lr * (double)h->weight_decay[id]);
-                tile += tiles_of(t.n);
+                tile += tiles_of(id);
             }
             tab->count = (int32_t)(j - i);
             const cudaError_t e = k == 0   ? step_launch<float, float>(tab, tiles, eight, stream)
