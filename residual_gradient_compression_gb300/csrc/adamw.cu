@@ -32,7 +32,8 @@ struct AwTensor {
 struct AwTable {
     AwTensor t[kAwTensors];
     int32_t count;
-    float beta1, beta2, rest1, rest2, step, root, eps, scale;
+    int32_t fast;  // eps and root lie where the step's own root and quotient are exact (adam_lane)
+    float beta1, beta2, rest1, rest2, step, root, eps, one, scale;
     const float* coefficient;
 };
 static_assert(sizeof(AwTable) <= 32764, "kernel parameters");
@@ -103,10 +104,10 @@ __device__ __forceinline__ Scales scales_of(uint32_t bits)
 
 // ---------------------------------------------------------------- step
 struct Adam {
-    float c, beta1, beta2, rest1, rest2, step, root, eps, decay;
+    float c, beta1, beta2, rest1, rest2, step, root, eps, one, decay;
 };
 
-// One element: the new m, v's root u and the weight, from m, v, the gradient and the weight.
+// One element: the new m, v, its root u and the weight, from m, v, the gradient and the weight.
 __device__ __forceinline__ void adam(const Adam& k, float g, float& m, float& v, float& u, float& w)
 {
     g = __fmul_rn(k.c, g);
@@ -117,8 +118,86 @@ __device__ __forceinline__ void adam(const Adam& k, float g, float& m, float& v,
     w = __fsub_rn(__fmul_rn(k.decay, w), __fmul_rn(k.step, q));
 }
 
+// Two fp32 values that one instruction computes with. Every operation rounds as its scalar
+// form does (.rn: no contraction).
+struct Pair {
+    unsigned long long b;
+};
+
+__device__ __forceinline__ Pair pair(float x, float y)
+{
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.b) : "f"(x), "f"(y));
+    return p;
+}
+
+__device__ __forceinline__ Pair pair(float x) { return pair(x, x); }
+
+__device__ __forceinline__ void split(Pair p, float& x, float& y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.b));
+}
+
+__device__ __forceinline__ Pair operator*(Pair x, Pair y)
+{
+    Pair p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.b) : "l"(x.b), "l"(y.b));
+    return p;
+}
+
+__device__ __forceinline__ Pair fma2(Pair x, Pair y, Pair z)
+{
+    Pair p;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.b) : "l"(x.b), "l"(y.b), "l"(z.b));
+    return p;
+}
+
+// The sum of two products, each rounded before it: `one` is 1, which the compiler does not
+// know. It fuses add.rn.f32x2 with mul.rn.f32x2 (seen with CUDA 13.0), but not this.
+__device__ __forceinline__ Pair sum2(Pair x, Pair y, Pair one) { return fma2(x, one, y); }
+
+// The correctly rounded root of two values within 2^+-60: s = v * rsqrt(v), and one Newton
+// step with the residual v - s * s from a fused multiply-add (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990). That the step rounds
+// as sqrt does was checked for every significand of both parities of the exponent.
+__device__ __forceinline__ Pair root2(Pair v)
+{
+    float x, y;
+    split(v, x, y);
+    asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(x));
+    asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(y));
+    const Pair r = pair(x, y);
+    const Pair s = v * r, minus = s * pair(-1.0f);
+    return fma2(fma2(minus, s, v), r * pair(0.5f), s);
+}
+
+// The correctly rounded quotients a / b of values within 2^+-60 (or a = 0): with y the
+// correctly rounded reciprocal (one Newton step on the approximate one; checked for every
+// significand) and q = a * y, the residual r = a - b * q is exact and q + r * y rounds as
+// a / b does (Markstein's theorem, same paper). The signs are placed so that a zero a keeps
+// its own.
+__device__ __forceinline__ Pair quotient2(Pair a, Pair b)
+{
+    float x, y;
+    split(b, x, y);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y));
+    Pair n = pair(-x, -y);  // about -1 / b
+    n = fma2(fma2(b, n, pair(1.0f)), n, n);
+    const Pair minus = a * pair(-1.0f);
+    const Pair q = minus * n;
+    return fma2(fma2(b, q, minus), n, q);
+}
+
+__device__ __forceinline__ float top3(float x, float y, float z)  // the largest magnitude; NaN if one is
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 // Four consecutive elements. Past a tensor's end they read as zero and are not written.
-__device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, float (&v)[4])
+__device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, float* v)
 {
     if (i + 4 <= n) {
         const float4 q = *reinterpret_cast<const float4*>(p + i);
@@ -129,7 +208,7 @@ __device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, floa
     for (int j = 0; j < 4; ++j) v[j] = i + j < n ? p[i + j] : 0.0f;
 }
 
-__device__ __forceinline__ void load4(const bf16* p, int64_t i, int64_t n, float (&v)[4])
+__device__ __forceinline__ void load4(const bf16* p, int64_t i, int64_t n, float* v)
 {
     if (i + 4 <= n) {
         const uint2 q = *reinterpret_cast<const uint2*>(p + i);
@@ -151,7 +230,7 @@ __device__ __forceinline__ uint32_t load4(const uint8_t* p, int64_t i, int64_t n
     return r;
 }
 
-__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const float (&v)[4])
+__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const float* v)
 {
     if (i + 4 <= n) {
         *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
@@ -162,7 +241,7 @@ __device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const flo
         if (i + j < n) p[i + j] = v[j];
 }
 
-__device__ __forceinline__ void store4(bf16* p, int64_t i, int64_t n, const float (&v)[4])
+__device__ __forceinline__ void store4(bf16* p, int64_t i, int64_t n, const float* v)
 {
     if (i + 4 <= n) {
         const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
@@ -186,12 +265,60 @@ __device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, uint32_
         if (i + j < n) p[i + j] = (uint8_t)(v >> (8 * j));
 }
 
+constexpr int kAwEach = kAwBlock / 32;  // elements of a lane
+
+// The step on a lane's elements, two at a time. Where all of them lie in the range of
+// root2 and quotient2 (v and |m| within 2^+-60, or m zero, and the bounds that the host
+// keeps on eps and root: `fast`), those are used; otherwise the scalar operations are.
+// v is left as its root when kRoot.
+template <bool kRoot>
+__device__ __forceinline__ void adam_lane(const Adam& k, bool fast, const float (&g)[kAwEach], float (&m)[kAwEach],
+                                          float (&v)[kAwEach], float (&w)[kAwEach], float& mtop, float& vtop)
+{
+    float vlow = INFINITY;
+    uint32_t mlow = 0xffffffffu;  // of the bits without the sign, minus one: zero does not count
+    const Pair one = pair(k.one);
+    Pair m2[kAwEach / 2], v2[kAwEach / 2];
+    mtop = vtop = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kAwEach / 2; ++j) {
+        const Pair d = pair(k.c) * pair(g[2 * j], g[2 * j + 1]);
+        m2[j] = sum2(pair(k.beta1) * pair(m[2 * j], m[2 * j + 1]), pair(k.rest1) * d, one);
+        v2[j] = sum2(pair(k.beta2) * pair(v[2 * j], v[2 * j + 1]), pair(k.rest2) * (d * d), one);
+        float x, y, p, q;
+        split(m2[j], x, y);
+        split(v2[j], p, q);
+        mtop = top3(mtop, x, y);
+        vtop = top3(vtop, p, q);
+        vlow = fminf(vlow, fminf(p, q));
+        mlow = min(mlow, min(2u * __float_as_uint(x) - 1u, 2u * __float_as_uint(y) - 1u));
+    }
+    constexpr float kLow = 0x1p-60f, kHigh = 0x1p60f;
+    if (fast && vlow >= kLow && vtop <= kHigh && mtop <= kHigh && mlow >= 2u * 0x21800000u - 1u) {  // 0x21800000: 2^-60
+#pragma unroll
+        for (int j = 0; j < kAwEach / 2; ++j) {
+            const Pair u = root2(v2[j]);
+            const Pair q = quotient2(m2[j], sum2(u * pair(k.root), pair(k.eps), one));
+            const Pair x = sum2(pair(k.decay) * pair(w[2 * j], w[2 * j + 1]), pair(-k.step) * q, one);
+            split(x, w[2 * j], w[2 * j + 1]);
+            split(m2[j], m[2 * j], m[2 * j + 1]);
+            split(kRoot ? u : v2[j], v[2 * j], v[2 * j + 1]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kAwEach; ++j) {  // unrolled: the elements are in registers
+        float u;
+        adam(k, g[j], m[j], v[j], u, w[j]);
+        if (kRoot) v[j] = u;
+    }
+}
+
 // One warp per block of 256 elements, a tile of eight blocks per CTA; a lane has four
 // elements of either half of its block, so that every access of a warp is contiguous.
 template <typename W, typename G, bool kEight>
 __global__ void __launch_bounds__(kAwThreads) adamw_kernel(const __grid_constant__ AwTable tab)
 {
-    constexpr int kParts = kAwBlock / 128;
     ptx::griddep_wait();
     const AwTensor& t = tab.t[owner_of(tab, blockIdx.x)];
     const int64_t block = (int64_t)(blockIdx.x - t.tile_begin) * kAwWarps + (threadIdx.x >> 5);
@@ -200,72 +327,68 @@ __global__ void __launch_bounds__(kAwThreads) adamw_kernel(const __grid_constant
     W* w = static_cast<W*>(t.w);
     const G* g = static_cast<const G*>(t.g);
     bf16* copy = static_cast<bf16*>(t.copy);
-    float wv[kParts][4], gv[kParts][4], mv[kParts][4], vv[kParts][4], ms, us;
-    uint32_t mc[kParts], uc[kParts];
+    float wv[kAwEach], gv[kAwEach], mv[kAwEach], vv[kAwEach], ms = 0.0f, us = 0.0f;
+    uint32_t mc[2], uc[2];
 #pragma unroll
-    for (int k = 0; k < kParts; ++k) {
+    for (int k = 0; k < 2; ++k) {
         const int64_t i = first + k * 128;
-        load4(w, i, n, wv[k]);
-        load4(g, i, n, gv[k]);
+        load4(w, i, n, wv + 4 * k);
+        load4(g, i, n, gv + 4 * k);
         if (kEight) {
             mc[k] = load4(static_cast<const uint8_t*>(t.m), i, n);
             uc[k] = load4(static_cast<const uint8_t*>(t.v), i, n);
         } else {
-            load4(static_cast<const float*>(t.m), i, n, mv[k]);
-            load4(static_cast<const float*>(t.v), i, n, vv[k]);
+            load4(static_cast<const float*>(t.m), i, n, mv + 4 * k);
+            load4(static_cast<const float*>(t.v), i, n, vv + 4 * k);
         }
     }
     if (kEight) {
         ms = t.ms[block];
         us = t.vs[block];
     }
-    Adam a = {tab.scale, tab.beta1, tab.beta2, tab.rest1, tab.rest2, tab.step, tab.root, tab.eps, t.decay};
+    Adam a = {tab.scale, tab.beta1, tab.beta2, tab.rest1, tab.rest2, tab.step, tab.root, tab.eps, tab.one, t.decay};
     if (tab.coefficient) a.c = *tab.coefficient;
     if (!isfinite(a.c)) return;
-    uint32_t mtop = 0, utop = 0;
+    if (kEight) {
 #pragma unroll
-    for (int k = 0; k < kParts; ++k) {
+        for (int j = 0; j < kAwEach / 2; ++j) {
+            const float2 m = from_e4m3x2(mc[j / 2] >> (16 * (j & 1))), u = from_e4m3x2(uc[j / 2] >> (16 * (j & 1)));
+            split(pair(m.x, m.y) * pair(ms), mv[2 * j], mv[2 * j + 1]);
+            const Pair r = pair(u.x, u.y) * pair(us);
+            split(r * r, vv[2 * j], vv[2 * j + 1]);
+        }
+    }
+    float mtop, vtop;
+    adam_lane<kEight>(a, tab.fast != 0, gv, mv, vv, wv, mtop, vtop);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
         const int64_t i = first + k * 128;
-        if (kEight) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float2 m = from_e4m3x2(mc[k] >> (16 * j)), u = from_e4m3x2(uc[k] >> (16 * j));
-                mv[k][2 * j] = __fmul_rn(m.x, ms), mv[k][2 * j + 1] = __fmul_rn(m.y, ms);
-                const float x = __fmul_rn(u.x, us), y = __fmul_rn(u.y, us);
-                vv[k][2 * j] = __fmul_rn(x, x), vv[k][2 * j + 1] = __fmul_rn(y, y);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float u;
-            adam(a, gv[k][j], mv[k][j], vv[k][j], u, wv[k][j]);
-            if (kEight) {
-                vv[k][j] = u;
-                mtop = max(mtop, __float_as_uint(mv[k][j]) & 0x7fffffffu);
-                utop = max(utop, __float_as_uint(u) & 0x7fffffffu);
-            }
-        }
-        store4(w, i, n, wv[k]);
-        if (copy) store4(copy, i, n, wv[k]);
+        store4(w, i, n, wv + 4 * k);
+        if (copy) store4(copy, i, n, wv + 4 * k);
         if (!kEight) {
-            store4(static_cast<float*>(t.m), i, n, mv[k]);
-            store4(static_cast<float*>(t.v), i, n, vv[k]);
+            store4(static_cast<float*>(t.m), i, n, mv + 4 * k);
+            store4(static_cast<float*>(t.v), i, n, vv + 4 * k);
         }
     }
     if (!kEight) return;
-    const Scales p = scales_of(__reduce_max_sync(0xffffffffu, mtop));
-    const Scales q = scales_of(__reduce_max_sync(0xffffffffu, utop));
+    // magnitudes order as their bits do; the largest root is the root of the largest v
+    const Scales p = scales_of(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
+    const Scales q =
+        scales_of(__float_as_uint(__fsqrt_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop))))));
 #pragma unroll
-    for (int k = 0; k < kParts; ++k) {
+    for (int k = 0; k < 2; ++k) {
         uint32_t m = 0, u = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            m |= to_e4m3x2(__fmul_rn(mv[k][2 * j], p.inverse), __fmul_rn(mv[k][2 * j + 1], p.inverse)) << (16 * j);
-            u |= to_e4m3x2(__fmul_rn(vv[k][2 * j], q.inverse), __fmul_rn(vv[k][2 * j + 1], q.inverse)) << (16 * j);
+            const int e = 4 * k + 2 * j;
+            float x, y;
+            split(pair(mv[e], mv[e + 1]) * pair(p.inverse), x, y);
+            m |= to_e4m3x2(x, y) << (16 * j);
+            split(pair(vv[e], vv[e + 1]) * pair(q.inverse), x, y);
+            if (vv[e] > 0.0f) x = fmaxf(x, 0x1p-9f);  // the smallest e4m3: a root that is not zero does not become so
+            if (vv[e + 1] > 0.0f) y = fmaxf(y, 0x1p-9f);
+            u |= to_e4m3x2(x, y) << (16 * j);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if ((u >> (8 * j) & 0xffu) == 0 && vv[k][j] > 0.0f) u |= 1u << (8 * j);
         store4(static_cast<uint8_t*>(t.m), first + k * 128, n, m);
         store4(static_cast<uint8_t*>(t.v), first + k * 128, n, u);
     }
@@ -555,6 +678,9 @@ adacomp_status adacomp_adamw_step(adacomp_adamw_t h, void* const* weight, const 
     tab->step = (float)((double)lr / (double)bias_correction1);
     tab->root = (float)(1.0 / std::sqrt((double)bias_correction2));
     tab->eps = eps;
+    tab->one = 1.0f;
+    // u <= 2^30 in adam_lane's range, so that u * root + eps lies within 2^+-40
+    tab->fast = eps >= 0x1p-40f && eps <= 0x1p30f && tab->root <= 0x1p9f;
     tab->scale = grad_scale;
     tab->coefficient = coefficient;
     adacomp_status st = ADACOMP_OK;

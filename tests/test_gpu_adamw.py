@@ -198,6 +198,48 @@ def test_against_64_bits(bits):
             assert float(off.float().mean()) < 1e-3  # but for ties that rounding moves, the nearest number
 
 
+@pytest.mark.parametrize("exponent", [0, -31, 29, -59])
+def test_root_and_quotient_round_correctly_for_every_significand(exponent):
+    """beta2 = 0.5 and no gradient: v = 2^exponent * [1, 4), all 2^24 values; lr * weight_decay
+    = 1 and w = 0 leave w = -m / (u + eps), whose rounding torch's root and quotient give."""
+    n = 1 << 24
+    h = ac.adacomp_adamw_init([n], [ac.F32], [ac.F32], [1.0], 32)
+    v = (torch.arange(n, dtype=torch.int32, device="cuda") + ((127 + exponent) << 23)).view(F)
+    want_v = v.clone()
+    v *= 2.0
+    gen = _gen(exponent + 100)
+    m = torch.randn(n, generator=gen, device="cuda") * torch.exp2(
+        torch.randint(-55, 55, (n,), generator=gen, device="cuda").float())
+    m[::1001] = 0.0
+    m[1::1003] = -0.0
+    w, g = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    want = -((m * 0.5) / (torch.sqrt(want_v) + 2.0 ** -40))
+    ac.adacomp_adamw_step(h, [w], [g], [m], [v], 1.0, 0.5, 0.5, 2.0 ** -40, 1.0, 1.0)
+    assert torch.equal(v, want_v)
+    assert torch.equal(w, want)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_values_outside_the_usual_range(bits):
+    """Moments and constants from one end of fp32 to the other, elements of both kinds in one lane."""
+    n = 1 << 16
+    net = Net([n], [F], [F], bits, seed=5)
+    gen = _gen(77)
+    net.g[0].copy_(torch.randn(n, generator=gen, device="cuda") * torch.exp2(
+        torch.randint(-70, 62, (n,), generator=gen, device="cuda").float()))
+    net.g[0][::5] = 0.0
+    if bits == 32:
+        net.m[0].copy_(torch.randn(n, generator=gen, device="cuda") * torch.exp2(
+            torch.randint(-148, 100, (n,), generator=gen, device="cuda").float()))
+        net.v[0].copy_(torch.rand(n, generator=gen, device="cuda") * torch.exp2(
+            torch.randint(-148, 126, (n,), generator=gen, device="cuda").float()))
+        net.v[0][::7] = 0.0
+    for t in (1, 2, 1000):
+        ref = net.expected(t)
+        net.step(t)
+        _same(net.state(), ref, f"step {t}")
+
+
 def test_eight_bit_blocks_of_zeros_tiny_huge_and_few_values():
     n = 256 * 8 + 5
     net = Net([n], [F], [F], 8, fresh=True)
