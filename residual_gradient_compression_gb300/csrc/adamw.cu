@@ -2,6 +2,7 @@
 // 32 or in 8 bits: kernels and C entry points (adacomp.h).
 #include <cstring>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include <cuda_fp16.h>
@@ -32,6 +33,7 @@ struct AwTensor {
 struct AwTable {
     AwTensor t[kAwTensors];
     int32_t count;
+    uint32_t tiles;  // of this launch
     int32_t fast;  // eps and root lie where the step's own root and quotient are exact (adam_lane)
     float beta1, beta2, rest1, rest2, step, root, eps, one, scale;
     const float* coefficient;
@@ -196,38 +198,45 @@ __device__ __forceinline__ float top3(float x, float y, float z)  // the largest
     return r;
 }
 
-// Four consecutive elements. Past a tensor's end they read as zero and are not written.
-__device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, float* v)
-{
-    if (i + 4 <= n) {
-        const float4 q = *reinterpret_cast<const float4*>(p + i);
-        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = i + j < n ? p[i + j] : 0.0f;
-}
+// Four consecutive elements as they lie in memory. Past a tensor's end they read as zero
+// and are not written.
+template <typename T> struct Four;
+template <> struct Four<float> {
+    uint4 q;
+};
+template <> struct Four<bf16> {
+    uint2 q;
+};
+template <> struct Four<uint8_t> {
+    uint32_t q;
+};
 
-__device__ __forceinline__ void load4(const bf16* p, int64_t i, int64_t n, float* v)
+template <typename T> __device__ __forceinline__ Four<T> load4(const void* base, int64_t i, int64_t n)
 {
-    if (i + 4 <= n) {
-        const uint2 q = *reinterpret_cast<const uint2*>(p + i);
-        v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
-        v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = i + j < n ? to_f32(p[i + j]) : 0.0f;
-}
-
-__device__ __forceinline__ uint32_t load4(const uint8_t* p, int64_t i, int64_t n)
-{
-    if (i + 4 <= n) return *reinterpret_cast<const uint32_t*>(p + i);
-    uint32_t r = 0;
+    const T* p = static_cast<const T*>(base);
+    if (i + 4 <= n) return *reinterpret_cast<const Four<T>*>(p + i);
+    Four<T> r = {};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        if (i + j < n) r |= (uint32_t)p[i + j] << (8 * j);
+        if (i + j < n) {
+            if constexpr (sizeof(T) == 4) (&r.q.x)[j] = reinterpret_cast<const uint32_t*>(p)[i + j];
+            else if constexpr (sizeof(T) == 2)
+                (&r.q.x)[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i + j] << (16 * (j & 1));
+            else r.q |= (uint32_t)p[i + j] << (8 * j);
+        }
     return r;
+}
+
+__device__ __forceinline__ void widen(const Four<float>& r, float* v)
+{
+    v[0] = __uint_as_float(r.q.x), v[1] = __uint_as_float(r.q.y);
+    v[2] = __uint_as_float(r.q.z), v[3] = __uint_as_float(r.q.w);
+}
+
+__device__ __forceinline__ void widen(const Four<bf16>& r, float* v)
+{
+    v[0] = __uint_as_float(r.q.x << 16), v[1] = __uint_as_float(r.q.x & 0xffff0000u);
+    v[2] = __uint_as_float(r.q.y << 16), v[3] = __uint_as_float(r.q.y & 0xffff0000u);
 }
 
 __device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const float* v)
@@ -314,56 +323,66 @@ __device__ __forceinline__ void adam_lane(const Adam& k, bool fast, const float 
     }
 }
 
-// One warp per block of 256 elements, a tile of eight blocks per CTA; a lane has four
-// elements of either half of its block, so that every access of a warp is contiguous.
-template <typename W, typename G, bool kEight>
-__global__ void __launch_bounds__(kAwThreads) adamw_kernel(const __grid_constant__ AwTable tab)
-{
-    ptx::griddep_wait();
-    const AwTensor& t = tab.t[owner_of(tab, blockIdx.x)];
-    const int64_t block = (int64_t)(blockIdx.x - t.tile_begin) * kAwWarps + (threadIdx.x >> 5);
-    const int64_t n = t.n, first = block * kAwBlock + (threadIdx.x & 31) * 4;
-    if (block * kAwBlock >= n) return;
-    W* w = static_cast<W*>(t.w);
-    const G* g = static_cast<const G*>(t.g);
-    bf16* copy = static_cast<bf16*>(t.copy);
-    float wv[kAwEach], gv[kAwEach], mv[kAwEach], vv[kAwEach], ms = 0.0f, us = 0.0f;
-    uint32_t mc[2], uc[2];
+// A lane's part of a block, as it lies in memory: four elements of either half, so that
+// every access of a warp is contiguous.
+template <typename W, typename G, bool kEight> struct Part {
+    using S = typename std::conditional<kEight, uint8_t, float>::type;
+    Four<W> w[2];
+    Four<G> g[2];
+    Four<S> m[2], v[2];
+    float ms, vs;
+
+    __device__ __forceinline__ void load(const AwTensor& t, int64_t block)
+    {
+        if (block * kAwBlock >= t.n) return;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int64_t i = first + k * 128;
-        load4(w, i, n, wv + 4 * k);
-        load4(g, i, n, gv + 4 * k);
+        for (int k = 0; k < 2; ++k) {
+            const int64_t i = block * kAwBlock + (threadIdx.x & 31) * 4 + k * 128;
+            w[k] = load4<W>(t.w, i, t.n);
+            g[k] = load4<G>(t.g, i, t.n);
+            m[k] = load4<S>(t.m, i, t.n);
+            v[k] = load4<S>(t.v, i, t.n);
+        }
         if (kEight) {
-            mc[k] = load4(static_cast<const uint8_t*>(t.m), i, n);
-            uc[k] = load4(static_cast<const uint8_t*>(t.v), i, n);
-        } else {
-            load4(static_cast<const float*>(t.m), i, n, mv + 4 * k);
-            load4(static_cast<const float*>(t.v), i, n, vv + 4 * k);
+            ms = t.ms[block];
+            vs = t.vs[block];
         }
     }
-    if (kEight) {
-        ms = t.ms[block];
-        us = t.vs[block];
-    }
-    Adam a = {tab.scale, tab.beta1, tab.beta2, tab.rest1, tab.rest2, tab.step, tab.root, tab.eps, tab.one, t.decay};
-    if (tab.coefficient) a.c = *tab.coefficient;
-    if (!isfinite(a.c)) return;
-    if (kEight) {
+};
+
+template <typename W, typename G, bool kEight>
+__device__ __forceinline__ void adamw_block(const AwTensor& t, int64_t block, const Part<W, G, kEight>& r, Adam a,
+                                            bool fast)
+{
+    const int64_t n = t.n, first = block * kAwBlock + (threadIdx.x & 31) * 4;
+    if (block * kAwBlock >= n) return;
+    a.decay = t.decay;
+    bf16* copy = static_cast<bf16*>(t.copy);
+    float wv[kAwEach], gv[kAwEach], mv[kAwEach], vv[kAwEach];
 #pragma unroll
-        for (int j = 0; j < kAwEach / 2; ++j) {
-            const float2 m = from_e4m3x2(mc[j / 2] >> (16 * (j & 1))), u = from_e4m3x2(uc[j / 2] >> (16 * (j & 1)));
-            split(pair(m.x, m.y) * pair(ms), mv[2 * j], mv[2 * j + 1]);
-            const Pair r = pair(u.x, u.y) * pair(us);
-            split(r * r, vv[2 * j], vv[2 * j + 1]);
+    for (int k = 0; k < 2; ++k) {
+        widen(r.w[k], wv + 4 * k);
+        widen(r.g[k], gv + 4 * k);
+        if constexpr (kEight) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int e = 4 * k + 2 * j;
+                const float2 m = from_e4m3x2(r.m[k].q >> (16 * j)), u = from_e4m3x2(r.v[k].q >> (16 * j));
+                split(pair(m.x, m.y) * pair(r.ms), mv[e], mv[e + 1]);
+                const Pair x = pair(u.x, u.y) * pair(r.vs);
+                split(x * x, vv[e], vv[e + 1]);
+            }
+        } else {
+            widen(r.m[k], mv + 4 * k);
+            widen(r.v[k], vv + 4 * k);
         }
     }
     float mtop, vtop;
-    adam_lane<kEight>(a, tab.fast != 0, gv, mv, vv, wv, mtop, vtop);
+    adam_lane<kEight>(a, fast, gv, mv, vv, wv, mtop, vtop);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int64_t i = first + k * 128;
-        store4(w, i, n, wv + 4 * k);
+        store4(static_cast<W*>(t.w), i, n, wv + 4 * k);
         if (copy) store4(copy, i, n, wv + 4 * k);
         if (!kEight) {
             store4(static_cast<float*>(t.m), i, n, mv + 4 * k);
@@ -395,6 +414,60 @@ __global__ void __launch_bounds__(kAwThreads) adamw_kernel(const __grid_constant
     if ((threadIdx.x & 31) == 0) {
         t.ms[block] = p.scale;
         t.vs[block] = q.scale;
+    }
+}
+
+// The tensor of consecutive tiles.
+template <typename Table> struct Cursor {
+    int id;
+    uint32_t next;  // where the next tensor begins
+
+    __device__ __forceinline__ Cursor(const Table& tab, uint32_t tile) : id(owner_of(tab, tile)) { bound(tab); }
+    __device__ __forceinline__ void bound(const Table& tab)
+    {
+        next = id + 1 < tab.count ? tab.t[id + 1].tile_begin : 0xffffffffu;
+    }
+    __device__ __forceinline__ void to(const Table& tab, uint32_t tile)
+    {
+        if (tile < next) return;
+        ++id;
+        bound(tab);
+    }
+};
+
+// One warp per block of 256 elements, a tile of eight blocks per CTA and turn; a CTA takes
+// a run of consecutive tiles. With 8-bit states the next tile's loads are issued before the
+// current one is computed: a block is 2 KB of loads for some 500 instructions, so that
+// warps that wait for their own loads alone leave the memory idle. 32-bit states (one tile
+// per CTA) fill it with the loads of their other warps.
+template <typename W, typename G, bool kEight>
+__global__ void __launch_bounds__(kAwThreads) adamw_kernel(const __grid_constant__ AwTable tab)
+{
+    ptx::griddep_wait();
+    const int warp = threadIdx.x >> 5;
+    uint32_t tile = (uint32_t)((uint64_t)tab.tiles * blockIdx.x / gridDim.x);
+    const uint32_t end = (uint32_t)((uint64_t)tab.tiles * (blockIdx.x + 1) / gridDim.x);
+    Cursor<AwTable> at(tab, tile);
+    const auto block_of = [&](const AwTensor& t, uint32_t i) { return (int64_t)(i - t.tile_begin) * kAwWarps + warp; };
+    Part<W, G, kEight> now, next;
+    const AwTensor* t = &tab.t[at.id];
+    now.load(*t, block_of(*t, tile));
+    Adam a = {tab.scale, tab.beta1, tab.beta2, tab.rest1, tab.rest2, tab.step, tab.root, tab.eps, tab.one, 1.0f};
+    if (tab.coefficient) a.c = *tab.coefficient;
+    if (!isfinite(a.c)) return;
+    while (true) {
+        const AwTensor* t_next = t;
+        const bool more = kEight && tile + 1 < end;
+        if (more) {
+            at.to(tab, tile + 1);
+            t_next = &tab.t[at.id];
+            next.load(*t_next, block_of(*t_next, tile + 1));
+        }
+        adamw_block(*t, block_of(*t, tile), now, a, tab.fast != 0);
+        if (!more) break;
+        now = next;
+        t = t_next;
+        ++tile;
     }
 }
 
@@ -446,14 +519,10 @@ __global__ void __launch_bounds__(kAwThreads, 6) grad_norm_kernel(const __grid_c
     double sum = 0.0;
     uint32_t tile = (uint32_t)((uint64_t)tab.tiles * blockIdx.x / gridDim.x);
     const uint32_t end = (uint32_t)((uint64_t)tab.tiles * (blockIdx.x + 1) / gridDim.x);
-    int id = owner_of(tab, tile);
-    uint32_t next = id + 1 < tab.count ? tab.t[id + 1].tile_begin : tab.tiles;
+    Cursor<NormTable> at(tab, tile);
     for (; tile < end; ++tile) {
-        if (tile >= next) {
-            ++id;
-            next = id + 1 < tab.count ? tab.t[id + 1].tile_begin : tab.tiles;
-        }
-        const NormTensor& t = tab.t[id];
+        at.to(tab, tile);
+        const NormTensor& t = tab.t[at.id];
         const G* g = static_cast<const G*>(t.g);
         const int64_t first = (int64_t)(tile - t.tile_begin) * (kNormVectors * kAwThreads * kPer) + threadIdx.x * kPer;
         uint32_t word[kNormVectors][4];
@@ -553,10 +622,17 @@ template <typename T, typename F> adacomp_status for_runs(const std::vector<int3
     return ADACOMP_OK;
 }
 
-template <typename W, typename G> cudaError_t step_launch(const AwTable* tab, uint32_t tiles, bool eight, cudaStream_t s)
+template <typename W, typename G> cudaError_t step_launch(const AwTable* tab, bool eight, cudaStream_t stream)
 {
-    return launch_after(eight ? adamw_kernel<W, G, true> : adamw_kernel<W, G, false>, dim3(tiles), dim3(kAwThreads), 0,
-                        s, *tab);
+    if (!eight) return launch_after(adamw_kernel<W, G, false>, dim3(tab->tiles), dim3(kAwThreads), 0, stream, *tab);
+    int sms = 0, per = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, adamw_kernel<W, G, true>, kAwThreads, 0);
+    if (e != cudaSuccess) return e;
+    const uint32_t most = (uint32_t)(sms * (per > 0 ? per : 1));
+    return launch_after(adamw_kernel<W, G, true>, dim3(tab->tiles < most ? tab->tiles : most), dim3(kAwThreads), 0,
+                        stream, *tab);
 }
 
 }  // namespace
@@ -704,10 +780,11 @@ adacomp_status adacomp_adamw_step(adacomp_adamw_t h, void* const* weight, const 
                 tile += tiles_of(id);
             }
             tab->count = (int32_t)(j - i);
-            const cudaError_t e = k == 0   ? step_launch<float, float>(tab, tiles, eight, stream)
-                                  : k == 1 ? step_launch<float, bf16>(tab, tiles, eight, stream)
-                                  : k == 2 ? step_launch<bf16, float>(tab, tiles, eight, stream)
-                                           : step_launch<bf16, bf16>(tab, tiles, eight, stream);
+            tab->tiles = tiles;
+            const cudaError_t e = k == 0   ? step_launch<float, float>(tab, eight, stream)
+                                  : k == 1 ? step_launch<float, bf16>(tab, eight, stream)
+                                  : k == 2 ? step_launch<bf16, float>(tab, eight, stream)
+                                           : step_launch<bf16, bf16>(tab, eight, stream);
             return launch_result(e, stream);
         });
     delete tab;
