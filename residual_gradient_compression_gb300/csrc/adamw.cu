@@ -17,9 +17,21 @@ constexpr int kAwWarps = kAwThreads / 32;
 constexpr int kAwBlock = ADACOMP_ADAMW_BLOCK;      // elements per scale, and per warp and turn
 constexpr int kAwTile = kAwWarps * kAwBlock;       // elements per CTA
 constexpr int kAwTensors = 400;                    // tensors per launch (a by-value kernel parameter)
-constexpr int kNormTensors = 1300;
+constexpr int kNormTensors = 1200;
+constexpr int kJumps = 1024;                       // see owner_of
 constexpr int kNormGrid = 912;                     // CTAs per launch at most (six per SM), each with a partial sum
 constexpr int kNormVectors = 4;                    // 16-byte vectors per thread and tile
+
+// Two fp32 values that one instruction computes with. Every operation rounds as its scalar
+// form does (.rn: no contraction).
+struct Pair {
+    unsigned long long b;
+};
+
+// The step's constants, each twice (as the paired operations take them from constant memory).
+struct Adam {
+    float c, beta1, beta2, rest1, rest2, step, root, eps, one, half, minus, decay;
+};
 
 struct AwTensor {
     void *w, *m, *v, *copy;
@@ -30,12 +42,19 @@ struct AwTensor {
     float decay;  // 1 - lr * weight_decay
 };
 
+struct Jumps {
+    int32_t shift;
+    uint16_t id[kJumps];  // the tensor of tile k << shift
+};
+
 struct AwTable {
     AwTensor t[kAwTensors];
+    Jumps jump;
     int32_t count;
     uint32_t tiles;  // of this launch
+    uint32_t ahead;  // tiles from a CTA's own to the one that it has brought into L2 (8-bit states)
     int32_t fast;  // eps and root lie where the step's own root and quotient are exact (adam_lane)
-    float beta1, beta2, rest1, rest2, step, root, eps, one, scale;
+    Adam k;          // its c and decay are filled in by the kernel
     const float* coefficient;
 };
 static_assert(sizeof(AwTable) <= 32764, "kernel parameters");
@@ -48,6 +67,7 @@ struct NormTensor {
 
 struct NormTable {
     NormTensor t[kNormTensors];
+    Jumps jump;
     int32_t count;
     uint32_t tiles;        // of this launch
     uint32_t first_part;   // where its partial sums start
@@ -59,16 +79,25 @@ struct NormTable {
 };
 static_assert(sizeof(NormTable) <= 32764, "kernel parameters");
 
-// The last tensor whose first tile is at or before `tile`.
+// The last tensor whose first tile is at or before `tile`: from the first tile's of its
+// stretch of 2^shift tiles on (a search by halves over hundreds of tensors is nine
+// dependent reads).
 template <typename Table> __device__ __forceinline__ int owner_of(const Table& tab, uint32_t tile)
 {
-    int lo = 0, hi = tab.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (tab.t[mid].tile_begin <= tile) lo = mid;
-        else hi = mid - 1;
+    int id = tab.jump.id[tile >> tab.jump.shift];
+    while (id + 1 < tab.count && tab.t[id + 1].tile_begin <= tile) ++id;
+    return id;
+}
+
+template <typename Table> void fill_jumps(Table* tab)
+{
+    int shift = 0, id = 0;
+    while ((tab->tiles - 1) >> shift >= (uint32_t)kJumps) ++shift;
+    tab->jump.shift = shift;
+    for (uint32_t k = 0; k <= (tab->tiles - 1) >> shift; ++k) {
+        while (id + 1 < tab->count && tab->t[id + 1].tile_begin <= k << shift) ++id;
+        tab->jump.id[k] = (uint16_t)id;
     }
-    return lo;
 }
 
 // ---------------------------------------------------------------- e4m3
@@ -87,45 +116,7 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c)
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-struct Scales {
-    float scale, inverse;
-};
-
-// The scale of a block whose largest magnitude is `top`, given as its bits (NaN is the
-// largest of all). Below 2^-96, where 448 / top would come near overflow, there is none.
-__device__ __forceinline__ Scales scales_of(uint32_t bits)
-{
-    const float top = __uint_as_float(bits);
-    Scales s = {0.0f, 0.0f};
-    if (!(top < 0x1p-96f)) {
-        s.scale = __fdiv_rn(top, 448.0f);
-        s.inverse = __fdiv_rn(448.0f, top);
-    }
-    return s;
-}
-
 // ---------------------------------------------------------------- step
-struct Adam {
-    float c, beta1, beta2, rest1, rest2, step, root, eps, one, decay;
-};
-
-// One element: the new m, v, its root u and the weight, from m, v, the gradient and the weight.
-__device__ __forceinline__ void adam(const Adam& k, float g, float& m, float& v, float& u, float& w)
-{
-    g = __fmul_rn(k.c, g);
-    m = __fadd_rn(__fmul_rn(k.beta1, m), __fmul_rn(k.rest1, g));
-    v = __fadd_rn(__fmul_rn(k.beta2, v), __fmul_rn(k.rest2, __fmul_rn(g, g)));
-    u = __fsqrt_rn(v);
-    const float q = __fdiv_rn(m, __fadd_rn(__fmul_rn(u, k.root), k.eps));
-    w = __fsub_rn(__fmul_rn(k.decay, w), __fmul_rn(k.step, q));
-}
-
-// Two fp32 values that one instruction computes with. Every operation rounds as its scalar
-// form does (.rn: no contraction).
-struct Pair {
-    unsigned long long b;
-};
-
 __device__ __forceinline__ Pair pair(float x, float y)
 {
     Pair p;
@@ -138,6 +129,14 @@ __device__ __forceinline__ Pair pair(float x) { return pair(x, x); }
 __device__ __forceinline__ void split(Pair p, float& x, float& y)
 {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.b));
+}
+
+// One element's root u of v, and its weight, by the scalar operations.
+__device__ __forceinline__ void root_and_weight(const Adam& k, float m, float v, float& u, float& w)
+{
+    u = __fsqrt_rn(v);
+    const float q = __fdiv_rn(m, __fadd_rn(__fmul_rn(u, k.root), k.eps));
+    w = __fsub_rn(__fmul_rn(k.decay, w), __fmul_rn(k.step, q));
 }
 
 __device__ __forceinline__ Pair operator*(Pair x, Pair y)
@@ -162,39 +161,45 @@ __device__ __forceinline__ Pair sum2(Pair x, Pair y, Pair one) { return fma2(x, 
 // step with the residual v - s * s from a fused multiply-add (P. Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990). That the step rounds
 // as sqrt does was checked for every significand of both parities of the exponent.
-__device__ __forceinline__ Pair root2(Pair v)
+__device__ __forceinline__ Pair root2(Pair v, const Adam& k)
 {
     float x, y;
     split(v, x, y);
     asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(x));
     asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(y));
     const Pair r = pair(x, y);
-    const Pair s = v * r, minus = s * pair(-1.0f);
-    return fma2(fma2(minus, s, v), r * pair(0.5f), s);
+    const Pair s = v * r, minus = s * pair(k.minus);
+    return fma2(fma2(minus, s, v), r * pair(k.half), s);
 }
 
-// The correctly rounded quotients a / b of values within 2^+-60 (or a = 0): with y the
-// correctly rounded reciprocal (one Newton step on the approximate one; checked for every
-// significand) and q = a * y, the residual r = a - b * q is exact and q + r * y rounds as
-// a / b does (Markstein's theorem, same paper). The signs are placed so that a zero a keeps
-// its own.
-__device__ __forceinline__ Pair quotient2(Pair a, Pair b)
+// The correctly rounded quotients -a / b of values within 2^+-60 (or a = 0): with n the
+// correctly rounded -1 / b (one Newton step on the approximate one; checked for every
+// significand) and q = a * n, the residual r = a + b * q is exact and q + r * n rounds as
+// -a / b does (Markstein's theorem, same paper), a zero with its sign.
+__device__ __forceinline__ Pair minus_quotient2(Pair a, Pair b, const Adam& k)
 {
     float x, y;
     split(b, x, y);
+    x = -x, y = -y;
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y));
-    Pair n = pair(-x, -y);  // about -1 / b
-    n = fma2(fma2(b, n, pair(1.0f)), n, n);
-    const Pair minus = a * pair(-1.0f);
-    const Pair q = minus * n;
-    return fma2(fma2(b, q, minus), n, q);
+    Pair n = pair(x, y);
+    n = fma2(fma2(b, n, pair(k.one)), n, n);
+    const Pair q = a * n;
+    return fma2(fma2(b, q, a), n, q);
 }
 
 __device__ __forceinline__ float top3(float x, float y, float z)  // the largest magnitude; NaN if one is
 {
     float r;
     asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+__device__ __forceinline__ float low3(float x, float y, float z)  // the smallest magnitude
+{
+    float r;
+    asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
 }
 
@@ -211,10 +216,10 @@ template <> struct Four<uint8_t> {
     uint32_t q;
 };
 
-template <typename T> __device__ __forceinline__ Four<T> load4(const void* base, int64_t i, int64_t n)
+template <bool kWhole, typename T> __device__ __forceinline__ Four<T> load4(const void* base, int64_t i, int64_t n)
 {
     const T* p = static_cast<const T*>(base);
-    if (i + 4 <= n) return *reinterpret_cast<const Four<T>*>(p + i);
+    if (kWhole || i + 4 <= n) return *reinterpret_cast<const Four<T>*>(p + i);
     Four<T> r = {};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -239,9 +244,9 @@ __device__ __forceinline__ void widen(const Four<bf16>& r, float* v)
     v[2] = __uint_as_float(r.q.y << 16), v[3] = __uint_as_float(r.q.y & 0xffff0000u);
 }
 
-__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const float* v)
+template <bool kWhole> __device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const float* v)
 {
-    if (i + 4 <= n) {
+    if (kWhole || i + 4 <= n) {
         *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
         return;
     }
@@ -250,9 +255,9 @@ __device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const flo
         if (i + j < n) p[i + j] = v[j];
 }
 
-__device__ __forceinline__ void store4(bf16* p, int64_t i, int64_t n, const float* v)
+template <bool kWhole> __device__ __forceinline__ void store4(bf16* p, int64_t i, int64_t n, const float* v)
 {
-    if (i + 4 <= n) {
+    if (kWhole || i + 4 <= n) {
         const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
         *reinterpret_cast<uint2*>(p + i) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
@@ -263,9 +268,9 @@ __device__ __forceinline__ void store4(bf16* p, int64_t i, int64_t n, const floa
         if (i + j < n) p[i + j] = from_f32<bf16>(v[j]);
 }
 
-__device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, uint32_t v)
+template <bool kWhole> __device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, uint32_t v)
 {
-    if (i + 4 <= n) {
+    if (kWhole || i + 4 <= n) {
         *reinterpret_cast<uint32_t*>(p + i) = v;
         return;
     }
@@ -275,52 +280,74 @@ __device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, uint32_
 }
 
 constexpr int kAwEach = kAwBlock / 32;  // elements of a lane
+constexpr float kLow = 0x1p-60f, kHigh = 0x1p60f;
 
-// The step on a lane's elements, two at a time. Where all of them lie in the range of
-// root2 and quotient2 (v and |m| within 2^+-60, or m zero, and the bounds that the host
-// keeps on eps and root: `fast`), those are used; otherwise the scalar operations are.
-// v is left as its root when kRoot.
+// The step on a lane's elements, two at a time. Where all of v and |m| lie in the range of
+// root2 and minus_quotient2 (2^+-60, with the bounds that the host keeps on eps and root:
+// `fast`), those are used; otherwise, also for zeros, the scalar operations are. v is left
+// as its root when kRoot. Returns whether all of v is positive for sure.
 template <bool kRoot>
-__device__ __forceinline__ void adam_lane(const Adam& k, bool fast, const float (&g)[kAwEach], float (&m)[kAwEach],
+__device__ __forceinline__ bool adam_lane(const Adam& k, bool fast, const float (&g)[kAwEach], float (&m)[kAwEach],
                                           float (&v)[kAwEach], float (&w)[kAwEach], float& mtop, float& vtop)
 {
-    float vlow = INFINITY;
-    uint32_t mlow = 0xffffffffu;  // of the bits without the sign, minus one: zero does not count
-    const Pair one = pair(k.one);
+    float mlow = kHigh, vlow = kHigh;
     Pair m2[kAwEach / 2], v2[kAwEach / 2];
     mtop = vtop = 0.0f;
 #pragma unroll
     for (int j = 0; j < kAwEach / 2; ++j) {
         const Pair d = pair(k.c) * pair(g[2 * j], g[2 * j + 1]);
-        m2[j] = sum2(pair(k.beta1) * pair(m[2 * j], m[2 * j + 1]), pair(k.rest1) * d, one);
-        v2[j] = sum2(pair(k.beta2) * pair(v[2 * j], v[2 * j + 1]), pair(k.rest2) * (d * d), one);
+        m2[j] = sum2(pair(k.beta1) * pair(m[2 * j], m[2 * j + 1]), pair(k.rest1) * d, pair(k.one));
+        v2[j] = sum2(pair(k.beta2) * pair(v[2 * j], v[2 * j + 1]), pair(k.rest2) * (d * d), pair(k.one));
         float x, y, p, q;
         split(m2[j], x, y);
         split(v2[j], p, q);
         mtop = top3(mtop, x, y);
         vtop = top3(vtop, p, q);
-        vlow = fminf(vlow, fminf(p, q));
-        mlow = min(mlow, min(2u * __float_as_uint(x) - 1u, 2u * __float_as_uint(y) - 1u));
+        mlow = low3(mlow, x, y);
+        vlow = low3(vlow, p, q);
     }
-    constexpr float kLow = 0x1p-60f, kHigh = 0x1p60f;
-    if (fast && vlow >= kLow && vtop <= kHigh && mtop <= kHigh && mlow >= 2u * 0x21800000u - 1u) {  // 0x21800000: 2^-60
+    if (fast && fminf(mlow, vlow) >= kLow && mtop <= kHigh && vtop <= kHigh) {
 #pragma unroll
         for (int j = 0; j < kAwEach / 2; ++j) {
-            const Pair u = root2(v2[j]);
-            const Pair q = quotient2(m2[j], sum2(u * pair(k.root), pair(k.eps), one));
-            const Pair x = sum2(pair(k.decay) * pair(w[2 * j], w[2 * j + 1]), pair(-k.step) * q, one);
+            const Pair u = root2(v2[j], k);
+            const Pair q = minus_quotient2(m2[j], sum2(u * pair(k.root), pair(k.eps), pair(k.one)), k);
+            const Pair x = sum2(pair(k.decay) * pair(w[2 * j], w[2 * j + 1]), pair(k.step) * q, pair(k.one));
             split(x, w[2 * j], w[2 * j + 1]);
             split(m2[j], m[2 * j], m[2 * j + 1]);
             split(kRoot ? u : v2[j], v[2 * j], v[2 * j + 1]);
         }
-        return;
+        return true;
+    }
+#pragma unroll
+    for (int j = 0; j < kAwEach / 2; ++j) {
+        split(m2[j], m[2 * j], m[2 * j + 1]);
+        split(v2[j], v[2 * j], v[2 * j + 1]);
     }
 #pragma unroll
     for (int j = 0; j < kAwEach; ++j) {  // unrolled: the elements are in registers
         float u;
-        adam(k, g[j], m[j], v[j], u, w[j]);
+        root_and_weight(k, m[j], v[j], u, w[j]);
         if (kRoot) v[j] = u;
     }
+    return false;
+}
+
+struct Scales {
+    float scale, inverse;
+};
+
+// The scale of a block whose largest magnitude is `top`, given as its bits (NaN is the
+// largest of all). Below 2^-96, where 448 / top would come near overflow, there is none.
+__device__ __forceinline__ Scales scales_of(float top, const Adam& k)
+{
+    Scales s = {0.0f, 0.0f};
+    if (top >= kLow && top <= kHigh) {
+        split(minus_quotient2(pair(-top, -448.0f), pair(448.0f, top), k), s.scale, s.inverse);
+    } else if (!(top < 0x1p-96f)) {
+        s.scale = __fdiv_rn(top, 448.0f);
+        s.inverse = __fdiv_rn(448.0f, top);
+    }
+    return s;
 }
 
 // A lane's part of a block, as it lies in memory: four elements of either half, so that
@@ -331,33 +358,22 @@ template <typename W, typename G, bool kEight> struct Part {
     Four<G> g[2];
     Four<S> m[2], v[2];
     float ms, vs;
-
-    __device__ __forceinline__ void load(const AwTensor& t, int64_t block)
-    {
-        if (block * kAwBlock >= t.n) return;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int64_t i = block * kAwBlock + (threadIdx.x & 31) * 4 + k * 128;
-            w[k] = load4<W>(t.w, i, t.n);
-            g[k] = load4<G>(t.g, i, t.n);
-            m[k] = load4<S>(t.m, i, t.n);
-            v[k] = load4<S>(t.v, i, t.n);
-        }
-        if (kEight) {
-            ms = t.ms[block];
-            vs = t.vs[block];
-        }
-    }
 };
 
-template <typename W, typename G, bool kEight>
-__device__ __forceinline__ void adamw_block(const AwTensor& t, int64_t block, const Part<W, G, kEight>& r, Adam a,
-                                            bool fast)
+// Where a block's results go.
+template <typename W, typename S> struct Out {
+    W* w;
+    S *m, *v;
+    bf16* copy;
+    float *ms, *vs;
+};
+
+// `left`: elements from the block's start to the tensor's end; kWhole: at least a block.
+template <bool kWhole, typename W, typename G, bool kEight>
+__device__ __forceinline__ void adamw_block(const Out<W, typename Part<W, G, kEight>::S>& o, int64_t left,
+                                            const Part<W, G, kEight>& r, const Adam& a, bool fast)
 {
-    const int64_t n = t.n, first = block * kAwBlock + (threadIdx.x & 31) * 4;
-    if (block * kAwBlock >= n) return;
-    a.decay = t.decay;
-    bf16* copy = static_cast<bf16*>(t.copy);
+    const int lane4 = (threadIdx.x & 31) * 4;
     float wv[kAwEach], gv[kAwEach], mv[kAwEach], vv[kAwEach];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -378,42 +394,43 @@ __device__ __forceinline__ void adamw_block(const AwTensor& t, int64_t block, co
         }
     }
     float mtop, vtop;
-    adam_lane<kEight>(a, fast, gv, mv, vv, wv, mtop, vtop);
+    const bool positive = adam_lane<kEight>(a, fast, gv, mv, vv, wv, mtop, vtop);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int64_t i = first + k * 128;
-        store4(static_cast<W*>(t.w), i, n, wv + 4 * k);
-        if (copy) store4(copy, i, n, wv + 4 * k);
-        if (!kEight) {
-            store4(static_cast<float*>(t.m), i, n, mv + 4 * k);
-            store4(static_cast<float*>(t.v), i, n, vv + 4 * k);
+        const int i = lane4 + k * 128;
+        store4<kWhole>(o.w, i, left, wv + 4 * k);
+        if (o.copy) store4<kWhole>(o.copy, i, left, wv + 4 * k);
+        if constexpr (!kEight) {
+            store4<kWhole>(o.m, i, left, mv + 4 * k);
+            store4<kWhole>(o.v, i, left, vv + 4 * k);
         }
     }
-    if (!kEight) return;
-    // magnitudes order as their bits do; the largest root is the root of the largest v
-    const Scales p = scales_of(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
-    const Scales q =
-        scales_of(__float_as_uint(__fsqrt_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop))))));
+    if constexpr (kEight) {
+        // magnitudes order as their bits do; the largest root is the root of the largest v
+        const Scales p = scales_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop))), a);
+        const Scales q =
+            scales_of(__fsqrt_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)))), a);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        uint32_t m = 0, u = 0;
+        for (int k = 0; k < 2; ++k) {
+            uint32_t m = 0, u = 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int e = 4 * k + 2 * j;
-            float x, y;
-            split(pair(mv[e], mv[e + 1]) * pair(p.inverse), x, y);
-            m |= to_e4m3x2(x, y) << (16 * j);
-            split(pair(vv[e], vv[e + 1]) * pair(q.inverse), x, y);
-            if (vv[e] > 0.0f) x = fmaxf(x, 0x1p-9f);  // the smallest e4m3: a root that is not zero does not become so
-            if (vv[e + 1] > 0.0f) y = fmaxf(y, 0x1p-9f);
-            u |= to_e4m3x2(x, y) << (16 * j);
+            for (int j = 0; j < 2; ++j) {
+                const int e = 4 * k + 2 * j;
+                float x, y;
+                split(pair(mv[e], mv[e + 1]) * pair(p.inverse), x, y);
+                m |= to_e4m3x2(x, y) << (16 * j);
+                split(pair(vv[e], vv[e + 1]) * pair(q.inverse), x, y);
+                if (positive || vv[e] > 0.0f) x = fmaxf(x, 0x1p-9f);  // the smallest e4m3: a positive root stays so
+                if (positive || vv[e + 1] > 0.0f) y = fmaxf(y, 0x1p-9f);
+                u |= to_e4m3x2(x, y) << (16 * j);
+            }
+            store4<kWhole>(o.m, lane4 + k * 128, left, m);
+            store4<kWhole>(o.v, lane4 + k * 128, left, u);
         }
-        store4(static_cast<uint8_t*>(t.m), first + k * 128, n, m);
-        store4(static_cast<uint8_t*>(t.v), first + k * 128, n, u);
-    }
-    if ((threadIdx.x & 31) == 0) {
-        t.ms[block] = p.scale;
-        t.vs[block] = q.scale;
+        if (lane4 == 0) {
+            *o.ms = p.scale;
+            *o.vs = q.scale;
+        }
     }
 }
 
@@ -435,39 +452,81 @@ template <typename Table> struct Cursor {
     }
 };
 
-// One warp per block of 256 elements, a tile of eight blocks per CTA and turn; a CTA takes
-// a run of consecutive tiles. With 8-bit states the next tile's loads are issued before the
-// current one is computed: a block is 2 KB of loads for some 500 instructions, so that
-// warps that wait for their own loads alone leave the memory idle. 32-bit states (one tile
-// per CTA) fill it with the loads of their other warps.
-template <typename W, typename G, bool kEight>
-__global__ void __launch_bounds__(kAwThreads) adamw_kernel(const __grid_constant__ AwTable tab)
+// Fills in what a kernel knows of the constants; false if the step is to be left out.
+__device__ __forceinline__ bool step_constants(const AwTable& tab, Adam* a)
 {
+    *a = tab.k;
+    if (tab.coefficient) a->c = *tab.coefficient;
+    return isfinite(a->c);
+}
+
+// Asks for `bytes` from p on to be brought into L2 (whole 16-byte pieces).
+__device__ __forceinline__ void prefetch(const void* p, int64_t bytes)
+{
+    if (bytes >= 16)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((uint32_t)bytes & ~15u) : "memory");
+}
+
+// The step. Bound by memory: 28 bytes per element with fp32 weights, gradients and states,
+// 14 with bf16 gradients and 8-bit states. One warp per block of 256 elements (one scale),
+// a tile of eight blocks per CTA, no loop: the resident warps' loads keep the memory busy
+// (134M elements, 32-bit states: 0.530 ms, 7.1 TB/s). With 8-bit states there are 2 KB of
+// loads to a warp's 400 instructions; there one thread also has the tile `ahead` CTAs on
+// (four per SM, less than run at once; 300 to 900 measure alike) brought into L2, so that
+// its loads take an L2 access's time (1.3B elements: 2.58 ms, 7.2 TB/s; 2.80 without).
+// Registers decide here: at 48 to 62 there are 40 or 32 warps per SM; with the scalar
+// operations' inputs kept alive behind the test for them there were 24, and it took 3.4.
+// Loading the next block ahead into registers (3.6) or shared memory (3.5) cost more warps
+// than it gained. bf16 weights and gradients with 8-bit states (10 bytes per element) are
+// bound by instructions: 134M elements 0.243 ms, 5.6 TB/s.
+template <typename W, typename G, bool kEight>
+__global__ void __launch_bounds__(kAwThreads, kEight ? 5 : 4) adamw_kernel(const __grid_constant__ AwTable tab)
+{
+    using S = typename Part<W, G, kEight>::S;
     ptx::griddep_wait();
-    const int warp = threadIdx.x >> 5;
-    uint32_t tile = (uint32_t)((uint64_t)tab.tiles * blockIdx.x / gridDim.x);
-    const uint32_t end = (uint32_t)((uint64_t)tab.tiles * (blockIdx.x + 1) / gridDim.x);
-    Cursor<AwTable> at(tab, tile);
-    const auto block_of = [&](const AwTensor& t, uint32_t i) { return (int64_t)(i - t.tile_begin) * kAwWarps + warp; };
-    Part<W, G, kEight> now, next;
-    const AwTensor* t = &tab.t[at.id];
-    now.load(*t, block_of(*t, tile));
-    Adam a = {tab.scale, tab.beta1, tab.beta2, tab.rest1, tab.rest2, tab.step, tab.root, tab.eps, tab.one, 1.0f};
-    if (tab.coefficient) a.c = *tab.coefficient;
-    if (!isfinite(a.c)) return;
-    while (true) {
-        const AwTensor* t_next = t;
-        const bool more = kEight && tile + 1 < end;
-        if (more) {
-            at.to(tab, tile + 1);
-            t_next = &tab.t[at.id];
-            next.load(*t_next, block_of(*t_next, tile + 1));
+    if (kEight && threadIdx.x == kAwThreads - 32 && blockIdx.x + tab.ahead < tab.tiles) {
+        const uint32_t tile = blockIdx.x + tab.ahead;
+        const AwTensor& t = tab.t[owner_of(tab, tile)];
+        const int64_t first = (int64_t)(tile - t.tile_begin) * kAwTile;
+        const int64_t count = t.n - first < kAwTile ? t.n - first : kAwTile;
+        prefetch(static_cast<const W*>(t.w) + first, count * (int)sizeof(W));
+        prefetch(static_cast<const G*>(t.g) + first, count * (int)sizeof(G));
+        prefetch(static_cast<const uint8_t*>(t.m) + first, count);
+        prefetch(static_cast<const uint8_t*>(t.v) + first, count);
+    }
+    const AwTensor& t = tab.t[owner_of(tab, blockIdx.x)];
+    const int64_t block = (int64_t)(blockIdx.x - t.tile_begin) * kAwWarps + (threadIdx.x >> 5);
+    const int64_t first = block * kAwBlock, left = t.n - first;
+    if (left <= 0) return;
+    const Out<W, S> o = {static_cast<W*>(t.w) + first, static_cast<S*>(t.m) + first, static_cast<S*>(t.v) + first,
+                         t.copy ? static_cast<bf16*>(t.copy) + first : nullptr, t.ms + block, t.vs + block};
+    const G* g = static_cast<const G*>(t.g) + first;
+    Part<W, G, kEight> r;
+    const auto load = [&](auto whole) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = (threadIdx.x & 31) * 4 + k * 128;
+            r.w[k] = load4<whole.value, W>(o.w, i, left);
+            r.g[k] = load4<whole.value, G>(g, i, left);
+            r.m[k] = load4<whole.value, S>(o.m, i, left);
+            r.v[k] = load4<whole.value, S>(o.v, i, left);
         }
-        adamw_block(*t, block_of(*t, tile), now, a, tab.fast != 0);
-        if (!more) break;
-        now = next;
-        t = t_next;
-        ++tile;
+        if (kEight) {
+            r.ms = *o.ms;
+            r.vs = *o.vs;
+        }
+    };
+    Adam a;
+    if (left >= kAwBlock) {
+        load(std::true_type());
+        if (!step_constants(tab, &a)) return;
+        a.decay = t.decay;
+        adamw_block<true>(o, left, r, a, tab.fast != 0);
+    } else {
+        load(std::false_type());
+        if (!step_constants(tab, &a)) return;
+        a.decay = t.decay;
+        adamw_block<false>(o, left, r, a, tab.fast != 0);
     }
 }
 
@@ -507,8 +566,12 @@ template <typename G> __device__ __forceinline__ int values_of(uint32_t word, fl
     return 2;
 }
 
-// A CTA sums a run of consecutive tiles and leaves one fp64 partial sum; the last CTA of
-// the call adds the partial sums in their order.
+// The sum of squares of all gradients. Bound by memory: each CTA (six per SM) reads a run of
+// consecutive tiles, 64 bytes per thread in flight (1.3B bf16 elements: 0.366 ms, 7.2 TB/s).
+// fp32 sums over the 16 or 32 elements of a thread's turn, fp64 from there on; a turn whose
+// fp32 sum overflows, or is so small that squares may have vanished, is summed again in
+// fp64. A CTA leaves one fp64 partial sum; the last CTA of the call adds the partial sums in
+// their order.
 template <typename G>
 __global__ void __launch_bounds__(kAwThreads, 6) grad_norm_kernel(const __grid_constant__ NormTable tab)
 {
@@ -622,17 +685,14 @@ template <typename T, typename F> adacomp_status for_runs(const std::vector<int3
     return ADACOMP_OK;
 }
 
-template <typename W, typename G> cudaError_t step_launch(const AwTable* tab, bool eight, cudaStream_t stream)
+template <typename W, typename G> cudaError_t step_launch(AwTable* tab, bool eight, cudaStream_t stream)
 {
-    if (!eight) return launch_after(adamw_kernel<W, G, false>, dim3(tab->tiles), dim3(kAwThreads), 0, stream, *tab);
-    int sms = 0, per = 0;
-    cudaError_t e = sm_count(&sms);
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, adamw_kernel<W, G, true>, kAwThreads, 0);
-    if (e != cudaSuccess) return e;
-    const uint32_t most = (uint32_t)(sms * (per > 0 ? per : 1));
-    return launch_after(adamw_kernel<W, G, true>, dim3(tab->tiles < most ? tab->tiles : most), dim3(kAwThreads), 0,
-                        stream, *tab);
+    tab->ahead = (uint32_t)(4 * sms);
+    return launch_after(eight ? adamw_kernel<W, G, true> : adamw_kernel<W, G, false>, dim3(tab->tiles),
+                        dim3(kAwThreads), 0, stream, *tab);
 }
 
 }  // namespace
@@ -715,6 +775,7 @@ adacomp_status adacomp_grad_norm(adacomp_adamw_t h, const void* const* grad, flo
             tab->count = (int32_t)(j - i);
             tab->tiles = tiles;
             tab->first_part = parts;
+            fill_jumps(tab);
             parts += grid;
             return launch_result(launch_after(k ? grad_norm_kernel<bf16> : grad_norm_kernel<float>, dim3(grid),
                                               dim3(kAwThreads), 0, stream, *tab), stream);
@@ -747,17 +808,26 @@ adacomp_status adacomp_adamw_step(adacomp_adamw_t h, void* const* weight, const 
     }
     AwTable* tab = new (std::nothrow) AwTable;
     if (!tab) return ADACOMP_ERR_INVALID_ARG;
-    tab->beta1 = beta1;
-    tab->beta2 = beta2;
-    tab->rest1 = 1.0f - beta1;
-    tab->rest2 = 1.0f - beta2;
-    tab->step = (float)((double)lr / (double)bias_correction1);
-    tab->root = (float)(1.0 / std::sqrt((double)bias_correction2));
-    tab->eps = eps;
-    tab->one = 1.0f;
+    const auto twice = [](float x) {
+        uint32_t b;
+        std::memcpy(&b, &x, 4);
+        return Pair{((unsigned long long)b << 32) | b};
+    };
+    const float root = (float)(1.0 / std::sqrt((double)bias_correction2));
+    tab->k.c = grad_scale;
+    tab->k.beta1 = beta1;
+    tab->k.beta2 = beta2;
+    tab->k.rest1 = 1.0f - beta1;
+    tab->k.rest2 = 1.0f - beta2;
+    tab->k.step = (float)((double)lr / (double)bias_correction1);
+    tab->k.root = root;
+    tab->k.eps = eps;
+    tab->k.one = 1.0f;
+    tab->k.half = 0.5f;
+    tab->k.minus = -1.0f;
+    tab->k.decay = 1.0f;
     // u <= 2^30 in adam_lane's range, so that u * root + eps lies within 2^+-40
-    tab->fast = eps >= 0x1p-40f && eps <= 0x1p30f && tab->root <= 0x1p9f;
-    tab->scale = grad_scale;
+    tab->fast = eps >= 0x1p-40f && eps <= 0x1p30f && root <= 0x1p9f;
     tab->coefficient = coefficient;
     adacomp_status st = ADACOMP_OK;
     const auto tiles_of = [&](size_t id) { return step_tiles(h->n[id]); };
@@ -781,6 +851,7 @@ adacomp_status adacomp_adamw_step(adacomp_adamw_t h, void* const* weight, const 
             }
             tab->count = (int32_t)(j - i);
             tab->tiles = tiles;
+            fill_jumps(tab);
             const cudaError_t e = k == 0   ? step_launch<float, float>(tab, eight, stream)
                                   : k == 1 ? step_launch<float, bf16>(tab, eight, stream)
                                   : k == 2 ? step_launch<bf16, float>(tab, eight, stream)
