@@ -22,13 +22,7 @@ constexpr int kJumps = 1024;                       // see owner_of
 constexpr int kNormGrid = 912;                     // CTAs per launch at most (six per SM), each with a partial sum
 constexpr int kNormVectors = 4;                    // 16-byte vectors per thread and tile
 
-// Two fp32 values that one instruction computes with. Every operation rounds as its scalar
-// form does (.rn: no contraction).
-struct Pair {
-    unsigned long long b;
-};
-
-// The step's constants, each twice (as the paired operations take them from constant memory).
+// The step's constants.
 struct Adam {
     float c, beta1, beta2, rest1, rest2, step, root, eps, one, half, minus, decay;
 };
@@ -117,40 +111,12 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c)
 }
 
 // ---------------------------------------------------------------- step
-__device__ __forceinline__ Pair pair(float x, float y)
-{
-    Pair p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p.b) : "f"(x), "f"(y));
-    return p;
-}
-
-__device__ __forceinline__ Pair pair(float x) { return pair(x, x); }
-
-__device__ __forceinline__ void split(Pair p, float& x, float& y)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.b));
-}
-
 // One element's root u of v, and its weight, by the scalar operations.
 __device__ __forceinline__ void root_and_weight(const Adam& k, float m, float v, float& u, float& w)
 {
     u = __fsqrt_rn(v);
     const float q = __fdiv_rn(m, __fadd_rn(__fmul_rn(u, k.root), k.eps));
     w = __fsub_rn(__fmul_rn(k.decay, w), __fmul_rn(k.step, q));
-}
-
-__device__ __forceinline__ Pair operator*(Pair x, Pair y)
-{
-    Pair p;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.b) : "l"(x.b), "l"(y.b));
-    return p;
-}
-
-__device__ __forceinline__ Pair fma2(Pair x, Pair y, Pair z)
-{
-    Pair p;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.b) : "l"(x.b), "l"(y.b), "l"(z.b));
-    return p;
 }
 
 // The sum of two products, each rounded before it: `one` is 1, which the compiler does not

@@ -1,6 +1,8 @@
 // The gated linear recurrence h_t = a_t h_{t-1} + (1 - a_t) x_t, a_t = sigmoid(z_t),
 // forward and backward: kernels and C entry points (adacomp.h).
+#include <initializer_list>
 #include <new>
+#include <type_traits>
 
 #include "train_common.cuh"
 
@@ -27,17 +29,22 @@ struct RecArgs {
     const int32_t* lengths;
     float *h_last, *dh0, *carry;
     int64_t batch, steps, channels, chunks;
+    uint32_t blocks;  // of 64 channels, in a row
 };
 
-// a = sigmoid(z) and 1 - a = sigmoid(-z), neither formed by a subtraction.
+// a = sigmoid(z) and 1 - a = sigmoid(-z), neither formed by a subtraction: with
+// e = exp(-|z|), 1 / (1 + e) is the larger of the two and e / (1 + e) the smaller. exp is to
+// 2 + 1.2 |z| units in the last place and 0 from |z| = 87.4 on; NaN stays NaN.
 __device__ __forceinline__ void gate(float z, float* a, float* b)
 {
-    const float e = __expf(-fabsf(z));
-    const float r = __fdividef(1.0f, 1.0f + e);
+    float e = -1.44269504f * fabsf(z), r = 1.0f;
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e));
+    r += e;
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r));
     const float s = e * r;
-    *a = z >= 0.0f ? r : s;
-    *b = z >= 0.0f ? s : r;
-    if (z != z) *a = *b = z;
+    const bool open = z >= 0.0f;
+    *a = open ? r : s;
+    *b = open ? s : r;
 }
 
 __device__ __forceinline__ int64_t length_of(const RecArgs& p, int64_t b)
@@ -74,14 +81,18 @@ template <typename T> __global__ void __launch_bounds__(kRecThreads) rec_forward
 }
 
 // ---------------------------------------------------------------- many steps
-// The steps are split: a warp has 32 columns and S consecutive steps, a CTA one chunk of
-// 128 steps, a cluster of up to eight CTAs consecutive chunks, and where the sequence is
-// longer than that the cluster goes on in rounds. Each warp forms what its steps do to a
-// state, h -> A h + H with A the product of its gates; the CTA's warps exchange these
-// through shared memory and the cluster's CTAs through each other's; then each warp knows
-// the state before its first step and goes through its steps again, from registers. So
-// every element is read once, and no CTA waits for one that may not be running. The split
-// depends on the number of steps alone.
+// The steps are split: a warp has 64 columns (two per lane) and eight consecutive steps, a
+// CTA 64 steps, a cluster of up to eight CTAs up to 512, and where the sequence is longer the
+// cluster goes on in rounds. Each warp forms what its steps do to a state, h -> A h + H with
+// A the product of its gates; the CTA's warps exchange these through shared memory and the
+// cluster's CTAs write them into each other's; then each warp knows the state before its
+// first step and goes through its steps again, from registers. So every element is read
+// once, and no CTA waits for one that may not be running. The next round's elements are
+// copied to shared memory meanwhile. The split depends on the number of steps alone.
+constexpr int kCols = 64, kSteps = 8, kWarps = 8, kThreads = 32 * kWarps, kSpan = kSteps * kWarps;
+constexpr int kRanks = 8;
+static_assert(kRecChunk == 2 * kSpan, "a kept state every second CTA");
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -94,230 +105,461 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A float2 of this CTA's shared memory, as it lies in the CTA `rank` of the cluster.
-__device__ __forceinline__ float2 remote(const float2* p, uint32_t rank)
+// Writes v where `p` of this CTA's shared memory is in the CTA `rank` of the cluster.
+__device__ __forceinline__ void push(float4* p, uint32_t rank, float4 v)
 {
     uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ Pair low_pair(float4 v) { return pair(v.x, v.y); }
+__device__ __forceinline__ Pair high_pair(float4 v) { return pair(v.z, v.w); }
+
+__device__ __forceinline__ float4 quad(Pair a, Pair b)
+{
+    float4 v;
+    split(a, v.x, v.y);
+    split(b, v.z, v.w);
     return v;
 }
 
-struct Column {
+// The columns of a tile. Where a sequence's rows are read 16 bytes at a time (kBytes), a
+// tile is 64 channels of one sequence; otherwise the channels of all sequences are numbered
+// through, so that few channels fill a tile too.
+template <int kBytes> struct Column {
+    int64_t b, c;
+    int32_t len;  // of its sequence; 0 past the last column
     bool on;
-    int64_t i, b, c;
-    int64_t len;
 
-    __device__ __forceinline__ Column(const RecArgs& p, uint32_t tile)
+    __device__ __forceinline__ Column(const RecArgs& p, uint32_t tile, int j)
     {
-        i = (int64_t)tile * 32 + (threadIdx.x & 31);
-        on = i < p.batch * p.channels;
-        if (!on) i = 0;
-        b = i / p.channels;
-        c = i - b * p.channels;
-        len = on ? length_of(p, b) : 0;
+        if (kBytes == 16) {
+            b = tile / p.blocks;
+            c = (int64_t)(tile - (uint32_t)b * p.blocks) * kCols + j;
+            on = c < p.channels;
+        } else {
+            const int64_t i = (int64_t)tile * kCols + j;
+            on = i < p.batch * p.channels;
+            b = on ? i / p.channels : 0;
+            c = on ? i - b * p.channels : 0;
+        }
+        len = on ? (int32_t)length_of(p, b) : 0;
     }
 };
 
-constexpr int kForwardSteps = 16, kForwardCtas = 3;
+// Copies a CTA's 64 steps of a tile to shared memory, [step][column], kBytes at a time:
+// every thread has one place in the rows and takes every kStride-th of them. What lies past
+// a sequence's length or the last channel is not read, and what stands there not used.
+template <typename T, int kBytes> struct Copier {
+    static constexpr int kPlaces = kCols * (int)sizeof(T) / kBytes;
+    static constexpr int kStride = kThreads / kPlaces;
+    static constexpr int kEach = kBytes / (int)sizeof(T);  // elements at a time
+    int64_t b, c;
+    int32_t len;
+    uint32_t bytes;
 
-template <typename T, int S>
-__global__ void __launch_bounds__(32 * kRecChunk / S, kForwardCtas) rec_forward_kernel(const RecArgs p, const uint32_t ranks)
-{
-    constexpr int kWarpsPer = kRecChunk / S;
-    __shared__ float2 part[2][kWarpsPer][32];  // a warp's (A, H), by the round's parity
-    __shared__ float2 total[2][32];            // and the CTA's
-    ptx::griddep_wait();
-    const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Column col(p, blockIdx.x / ranks);
-    float h0 = p.h0 && col.on ? p.h0[col.i] : 0.0f;  // before the round's first step
-    int par = 0;
-    for (int64_t t0 = 0; t0 < p.steps; t0 += (int64_t)ranks * kRecChunk, par ^= 1) {
-        const int64_t ts = t0 + rank * kRecChunk + warp * S;
-        const int live = (int)(col.len - ts < 0 ? 0 : col.len - ts > S ? S : col.len - ts);
-        const int whole = !col.on || p.steps <= ts ? 0 : (int)(p.steps - ts > S ? S : p.steps - ts);
-        T zr[S], xr[S];
-        {
-            const T* z = at<T>(p.z, col.b, ts, col.c);
-            const T* x = at<T>(p.x, col.b, ts, col.c);
+    __device__ __forceinline__ Copier(const RecArgs& p, uint32_t tile)
+    {
+        const Column<kBytes> col(p, tile, (threadIdx.x % kPlaces) * kEach);
+        b = col.b;
+        c = col.c;
+        len = col.len;
+        const int64_t rest = (p.channels - c) * (int)sizeof(T);
+        bytes = !col.on ? 0u : rest < kBytes ? (uint32_t)rest : (uint32_t)kBytes;
+        if (bytes == 0) len = 0;
+    }
+
+    __device__ __forceinline__ void copy(T* to, const RecSeq& s, int64_t t0) const
+    {
+        const int row0 = threadIdx.x / kPlaces;
+        const int left = (int)(len - t0 < 0 ? 0 : len - t0 > kSpan ? kSpan : len - t0);
+        const T* from = static_cast<const T*>(s.p) + b * s.batch + (t0 + row0) * s.step + c;
+        T* at = to + row0 * kCols + (threadIdx.x % kPlaces) * kEach;
+        if constexpr (kBytes == 2) {
+            T v[kSpan / kStride];
 #pragma unroll
-            for (int k = 0; k < S; ++k, z += p.z.step, x += p.x.step)
-                if (k < live) {
-                    zr[k] = *z;
-                    xr[k] = *x;
+            for (int k = 0; k < kSpan / kStride; ++k, from += kStride * s.step)
+                if (row0 + k * kStride < left) v[k] = *from;
+#pragma unroll
+            for (int k = 0; k < kSpan / kStride; ++k) at[k * kStride * kCols] = v[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < kSpan / kStride; ++k, from += kStride * s.step)
+                if (row0 + k * kStride < left) {
+                    const uint32_t d = (uint32_t)__cvta_generic_to_shared(at + k * kStride * kCols);
+                    if constexpr (kBytes == 16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(from), "r"(bytes)
+                                     : "memory");
+                    else
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(from) : "memory");
                 }
         }
-        float a[S], u[S], A = 1.0f, H = 0.0f;
-#pragma unroll
-        for (int k = 0; k < S; ++k) {
-            a[k] = 1.0f;
-            u[k] = 0.0f;
-            if (k < live) {
-                float r;
-                gate(to_f32(zr[k]), &a[k], &r);
-                u[k] = r * to_f32(xr[k]);
-            }
-            H = fmaf(a[k], H, u[k]);
-            A *= a[k];
-        }
-        part[par][warp][lane] = make_float2(A, H);
-        __syncthreads();
-        A = 1.0f;
-        H = 0.0f;
-        for (int w = 0; w < warp; ++w) {
-            const float2 q = part[par][w][lane];
-            H = fmaf(q.x, H, q.y);
-            A *= q.x;
-        }
-        float hc = h0;  // before the CTA's first step
-        if (ranks > 1) {
-            if (warp == kWarpsPer - 1) {
-                const float2 q = part[par][warp][lane];
-                total[par][lane] = make_float2(A * q.x, fmaf(q.x, H, q.y));
-            }
-            cluster_sync();
-            for (uint32_t r = 0; r < ranks; ++r) {
-                if (r == rank) hc = h0;
-                const float2 q = remote(&total[par][lane], r);
-                h0 = fmaf(q.x, h0, q.y);
+    }
+};
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void two(const float* p, float& x, float& y)
+{
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x = v.x, y = v.y;
+}
+
+__device__ __forceinline__ void two(const bf16* p, float& x, float& y)
+{
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    x = bf16_low(v), y = bf16_high(v);
+}
+
+// One step of a lane's two columns.
+template <typename T, int kBytes> struct Writer {
+    T* p[2];
+    int64_t step;
+
+    __device__ __forceinline__ Writer(const RecSeq& s, const Column<kBytes> (&col)[2], int64_t t) : step(s.step)
+    {
+        p[0] = at<T>(s, col[0].b, t, col[0].c);
+        if (kBytes != 16) p[1] = at<T>(s, col[1].b, t, col[1].c);
+    }
+    __device__ __forceinline__ void move(int by)
+    {
+        p[0] += by * step;
+        if (kBytes != 16) p[1] += by * step;
+    }
+    __device__ __forceinline__ void put(float x, float y, bool on0, bool on1) const
+    {
+        if (kBytes == 16) {
+            if (on1) {
+                if constexpr (sizeof(T) == 4) {
+                    *reinterpret_cast<float2*>(p[0]) = make_float2(x, y);
+                } else {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+                    *reinterpret_cast<__nv_bfloat162*>(p[0]) = v;
+                }
+            } else if (on0) {
+                *p[0] = from_f32<T>(x);
             }
         } else {
-            float e = h0;
-            for (int w = 0; w < kWarpsPer; ++w) {
-                const float2 q = part[par][w][lane];
-                e = fmaf(q.x, e, q.y);
-            }
-            h0 = e;
-        }
-        float h = fmaf(A, hc, H);
-        if (p.carry && warp == 0 && whole > 0)
-            p.carry[(col.b * p.chunks + ts / kRecChunk) * p.channels + col.c] = h;
-        T* y = at<T>(p.y, col.b, ts, col.c);
-#pragma unroll
-        for (int k = 0; k < S; ++k, y += p.y.step) {
-            h = fmaf(a[k], h, u[k]);
-            if (k < whole) *y = from_f32<T>(k < live ? h : 0.0f);
+            if (on0) *p[0] = from_f32<T>(x);
+            if (on1) *p[1] = from_f32<T>(y);
         }
     }
-    if (p.h_last && col.on && rank == 0 && warp == 0) p.h_last[col.i] = h0;
-    if (ranks > 1) cluster_sync();  // the others may still read this CTA's totals
+};
+
+// How many of a warp's steps from ts on lie within `len`.
+__device__ __forceinline__ int within(int64_t len, int64_t ts)
+{
+    return (int)(len - ts < 0 ? 0 : len - ts > kSteps ? kSteps : len - ts);
+}
+
+template <typename T, int kBytes>
+__global__ void __launch_bounds__(kThreads, 3) rec_forward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
+{
+    extern __shared__ __align__(16) uint8_t shared_bytes[];
+    __shared__ float4 part[kWarps][32];      // a warp's (A, H) of the lane's columns
+    __shared__ float4 total[2][kRanks][32];  // the CTAs', by the round's parity: a slower one may still read the last
+    constexpr int kTile = kSpan * kCols;
+    const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (2 * kTile); };
+    ptx::griddep_wait();
+    if (ranks > 1) cluster_sync();  // all CTAs run before one writes to another
+    const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Column<kBytes> col[2] = {Column<kBytes>(p, tile, 2 * lane), Column<kBytes>(p, tile, 2 * lane + 1)};
+    const Copier<T, kBytes> copier(p, tile);
+    const int64_t span = (int64_t)ranks * kSpan;
+    const auto stage = [&](int64_t t0, int par) {
+        copier.copy(tile_of(par), p.z, t0 + rank * kSpan);
+        copier.copy(tile_of(par) + kTile, p.x, t0 + rank * kSpan);
+        copies_commit();
+    };
+    Pair h0;  // before the round's first step
+    {
+        float v[2] = {0.0f, 0.0f};
+        for (int j = 0; j < 2; ++j)
+            if (p.h0 && col[j].on) v[j] = p.h0[col[j].b * p.channels + col[j].c];
+        h0 = pair(v[0], v[1]);
+    }
+    stage(0, 0);
+    int par = 0;
+    for (int64_t t0 = 0; t0 < p.steps; t0 += span, par ^= 1) {
+        copies_wait();
+        __syncthreads();
+        if (t0 + span < p.steps) stage(t0 + span, par ^ 1);
+        const int64_t tc = t0 + rank * kSpan, ts = tc + warp * kSteps;
+        const int live0 = within(col[0].len, ts), live1 = within(col[1].len, ts);
+        const bool all = __all_sync(0xffffffffu, (live0 == kSteps || !col[0].on) && (live1 == kSteps || !col[1].on));
+        const T* z = tile_of(par) + warp * kSteps * kCols + 2 * lane;
+        const T* x = z + kTile;
+        Pair a[kSteps], u[kSteps], A = pair(1.0f), H = pair(0.0f);
+        const auto form = [&](auto masked) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                float z0, z1, x0, x1, a0, a1, b0, b1;
+                two(z + k * kCols, z0, z1);
+                two(x + k * kCols, x0, x1);
+                gate(z0, &a0, &b0);
+                gate(z1, &a1, &b1);
+                if (masked.value) {  // past the length the state stays as it is
+                    if (k >= live0) a0 = 1.0f, b0 = x0 = 0.0f;
+                    if (k >= live1) a1 = 1.0f, b1 = x1 = 0.0f;
+                }
+                a[k] = pair(a0, a1);
+                u[k] = pair(b0, b1) * pair(x0, x1);
+                H = fma2(a[k], H, u[k]);
+                A = A * a[k];
+            }
+        };
+        if (all) form(std::false_type());
+        else form(std::true_type());
+        part[warp][lane] = quad(A, H);
+        __syncthreads();
+        if (ranks > 1) {  // a warp for each CTA to write to
+            if (warp < (int)ranks) {
+                Pair tA = pair(1.0f), tH = pair(0.0f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 q = part[w][lane];
+                    tH = fma2(low_pair(q), tH, high_pair(q));
+                    tA = tA * low_pair(q);
+                }
+                push(&total[par][rank][lane], (uint32_t)warp, quad(tA, tH));
+            }
+            cluster_sync();
+        }
+        Pair h = h0;  // before the CTA's first step
+        if (ranks > 1) {
+            for (uint32_t r = 0; r < ranks; ++r) {
+                if (r == rank) h = h0;
+                const float4 q = total[par][r][lane];
+                h0 = fma2(low_pair(q), h0, high_pair(q));
+            }
+        } else {
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 q = part[w][lane];
+                h0 = fma2(low_pair(q), h0, high_pair(q));
+            }
+        }
+        if (p.carry && warp == 0 && tc % kRecChunk == 0 && tc < p.steps) {
+            float v[2];
+            split(h, v[0], v[1]);
+            for (int j = 0; j < 2; ++j)
+                if (col[j].on) p.carry[(col[j].b * p.chunks + tc / kRecChunk) * p.channels + col[j].c] = v[j];
+        }
+        for (int w = 0; w < warp; ++w) {
+            const float4 q = part[w][lane];
+            h = fma2(low_pair(q), h, high_pair(q));
+        }
+        Writer<T, kBytes> y(p.y, col, ts);
+        const int whole = within(p.steps, ts);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            h = fma2(a[k], h, u[k]);
+            float v0, v1;
+            split(h, v0, v1);
+            if (k < whole) y.put(k < live0 ? v0 : 0.0f, k < live1 ? v1 : 0.0f, col[0].on, col[1].on);
+            y.move(1);
+        }
+    }
+    if (p.h_last && rank == 0 && warp == 0) {
+        float v[2];
+        split(h0, v[0], v[1]);
+        for (int j = 0; j < 2; ++j)
+            if (col[j].on) p.h_last[col[j].b * p.channels + col[j].c] = v[j];
+    }
+    if (ranks > 1) cluster_sync();  // no CTA ends while another may write to it
 }
 
 // The reverse of it: p, the gradient that reaches a state from the steps after it, goes
 // through a warp's steps as p -> A p + P, P = sum of dy_k times the gates up to and with
-// step k. The states are formed again from the chunk's first one, which the forward pass
-// kept: that is less to read than y, and not rounded.
-constexpr int kBackwardSteps = 16, kBackwardCtas = 2;
-
-template <typename T, int S>
-__global__ void __launch_bounds__(32 * kRecChunk / S, kBackwardCtas) rec_backward_kernel(const RecArgs p, const uint32_t ranks)
+// step k. The states are formed again from the one that the forward pass kept for the chunk
+// of two CTAs: that is less to read than y, and not rounded.
+template <typename T, int kBytes>
+__global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
 {
-    constexpr int kWarpsPer = kRecChunk / S;
-    __shared__ float2 part[2][kWarpsPer][32];  // a warp's (A, H), by the round's parity
-    __shared__ float grad[2][kWarpsPer][32];   // its P
-    __shared__ float2 total[2][32];            // the CTA's (A, P)
+    extern __shared__ __align__(16) uint8_t shared_bytes[];
+    __shared__ float4 part[kWarps][32];      // a warp's (A, H)
+    __shared__ float2 grad[kWarps][32];      // its P
+    __shared__ float4 total[2][kRanks][32];  // the CTAs' (A, P)
+    __shared__ float4 first[2][32];          // the (A, H) of the CTA before, where the chunk is its
+    constexpr int kTile = kSpan * kCols;
+    const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (3 * kTile); };
     ptx::griddep_wait();
-    const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
+    if (ranks > 1) cluster_sync();  // all CTAs run before one writes to another
+    const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Column col(p, blockIdx.x / ranks);
-    float p0 = p.dh_last && col.on ? p.dh_last[col.i] : 0.0f;  // after the round's last step
-    const int64_t span = (int64_t)ranks * kRecChunk;
+    const Column<kBytes> col[2] = {Column<kBytes>(p, tile, 2 * lane), Column<kBytes>(p, tile, 2 * lane + 1)};
+    const Copier<T, kBytes> copier(p, tile);
+    const int64_t span = (int64_t)ranks * kSpan;
+    const auto stage = [&](int64_t t0, int par) {
+        copier.copy(tile_of(par), p.z, t0 + rank * kSpan);
+        copier.copy(tile_of(par) + kTile, p.x, t0 + rank * kSpan);
+        copier.copy(tile_of(par) + 2 * kTile, p.dy, t0 + rank * kSpan);
+        copies_commit();
+    };
+    Pair p0;  // after the round's last step
+    {
+        float v[2] = {0.0f, 0.0f};
+        for (int j = 0; j < 2; ++j)
+            if (p.dh_last && col[j].on) v[j] = p.dh_last[col[j].b * p.channels + col[j].c];
+        p0 = pair(v[0], v[1]);
+    }
+    const int64_t last = p.steps > 0 ? (p.steps - 1) / span * span : -1;
+    if (last >= 0) stage(last, 0);
     int par = 0;
-    for (int64_t t0 = (p.steps - 1) / span * span; t0 >= 0; t0 -= span, par ^= 1) {
-        const int64_t tc = t0 + rank * kRecChunk, ts = tc + warp * S;
-        const int live = (int)(col.len - ts < 0 ? 0 : col.len - ts > S ? S : col.len - ts);
-        const int whole = !col.on || p.steps <= ts ? 0 : (int)(p.steps - ts > S ? S : p.steps - ts);
-        T zr[S], xr[S], dr[S];
+    for (int64_t t0 = last; t0 >= 0; t0 -= span, par ^= 1) {
+        const int64_t tc = t0 + rank * kSpan, ts = tc + warp * kSteps, chunk = tc / kRecChunk;
+        Pair h = pair(0.0f);  // before the chunk's first step
         {
-            const T* z = at<T>(p.z, col.b, ts, col.c);
-            const T* x = at<T>(p.x, col.b, ts, col.c);
-            const T* d = at<T>(p.dy, col.b, ts, col.c);
-#pragma unroll
-            for (int k = 0; k < S; ++k, z += p.z.step, x += p.x.step, d += p.dy.step)
-                if (k < live) {
-                    zr[k] = *z;
-                    xr[k] = *x;
-                    dr[k] = *d;
-                }
+            float v[2] = {0.0f, 0.0f};
+            for (int j = 0; j < 2; ++j)
+                if (col[j].on && tc < p.steps) v[j] = p.carry[(col[j].b * p.chunks + chunk) * p.channels + col[j].c];
+            h = pair(v[0], v[1]);
         }
-        float hc = col.on && tc < p.steps ? p.carry[(col.b * p.chunks + tc / kRecChunk) * p.channels + col.c] : 0.0f;
-        float a[S], b[S], x[S], g[S], A = 1.0f, H = 0.0f, P = 0.0f;
-#pragma unroll
-        for (int k = 0; k < S; ++k) {
-            a[k] = 1.0f;
-            b[k] = x[k] = g[k] = 0.0f;
-            if (k < live) {
-                gate(to_f32(zr[k]), &a[k], &b[k]);
-                x[k] = to_f32(xr[k]);
-                g[k] = to_f32(dr[k]);
-            }
-            H = fmaf(a[k], H, b[k] * x[k]);
-            A *= a[k];
-            P = fmaf(A, g[k], P);
-        }
-        part[par][warp][lane] = make_float2(A, H);
-        grad[par][warp][lane] = P;
+        copies_wait();
         __syncthreads();
-        float h = hc;
-        for (int w = 0; w < warp; ++w) {
-            const float2 q = part[par][w][lane];
-            h = fmaf(q.x, h, q.y);
+        if (t0 > 0) stage(t0 - span, par ^ 1);
+        const int live0 = within(col[0].len, ts), live1 = within(col[1].len, ts);
+        const bool all = __all_sync(0xffffffffu, (live0 == kSteps || !col[0].on) && (live1 == kSteps || !col[1].on));
+        const T* z = tile_of(par) + warp * kSteps * kCols + 2 * lane;
+        const T *x = z + kTile, *d = x + kTile;
+        Pair a[kSteps], b[kSteps], A = pair(1.0f), H = pair(0.0f), P = pair(0.0f);
+        const auto form = [&](auto masked) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                float z0, z1, x0, x1, d0, d1, a0, a1, b0, b1;
+                two(z + k * kCols, z0, z1);
+                two(x + k * kCols, x0, x1);
+                two(d + k * kCols, d0, d1);
+                gate(z0, &a0, &b0);
+                gate(z1, &a1, &b1);
+                if (masked.value) {
+                    if (k >= live0) a0 = 1.0f, b0 = x0 = d0 = 0.0f;
+                    if (k >= live1) a1 = 1.0f, b1 = x1 = d1 = 0.0f;
+                }
+                a[k] = pair(a0, a1);
+                b[k] = pair(b0, b1);
+                H = fma2(a[k], H, b[k] * pair(x0, x1));
+                A = A * a[k];
+                P = fma2(A, pair(d0, d1), P);
+            }
+        };
+        if (all) form(std::false_type());
+        else form(std::true_type());
+        part[warp][lane] = quad(A, H);
+        {
+            float2 v;
+            split(P, v.x, v.y);
+            grad[warp][lane] = v;
         }
-        float Pa = 1.0f, Pp = 0.0f;  // from after the CTA's last step to after the warp's
-        for (int w = kWarpsPer - 1; w > warp; --w) {
-            const float q = part[par][w][lane].x;
-            Pp = fmaf(q, Pp, grad[par][w][lane]);
-            Pa *= q;
-        }
-        float pc = p0;  // after the CTA's last step
+        __syncthreads();
         if (ranks > 1) {
-            if (warp == 0) total[par][lane] = make_float2(A * Pa, fmaf(A, Pp, P));
+            if (warp < (int)ranks) {
+                Pair tA = pair(1.0f), tH = pair(0.0f), tP = pair(0.0f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 q = part[w][lane];
+                    const float2 g = grad[w][lane];
+                    tH = fma2(low_pair(q), tH, high_pair(q));
+                    tP = fma2(tA, pair(g.x, g.y), tP);
+                    tA = tA * low_pair(q);
+                }
+                push(&total[par][rank][lane], (uint32_t)warp, quad(tA, tP));
+                if ((rank & 1) == 0 && warp == (int)rank + 1) push(&first[par][lane], (uint32_t)warp, quad(tA, tH));
+            }
             cluster_sync();
+        }
+        Pair q = p0;  // after the CTA's last step
+        if (ranks > 1) {
             for (uint32_t r = ranks; r-- > 0;) {
-                if (r == rank) pc = p0;
-                const float2 q = remote(&total[par][lane], r);
-                p0 = fmaf(q.x, p0, q.y);
+                if (r == rank) q = p0;
+                const float4 v = total[par][r][lane];
+                p0 = fma2(low_pair(v), p0, high_pair(v));
             }
+            if (rank & 1) h = fma2(low_pair(first[par][lane]), h, high_pair(first[par][lane]));
         } else {
-            float e = p0;
-            for (int w = kWarpsPer - 1; w >= 0; --w) e = fmaf(part[par][w][lane].x, e, grad[par][w][lane]);
-            p0 = e;
-        }
-        float before[S];
-#pragma unroll
-        for (int k = 0; k < S; ++k) {
-            before[k] = h;
-            h = fmaf(a[k], h, b[k] * x[k]);
-        }
-        float q = fmaf(Pa, pc, Pp);
-        T* dz = at<T>(p.dz, col.b, ts + (S - 1), col.c);
-        T* dx = at<T>(p.dx, col.b, ts + (S - 1), col.c);
-#pragma unroll
-        for (int k = S - 1; k >= 0; --k, dz -= p.dz.step, dx -= p.dx.step) {
-            const float G = g[k] + q, d = b[k] * G;
-            if (k < whole) {
-                *dx = from_f32<T>(k < live ? d : 0.0f);
-                *dz = from_f32<T>(k < live ? a[k] * d * (before[k] - x[k]) : 0.0f);
+            for (int w = kWarps - 1; w >= 0; --w) {
+                const float2 g = grad[w][lane];
+                p0 = fma2(low_pair(part[w][lane]), p0, pair(g.x, g.y));
             }
+        }
+        for (int w = 0; w < warp; ++w) {
+            const float4 v = part[w][lane];
+            h = fma2(low_pair(v), h, high_pair(v));
+        }
+        for (int w = kWarps - 1; w > warp; --w) {
+            const float2 g = grad[w][lane];
+            q = fma2(low_pair(part[w][lane]), q, pair(g.x, g.y));
+        }
+        Pair before[kSteps];
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            float x0, x1;
+            two(x + k * kCols, x0, x1);
+            if (!all) {
+                if (k >= live0) x0 = 0.0f;
+                if (k >= live1) x1 = 0.0f;
+            }
+            const Pair xv = pair(x0, x1);
+            before[k] = fma2(xv, pair(-1.0f), h);  // h_{t-1} - x_t
+            h = fma2(a[k], h, b[k] * xv);
+        }
+        Writer<T, kBytes> dz(p.dz, col, ts + kSteps - 1), dx(p.dx, col, ts + kSteps - 1);
+        const int whole = within(p.steps, ts);
+#pragma unroll
+        for (int k = kSteps - 1; k >= 0; --k) {
+            float d0, d1;
+            two(d + k * kCols, d0, d1);
+            if (!all) {
+                if (k >= live0) d0 = 0.0f;
+                if (k >= live1) d1 = 0.0f;
+            }
+            const Pair G = fma2(q, pair(1.0f), pair(d0, d1)), g = b[k] * G;
             q = a[k] * G;
+            float v0, v1;
+            if (k < whole) {
+                split(g, v0, v1);
+                dx.put(k < live0 ? v0 : 0.0f, k < live1 ? v1 : 0.0f, col[0].on, col[1].on);
+                split(a[k] * g * before[k], v0, v1);
+                dz.put(k < live0 ? v0 : 0.0f, k < live1 ? v1 : 0.0f, col[0].on, col[1].on);
+            }
+            dz.move(-1);
+            dx.move(-1);
         }
     }
-    if (p.dh0 && col.on && rank == 0 && warp == 0) p.dh0[col.i] = p0;
-    if (ranks > 1) cluster_sync();  // the others may still read this CTA's totals
+    if (p.dh0 && rank == 0 && warp == 0) {
+        float v[2];
+        split(p0, v[0], v[1]);
+        for (int j = 0; j < 2; ++j)
+            if (col[j].on) p.dh0[col[j].b * p.channels + col[j].c] = v[j];
+    }
+    if (ranks > 1) cluster_sync();  // no CTA ends while another may write to it
 }
 
 // Launches a kernel of clusters, behind the kernel ahead of it as launch_after does.
-cudaError_t launch_ranks(void (*kern)(RecArgs, uint32_t), int threads, const RecArgs& p, cudaStream_t stream)
+template <void (*kern)(RecArgs, uint32_t)>
+cudaError_t launch_ranks(bool rows16, int shared, const RecArgs& p, cudaStream_t stream)
 {
+    static bool set[64] = {};  // the kernel's shared memory, once per device
+
     uint32_t ranks = 1;
-    while (ranks < 8 && (int64_t)ranks * kRecChunk < p.steps) ranks *= 2;
-    const int64_t tiles = (p.batch * p.channels + 31) / 32;
-    if (tiles > 0x7fffffff / ranks) return cudaErrorInvalidConfiguration;
+    while (ranks < (uint32_t)kRanks && (int64_t)ranks * kSpan < p.steps) ranks *= 2;
+    const int64_t tiles = rows16 ? p.batch * p.blocks : (p.batch * p.channels + kCols - 1) / kCols;
+    if (tiles > 0x7fffffff / (int64_t)ranks) return cudaErrorInvalidConfiguration;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+    if (e == cudaSuccess && !set[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+        set[dev] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * ranks));
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = dim3((unsigned)kThreads);
+    cfg.dynamicSmemBytes = (size_t)shared;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -330,6 +572,15 @@ cudaError_t launch_ranks(void (*kern)(RecArgs, uint32_t), int threads, const Rec
     return cudaLaunchKernelEx(&cfg, kern, p, ranks);
 }
 
+// How many bytes at a time the rows of all given tensors can be copied: 16, 4 or 2.
+int row_bytes(const RecArgs& p, int e, std::initializer_list<const RecSeq*> seqs)
+{
+    int64_t bits = 0;
+    for (const RecSeq* s : seqs) bits |= (int64_t)reinterpret_cast<uintptr_t>(s->p) | s->batch * e | s->step * e;
+    if (bits % 16 == 0 && p.channels >= kCols) return 16;
+    return e == 4 || ((bits | p.channels * e) % 4 == 0) ? 4 : 2;
+}
+
 template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
 {
     const int64_t n = p.batch * p.channels;
@@ -338,12 +589,21 @@ template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
         return launch_after(rec_forward_few_kernel<T>, dim3((unsigned)((n + kRecThreads - 1) / kRecThreads)),
                             dim3(kRecThreads), 0, stream, p);
     }
-    return launch_ranks(rec_forward_kernel<T, kForwardSteps>, 32 * kRecChunk / kForwardSteps, p, stream);
+    const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.y}), shared = 4 * kSpan * kCols * (int)sizeof(T);
+    if (by == 16) return launch_ranks<rec_forward_kernel<T, 16>>(true, shared, p, stream);
+    if constexpr (sizeof(T) == 2)
+        if (by == 2) return launch_ranks<rec_forward_kernel<T, 2>>(false, shared, p, stream);
+    return launch_ranks<rec_forward_kernel<T, 4>>(false, shared, p, stream);
 }
 
 template <typename T> cudaError_t backward(const RecArgs& p, cudaStream_t stream)
 {
-    return launch_ranks(rec_backward_kernel<T, kBackwardSteps>, 32 * kRecChunk / kBackwardSteps, p, stream);
+    const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.dy, &p.dz, &p.dx});
+    const int shared = 6 * kSpan * kCols * (int)sizeof(T);
+    if (by == 16) return launch_ranks<rec_backward_kernel<T, 16>>(true, shared, p, stream);
+    if constexpr (sizeof(T) == 2)
+        if (by == 2) return launch_ranks<rec_backward_kernel<T, 2>>(false, shared, p, stream);
+    return launch_ranks<rec_backward_kernel<T, 4>>(false, shared, p, stream);
 }
 
 bool rec_seq_ok(const RecSeq& s, int64_t batch, int64_t steps, int64_t channels, bool written)
@@ -414,6 +674,7 @@ adacomp_status adacomp_recurrence_forward(adacomp_recurrence_t h, int64_t batch,
     p.steps = steps;
     p.channels = h->channels;
     p.chunks = (steps + adacomp::kRecChunk - 1) / adacomp::kRecChunk;
+    p.blocks = (uint32_t)((h->channels + adacomp::kCols - 1) / adacomp::kCols);
     const cudaError_t err = h->dtype == ADACOMP_BF16 ? adacomp::forward<adacomp::bf16>(p, stream)
                                                      : adacomp::forward<float>(p, stream);
     return adacomp::launch_result(err, stream);
@@ -453,6 +714,7 @@ adacomp_status adacomp_recurrence_backward(adacomp_recurrence_t h, int64_t batch
     p.steps = steps;
     p.channels = h->channels;
     p.chunks = (steps + adacomp::kRecChunk - 1) / adacomp::kRecChunk;
+    p.blocks = (uint32_t)((h->channels + adacomp::kCols - 1) / adacomp::kCols);
     const cudaError_t err = h->dtype == ADACOMP_BF16 ? adacomp::backward<adacomp::bf16>(p, stream)
                                                      : adacomp::backward<float>(p, stream);
     return adacomp::launch_result(err, stream);

@@ -56,11 +56,49 @@ template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ bf16 from_f32<bf16>(float v) { return __float2bfloat16_rn(v); }
 
+__device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// ---------------------------------------------------------------- pairs
+// Two fp32 values that one instruction computes with. Every operation rounds as its scalar
+// form does (.rn: no contraction).
+struct Pair {
+    unsigned long long b;
+};
+
+__device__ __forceinline__ Pair pair(float x, float y)
+{
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.b) : "f"(x), "f"(y));
+    return p;
+}
+
+__device__ __forceinline__ Pair pair(float x) { return pair(x, x); }
+
+__device__ __forceinline__ void split(Pair p, float& x, float& y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.b));
+}
+
+__device__ __forceinline__ Pair operator*(Pair x, Pair y)
+{
+    Pair p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.b) : "l"(x.b), "l"(y.b));
+    return p;
+}
+
+__device__ __forceinline__ Pair fma2(Pair x, Pair y, Pair z)
+{
+    Pair p;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.b) : "l"(x.b), "l"(y.b), "l"(z.b));
+    return p;
 }
 
 }  // namespace
