@@ -84,13 +84,14 @@ template <typename T> __global__ void __launch_bounds__(kRecThreads) rec_forward
 // The steps are split: a warp has 64 columns (two per lane) and eight consecutive steps, a
 // CTA 64 steps, a cluster of up to eight CTAs up to 512, and where the sequence is longer the
 // cluster goes on in rounds. Each warp forms what its steps do to a state, h -> A h + H with
-// A the product of its gates; the CTA's warps exchange these through shared memory and the
-// cluster's CTAs write them into each other's; then each warp knows the state before its
-// first step and goes through its steps again, from registers. So every element is read
-// once, and no CTA waits for one that may not be running. The next round's elements are
-// copied to shared memory meanwhile. The split depends on the number of steps alone.
+// A the product of its gates. One warp of the CTA joins them, writes the CTA's own (A, H)
+// into every CTA of the cluster, waits for theirs, and leaves each warp the state before its
+// first step; the warps then go through their steps again, from registers. So every element
+// is read once, and no CTA waits for one that may not be running. The next round's elements
+// are copied to shared memory meanwhile. The split depends on the number of steps alone.
 constexpr int kCols = 64, kSteps = 8, kWarps = 8, kThreads = 32 * kWarps, kSpan = kSteps * kWarps;
 constexpr int kRanks = 8;
+constexpr int kTile = kSpan * kCols;  // elements of a tensor that a CTA has in a round
 static_assert(kRecChunk == 2 * kSpan, "a kept state every second CTA");
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -105,14 +106,7 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Writes v where `p` of this CTA's shared memory is in the CTA `rank` of the cluster.
-__device__ __forceinline__ void push(float4* p, uint32_t rank, float4 v)
-{
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
-}
+__device__ __forceinline__ uint32_t shared_address(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ Pair low_pair(float4 v) { return pair(v.x, v.y); }
 __device__ __forceinline__ Pair high_pair(float4 v) { return pair(v.z, v.w); }
@@ -123,6 +117,63 @@ __device__ __forceinline__ float4 quad(Pair a, Pair b)
     split(a, v.x, v.y);
     split(b, v.z, v.w);
     return v;
+}
+
+__device__ __forceinline__ float2 duo(Pair a)
+{
+    float2 v;
+    split(a, v.x, v.y);
+    return v;
+}
+
+// What the CTAs of a cluster write to each other in a round: each CTA's values, and the
+// barrier that counts their bytes. Two of them take turns: a CTA that writes for the round
+// after next has all others' values of the next one, so that they have read these.
+// (A barrier of the whole cluster would have to wait for each round's stores of results.)
+struct Exchange {
+    float4 value[kRanks][32];
+    float4 before[32];  // backward: the (A, H) of the CTA before, where the chunk is its
+    unsigned long long barrier;
+};
+
+__device__ __forceinline__ void exchange_init(Exchange* x)
+{
+    if (threadIdx.x < 2)
+        asm volatile("mbarrier.init.shared.b64 [%0], 1;" ::"r"(shared_address(&x[threadIdx.x].barrier)) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+__device__ __forceinline__ void exchange_expect(Exchange* x, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(shared_address(&x->barrier)), "r"(bytes)
+                 : "memory");
+}
+
+// Writes v to the place of `p` in the CTA `rank`, and counts it at that CTA's barrier.
+__device__ __forceinline__ void push(Exchange* x, float4* p, uint32_t rank, float4 v)
+{
+    uint32_t a, b;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(shared_address(p)), "r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(shared_address(&x->barrier)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(b)
+                 : "memory");
+}
+
+// Waits for a barrier's phase. The CTAs of a cluster run together and each writes before it
+// waits, so the wait ends; were it not to, it is given up after some seconds.
+__device__ __forceinline__ bool exchange_wait(Exchange* x, uint32_t phase)
+{
+    for (uint32_t i = 0; i < (1u << 22); ++i) {
+        uint32_t done;
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+            : "=r"(done)
+            : "r"(shared_address(&x->barrier)), "r"(phase)
+            : "memory");
+        if (done) return true;
+    }
+    return false;
 }
 
 // The columns of a tile. Where a sequence's rows are read 16 bytes at a time (kBytes), a
@@ -147,59 +198,71 @@ template <int kBytes> struct Column {
         }
         len = on ? (int32_t)length_of(p, b) : 0;
     }
+    __device__ __forceinline__ int64_t state(const RecArgs& p) const { return b * p.channels + c; }
 };
+
+// Distances between rows: in 32 bits where the rows are read 16 bytes at a time (the host
+// sees to it), so that an address is one instruction.
+template <int kBytes> using Distance = typename std::conditional<kBytes == 16, int32_t, int64_t>::type;
+
+template <typename T> __device__ __forceinline__ T* moved(T* p, int64_t bytes)
+{
+    return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + bytes);
+}
 
 // Copies a CTA's 64 steps of a tile to shared memory, [step][column], kBytes at a time:
 // every thread has one place in the rows and takes every kStride-th of them. What lies past
 // a sequence's length or the last channel is not read, and what stands there not used.
-template <typename T, int kBytes> struct Copier {
+template <typename T, int kBytes, int kTensors> struct Copier {
     static constexpr int kPlaces = kCols * (int)sizeof(T) / kBytes;
     static constexpr int kStride = kThreads / kPlaces;
     static constexpr int kEach = kBytes / (int)sizeof(T);  // elements at a time
-    int64_t b, c;
+    const T* from[kTensors];
+    Distance<kBytes> step[kTensors];
     int32_t len;
     uint32_t bytes;
 
-    __device__ __forceinline__ Copier(const RecArgs& p, uint32_t tile)
+    __device__ __forceinline__ Copier(const RecArgs& p, uint32_t tile, const RecSeq* const (&s)[kTensors])
     {
         const Column<kBytes> col(p, tile, (threadIdx.x % kPlaces) * kEach);
-        b = col.b;
-        c = col.c;
-        len = col.len;
-        const int64_t rest = (p.channels - c) * (int)sizeof(T);
+        const int64_t rest = (p.channels - col.c) * (int)sizeof(T);
         bytes = !col.on ? 0u : rest < kBytes ? (uint32_t)rest : (uint32_t)kBytes;
-        if (bytes == 0) len = 0;
+        len = bytes == 0 ? 0 : col.len;
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i) {
+            from[i] = at<const T>(*s[i], col.b, 0, col.c);
+            step[i] = (Distance<kBytes>)(s[i]->step * (int)sizeof(T));
+        }
     }
 
-    __device__ __forceinline__ void copy(T* to, const RecSeq& s, int64_t t0) const
+    __device__ __forceinline__ void copy(T* to, int32_t t0) const
     {
-        const int row0 = threadIdx.x / kPlaces;
-        const int left = (int)(len - t0 < 0 ? 0 : len - t0 > kSpan ? kSpan : len - t0);
-        const T* from = static_cast<const T*>(s.p) + b * s.batch + (t0 + row0) * s.step + c;
-        T* at = to + row0 * kCols + (threadIdx.x % kPlaces) * kEach;
-        if constexpr (kBytes == 2) {
+        const int row0 = threadIdx.x / kPlaces, left = len - t0;
+        T* const place = to + row0 * kCols + (threadIdx.x % kPlaces) * kEach;
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i) {
+            const T* const f = moved(from[i], (int64_t)(t0 + row0) * step[i]);
             T v[kSpan / kStride];
 #pragma unroll
-            for (int k = 0; k < kSpan / kStride; ++k, from += kStride * s.step)
-                if (row0 + k * kStride < left) v[k] = *from;
-#pragma unroll
-            for (int k = 0; k < kSpan / kStride; ++k) at[k * kStride * kCols] = v[k];
-        } else {
-#pragma unroll
-            for (int k = 0; k < kSpan / kStride; ++k, from += kStride * s.step)
+            for (int k = 0; k < kSpan / kStride; ++k)
                 if (row0 + k * kStride < left) {
-                    const uint32_t d = (uint32_t)__cvta_generic_to_shared(at + k * kStride * kCols);
-                    if constexpr (kBytes == 16)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(from), "r"(bytes)
-                                     : "memory");
-                    else
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(from) : "memory");
+                    const T* const g = moved(f, (Distance<kBytes>)(k * kStride) * step[i]);
+                    const uint32_t d = shared_address(place + i * kTile + k * kStride * kCols);
+                    if constexpr (kBytes == 2) v[k] = *g;
+                    else if constexpr (kBytes == 16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(g), "r"(bytes) : "memory");
+                    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(g) : "memory");
                 }
+            if constexpr (kBytes == 2) {
+#pragma unroll
+                for (int k = 0; k < kSpan / kStride; ++k)
+                    if (row0 + k * kStride < left) place[i * kTile + k * kStride * kCols] = v[k];
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
 };
 
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ void two(const float* p, float& x, float& y)
@@ -214,97 +277,122 @@ __device__ __forceinline__ void two(const bf16* p, float& x, float& y)
     x = bf16_low(v), y = bf16_high(v);
 }
 
-// One step of a lane's two columns.
+// Where a lane's two columns of a warp's steps go.
 template <typename T, int kBytes> struct Writer {
     T* p[2];
-    int64_t step;
+    Distance<kBytes> step;
 
-    __device__ __forceinline__ Writer(const RecSeq& s, const Column<kBytes> (&col)[2], int64_t t) : step(s.step)
+    __device__ __forceinline__ Writer(const RecSeq& s, const Column<kBytes> (&col)[2], int64_t t)
+        : step((Distance<kBytes>)(s.step * (int)sizeof(T)))
     {
         p[0] = at<T>(s, col[0].b, t, col[0].c);
         if (kBytes != 16) p[1] = at<T>(s, col[1].b, t, col[1].c);
     }
-    __device__ __forceinline__ void move(int by)
+    // step k of both columns, which are there
+    __device__ __forceinline__ void put(int k, Pair v) const
     {
-        p[0] += by * step;
-        if (kBytes != 16) p[1] += by * step;
-    }
-    __device__ __forceinline__ void put(float x, float y, bool on0, bool on1) const
-    {
-        if (kBytes == 16) {
-            if (on1) {
-                if constexpr (sizeof(T) == 4) {
-                    *reinterpret_cast<float2*>(p[0]) = make_float2(x, y);
-                } else {
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-                    *reinterpret_cast<__nv_bfloat162*>(p[0]) = v;
-                }
-            } else if (on0) {
-                *p[0] = from_f32<T>(x);
-            }
+        float x, y;
+        split(v, x, y);
+        T* const q = moved(p[0], k * step);
+        if constexpr (kBytes == 16) {
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(q) = make_float2(x, y);
+            else *reinterpret_cast<__nv_bfloat162*>(q) = __floats2bfloat162_rn(x, y);
         } else {
-            if (on0) *p[0] = from_f32<T>(x);
-            if (on1) *p[1] = from_f32<T>(y);
+            *q = from_f32<T>(x);
+            *moved(p[1], k * step) = from_f32<T>(y);
         }
+    }
+    __device__ __forceinline__ void put(int k, float x, float y, bool on0, bool on1) const
+    {
+        T* const q = moved(p[0], k * step);
+        if (on0) *q = from_f32<T>(x);
+        if (on1) *(kBytes == 16 ? q + 1 : moved(p[1], k * step)) = from_f32<T>(y);
     }
 };
 
-// How many of a warp's steps from ts on lie within `len`.
-__device__ __forceinline__ int within(int64_t len, int64_t ts)
+// What a warp has to mind in a round: how many of its steps lie within each column's length
+// and within the tensors, and whether all do.
+struct Live {
+    int live0, live1, whole;
+    bool all;
+
+    template <int kBytes>
+    __device__ __forceinline__ Live(const RecArgs& p, const Column<kBytes> (&col)[2], int32_t ts)
+        : live0(max(0, min(kSteps, col[0].len - ts))), live1(max(0, min(kSteps, col[1].len - ts))),
+          whole(max(0, min(kSteps, (int32_t)p.steps - ts))),
+          all(__all_sync(0xffffffffu, live0 == kSteps && live1 == kSteps))
+    {
+    }
+};
+
+template <int kBytes>
+__device__ __forceinline__ Pair load_state(const float* p, const RecArgs& a, const Column<kBytes> (&col)[2], int64_t more = 0)
 {
-    return (int)(len - ts < 0 ? 0 : len - ts > kSteps ? kSteps : len - ts);
+    float v[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (p && col[j].on) v[j] = p[col[j].state(a) + more];
+    return pair(v[0], v[1]);
+}
+
+template <int kBytes>
+__device__ __forceinline__ void store_state(float* p, const RecArgs& a, const Column<kBytes> (&col)[2], Pair s)
+{
+    float v[2];
+    split(s, v[0], v[1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (p && col[j].on) p[col[j].state(a)] = v[j];
+}
+
+// The address of a column's kept state: [batch][chunks][channels].
+template <int kBytes> __device__ __forceinline__ float* kept(const RecArgs& p, const Column<kBytes>& col, int32_t t)
+{
+    return p.carry + (col.b * p.chunks + t / kRecChunk) * p.channels + col.c;
 }
 
 template <typename T, int kBytes>
-__global__ void __launch_bounds__(kThreads, 3) rec_forward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
+__global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
 {
     extern __shared__ __align__(16) uint8_t shared_bytes[];
-    __shared__ float4 part[kWarps][32];      // a warp's (A, H) of the lane's columns
-    __shared__ float4 total[2][kRanks][32];  // the CTAs', by the round's parity: a slower one may still read the last
-    constexpr int kTile = kSpan * kCols;
+    __shared__ float4 part[kWarps][32];   // a warp's (A, H) of the lane's columns
+    __shared__ float2 begin[kWarps][32];  // the state before its first step
+    __shared__ Exchange exchange[2];
     const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (2 * kTile); };
     ptx::griddep_wait();
-    if (ranks > 1) cluster_sync();  // all CTAs run before one writes to another
+    if (ranks > 1) {
+        exchange_init(exchange);
+        cluster_sync();  // all CTAs run, and their barriers are there, before one writes to another
+    }
     const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Column<kBytes> col[2] = {Column<kBytes>(p, tile, 2 * lane), Column<kBytes>(p, tile, 2 * lane + 1)};
-    const Copier<T, kBytes> copier(p, tile);
-    const int64_t span = (int64_t)ranks * kSpan;
-    const auto stage = [&](int64_t t0, int par) {
-        copier.copy(tile_of(par), p.z, t0 + rank * kSpan);
-        copier.copy(tile_of(par) + kTile, p.x, t0 + rank * kSpan);
-        copies_commit();
-    };
-    Pair h0;  // before the round's first step
-    {
-        float v[2] = {0.0f, 0.0f};
-        for (int j = 0; j < 2; ++j)
-            if (p.h0 && col[j].on) v[j] = p.h0[col[j].b * p.channels + col[j].c];
-        h0 = pair(v[0], v[1]);
-    }
-    stage(0, 0);
-    int par = 0;
-    for (int64_t t0 = 0; t0 < p.steps; t0 += span, par ^= 1) {
+    const Copier<T, kBytes, 2> copier(p, tile, {&p.z, &p.x});
+    const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
+    Pair h0 = load_state(p.h0, p, col);  // before the round's first step (the joining warp's)
+    bool given_up = false;
+    int32_t tc = (int32_t)rank * kSpan;
+    copier.copy(tile_of(0), tc);
+    for (int32_t t0 = 0, round = 0; t0 < steps; t0 += span, tc += span, ++round) {
+        const int par = round & 1;
         copies_wait();
         __syncthreads();
-        if (t0 + span < p.steps) stage(t0 + span, par ^ 1);
-        const int64_t tc = t0 + rank * kSpan, ts = tc + warp * kSteps;
-        const int live0 = within(col[0].len, ts), live1 = within(col[1].len, ts);
-        const bool all = __all_sync(0xffffffffu, (live0 == kSteps || !col[0].on) && (live1 == kSteps || !col[1].on));
+        if (t0 + span < steps) copier.copy(tile_of(par ^ 1), tc + span);
+        const int32_t ts = tc + warp * kSteps;
+        const Live at_hand(p, col, ts);
         const T* z = tile_of(par) + warp * kSteps * kCols + 2 * lane;
-        const T* x = z + kTile;
         Pair a[kSteps], u[kSteps], A = pair(1.0f), H = pair(0.0f);
         const auto form = [&](auto masked) {
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
                 float z0, z1, x0, x1, a0, a1, b0, b1;
                 two(z + k * kCols, z0, z1);
-                two(x + k * kCols, x0, x1);
+                two(z + k * kCols + kTile, x0, x1);
                 gate(z0, &a0, &b0);
                 gate(z1, &a1, &b1);
                 if (masked.value) {  // past the length the state stays as it is
-                    if (k >= live0) a0 = 1.0f, b0 = x0 = 0.0f;
-                    if (k >= live1) a1 = 1.0f, b1 = x1 = 0.0f;
+                    if (k >= at_hand.live0) a0 = 1.0f, b0 = x0 = 0.0f;
+                    if (k >= at_hand.live1) a1 = 1.0f, b1 = x1 = 0.0f;
                 }
                 a[k] = pair(a0, a1);
                 u[k] = pair(b0, b1) * pair(x0, x1);
@@ -312,12 +400,15 @@ __global__ void __launch_bounds__(kThreads, 3) rec_forward_kernel(const __grid_c
                 A = A * a[k];
             }
         };
-        if (all) form(std::false_type());
+        if (at_hand.all) form(std::false_type());
         else form(std::true_type());
         part[warp][lane] = quad(A, H);
         __syncthreads();
-        if (ranks > 1) {  // a warp for each CTA to write to
-            if (warp < (int)ranks) {
+        if (warp == 0) {
+            Pair h = h0;  // before the CTA's first step
+            if (ranks > 1) {
+                Exchange& x = exchange[par];
+                if (lane == 0) exchange_expect(&x, ranks * 512);
                 Pair tA = pair(1.0f), tH = pair(0.0f);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
@@ -325,50 +416,52 @@ __global__ void __launch_bounds__(kThreads, 3) rec_forward_kernel(const __grid_c
                     tH = fma2(low_pair(q), tH, high_pair(q));
                     tA = tA * low_pair(q);
                 }
-                push(&total[par][rank][lane], (uint32_t)warp, quad(tA, tH));
+                for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tH));
+                if (!given_up) given_up = !exchange_wait(&x, (round >> 1) & 1);
+                for (uint32_t r = 0; r < ranks; ++r) {
+                    if (r == rank) h = h0;
+                    const float4 q = x.value[r][lane];
+                    h0 = fma2(low_pair(q), h0, high_pair(q));
+                }
+                if (given_up) h = h0 = pair(NAN);
             }
-            cluster_sync();
+            if (p.carry && tc % kRecChunk == 0 && tc < steps) {
+                const float2 v = duo(h);
+                if (col[0].on) *kept(p, col[0], tc) = v.x;
+                if (col[1].on) *kept(p, col[1], tc) = v.y;
+            }
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                begin[w][lane] = duo(h);
+                const float4 q = part[w][lane];
+                h = fma2(low_pair(q), h, high_pair(q));
+            }
+            if (ranks == 1) h0 = h;
         }
-        Pair h = h0;  // before the CTA's first step
-        if (ranks > 1) {
-            for (uint32_t r = 0; r < ranks; ++r) {
-                if (r == rank) h = h0;
-                const float4 q = total[par][r][lane];
-                h0 = fma2(low_pair(q), h0, high_pair(q));
+        __syncthreads();
+        Pair h;
+        {
+            const float2 v = begin[warp][lane];
+            h = pair(v.x, v.y);
+        }
+        const Writer<T, kBytes> y(p.y, col, ts);
+        if (at_hand.all) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                h = fma2(a[k], h, u[k]);
+                y.put(k, h);
             }
         } else {
-            for (int w = 0; w < kWarps; ++w) {
-                const float4 q = part[w][lane];
-                h0 = fma2(low_pair(q), h0, high_pair(q));
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                h = fma2(a[k], h, u[k]);
+                const float2 v = duo(h);
+                if (k < at_hand.whole)
+                    y.put(k, k < at_hand.live0 ? v.x : 0.0f, k < at_hand.live1 ? v.y : 0.0f, col[0].on, col[1].on);
             }
         }
-        if (p.carry && warp == 0 && tc % kRecChunk == 0 && tc < p.steps) {
-            float v[2];
-            split(h, v[0], v[1]);
-            for (int j = 0; j < 2; ++j)
-                if (col[j].on) p.carry[(col[j].b * p.chunks + tc / kRecChunk) * p.channels + col[j].c] = v[j];
-        }
-        for (int w = 0; w < warp; ++w) {
-            const float4 q = part[w][lane];
-            h = fma2(low_pair(q), h, high_pair(q));
-        }
-        Writer<T, kBytes> y(p.y, col, ts);
-        const int whole = within(p.steps, ts);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-            h = fma2(a[k], h, u[k]);
-            float v0, v1;
-            split(h, v0, v1);
-            if (k < whole) y.put(k < live0 ? v0 : 0.0f, k < live1 ? v1 : 0.0f, col[0].on, col[1].on);
-            y.move(1);
-        }
     }
-    if (p.h_last && rank == 0 && warp == 0) {
-        float v[2];
-        split(h0, v[0], v[1]);
-        for (int j = 0; j < 2; ++j)
-            if (col[j].on) p.h_last[col[j].b * p.channels + col[j].c] = v[j];
-    }
+    if (rank == 0 && warp == 0) store_state(p.h_last, p, col, h0);
     if (ranks > 1) cluster_sync();  // no CTA ends while another may write to it
 }
 
@@ -380,161 +473,141 @@ template <typename T, int kBytes>
 __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
 {
     extern __shared__ __align__(16) uint8_t shared_bytes[];
-    __shared__ float4 part[kWarps][32];      // a warp's (A, H)
-    __shared__ float2 grad[kWarps][32];      // its P
-    __shared__ float4 total[2][kRanks][32];  // the CTAs' (A, P)
-    __shared__ float4 first[2][32];          // the (A, H) of the CTA before, where the chunk is its
-    constexpr int kTile = kSpan * kCols;
+    __shared__ float4 part[kWarps][32];   // a warp's (A, H)
+    __shared__ float2 grad[kWarps][32];   // its P
+    __shared__ float4 begin[kWarps][32];  // the state before its first step, and p after its last
+    __shared__ Exchange exchange[2];
     const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (3 * kTile); };
     ptx::griddep_wait();
-    if (ranks > 1) cluster_sync();  // all CTAs run before one writes to another
+    if (ranks > 1) {
+        exchange_init(exchange);
+        cluster_sync();  // all CTAs run, and their barriers are there, before one writes to another
+    }
     const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Column<kBytes> col[2] = {Column<kBytes>(p, tile, 2 * lane), Column<kBytes>(p, tile, 2 * lane + 1)};
-    const Copier<T, kBytes> copier(p, tile);
-    const int64_t span = (int64_t)ranks * kSpan;
-    const auto stage = [&](int64_t t0, int par) {
-        copier.copy(tile_of(par), p.z, t0 + rank * kSpan);
-        copier.copy(tile_of(par) + kTile, p.x, t0 + rank * kSpan);
-        copier.copy(tile_of(par) + 2 * kTile, p.dy, t0 + rank * kSpan);
-        copies_commit();
-    };
-    Pair p0;  // after the round's last step
-    {
-        float v[2] = {0.0f, 0.0f};
-        for (int j = 0; j < 2; ++j)
-            if (p.dh_last && col[j].on) v[j] = p.dh_last[col[j].b * p.channels + col[j].c];
-        p0 = pair(v[0], v[1]);
-    }
-    const int64_t last = p.steps > 0 ? (p.steps - 1) / span * span : -1;
-    if (last >= 0) stage(last, 0);
-    int par = 0;
-    for (int64_t t0 = last; t0 >= 0; t0 -= span, par ^= 1) {
-        const int64_t tc = t0 + rank * kSpan, ts = tc + warp * kSteps, chunk = tc / kRecChunk;
+    const Copier<T, kBytes, 3> copier(p, tile, {&p.z, &p.x, &p.dy});
+    const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
+    Pair p0 = load_state(p.dh_last, p, col);  // after the round's last step (the joining warp's)
+    bool given_up = false;
+    int32_t t0 = steps > 0 ? (steps - 1) / span * span : -1, tc = t0 + (int32_t)rank * kSpan;
+    if (t0 >= 0) copier.copy(tile_of(0), tc);
+    for (int32_t round = 0; t0 >= 0; t0 -= span, tc -= span, ++round) {
+        const int par = round & 1;
         Pair h = pair(0.0f);  // before the chunk's first step
-        {
-            float v[2] = {0.0f, 0.0f};
-            for (int j = 0; j < 2; ++j)
-                if (col[j].on && tc < p.steps) v[j] = p.carry[(col[j].b * p.chunks + chunk) * p.channels + col[j].c];
-            h = pair(v[0], v[1]);
-        }
+        if (warp == 0 && tc < steps)
+            h = pair(col[0].on ? *kept(p, col[0], tc) : 0.0f, col[1].on ? *kept(p, col[1], tc) : 0.0f);
         copies_wait();
         __syncthreads();
-        if (t0 > 0) stage(t0 - span, par ^ 1);
-        const int live0 = within(col[0].len, ts), live1 = within(col[1].len, ts);
-        const bool all = __all_sync(0xffffffffu, (live0 == kSteps || !col[0].on) && (live1 == kSteps || !col[1].on));
+        if (t0 > 0) copier.copy(tile_of(par ^ 1), tc - span);
+        const int32_t ts = tc + warp * kSteps;
+        const Live at_hand(p, col, ts);
         const T* z = tile_of(par) + warp * kSteps * kCols + 2 * lane;
-        const T *x = z + kTile, *d = x + kTile;
         Pair a[kSteps], b[kSteps], A = pair(1.0f), H = pair(0.0f), P = pair(0.0f);
+        const auto inputs = [&](auto masked, int tensor, int k) {  // x or dy
+            float v0, v1;
+            two(z + k * kCols + tensor * kTile, v0, v1);
+            if (masked.value) {
+                if (k >= at_hand.live0) v0 = 0.0f;
+                if (k >= at_hand.live1) v1 = 0.0f;
+            }
+            return pair(v0, v1);
+        };
         const auto form = [&](auto masked) {
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
-                float z0, z1, x0, x1, d0, d1, a0, a1, b0, b1;
+                float z0, z1, a0, a1, b0, b1;
                 two(z + k * kCols, z0, z1);
-                two(x + k * kCols, x0, x1);
-                two(d + k * kCols, d0, d1);
                 gate(z0, &a0, &b0);
                 gate(z1, &a1, &b1);
                 if (masked.value) {
-                    if (k >= live0) a0 = 1.0f, b0 = x0 = d0 = 0.0f;
-                    if (k >= live1) a1 = 1.0f, b1 = x1 = d1 = 0.0f;
+                    if (k >= at_hand.live0) a0 = 1.0f, b0 = 0.0f;
+                    if (k >= at_hand.live1) a1 = 1.0f, b1 = 0.0f;
                 }
                 a[k] = pair(a0, a1);
                 b[k] = pair(b0, b1);
-                H = fma2(a[k], H, b[k] * pair(x0, x1));
+                H = fma2(a[k], H, b[k] * inputs(masked, 1, k));
                 A = A * a[k];
-                P = fma2(A, pair(d0, d1), P);
+                P = fma2(A, inputs(masked, 2, k), P);
             }
         };
-        if (all) form(std::false_type());
+        if (at_hand.all) form(std::false_type());
         else form(std::true_type());
         part[warp][lane] = quad(A, H);
-        {
-            float2 v;
-            split(P, v.x, v.y);
-            grad[warp][lane] = v;
-        }
+        grad[warp][lane] = duo(P);
         __syncthreads();
-        if (ranks > 1) {
-            if (warp < (int)ranks) {
+        if (warp == 0) {
+            Pair q = p0;  // after the CTA's last step
+            if (ranks > 1) {
+                Exchange& x = exchange[par];
+                if (lane == 0) exchange_expect(&x, ranks * 512 + (rank & 1) * 512);
                 Pair tA = pair(1.0f), tH = pair(0.0f), tP = pair(0.0f);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float4 q = part[w][lane];
+                    const float4 v = part[w][lane];
                     const float2 g = grad[w][lane];
-                    tH = fma2(low_pair(q), tH, high_pair(q));
+                    tH = fma2(low_pair(v), tH, high_pair(v));
                     tP = fma2(tA, pair(g.x, g.y), tP);
-                    tA = tA * low_pair(q);
+                    tA = tA * low_pair(v);
                 }
-                push(&total[par][rank][lane], (uint32_t)warp, quad(tA, tP));
-                if ((rank & 1) == 0 && warp == (int)rank + 1) push(&first[par][lane], (uint32_t)warp, quad(tA, tH));
+                for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tP));
+                if ((rank & 1) == 0) push(&x, &x.before[lane], rank + 1, quad(tA, tH));
+                if (!given_up) given_up = !exchange_wait(&x, (round >> 1) & 1);
+                for (uint32_t r = ranks; r-- > 0;) {
+                    if (r == rank) q = p0;
+                    const float4 v = x.value[r][lane];
+                    p0 = fma2(low_pair(v), p0, high_pair(v));
+                }
+                if (rank & 1) h = fma2(low_pair(x.before[lane]), h, high_pair(x.before[lane]));
+                if (given_up) h = q = p0 = pair(NAN);
             }
-            cluster_sync();
-        }
-        Pair q = p0;  // after the CTA's last step
-        if (ranks > 1) {
-            for (uint32_t r = ranks; r-- > 0;) {
-                if (r == rank) q = p0;
-                const float4 v = total[par][r][lane];
-                p0 = fma2(low_pair(v), p0, high_pair(v));
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 v = duo(h);
+                begin[w][lane].x = v.x;
+                begin[w][lane].y = v.y;
+                h = fma2(low_pair(part[w][lane]), h, high_pair(part[w][lane]));
             }
-            if (rank & 1) h = fma2(low_pair(first[par][lane]), h, high_pair(first[par][lane]));
-        } else {
+#pragma unroll
             for (int w = kWarps - 1; w >= 0; --w) {
-                const float2 g = grad[w][lane];
-                p0 = fma2(low_pair(part[w][lane]), p0, pair(g.x, g.y));
+                const float2 v = duo(q), g = grad[w][lane];
+                begin[w][lane].z = v.x;
+                begin[w][lane].w = v.y;
+                q = fma2(low_pair(part[w][lane]), q, pair(g.x, g.y));
             }
+            if (ranks == 1) p0 = q;
         }
-        for (int w = 0; w < warp; ++w) {
-            const float4 v = part[w][lane];
-            h = fma2(low_pair(v), h, high_pair(v));
-        }
-        for (int w = kWarps - 1; w > warp; --w) {
-            const float2 g = grad[w][lane];
-            q = fma2(low_pair(part[w][lane]), q, pair(g.x, g.y));
-        }
-        Pair before[kSteps];
+        __syncthreads();
+        const float4 start = begin[warp][lane];
+        const Writer<T, kBytes> dz(p.dz, col, ts), dx(p.dx, col, ts);
+        const auto finish = [&](auto masked) {
+            Pair h = low_pair(start), q = high_pair(start), before[kSteps];
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-            float x0, x1;
-            two(x + k * kCols, x0, x1);
-            if (!all) {
-                if (k >= live0) x0 = 0.0f;
-                if (k >= live1) x1 = 0.0f;
+            for (int k = 0; k < kSteps; ++k) {
+                const Pair x = inputs(masked, 1, k);
+                before[k] = fma2(x, pair(-1.0f), h);  // h_{t-1} - x_t
+                h = fma2(a[k], h, b[k] * x);
             }
-            const Pair xv = pair(x0, x1);
-            before[k] = fma2(xv, pair(-1.0f), h);  // h_{t-1} - x_t
-            h = fma2(a[k], h, b[k] * xv);
-        }
-        Writer<T, kBytes> dz(p.dz, col, ts + kSteps - 1), dx(p.dx, col, ts + kSteps - 1);
-        const int whole = within(p.steps, ts);
 #pragma unroll
-        for (int k = kSteps - 1; k >= 0; --k) {
-            float d0, d1;
-            two(d + k * kCols, d0, d1);
-            if (!all) {
-                if (k >= live0) d0 = 0.0f;
-                if (k >= live1) d1 = 0.0f;
+            for (int k = kSteps - 1; k >= 0; --k) {
+                const Pair G = fma2(q, pair(1.0f), inputs(masked, 2, k)), g = b[k] * G;
+                q = a[k] * G;
+                const Pair v = a[k] * g * before[k];
+                if (!masked.value) {
+                    dx.put(k, g);
+                    dz.put(k, v);
+                } else if (k < at_hand.whole) {
+                    const float2 e = duo(g), f = duo(v);
+                    const bool l0 = k < at_hand.live0, l1 = k < at_hand.live1;
+                    dx.put(k, l0 ? e.x : 0.0f, l1 ? e.y : 0.0f, col[0].on, col[1].on);
+                    dz.put(k, l0 ? f.x : 0.0f, l1 ? f.y : 0.0f, col[0].on, col[1].on);
+                }
             }
-            const Pair G = fma2(q, pair(1.0f), pair(d0, d1)), g = b[k] * G;
-            q = a[k] * G;
-            float v0, v1;
-            if (k < whole) {
-                split(g, v0, v1);
-                dx.put(k < live0 ? v0 : 0.0f, k < live1 ? v1 : 0.0f, col[0].on, col[1].on);
-                split(a[k] * g * before[k], v0, v1);
-                dz.put(k < live0 ? v0 : 0.0f, k < live1 ? v1 : 0.0f, col[0].on, col[1].on);
-            }
-            dz.move(-1);
-            dx.move(-1);
-        }
+        };
+        if (at_hand.all) finish(std::false_type());
+        else finish(std::true_type());
     }
-    if (p.dh0 && rank == 0 && warp == 0) {
-        float v[2];
-        split(p0, v[0], v[1]);
-        for (int j = 0; j < 2; ++j)
-            if (col[j].on) p.dh0[col[j].b * p.channels + col[j].c] = v[j];
-    }
+    if (rank == 0 && warp == 0) store_state(p.dh0, p, col, p0);
     if (ranks > 1) cluster_sync();  // no CTA ends while another may write to it
 }
 
@@ -576,8 +649,12 @@ cudaError_t launch_ranks(bool rows16, int shared, const RecArgs& p, cudaStream_t
 int row_bytes(const RecArgs& p, int e, std::initializer_list<const RecSeq*> seqs)
 {
     int64_t bits = 0;
-    for (const RecSeq* s : seqs) bits |= (int64_t)reinterpret_cast<uintptr_t>(s->p) | s->batch * e | s->step * e;
-    if (bits % 16 == 0 && p.channels >= kCols) return 16;
+    bool near = true;  // a CTA's steps span less than 2^31 bytes
+    for (const RecSeq* s : seqs) {
+        bits |= (int64_t)reinterpret_cast<uintptr_t>(s->p) | s->batch * e | s->step * e;
+        near = near && s->step < (int64_t)1 << 22;
+    }
+    if (bits % 16 == 0 && near && p.channels >= kCols) return 16;
     return e == 4 || ((bits | p.channels * e) % 4 == 0) ? 4 : 2;
 }
 
@@ -641,7 +718,7 @@ size_t adacomp_recurrence_carry_bytes(adacomp_recurrence_t h, int64_t batch, int
 
 static adacomp_status rec_sizes(const adacomp_recurrence* h, int64_t batch, int64_t steps)
 {
-    if (!h || batch < 0 || steps < 0 || batch > 0x7fffffff || steps > 0x7fffffff) return ADACOMP_ERR_INVALID_ARG;
+    if (!h || batch < 0 || steps < 0 || batch > 0x7fffffff || steps > 0x7fff0000) return ADACOMP_ERR_INVALID_ARG;
     return ADACOMP_OK;
 }
 
