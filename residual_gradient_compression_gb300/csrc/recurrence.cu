@@ -84,11 +84,11 @@ template <typename T> __global__ void __launch_bounds__(kRecThreads) rec_forward
 // The steps are split: a warp has 64 columns (two per lane) and eight consecutive steps, a
 // CTA 64 steps, a cluster of up to eight CTAs up to 512, and where the sequence is longer the
 // cluster goes on in rounds. Each warp forms what its steps do to a state, h -> A h + H with
-// A the product of its gates. One warp of the CTA joins them, writes the CTA's own (A, H)
-// into every CTA of the cluster, waits for theirs, and leaves each warp the state before its
-// first step; the warps then go through their steps again, from registers. So every element
+// A the product of its gates. The warps exchange these through shared memory, and the CTAs
+// write theirs into every CTA of the cluster (one warp of each does); then each warp knows
+// the state before its first step and goes through its steps again, from registers. So every element
 // is read once, and no CTA waits for one that may not be running. The next round's elements
-// are copied to shared memory meanwhile. The split depends on the number of steps alone.
+// are copied to shared memory meanwhile.
 constexpr int kCols = 64, kSteps = 8, kWarps = 8, kThreads = 32 * kWarps, kSpan = kSteps * kWarps;
 constexpr int kRanks = 8;
 constexpr int kTile = kSpan * kCols;  // elements of a tensor that a CTA has in a round
@@ -104,6 +104,12 @@ __device__ __forceinline__ uint32_t cluster_rank()
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Waits for the CTAs of the cluster without an order of memory: the results' stores need none.
+__device__ __forceinline__ void cluster_meet()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t shared_address(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
         }
     }
     if (rank == 0 && warp == 0) store_state(p.h_last, p, col, h0);
-    if (ranks > 1) cluster_sync();  // no CTA ends while another may write to it
+    if (ranks > 1) cluster_meet();  // no CTA ends while another may write to it
 }
 
 // The reverse of it: p, the gradient that reaches a state from the steps after it, goes
@@ -470,12 +476,12 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
 // step k. The states are formed again from the one that the forward pass kept for the chunk
 // of two CTAs: that is less to read than y, and not rounded.
 template <typename T, int kBytes>
-__global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
+__global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
 {
     extern __shared__ __align__(16) uint8_t shared_bytes[];
-    __shared__ float4 part[kWarps][32];   // a warp's (A, H)
-    __shared__ float2 grad[kWarps][32];   // its P
-    __shared__ float4 begin[kWarps][32];  // the state before its first step, and p after its last
+    __shared__ float4 part[kWarps][32];  // a warp's (A, H)
+    __shared__ float2 grad[kWarps][32];  // its P
+    __shared__ float4 begin[32];         // the state before the CTA's first step, and p after its last
     __shared__ Exchange exchange[2];
     const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (3 * kTile); };
     ptx::griddep_wait();
@@ -486,16 +492,16 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(const __grid_
     const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Column<kBytes> col[2] = {Column<kBytes>(p, tile, 2 * lane), Column<kBytes>(p, tile, 2 * lane + 1)};
-    const Copier<T, kBytes, 3> copier(p, tile, {&p.z, &p.x, &p.dy});
     const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
+    int32_t t0 = steps > 0 ? (steps - 1) / span * span : -1, tc = t0 + (int32_t)rank * kSpan;
+    const Copier<T, kBytes, 3> copier(p, tile, {&p.z, &p.x, &p.dy});
     Pair p0 = load_state(p.dh_last, p, col);  // after the round's last step (the joining warp's)
     bool given_up = false;
-    int32_t t0 = steps > 0 ? (steps - 1) / span * span : -1, tc = t0 + (int32_t)rank * kSpan;
     if (t0 >= 0) copier.copy(tile_of(0), tc);
     for (int32_t round = 0; t0 >= 0; t0 -= span, tc -= span, ++round) {
         const int par = round & 1;
         Pair h = pair(0.0f);  // before the chunk's first step
-        if (warp == 0 && tc < steps)
+        if (warp == kWarps - 1 && tc < steps)
             h = pair(col[0].on ? *kept(p, col[0], tc) : 0.0f, col[1].on ? *kept(p, col[1], tc) : 0.0f);
         copies_wait();
         __syncthreads();
@@ -536,20 +542,29 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(const __grid_
         part[warp][lane] = quad(A, H);
         grad[warp][lane] = duo(P);
         __syncthreads();
-        if (warp == 0) {
-            Pair q = p0;  // after the CTA's last step
+        A = pair(1.0f), H = pair(0.0f);  // from the CTA's first step to the warp's
+        for (int w = 0; w < warp; ++w) {
+            const float4 v = part[w][lane];
+            H = fma2(low_pair(v), H, high_pair(v));
+            A = A * low_pair(v);
+        }
+        Pair B = pair(1.0f);  // and from the CTA's end back to the warp's
+        P = pair(0.0f);
+        for (int w = kWarps - 1; w > warp; --w) {
+            const Pair v = low_pair(part[w][lane]);
+            P = fma2(v, P, pair(grad[w][lane].x, grad[w][lane].y));
+            B = B * v;
+        }
+        if (warp == kWarps - 1) {
+            const float4 own = part[warp][lane];
+            const Pair tA = A * low_pair(own), tH = fma2(low_pair(own), H, high_pair(own));
+            Pair tP = pair(0.0f), q = p0;  // q: after the CTA's last step
+#pragma unroll
+            for (int w = kWarps - 1; w >= 0; --w)
+                tP = fma2(low_pair(part[w][lane]), tP, pair(grad[w][lane].x, grad[w][lane].y));
             if (ranks > 1) {
                 Exchange& x = exchange[par];
                 if (lane == 0) exchange_expect(&x, ranks * 512 + (rank & 1) * 512);
-                Pair tA = pair(1.0f), tH = pair(0.0f), tP = pair(0.0f);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float4 v = part[w][lane];
-                    const float2 g = grad[w][lane];
-                    tH = fma2(low_pair(v), tH, high_pair(v));
-                    tP = fma2(tA, pair(g.x, g.y), tP);
-                    tA = tA * low_pair(v);
-                }
                 for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tP));
                 if ((rank & 1) == 0) push(&x, &x.before[lane], rank + 1, quad(tA, tH));
                 if (!given_up) given_up = !exchange_wait(&x, (round >> 1) & 1);
@@ -560,28 +575,17 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(const __grid_
                 }
                 if (rank & 1) h = fma2(low_pair(x.before[lane]), h, high_pair(x.before[lane]));
                 if (given_up) h = q = p0 = pair(NAN);
+            } else {
+                p0 = fma2(tA, p0, tP);
             }
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 v = duo(h);
-                begin[w][lane].x = v.x;
-                begin[w][lane].y = v.y;
-                h = fma2(low_pair(part[w][lane]), h, high_pair(part[w][lane]));
-            }
-#pragma unroll
-            for (int w = kWarps - 1; w >= 0; --w) {
-                const float2 v = duo(q), g = grad[w][lane];
-                begin[w][lane].z = v.x;
-                begin[w][lane].w = v.y;
-                q = fma2(low_pair(part[w][lane]), q, pair(g.x, g.y));
-            }
-            if (ranks == 1) p0 = q;
+            begin[lane] = quad(h, q);
         }
         __syncthreads();
-        const float4 start = begin[warp][lane];
+        h = fma2(A, low_pair(begin[lane]), H);
+        Pair q = fma2(B, high_pair(begin[lane]), P);
         const Writer<T, kBytes> dz(p.dz, col, ts), dx(p.dx, col, ts);
         const auto finish = [&](auto masked) {
-            Pair h = low_pair(start), q = high_pair(start), before[kSteps];
+            Pair before[kSteps];
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
                 const Pair x = inputs(masked, 1, k);
@@ -607,8 +611,8 @@ __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(const __grid_
         if (at_hand.all) finish(std::false_type());
         else finish(std::true_type());
     }
-    if (rank == 0 && warp == 0) store_state(p.dh0, p, col, p0);
-    if (ranks > 1) cluster_sync();  // no CTA ends while another may write to it
+    if (rank == 0 && warp == kWarps - 1) store_state(p.dh0, p, col, p0);
+    if (ranks > 1) cluster_meet();  // no CTA ends while another may write to it
 }
 
 // Launches a kernel of clusters, behind the kernel ahead of it as launch_after does.
@@ -618,8 +622,9 @@ cudaError_t launch_ranks(bool rows16, int shared, const RecArgs& p, cudaStream_t
     static bool set[64] = {};  // the kernel's shared memory, once per device
 
     uint32_t ranks = 1;
-    while (ranks < (uint32_t)kRanks && (int64_t)ranks * kSpan < p.steps) ranks *= 2;
     const int64_t tiles = rows16 ? p.batch * p.blocks : (p.batch * p.channels + kCols - 1) / kCols;
+    // a CTA more in a cluster is worth its exchange where the GPU is not full without it
+    while (ranks < (uint32_t)kRanks && (int64_t)ranks * kSpan < p.steps && tiles * ranks < 1024) ranks *= 2;
     if (tiles > 0x7fffffff / (int64_t)ranks) return cudaErrorInvalidConfiguration;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
