@@ -1,5 +1,6 @@
 // Layer norm, forward and backward with the gradients of the weight and the bias:
 // kernels and C entry points (adacomp.h).
+#include <initializer_list>
 #include <new>
 
 #include "train_common.cuh"
@@ -13,8 +14,12 @@ struct adacomp_layer_norm {
 namespace adacomp {
 namespace {
 
-constexpr int kLnThreads = 256;
-constexpr int kLnWarps = kLnThreads / 32;
+constexpr int kLnThreads = 256;   // forward pass, and rows that are too wide for registers
+constexpr int kLnBack = 512;      // backward pass
+constexpr int kLnParts = 304;     // CTAs of a backward pass at most, each with partial sums of dw and db
+constexpr int kLnBackCols = 16;   // columns of a thread there
+constexpr int64_t kLnBackDim = (int64_t)kLnBack * kLnBackCols;
+constexpr int kLnWideSlices = 128;
 
 struct LnArgs {
     const void *x, *dy, *w, *b;
@@ -24,69 +29,424 @@ struct LnArgs {
     float* part;                 // [slices][2][dim] partial sums of dw and db
     int64_t rows, dim, x_stride, y_stride, dy_stride, dx_stride;
     int32_t slices;
+    int32_t group;               // threads of a row
     float eps;
 };
 
-// One warp per row, three passes over it (the second and third from L1 or L2).
-template <typename X, typename W>
+// N consecutive elements as they lie in memory: 16, 4 or 2 bytes, as the rows' alignment allows.
+template <int kBytes> struct RawOf;
+template <> struct RawOf<16> {
+    using type = uint4;
+};
+template <> struct RawOf<4> {
+    using type = uint32_t;
+};
+template <> struct RawOf<2> {
+    using type = uint16_t;
+};
+
+template <typename X, int N> struct Piece {
+    static constexpr int kBytes = N * (int)sizeof(X);
+    using Raw = typename RawOf<kBytes>::type;
+    Raw q;
+    __device__ __forceinline__ void load(const X* p) { q = *reinterpret_cast<const Raw*>(p); }
+    __device__ __forceinline__ void zero() { q = Raw{}; }
+    __device__ __forceinline__ float get(int j) const
+    {
+        if constexpr (kBytes == 16) {
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            if constexpr (sizeof(X) == 4) return __uint_as_float(w[j]);
+            else return j & 1 ? bf16_high(w[j / 2]) : bf16_low(w[j / 2]);
+        } else if constexpr (sizeof(X) == 4) {
+            return __uint_as_float(q);
+        } else {
+            return j & 1 ? bf16_high(q) : bf16_low(q);
+        }
+    }
+};
+
+template <int N> __device__ __forceinline__ void put_piece(float* p, const float (&v)[N])
+{
+    if constexpr (N == 1) *p = v[0];
+    else *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+template <int N> __device__ __forceinline__ void put_piece(bf16* p, const float (&v)[N])
+{
+    if constexpr (N == 1) {
+        *p = from_f32<bf16>(v[0]);
+    } else if constexpr (N == 2) {
+        *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v[0], v[1]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// N weights from p on (4 or 8 of them: from a 16-byte boundary).
+template <int N> __device__ __forceinline__ void weights(const float* p, float (&v)[N])
+{
+    if constexpr (N < 4) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = p[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(p + j);
+            v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
+        }
+    }
+}
+
+template <int N> __device__ __forceinline__ void weights(const bf16* p, float (&v)[N])
+{
+    if constexpr (N < 4) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = to_f32(p[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const uint2 q = *reinterpret_cast<const uint2*>(p + j);
+            v[j] = bf16_low(q.x), v[j + 1] = bf16_high(q.x), v[j + 2] = bf16_low(q.y), v[j + 3] = bf16_high(q.y);
+        }
+    }
+}
+
+// The sum over the lanes of a group of up to 32 (a power of two).
+__device__ __forceinline__ float group_sum(float v, int group)
+{
+    for (int o = group >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// ---------------------------------------------------------------- forward
+// Bound by memory. A row is read once, to registers, as it lies in memory (N elements at a
+// time, kCols per thread at most); the mean and then the sum of squared deviations are
+// formed from there. A row is a group of 1 to 32 lanes, so that there is no barrier, or,
+// where it is wider than 32 * 64 elements, a CTA. The weights come from L1 or L2 for every row.
+template <typename X, typename W, int N, int kCols, bool kWide>
 __global__ void __launch_bounds__(kLnThreads) ln_forward_kernel(const LnArgs a)
 {
+    constexpr int kPieces = kCols / N;
+    __shared__ float shared[2][kLnThreads / 32];
     ptx::griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kLnWarps + (threadIdx.x >> 5);
-    if (row >= a.rows) return;
-    const X* x = static_cast<const X*>(a.x) + row * a.x_stride;
-    X* y = static_cast<X*>(a.y) + row * a.y_stride;
+    const int group = kWide ? kLnThreads : a.group;
+    const int place = threadIdx.x & (group - 1);
+    const int64_t row = kWide ? blockIdx.x : (int64_t)blockIdx.x * (kLnThreads / group) + threadIdx.x / group;
+    const bool on = row < a.rows;
+    const X* x = static_cast<const X*>(a.x) + (on ? row : 0) * a.x_stride;
+    const int dim = (int)a.dim;
+    const auto sum = [&](float v, int turn) {
+        v = group_sum(v, kWide ? 32 : group);
+        if (kWide) {
+            if ((threadIdx.x & 31) == 0) shared[turn][threadIdx.x >> 5] = v;
+            __syncthreads();
+            v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kLnThreads / 32; ++i) v += shared[turn][i];
+        }
+        return v;
+    };
+    Piece<X, N> r[kPieces];
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        const int c = (k * group + place) * N;
+        r[k].zero();
+        if (on && c < dim) r[k].load(x + c);
+    }
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+        for (int j = 0; j < N; ++j) s += r[k].get(j);
+    const float mean = sum(s, 0) / (float)dim;
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+        if ((k * group + place) * N < dim) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float d = r[k].get(j) - mean;
+                s = fmaf(d, d, s);
+            }
+        }
+    const float rstd = 1.0f / sqrtf(sum(s, 1) / (float)dim + a.eps);
+    if (!on) return;
     const W* w = static_cast<const W*>(a.w);
     const W* b = static_cast<const W*>(a.b);
-    const float n = (float)a.dim;
-    float s = 0.0f;
-    for (int64_t i = lane; i < a.dim; i += 32) s += to_f32(x[i]);
-    const float mean = warp_sum(s) / n;
-    s = 0.0f;
-    for (int64_t i = lane; i < a.dim; i += 32) {
-        const float d = to_f32(x[i]) - mean;
-        s += d * d;
+    X* y = static_cast<X*>(a.y) + row * a.y_stride;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        const int c = (k * group + place) * N;
+        if (c < dim) {
+            float wv[N], bv[N] = {}, v[N];
+            weights<N>(w + c, wv);
+            if (b) weights<N>(b + c, bv);
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = fmaf((r[k].get(j) - mean) * rstd, wv[j], bv[j]);
+            put_piece<N>(y + c, v);
+        }
     }
-    const float rstd = 1.0f / sqrtf(warp_sum(s) / n + a.eps);
-    for (int64_t i = lane; i < a.dim; i += 32)
-        y[i] = from_f32<X>((to_f32(x[i]) - mean) * rstd * to_f32(w[i]) + (b ? to_f32(b[i]) : 0.0f));
-    if (lane == 0) {
+    if (place == 0) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
     }
 }
 
-template <typename X, typename W>
-__global__ void __launch_bounds__(kLnThreads) ln_backward_kernel(const LnArgs a)
+// Rows too wide for registers: a CTA per row, three passes over it (the second and third
+// from L2).
+template <typename X, typename W> __global__ void __launch_bounds__(kLnThreads) ln_forward_long_kernel(const LnArgs a)
 {
+    __shared__ float shared[2][kLnThreads / 32];
     ptx::griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kLnWarps + (threadIdx.x >> 5);
-    if (row >= a.rows) return;
+    const int64_t row = blockIdx.x;
     const X* x = static_cast<const X*>(a.x) + row * a.x_stride;
-    const X* dy = static_cast<const X*>(a.dy) + row * a.dy_stride;
-    X* dx = static_cast<X*>(a.dx) + row * a.dx_stride;
+    X* y = static_cast<X*>(a.y) + row * a.y_stride;
     const W* w = static_cast<const W*>(a.w);
-    const float mean = a.mean_in[row], rstd = a.rstd_in[row], n = (float)a.dim;
-    float s0 = 0.0f, s1 = 0.0f;
-    for (int64_t i = lane; i < a.dim; i += 32) {
-        const float g = to_f32(dy[i]) * to_f32(w[i]);
-        s0 += g;
-        s1 += g * (to_f32(x[i]) - mean) * rstd;
+    const W* b = static_cast<const W*>(a.b);
+    const auto sum = [&](float v, int turn) {
+        v = warp_sum(v);
+        if ((threadIdx.x & 31) == 0) shared[turn][threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.0f;
+        for (int i = 0; i < kLnThreads / 32; ++i) v += shared[turn][i];
+        return v;
+    };
+    float s = 0.0f;
+    for (int64_t i = threadIdx.x; i < a.dim; i += kLnThreads) s += to_f32(x[i]);
+    const float mean = sum(s, 0) / (float)a.dim;
+    s = 0.0f;
+    for (int64_t i = threadIdx.x; i < a.dim; i += kLnThreads) {
+        const float d = to_f32(x[i]) - mean;
+        s = fmaf(d, d, s);
     }
-    s0 = warp_sum(s0) / n;
-    s1 = warp_sum(s1) / n;
-    for (int64_t i = lane; i < a.dim; i += 32) {
-        const float g = to_f32(dy[i]) * to_f32(w[i]);
-        dx[i] = from_f32<X>(rstd * (g - s0 - (to_f32(x[i]) - mean) * rstd * s1));
+    const float rstd = 1.0f / sqrtf(sum(s, 1) / (float)a.dim + a.eps);
+    for (int64_t i = threadIdx.x; i < a.dim; i += kLnThreads)
+        y[i] = from_f32<X>(fmaf((to_f32(x[i]) - mean) * rstd, to_f32(w[i]), b ? to_f32(b[i]) : 0.0f));
+    if (threadIdx.x == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
     }
 }
 
-// Column sums: a slice of the rows per blockIdx.y, one column per thread. Runs before
-// dx is written, which may be in place of dy or x.
-template <typename X>
-__global__ void __launch_bounds__(kLnThreads) ln_columns_kernel(const LnArgs a)
+// ---------------------------------------------------------------- backward
+// Bound by memory: dy and x are read once and dx written. A group of threads (1 to 512, a
+// power of two) has a row, 16 columns per thread at most, and goes from row to row, so that
+// the weights, and the sums for dw and db over its rows, stay in its registers. The rows to
+// come are copied to shared memory four ahead (every thread its own pieces: no barrier);
+// pieces of single elements are loaded one row ahead. The two sums of a row need one
+// barrier of the group where it is more than a warp. At the end the CTA's groups add their
+// column sums in order, and a second kernel adds the CTAs'.
+__device__ __forceinline__ void group_barrier(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// How many rows a thread has on their way, and the shared memory for them.
+template <typename X, int N> struct LnRing {
+    static constexpr int kRow = (kLnBackCols / N) * 2 * kLnBack * Piece<X, N>::kBytes;
+    static constexpr int kStages = sizeof(X) == 2 ? 6 : 3;
+    static constexpr int kSums = 2 * (int)kLnBackDim * 4;
+    static constexpr int kShared = Piece<X, N>::kBytes >= 4 && kStages * kRow > kSums ? kStages * kRow : kSums;
+};
+
+template <int kBytes> __device__ __forceinline__ void copy_piece(void* to, const void* from)
+{
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(from) : "memory");
+}
+
+template <typename X, typename W, int N>
+__global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
+{
+    constexpr int kPieces = kLnBackCols / N;
+    constexpr int kBytes = Piece<X, N>::kBytes, kStages = LnRing<X, N>::kStages;
+    constexpr bool kRing = kBytes >= 4;
+    using Raw = typename Piece<X, N>::Raw;
+    extern __shared__ __align__(16) uint8_t shared_bytes[];
+    __shared__ float2 sums[2][kLnBack / 32];
+    ptx::griddep_wait();
+    const int group = a.group, place = threadIdx.x & (group - 1), dim = (int)a.dim;
+    const int groups = kLnBack / group, which = threadIdx.x / group;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float inv_n = 1.0f / (float)dim;
+    const X* x = static_cast<const X*>(a.x);
+    const X* dy = static_cast<const X*>(a.dy);
+    X* dx = static_cast<X*>(a.dx);
+    float w[kLnBackCols], dw[kLnBackCols], db[kLnBackCols];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        const int c = (k * group + place) * N;
+        float v[N] = {};
+        if (c < dim) weights<N>(static_cast<const W*>(a.w) + c, v);
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[k * N + j] = v[j], dw[k * N + j] = db[k * N + j] = 0.0f;
+    }
+    // the ring: [stage][piece][x, dy][thread]
+    const auto slot = [&](int stage, int k, int tensor) {
+        return reinterpret_cast<Raw*>(shared_bytes) + ((stage * kPieces + k) * 2 + tensor) * kLnBack + threadIdx.x;
+    };
+    const int64_t stride = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + which;
+    const auto stage_row = [&](int64_t r, int stage) {
+        if constexpr (kRing) {
+            if (r < a.rows) {
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k) {
+                    const int c = (k * group + place) * N;
+                    if (c < dim) {
+                        copy_piece<kBytes>(slot(stage, k, 0), x + r * a.x_stride + c);
+                        copy_piece<kBytes>(slot(stage, k, 1), dy + r * a.dy_stride + c);
+                    }
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+    Piece<X, N> px[kPieces], pd[kPieces];
+    float mean = 0.0f, rstd = 0.0f;
+    if (row < a.rows) mean = a.mean_in[row], rstd = a.rstd_in[row];
+    if (kRing) {
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) stage_row(row + i * stride, i);
+    }
+    // every lane of a warp takes part as long as the warp's first group has a row
+    const int64_t lead = (int64_t)blockIdx.x * groups + (group < 32 ? warp * (32 / group) : which);
+    int stage = 0, turn = 0;
+    for (int64_t at = lead; at < a.rows; at += stride, row += stride) {
+        const bool on = row < a.rows;
+        float mean_next = 0.0f, rstd_next = 0.0f;
+        if (row + stride < a.rows) mean_next = a.mean_in[row + stride], rstd_next = a.rstd_in[row + stride];
+        if (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const int c = (k * group + place) * N;
+            px[k].zero();
+            pd[k].zero();
+            if (on && c < dim) {
+                if constexpr (kRing) {
+                    px[k].q = *slot(stage, k, 0);
+                    pd[k].q = *slot(stage, k, 1);
+                } else {
+                    px[k].load(x + row * a.x_stride + c);
+                    pd[k].load(dy + row * a.dy_stride + c);
+                }
+            }
+        }
+        if (kRing) {
+            stage_row(row + kStages * stride, stage);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+        }
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float g = pd[k].get(j), h = (px[k].get(j) - mean) * rstd;
+                db[k * N + j] += g;
+                dw[k * N + j] = fmaf(g, h, dw[k * N + j]);
+                s0 = fmaf(g, w[k * N + j], s0);
+                s1 = fmaf(g * w[k * N + j], h, s1);
+            }
+        const int within = group < 32 ? group : 32;
+        s0 = group_sum(s0, within);
+        s1 = group_sum(s1, within);
+        if (group > 32) {
+            if (lane == 0) sums[turn][warp] = make_float2(s0, s1);
+            group_barrier(1 + which, group);
+            const int first = which * (group >> 5);
+            s0 = s1 = 0.0f;
+            for (int i = 0; i < group >> 5; ++i) {
+                s0 += sums[turn][first + i].x;
+                s1 += sums[turn][first + i].y;
+            }
+            turn ^= 1;
+        }
+        s0 *= inv_n;
+        s1 *= inv_n;
+        if (on) {
+            X* const to = dx + row * a.dx_stride;
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const int c = (k * group + place) * N;
+                if (c < dim) {
+                    float v[N];
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        const float h = (px[k].get(j) - mean) * rstd;
+                        v[j] = rstd * (fmaf(pd[k].get(j), w[k * N + j], -s0) - h * s1);
+                    }
+                    put_piece<N>(to + c, v);
+                }
+            }
+        }
+        mean = mean_next;
+        rstd = rstd_next;
+    }
+    if (kRing) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the ring is free: it takes the CTA's column sums, [2][dim]
+    float* const total = reinterpret_cast<float*>(shared_bytes);
+    if (group < 32) {  // the warp's groups first
+#pragma unroll
+        for (int i = 0; i < kLnBackCols; ++i)
+            for (int o = group; o < 32; o <<= 1) {
+                dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
+                db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
+            }
+    }
+    const int owners = group < 32 ? kLnBack / 32 : groups, mine = group < 32 ? warp : which;
+    for (int g = 0; g < owners; ++g) {
+        if (g == mine && (group >= 32 || lane < group)) {
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const int c = (k * group + place) * N;
+                if (c < dim)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        total[c + j] = (g ? total[c + j] : 0.0f) + dw[k * N + j];
+                        total[dim + c + j] = (g ? total[dim + c + j] : 0.0f) + db[k * N + j];
+                    }
+            }
+        }
+        __syncthreads();
+    }
+    float* const part = a.part + (int64_t)blockIdx.x * 2 * dim;
+    for (int i = threadIdx.x; i < 2 * dim; i += kLnBack) part[i] = total[i];
+}
+
+// Adds the partial sums: 32 columns per CTA, eight rows of threads that each add every
+// eighth partial sum.
+template <typename W> __global__ void __launch_bounds__(kLnThreads) ln_join_kernel(const LnArgs a)
+{
+    __shared__ float shared[kLnThreads / 32][33];
+    ptx::griddep_wait();
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * 32 + lane, n = 2 * a.dim;
+    float s = 0.0f;
+    if (i < n)
+#pragma unroll 4
+        for (int p = row; p < a.slices; p += kLnThreads / 32) s += a.part[p * n + i];
+    shared[row][lane] = s;
+    __syncthreads();
+    if (row != 0 || i >= n) return;
+    s = 0.0f;
+#pragma unroll
+    for (int p = 0; p < kLnThreads / 32; ++p) s += shared[p][lane];
+    if (i < a.dim) static_cast<W*>(a.dw)[i] = from_f32<W>(s);
+    else if (a.db) static_cast<W*>(a.db)[i - a.dim] = from_f32<W>(s);
+}
+
+// Rows too wide for the registers of a CTA: the column sums by one thread per column and
+// slice of the rows (before dx is written, which may be in place of dy or x), then dx by a
+// CTA per row, in two passes.
+template <typename X> __global__ void __launch_bounds__(kLnThreads) ln_columns_kernel(const LnArgs a)
 {
     ptx::griddep_wait();
     const int64_t c = (int64_t)blockIdx.x * kLnThreads + threadIdx.x;
@@ -97,45 +457,147 @@ __global__ void __launch_bounds__(kLnThreads) ln_columns_kernel(const LnArgs a)
     for (int64_t r = blockIdx.y; r < a.rows; r += a.slices) {
         const float g = to_f32(dy[r * a.dy_stride + c]);
         db += g;
-        dw += g * (to_f32(x[r * a.x_stride + c]) - a.mean_in[r]) * a.rstd_in[r];
+        dw = fmaf(g, (to_f32(x[r * a.x_stride + c]) - a.mean_in[r]) * a.rstd_in[r], dw);
     }
     float* p = a.part + (int64_t)blockIdx.y * 2 * a.dim;
     p[c] = dw;
     p[a.dim + c] = db;
 }
 
-template <typename W>
-__global__ void __launch_bounds__(kLnThreads) ln_join_kernel(const LnArgs a)
+template <typename X, typename W> __global__ void __launch_bounds__(kLnThreads) ln_backward_long_kernel(const LnArgs a)
 {
+    __shared__ float2 shared[kLnThreads / 32];
     ptx::griddep_wait();
-    const int64_t c = (int64_t)blockIdx.x * kLnThreads + threadIdx.x;
-    if (c >= a.dim) return;
-    float dw = 0.0f, db = 0.0f;
-    for (int s = 0; s < a.slices; ++s) {
-        dw += a.part[(int64_t)s * 2 * a.dim + c];
-        db += a.part[(int64_t)s * 2 * a.dim + a.dim + c];
+    const int64_t row = blockIdx.x;
+    const X* x = static_cast<const X*>(a.x) + row * a.x_stride;
+    const X* dy = static_cast<const X*>(a.dy) + row * a.dy_stride;
+    X* dx = static_cast<X*>(a.dx) + row * a.dx_stride;
+    const W* w = static_cast<const W*>(a.w);
+    const float mean = a.mean_in[row], rstd = a.rstd_in[row];
+    float s0 = 0.0f, s1 = 0.0f;
+    for (int64_t i = threadIdx.x; i < a.dim; i += kLnThreads) {
+        const float g = to_f32(dy[i]) * to_f32(w[i]);
+        s0 += g;
+        s1 = fmaf(g, (to_f32(x[i]) - mean) * rstd, s1);
     }
-    static_cast<W*>(a.dw)[c] = from_f32<W>(dw);
-    if (a.db) static_cast<W*>(a.db)[c] = from_f32<W>(db);
+    s0 = warp_sum(s0);
+    s1 = warp_sum(s1);
+    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = make_float2(s0, s1);
+    __syncthreads();
+    s0 = s1 = 0.0f;
+    for (int i = 0; i < kLnThreads / 32; ++i) {
+        s0 += shared[i].x;
+        s1 += shared[i].y;
+    }
+    s0 /= (float)a.dim;
+    s1 /= (float)a.dim;
+    for (int64_t i = threadIdx.x; i < a.dim; i += kLnThreads) {
+        const float h = (to_f32(x[i]) - mean) * rstd;
+        dx[i] = from_f32<X>(rstd * (fmaf(to_f32(dy[i]), to_f32(w[i]), -s0) - h * s1));
+    }
 }
 
-int ln_slices(int64_t rows) { return (int)(rows < 1 ? 1 : rows < 128 ? rows : 128); }
+// ---------------------------------------------------------------- launches
+// How many elements of the rows can be read and written at a time: 16 bytes of them, 4 or one.
+int piece_of(const LnArgs& a, int ex, std::initializer_list<const void*> p, std::initializer_list<int64_t> strides,
+             std::initializer_list<const void*> weights)
+{
+    int64_t bits = a.dim * ex;
+    for (const void* q : p) bits |= (int64_t)reinterpret_cast<uintptr_t>(q);
+    if (a.rows > 1)
+        for (int64_t s : strides) bits |= s * ex;
+    bool whole = bits % 16 == 0;
+    for (const void* q : weights) whole = whole && is_aligned(q, 16);
+    return whole ? 16 / ex : bits % 4 == 0 ? 4 / ex : 1;
+}
+
+int group_of(int64_t places, int most)  // the smallest power of two with room for them
+{
+    int g = 1;
+    while (g < most && g < places) g *= 2;
+    return g;
+}
+
+template <typename X, typename W, int N> cudaError_t ln_forward_n(LnArgs a, cudaStream_t stream)
+{
+    constexpr bool kVector = Piece<X, N>::kBytes == 16;
+    const dim3 one((unsigned)a.rows), threads(kLnThreads);
+    if (a.dim > 64 * kLnThreads) return launch_after(ln_forward_long_kernel<X, W>, one, threads, 0, stream, a);
+    if (a.dim > 16 * kLnThreads) return launch_after(ln_forward_kernel<X, W, N, 64, true>, one, threads, 0, stream, a);
+    // a lane's 64 columns in small pieces are too many instructions and registers: a CTA per row
+    if (a.dim > (kVector ? 64 : 16) * 32)
+        return launch_after(ln_forward_kernel<X, W, N, 16, true>, one, threads, 0, stream, a);
+    a.group = group_of((a.dim + N - 1) / N, 32);
+    const dim3 grid((unsigned)((a.rows * a.group + kLnThreads - 1) / kLnThreads));
+    if constexpr (kVector)
+        if (a.dim > 16 * 32) return launch_after(ln_forward_kernel<X, W, N, 64, false>, grid, threads, 0, stream, a);
+    return launch_after(ln_forward_kernel<X, W, N, 16, false>, grid, threads, 0, stream, a);
+}
 
 template <typename X, typename W> cudaError_t ln_forward(const LnArgs& a, cudaStream_t stream)
 {
-    return launch_after(ln_forward_kernel<X, W>, dim3((unsigned)((a.rows + kLnWarps - 1) / kLnWarps)), dim3(kLnThreads),
-                        0, stream, a);
+    const int n = piece_of(a, (int)sizeof(X), {a.x, a.y}, {a.x_stride, a.y_stride}, {a.w, a.b});
+    if (n == 16 / (int)sizeof(X)) return ln_forward_n<X, W, 16 / sizeof(X)>(a, stream);
+    if constexpr (sizeof(X) == 2)
+        if (n == 2) return ln_forward_n<X, W, 2>(a, stream);
+    return ln_forward_n<X, W, 1>(a, stream);
 }
 
-template <typename X, typename W> cudaError_t ln_backward(const LnArgs& a, cudaStream_t stream)
+// The threads of a row, and the CTAs, of a backward pass.
+int back_group(int64_t dim, int n)
 {
+    const int64_t places = (dim + n - 1) / n;
+    if (places <= 16) return group_of(places, 16);
+    return 32 * group_of((dim + 32 * kLnBackCols - 1) / (32 * kLnBackCols), kLnBack / 32);
+}
+
+int ln_slices(int64_t rows, int64_t dim)
+{
+    const int64_t most = dim > kLnBackDim ? kLnWideSlices : kLnParts;
+    return (int)(rows < 1 ? 1 : rows < most ? rows : most);
+}
+
+template <typename X, typename W, int N> cudaError_t ln_backward_n(LnArgs a, cudaStream_t stream)
+{
+    static bool set[64] = {};
+    constexpr int shared = LnRing<X, N>::kShared;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = sm_count(&sms);
+    if (e == cudaSuccess && !set[dev]) {
+        e = cudaFuncSetAttribute(ln_backward_kernel<X, W, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+        set[dev] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess) return e;
+    a.group = back_group(a.dim, N);
+    const int64_t per = kLnBack / a.group, need = (a.rows + per - 1) / per;
+    const int64_t most = sms < kLnParts ? sms : kLnParts;
+    a.slices = (int)(need < most ? need : most);
+    e = launch_after(ln_backward_kernel<X, W, N>, dim3((unsigned)a.slices), dim3(kLnBack), shared, stream, a);
+    if (e != cudaSuccess) return e;
+    return launch_after(ln_join_kernel<W>, dim3((unsigned)((2 * a.dim + 31) / 32)), dim3(kLnThreads), 0, stream, a);
+}
+
+template <typename X, typename W> cudaError_t ln_backward(LnArgs a, cudaStream_t stream)
+{
+    if (a.rows == 0) {
+        a.slices = 0;
+        return launch_after(ln_join_kernel<W>, dim3((unsigned)((2 * a.dim + 31) / 32)), dim3(kLnThreads), 0, stream, a);
+    }
+    if (a.dim <= kLnBackDim) {
+        const int n = piece_of(a, (int)sizeof(X), {a.x, a.dy, a.dx}, {a.x_stride, a.dy_stride, a.dx_stride}, {a.w});
+        if (n == 16 / (int)sizeof(X)) return ln_backward_n<X, W, 16 / sizeof(X)>(a, stream);
+        if constexpr (sizeof(X) == 2)
+            if (n == 2) return ln_backward_n<X, W, 2>(a, stream);
+        return ln_backward_n<X, W, 1>(a, stream);
+    }
+    a.slices = ln_slices(a.rows, a.dim);
     const unsigned cols = (unsigned)((a.dim + kLnThreads - 1) / kLnThreads);
     cudaError_t e = launch_after(ln_columns_kernel<X>, dim3(cols, (unsigned)a.slices), dim3(kLnThreads), 0, stream, a);
     if (e != cudaSuccess) return e;
-    e = launch_after(ln_join_kernel<W>, dim3(cols), dim3(kLnThreads), 0, stream, a);
-    if (e != cudaSuccess || a.rows == 0) return e;
-    return launch_after(ln_backward_kernel<X, W>, dim3((unsigned)((a.rows + kLnWarps - 1) / kLnWarps)),
-                        dim3(kLnThreads), 0, stream, a);
+    e = launch_after(ln_join_kernel<W>, dim3((unsigned)((2 * a.dim + 31) / 32)), dim3(kLnThreads), 0, stream, a);
+    if (e != cudaSuccess) return e;
+    return launch_after(ln_backward_long_kernel<X, W>, dim3((unsigned)a.rows), dim3(kLnThreads), 0, stream, a);
 }
 
 }  // namespace
@@ -150,7 +612,7 @@ adacomp_status adacomp_layer_norm_init(adacomp_layer_norm_t* out, int64_t dim, a
 {
     if (!out) return ADACOMP_ERR_INVALID_ARG;
     *out = nullptr;
-    if (dim < 1 || dim > (int64_t)1 << 31 || !adacomp::known_dtype(x_dtype) || !adacomp::known_dtype(w_dtype) ||
+    if (dim < 1 || dim > (int64_t)1 << 30 || !adacomp::known_dtype(x_dtype) || !adacomp::known_dtype(w_dtype) ||
         !(eps >= 0.0f) || !std::isfinite(eps))
         return ADACOMP_ERR_INVALID_ARG;
     adacomp_layer_norm* h = new (std::nothrow) adacomp_layer_norm;
@@ -197,7 +659,7 @@ adacomp_status adacomp_layer_norm_forward(adacomp_layer_norm_t h, int64_t rows, 
 size_t adacomp_layer_norm_backward_ws_bytes(adacomp_layer_norm_t h, int64_t rows)
 {
     if (!h || rows < 0) return 0;
-    return (size_t)adacomp::ln_slices(rows) * 2 * (size_t)h->dim * 4;
+    return (size_t)adacomp::ln_slices(rows, h->dim) * 2 * (size_t)h->dim * 4;
 }
 
 adacomp_status adacomp_layer_norm_backward(adacomp_layer_norm_t h, int64_t rows, const void* dy, int64_t dy_stride,
@@ -230,7 +692,6 @@ adacomp_status adacomp_layer_norm_backward(adacomp_layer_norm_t h, int64_t rows,
     a.x_stride = x_stride;
     a.dy_stride = dy_stride;
     a.dx_stride = dx_stride;
-    a.slices = adacomp::ln_slices(rows);
     const bool xb = h->x_dtype == ADACOMP_BF16, wb = h->w_dtype == ADACOMP_BF16;
     using adacomp::bf16;
     const cudaError_t e = xb ? (wb ? adacomp::ln_backward<bf16, bf16>(a, stream) : adacomp::ln_backward<bf16, float>(a, stream))
