@@ -65,6 +65,12 @@ template <typename X, int N> struct Piece {
     }
 };
 
+// The elements of a thread's pieces, two at a time, across the pieces where they are single.
+template <typename X, int N, int kPieces> __device__ __forceinline__ Pair pair_of(const Piece<X, N> (&p)[kPieces], int i)
+{
+    return pair(p[2 * i / N].get(2 * i % N), p[(2 * i + 1) / N].get((2 * i + 1) % N));
+}
+
 template <int N> __device__ __forceinline__ void put_piece(float* p, const float (&v)[N])
 {
     if constexpr (N == 1) *p = v[0];
@@ -130,7 +136,7 @@ __device__ __forceinline__ float group_sum(float v, int group)
 // formed from there. A row is a group of 1 to 32 lanes, so that there is no barrier, or,
 // where it is wider than 32 * 64 elements, a CTA. The weights come from L1 or L2 for every row.
 template <typename X, typename W, int N, int kCols, bool kWide>
-__global__ void __launch_bounds__(kLnThreads) ln_forward_kernel(const LnArgs a)
+__global__ void __launch_bounds__(kLnThreads, kCols == 64 && N > 2 ? 3 : 1) ln_forward_kernel(const LnArgs a)
 {
     constexpr int kPieces = kCols / N;
     __shared__ float shared[2][kLnThreads / 32];
@@ -153,29 +159,33 @@ __global__ void __launch_bounds__(kLnThreads) ln_forward_kernel(const LnArgs a)
         return v;
     };
     Piece<X, N> r[kPieces];
-    float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
         const int c = (k * group + place) * N;
         r[k].zero();
         if (on && c < dim) r[k].load(x + c);
     }
+    Pair s[2] = {pair(0.0f), pair(0.0f)};
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k)
-#pragma unroll
-        for (int j = 0; j < N; ++j) s += r[k].get(j);
-    const float mean = sum(s, 0) / (float)dim;
-    s = 0.0f;
+    for (int i = 0; i < kCols / 2; ++i) s[i & 1] = s[i & 1] + pair_of(r, i);
+    const float mean = sum(both(s[0] + s[1]), 0) / (float)dim;
+    const Pair minus = pair(-mean);
+    s[0] = s[1] = pair(0.0f);
 #pragma unroll
     for (int k = 0; k < kPieces; ++k)
         if ((k * group + place) * N < dim) {
+            if constexpr (N > 1) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float d = r[k].get(j) - mean;
-                s = fmaf(d, d, s);
+                for (int i = k * N / 2; i < (k + 1) * N / 2; ++i) {
+                    const Pair d = pair_of(r, i) + minus;
+                    s[i & 1] = fma2(d, d, s[i & 1]);
+                }
+            } else {
+                const float d = r[k].get(0) - mean;
+                s[0] = fma2(pair(d, 0.0f), pair(d, 0.0f), s[0]);
             }
         }
-    const float rstd = 1.0f / sqrtf(sum(s, 1) / (float)dim + a.eps);
+    const float rstd = 1.0f / sqrtf(sum(both(s[0] + s[1]), 1) / (float)dim + a.eps);
     if (!on) return;
     const W* w = static_cast<const W*>(a.w);
     const W* b = static_cast<const W*>(a.b);
@@ -187,8 +197,15 @@ __global__ void __launch_bounds__(kLnThreads) ln_forward_kernel(const LnArgs a)
             float wv[N], bv[N] = {}, v[N];
             weights<N>(w + c, wv);
             if (b) weights<N>(b + c, bv);
+            if constexpr (N > 1) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) v[j] = fmaf((r[k].get(j) - mean) * rstd, wv[j], bv[j]);
+                for (int j = 0; j < N; j += 2) {
+                    const Pair d = (pair_of(r, (k * N + j) / 2) + minus) * pair(rstd);
+                    split(fma2(d, pair(wv[j], wv[j + 1]), pair(bv[j], bv[j + 1])), v[j], v[j + 1]);
+                }
+            } else {
+                v[0] = fmaf((r[k].get(0) - mean) * rstd, wv[0], bv[0]);
+            }
             put_piece<N>(y + c, v);
         }
     }
@@ -280,14 +297,20 @@ __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
     const X* x = static_cast<const X*>(a.x);
     const X* dy = static_cast<const X*>(a.dy);
     X* dx = static_cast<X*>(a.dx);
-    float w[kLnBackCols], dw[kLnBackCols], db[kLnBackCols];
+    constexpr int kPairs = kLnBackCols / 2;
+    Pair w[kPairs], dw[kPairs], db[kPairs];
+    {
+        float v[kLnBackCols] = {};
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-        const int c = (k * group + place) * N;
-        float v[N] = {};
-        if (c < dim) weights<N>(static_cast<const W*>(a.w) + c, v);
+        for (int k = 0; k < kPieces; ++k) {
+            const int c = (k * group + place) * N;
+            if (c < dim) weights<N>(static_cast<const W*>(a.w) + c, *reinterpret_cast<float(*)[N]>(v + k * N));
+        }
 #pragma unroll
-        for (int j = 0; j < N; ++j) w[k * N + j] = v[j], dw[k * N + j] = db[k * N + j] = 0.0f;
+        for (int i = 0; i < kPairs; ++i) {
+            w[i] = pair(v[2 * i], v[2 * i + 1]);
+            dw[i] = db[i] = pair(0.0f);
+        }
     }
     // the ring: [stage][piece][x, dy][thread]
     const auto slot = [&](int stage, int k, int tensor) {
@@ -344,17 +367,19 @@ __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
             stage_row(row + kStages * stride, stage);
             stage = stage + 1 == kStages ? 0 : stage + 1;
         }
-        float s0 = 0.0f, s1 = 0.0f;
+        // with d = x - mean: xh = rstd * d, and the sum of g * xh is rstd times that of g * d
+        Pair d[kPairs], g[kPairs], t0 = pair(0.0f), t1 = pair(0.0f);
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k)
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float g = pd[k].get(j), h = (px[k].get(j) - mean) * rstd;
-                db[k * N + j] += g;
-                dw[k * N + j] = fmaf(g, h, dw[k * N + j]);
-                s0 = fmaf(g, w[k * N + j], s0);
-                s1 = fmaf(g * w[k * N + j], h, s1);
-            }
+        for (int i = 0; i < kPairs; ++i) {
+            const Pair v = pair_of(pd, i);
+            d[i] = pair_of(px, i) + pair(-mean);
+            g[i] = v * w[i];
+            db[i] = db[i] + v;
+            dw[i] = fma2(v * pair(rstd), d[i], dw[i]);
+            t0 = t0 + g[i];
+            t1 = fma2(g[i], d[i], t1);
+        }
+        float s0 = both(t0), s1 = both(t1) * rstd;
         const int within = group < 32 ? group : 32;
         s0 = group_sum(s0, within);
         s1 = group_sum(s1, within);
@@ -369,22 +394,18 @@ __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
             }
             turn ^= 1;
         }
-        s0 *= inv_n;
-        s1 *= inv_n;
         if (on) {
+            // dx = rstd * (g - s0 / n - xh * s1 / n)
+            const Pair scale = pair(rstd), k0 = pair(-(s0 * inv_n) * rstd), k1 = pair(-(s1 * inv_n) * rstd * rstd);
+            float v[kLnBackCols];
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i)
+                split(fma2(g[i], scale, fma2(d[i], k1, k0)), v[2 * i], v[2 * i + 1]);
             X* const to = dx + row * a.dx_stride;
 #pragma unroll
             for (int k = 0; k < kPieces; ++k) {
                 const int c = (k * group + place) * N;
-                if (c < dim) {
-                    float v[N];
-#pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        const float h = (px[k].get(j) - mean) * rstd;
-                        v[j] = rstd * (fmaf(pd[k].get(j), w[k * N + j], -s0) - h * s1);
-                    }
-                    put_piece<N>(to + c, v);
-                }
+                if (c < dim) put_piece<N>(to + c, *reinterpret_cast<const float(*)[N]>(v + k * N));
             }
         }
         mean = mean_next;
@@ -393,25 +414,31 @@ __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
     if (kRing) asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // the ring is free: it takes the CTA's column sums, [2][dim]
     float* const total = reinterpret_cast<float*>(shared_bytes);
+    float sw[kLnBackCols], sb[kLnBackCols];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        split(dw[i], sw[2 * i], sw[2 * i + 1]);
+        split(db[i], sb[2 * i], sb[2 * i + 1]);
+    }
     if (group < 32) {  // the warp's groups first
 #pragma unroll
         for (int i = 0; i < kLnBackCols; ++i)
             for (int o = group; o < 32; o <<= 1) {
-                dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
-                db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
+                sw[i] += __shfl_xor_sync(0xffffffffu, sw[i], o);
+                sb[i] += __shfl_xor_sync(0xffffffffu, sb[i], o);
             }
     }
     const int owners = group < 32 ? kLnBack / 32 : groups, mine = group < 32 ? warp : which;
-    for (int g = 0; g < owners; ++g) {
-        if (g == mine && (group >= 32 || lane < group)) {
+    for (int o = 0; o < owners; ++o) {
+        if (o == mine && (group >= 32 || lane < group)) {
 #pragma unroll
             for (int k = 0; k < kPieces; ++k) {
                 const int c = (k * group + place) * N;
                 if (c < dim)
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
-                        total[c + j] = (g ? total[c + j] : 0.0f) + dw[k * N + j];
-                        total[dim + c + j] = (g ? total[dim + c + j] : 0.0f) + db[k * N + j];
+                        total[c + j] = (o ? total[c + j] : 0.0f) + sw[k * N + j];
+                        total[dim + c + j] = (o ? total[dim + c + j] : 0.0f) + sb[k * N + j];
                     }
             }
         }
@@ -421,26 +448,26 @@ __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
     for (int i = threadIdx.x; i < 2 * dim; i += kLnBack) part[i] = total[i];
 }
 
-// Adds the partial sums: 32 columns per CTA, eight rows of threads that each add every
-// eighth partial sum.
-template <typename W> __global__ void __launch_bounds__(kLnThreads) ln_join_kernel(const LnArgs a)
+// Adds the partial sums: 32 columns per CTA, 32 rows of threads that each add every 32nd.
+constexpr int kLnJoin = 1024;
+
+template <typename W> __global__ void __launch_bounds__(kLnJoin) ln_join_kernel(const LnArgs a)
 {
-    __shared__ float shared[kLnThreads / 32][33];
+    __shared__ float shared[kLnJoin / 32][33];
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int64_t i = (int64_t)blockIdx.x * 32 + lane, n = 2 * a.dim;
     float s = 0.0f;
     if (i < n)
-#pragma unroll 4
-        for (int p = row; p < a.slices; p += kLnThreads / 32) s += a.part[p * n + i];
+#pragma unroll 5
+        for (int p = row; p < a.slices; p += kLnJoin / 32) s += a.part[p * n + i];
     shared[row][lane] = s;
     __syncthreads();
-    if (row != 0 || i >= n) return;
-    s = 0.0f;
-#pragma unroll
-    for (int p = 0; p < kLnThreads / 32; ++p) s += shared[p][lane];
-    if (i < a.dim) static_cast<W*>(a.dw)[i] = from_f32<W>(s);
-    else if (a.db) static_cast<W*>(a.db)[i - a.dim] = from_f32<W>(s);
+    s = warp_sum(shared[lane][row]);  // column `row` of the CTA's
+    const int64_t c = (int64_t)blockIdx.x * 32 + row;
+    if (lane != 0 || c >= n) return;
+    if (c < a.dim) static_cast<W*>(a.dw)[c] = from_f32<W>(s);
+    else if (a.db) static_cast<W*>(a.db)[c - a.dim] = from_f32<W>(s);
 }
 
 // Rows too wide for the registers of a CTA: the column sums by one thread per column and
@@ -575,14 +602,14 @@ template <typename X, typename W, int N> cudaError_t ln_backward_n(LnArgs a, cud
     a.slices = (int)(need < most ? need : most);
     e = launch_after(ln_backward_kernel<X, W, N>, dim3((unsigned)a.slices), dim3(kLnBack), shared, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_after(ln_join_kernel<W>, dim3((unsigned)((2 * a.dim + 31) / 32)), dim3(kLnThreads), 0, stream, a);
+    return launch_after(ln_join_kernel<W>, dim3((unsigned)((2 * a.dim + 31) / 32)), dim3(kLnJoin), 0, stream, a);
 }
 
 template <typename X, typename W> cudaError_t ln_backward(LnArgs a, cudaStream_t stream)
 {
     if (a.rows == 0) {
         a.slices = 0;
-        return launch_after(ln_join_kernel<W>, dim3((unsigned)((2 * a.dim + 31) / 32)), dim3(kLnThreads), 0, stream, a);
+        return launch_after(ln_join_kernel<W>, dim3((unsigned)((2 * a.dim + 31) / 32)), dim3(kLnJoin), 0, stream, a);
     }
     if (a.dim <= kLnBackDim) {
         const int n = piece_of(a, (int)sizeof(X), {a.x, a.dy, a.dx}, {a.x_stride, a.dy_stride, a.dx_stride}, {a.w});
@@ -595,7 +622,7 @@ template <typename X, typename W> cudaError_t ln_backward(LnArgs a, cudaStream_t
     const unsigned cols = (unsigned)((a.dim + kLnThreads - 1) / kLnThreads);
     cudaError_t e = launch_after(ln_columns_kernel<X>, dim3(cols, (unsigned)a.slices), dim3(kLnThreads), 0, stream, a);
     if (e != cudaSuccess) return e;
-    e = launch_after(ln_join_kernel<W>, dim3((unsigned)((2 * a.dim + 31) / 32)), dim3(kLnThreads), 0, stream, a);
+    e = launch_after(ln_join_kernel<W>, dim3((unsigned)((2 * a.dim + 31) / 32)), dim3(kLnJoin), 0, stream, a);
     if (e != cudaSuccess) return e;
     return launch_after(ln_backward_long_kernel<X, W>, dim3((unsigned)a.rows), dim3(kLnThreads), 0, stream, a);
 }

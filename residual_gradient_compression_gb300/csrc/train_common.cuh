@@ -87,6 +87,13 @@ __device__ __forceinline__ void split(Pair p, float& x, float& y)
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.b));
 }
 
+__device__ __forceinline__ float both(Pair p)  // the sum of the two
+{
+    float x, y;
+    split(p, x, y);
+    return x + y;
+}
+
 __device__ __forceinline__ Pair operator*(Pair x, Pair y)
 {
     Pair p;
@@ -100,6 +107,8 @@ __device__ __forceinline__ Pair fma2(Pair x, Pair y, Pair z)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.b) : "l"(x.b), "l"(y.b), "l"(z.b));
     return p;
 }
+
+__device__ __forceinline__ Pair operator+(Pair x, Pair y) { return fma2(x, pair(1.0f), y); }  // x + y, in any company
 
 }  // namespace
 }  // namespace adacomp
