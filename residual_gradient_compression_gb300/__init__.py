@@ -114,8 +114,15 @@ def _check(status: int, where: str):
         raise AdacompError(status, where)
 
 
+# torch's current stream without the Stream object that torch.cuda.current_stream() makes (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_device())
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -357,28 +364,29 @@ def _array(t, count: int, dtype, what: str):
     """The address of a contiguous CUDA tensor of `count` elements; None stays None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != count or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != count or not t.is_cuda or not t.is_contiguous():
         _bad(f"{what} must be a contiguous CUDA tensor of {count} {dtype} elements")
     return t.data_ptr()
 
 
 def _matrix(t, h, what: str):
     """(address, rows, row stride) of a tensor whose last axis is a row of h.dim elements."""
-    if t.dtype != h.torch_dtype or not t.is_cuda or t.dim() < 1 or t.shape[-1] != h.dim:
-        _bad(f"{what} must be a CUDA tensor of {h.torch_dtype} with rows of {h.dim}")
-    if t.dim() == 2:
-        rows, stride = t.shape[0], t.stride(0)
-        if h.dim > 1 and t.stride(1) != 1:
+    shape, dim = t.shape, h.dim
+    if t.dtype is not h.torch_dtype or not t.is_cuda or not shape or shape[-1] != dim:
+        _bad(f"{what} must be a CUDA tensor of {h.torch_dtype} with rows of {dim}")
+    if len(shape) == 2:
+        stride, one = t.stride()
+        if one != 1 and dim > 1:
             _bad(f"{what}: the elements of a row must be contiguous")
-        return t.data_ptr(), rows, stride
+        return t.data_ptr(), shape[0], stride
     if not t.is_contiguous():
         _bad(f"{what}: a tensor that is not a matrix must be contiguous")
-    return t.data_ptr(), t.numel() // h.dim, h.dim
+    return t.data_ptr(), t.numel() // dim, dim
 
 
 def _sequence(t, h, shape, what: str):
     """(address, batch stride, step stride) of a [batch, steps, channels] tensor."""
-    if t.dtype != h.torch_dtype or not t.is_cuda or t.shape != shape:
+    if t.dtype is not h.torch_dtype or not t.is_cuda or t.shape != shape:
         _bad(f"{what} must be a CUDA tensor of {h.torch_dtype} and shape {tuple(shape)}")
     batch, step, one = t.stride()
     if one != 1 and shape[2] > 1:

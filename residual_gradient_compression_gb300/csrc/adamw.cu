@@ -1,6 +1,6 @@
 // The norm of many gradients and an AdamW step over many tensors, with the moments in
 // 32 or in 8 bits: kernels and C entry points (adacomp.h).
-#include <cstring>
+#include <memory>
 #include <new>
 #include <type_traits>
 #include <vector>
@@ -17,8 +17,10 @@ constexpr int kAwWarps = kAwThreads / 32;
 constexpr int kAwBlock = ADACOMP_ADAMW_BLOCK;      // elements per scale, and per warp and turn
 constexpr int kAwTile = kAwWarps * kAwBlock;       // elements per CTA
 constexpr int kAwTensors = 400;                    // tensors per launch (a by-value kernel parameter)
+constexpr int kAwFew = 16;                         // and of its short form: 32 KB of parameters cost a launch 4 us
 constexpr int kNormTensors = 1200;
-constexpr int kJumps = 1024;                       // see owner_of
+constexpr int kNormFew = 64;
+constexpr int kJumps = 1024, kJumpsFew = 64;       // see owner_of
 constexpr int kNormGrid = 912;                     // CTAs per launch at most (six per SM), each with a partial sum
 constexpr int kNormVectors = 4;                    // 16-byte vectors per thread and tile
 
@@ -36,22 +38,28 @@ struct AwTensor {
     float decay;  // 1 - lr * weight_decay
 };
 
-struct Jumps {
+template <int N> struct Jumps {
+    static constexpr int kCount = N;
     int32_t shift;
-    uint16_t id[kJumps];  // the tensor of tile k << shift
+    uint16_t id[N];  // the tensor of tile k << shift
 };
 
-struct AwTable {
-    AwTensor t[kAwTensors];
-    Jumps jump;
+struct AwHead {
     int32_t count;
     uint32_t tiles;  // of this launch
     uint32_t ahead;  // tiles from a CTA's own to the one that it has brought into L2 (8-bit states)
-    int32_t fast;  // eps and root lie where the step's own root and quotient are exact (adam_lane)
+    int32_t fast;    // eps and root lie where the step's own root and quotient are exact (adam_lane)
     Adam k;          // its c and decay are filled in by the kernel
     const float* coefficient;
 };
-static_assert(sizeof(AwTable) <= 32764, "kernel parameters");
+
+template <int N, int J> struct AwTable : AwHead {
+    AwTensor t[N];
+    Jumps<J> jump;
+};
+using AwLong = AwTable<kAwTensors, kJumps>;
+using AwShort = AwTable<kAwFew, kJumpsFew>;
+static_assert(sizeof(AwLong) <= 32764, "kernel parameters");
 
 struct NormTensor {
     const void* g;
@@ -59,9 +67,7 @@ struct NormTensor {
     uint32_t tile_begin;
 };
 
-struct NormTable {
-    NormTensor t[kNormTensors];
-    Jumps jump;
+struct NormHead {
     int32_t count;
     uint32_t tiles;        // of this launch
     uint32_t first_part;   // where its partial sums start
@@ -71,7 +77,14 @@ struct NormTable {
     uint32_t* ticket;
     double* part;
 };
-static_assert(sizeof(NormTable) <= 32764, "kernel parameters");
+
+template <int N, int J> struct NormTable : NormHead {
+    NormTensor t[N];
+    Jumps<J> jump;
+};
+using NormLong = NormTable<kNormTensors, kJumps>;
+using NormShort = NormTable<kNormFew, kJumpsFew>;
+static_assert(sizeof(NormLong) <= 32764, "kernel parameters");
 
 // The last tensor whose first tile is at or before `tile`: from the first tile's of its
 // stretch of 2^shift tiles on (a search by halves over hundreds of tensors is nine
@@ -86,7 +99,7 @@ template <typename Table> __device__ __forceinline__ int owner_of(const Table& t
 template <typename Table> void fill_jumps(Table* tab)
 {
     int shift = 0, id = 0;
-    while ((tab->tiles - 1) >> shift >= (uint32_t)kJumps) ++shift;
+    while ((tab->tiles - 1) >> shift >= (uint32_t)decltype(tab->jump)::kCount) ++shift;
     tab->jump.shift = shift;
     for (uint32_t k = 0; k <= (tab->tiles - 1) >> shift; ++k) {
         while (id + 1 < tab->count && tab->t[id + 1].tile_begin <= k << shift) ++id;
@@ -185,16 +198,19 @@ template <> struct Four<uint8_t> {
 template <bool kWhole, typename T> __device__ __forceinline__ Four<T> load4(const void* base, int64_t i, int64_t n)
 {
     const T* p = static_cast<const T*>(base);
-    if (kWhole || i + 4 <= n) return *reinterpret_cast<const Four<T>*>(p + i);
     Four<T> r = {};
+    if (kWhole || i + 4 <= n) {
+        r = *reinterpret_cast<const Four<T>*>(p + i);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (i + j < n) {
-            if constexpr (sizeof(T) == 4) (&r.q.x)[j] = reinterpret_cast<const uint32_t*>(p)[i + j];
-            else if constexpr (sizeof(T) == 2)
-                (&r.q.x)[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i + j] << (16 * (j & 1));
-            else r.q |= (uint32_t)p[i + j] << (8 * j);
-        }
+        for (int j = 0; j < 4; ++j)
+            if (i + j < n) {
+                if constexpr (sizeof(T) == 4) (&r.q.x)[j] = reinterpret_cast<const uint32_t*>(p)[i + j];
+                else if constexpr (sizeof(T) == 2)
+                    (&r.q.x)[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i + j] << (16 * (j & 1));
+                else r.q |= (uint32_t)p[i + j] << (8 * j);
+            }
+    }
     return r;
 }
 
@@ -214,11 +230,11 @@ template <bool kWhole> __device__ __forceinline__ void store4(float* p, int64_t 
 {
     if (kWhole || i + 4 <= n) {
         *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (i + j < n) p[i + j] = v[j];
+        for (int j = 0; j < 4; ++j)
+            if (i + j < n) p[i + j] = v[j];
+    }
 }
 
 template <bool kWhole> __device__ __forceinline__ void store4(bf16* p, int64_t i, int64_t n, const float* v)
@@ -227,22 +243,22 @@ template <bool kWhole> __device__ __forceinline__ void store4(bf16* p, int64_t i
         const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
         *reinterpret_cast<uint2*>(p + i) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (i + j < n) p[i + j] = from_f32<bf16>(v[j]);
+        for (int j = 0; j < 4; ++j)
+            if (i + j < n) p[i + j] = from_f32<bf16>(v[j]);
+    }
 }
 
 template <bool kWhole> __device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, uint32_t v)
 {
     if (kWhole || i + 4 <= n) {
         *reinterpret_cast<uint32_t*>(p + i) = v;
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (i + j < n) p[i + j] = (uint8_t)(v >> (8 * j));
+        for (int j = 0; j < 4; ++j)
+            if (i + j < n) p[i + j] = (uint8_t)(v >> (8 * j));
+    }
 }
 
 constexpr int kAwEach = kAwBlock / 32;  // elements of a lane
@@ -419,7 +435,7 @@ template <typename Table> struct Cursor {
 };
 
 // Fills in what a kernel knows of the constants; false if the step is to be left out.
-__device__ __forceinline__ bool step_constants(const AwTable& tab, Adam* a)
+__device__ __forceinline__ bool step_constants(const AwHead& tab, Adam* a)
 {
     *a = tab.k;
     if (tab.coefficient) a->c = *tab.coefficient;
@@ -445,8 +461,8 @@ __device__ __forceinline__ void prefetch(const void* p, int64_t bytes)
 // Loading the next block ahead into registers (3.6) or shared memory (3.5) cost more warps
 // than it gained. bf16 weights and gradients with 8-bit states (10 bytes per element) are
 // bound by instructions: 134M elements 0.243 ms, 5.6 TB/s.
-template <typename W, typename G, bool kEight>
-__global__ void __launch_bounds__(kAwThreads, kEight ? 5 : 4) adamw_kernel(const __grid_constant__ AwTable tab)
+template <typename Table, typename W, typename G, bool kEight>
+__global__ void __launch_bounds__(kAwThreads, kEight ? 5 : 4) adamw_kernel(const __grid_constant__ Table tab)
 {
     using S = typename Part<W, G, kEight>::S;
     ptx::griddep_wait();
@@ -538,8 +554,8 @@ template <typename G> __device__ __forceinline__ int values_of(uint32_t word, fl
 // fp32 sum overflows, or is so small that squares may have vanished, is summed again in
 // fp64. A CTA leaves one fp64 partial sum; the last CTA of the call adds the partial sums in
 // their order.
-template <typename G>
-__global__ void __launch_bounds__(kAwThreads, 6) grad_norm_kernel(const __grid_constant__ NormTable tab)
+template <typename Table, typename G>
+__global__ void __launch_bounds__(kAwThreads, 6) grad_norm_kernel(const __grid_constant__ Table tab)
 {
     constexpr int kPer = 16 / (int)sizeof(G);
     ptx::griddep_wait();
@@ -548,7 +564,7 @@ __global__ void __launch_bounds__(kAwThreads, 6) grad_norm_kernel(const __grid_c
     double sum = 0.0;
     uint32_t tile = (uint32_t)((uint64_t)tab.tiles * blockIdx.x / gridDim.x);
     const uint32_t end = (uint32_t)((uint64_t)tab.tiles * (blockIdx.x + 1) / gridDim.x);
-    Cursor<NormTable> at(tab, tile);
+    Cursor<Table> at(tab, tile);
     for (; tile < end; ++tile) {
         at.to(tab, tile);
         const NormTensor& t = tab.t[at.id];
@@ -651,14 +667,81 @@ template <typename T, typename F> adacomp_status for_runs(const std::vector<int3
     return ADACOMP_OK;
 }
 
-template <typename W, typename G> cudaError_t step_launch(AwTable* tab, bool eight, cudaStream_t stream)
+// The pointers of a step, as the caller gave them.
+struct StepPointers {
+    void* const* weight;
+    const void* const* grad;
+    void *const *m, *const *v;
+    float *const *m_scale, *const *v_scale;
+    void* const* copy;
+    float lr;
+};
+
+template <typename Table, typename W, typename G>
+cudaError_t step_launch(const Table& tab, bool eight, cudaStream_t stream)
 {
-    int sms = 0;
-    const cudaError_t e = sm_count(&sms);
-    if (e != cudaSuccess) return e;
-    tab->ahead = (uint32_t)(4 * sms);
-    return launch_after(eight ? adamw_kernel<W, G, true> : adamw_kernel<W, G, false>, dim3(tab->tiles),
-                        dim3(kAwThreads), 0, stream, *tab);
+    return launch_after(eight ? adamw_kernel<Table, W, G, true> : adamw_kernel<Table, W, G, false>, dim3(tab.tiles),
+                        dim3(kAwThreads), 0, stream, tab);
+}
+
+// One launch: tensors list[i .. j) of weight and gradient type `kind`.
+template <typename Table>
+adacomp_status step_run(const adacomp_adamw* h, const AwHead& head, const StepPointers& p,
+                        const std::vector<int32_t>& list, size_t i, size_t j, int kind, cudaStream_t stream)
+{
+    const std::unique_ptr<Table> tab(new (std::nothrow) Table);
+    if (!tab) return ADACOMP_ERR_INVALID_ARG;
+    static_cast<AwHead&>(*tab) = head;
+    const bool eight = h->state_bits == 8;
+    uint32_t tile = 0;
+    for (size_t q = i; q < j; ++q) {
+        const size_t id = (size_t)list[q];
+        AwTensor& t = tab->t[q - i];
+        t.w = p.weight[id];
+        t.g = p.grad[id];
+        t.m = p.m[id];
+        t.v = p.v[id];
+        t.ms = eight ? p.m_scale[id] : nullptr;
+        t.vs = eight ? p.v_scale[id] : nullptr;
+        t.copy = p.copy ? p.copy[id] : nullptr;
+        t.n = h->n[id];
+        t.tile_begin = tile;
+        t.decay = (float)(1.0 - (double)p.lr * (double)h->weight_decay[id]);
+        tile += step_tiles(t.n);
+    }
+    tab->count = (int32_t)(j - i);
+    tab->tiles = tile;
+    fill_jumps(tab.get());
+    const cudaError_t e = kind == 0   ? step_launch<Table, float, float>(*tab, eight, stream)
+                          : kind == 1 ? step_launch<Table, float, bf16>(*tab, eight, stream)
+                          : kind == 2 ? step_launch<Table, bf16, float>(*tab, eight, stream)
+                                      : step_launch<Table, bf16, bf16>(*tab, eight, stream);
+    return launch_result(e, stream);
+}
+
+// The same of the norm; *parts is where its partial sums start, and is moved past them.
+template <typename Table>
+adacomp_status norm_run(const adacomp_adamw* h, const NormHead& head, const void* const* grad,
+                        const std::vector<int32_t>& list, size_t i, size_t j, bool is_bf16, uint32_t* parts,
+                        cudaStream_t stream)
+{
+    const std::unique_ptr<Table> tab(new (std::nothrow) Table);
+    if (!tab) return ADACOMP_ERR_INVALID_ARG;
+    static_cast<NormHead&>(*tab) = head;
+    uint32_t tile = 0;
+    for (size_t q = i; q < j; ++q) {
+        const size_t id = (size_t)list[q];
+        tab->t[q - i] = {grad[id], h->n[id], tile};
+        tile += norm_tiles(h->n[id], is_bf16);
+    }
+    const uint32_t grid = tile < (uint32_t)kNormGrid ? tile : (uint32_t)kNormGrid;
+    tab->count = (int32_t)(j - i);
+    tab->tiles = tile;
+    tab->first_part = *parts;
+    *parts += grid;
+    fill_jumps(tab.get());
+    return launch_result(launch_after(is_bf16 ? grad_norm_kernel<Table, bf16> : grad_norm_kernel<Table, float>,
+                                      dim3(grid), dim3(kAwThreads), 0, stream, *tab), stream);
 }
 
 }  // namespace
@@ -718,36 +801,24 @@ adacomp_status adacomp_grad_norm(adacomp_adamw_t h, const void* const* grad, flo
         if (!grad[i]) return ADACOMP_ERR_INVALID_ARG;
         if (!is_aligned(grad[i], 16)) return ADACOMP_ERR_ALIGNMENT;
     }
-    NormTable* tab = new (std::nothrow) NormTable;
-    if (!tab) return ADACOMP_ERR_INVALID_ARG;
-    tab->all_parts = h->norm_parts;
-    tab->scale = grad_scale;
-    tab->max_norm = max_norm;
-    tab->result = result;
-    tab->ticket = static_cast<uint32_t*>(ws);
-    tab->part = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + 16);
+    NormHead head = {};
+    head.all_parts = h->norm_parts;
+    head.scale = grad_scale;
+    head.max_norm = max_norm;
+    head.result = result;
+    head.ticket = static_cast<uint32_t*>(ws);
+    head.part = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + 16);
     uint32_t parts = 0;
     adacomp_status st = ADACOMP_OK;
     for (int k = 0; k < 2 && st == ADACOMP_OK; ++k) {
-        const auto tiles_of = [&](size_t id) { return norm_tiles(h->n[id], k); };
-        st = for_runs(h->by_g[k], kNormTensors, tiles_of, [&](size_t i, size_t j, uint32_t tiles) {
-            uint32_t tile = 0;
-            for (size_t q = i; q < j; ++q) {
-                const size_t id = (size_t)h->by_g[k][q];
-                tab->t[q - i] = {grad[id], h->n[id], tile};
-                tile += tiles_of(id);
-            }
-            const uint32_t grid = tiles < (uint32_t)kNormGrid ? tiles : (uint32_t)kNormGrid;
-            tab->count = (int32_t)(j - i);
-            tab->tiles = tiles;
-            tab->first_part = parts;
-            fill_jumps(tab);
-            parts += grid;
-            return launch_result(launch_after(k ? grad_norm_kernel<bf16> : grad_norm_kernel<float>, dim3(grid),
-                                              dim3(kAwThreads), 0, stream, *tab), stream);
-        });
+        const std::vector<int32_t>& list = h->by_g[k];
+        st = for_runs(list, kNormTensors, [&](size_t id) { return norm_tiles(h->n[id], k); },
+                      [&](size_t i, size_t j, uint32_t) {
+                          return j - i <= (size_t)kNormFew
+                                     ? norm_run<NormShort>(h, head, grad, list, i, j, k, &parts, stream)
+                                     : norm_run<NormLong>(h, head, grad, list, i, j, k, &parts, stream);
+                      });
     }
-    delete tab;
     return st;
 }
 
@@ -772,59 +843,34 @@ adacomp_status adacomp_adamw_step(adacomp_adamw_t h, void* const* weight, const 
             (eight && (!is_aligned(m_scale[i], 4) || !is_aligned(v_scale[i], 4))) || (copy && !is_aligned(copy[i], 16)))
             return ADACOMP_ERR_ALIGNMENT;
     }
-    AwTable* tab = new (std::nothrow) AwTable;
-    if (!tab) return ADACOMP_ERR_INVALID_ARG;
-    const auto twice = [](float x) {
-        uint32_t b;
-        std::memcpy(&b, &x, 4);
-        return Pair{((unsigned long long)b << 32) | b};
-    };
-    const float root = (float)(1.0 / std::sqrt((double)bias_correction2));
-    tab->k.c = grad_scale;
-    tab->k.beta1 = beta1;
-    tab->k.beta2 = beta2;
-    tab->k.rest1 = 1.0f - beta1;
-    tab->k.rest2 = 1.0f - beta2;
-    tab->k.step = (float)((double)lr / (double)bias_correction1);
-    tab->k.root = root;
-    tab->k.eps = eps;
-    tab->k.one = 1.0f;
-    tab->k.half = 0.5f;
-    tab->k.minus = -1.0f;
-    tab->k.decay = 1.0f;
+    AwHead head = {};
+    head.k.c = grad_scale;
+    head.k.beta1 = beta1;
+    head.k.beta2 = beta2;
+    head.k.rest1 = 1.0f - beta1;
+    head.k.rest2 = 1.0f - beta2;
+    head.k.step = (float)((double)lr / (double)bias_correction1);
+    head.k.root = (float)(1.0 / std::sqrt((double)bias_correction2));
+    head.k.eps = eps;
+    head.k.one = 1.0f;
+    head.k.half = 0.5f;
+    head.k.minus = -1.0f;
     // u <= 2^30 in adam_lane's range, so that u * root + eps lies within 2^+-40
-    tab->fast = eps >= 0x1p-40f && eps <= 0x1p30f && root <= 0x1p9f;
-    tab->coefficient = coefficient;
+    head.fast = eps >= 0x1p-40f && eps <= 0x1p30f && head.k.root <= 0x1p9f;
+    head.coefficient = coefficient;
+    int sms = 0;
+    if (sm_count(&sms) != cudaSuccess) return ADACOMP_ERR_CUDA;
+    head.ahead = (uint32_t)(4 * sms);
+    const StepPointers p = {weight, grad, m, v, m_scale, v_scale, copy, lr};
     adacomp_status st = ADACOMP_OK;
-    const auto tiles_of = [&](size_t id) { return step_tiles(h->n[id]); };
-    for (int k = 0; k < 4 && st == ADACOMP_OK; ++k)
-        st = for_runs(h->by_wg[k], kAwTensors, tiles_of, [&](size_t i, size_t j, uint32_t tiles) {
-            uint32_t tile = 0;
-            for (size_t q = i; q < j; ++q) {
-                const size_t id = (size_t)h->by_wg[k][q];
-                AwTensor& t = tab->t[q - i];
-                t.w = weight[id];
-                t.g = grad[id];
-                t.m = m[id];
-                t.v = v[id];
-                t.ms = eight ? m_scale[id] : nullptr;
-                t.vs = eight ? v_scale[id] : nullptr;
-                t.copy = copy ? copy[id] : nullptr;
-                t.n = h->n[id];
-                t.tile_begin = tile;
-                t.decay = (float)(1.0 - (double)lr * (double)h->weight_decay[id]);
-                tile += tiles_of(id);
-            }
-            tab->count = (int32_t)(j - i);
-            tab->tiles = tiles;
-            fill_jumps(tab);
-            const cudaError_t e = k == 0   ? step_launch<float, float>(tab, eight, stream)
-                                  : k == 1 ? step_launch<float, bf16>(tab, eight, stream)
-                                  : k == 2 ? step_launch<bf16, float>(tab, eight, stream)
-                                           : step_launch<bf16, bf16>(tab, eight, stream);
-            return launch_result(e, stream);
-        });
-    delete tab;
+    for (int k = 0; k < 4 && st == ADACOMP_OK; ++k) {
+        const std::vector<int32_t>& list = h->by_wg[k];
+        st = for_runs(list, kAwTensors, [&](size_t id) { return step_tiles(h->n[id]); },
+                      [&](size_t i, size_t j, uint32_t) {
+                          return j - i <= (size_t)kAwFew ? step_run<AwShort>(h, head, p, list, i, j, k, stream)
+                                                         : step_run<AwLong>(h, head, p, list, i, j, k, stream);
+                      });
+    }
     return st;
 }
 
