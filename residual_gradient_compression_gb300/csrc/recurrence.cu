@@ -95,7 +95,7 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) { return {fmaf(a.x, b.x
 
 // ---------------------------------------------------------------- many steps
 // The steps are split: a warp has 64 columns (two per lane) and eight consecutive steps, a
-// CTA 64 steps, a cluster of up to eight CTAs up to 512, and where the sequence is longer the
+// CTA 64 steps, a cluster of up to 16 CTAs up to 1024, and where the sequence is longer the
 // cluster goes on in rounds. Each warp forms what its steps do to a state, h -> A h + H with
 // A the product of its gates. The warps exchange these through shared memory, and the CTAs
 // write theirs into every CTA of the cluster (one warp of each does); then each warp knows
@@ -103,7 +103,6 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) { return {fmaf(a.x, b.x
 // is read once, and no CTA waits for one that may not be running. The next round's elements
 // are copied to shared memory meanwhile.
 constexpr int kCols = 64, kSteps = 8, kWarps = 8, kThreads = 32 * kWarps, kSpan = kSteps * kWarps;
-constexpr int kRanks = 8;
 constexpr int kTile = kSpan * kCols;  // elements of a tensor that a CTA has in a round
 static_assert(kRecChunk == 2 * kSpan, "a kept state every second CTA");
 
@@ -136,27 +135,31 @@ __device__ __forceinline__ float4 quad(Two a, Two b) { return make_float4(a.x, a
 // barrier that counts their bytes. Two of them take turns: a CTA that writes for the round
 // after next has all others' values of the next one, so that they have read these.
 // (A barrier of the whole cluster would have to wait for each round's stores of results.)
-struct Exchange {
+template <int kRanks> struct Exchange {
     float4 value[kRanks][32];
     float4 before[32];  // backward: the (A, H) of the CTA before, where the chunk is its
     unsigned long long barrier;
 };
 
-__device__ __forceinline__ void exchange_init(Exchange* x)
+// CTAs of a cluster at most. Sixteen halve the rounds of few and long sequences; but for rows
+// of bf16 by 16 bytes the exchange's memory would cost an SM one of its CTAs.
+template <typename T, int kBytes> constexpr int kRanks = sizeof(T) == 2 && kBytes == 16 ? 16 : 8;
+
+template <int R> __device__ __forceinline__ void exchange_init(Exchange<R>* x)
 {
     if (threadIdx.x < 2)
         asm volatile("mbarrier.init.shared.b64 [%0], 1;" ::"r"(shared_address(&x[threadIdx.x].barrier)) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
-__device__ __forceinline__ void exchange_expect(Exchange* x, uint32_t bytes)
+template <int R> __device__ __forceinline__ void exchange_expect(Exchange<R>* x, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(shared_address(&x->barrier)), "r"(bytes)
                  : "memory");
 }
 
 // Writes v to the place of `p` in the CTA `rank`, and counts it at that CTA's barrier.
-__device__ __forceinline__ void push(Exchange* x, float4* p, uint32_t rank, float4 v)
+template <int R> __device__ __forceinline__ void push(Exchange<R>* x, float4* p, uint32_t rank, float4 v)
 {
     uint32_t a, b;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(shared_address(p)), "r"(rank));
@@ -168,7 +171,7 @@ __device__ __forceinline__ void push(Exchange* x, float4* p, uint32_t rank, floa
 
 // Waits for a barrier's phase. The CTAs of a cluster run together and each writes before it
 // waits, so the wait ends; were it not to, it is given up after some seconds.
-__device__ __forceinline__ bool exchange_wait(Exchange* x, uint32_t phase)
+template <int R> __device__ __forceinline__ bool exchange_wait(Exchange<R>* x, uint32_t phase)
 {
     for (uint32_t i = 0; i < (1u << 22); ++i) {
         uint32_t done;
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
     extern __shared__ __align__(16) uint8_t shared_bytes[];
     __shared__ float4 part[kWarps][32];   // a warp's (A, H) of the lane's columns
     __shared__ Two begin[kWarps][32];  // the state before its first step
-    __shared__ Exchange exchange[2];
+    __shared__ Exchange<kRanks<T, kBytes>> exchange[2];
     const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (2 * kTile); };
     ptx::griddep_wait();
     if (ranks > 1) {
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
         if (warp == 0) {
             Two h = h0;  // before the CTA's first step
             if (ranks > 1) {
-                Exchange& x = exchange[par];
+                Exchange<kRanks<T, kBytes>>& x = exchange[par];
                 if (lane == 0) exchange_expect(&x, ranks * 512);
                 Two tA = two_of(1.0f), tH = two_of(0.0f);
 #pragma unroll
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_ke
     __shared__ float4 part[kWarps][32];  // a warp's (A, H)
     __shared__ Two grad[kWarps][32];  // its P
     __shared__ float4 begin[32];         // the state before the CTA's first step, and p after its last
-    __shared__ Exchange exchange[2];
+    __shared__ Exchange<kRanks<T, kBytes>> exchange[2];
     const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (3 * kTile); };
     ptx::griddep_wait();
     if (ranks > 1) {
@@ -554,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_ke
             for (int w = kWarps - 1; w >= 0; --w)
                 tP = fma2(low(part[w][lane]), tP, grad[w][lane]);
             if (ranks > 1) {
-                Exchange& x = exchange[par];
+                Exchange<kRanks<T, kBytes>>& x = exchange[par];
                 if (lane == 0) exchange_expect(&x, ranks * 512 + (rank & 1) * 512);
                 for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tP));
                 if ((rank & 1) == 0) push(&x, &x.before[lane], rank + 1, quad(tA, tH));
@@ -607,21 +610,25 @@ __global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_ke
 }
 
 // Launches a kernel of clusters, behind the kernel ahead of it as launch_after does.
-template <void (*kern)(RecArgs, uint32_t)>
+template <int kRanks, void (*kern)(RecArgs, uint32_t)>
 cudaError_t launch_ranks(bool rows16, int shared, const RecArgs& p, cudaStream_t stream)
 {
     static bool set[64] = {};  // the kernel's shared memory, once per device
 
     uint32_t ranks = 1;
     const int64_t tiles = rows16 ? p.batch * p.blocks : (p.batch * p.channels + kCols - 1) / kCols;
-    // a CTA more in a cluster is worth its exchange where the GPU is not full without it
-    while (ranks < (uint32_t)kRanks && (int64_t)ranks * kSpan < p.steps && tiles * ranks < 1024) ranks *= 2;
+    // a CTA more in a cluster is worth its exchange where the GPU is not full without it; more
+    // than eight where all clusters still run at once
+    const uint32_t most = tiles <= 19 ? (uint32_t)kRanks : 8;
+    while (ranks < most && (int64_t)ranks * kSpan < p.steps && tiles * ranks < 1024) ranks *= 2;
     if (tiles > 0x7fffffff / (int64_t)ranks) return cudaErrorInvalidConfiguration;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
     if (e == cudaSuccess && !set[dev]) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+        if (e == cudaSuccess && kRanks > 8)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         set[dev] = e == cudaSuccess;
     }
     if (e != cudaSuccess) return e;
@@ -663,20 +670,20 @@ template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
                             dim3(kRecThreads), 0, stream, p);
     }
     const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.y}), shared = 4 * kSpan * kCols * (int)sizeof(T);
-    if (by == 16) return launch_ranks<rec_forward_kernel<T, 16>>(true, shared, p, stream);
+    if (by == 16) return launch_ranks<kRanks<T, 16>, rec_forward_kernel<T, 16>>(true, shared, p, stream);
     if constexpr (sizeof(T) == 2)
-        if (by == 2) return launch_ranks<rec_forward_kernel<T, 2>>(false, shared, p, stream);
-    return launch_ranks<rec_forward_kernel<T, 4>>(false, shared, p, stream);
+        if (by == 2) return launch_ranks<kRanks<T, 2>, rec_forward_kernel<T, 2>>(false, shared, p, stream);
+    return launch_ranks<kRanks<T, 4>, rec_forward_kernel<T, 4>>(false, shared, p, stream);
 }
 
 template <typename T> cudaError_t backward(const RecArgs& p, cudaStream_t stream)
 {
     const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.dy, &p.dz, &p.dx});
     const int shared = 6 * kSpan * kCols * (int)sizeof(T);
-    if (by == 16) return launch_ranks<rec_backward_kernel<T, 16>>(true, shared, p, stream);
+    if (by == 16) return launch_ranks<kRanks<T, 16>, rec_backward_kernel<T, 16>>(true, shared, p, stream);
     if constexpr (sizeof(T) == 2)
-        if (by == 2) return launch_ranks<rec_backward_kernel<T, 2>>(false, shared, p, stream);
-    return launch_ranks<rec_backward_kernel<T, 4>>(false, shared, p, stream);
+        if (by == 2) return launch_ranks<kRanks<T, 2>, rec_backward_kernel<T, 2>>(false, shared, p, stream);
+    return launch_ranks<kRanks<T, 4>, rec_backward_kernel<T, 4>>(false, shared, p, stream);
 }
 
 bool rec_seq_ok(const RecSeq& s, int64_t batch, int64_t steps, int64_t channels, bool written)
