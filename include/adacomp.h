@@ -411,7 +411,7 @@ adacomp_status adacomp_recurrence_init(adacomp_recurrence_t* out, int64_t channe
 
 /* Bytes of the fp32 states that a forward pass keeps for the backward pass: one every
  * ADACOMP_RECURRENCE_CHUNK steps, [batch][ceil(steps / chunk)][channels]. */
-#define ADACOMP_RECURRENCE_CHUNK 128
+#define ADACOMP_RECURRENCE_CHUNK 64
 size_t adacomp_recurrence_carry_bytes(adacomp_recurrence_t h, int64_t batch, int64_t steps);
 
 /* The forward pass. z, x and y each have a stride between sequences and one between

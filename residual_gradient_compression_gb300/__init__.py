@@ -29,7 +29,7 @@ RULE_ADACOMP, RULE_LOCAL_SELECTION = 0, 1
 MAX_GROUP = 128
 MAX_LEARNERS = 256
 DECODE_WS_FIXED = 10240
-RECURRENCE_CHUNK = 128  # steps between the states that the recurrence's forward pass keeps
+RECURRENCE_CHUNK = 64   # steps between the states that the recurrence's forward pass keeps
 ADAMW_BLOCK = 256       # elements that share a scale of 8-bit optimiser states
 STATIC_WS_BYTES = 1 << 20  # ADACOMP_STATIC_WS_BYTES: the largest workspace adacomp_compress_static_ws holds
 

@@ -2,9 +2,8 @@
 // forward and backward: kernels and C entry points (adacomp.h).
 #include <initializer_list>
 #include <new>
-#include <type_traits>
 
-#include "train_common.cuh"
+#include "recurrence.cuh"
 
 struct adacomp_recurrence {
     int64_t channels = 0;
@@ -16,48 +15,6 @@ namespace {
 
 constexpr int kRecThreads = 128;
 constexpr int kRecFew = 4;  // steps up to which a thread takes all of them
-constexpr int kRecChunk = ADACOMP_RECURRENCE_CHUNK;
-
-struct RecSeq {  // one strided [batch, steps, channels] tensor
-    void* p;
-    int64_t batch, step;
-};
-
-struct RecArgs {
-    RecSeq z, x, y, dy, dz, dx;
-    const float *h0, *dh_last;
-    const int32_t* lengths;
-    float *h_last, *dh0, *carry;
-    int64_t batch, steps, channels, chunks;
-    uint32_t blocks;  // of 64 channels, in a row
-};
-
-// a = sigmoid(z) and 1 - a = sigmoid(-z), neither formed by a subtraction: with
-// e = exp(-|z|), 1 / (1 + e) is the larger of the two and e / (1 + e) the smaller. exp is to
-// 2 + 1.2 |z| units in the last place and 0 from |z| = 87.4 on; NaN stays NaN.
-__device__ __forceinline__ void gate(float z, float* a, float* b)
-{
-    float e = -1.44269504f * fabsf(z), r = 1.0f;
-    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e));
-    r += e;
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r));
-    const float s = e * r;
-    const bool open = z >= 0.0f;
-    *a = open ? r : s;
-    *b = open ? s : r;
-}
-
-__device__ __forceinline__ int64_t length_of(const RecArgs& p, int64_t b)
-{
-    if (!p.lengths) return p.steps;
-    const int64_t n = p.lengths[b];
-    return n < 0 ? 0 : n > p.steps ? p.steps : n;
-}
-
-template <typename T> __device__ __forceinline__ T* at(const RecSeq& s, int64_t b, int64_t t, int64_t c)
-{
-    return static_cast<T*>(s.p) + b * s.batch + t * s.step + c;
-}
 
 // ---------------------------------------------------------------- few steps
 // One thread per column (a channel of a sequence), step after step.
@@ -80,115 +37,33 @@ template <typename T> __global__ void __launch_bounds__(kRecThreads) rec_forward
     if (p.h_last) p.h_last[i] = h;
 }
 
-// A lane's two columns. (Two values per instruction, add.f32x2 and its like, need fewer
-// instructions here but have longer latencies, and the chains are what is waited for:
-// backward 88 us with them, 77 without, at 16 sequences of 2048 steps of 1024 bf16 channels.)
-struct Two {
-    float x, y;
-};
-__device__ __forceinline__ Two two_of(float x, float y) { return {x, y}; }
-__device__ __forceinline__ Two two_of(float x) { return {x, x}; }
-__device__ __forceinline__ Two operator*(Two a, Two b) { return {__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y)}; }
-__device__ __forceinline__ Two operator+(Two a, Two b) { return {__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)}; }
-__device__ __forceinline__ Two operator-(Two a, Two b) { return {__fsub_rn(a.x, b.x), __fsub_rn(a.y, b.y)}; }
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) { return {fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)}; }
-
 // ---------------------------------------------------------------- many steps
-// The steps are split: a warp has 64 columns (two per lane) and eight consecutive steps, a
-// CTA 64 steps, a cluster of up to 16 CTAs up to 1024, and where the sequence is longer the
-// cluster goes on in rounds. Each warp forms what its steps do to a state, h -> A h + H with
-// A the product of its gates. The warps exchange these through shared memory, and the CTAs
-// write theirs into every CTA of the cluster (one warp of each does); then each warp knows
-// the state before its first step and goes through its steps again, from registers. So every element
-// is read once, and no CTA waits for one that may not be running. The next round's elements
-// are copied to shared memory meanwhile.
-constexpr int kCols = 64, kSteps = 8, kWarps = 8, kThreads = 32 * kWarps, kSpan = kSteps * kWarps;
-constexpr int kTile = kSpan * kCols;  // elements of a tensor that a CTA has in a round
-static_assert(kRecChunk == 2 * kSpan, "a kept state every second CTA");
+// A warp has 32 or 64 columns and some consecutive steps, a chunk, and the warps of a CTA take
+// the chunks of their columns in turn. Each forms from its elements alone what its steps do to
+// a state, h -> A h + H with A the product of its gates; then it waits for the state before its
+// first step from the warp that has the chunk before, hands A h + H on to the next at once, and
+// goes through its steps again, from registers. So every element is read once, the chain
+// through the sequence is one fused multiply-add and one hand-over per chunk, and no warp waits
+// for one that may not be running. A hand-over is a named barrier of the two warps. The warp's
+// next chunk is copied to shared memory meanwhile.
+constexpr int kWarps = 8;
 
-__device__ __forceinline__ uint32_t cluster_rank()
+__device__ __forceinline__ void hand_on(int barrier)
 {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
+    __syncwarp();
+    asm volatile("bar.arrive %0, 64;" ::"r"(barrier) : "memory");
 }
 
-__device__ __forceinline__ void cluster_sync()
+__device__ __forceinline__ void take_over(int barrier)
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    __syncwarp();
+    asm volatile("bar.sync %0, 64;" ::"r"(barrier) : "memory");
 }
 
-// Waits for the CTAs of the cluster without an order of memory: the results' stores need none.
-__device__ __forceinline__ void cluster_meet()
-{
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t shared_address(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ Two low(float4 v) { return two_of(v.x, v.y); }
-__device__ __forceinline__ Two high(float4 v) { return two_of(v.z, v.w); }
-
-__device__ __forceinline__ float4 quad(Two a, Two b) { return make_float4(a.x, a.y, b.x, b.y); }
-
-// What the CTAs of a cluster write to each other in a round: each CTA's values, and the
-// barrier that counts their bytes. Two of them take turns: a CTA that writes for the round
-// after next has all others' values of the next one, so that they have read these.
-// (A barrier of the whole cluster would have to wait for each round's stores of results.)
-template <int kRanks> struct Exchange {
-    float4 value[kRanks][32];
-    float4 before[32];  // backward: the (A, H) of the CTA before, where the chunk is its
-    unsigned long long barrier;
-};
-
-// CTAs of a cluster at most. Sixteen halve the rounds of few and long sequences; but for rows
-// of bf16 by 16 bytes the exchange's memory would cost an SM one of its CTAs.
-template <typename T, int kBytes> constexpr int kRanks = sizeof(T) == 2 && kBytes == 16 ? 16 : 8;
-
-template <int R> __device__ __forceinline__ void exchange_init(Exchange<R>* x)
-{
-    if (threadIdx.x < 2)
-        asm volatile("mbarrier.init.shared.b64 [%0], 1;" ::"r"(shared_address(&x[threadIdx.x].barrier)) : "memory");
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-}
-
-template <int R> __device__ __forceinline__ void exchange_expect(Exchange<R>* x, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(shared_address(&x->barrier)), "r"(bytes)
-                 : "memory");
-}
-
-// Writes v to the place of `p` in the CTA `rank`, and counts it at that CTA's barrier.
-template <int R> __device__ __forceinline__ void push(Exchange<R>* x, float4* p, uint32_t rank, float4 v)
-{
-    uint32_t a, b;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(shared_address(p)), "r"(rank));
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(shared_address(&x->barrier)), "r"(rank));
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
-                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(b)
-                 : "memory");
-}
-
-// Waits for a barrier's phase. The CTAs of a cluster run together and each writes before it
-// waits, so the wait ends; were it not to, it is given up after some seconds.
-template <int R> __device__ __forceinline__ bool exchange_wait(Exchange<R>* x, uint32_t phase)
-{
-    for (uint32_t i = 0; i < (1u << 22); ++i) {
-        uint32_t done;
-        asm volatile(
-            "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-            : "=r"(done)
-            : "r"(shared_address(&x->barrier)), "r"(phase)
-            : "memory");
-        if (done) return true;
-    }
-    return false;
-}
-
-// The columns of a tile. Where a sequence's rows are read 16 bytes at a time (kBytes), a
-// tile is 64 channels of one sequence; otherwise the channels of all sequences are numbered
+// A column of a tile. Where a sequence's rows are read 16 bytes at a time (kBytes), a tile is
+// kCols channels of one sequence; otherwise the channels of all sequences are numbered
 // through, so that few channels fill a tile too.
-template <int kBytes> struct Column {
+template <int kBytes, int kCols> struct Column {
     int64_t b, c;
     int32_t len;  // of its sequence; 0 past the last column
     bool on;
@@ -196,8 +71,9 @@ template <int kBytes> struct Column {
     __device__ __forceinline__ Column(const RecArgs& p, uint32_t tile, int j)
     {
         if (kBytes == 16) {
-            b = tile / p.blocks;
-            c = (int64_t)(tile - (uint32_t)b * p.blocks) * kCols + j;
+            const uint32_t blocks = (uint32_t)((p.channels + kCols - 1) / kCols);
+            b = tile / blocks;
+            c = (int64_t)(tile - (uint32_t)b * blocks) * kCols + j;
             on = c < p.channels;
         } else {
             const int64_t i = (int64_t)tile * kCols + j;
@@ -208,24 +84,21 @@ template <int kBytes> struct Column {
         len = on ? (int32_t)length_of(p, b) : 0;
     }
     __device__ __forceinline__ int64_t state(const RecArgs& p) const { return b * p.channels + c; }
+    __device__ __forceinline__ int64_t kept(const RecArgs& p, int32_t t) const
+    {
+        return (b * p.chunks + t / kRecChunk) * p.channels + c;
+    }
 };
 
-// Distances between rows: in 32 bits where the rows are read 16 bytes at a time (the host
-// sees to it), so that an address is one instruction.
-template <int kBytes> using Distance = typename std::conditional<kBytes == 16, int32_t, int64_t>::type;
-
-template <typename T> __device__ __forceinline__ T* moved(T* p, int64_t bytes)
-{
-    return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + bytes);
-}
-
-// Copies a CTA's 64 steps of a tile to shared memory, [step][column], kBytes at a time:
-// every thread has one place in the rows and takes every kStride-th of them. What lies past
-// a sequence's length or the last channel is not read, and what stands there not used.
-template <typename T, int kBytes, int kTensors> struct Copier {
+// Copies a warp's chunk of kTensors tensors to shared memory, [tensor][step][column], kBytes
+// at a time: every lane has one place in the rows and takes every kStride-th of them. What
+// lies past a sequence's length or the last channel is not read, and what stands there not used.
+template <typename T, int kBytes, int kCols, int kChunk, int kTensors> struct Copier {
     static constexpr int kPlaces = kCols * (int)sizeof(T) / kBytes;
-    static constexpr int kStride = kThreads / kPlaces;
+    static constexpr int kStride = 32 / kPlaces < kChunk ? 32 / kPlaces : kChunk;
     static constexpr int kEach = kBytes / (int)sizeof(T);  // elements at a time
+    static constexpr int kElements = kChunk * kCols;       // of one tensor
+    static_assert(kPlaces <= 32 && kChunk % kStride == 0, "whole rows");
     const T* from[kTensors];
     Distance<kBytes> step[kTensors];
     int32_t len;
@@ -233,7 +106,8 @@ template <typename T, int kBytes, int kTensors> struct Copier {
 
     __device__ __forceinline__ Copier(const RecArgs& p, uint32_t tile, const RecSeq* const (&s)[kTensors])
     {
-        const Column<kBytes> col(p, tile, (threadIdx.x % kPlaces) * kEach);
+        const int lane = threadIdx.x & 31;
+        const Column<kBytes, kCols> col(p, tile, lane % kPlaces * kEach);
         const int64_t rest = (p.channels - col.c) * (int)sizeof(T);
         bytes = !col.on ? 0u : rest < kBytes ? (uint32_t)rest : (uint32_t)kBytes;
         len = bytes == 0 ? 0 : col.len;
@@ -246,420 +120,361 @@ template <typename T, int kBytes, int kTensors> struct Copier {
 
     __device__ __forceinline__ void copy(T* to, int32_t t0) const
     {
-        const int row0 = threadIdx.x / kPlaces, left = len - t0;
-        T* const place = to + row0 * kCols + (threadIdx.x % kPlaces) * kEach;
+        const int lane = threadIdx.x & 31, row0 = lane / kPlaces;
+        const int left = row0 < kChunk ? len - t0 - row0 : 0;  // the other lanes have no place
+        T* const place = to + row0 * kCols + lane % kPlaces * kEach;
 #pragma unroll
         for (int i = 0; i < kTensors; ++i) {
             const T* const f = moved(from[i], (int64_t)(t0 + row0) * step[i]);
-            T v[kSpan / kStride];
+            T v[kChunk / kStride];
 #pragma unroll
-            for (int k = 0; k < kSpan / kStride; ++k)
-                if (row0 + k * kStride < left) {
+            for (int k = 0; k < kChunk / kStride; ++k)
+                if (k * kStride < left) {
                     const T* const g = moved(f, (Distance<kBytes>)(k * kStride) * step[i]);
-                    const uint32_t d = shared_address(place + i * kTile + k * kStride * kCols);
+                    const uint32_t d = (uint32_t)__cvta_generic_to_shared(place + i * kElements + k * kStride * kCols);
                     if constexpr (kBytes == 2) v[k] = *g;
                     else if constexpr (kBytes == 16)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(g), "r"(bytes) : "memory");
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(g), "r"(bytes)
+                                     : "memory");
                     else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(g) : "memory");
                 }
             if constexpr (kBytes == 2) {
 #pragma unroll
-                for (int k = 0; k < kSpan / kStride; ++k)
-                    if (row0 + k * kStride < left) place[i * kTile + k * kStride * kCols] = v[k];
+                for (int k = 0; k < kChunk / kStride; ++k)
+                    if (k * kStride < left) place[i * kElements + k * kStride * kCols] = v[k];
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
 };
 
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-
-__device__ __forceinline__ void two(const float* p, float& x, float& y)
+__device__ __forceinline__ void copies_wait()
 {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    x = v.x, y = v.y;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();  // the other lanes' too, and their reads of what is copied over next
 }
 
-__device__ __forceinline__ void two(const bf16* p, float& x, float& y)
-{
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
-    x = bf16_low(v), y = bf16_high(v);
-}
-
-// Where a lane's two columns of a warp's steps go.
-template <typename T, int kBytes> struct Writer {
-    T* p[2];
-    Distance<kBytes> step;
-
-    __device__ __forceinline__ Writer(const RecSeq& s, const Column<kBytes> (&col)[2], int64_t t)
-        : step((Distance<kBytes>)(s.step * (int)sizeof(T)))
-    {
-        p[0] = at<T>(s, col[0].b, t, col[0].c);
-        if (kBytes != 16) p[1] = at<T>(s, col[1].b, t, col[1].c);
-    }
-    // step k of both columns, which are there
-    __device__ __forceinline__ void put(int k, Two v) const
-    {
-        T* const q = moved(p[0], k * step);
-        if constexpr (kBytes == 16) {
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(q) = make_float2(v.x, v.y);
-            else *reinterpret_cast<__nv_bfloat162*>(q) = __floats2bfloat162_rn(v.x, v.y);
-        } else {
-            *q = from_f32<T>(v.x);
-            *moved(p[1], k * step) = from_f32<T>(v.y);
-        }
-    }
-    __device__ __forceinline__ void put(int k, float x, float y, bool on0, bool on1) const
-    {
-        T* const q = moved(p[0], k * step);
-        if (on0) *q = from_f32<T>(x);
-        if (on1) *(kBytes == 16 ? q + 1 : moved(p[1], k * step)) = from_f32<T>(y);
-    }
+// h -> A h + H, or the gradient's p -> A p + H.
+struct Step {
+    float A, H;
 };
 
-// What a warp has to mind in a round: how many of its steps lie within each column's length
-// and within the tensors, and whether all do.
-struct Live {
-    int live0, live1, whole;
-    bool all;
-
-    template <int kBytes>
-    __device__ __forceinline__ Live(const RecArgs& p, const Column<kBytes> (&col)[2], int32_t ts)
-        : live0(max(0, min(kSteps, col[0].len - ts))), live1(max(0, min(kSteps, col[1].len - ts))),
-          whole(max(0, min(kSteps, (int32_t)p.steps - ts))),
-          all(__all_sync(0xffffffffu, live0 == kSteps && live1 == kSteps))
-    {
+// kV neighbouring values of a row.
+template <int kV> __device__ __forceinline__ void values(const float* p, float (&v)[kV])
+{
+    if constexpr (kV == 2) {
+        const float2 q = *reinterpret_cast<const float2*>(p);
+        v[0] = q.x, v[1] = q.y;
+    } else {
+        v[0] = *p;
     }
-};
-
-template <int kBytes>
-__device__ __forceinline__ Two load_state(const float* p, const RecArgs& a, const Column<kBytes> (&col)[2], int64_t more = 0)
-{
-    float v[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-        if (p && col[j].on) v[j] = p[col[j].state(a) + more];
-    return two_of(v[0], v[1]);
 }
 
-template <int kBytes>
-__device__ __forceinline__ void store_state(float* p, const RecArgs& a, const Column<kBytes> (&col)[2], Two s)
+template <int kV> __device__ __forceinline__ void values(const bf16* p, float (&v)[kV])
 {
-    if (p && col[0].on) p[col[0].state(a)] = s.x;
-    if (p && col[1].on) p[col[1].state(a)] = s.y;
+    if constexpr (kV == 2) {
+        const uint32_t q = *reinterpret_cast<const uint32_t*>(p);
+        v[0] = bf16_low(q), v[1] = bf16_high(q);
+    } else {
+        v[0] = to_f32(*p);
+    }
 }
 
-// The address of a column's kept state: [batch][chunks][channels].
-template <int kBytes> __device__ __forceinline__ float* kept(const RecArgs& p, const Column<kBytes>& col, int32_t t)
+template <int kV> __device__ __forceinline__ void put(float* p, const float (&v)[kV])
 {
-    return p.carry + (col.b * p.chunks + t / kRecChunk) * p.channels + col.c;
+    if constexpr (kV == 2) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    else *p = v[0];
 }
 
-template <typename T, int kBytes>
-__global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
+template <int kV> __device__ __forceinline__ void put(bf16* p, const float (&v)[kV])
 {
+    if constexpr (kV == 2) *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v[0], v[1]);
+    else *p = from_f32<bf16>(v[0]);
+}
+
+// kV: columns of a lane, two where rows are read 16 bytes at a time and there are many.
+constexpr int kForward = 16;  // steps of a chunk
+
+template <typename T, int kBytes, int kV>
+__global__ void __launch_bounds__(32 * kWarps, kV == 2 ? 2 : 4) rec_forward_kernel(const __grid_constant__ RecArgs p)
+{
+    constexpr int kCols = 32 * kV, S = kForward;
+    static_assert(kV == 1 || kBytes == 16, "neighbours lie in one row");
+    using Copy = Copier<T, kBytes, kCols, S, 2>;
     extern __shared__ __align__(16) uint8_t shared_bytes[];
-    __shared__ float4 part[kWarps][32];   // a warp's (A, H) of the lane's columns
-    __shared__ Two begin[kWarps][32];  // the state before its first step
-    __shared__ Exchange<kRanks<T, kBytes>> exchange[2];
-    const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (2 * kTile); };
+    __shared__ float state[kWarps][kCols];  // after a warp's chunk
     ptx::griddep_wait();
-    if (ranks > 1) {
-        exchange_init(exchange);
-        cluster_sync();  // all CTAs run, and their barriers are there, before one writes to another
-    }
-    const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Column<kBytes> col[2] = {Column<kBytes>(p, tile, 2 * lane), Column<kBytes>(p, tile, 2 * lane + 1)};
-    const Copier<T, kBytes, 2> copier(p, tile, {&p.z, &p.x});
-    const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
-    Two h0 = load_state(p.h0, p, col);  // before the round's first step (the joining warp's)
-    bool given_up = false;
-    int32_t tc = (int32_t)rank * kSpan;
-    copier.copy(tile_of(0), tc);
-    for (int32_t t0 = 0, round = 0; t0 < steps; t0 += span, tc += span, ++round) {
-        const int par = round & 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, j = lane * kV;
+    T* const ring = reinterpret_cast<T*>(shared_bytes) + warp * (4 * Copy::kElements);  // two chunks
+    const Column<kBytes, kCols> col(p, blockIdx.x, j);
+    const int on = !col.on ? 0 : kV == 2 && col.c + 1 < p.channels ? 2 : 1;  // of the lane's columns
+    const Copy copier(p, blockIdx.x, {&p.z, &p.x});
+    const Distance<kBytes> step = (Distance<kBytes>)(p.y.step * (int)sizeof(T));
+    const int32_t steps = (int32_t)p.steps, turn = warps * S;
+    const int prev = warp == 0 ? warps - 1 : warp - 1;
+    int32_t t0 = warp * S;
+    if (t0 < steps) copier.copy(ring, t0);
+    for (int slot = 0; t0 < steps; t0 += turn, slot ^= 1) {
         copies_wait();
-        __syncthreads();
-        if (t0 + span < steps) copier.copy(tile_of(par ^ 1), tc + span);
-        const int32_t ts = tc + warp * kSteps;
-        const Live at_hand(p, col, ts);
-        const T* z = tile_of(par) + warp * kSteps * kCols + 2 * lane;
-        Two a[kSteps], u[kSteps], A = two_of(1.0f), H = two_of(0.0f);
+        if (t0 + turn < steps) copier.copy(ring + (slot ^ 1) * (2 * Copy::kElements), t0 + turn);
+        const T* z = ring + slot * (2 * Copy::kElements) + j;
+        const int32_t live = col.len - t0;
+        const bool all = __all_sync(0xffffffffu, live >= S && on == kV);
+        float a[S][kV], u[S][kV], h[kV], after[kV];
+        Step own[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) own[v] = {1.0f, 0.0f};
         const auto form = [&](auto masked) {
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                float z0, z1, x0, x1, a0, a1, b0, b1;
-                two(z + k * kCols, z0, z1);
-                two(z + k * kCols + kTile, x0, x1);
-                gate(z0, &a0, &b0);
-                gate(z1, &a1, &b1);
-                if (masked.value) {  // past the length the state stays as it is
-                    if (k >= at_hand.live0) a0 = 1.0f, b0 = x0 = 0.0f;
-                    if (k >= at_hand.live1) a1 = 1.0f, b1 = x1 = 0.0f;
+            for (int k = 0; k < S; ++k) {
+                float zv[kV], xv[kV];
+                values(z + k * kCols, zv);
+                values(z + k * kCols + Copy::kElements, xv);
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    float r;
+                    gate(zv[v], &a[k][v], &r);
+                    u[k][v] = r * xv[v];
+                    if (masked.value && k >= live) a[k][v] = 1.0f, u[k][v] = 0.0f;  // past the length the state stays
+                    own[v].H = fmaf(a[k][v], own[v].H, u[k][v]);
+                    own[v].A *= a[k][v];
                 }
-                a[k] = two_of(a0, a1);
-                u[k] = two_of(b0, b1) * two_of(x0, x1);
-                H = fma2(a[k], H, u[k]);
-                A = A * a[k];
             }
         };
-        if (at_hand.all) form(std::false_type());
+        if (all) form(std::false_type());
         else form(std::true_type());
-        part[warp][lane] = quad(A, H);
-        __syncthreads();
-        if (warp == 0) {
-            Two h = h0;  // before the CTA's first step
-            if (ranks > 1) {
-                Exchange<kRanks<T, kBytes>>& x = exchange[par];
-                if (lane == 0) exchange_expect(&x, ranks * 512);
-                Two tA = two_of(1.0f), tH = two_of(0.0f);
+        if (t0 == 0) {
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float4 q = part[w][lane];
-                    tH = fma2(low(q), tH, high(q));
-                    tA = tA * low(q);
-                }
-                for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tH));
-                if (!given_up) given_up = !exchange_wait(&x, (round >> 1) & 1);
-                for (uint32_t r = 0; r < ranks; ++r) {
-                    if (r == rank) h = h0;
-                    const float4 q = x.value[r][lane];
-                    h0 = fma2(low(q), h0, high(q));
-                }
-                if (given_up) h = h0 = two_of(NAN);
-            }
-            if (p.carry && tc % kRecChunk == 0 && tc < steps) {
-                const Two v = h;
-                if (col[0].on) *kept(p, col[0], tc) = v.x;
-                if (col[1].on) *kept(p, col[1], tc) = v.y;
-            }
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                begin[w][lane] = h;
-                const float4 q = part[w][lane];
-                h = fma2(low(q), h, high(q));
-            }
-            if (ranks == 1) h0 = h;
+            for (int v = 0; v < kV; ++v) h[v] = p.h0 && v < on ? p.h0[col.state(p) + v] : 0.0f;
+        } else {
+            take_over(1 + prev);
+            values(&state[prev][j], h);
         }
-        __syncthreads();
-        Two h = begin[warp][lane];
-        const Writer<T, kBytes> y(p.y, col, ts);
-        if (at_hand.all) {
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                h = fma2(a[k], h, u[k]);
-                y.put(k, h);
+        for (int v = 0; v < kV; ++v) after[v] = fmaf(own[v].A, h[v], own[v].H);
+        if (t0 + S < steps) {
+            put(&state[warp][j], after);
+            hand_on(1 + warp);
+        } else if (p.h_last) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+                if (v < on) p.h_last[col.state(p) + v] = after[v];
+        }
+        if (p.carry && t0 % kRecChunk == 0) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+                if (v < on) p.carry[col.kept(p, t0) + v] = h[v];
+        }
+        T* const y = at<T>(p.y, col.b, t0, col.c);
+        if (all) {
+#pragma unroll
+            for (int k = 0; k < S; ++k) {
+#pragma unroll
+                for (int v = 0; v < kV; ++v) h[v] = fmaf(a[k][v], h[v], u[k][v]);
+                put(moved(y, k * step), h);
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                h = fma2(a[k], h, u[k]);
-                const Two v = h;
-                if (k < at_hand.whole)
-                    y.put(k, k < at_hand.live0 ? v.x : 0.0f, k < at_hand.live1 ? v.y : 0.0f, col[0].on, col[1].on);
-            }
+            for (int k = 0; k < S; ++k)
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    h[v] = fmaf(a[k][v], h[v], u[k][v]);
+                    if (v < on && t0 + k < steps) moved(y, k * step)[v] = from_f32<T>(k < live ? h[v] : 0.0f);
+                }
         }
     }
-    if (rank == 0 && warp == 0) store_state(p.h_last, p, col, h0);
-    if (ranks > 1) cluster_meet();  // no CTA ends while another may write to it
 }
 
 // The reverse of it: p, the gradient that reaches a state from the steps after it, goes
-// through a warp's steps as p -> A p + P, P = sum of dy_k times the gates up to and with
-// step k. The states are formed again from the one that the forward pass kept for the chunk
-// of two CTAs: that is less to read than y, and not rounded.
-template <typename T, int kBytes>
-__global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
+// through a chunk as p -> A p + P, P = sum of dy_k times the gates up to and with step k. A
+// CTA's warps have the chunks of a kept state at a time, and form the states again from it
+// (handed on from the first to the last of them): that is less to read than y, and not rounded.
+template <int kV> constexpr int kBackward = kV == 2 ? 8 : 16;  // steps of a chunk
+template <int kV> constexpr int kBackWarps = kRecChunk / kBackward<kV>;
+static_assert(kBackWarps<2> <= 8, "fifteen named barriers");
+
+template <typename T, int kBytes, int kV>
+__global__ void __launch_bounds__(32 * kBackWarps<kV>, kV == 2 ? 2 : 6) rec_backward_kernel(const __grid_constant__ RecArgs p)
 {
+    constexpr int kCols = 32 * kV, S = kBackward<kV>, W = kBackWarps<kV>;
+    using Copy = Copier<T, kBytes, kCols, S, 3>;
     extern __shared__ __align__(16) uint8_t shared_bytes[];
-    __shared__ float4 part[kWarps][32];  // a warp's (A, H)
-    __shared__ Two grad[kWarps][32];  // its P
-    __shared__ float4 begin[32];         // the state before the CTA's first step, and p after its last
-    __shared__ Exchange<kRanks<T, kBytes>> exchange[2];
-    const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (3 * kTile); };
+    __shared__ float state[W][kCols];  // after a warp's chunk
+    __shared__ float grad[W][kCols];   // the gradient before it
     ptx::griddep_wait();
-    if (ranks > 1) {
-        exchange_init(exchange);
-        cluster_sync();  // all CTAs run, and their barriers are there, before one writes to another
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane * kV;
+    T* const ring = reinterpret_cast<T*>(shared_bytes) + warp * (6 * Copy::kElements);  // two chunks
+    const Column<kBytes, kCols> col(p, blockIdx.x, j);
+    const int on = !col.on ? 0 : kV == 2 && col.c + 1 < p.channels ? 2 : 1;  // of the lane's columns
+    const Copy copier(p, blockIdx.x, {&p.z, &p.x, &p.dy});
+    const Distance<kBytes> step_z = (Distance<kBytes>)(p.dz.step * (int)sizeof(T));
+    const Distance<kBytes> step_x = (Distance<kBytes>)(p.dx.step * (int)sizeof(T));
+    const int32_t steps = (int32_t)p.steps;
+    const int next = warp == W - 1 ? 0 : warp + 1;  // has the chunk after this warp's
+    if (steps == 0) {
+#pragma unroll
+        for (int v = 0; v < kV; ++v)
+            if (p.dh0 && warp == 0 && v < on) p.dh0[col.state(p) + v] = p.dh_last ? p.dh_last[col.state(p) + v] : 0.0f;
+        return;
     }
-    const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Column<kBytes> col[2] = {Column<kBytes>(p, tile, 2 * lane), Column<kBytes>(p, tile, 2 * lane + 1)};
-    const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
-    int32_t t0 = steps > 0 ? (steps - 1) / span * span : -1, tc = t0 + (int32_t)rank * kSpan;
-    const Copier<T, kBytes, 3> copier(p, tile, {&p.z, &p.x, &p.dy});
-    Two p0 = load_state(p.dh_last, p, col);  // after the round's last step (the joining warp's)
-    bool given_up = false;
-    if (t0 >= 0) copier.copy(tile_of(0), tc);
-    for (int32_t round = 0; t0 >= 0; t0 -= span, tc -= span, ++round) {
-        const int par = round & 1;
-        Two h = two_of(0.0f);  // before the chunk's first step
-        if (warp == kWarps - 1 && tc < steps)
-            h = two_of(col[0].on ? *kept(p, col[0], tc) : 0.0f, col[1].on ? *kept(p, col[1], tc) : 0.0f);
+    // the last of the warp's chunks, if it has one
+    int32_t t0 = (steps - 1) / kRecChunk * kRecChunk + warp * S;
+    if (t0 >= steps) t0 -= kRecChunk;
+    if (t0 >= 0) copier.copy(ring, t0);
+    for (int slot = 0; t0 >= 0; t0 -= kRecChunk, slot ^= 1) {
+        float h[kV], q[kV];  // before the chunk's first step, and after its last
+#pragma unroll
+        for (int v = 0; v < kV; ++v) h[v] = warp == 0 && v < on ? p.carry[col.kept(p, t0) + v] : 0.0f;
         copies_wait();
-        __syncthreads();
-        if (t0 > 0) copier.copy(tile_of(par ^ 1), tc - span);
-        const int32_t ts = tc + warp * kSteps;
-        const Live at_hand(p, col, ts);
-        const T* z = tile_of(par) + warp * kSteps * kCols + 2 * lane;
-        Two a[kSteps], b[kSteps], A = two_of(1.0f), H = two_of(0.0f), P = two_of(0.0f);
-        const auto inputs = [&](auto masked, int tensor, int k) {  // x or dy
-            float v0, v1;
-            two(z + k * kCols + tensor * kTile, v0, v1);
-            if (masked.value) {
-                if (k >= at_hand.live0) v0 = 0.0f;
-                if (k >= at_hand.live1) v1 = 0.0f;
-            }
-            return two_of(v0, v1);
-        };
+        if (t0 >= kRecChunk) copier.copy(ring + (slot ^ 1) * (3 * Copy::kElements), t0 - kRecChunk);
+        const T* z = ring + slot * (3 * Copy::kElements) + j;
+        const T *x = z + Copy::kElements, *d = x + Copy::kElements;
+        const int32_t live = col.len - t0;
+        const bool all = __all_sync(0xffffffffu, live >= S && on == kV);
+        float a[S][kV], b[S][kV], from_x[S][kV];  // from_x: x_t, later h_{t-1} - x_t
+        Step own[kV];
+        float P[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) own[v] = {1.0f, 0.0f}, P[v] = 0.0f;
         const auto form = [&](auto masked) {
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                float z0, z1, a0, a1, b0, b1;
-                two(z + k * kCols, z0, z1);
-                gate(z0, &a0, &b0);
-                gate(z1, &a1, &b1);
-                if (masked.value) {
-                    if (k >= at_hand.live0) a0 = 1.0f, b0 = 0.0f;
-                    if (k >= at_hand.live1) a1 = 1.0f, b1 = 0.0f;
+            for (int k = 0; k < S; ++k) {
+                float zv[kV], dv[kV];
+                values(z + k * kCols, zv);
+                values(x + k * kCols, from_x[k]);
+                values(d + k * kCols, dv);
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    gate(zv[v], &a[k][v], &b[k][v]);
+                    if (masked.value && k >= live) a[k][v] = 1.0f, b[k][v] = from_x[k][v] = dv[v] = 0.0f;
+                    own[v].H = fmaf(a[k][v], own[v].H, b[k][v] * from_x[k][v]);
+                    own[v].A *= a[k][v];
+                    P[v] = fmaf(own[v].A, dv[v], P[v]);
                 }
-                a[k] = two_of(a0, a1);
-                b[k] = two_of(b0, b1);
-                H = fma2(a[k], H, b[k] * inputs(masked, 1, k));
-                A = A * a[k];
-                P = fma2(A, inputs(masked, 2, k), P);
             }
         };
-        if (at_hand.all) form(std::false_type());
+        if (all) form(std::false_type());
         else form(std::true_type());
-        part[warp][lane] = quad(A, H);
-        grad[warp][lane] = P;
-        __syncthreads();
-        A = two_of(1.0f), H = two_of(0.0f);  // from the CTA's first step to the warp's
-        for (int w = 0; w < warp; ++w) {
-            const float4 v = part[w][lane];
-            H = fma2(low(v), H, high(v));
-            A = A * low(v);
-        }
-        Two B = two_of(1.0f);  // and from the CTA's end back to the warp's
-        P = two_of(0.0f);
-        for (int w = kWarps - 1; w > warp; --w) {
-            const Two v = low(part[w][lane]);
-            P = fma2(v, P, grad[w][lane]);
-            B = B * v;
-        }
-        if (warp == kWarps - 1) {
-            const float4 own = part[warp][lane];
-            const Two tA = A * low(own), tH = fma2(low(own), H, high(own));
-            Two tP = two_of(0.0f), q = p0;  // q: after the CTA's last step
+        // The gradient's hand-over comes first, so that the next kept state's last warp, which
+        // starts from it, has it soon; a warp's next hand-overs wait for one that follows them.
+        if (t0 + S >= steps) {
 #pragma unroll
-            for (int w = kWarps - 1; w >= 0; --w)
-                tP = fma2(low(part[w][lane]), tP, grad[w][lane]);
-            if (ranks > 1) {
-                Exchange<kRanks<T, kBytes>>& x = exchange[par];
-                if (lane == 0) exchange_expect(&x, ranks * 512 + (rank & 1) * 512);
-                for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tP));
-                if ((rank & 1) == 0) push(&x, &x.before[lane], rank + 1, quad(tA, tH));
-                if (!given_up) given_up = !exchange_wait(&x, (round >> 1) & 1);
-                for (uint32_t r = ranks; r-- > 0;) {
-                    if (r == rank) q = p0;
-                    const float4 v = x.value[r][lane];
-                    p0 = fma2(low(v), p0, high(v));
-                }
-                if (rank & 1) h = fma2(low(x.before[lane]), h, high(x.before[lane]));
-                if (given_up) h = q = p0 = two_of(NAN);
-            } else {
-                p0 = fma2(tA, p0, tP);
-            }
-            begin[lane] = quad(h, q);
+            for (int v = 0; v < kV; ++v) q[v] = p.dh_last && v < on ? p.dh_last[col.state(p) + v] : 0.0f;
+        } else {
+            take_over(8 + next);
+            values(&grad[next][j], q);
         }
-        __syncthreads();
-        h = fma2(A, low(begin[lane]), H);
-        Two q = fma2(B, high(begin[lane]), P);
-        const Writer<T, kBytes> dz(p.dz, col, ts), dx(p.dx, col, ts);
+        float on_to[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) on_to[v] = fmaf(own[v].A, q[v], P[v]);
+        if (t0 > 0) {
+            put(&grad[warp][j], on_to);
+            hand_on(8 + warp);
+        } else if (p.dh0) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+                if (v < on) p.dh0[col.state(p) + v] = on_to[v];
+        }
+        if (warp > 0) {
+            take_over(warp);
+            values(&state[warp - 1][j], h);
+        }
+        if (warp < W - 1 && t0 + S < steps) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) on_to[v] = fmaf(own[v].A, h[v], own[v].H);
+            put(&state[warp][j], on_to);
+            hand_on(1 + warp);
+        }
+        T* const dz = at<T>(p.dz, col.b, t0, col.c);
+        T* const dx = at<T>(p.dx, col.b, t0, col.c);
         const auto finish = [&](auto masked) {
-            Two before[kSteps];
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const Two x = inputs(masked, 1, k);
-                before[k] = h - x;  // h_{t-1} - x_t
-                h = fma2(a[k], h, b[k] * x);
-            }
+            for (int k = 0; k < S; ++k)
 #pragma unroll
-            for (int k = kSteps - 1; k >= 0; --k) {
-                const Two G = q + inputs(masked, 2, k), g = b[k] * G;
-                q = a[k] * G;
-                const Two v = a[k] * g * before[k];
+                for (int v = 0; v < kV; ++v) {
+                    const float xv = from_x[k][v];
+                    from_x[k][v] = h[v] - xv;
+                    h[v] = fmaf(a[k][v], h[v], b[k][v] * xv);
+                }
+#pragma unroll
+            for (int k = S - 1; k >= 0; --k) {
+                float dv[kV], gx[kV], gz[kV];
+                values(d + k * kCols, dv);
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    const float G = __fadd_rn(q[v], masked.value && k >= live ? 0.0f : dv[v]);
+                    gx[v] = b[k][v] * G;
+                    gz[v] = a[k][v] * gx[v] * from_x[k][v];
+                    q[v] = __fmul_rn(a[k][v], G);
+                }
                 if (!masked.value) {
-                    dx.put(k, g);
-                    dz.put(k, v);
-                } else if (k < at_hand.whole) {
-                    const Two e = g, f = v;
-                    const bool l0 = k < at_hand.live0, l1 = k < at_hand.live1;
-                    dx.put(k, l0 ? e.x : 0.0f, l1 ? e.y : 0.0f, col[0].on, col[1].on);
-                    dz.put(k, l0 ? f.x : 0.0f, l1 ? f.y : 0.0f, col[0].on, col[1].on);
+                    put(moved(dx, k * step_x), gx);
+                    put(moved(dz, k * step_z), gz);
+                } else if (t0 + k < steps) {
+#pragma unroll
+                    for (int v = 0; v < kV; ++v)
+                        if (v < on) {
+                            moved(dx, k * step_x)[v] = from_f32<T>(k < live ? gx[v] : 0.0f);
+                            moved(dz, k * step_z)[v] = from_f32<T>(k < live ? gz[v] : 0.0f);
+                        }
                 }
             }
         };
-        if (at_hand.all) finish(std::false_type());
+        if (all) finish(std::false_type());
         else finish(std::true_type());
     }
-    if (rank == 0 && warp == kWarps - 1) store_state(p.dh0, p, col, p0);
-    if (ranks > 1) cluster_meet();  // no CTA ends while another may write to it
 }
 
-// Launches a kernel of clusters, behind the kernel ahead of it as launch_after does.
-template <int kRanks, void (*kern)(RecArgs, uint32_t)>
-cudaError_t launch_ranks(bool rows16, int shared, const RecArgs& p, cudaStream_t stream)
-{
-    static bool set[64] = {};  // the kernel's shared memory, once per device
-
-    uint32_t ranks = 1;
-    const int64_t tiles = rows16 ? p.batch * p.blocks : (p.batch * p.channels + kCols - 1) / kCols;
-    // a CTA more in a cluster is worth its exchange where the GPU is not full without it; more
-    // than eight where all clusters still run at once
-    const uint32_t most = tiles <= 19 ? (uint32_t)kRanks : 8;
-    while (ranks < most && (int64_t)ranks * kSpan < p.steps && tiles * ranks < 1024) ranks *= 2;
-    if (tiles > 0x7fffffff / (int64_t)ranks) return cudaErrorInvalidConfiguration;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
-    if (e == cudaSuccess && !set[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
-        if (e == cudaSuccess && kRanks > 8)
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        set[dev] = e == cudaSuccess;
-    }
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * ranks));
-    cfg.blockDim = dim3((unsigned)kThreads);
-    cfg.dynamicSmemBytes = (size_t)shared;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ranks;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, p, ranks);
-}
-
+// ---------------------------------------------------------------- launches
 // How many bytes at a time the rows of all given tensors can be copied: 16, 4 or 2.
 int row_bytes(const RecArgs& p, int e, std::initializer_list<const RecSeq*> seqs)
 {
     int64_t bits = 0;
-    bool near = true;  // a CTA's steps span less than 2^31 bytes
+    bool near = true;  // a chunk's steps span less than 2^31 bytes
     for (const RecSeq* s : seqs) {
         bits |= (int64_t)reinterpret_cast<uintptr_t>(s->p) | s->batch * e | s->step * e;
         near = near && s->step < (int64_t)1 << 22;
     }
-    if (bits % 16 == 0 && near && p.channels >= kCols) return 16;
+    if (bits % 16 == 0 && near && p.channels >= 32) return 16;
     return e == 4 || ((bits | p.channels * e) % 4 == 0) ? 4 : 2;
 }
+
+// A kernel with a CTA of `warps` per tile of `cols` columns; per_warp: shared bytes of a warp.
+template <void (*kern)(RecArgs)>
+cudaError_t launch_tiles(const RecArgs& p, bool rows16, int cols, int most, int warps, int per_warp, cudaStream_t stream)
+{
+    static bool set[64] = {};  // the kernel's shared memory, once per device
+    const int64_t tiles = rows16 ? p.batch * ((p.channels + cols - 1) / cols) : (p.batch * p.channels + cols - 1) / cols;
+    if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+    if (e == cudaSuccess && !set[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most * per_warp);
+        set[dev] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess) return e;
+    return launch_after(kern, dim3((unsigned)tiles), dim3(32 * (unsigned)warps), (size_t)(warps * per_warp), stream, p);
+}
+
+template <typename T, int kBytes, int kV> cudaError_t forward_v(const RecArgs& p, cudaStream_t stream)
+{
+    const int64_t chunks = (p.steps + kForward - 1) / kForward;
+    return launch_tiles<rec_forward_kernel<T, kBytes, kV>>(p, kBytes == 16, 32 * kV, kWarps,
+                                                           chunks < kWarps ? (int)chunks : kWarps,
+                                                           2 * 2 * kForward * 32 * kV * (int)sizeof(T), stream);
+}
+
+template <typename T, int kBytes, int kV> cudaError_t backward_v(const RecArgs& p, cudaStream_t stream)
+{
+    return launch_tiles<rec_backward_kernel<T, kBytes, kV>>(p, kBytes == 16, 32 * kV, kBackWarps<kV>, kBackWarps<kV>,
+                                                            2 * 3 * kBackward<kV> * 32 * kV * (int)sizeof(T), stream);
+}
+
+// How a call is split. Many columns: a CTA for 64 or 32 of them, if that makes one for every
+// SM; otherwise, if there are steps to split, clusters (recurrence_split.cu).
+constexpr int64_t kManyColumns = 152 * 32;
+constexpr int64_t kSplitSteps = 128;
 
 template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
 {
@@ -669,21 +484,23 @@ template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
         return launch_after(rec_forward_few_kernel<T>, dim3((unsigned)((n + kRecThreads - 1) / kRecThreads)),
                             dim3(kRecThreads), 0, stream, p);
     }
-    const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.y}), shared = 4 * kSpan * kCols * (int)sizeof(T);
-    if (by == 16) return launch_ranks<kRanks<T, 16>, rec_forward_kernel<T, 16>>(true, shared, p, stream);
+    const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.y});
+    if (n < kManyColumns && p.steps > kSplitSteps) return rec_split_forward<T>(p, by, stream);
+    if (by == 16) return n >= 2 * kManyColumns ? forward_v<T, 16, 2>(p, stream) : forward_v<T, 16, 1>(p, stream);
     if constexpr (sizeof(T) == 2)
-        if (by == 2) return launch_ranks<kRanks<T, 2>, rec_forward_kernel<T, 2>>(false, shared, p, stream);
-    return launch_ranks<kRanks<T, 4>, rec_forward_kernel<T, 4>>(false, shared, p, stream);
+        if (by == 2) return forward_v<T, 2, 1>(p, stream);
+    return forward_v<T, 4, 1>(p, stream);
 }
 
 template <typename T> cudaError_t backward(const RecArgs& p, cudaStream_t stream)
 {
+    const int64_t n = p.batch * p.channels;
     const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.dy, &p.dz, &p.dx});
-    const int shared = 6 * kSpan * kCols * (int)sizeof(T);
-    if (by == 16) return launch_ranks<kRanks<T, 16>, rec_backward_kernel<T, 16>>(true, shared, p, stream);
+    if (n < kManyColumns && p.steps > kSplitSteps) return rec_split_backward<T>(p, by, stream);
+    if (by == 16) return n >= 2 * kManyColumns ? backward_v<T, 16, 2>(p, stream) : backward_v<T, 16, 1>(p, stream);
     if constexpr (sizeof(T) == 2)
-        if (by == 2) return launch_ranks<kRanks<T, 2>, rec_backward_kernel<T, 2>>(false, shared, p, stream);
-    return launch_ranks<kRanks<T, 4>, rec_backward_kernel<T, 4>>(false, shared, p, stream);
+        if (by == 2) return backward_v<T, 2, 1>(p, stream);
+    return backward_v<T, 4, 1>(p, stream);
 }
 
 bool rec_seq_ok(const RecSeq& s, int64_t batch, int64_t steps, int64_t channels, bool written)
@@ -754,7 +571,6 @@ adacomp_status adacomp_recurrence_forward(adacomp_recurrence_t h, int64_t batch,
     p.steps = steps;
     p.channels = h->channels;
     p.chunks = (steps + adacomp::kRecChunk - 1) / adacomp::kRecChunk;
-    p.blocks = (uint32_t)((h->channels + adacomp::kCols - 1) / adacomp::kCols);
     const cudaError_t err = h->dtype == ADACOMP_BF16 ? adacomp::forward<adacomp::bf16>(p, stream)
                                                      : adacomp::forward<float>(p, stream);
     return adacomp::launch_result(err, stream);
@@ -794,7 +610,6 @@ adacomp_status adacomp_recurrence_backward(adacomp_recurrence_t h, int64_t batch
     p.steps = steps;
     p.channels = h->channels;
     p.chunks = (steps + adacomp::kRecChunk - 1) / adacomp::kRecChunk;
-    p.blocks = (uint32_t)((h->channels + adacomp::kCols - 1) / adacomp::kCols);
     const cudaError_t err = h->dtype == ADACOMP_BF16 ? adacomp::backward<adacomp::bf16>(p, stream)
                                                      : adacomp::backward<float>(p, stream);
     return adacomp::launch_result(err, stream);

@@ -1,0 +1,591 @@
+// The recurrence where there are few columns: the steps split over warps, CTAs and clusters.
+#include <cmath>
+
+#include "recurrence.cuh"
+
+namespace adacomp {
+namespace {
+
+// A lane's two columns. (Two values per instruction, add.f32x2 and its like, need fewer
+// instructions here but have longer latencies, and the chains are what is waited for:
+// backward 88 us with them, 77 without, at 16 sequences of 2048 steps of 1024 bf16 channels.)
+struct Two {
+    float x, y;
+};
+__device__ __forceinline__ Two two_of(float x, float y) { return {x, y}; }
+__device__ __forceinline__ Two two_of(float x) { return {x, x}; }
+__device__ __forceinline__ Two operator*(Two a, Two b) { return {__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y)}; }
+__device__ __forceinline__ Two operator+(Two a, Two b) { return {__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)}; }
+__device__ __forceinline__ Two operator-(Two a, Two b) { return {__fsub_rn(a.x, b.x), __fsub_rn(a.y, b.y)}; }
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) { return {fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)}; }
+
+// ---------------------------------------------------------------- many steps
+// The steps are split: a warp has 64 columns (two per lane) and eight consecutive steps, a
+// CTA 64 steps, a cluster of up to 16 CTAs up to 1024, and where the sequence is longer the
+// cluster goes on in rounds. Each warp forms what its steps do to a state, h -> A h + H with
+// A the product of its gates. The warps exchange these through shared memory, and the CTAs
+// write theirs into every CTA of the cluster (one warp of each does); then each warp knows
+// the state before its first step and goes through its steps again, from registers. So every element
+// is read once, and no CTA waits for one that may not be running. The next round's elements
+// are copied to shared memory meanwhile.
+constexpr int kCols = 64, kSteps = 8, kWarps = 8, kThreads = 32 * kWarps, kSpan = kSteps * kWarps;
+constexpr int kTile = kSpan * kCols;  // elements of a tensor that a CTA has in a round
+static_assert(kRecChunk == kSpan, "a kept state for every CTA");
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Waits for the CTAs of the cluster without an order of memory: the results' stores need none.
+__device__ __forceinline__ void cluster_meet()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t shared_address(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ Two low(float4 v) { return two_of(v.x, v.y); }
+__device__ __forceinline__ Two high(float4 v) { return two_of(v.z, v.w); }
+
+__device__ __forceinline__ float4 quad(Two a, Two b) { return make_float4(a.x, a.y, b.x, b.y); }
+
+// What the CTAs of a cluster write to each other in a round: each CTA's values, and the
+// barrier that counts their bytes. Two of them take turns: a CTA that writes for the round
+// after next has all others' values of the next one, so that they have read these.
+// (A barrier of the whole cluster would have to wait for each round's stores of results.)
+template <int kRanks> struct Exchange {
+    float4 value[kRanks][32];
+    unsigned long long barrier;
+};
+
+// CTAs of a cluster at most. Sixteen halve the rounds of few and long sequences; but for rows
+// of bf16 by 16 bytes the exchange's memory would cost an SM one of its CTAs.
+template <typename T, int kBytes> constexpr int kRanks = sizeof(T) == 2 && kBytes == 16 ? 16 : 8;
+
+template <int R> __device__ __forceinline__ void exchange_init(Exchange<R>* x)
+{
+    if (threadIdx.x < 2)
+        asm volatile("mbarrier.init.shared.b64 [%0], 1;" ::"r"(shared_address(&x[threadIdx.x].barrier)) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+template <int R> __device__ __forceinline__ void exchange_expect(Exchange<R>* x, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(shared_address(&x->barrier)), "r"(bytes)
+                 : "memory");
+}
+
+// Writes v to the place of `p` in the CTA `rank`, and counts it at that CTA's barrier.
+template <int R> __device__ __forceinline__ void push(Exchange<R>* x, float4* p, uint32_t rank, float4 v)
+{
+    uint32_t a, b;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(shared_address(p)), "r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(shared_address(&x->barrier)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(b)
+                 : "memory");
+}
+
+// Waits for a barrier's phase. The CTAs of a cluster run together and each writes before it
+// waits, so the wait ends; were it not to, it is given up after some seconds.
+template <int R> __device__ __forceinline__ bool exchange_wait(Exchange<R>* x, uint32_t phase)
+{
+    for (uint32_t i = 0; i < (1u << 22); ++i) {
+        uint32_t done;
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+            : "=r"(done)
+            : "r"(shared_address(&x->barrier)), "r"(phase)
+            : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+
+// The columns of a tile. Where a sequence's rows are read 16 bytes at a time (kBytes), a
+// tile is 64 channels of one sequence; otherwise the channels of all sequences are numbered
+// through, so that few channels fill a tile too.
+template <int kBytes> struct Column {
+    int64_t b, c;
+    int32_t len;  // of its sequence; 0 past the last column
+    bool on;
+
+    __device__ __forceinline__ Column(const RecArgs& p, uint32_t tile, int j)
+    {
+        if (kBytes == 16) {
+            const uint32_t blocks = (uint32_t)((p.channels + kCols - 1) / kCols);
+            b = tile / blocks;
+            c = (int64_t)(tile - (uint32_t)b * blocks) * kCols + j;
+            on = c < p.channels;
+        } else {
+            const int64_t i = (int64_t)tile * kCols + j;
+            on = i < p.batch * p.channels;
+            b = on ? i / p.channels : 0;
+            c = on ? i - b * p.channels : 0;
+        }
+        len = on ? (int32_t)length_of(p, b) : 0;
+    }
+    __device__ __forceinline__ int64_t state(const RecArgs& p) const { return b * p.channels + c; }
+};
+
+// Copies a CTA's 64 steps of a tile to shared memory, [step][column], kBytes at a time:
+// every thread has one place in the rows and takes every kStride-th of them. What lies past
+// a sequence's length or the last channel is not read, and what stands there not used.
+template <typename T, int kBytes, int kTensors> struct Copier {
+    static constexpr int kPlaces = kCols * (int)sizeof(T) / kBytes;
+    static constexpr int kStride = kThreads / kPlaces;
+    static constexpr int kEach = kBytes / (int)sizeof(T);  // elements at a time
+    const T* from[kTensors];
+    Distance<kBytes> step[kTensors];
+    int32_t len;
+    uint32_t bytes;
+
+    __device__ __forceinline__ Copier(const RecArgs& p, uint32_t tile, const RecSeq* const (&s)[kTensors])
+    {
+        const Column<kBytes> col(p, tile, (threadIdx.x % kPlaces) * kEach);
+        const int64_t rest = (p.channels - col.c) * (int)sizeof(T);
+        bytes = !col.on ? 0u : rest < kBytes ? (uint32_t)rest : (uint32_t)kBytes;
+        len = bytes == 0 ? 0 : col.len;
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i) {
+            from[i] = at<const T>(*s[i], col.b, 0, col.c);
+            step[i] = (Distance<kBytes>)(s[i]->step * (int)sizeof(T));
+        }
+    }
+
+    __device__ __forceinline__ void copy(T* to, int32_t t0) const
+    {
+        const int row0 = threadIdx.x / kPlaces, left = len - t0;
+        T* const place = to + row0 * kCols + (threadIdx.x % kPlaces) * kEach;
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i) {
+            const T* const f = moved(from[i], (int64_t)(t0 + row0) * step[i]);
+            T v[kSpan / kStride];
+#pragma unroll
+            for (int k = 0; k < kSpan / kStride; ++k)
+                if (row0 + k * kStride < left) {
+                    const T* const g = moved(f, (Distance<kBytes>)(k * kStride) * step[i]);
+                    const uint32_t d = shared_address(place + i * kTile + k * kStride * kCols);
+                    if constexpr (kBytes == 2) v[k] = *g;
+                    else if constexpr (kBytes == 16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(g), "r"(bytes) : "memory");
+                    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(g) : "memory");
+                }
+            if constexpr (kBytes == 2) {
+#pragma unroll
+                for (int k = 0; k < kSpan / kStride; ++k)
+                    if (row0 + k * kStride < left) place[i * kTile + k * kStride * kCols] = v[k];
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+};
+
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void two(const float* p, float& x, float& y)
+{
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x = v.x, y = v.y;
+}
+
+__device__ __forceinline__ void two(const bf16* p, float& x, float& y)
+{
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    x = bf16_low(v), y = bf16_high(v);
+}
+
+// Where a lane's two columns of a warp's steps go.
+template <typename T, int kBytes> struct Writer {
+    T* p[2];
+    Distance<kBytes> step;
+
+    __device__ __forceinline__ Writer(const RecSeq& s, const Column<kBytes> (&col)[2], int64_t t)
+        : step((Distance<kBytes>)(s.step * (int)sizeof(T)))
+    {
+        p[0] = at<T>(s, col[0].b, t, col[0].c);
+        if (kBytes != 16) p[1] = at<T>(s, col[1].b, t, col[1].c);
+    }
+    // step k of both columns, which are there
+    __device__ __forceinline__ void put(int k, Two v) const
+    {
+        T* const q = moved(p[0], k * step);
+        if constexpr (kBytes == 16) {
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(q) = make_float2(v.x, v.y);
+            else *reinterpret_cast<__nv_bfloat162*>(q) = __floats2bfloat162_rn(v.x, v.y);
+        } else {
+            *q = from_f32<T>(v.x);
+            *moved(p[1], k * step) = from_f32<T>(v.y);
+        }
+    }
+    __device__ __forceinline__ void put(int k, float x, float y, bool on0, bool on1) const
+    {
+        T* const q = moved(p[0], k * step);
+        if (on0) *q = from_f32<T>(x);
+        if (on1) *(kBytes == 16 ? q + 1 : moved(p[1], k * step)) = from_f32<T>(y);
+    }
+};
+
+// What a warp has to mind in a round: how many of its steps lie within each column's length
+// and within the tensors, and whether all do.
+struct Live {
+    int live0, live1, whole;
+    bool all;
+
+    template <int kBytes>
+    __device__ __forceinline__ Live(const RecArgs& p, const Column<kBytes> (&col)[2], int32_t ts)
+        : live0(max(0, min(kSteps, col[0].len - ts))), live1(max(0, min(kSteps, col[1].len - ts))),
+          whole(max(0, min(kSteps, (int32_t)p.steps - ts))),
+          all(__all_sync(0xffffffffu, live0 == kSteps && live1 == kSteps))
+    {
+    }
+};
+
+template <int kBytes>
+__device__ __forceinline__ Two load_state(const float* p, const RecArgs& a, const Column<kBytes> (&col)[2], int64_t more = 0)
+{
+    float v[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (p && col[j].on) v[j] = p[col[j].state(a) + more];
+    return two_of(v[0], v[1]);
+}
+
+template <int kBytes>
+__device__ __forceinline__ void store_state(float* p, const RecArgs& a, const Column<kBytes> (&col)[2], Two s)
+{
+    if (p && col[0].on) p[col[0].state(a)] = s.x;
+    if (p && col[1].on) p[col[1].state(a)] = s.y;
+}
+
+// The address of a column's kept state: [batch][chunks][channels].
+template <int kBytes> __device__ __forceinline__ float* kept(const RecArgs& p, const Column<kBytes>& col, int32_t t)
+{
+    return p.carry + (col.b * p.chunks + t / kRecChunk) * p.channels + col.c;
+}
+
+template <typename T, int kBytes>
+__global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
+{
+    extern __shared__ __align__(16) uint8_t shared_bytes[];
+    __shared__ float4 part[kWarps][32];   // a warp's (A, H) of the lane's columns
+    __shared__ Two begin[kWarps][32];  // the state before its first step
+    __shared__ Exchange<kRanks<T, kBytes>> exchange[2];
+    const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (2 * kTile); };
+    ptx::griddep_wait();
+    if (ranks > 1) {
+        exchange_init(exchange);
+        cluster_sync();  // all CTAs run, and their barriers are there, before one writes to another
+    }
+    const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Column<kBytes> col[2] = {Column<kBytes>(p, tile, 2 * lane), Column<kBytes>(p, tile, 2 * lane + 1)};
+    const Copier<T, kBytes, 2> copier(p, tile, {&p.z, &p.x});
+    const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
+    Two h0 = load_state(p.h0, p, col);  // before the round's first step (the joining warp's)
+    bool given_up = false;
+    int32_t tc = (int32_t)rank * kSpan;
+    copier.copy(tile_of(0), tc);
+    for (int32_t t0 = 0, round = 0; t0 < steps; t0 += span, tc += span, ++round) {
+        const int par = round & 1;
+        copies_wait();
+        __syncthreads();
+        if (t0 + span < steps) copier.copy(tile_of(par ^ 1), tc + span);
+        const int32_t ts = tc + warp * kSteps;
+        const Live at_hand(p, col, ts);
+        const T* z = tile_of(par) + warp * kSteps * kCols + 2 * lane;
+        Two a[kSteps], u[kSteps], A = two_of(1.0f), H = two_of(0.0f);
+        const auto form = [&](auto masked) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                float z0, z1, x0, x1, a0, a1, b0, b1;
+                two(z + k * kCols, z0, z1);
+                two(z + k * kCols + kTile, x0, x1);
+                gate(z0, &a0, &b0);
+                gate(z1, &a1, &b1);
+                if (masked.value) {  // past the length the state stays as it is
+                    if (k >= at_hand.live0) a0 = 1.0f, b0 = x0 = 0.0f;
+                    if (k >= at_hand.live1) a1 = 1.0f, b1 = x1 = 0.0f;
+                }
+                a[k] = two_of(a0, a1);
+                u[k] = two_of(b0, b1) * two_of(x0, x1);
+                H = fma2(a[k], H, u[k]);
+                A = A * a[k];
+            }
+        };
+        if (at_hand.all) form(std::false_type());
+        else form(std::true_type());
+        part[warp][lane] = quad(A, H);
+        __syncthreads();
+        if (warp == 0) {
+            Two h = h0;  // before the CTA's first step
+            if (ranks > 1) {
+                Exchange<kRanks<T, kBytes>>& x = exchange[par];
+                if (lane == 0) exchange_expect(&x, ranks * 512);
+                Two tA = two_of(1.0f), tH = two_of(0.0f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 q = part[w][lane];
+                    tH = fma2(low(q), tH, high(q));
+                    tA = tA * low(q);
+                }
+                for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tH));
+                if (!given_up) given_up = !exchange_wait(&x, (round >> 1) & 1);
+                for (uint32_t r = 0; r < ranks; ++r) {
+                    if (r == rank) h = h0;
+                    const float4 q = x.value[r][lane];
+                    h0 = fma2(low(q), h0, high(q));
+                }
+                if (given_up) h = h0 = two_of(NAN);
+            }
+            if (p.carry && tc < steps) {
+                const Two v = h;
+                if (col[0].on) *kept(p, col[0], tc) = v.x;
+                if (col[1].on) *kept(p, col[1], tc) = v.y;
+            }
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                begin[w][lane] = h;
+                const float4 q = part[w][lane];
+                h = fma2(low(q), h, high(q));
+            }
+            if (ranks == 1) h0 = h;
+        }
+        __syncthreads();
+        Two h = begin[warp][lane];
+        const Writer<T, kBytes> y(p.y, col, ts);
+        if (at_hand.all) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                h = fma2(a[k], h, u[k]);
+                y.put(k, h);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                h = fma2(a[k], h, u[k]);
+                const Two v = h;
+                if (k < at_hand.whole)
+                    y.put(k, k < at_hand.live0 ? v.x : 0.0f, k < at_hand.live1 ? v.y : 0.0f, col[0].on, col[1].on);
+            }
+        }
+    }
+    if (rank == 0 && warp == 0) store_state(p.h_last, p, col, h0);
+    if (ranks > 1) cluster_meet();  // no CTA ends while another may write to it
+}
+
+// The reverse of it: p, the gradient that reaches a state from the steps after it, goes
+// through a warp's steps as p -> A p + P, P = sum of dy_k times the gates up to and with
+// step k. The states are formed again from the one that the forward pass kept for the CTA's
+// steps: that is less to read than y, and not rounded.
+template <typename T, int kBytes>
+__global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
+{
+    extern __shared__ __align__(16) uint8_t shared_bytes[];
+    __shared__ float4 part[kWarps][32];  // a warp's (A, H)
+    __shared__ Two grad[kWarps][32];  // its P
+    __shared__ float4 begin[32];         // the state before the CTA's first step, and p after its last
+    __shared__ Exchange<kRanks<T, kBytes>> exchange[2];
+    const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (3 * kTile); };
+    ptx::griddep_wait();
+    if (ranks > 1) {
+        exchange_init(exchange);
+        cluster_sync();  // all CTAs run, and their barriers are there, before one writes to another
+    }
+    const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Column<kBytes> col[2] = {Column<kBytes>(p, tile, 2 * lane), Column<kBytes>(p, tile, 2 * lane + 1)};
+    const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
+    int32_t t0 = steps > 0 ? (steps - 1) / span * span : -1, tc = t0 + (int32_t)rank * kSpan;
+    const Copier<T, kBytes, 3> copier(p, tile, {&p.z, &p.x, &p.dy});
+    Two p0 = load_state(p.dh_last, p, col);  // after the round's last step (the joining warp's)
+    bool given_up = false;
+    if (t0 >= 0) copier.copy(tile_of(0), tc);
+    for (int32_t round = 0; t0 >= 0; t0 -= span, tc -= span, ++round) {
+        const int par = round & 1;
+        Two h = two_of(0.0f);  // before the CTA's first step
+        if (warp == kWarps - 1 && tc < steps)
+            h = two_of(col[0].on ? *kept(p, col[0], tc) : 0.0f, col[1].on ? *kept(p, col[1], tc) : 0.0f);
+        copies_wait();
+        __syncthreads();
+        if (t0 > 0) copier.copy(tile_of(par ^ 1), tc - span);
+        const int32_t ts = tc + warp * kSteps;
+        const Live at_hand(p, col, ts);
+        const T* z = tile_of(par) + warp * kSteps * kCols + 2 * lane;
+        Two a[kSteps], b[kSteps], A = two_of(1.0f), H = two_of(0.0f), P = two_of(0.0f);
+        const auto inputs = [&](auto masked, int tensor, int k) {  // x or dy
+            float v0, v1;
+            two(z + k * kCols + tensor * kTile, v0, v1);
+            if (masked.value) {
+                if (k >= at_hand.live0) v0 = 0.0f;
+                if (k >= at_hand.live1) v1 = 0.0f;
+            }
+            return two_of(v0, v1);
+        };
+        const auto form = [&](auto masked) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                float z0, z1, a0, a1, b0, b1;
+                two(z + k * kCols, z0, z1);
+                gate(z0, &a0, &b0);
+                gate(z1, &a1, &b1);
+                if (masked.value) {
+                    if (k >= at_hand.live0) a0 = 1.0f, b0 = 0.0f;
+                    if (k >= at_hand.live1) a1 = 1.0f, b1 = 0.0f;
+                }
+                a[k] = two_of(a0, a1);
+                b[k] = two_of(b0, b1);
+                H = fma2(a[k], H, b[k] * inputs(masked, 1, k));
+                A = A * a[k];
+                P = fma2(A, inputs(masked, 2, k), P);
+            }
+        };
+        if (at_hand.all) form(std::false_type());
+        else form(std::true_type());
+        part[warp][lane] = quad(A, H);
+        grad[warp][lane] = P;
+        __syncthreads();
+        A = two_of(1.0f), H = two_of(0.0f);  // from the CTA's first step to the warp's
+        for (int w = 0; w < warp; ++w) {
+            const float4 v = part[w][lane];
+            H = fma2(low(v), H, high(v));
+            A = A * low(v);
+        }
+        Two B = two_of(1.0f);  // and from the CTA's end back to the warp's
+        P = two_of(0.0f);
+        for (int w = kWarps - 1; w > warp; --w) {
+            const Two v = low(part[w][lane]);
+            P = fma2(v, P, grad[w][lane]);
+            B = B * v;
+        }
+        if (warp == kWarps - 1) {
+            const float4 own = part[warp][lane];
+            const Two tA = A * low(own);
+            Two tP = two_of(0.0f), q = p0;  // q: after the CTA's last step
+#pragma unroll
+            for (int w = kWarps - 1; w >= 0; --w)
+                tP = fma2(low(part[w][lane]), tP, grad[w][lane]);
+            if (ranks > 1) {
+                Exchange<kRanks<T, kBytes>>& x = exchange[par];
+                if (lane == 0) exchange_expect(&x, ranks * 512);
+                for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tP));
+                if (!given_up) given_up = !exchange_wait(&x, (round >> 1) & 1);
+                for (uint32_t r = ranks; r-- > 0;) {
+                    if (r == rank) q = p0;
+                    const float4 v = x.value[r][lane];
+                    p0 = fma2(low(v), p0, high(v));
+                }
+                if (given_up) h = q = p0 = two_of(NAN);
+            } else {
+                p0 = fma2(tA, p0, tP);
+            }
+            begin[lane] = quad(h, q);
+        }
+        __syncthreads();
+        h = fma2(A, low(begin[lane]), H);
+        Two q = fma2(B, high(begin[lane]), P);
+        const Writer<T, kBytes> dz(p.dz, col, ts), dx(p.dx, col, ts);
+        const auto finish = [&](auto masked) {
+            Two before[kSteps];
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                const Two x = inputs(masked, 1, k);
+                before[k] = h - x;  // h_{t-1} - x_t
+                h = fma2(a[k], h, b[k] * x);
+            }
+#pragma unroll
+            for (int k = kSteps - 1; k >= 0; --k) {
+                const Two G = q + inputs(masked, 2, k), g = b[k] * G;
+                q = a[k] * G;
+                const Two v = a[k] * g * before[k];
+                if (!masked.value) {
+                    dx.put(k, g);
+                    dz.put(k, v);
+                } else if (k < at_hand.whole) {
+                    const Two e = g, f = v;
+                    const bool l0 = k < at_hand.live0, l1 = k < at_hand.live1;
+                    dx.put(k, l0 ? e.x : 0.0f, l1 ? e.y : 0.0f, col[0].on, col[1].on);
+                    dz.put(k, l0 ? f.x : 0.0f, l1 ? f.y : 0.0f, col[0].on, col[1].on);
+                }
+            }
+        };
+        if (at_hand.all) finish(std::false_type());
+        else finish(std::true_type());
+    }
+    if (rank == 0 && warp == kWarps - 1) store_state(p.dh0, p, col, p0);
+    if (ranks > 1) cluster_meet();  // no CTA ends while another may write to it
+}
+
+// Launches a kernel of clusters, behind the kernel ahead of it as launch_after does.
+template <int kRanks, void (*kern)(RecArgs, uint32_t)>
+cudaError_t launch_ranks(bool rows16, int shared, const RecArgs& p, cudaStream_t stream)
+{
+    static bool set[64] = {};  // the kernel's shared memory, once per device
+
+    uint32_t ranks = 1;
+    const int64_t tiles = rows16 ? p.batch * ((p.channels + kCols - 1) / kCols) : (p.batch * p.channels + kCols - 1) / kCols;
+    // a CTA more in a cluster is worth its exchange where the GPU is not full without it; more
+    // than eight where all clusters still run at once
+    const uint32_t most = tiles <= 19 ? (uint32_t)kRanks : 8;
+    while (ranks < most && (int64_t)ranks * kSpan < p.steps && tiles * ranks < 1024) ranks *= 2;
+    if (tiles > 0x7fffffff / (int64_t)ranks) return cudaErrorInvalidConfiguration;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+    if (e == cudaSuccess && !set[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+        if (e == cudaSuccess && kRanks > 8)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        set[dev] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * ranks));
+    cfg.blockDim = dim3((unsigned)kThreads);
+    cfg.dynamicSmemBytes = (size_t)shared;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p, ranks);
+}
+
+}  // namespace
+
+template <typename T> cudaError_t rec_split_forward(const RecArgs& p, int by, cudaStream_t stream)
+{
+    constexpr int shared = 4 * kSpan * kCols * (int)sizeof(T);
+    if (by == 16) return launch_ranks<kRanks<T, 16>, rec_forward_kernel<T, 16>>(true, shared, p, stream);
+    if constexpr (sizeof(T) == 2)
+        if (by == 2) return launch_ranks<kRanks<T, 2>, rec_forward_kernel<T, 2>>(false, shared, p, stream);
+    return launch_ranks<kRanks<T, 4>, rec_forward_kernel<T, 4>>(false, shared, p, stream);
+}
+
+template <typename T> cudaError_t rec_split_backward(const RecArgs& p, int by, cudaStream_t stream)
+{
+    constexpr int shared = 6 * kSpan * kCols * (int)sizeof(T);
+    if (by == 16) return launch_ranks<kRanks<T, 16>, rec_backward_kernel<T, 16>>(true, shared, p, stream);
+    if constexpr (sizeof(T) == 2)
+        if (by == 2) return launch_ranks<kRanks<T, 2>, rec_backward_kernel<T, 2>>(false, shared, p, stream);
+    return launch_ranks<kRanks<T, 4>, rec_backward_kernel<T, 4>>(false, shared, p, stream);
+}
+
+template cudaError_t rec_split_forward<float>(const RecArgs&, int, cudaStream_t);
+template cudaError_t rec_split_forward<bf16>(const RecArgs&, int, cudaStream_t);
+template cudaError_t rec_split_backward<float>(const RecArgs&, int, cudaStream_t);
+template cudaError_t rec_split_backward<bf16>(const RecArgs&, int, cudaStream_t);
+
+}  // namespace adacomp

@@ -89,7 +89,7 @@ def test_recurrence_calls_refuse_before_launch():
     h = ac.adacomp_recurrence_init(6, ac.F32)
     L = ac.lib()
     assert ac.adacomp_recurrence_carry_bytes(h, 3, 0) == 0
-    assert ac.adacomp_recurrence_carry_bytes(h, 3, 129) == 3 * 2 * 6 * 4
+    assert ac.adacomp_recurrence_carry_bytes(h, 3, 129) == 3 * 3 * 6 * 4
     good = [h.ptr, 2, 5, A, 30, 6, A, 30, 6, A, A, A, 30, 6, A, A, None]
 
     def forward(**change):
