@@ -28,6 +28,11 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) { return {fmaf(a.x, b.x
 // the state before its first step and goes through its steps again, from registers. So every element
 // is read once, and no CTA waits for one that may not be running. The next round's elements
 // are copied to shared memory meanwhile.
+//
+// Bound by the rounds' latency (some 3 us each: the gates, one exchange, the results), as a
+// few columns leave an SM one or two CTAs. Measured: one sequence of 32768 steps of 1024 bf16
+// channels 87 us forward (2.3 TB/s), 131 backward (2.6); four ragged ones of up to 20011 steps
+// of 501 fp32 channels 155 and 268.
 constexpr int kCols = 64, kSteps = 8, kWarps = 8, kThreads = 32 * kWarps, kSpan = kSteps * kWarps;
 constexpr int kTile = kSpan * kCols;  // elements of a tensor that a CTA has in a round
 static_assert(kRecChunk == kSpan, "a kept state for every CTA");
