@@ -14,11 +14,11 @@ struct adacomp_layer_norm {
 namespace adacomp {
 namespace {
 
-constexpr int kLnThreads = 256;   // forward pass, and rows that are too wide for registers
-constexpr int kLnBack = 512;      // backward pass
+constexpr int kLnThreads = 256;   // rows that are too wide for the registers of a CTA's turn
+constexpr int kLnBack = 512;      // the others
 constexpr int kLnParts = 304;     // CTAs of a backward pass at most, each with partial sums of dw and db
-constexpr int kLnBackCols = 16;   // columns of a thread there
-constexpr int64_t kLnBackDim = (int64_t)kLnBack * kLnBackCols;
+constexpr int kLnCols = 16;       // columns of a thread there, at most
+constexpr int64_t kLnDim = (int64_t)kLnBack * kLnCols;
 constexpr int kLnWideSlices = 128;
 
 struct LnArgs {
@@ -33,10 +33,13 @@ struct LnArgs {
     float eps;
 };
 
-// N consecutive elements as they lie in memory: 16, 4 or 2 bytes, as the rows' alignment allows.
+// N consecutive elements as they lie in memory: 16, 8, 4 or 2 bytes, as the rows' alignment allows.
 template <int kBytes> struct RawOf;
 template <> struct RawOf<16> {
     using type = uint4;
+};
+template <> struct RawOf<8> {
+    using type = uint2;
 };
 template <> struct RawOf<4> {
     using type = uint32_t;
@@ -57,6 +60,8 @@ template <typename X, int N> struct Piece {
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
             if constexpr (sizeof(X) == 4) return __uint_as_float(w[j]);
             else return j & 1 ? bf16_high(w[j / 2]) : bf16_low(w[j / 2]);
+        } else if constexpr (kBytes == 8) {
+            return j & 1 ? bf16_high(j < 2 ? q.x : q.y) : bf16_low(j < 2 ? q.x : q.y);
         } else if constexpr (sizeof(X) == 4) {
             return __uint_as_float(q);
         } else {
@@ -83,6 +88,10 @@ template <int N> __device__ __forceinline__ void put_piece(bf16* p, const float 
         *p = from_f32<bf16>(v[0]);
     } else if constexpr (N == 2) {
         *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v[0], v[1]);
+    } else if constexpr (N == 4) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(p) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     } else {
         uint32_t w[4];
 #pragma unroll
@@ -130,32 +139,251 @@ __device__ __forceinline__ float group_sum(float v, int group)
     return v;
 }
 
+__device__ __forceinline__ void group_barrier(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// How many rows of kTensors tensors a thread has on their way, and the shared memory for them.
+template <typename X, int N, int kTensors> struct LnRing {
+    // pieces of two bytes cannot be copied so: half the columns, and one row ahead in registers
+    static constexpr bool kRing = Piece<X, N>::kBytes >= 4;
+    static constexpr int kCols = kRing ? kLnCols : kLnCols / 2;
+    static constexpr int kRow = (kCols / N) * kTensors * kLnBack * Piece<X, N>::kBytes;
+    static constexpr int kStages = sizeof(X) == 2 ? 6 : 3;
+    static constexpr int kBytes = kRing ? kStages * kRow : 0;
+};
+
+template <int kBytes> __device__ __forceinline__ void copy_piece(void* to, const void* from)
+{
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(from) : "memory");
+}
+
 // ---------------------------------------------------------------- forward
-// Bound by memory. A row is read once, to registers, as it lies in memory (N elements at a
-// time, kCols per thread at most); the mean and then the sum of squared deviations are
-// formed from there. A row is a group of 1 to 32 lanes, so that there is no barrier, or,
-// where it is wider than 32 * 64 elements, a CTA. The weights come from L1 or L2 for every row.
-template <typename X, typename W, int N, int kCols, bool kWide>
-__global__ void __launch_bounds__(kLnThreads, kCols == 64 && N > 2 ? 3 : 1) ln_forward_kernel(const LnArgs a)
+// Bound by memory. A group of threads (1 to 512, a power of two) has a row, 16 columns per
+// thread at most, and goes from row to row, so that its weights stay in registers (read for
+// every row they filled L1's throughput: 16384 rows of 2048 bf16 33 us). The rows to come are
+// copied to shared memory ahead, every thread its own pieces, so that there is no barrier but
+// the group's two, of the mean and of the squared deviations, where it is more than a warp.
+template <typename X, typename W, int N>
+__global__ void __launch_bounds__(kLnBack, 1) ln_forward_kernel(const LnArgs a)
+{
+    using Ring = LnRing<X, N, 1>;
+    constexpr int kCols = Ring::kCols, kPieces = kCols / N, kPairs = kCols / 2;
+    constexpr int kBytes = Piece<X, N>::kBytes, kStages = Ring::kStages;
+    constexpr bool kRing = Ring::kRing;
+    using Raw = typename Piece<X, N>::Raw;
+    extern __shared__ __align__(16) uint8_t shared_bytes[];
+    __shared__ float sums[2][kLnBack / 32];
+    ptx::griddep_wait();
+    const int group = a.group, place = threadIdx.x & (group - 1), dim = (int)a.dim;
+    const int groups = kLnBack / group, which = threadIdx.x / group;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float inv_n = 1.0f / (float)dim;
+    const X* x = static_cast<const X*>(a.x);
+    X* y = static_cast<X*>(a.y);
+    Pair w[kPairs], b[kPairs];
+    {
+        float v[kCols] = {}, u[kCols] = {};
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const int c = (k * group + place) * N;
+            if (c < dim) {
+                weights<N>(static_cast<const W*>(a.w) + c, *reinterpret_cast<float(*)[N]>(v + k * N));
+                if (a.b) weights<N>(static_cast<const W*>(a.b) + c, *reinterpret_cast<float(*)[N]>(u + k * N));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            w[i] = pair(v[2 * i], v[2 * i + 1]);
+            b[i] = pair(u[2 * i], u[2 * i + 1]);
+        }
+    }
+    const auto there = [&](int k) { return (k * group + place) * N < dim ? 1.0f : 0.0f; };  // a piece of the row
+    const auto slot = [&](int stage, int k) {
+        return reinterpret_cast<Raw*>(shared_bytes) + (stage * kPieces + k) * kLnBack + threadIdx.x;
+    };
+    const auto stage_row = [&](int64_t r, int stage) {
+        if constexpr (kRing) {
+            if (r < a.rows) {
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k) {
+                    const int c = (k * group + place) * N;
+                    if (c < dim) copy_piece<kBytes>(slot(stage, k), x + r * a.x_stride + c);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+    const int64_t stride = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + which;
+    Piece<X, N> p[kPieces], next[kPieces];
+    const auto load_next = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const int c = (k * group + place) * N;
+            next[k].zero();
+            if (r < a.rows && c < dim) next[k].load(x + r * a.x_stride + c);
+        }
+    };
+    if (kRing) {
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) stage_row(row + i * stride, i);
+    } else {
+        load_next(row);
+    }
+    // the sum over the row's group
+    const auto sum = [&](float v, int turn) {
+        v = group_sum(v, group < 32 ? group : 32);
+        if (group > 32) {
+            if (lane == 0) sums[turn][warp] = v;
+            group_barrier(1 + which, group);
+            const int first = which * (group >> 5);
+            v = 0.0f;
+            for (int i = 0; i < group >> 5; ++i) v += sums[turn][first + i];
+        }
+        return v;
+    };
+    // every lane of a warp takes part as long as the warp's first group has a row
+    const int64_t lead = (int64_t)blockIdx.x * groups + (group < 32 ? warp * (32 / group) : which);
+    int stage = 0;
+    for (int64_t at = lead; at < a.rows; at += stride, row += stride) {
+        const bool on = row < a.rows;
+        if (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            if (kRing) {
+                p[k].zero();
+                if (on && (k * group + place) * N < dim) p[k].q = *slot(stage, k);
+            } else {
+                p[k] = next[k];
+            }
+        }
+        if (kRing) {
+            stage_row(row + kStages * stride, stage);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+        } else {
+            load_next(row + stride);
+        }
+        Pair d[kPairs], t = pair(0.0f);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            d[i] = pair_of(p, i);
+            t = t + d[i];
+        }
+        const float mean = sum(both(t), 0) * inv_n;
+        t = pair(0.0f);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            d[i] = d[i] + pair(-mean);
+            const Pair e = d[i] * pair(there(2 * i / N), there((2 * i + 1) / N));
+            t = fma2(e, e, t);
+        }
+        const float rstd = 1.0f / sqrtf(sum(both(t), 1) * inv_n + a.eps);
+        if (!on) continue;
+        float v[kCols];
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) split(fma2(d[i] * pair(rstd), w[i], b[i]), v[2 * i], v[2 * i + 1]);
+        X* const to = y + row * a.y_stride;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const int c = (k * group + place) * N;
+            if (c < dim) put_piece<N>(to + c, *reinterpret_cast<const float(*)[N]>(v + k * N));
+        }
+        if (place == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+    }
+}
+
+constexpr int kLnWarpThreads = 128;
+
+// Rows of 129 to 2048 elements that are aligned to 16 bytes: a warp per row, which it holds in
+// registers as it lies in memory, without a barrier. The weights come from L1 for every row, so
+// a lane's pieces are as long as four weights, which keeps its 16-byte loads of them side by
+// side (eight bf16 elements with fp32 weights: 33 us at 16384 rows of 2048, bound by L1).
+template <typename X, typename W, int N, int kCols>
+__global__ void __launch_bounds__(kLnWarpThreads, kCols == 64 ? 6 : 8) ln_forward_warp_kernel(const LnArgs a)
 {
     constexpr int kPieces = kCols / N;
+    ptx::griddep_wait();
+    ptx::griddep_launch();  // the next kernel's launch is under way while this one's last rows are
+    constexpr int group = 32;
+    const int place = threadIdx.x & 31, dim = (int)a.dim;
+    const int64_t row = (int64_t)blockIdx.x * (kLnWarpThreads / 32) + threadIdx.x / 32;
+    if (row >= a.rows) return;
+    const X* x = static_cast<const X*>(a.x) + row * a.x_stride;
+    Piece<X, N> r[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        const int c = (k * group + place) * N;
+        r[k].zero();
+        if (c < dim) r[k].load(x + c);
+    }
+    Pair s[2] = {pair(0.0f), pair(0.0f)};
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) s[i & 1] = s[i & 1] + pair_of(r, i);
+    const float mean = warp_sum(both(s[0] + s[1])) / (float)dim;
+    const Pair minus = pair(-mean);
+    s[0] = s[1] = pair(0.0f);
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+        if ((k * group + place) * N < dim) {
+#pragma unroll
+            for (int i = k * N / 2; i < (k + 1) * N / 2; ++i) {
+                const Pair d = pair_of(r, i) + minus;
+                s[i & 1] = fma2(d, d, s[i & 1]);
+            }
+        }
+    const float rstd = 1.0f / sqrtf(warp_sum(both(s[0] + s[1])) / (float)dim + a.eps);
+    const W* w = static_cast<const W*>(a.w);
+    const W* b = static_cast<const W*>(a.b);
+    X* y = static_cast<X*>(a.y) + row * a.y_stride;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        const int c = (k * group + place) * N;
+        if (c < dim) {
+            float wv[N], bv[N] = {}, v[N];
+            weights<N>(w + c, wv);
+            if (b) weights<N>(b + c, bv);
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                const Pair d = (pair_of(r, (k * N + j) / 2) + minus) * pair(rstd);
+                split(fma2(d, pair(wv[j], wv[j + 1]), pair(bv[j], bv[j + 1])), v[j], v[j + 1]);
+            }
+            put_piece<N>(y + c, v);
+        }
+    }
+    if (place == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+}
+
+// Wider rows, of up to 16384 elements: a CTA per row, which it holds in registers as it lies
+// in memory; the weights come from L2 for every row.
+template <typename X, typename W, int N>
+__global__ void __launch_bounds__(kLnThreads) ln_forward_wide_kernel(const LnArgs a)
+{
+    constexpr int kCols = 64, kPieces = kCols / N;
     __shared__ float shared[2][kLnThreads / 32];
     ptx::griddep_wait();
-    const int group = kWide ? kLnThreads : a.group;
-    const int place = threadIdx.x & (group - 1);
-    const int64_t row = kWide ? blockIdx.x : (int64_t)blockIdx.x * (kLnThreads / group) + threadIdx.x / group;
-    const bool on = row < a.rows;
-    const X* x = static_cast<const X*>(a.x) + (on ? row : 0) * a.x_stride;
+    constexpr int group = kLnThreads;
+    const int place = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const X* x = static_cast<const X*>(a.x) + row * a.x_stride;
     const int dim = (int)a.dim;
     const auto sum = [&](float v, int turn) {
-        v = group_sum(v, kWide ? 32 : group);
-        if (kWide) {
-            if ((threadIdx.x & 31) == 0) shared[turn][threadIdx.x >> 5] = v;
-            __syncthreads();
-            v = 0.0f;
+        v = warp_sum(v);
+        if ((threadIdx.x & 31) == 0) shared[turn][threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kLnThreads / 32; ++i) v += shared[turn][i];
-        }
+        for (int i = 0; i < kLnThreads / 32; ++i) v += shared[turn][i];
         return v;
     };
     Piece<X, N> r[kPieces];
@@ -163,7 +391,7 @@ __global__ void __launch_bounds__(kLnThreads, kCols == 64 && N > 2 ? 3 : 1) ln_f
     for (int k = 0; k < kPieces; ++k) {
         const int c = (k * group + place) * N;
         r[k].zero();
-        if (on && c < dim) r[k].load(x + c);
+        if (c < dim) r[k].load(x + c);
     }
     Pair s[2] = {pair(0.0f), pair(0.0f)};
 #pragma unroll
@@ -186,7 +414,6 @@ __global__ void __launch_bounds__(kLnThreads, kCols == 64 && N > 2 ? 3 : 1) ln_f
             }
         }
     const float rstd = 1.0f / sqrtf(sum(both(s[0] + s[1]), 1) / (float)dim + a.eps);
-    if (!on) return;
     const W* w = static_cast<const W*>(a.w);
     const W* b = static_cast<const W*>(a.b);
     X* y = static_cast<X*>(a.y) + row * a.y_stride;
@@ -259,33 +486,13 @@ template <typename X, typename W> __global__ void __launch_bounds__(kLnThreads) 
 // pieces of single elements are loaded one row ahead. The two sums of a row need one
 // barrier of the group where it is more than a warp. At the end the CTA's groups add their
 // column sums in order, and a second kernel adds the CTAs'.
-__device__ __forceinline__ void group_barrier(int id, int threads)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// How many rows a thread has on their way, and the shared memory for them.
-template <typename X, int N> struct LnRing {
-    static constexpr int kRow = (kLnBackCols / N) * 2 * kLnBack * Piece<X, N>::kBytes;
-    static constexpr int kStages = sizeof(X) == 2 ? 6 : 3;
-    static constexpr int kSums = 2 * (int)kLnBackDim * 4;
-    static constexpr int kShared = Piece<X, N>::kBytes >= 4 && kStages * kRow > kSums ? kStages * kRow : kSums;
-};
-
-template <int kBytes> __device__ __forceinline__ void copy_piece(void* to, const void* from)
-{
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(from) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(from) : "memory");
-}
-
 template <typename X, typename W, int N>
 __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
 {
-    constexpr int kPieces = kLnBackCols / N;
-    constexpr int kBytes = Piece<X, N>::kBytes, kStages = LnRing<X, N>::kStages;
-    constexpr bool kRing = kBytes >= 4;
+    using Ring = LnRing<X, N, 2>;
+    constexpr int kCols = Ring::kCols, kPieces = kCols / N, kPairs = kCols / 2;
+    constexpr int kBytes = Piece<X, N>::kBytes, kStages = Ring::kStages;
+    constexpr bool kRing = Ring::kRing;
     using Raw = typename Piece<X, N>::Raw;
     extern __shared__ __align__(16) uint8_t shared_bytes[];
     __shared__ float2 sums[2][kLnBack / 32];
@@ -297,10 +504,9 @@ __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
     const X* x = static_cast<const X*>(a.x);
     const X* dy = static_cast<const X*>(a.dy);
     X* dx = static_cast<X*>(a.dx);
-    constexpr int kPairs = kLnBackCols / 2;
     Pair w[kPairs], dw[kPairs], db[kPairs];
     {
-        float v[kLnBackCols] = {};
+        float v[kCols] = {};
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {
             const int c = (k * group + place) * N;
@@ -333,12 +539,26 @@ __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
     };
-    Piece<X, N> px[kPieces], pd[kPieces];
+    Piece<X, N> px[kPieces], pd[kPieces], next_x[kPieces], next_d[kPieces];
+    const auto load_next = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const int c = (k * group + place) * N;
+            next_x[k].zero();
+            next_d[k].zero();
+            if (r < a.rows && c < dim) {
+                next_x[k].load(x + r * a.x_stride + c);
+                next_d[k].load(dy + r * a.dy_stride + c);
+            }
+        }
+    };
     float mean = 0.0f, rstd = 0.0f;
     if (row < a.rows) mean = a.mean_in[row], rstd = a.rstd_in[row];
     if (kRing) {
 #pragma unroll
         for (int i = 0; i < kStages; ++i) stage_row(row + i * stride, i);
+    } else {
+        load_next(row);
     }
     // every lane of a warp takes part as long as the warp's first group has a row
     const int64_t lead = (int64_t)blockIdx.x * groups + (group < 32 ? warp * (32 / group) : which);
@@ -350,22 +570,23 @@ __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
         if (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {
-            const int c = (k * group + place) * N;
-            px[k].zero();
-            pd[k].zero();
-            if (on && c < dim) {
-                if constexpr (kRing) {
+            if (kRing) {
+                px[k].zero();
+                pd[k].zero();
+                if (on && (k * group + place) * N < dim) {
                     px[k].q = *slot(stage, k, 0);
                     pd[k].q = *slot(stage, k, 1);
-                } else {
-                    px[k].load(x + row * a.x_stride + c);
-                    pd[k].load(dy + row * a.dy_stride + c);
                 }
+            } else {
+                px[k] = next_x[k];
+                pd[k] = next_d[k];
             }
         }
         if (kRing) {
             stage_row(row + kStages * stride, stage);
             stage = stage + 1 == kStages ? 0 : stage + 1;
+        } else {
+            load_next(row + stride);
         }
         // with d = x - mean: xh = rstd * d, and the sum of g * xh is rstd times that of g * d
         Pair d[kPairs], g[kPairs], t0 = pair(0.0f), t1 = pair(0.0f);
@@ -397,7 +618,7 @@ __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
         if (on) {
             // dx = rstd * (g - s0 / n - xh * s1 / n)
             const Pair scale = pair(rstd), k0 = pair(-(s0 * inv_n) * rstd), k1 = pair(-(s1 * inv_n) * rstd * rstd);
-            float v[kLnBackCols];
+            float v[kCols];
 #pragma unroll
             for (int i = 0; i < kPairs; ++i)
                 split(fma2(g[i], scale, fma2(d[i], k1, k0)), v[2 * i], v[2 * i + 1]);
@@ -412,9 +633,9 @@ __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
         rstd = rstd_next;
     }
     if (kRing) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();  // the ring is free: it takes the CTA's column sums, [2][dim]
+    __syncthreads();  // the ring is free: it takes the groups' column sums, [group or warp][2][dim]
     float* const total = reinterpret_cast<float*>(shared_bytes);
-    float sw[kLnBackCols], sb[kLnBackCols];
+    float sw[kCols], sb[kCols];
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
         split(dw[i], sw[2 * i], sw[2 * i + 1]);
@@ -422,30 +643,33 @@ __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
     }
     if (group < 32) {  // the warp's groups first
 #pragma unroll
-        for (int i = 0; i < kLnBackCols; ++i)
+        for (int i = 0; i < kCols; ++i)
             for (int o = group; o < 32; o <<= 1) {
                 sw[i] += __shfl_xor_sync(0xffffffffu, sw[i], o);
                 sb[i] += __shfl_xor_sync(0xffffffffu, sb[i], o);
             }
     }
     const int owners = group < 32 ? kLnBack / 32 : groups, mine = group < 32 ? warp : which;
-    for (int o = 0; o < owners; ++o) {
-        if (o == mine && (group >= 32 || lane < group)) {
+    if (group >= 32 || lane < group) {
+        float* const to = total + mine * 2 * dim;
 #pragma unroll
-            for (int k = 0; k < kPieces; ++k) {
-                const int c = (k * group + place) * N;
-                if (c < dim)
+        for (int k = 0; k < kPieces; ++k) {
+            const int c = (k * group + place) * N;
+            if (c < dim)
 #pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        total[c + j] = (o ? total[c + j] : 0.0f) + sw[k * N + j];
-                        total[dim + c + j] = (o ? total[dim + c + j] : 0.0f) + sb[k * N + j];
-                    }
-            }
+                for (int j = 0; j < N; ++j) {
+                    to[c + j] = sw[k * N + j];
+                    to[dim + c + j] = sb[k * N + j];
+                }
         }
-        __syncthreads();
     }
+    __syncthreads();
     float* const part = a.part + (int64_t)blockIdx.x * 2 * dim;
-    for (int i = threadIdx.x; i < 2 * dim; i += kLnBack) part[i] = total[i];
+    for (int i = threadIdx.x; i < 2 * dim; i += kLnBack) {
+        float v = total[i];
+        for (int o = 1; o < owners; ++o) v += total[o * 2 * dim + i];
+        part[i] = v;
+    }
 }
 
 // Adds the partial sums: 32 columns per CTA, 32 rows of threads that each add every 32nd.
@@ -545,20 +769,42 @@ int group_of(int64_t places, int most)  // the smallest power of two with room f
     return g;
 }
 
+// The threads of a row.
+int row_group(int64_t dim, int n, int cols)
+{
+    const int64_t places = (dim + n - 1) / n;
+    if (places <= 16) return group_of(places, 16);
+    return 32 * group_of((dim + 32 * cols - 1) / (32 * cols), kLnBack / 32);
+}
+
 template <typename X, typename W, int N> cudaError_t ln_forward_n(LnArgs a, cudaStream_t stream)
 {
-    constexpr bool kVector = Piece<X, N>::kBytes == 16;
+    static bool set[64] = {};
     const dim3 one((unsigned)a.rows), threads(kLnThreads);
     if (a.dim > 64 * kLnThreads) return launch_after(ln_forward_long_kernel<X, W>, one, threads, 0, stream, a);
-    if (a.dim > 16 * kLnThreads) return launch_after(ln_forward_kernel<X, W, N, 64, true>, one, threads, 0, stream, a);
-    // a lane's 64 columns in small pieces are too many instructions and registers: a CTA per row
-    if (a.dim > (kVector ? 64 : 16) * 32)
-        return launch_after(ln_forward_kernel<X, W, N, 16, true>, one, threads, 0, stream, a);
-    a.group = group_of((a.dim + N - 1) / N, 32);
-    const dim3 grid((unsigned)((a.rows * a.group + kLnThreads - 1) / kLnThreads));
-    if constexpr (kVector)
-        if (a.dim > 16 * 32) return launch_after(ln_forward_kernel<X, W, N, 64, false>, grid, threads, 0, stream, a);
-    return launch_after(ln_forward_kernel<X, W, N, 16, false>, grid, threads, 0, stream, a);
+    if (a.dim > kLnBack * LnRing<X, N, 1>::kCols)
+        return launch_after(ln_forward_wide_kernel<X, W, N>, one, threads, 0, stream, a);
+    if constexpr (Piece<X, N>::kBytes == 16) {
+        if (a.dim > 128 && a.dim <= 2048) {
+            constexpr int M = sizeof(W) == 4 ? 4 : N;
+            const dim3 grid((unsigned)((a.rows + kLnWarpThreads / 32 - 1) / (kLnWarpThreads / 32)));
+            return launch_after(a.dim > 512 ? ln_forward_warp_kernel<X, W, M, 64> : ln_forward_warp_kernel<X, W, M, 16>,
+                                grid, dim3(kLnWarpThreads), 0, stream, a);
+        }
+    }
+    constexpr int shared = LnRing<X, N, 1>::kBytes;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = sm_count(&sms);
+    if (e == cudaSuccess && !set[dev]) {
+        e = cudaFuncSetAttribute(ln_forward_kernel<X, W, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+        set[dev] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess) return e;
+    a.group = row_group(a.dim, N, LnRing<X, N, 1>::kCols);
+    const int64_t per = kLnBack / a.group, need = (a.rows + per - 1) / per, most = sms;
+    return launch_after(ln_forward_kernel<X, W, N>, dim3((unsigned)(need < most ? need : most)), dim3(kLnBack), shared,
+                        stream, a);
 }
 
 template <typename X, typename W> cudaError_t ln_forward(const LnArgs& a, cudaStream_t stream)
@@ -570,24 +816,17 @@ template <typename X, typename W> cudaError_t ln_forward(const LnArgs& a, cudaSt
     return ln_forward_n<X, W, 1>(a, stream);
 }
 
-// The threads of a row, and the CTAs, of a backward pass.
-int back_group(int64_t dim, int n)
-{
-    const int64_t places = (dim + n - 1) / n;
-    if (places <= 16) return group_of(places, 16);
-    return 32 * group_of((dim + 32 * kLnBackCols - 1) / (32 * kLnBackCols), kLnBack / 32);
-}
-
 int ln_slices(int64_t rows, int64_t dim)
 {
-    const int64_t most = dim > kLnBackDim ? kLnWideSlices : kLnParts;
+    // either way of the backward pass, as the call's alignment decides, within these
+    const int64_t most = dim > kLnDim ? kLnWideSlices : kLnParts;
     return (int)(rows < 1 ? 1 : rows < most ? rows : most);
 }
 
 template <typename X, typename W, int N> cudaError_t ln_backward_n(LnArgs a, cudaStream_t stream)
 {
     static bool set[64] = {};
-    constexpr int shared = LnRing<X, N>::kShared;
+    constexpr int sums = 2 * (int)kLnDim * 4, ring = LnRing<X, N, 2>::kBytes, shared = ring > sums ? ring : sums;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = sm_count(&sms);
@@ -596,7 +835,7 @@ template <typename X, typename W, int N> cudaError_t ln_backward_n(LnArgs a, cud
         set[dev] = e == cudaSuccess;
     }
     if (e != cudaSuccess) return e;
-    a.group = back_group(a.dim, N);
+    a.group = row_group(a.dim, N, LnRing<X, N, 2>::kCols);
     const int64_t per = kLnBack / a.group, need = (a.rows + per - 1) / per;
     const int64_t most = sms < kLnParts ? sms : kLnParts;
     a.slices = (int)(need < most ? need : most);
@@ -611,14 +850,16 @@ template <typename X, typename W> cudaError_t ln_backward(LnArgs a, cudaStream_t
         a.slices = 0;
         return launch_after(ln_join_kernel<W>, dim3((unsigned)((2 * a.dim + 31) / 32)), dim3(kLnJoin), 0, stream, a);
     }
-    if (a.dim <= kLnBackDim) {
+    {
         const int n = piece_of(a, (int)sizeof(X), {a.x, a.dy, a.dx}, {a.x_stride, a.dy_stride, a.dx_stride}, {a.w});
-        if (n == 16 / (int)sizeof(X)) return ln_backward_n<X, W, 16 / sizeof(X)>(a, stream);
+        if (a.dim <= kLnDim) {
+            if (n == 16 / (int)sizeof(X)) return ln_backward_n<X, W, 16 / sizeof(X)>(a, stream);
+            if (n == 4 / (int)sizeof(X)) return ln_backward_n<X, W, 4 / sizeof(X)>(a, stream);
+        }
         if constexpr (sizeof(X) == 2)
-            if (n == 2) return ln_backward_n<X, W, 2>(a, stream);
-        return ln_backward_n<X, W, 1>(a, stream);
+            if (n == 1 && a.dim <= kLnDim / 2) return ln_backward_n<X, W, 1>(a, stream);
     }
-    a.slices = ln_slices(a.rows, a.dim);
+    a.slices = (int)(a.rows < kLnWideSlices ? a.rows : kLnWideSlices);
     const unsigned cols = (unsigned)((a.dim + kLnThreads - 1) / kLnThreads);
     cudaError_t e = launch_after(ln_columns_kernel<X>, dim3(cols, (unsigned)a.slices), dim3(kLnThreads), 0, stream, a);
     if (e != cudaSuccess) return e;
