@@ -144,12 +144,13 @@ __device__ __forceinline__ void group_barrier(int id, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// How many rows of kTensors tensors a thread has on their way, and the shared memory for them.
-template <typename X, int N, int kTensors> struct LnRing {
+// How many rows of x and dy a thread of the backward pass has on their way, and the shared memory
+// for them.
+template <typename X, int N> struct LnRing {
     // pieces of two bytes cannot be copied so: half the columns, and one row ahead in registers
     static constexpr bool kRing = Piece<X, N>::kBytes >= 4;
     static constexpr int kCols = kRing ? kLnCols : kLnCols / 2;
-    static constexpr int kRow = (kCols / N) * kTensors * kLnBack * Piece<X, N>::kBytes;
+    static constexpr int kRow = (kCols / N) * 2 * kLnBack * Piece<X, N>::kBytes;
     static constexpr int kStages = sizeof(X) == 2 ? 6 : 3;
     static constexpr int kBytes = kRing ? kStages * kRow : 0;
 };
@@ -163,229 +164,47 @@ template <int kBytes> __device__ __forceinline__ void copy_piece(void* to, const
 }
 
 // ---------------------------------------------------------------- forward
-// Bound by memory. A group of threads (1 to 512, a power of two) has a row, 16 columns per
-// thread at most, and goes from row to row, so that its weights stay in registers (read for
-// every row they filled L1's throughput: 16384 rows of 2048 bf16 33 us). The rows to come are
-// copied to shared memory ahead, every thread its own pieces, so that there is no barrier but
-// the group's two, of the mean and of the squared deviations, where it is more than a warp.
-template <typename X, typename W, int N>
-__global__ void __launch_bounds__(kLnBack, 1) ln_forward_kernel(const LnArgs a)
+// Bound by memory: x is read once and y written. A row is held in registers as it lies in
+// memory, kCols elements per thread, by a group of a.group lanes (kWarps 0), by a warp or by a
+// CTA of kWarps warps; the mean and the sum of the squared deviations from it are two sums over
+// the row's threads. The weights come from L1 for every row, so a thread's pieces are no longer
+// than four 32-bit weights, which keeps its 16-byte loads of them side by side (pieces of eight
+// bf16 elements: 33 us instead of 28 at 16384 rows of 2048, bound by L1). Nothing is loaded
+// ahead: the other rows on the SM hide a row's loads (a persistent CTA with its weights in
+// registers and the rows to come in shared memory took 33 us there, and 79 us instead of 50 at
+// 8192 rows of 8192 bf16, with two barriers for each row in turn).
+//
+// With 32-bit weights, all in us: 16384 x 2048 bf16 25 (5.3 TB/s; 65536 rows 84, 6.4 TB/s), fp32
+// 41 (6.5 TB/s); 8192 x 8192 bf16 50, fp32 79 (6.8 TB/s); 32768 x 1001 fp32 46 (5.7 TB/s).
+// Odd rows of bf16 are bound by their two-byte loads and stores: 32768 x 1001 47 (2.8 TB/s).
+template <int kWarps> constexpr int kLnRowThreads = kWarps > 1 ? 32 * kWarps : 128;  // a CTA's
+
+template <typename X, typename W, int N, int kCols, int kWarps>
+__global__ void __launch_bounds__(kLnRowThreads<kWarps>,
+                                  (kCols == 64 ? 768 : kCols == 32 ? 1024 : 1536) / kLnRowThreads<kWarps>)
+    ln_forward_row_kernel(const LnArgs a)
 {
-    using Ring = LnRing<X, N, 1>;
-    constexpr int kCols = Ring::kCols, kPieces = kCols / N, kPairs = kCols / 2;
-    constexpr int kBytes = Piece<X, N>::kBytes, kStages = Ring::kStages;
-    constexpr bool kRing = Ring::kRing;
-    using Raw = typename Piece<X, N>::Raw;
-    extern __shared__ __align__(16) uint8_t shared_bytes[];
-    __shared__ float sums[2][kLnBack / 32];
+    constexpr int kPieces = kCols / N, kThreads = kLnRowThreads<kWarps>;
+    __shared__ float sums[2][kThreads / 32];
     ptx::griddep_wait();
-    const int group = a.group, place = threadIdx.x & (group - 1), dim = (int)a.dim;
-    const int groups = kLnBack / group, which = threadIdx.x / group;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const float inv_n = 1.0f / (float)dim;
-    const X* x = static_cast<const X*>(a.x);
-    X* y = static_cast<X*>(a.y);
-    Pair w[kPairs], b[kPairs];
-    {
-        float v[kCols] = {}, u[kCols] = {};
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            const int c = (k * group + place) * N;
-            if (c < dim) {
-                weights<N>(static_cast<const W*>(a.w) + c, *reinterpret_cast<float(*)[N]>(v + k * N));
-                if (a.b) weights<N>(static_cast<const W*>(a.b) + c, *reinterpret_cast<float(*)[N]>(u + k * N));
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-            w[i] = pair(v[2 * i], v[2 * i + 1]);
-            b[i] = pair(u[2 * i], u[2 * i + 1]);
-        }
-    }
-    const auto there = [&](int k) { return (k * group + place) * N < dim ? 1.0f : 0.0f; };  // a piece of the row
-    const auto slot = [&](int stage, int k) {
-        return reinterpret_cast<Raw*>(shared_bytes) + (stage * kPieces + k) * kLnBack + threadIdx.x;
-    };
-    const auto stage_row = [&](int64_t r, int stage) {
-        if constexpr (kRing) {
-            if (r < a.rows) {
-#pragma unroll
-                for (int k = 0; k < kPieces; ++k) {
-                    const int c = (k * group + place) * N;
-                    if (c < dim) copy_piece<kBytes>(slot(stage, k), x + r * a.x_stride + c);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
-    };
-    const int64_t stride = (int64_t)gridDim.x * groups;
-    int64_t row = (int64_t)blockIdx.x * groups + which;
-    Piece<X, N> p[kPieces], next[kPieces];
-    const auto load_next = [&](int64_t r) {
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            const int c = (k * group + place) * N;
-            next[k].zero();
-            if (r < a.rows && c < dim) next[k].load(x + r * a.x_stride + c);
-        }
-    };
-    if (kRing) {
-#pragma unroll
-        for (int i = 0; i < kStages; ++i) stage_row(row + i * stride, i);
-    } else {
-        load_next(row);
-    }
-    // the sum over the row's group
+    if (kWarps < 2) ptx::griddep_launch();  // the next kernel's launch is under way while the last rows are
+    const int group = kWarps == 0 ? a.group : 32 * kWarps, place = threadIdx.x & (group - 1);
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / group) + threadIdx.x / group;
+    if (kWarps && row >= a.rows) return;
+    const float n = (float)a.dim;
+    const int dim = row < a.rows ? (int)a.dim : 0;  // lanes without a row take part in the sums
     const auto sum = [&](float v, int turn) {
-        v = group_sum(v, group < 32 ? group : 32);
-        if (group > 32) {
-            if (lane == 0) sums[turn][warp] = v;
-            group_barrier(1 + which, group);
-            const int first = which * (group >> 5);
-            v = 0.0f;
-            for (int i = 0; i < group >> 5; ++i) v += sums[turn][first + i];
-        }
-        return v;
-    };
-    // every lane of a warp takes part as long as the warp's first group has a row
-    const int64_t lead = (int64_t)blockIdx.x * groups + (group < 32 ? warp * (32 / group) : which);
-    int stage = 0;
-    for (int64_t at = lead; at < a.rows; at += stride, row += stride) {
-        const bool on = row < a.rows;
-        if (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            if (kRing) {
-                p[k].zero();
-                if (on && (k * group + place) * N < dim) p[k].q = *slot(stage, k);
-            } else {
-                p[k] = next[k];
-            }
-        }
-        if (kRing) {
-            stage_row(row + kStages * stride, stage);
-            stage = stage + 1 == kStages ? 0 : stage + 1;
-        } else {
-            load_next(row + stride);
-        }
-        Pair d[kPairs], t = pair(0.0f);
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-            d[i] = pair_of(p, i);
-            t = t + d[i];
-        }
-        const float mean = sum(both(t), 0) * inv_n;
-        t = pair(0.0f);
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-            d[i] = d[i] + pair(-mean);
-            const Pair e = d[i] * pair(there(2 * i / N), there((2 * i + 1) / N));
-            t = fma2(e, e, t);
-        }
-        const float rstd = 1.0f / sqrtf(sum(both(t), 1) * inv_n + a.eps);
-        if (!on) continue;
-        float v[kCols];
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) split(fma2(d[i] * pair(rstd), w[i], b[i]), v[2 * i], v[2 * i + 1]);
-        X* const to = y + row * a.y_stride;
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            const int c = (k * group + place) * N;
-            if (c < dim) put_piece<N>(to + c, *reinterpret_cast<const float(*)[N]>(v + k * N));
-        }
-        if (place == 0) {
-            if (a.mean) a.mean[row] = mean;
-            if (a.rstd) a.rstd[row] = rstd;
-        }
-    }
-}
-
-constexpr int kLnWarpThreads = 128;
-
-// Rows of 129 to 2048 elements that are aligned to 16 bytes: a warp per row, which it holds in
-// registers as it lies in memory, without a barrier. The weights come from L1 for every row, so
-// a lane's pieces are as long as four weights, which keeps its 16-byte loads of them side by
-// side (eight bf16 elements with fp32 weights: 33 us at 16384 rows of 2048, bound by L1).
-template <typename X, typename W, int N, int kCols>
-__global__ void __launch_bounds__(kLnWarpThreads, kCols == 64 ? 6 : 8) ln_forward_warp_kernel(const LnArgs a)
-{
-    constexpr int kPieces = kCols / N;
-    ptx::griddep_wait();
-    ptx::griddep_launch();  // the next kernel's launch is under way while this one's last rows are
-    constexpr int group = 32;
-    const int place = threadIdx.x & 31, dim = (int)a.dim;
-    const int64_t row = (int64_t)blockIdx.x * (kLnWarpThreads / 32) + threadIdx.x / 32;
-    if (row >= a.rows) return;
-    const X* x = static_cast<const X*>(a.x) + row * a.x_stride;
-    Piece<X, N> r[kPieces];
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-        const int c = (k * group + place) * N;
-        r[k].zero();
-        if (c < dim) r[k].load(x + c);
-    }
-    Pair s[2] = {pair(0.0f), pair(0.0f)};
-#pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) s[i & 1] = s[i & 1] + pair_of(r, i);
-    const float mean = warp_sum(both(s[0] + s[1])) / (float)dim;
-    const Pair minus = pair(-mean);
-    s[0] = s[1] = pair(0.0f);
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k)
-        if ((k * group + place) * N < dim) {
-#pragma unroll
-            for (int i = k * N / 2; i < (k + 1) * N / 2; ++i) {
-                const Pair d = pair_of(r, i) + minus;
-                s[i & 1] = fma2(d, d, s[i & 1]);
-            }
-        }
-    const float rstd = 1.0f / sqrtf(warp_sum(both(s[0] + s[1])) / (float)dim + a.eps);
-    const W* w = static_cast<const W*>(a.w);
-    const W* b = static_cast<const W*>(a.b);
-    X* y = static_cast<X*>(a.y) + row * a.y_stride;
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-        const int c = (k * group + place) * N;
-        if (c < dim) {
-            float wv[N], bv[N] = {}, v[N];
-            weights<N>(w + c, wv);
-            if (b) weights<N>(b + c, bv);
-#pragma unroll
-            for (int j = 0; j < N; j += 2) {
-                const Pair d = (pair_of(r, (k * N + j) / 2) + minus) * pair(rstd);
-                split(fma2(d, pair(wv[j], wv[j + 1]), pair(bv[j], bv[j + 1])), v[j], v[j + 1]);
-            }
-            put_piece<N>(y + c, v);
-        }
-    }
-    if (place == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
-    }
-}
-
-// Wider rows, of up to 16384 elements: a CTA per row, which it holds in registers as it lies
-// in memory; the weights come from L2 for every row.
-template <typename X, typename W, int N>
-__global__ void __launch_bounds__(kLnThreads) ln_forward_wide_kernel(const LnArgs a)
-{
-    constexpr int kCols = 64, kPieces = kCols / N;
-    __shared__ float shared[2][kLnThreads / 32];
-    ptx::griddep_wait();
-    constexpr int group = kLnThreads;
-    const int place = threadIdx.x;
-    const int64_t row = blockIdx.x;
-    const X* x = static_cast<const X*>(a.x) + row * a.x_stride;
-    const int dim = (int)a.dim;
-    const auto sum = [&](float v, int turn) {
+        if (kWarps == 0) return group_sum(v, group);
         v = warp_sum(v);
-        if ((threadIdx.x & 31) == 0) shared[turn][threadIdx.x >> 5] = v;
+        if (kWarps == 1) return v;
+        if ((threadIdx.x & 31) == 0) sums[turn][threadIdx.x >> 5] = v;
         __syncthreads();
         v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kLnThreads / 32; ++i) v += shared[turn][i];
+        for (int i = 0; i < kWarps; ++i) v += sums[turn][i];
         return v;
     };
+    const X* x = static_cast<const X*>(a.x) + row * a.x_stride;
     Piece<X, N> r[kPieces];
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
@@ -396,7 +215,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_forward_wide_kernel(const LnArg
     Pair s[2] = {pair(0.0f), pair(0.0f)};
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i) s[i & 1] = s[i & 1] + pair_of(r, i);
-    const float mean = sum(both(s[0] + s[1]), 0) / (float)dim;
+    const float mean = sum(both(s[0] + s[1]), 0) / n;
     const Pair minus = pair(-mean);
     s[0] = s[1] = pair(0.0f);
 #pragma unroll
@@ -409,11 +228,11 @@ __global__ void __launch_bounds__(kLnThreads) ln_forward_wide_kernel(const LnArg
                     s[i & 1] = fma2(d, d, s[i & 1]);
                 }
             } else {
-                const float d = r[k].get(0) - mean;
-                s[0] = fma2(pair(d, 0.0f), pair(d, 0.0f), s[0]);
+                const Pair d = pair(r[k].get(0) - mean, 0.0f);
+                s[k & 1] = fma2(d, d, s[k & 1]);
             }
         }
-    const float rstd = 1.0f / sqrtf(sum(both(s[0] + s[1]), 1) / (float)dim + a.eps);
+    const float rstd = 1.0f / sqrtf(sum(both(s[0] + s[1]), 1) / n + a.eps);
     const W* w = static_cast<const W*>(a.w);
     const W* b = static_cast<const W*>(a.b);
     X* y = static_cast<X*>(a.y) + row * a.y_stride;
@@ -436,7 +255,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_forward_wide_kernel(const LnArg
             put_piece<N>(y + c, v);
         }
     }
-    if (place == 0) {
+    if (place == 0 && (kWarps || row < a.rows)) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
     }
@@ -489,7 +308,7 @@ template <typename X, typename W> __global__ void __launch_bounds__(kLnThreads) 
 template <typename X, typename W, int N>
 __global__ void __launch_bounds__(kLnBack, 1) ln_backward_kernel(const LnArgs a)
 {
-    using Ring = LnRing<X, N, 2>;
+    using Ring = LnRing<X, N>;
     constexpr int kCols = Ring::kCols, kPieces = kCols / N, kPairs = kCols / 2;
     constexpr int kBytes = Piece<X, N>::kBytes, kStages = Ring::kStages;
     constexpr bool kRing = Ring::kRing;
@@ -779,32 +598,40 @@ int row_group(int64_t dim, int n, int cols)
 
 template <typename X, typename W, int N> cudaError_t ln_forward_n(LnArgs a, cudaStream_t stream)
 {
-    static bool set[64] = {};
     const dim3 one((unsigned)a.rows), threads(kLnThreads);
     if (a.dim > 64 * kLnThreads) return launch_after(ln_forward_long_kernel<X, W>, one, threads, 0, stream, a);
-    if (a.dim > kLnBack * LnRing<X, N, 1>::kCols)
-        return launch_after(ln_forward_wide_kernel<X, W, N>, one, threads, 0, stream, a);
-    if constexpr (Piece<X, N>::kBytes == 16) {
-        if (a.dim > 128 && a.dim <= 2048) {
-            constexpr int M = sizeof(W) == 4 ? 4 : N;
-            const dim3 grid((unsigned)((a.rows + kLnWarpThreads / 32 - 1) / (kLnWarpThreads / 32)));
-            return launch_after(a.dim > 512 ? ln_forward_warp_kernel<X, W, M, 64> : ln_forward_warp_kernel<X, W, M, 16>,
-                                grid, dim3(kLnWarpThreads), 0, stream, a);
-        }
+    // the elements of a piece: no more than four weights of 32 bits
+    constexpr bool kWhole = Piece<X, N>::kBytes == 16;
+    constexpr int M = kWhole && sizeof(W) == 4 ? 4 : N;
+    const auto with = [&](auto kernel, int group, int threads) {
+        a.group = group;
+        const int each = threads / group;
+        return launch_after(kernel, dim3((unsigned)((a.rows + each - 1) / each)), dim3(threads), 0, stream, a);
+    };
+    // Elements per thread and threads per row by measurement, us with the choice and with the
+    // next best. Aligned rows want many elements for each of few threads (16384 x 2048 bf16: two
+    // warps 25, one warp of 64 each 28, four of 16 each 27; 32768 x 1024 bf16: one warp 24, 64
+    // each 32), fp32 rows of 2049 to 4096 less so (8192 x 4096: 41, four warps of 32 each 43).
+    if (a.dim > 8192) return with(ln_forward_row_kernel<X, W, M, 64, 8>, 256, 256);
+    if (a.dim > 4096) return with(ln_forward_row_kernel<X, W, M, 32, 8>, 256, 256);
+    if (a.dim > 2048) {
+        if constexpr (kWhole && sizeof(X) == 2) return with(ln_forward_row_kernel<X, W, M, 32, 4>, 128, 128);
+        else return with(ln_forward_row_kernel<X, W, M, 16, 8>, 256, 256);
     }
-    constexpr int shared = LnRing<X, N, 1>::kBytes;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = sm_count(&sms);
-    if (e == cudaSuccess && !set[dev]) {
-        e = cudaFuncSetAttribute(ln_forward_kernel<X, W, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
-        set[dev] = e == cudaSuccess;
+    // Pieces of single elements are as many instructions, which wants more threads (32768 x 1001
+    // fp32: four warps 46, one warp 63).
+    if constexpr (N == 1) {
+        if (a.dim > 1024) return with(ln_forward_row_kernel<X, W, 1, 16, 4>, 128, 128);
+        if (a.dim > 512) return with(ln_forward_row_kernel<X, W, 1, 8, 4>, 128, 128);
+    } else {
+        if (a.dim > 1024) return with(ln_forward_row_kernel<X, W, M, 32, 2>, 64, 64);
+        if (a.dim > 512) return with(ln_forward_row_kernel<X, W, M, 32, 1>, 32, 128);
     }
-    if (e != cudaSuccess) return e;
-    a.group = row_group(a.dim, N, LnRing<X, N, 1>::kCols);
-    const int64_t per = kLnBack / a.group, need = (a.rows + per - 1) / per, most = sms;
-    return launch_after(ln_forward_kernel<X, W, N>, dim3((unsigned)(need < most ? need : most)), dim3(kLnBack), shared,
-                        stream, a);
+    // 65536 x 256 bf16: 16 lanes 16.5, a warp 18.5; x 254 (pieces of two): a warp 21, 16 lanes 27
+    if (a.dim > (kWhole ? 256 : 128)) return with(ln_forward_row_kernel<X, W, M, 16, 1>, 32, 128);
+    // 262144 x 64 bf16: 16 elements per lane 16, 8 per lane 20; x 63: 8 per lane 39, 4 per lane 47
+    constexpr int kCols = M < 4 ? 8 : 16;
+    return with(ln_forward_row_kernel<X, W, M, kCols, 0>, group_of((a.dim + kCols - 1) / kCols, 32), 128);
 }
 
 template <typename X, typename W> cudaError_t ln_forward(const LnArgs& a, cudaStream_t stream)
@@ -826,7 +653,7 @@ int ln_slices(int64_t rows, int64_t dim)
 template <typename X, typename W, int N> cudaError_t ln_backward_n(LnArgs a, cudaStream_t stream)
 {
     static bool set[64] = {};
-    constexpr int sums = 2 * (int)kLnDim * 4, ring = LnRing<X, N, 2>::kBytes, shared = ring > sums ? ring : sums;
+    constexpr int sums = 2 * (int)kLnDim * 4, ring = LnRing<X, N>::kBytes, shared = ring > sums ? ring : sums;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = sm_count(&sms);
@@ -835,7 +662,7 @@ template <typename X, typename W, int N> cudaError_t ln_backward_n(LnArgs a, cud
         set[dev] = e == cudaSuccess;
     }
     if (e != cudaSuccess) return e;
-    a.group = row_group(a.dim, N, LnRing<X, N, 2>::kCols);
+    a.group = row_group(a.dim, N, LnRing<X, N>::kCols);
     const int64_t per = kLnBack / a.group, need = (a.rows + per - 1) / per;
     const int64_t most = sms < kLnParts ? sms : kLnParts;
     a.slices = (int)(need < most ? need : most);

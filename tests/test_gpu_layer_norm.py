@@ -83,6 +83,21 @@ def test_forward_and_backward(rows, dim, xt, wt):
     _check_backward(h, _rand(gen, rows, dim, dtype=xt, scale=0.1), x, w, mean, rstd)
 
 
+# both sides of every width at which another variant takes over, in rows of each alignment
+WIDTHS = [w + d for w in (128, 256, 512, 1024, 2048, 4096, 8192, 16384) for d in (-1, 0, 2, 8)]
+
+
+@pytest.mark.parametrize("xt,wt", [(F, F), (B, F), (B, B)])
+@pytest.mark.parametrize("dim", WIDTHS)
+def test_widths(dim, xt, wt):
+    gen, rows = _gen(dim), 309
+    h = ac.adacomp_layer_norm_init(dim, CODE[xt], CODE[wt], EPS)
+    x = _rand(gen, rows, dim, dtype=xt, offset=0.5)
+    w, b = _params(gen, dim, wt)
+    _, mean, rstd = _check_forward(h, x, w, b)
+    _check_backward(h, _rand(gen, rows, dim, dtype=xt), x, w, mean, rstd)
+
+
 @pytest.mark.parametrize("rows,dim", [(100_000, 5), (70_000, 64), (20_001, 200), (4096, 768)])
 def test_many_rows(rows, dim):
     gen = _gen(rows)
