@@ -63,7 +63,8 @@ template <typename T> __device__ __forceinline__ T* moved(T* p, int64_t bytes)
 
 // Distances between rows, in bytes: in 32 bits where the rows are read 16 bytes at a time
 // (the host sees to it), so that an address is one instruction.
-template <int kBytes> using Distance = typename std::conditional<kBytes == 16, int32_t, int64_t>::type;
+template <int kBytes>
+using Distance = typename std::conditional<kBytes == 16 || kBytes < 0, int32_t, int64_t>::type;
 
 }  // namespace
 }  // namespace adacomp

@@ -1,5 +1,6 @@
 // The recurrence where there are few columns: the steps split over warps, CTAs and clusters.
 #include <cmath>
+#include <initializer_list>
 
 #include "recurrence.cuh"
 
@@ -32,10 +33,19 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) { return {fmaf(a.x, b.x
 // Bound by the rounds' latency (some 3 us each: the gates, one exchange, the results), as a
 // few columns leave an SM one or two CTAs. Measured: one sequence of 32768 steps of 1024 bf16
 // channels 87 us forward (2.3 TB/s), 131 backward (2.6); four ragged ones of up to 20011 steps
-// of 501 fp32 channels 155 and 268.
+// of 501 fp32 channels 115 (2.7 TB/s) and 174 (3.2).
 constexpr int kCols = 64, kSteps = 8, kWarps = 8, kThreads = 32 * kWarps, kSpan = kSteps * kWarps;
 constexpr int kTile = kSpan * kCols;  // elements of a tensor that a CTA has in a round
 static_assert(kRecChunk == kSpan, "a kept state for every CTA");
+
+// kBytes, by which the kernels take the rows: 16, 4 or 2 bytes at a time as they are aligned, or
+// less than zero: rows of elements of -kBytes bytes without alignment, by the aligned 16 bytes
+// that hold them, the first and last of which may hold a neighbour's elements too (a copy of four
+// bytes costs as much as one of 16). Such a tile has as many columns as 64 elements hold wherever
+// its row begins in the first 16 bytes.
+template <int kBytes> constexpr int kTileCols = kBytes > 0 ? kCols : kCols + 1 + 16 / kBytes;
+// Tiles of one sequence's channels, or of all sequences' numbered through.
+template <int kBytes> constexpr bool kApart = kBytes == 16 || kBytes < 0;
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -71,9 +81,9 @@ template <int kRanks> struct Exchange {
     unsigned long long barrier;
 };
 
-// CTAs of a cluster at most. Sixteen halve the rounds of few and long sequences; but for rows
-// of bf16 by 16 bytes the exchange's memory would cost an SM one of its CTAs.
-template <typename T, int kBytes> constexpr int kRanks = sizeof(T) == 2 && kBytes == 16 ? 16 : 8;
+// CTAs of a cluster at most. Sixteen halve the rounds of few and long sequences; but for others
+// than these the exchange's memory would cost an SM one of its CTAs.
+template <typename T, int kBytes> constexpr int kRanks = sizeof(T) == 2 && kApart<kBytes> ? 16 : 8;
 
 template <int R> __device__ __forceinline__ void exchange_init(Exchange<R>* x)
 {
@@ -115,9 +125,9 @@ template <int R> __device__ __forceinline__ bool exchange_wait(Exchange<R>* x, u
     return false;
 }
 
-// The columns of a tile. Where a sequence's rows are read 16 bytes at a time (kBytes), a
-// tile is 64 channels of one sequence; otherwise the channels of all sequences are numbered
-// through, so that few channels fill a tile too.
+// The columns of a tile. Where a sequence's rows are read 16 bytes at a time, a tile is of one
+// sequence's channels; otherwise the channels of all sequences are numbered through, so that
+// few channels fill a tile too.
 template <int kBytes> struct Column {
     int64_t b, c;
     int32_t len;  // of its sequence; 0 past the last column
@@ -125,11 +135,11 @@ template <int kBytes> struct Column {
 
     __device__ __forceinline__ Column(const RecArgs& p, uint32_t tile, int j)
     {
-        if (kBytes == 16) {
-            const uint32_t blocks = (uint32_t)((p.channels + kCols - 1) / kCols);
+        if (kApart<kBytes>) {
+            const uint32_t blocks = (uint32_t)((p.channels + kTileCols<kBytes> - 1) / kTileCols<kBytes>);
             b = tile / blocks;
-            c = (int64_t)(tile - (uint32_t)b * blocks) * kCols + j;
-            on = c < p.channels;
+            c = (int64_t)(tile - (uint32_t)b * blocks) * kTileCols<kBytes> + j;
+            on = j < kTileCols<kBytes> && c < p.channels;
         } else {
             const int64_t i = (int64_t)tile * kCols + j;
             on = i < p.batch * p.channels;
@@ -145,9 +155,10 @@ template <int kBytes> struct Column {
 // every thread has one place in the rows and takes every kStride-th of them. What lies past
 // a sequence's length or the last channel is not read, and what stands there not used.
 template <typename T, int kBytes, int kTensors> struct Copier {
-    static constexpr int kPlaces = kCols * (int)sizeof(T) / kBytes;
+    static constexpr int kCopy = kBytes < 0 ? 16 : kBytes;
+    static constexpr int kPlaces = kCols * (int)sizeof(T) / kCopy;
     static constexpr int kStride = kThreads / kPlaces;
-    static constexpr int kEach = kBytes / (int)sizeof(T);  // elements at a time
+    static constexpr int kEach = kBytes < 0 ? 0 : kBytes / (int)sizeof(T);  // elements at a time
     const T* from[kTensors];
     Distance<kBytes> step[kTensors];
     int32_t len;
@@ -157,7 +168,8 @@ template <typename T, int kBytes, int kTensors> struct Copier {
     {
         const Column<kBytes> col(p, tile, (threadIdx.x % kPlaces) * kEach);
         const int64_t rest = (p.channels - col.c) * (int)sizeof(T);
-        bytes = !col.on ? 0u : rest < kBytes ? (uint32_t)rest : (uint32_t)kBytes;
+        constexpr int most = kBytes < 0 ? kTileCols<kBytes> * (int)sizeof(T) : kBytes;  // of the row, or of a place in it
+        bytes = !col.on ? 0u : rest < most ? (uint32_t)rest : (uint32_t)most;
         len = bytes == 0 ? 0 : col.len;
 #pragma unroll
         for (int i = 0; i < kTensors; ++i) {
@@ -169,6 +181,26 @@ template <typename T, int kBytes, int kTensors> struct Copier {
     __device__ __forceinline__ void copy(T* to, int32_t t0) const
     {
         const int row0 = threadIdx.x / kPlaces, left = len - t0;
+        if constexpr (kBytes < 0) {
+            const int place = (threadIdx.x % kPlaces) * 16;
+#pragma unroll
+            for (int i = 0; i < kTensors; ++i) {
+                const T* const f = moved(from[i], (int64_t)(t0 + row0) * step[i]);
+                const uint32_t d0 = shared_address(to + i * kTile + row0 * kCols) + place;
+#pragma unroll
+                for (int k = 0; k < kSpan / kStride; ++k) {
+                    const uintptr_t g = reinterpret_cast<uintptr_t>(f) + (int64_t)(k * kStride * step[i]);
+                    const int before = (int)(g & 15), n = min(16, before + (int)bytes - place);
+                    if (row0 + k * kStride < left && n > 0)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         d0 + k * kStride * kCols * (int)sizeof(T)),
+                                     "l"(g - before + place), "r"(n)
+                                     : "memory");
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            return;
+        }
         T* const place = to + row0 * kCols + (threadIdx.x % kPlaces) * kEach;
 #pragma unroll
         for (int i = 0; i < kTensors; ++i) {
@@ -192,20 +224,34 @@ template <typename T, int kBytes, int kTensors> struct Copier {
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    // how many bytes are before step t's first element in its first 16 bytes
+    __device__ __forceinline__ uint32_t before(int tensor, int32_t t) const
+    {
+        return ((uint32_t)reinterpret_cast<uintptr_t>(from[tensor]) + (uint32_t)t * (uint32_t)step[tensor]) & 15;
+    }
 };
 
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-__device__ __forceinline__ void two(const float* p, float& x, float& y)
+// A lane's columns of a tile: two side by side where a row's elements are written two at a
+// time, and otherwise half a tile apart, which puts a warp's writes side by side.
+template <int kBytes> __device__ __forceinline__ int place_of(int lane, int j)
 {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    x = v.x, y = v.y;
+    return kBytes == 16 ? 2 * lane + j : lane + j * (kCols / 2);
 }
 
-__device__ __forceinline__ void two(const bf16* p, float& x, float& y)
+// Their elements, from the first one's on.
+template <int kBytes, typename T> __device__ __forceinline__ void two(const T* p, float& x, float& y)
 {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
-    x = bf16_low(v), y = bf16_high(v);
+    if constexpr (kBytes != 16) {
+        x = to_f32(p[0]), y = to_f32(p[kCols / 2]);
+    } else if constexpr (sizeof(T) == 4) {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        x = v.x, y = v.y;
+    } else {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+        x = bf16_low(v), y = bf16_high(v);
+    }
 }
 
 // Where a lane's two columns of a warp's steps go.
@@ -217,18 +263,18 @@ template <typename T, int kBytes> struct Writer {
         : step((Distance<kBytes>)(s.step * (int)sizeof(T)))
     {
         p[0] = at<T>(s, col[0].b, t, col[0].c);
-        if (kBytes != 16) p[1] = at<T>(s, col[1].b, t, col[1].c);
+        p[1] = kBytes < 0 ? p[0] + kCols / 2 : at<T>(s, col[1].b, t, col[1].c);
     }
-    // step k of both columns, which are there
-    __device__ __forceinline__ void put(int k, Two v) const
+    // step k of both columns, as far as they are there (two side by side are)
+    __device__ __forceinline__ void put(int k, Two v, bool on0, bool on1) const
     {
         T* const q = moved(p[0], k * step);
         if constexpr (kBytes == 16) {
             if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(q) = make_float2(v.x, v.y);
             else *reinterpret_cast<__nv_bfloat162*>(q) = __floats2bfloat162_rn(v.x, v.y);
         } else {
-            *q = from_f32<T>(v.x);
-            *moved(p[1], k * step) = from_f32<T>(v.y);
+            if (on0) *q = from_f32<T>(v.x);
+            if (on1) *moved(p[1], k * step) = from_f32<T>(v.y);
         }
     }
     __device__ __forceinline__ void put(int k, float x, float y, bool on0, bool on1) const
@@ -249,7 +295,8 @@ struct Live {
     __device__ __forceinline__ Live(const RecArgs& p, const Column<kBytes> (&col)[2], int32_t ts)
         : live0(max(0, min(kSteps, col[0].len - ts))), live1(max(0, min(kSteps, col[1].len - ts))),
           whole(max(0, min(kSteps, (int32_t)p.steps - ts))),
-          all(__all_sync(0xffffffffu, live0 == kSteps && live1 == kSteps))
+          all(__all_sync(0xffffffffu, (live0 == kSteps || (kBytes != 16 && !col[0].on)) &&
+                                          (live1 == kSteps || (kBytes != 16 && !col[1].on))))
     {
     }
 };
@@ -292,7 +339,8 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
     }
     const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Column<kBytes> col[2] = {Column<kBytes>(p, tile, 2 * lane), Column<kBytes>(p, tile, 2 * lane + 1)};
+    const Column<kBytes> col[2] = {Column<kBytes>(p, tile, place_of<kBytes>(lane, 0)),
+                                  Column<kBytes>(p, tile, place_of<kBytes>(lane, 1))};
     const Copier<T, kBytes, 2> copier(p, tile, {&p.z, &p.x});
     const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
     Two h0 = load_state(p.h0, p, col);  // before the round's first step (the joining warp's)
@@ -306,14 +354,18 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
         if (t0 + span < steps) copier.copy(tile_of(par ^ 1), tc + span);
         const int32_t ts = tc + warp * kSteps;
         const Live at_hand(p, col, ts);
-        const T* z = tile_of(par) + warp * kSteps * kCols + 2 * lane;
+        const T* const first = tile_of(par) + warp * kSteps * kCols + place_of<kBytes>(lane, 0);
+        const auto place = [&](int tensor, int k) {  // step k's
+            const T* q = first + tensor * kTile + k * kCols;
+            return kBytes < 0 ? moved(q, copier.before(tensor, ts + k)) : q;
+        };
         Two a[kSteps], u[kSteps], A = two_of(1.0f), H = two_of(0.0f);
         const auto form = [&](auto masked) {
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
                 float z0, z1, x0, x1, a0, a1, b0, b1;
-                two(z + k * kCols, z0, z1);
-                two(z + k * kCols + kTile, x0, x1);
+                two<kBytes>(place(0, k), z0, z1);
+                two<kBytes>(place(1, k), x0, x1);
                 gate(z0, &a0, &b0);
                 gate(z1, &a1, &b1);
                 if (masked.value) {  // past the length the state stays as it is
@@ -371,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
                 h = fma2(a[k], h, u[k]);
-                y.put(k, h);
+                y.put(k, h, col[0].on, col[1].on);
             }
         } else {
 #pragma unroll
@@ -392,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
 // step k. The states are formed again from the one that the forward pass kept for the CTA's
 // steps: that is less to read than y, and not rounded.
 template <typename T, int kBytes>
-__global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
+__global__ void __launch_bounds__(kThreads, kBytes == 4 || kBytes == -4 ? 2 : 3) rec_backward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
 {
     extern __shared__ __align__(16) uint8_t shared_bytes[];
     __shared__ float4 part[kWarps][32];  // a warp's (A, H)
@@ -407,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_ke
     }
     const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Column<kBytes> col[2] = {Column<kBytes>(p, tile, 2 * lane), Column<kBytes>(p, tile, 2 * lane + 1)};
+    const Column<kBytes> col[2] = {Column<kBytes>(p, tile, place_of<kBytes>(lane, 0)),
+                                  Column<kBytes>(p, tile, place_of<kBytes>(lane, 1))};
     const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
     int32_t t0 = steps > 0 ? (steps - 1) / span * span : -1, tc = t0 + (int32_t)rank * kSpan;
     const Copier<T, kBytes, 3> copier(p, tile, {&p.z, &p.x, &p.dy});
@@ -424,11 +477,15 @@ __global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_ke
         if (t0 > 0) copier.copy(tile_of(par ^ 1), tc - span);
         const int32_t ts = tc + warp * kSteps;
         const Live at_hand(p, col, ts);
-        const T* z = tile_of(par) + warp * kSteps * kCols + 2 * lane;
+        const T* const first = tile_of(par) + warp * kSteps * kCols + place_of<kBytes>(lane, 0);
+        const auto place = [&](int tensor, int k) {  // step k's
+            const T* q = first + tensor * kTile + k * kCols;
+            return kBytes < 0 ? moved(q, copier.before(tensor, ts + k)) : q;
+        };
         Two a[kSteps], b[kSteps], A = two_of(1.0f), H = two_of(0.0f), P = two_of(0.0f);
         const auto inputs = [&](auto masked, int tensor, int k) {  // x or dy
             float v0, v1;
-            two(z + k * kCols + tensor * kTile, v0, v1);
+            two<kBytes>(place(tensor, k), v0, v1);
             if (masked.value) {
                 if (k >= at_hand.live0) v0 = 0.0f;
                 if (k >= at_hand.live1) v1 = 0.0f;
@@ -439,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_ke
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
                 float z0, z1, a0, a1, b0, b1;
-                two(z + k * kCols, z0, z1);
+                two<kBytes>(place(0, k), z0, z1);
                 gate(z0, &a0, &b0);
                 gate(z1, &a1, &b1);
                 if (masked.value) {
@@ -512,8 +569,8 @@ __global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_ke
                 q = a[k] * G;
                 const Two v = a[k] * g * before[k];
                 if (!masked.value) {
-                    dx.put(k, g);
-                    dz.put(k, v);
+                    dx.put(k, g, col[0].on, col[1].on);
+                    dz.put(k, v, col[0].on, col[1].on);
                 } else if (k < at_hand.whole) {
                     const Two e = g, f = v;
                     const bool l0 = k < at_hand.live0, l1 = k < at_hand.live1;
@@ -531,12 +588,12 @@ __global__ void __launch_bounds__(kThreads, kBytes == 4 ? 2 : 3) rec_backward_ke
 
 // Launches a kernel of clusters, behind the kernel ahead of it as launch_after does.
 template <int kRanks, void (*kern)(RecArgs, uint32_t)>
-cudaError_t launch_ranks(bool rows16, int shared, const RecArgs& p, cudaStream_t stream)
+cudaError_t launch_ranks(int cols, int shared, const RecArgs& p, cudaStream_t stream)
 {
     static bool set[64] = {};  // the kernel's shared memory, once per device
 
     uint32_t ranks = 1;
-    const int64_t tiles = rows16 ? p.batch * ((p.channels + kCols - 1) / kCols) : (p.batch * p.channels + kCols - 1) / kCols;
+    const int64_t tiles = cols ? p.batch * ((p.channels + cols - 1) / cols) : (p.batch * p.channels + kCols - 1) / kCols;
     // a CTA more in a cluster is worth its exchange where the GPU is not full without it; more
     // than eight where all clusters still run at once
     const uint32_t most = tiles <= 19 ? (uint32_t)kRanks : 8;
@@ -568,24 +625,49 @@ cudaError_t launch_ranks(bool rows16, int shared, const RecArgs& p, cudaStream_t
     return cudaLaunchKernelEx(&cfg, kern, p, ranks);
 }
 
+// Whether rows without alignment are taken by the aligned 16 bytes that hold them: unless that
+// makes more tiles, as it does of few channels beyond a tile's, and more than run at once.
+// Training step, us with it and without: 4 x 20011 x 501 fp32 289 and 417, 4 x 4096 x 1001 bf16
+// 120 and 174, 32 x 4096 x 33 fp32 55 and 70; 32 x 4096 x 62 fp32 (two tiles for one) 115 and 93.
+template <typename T> bool by_granules(const RecArgs& p, std::initializer_list<const RecSeq*> seqs)
+{
+    constexpr int64_t cols = kTileCols<-(int)sizeof(T)>;
+    const int64_t apart = p.batch * ((p.channels + cols - 1) / cols), through = (p.batch * p.channels + kCols - 1) / kCols;
+    bool fits = p.channels >= 32 && (4 * apart <= 5 * through || apart <= 38);
+    for (const RecSeq* s : seqs) fits = fits && s->step < (int64_t)1 << 22;  // a tile's steps span less than 2^31 bytes
+    return fits;
+}
+
+template <typename T, int kBytes> cudaError_t forward_ranks(const RecArgs& p, cudaStream_t stream)
+{
+    constexpr int cols = kApart<kBytes> ? kTileCols<kBytes> : 0, pad = kBytes < 0 ? 16 : 0;
+    return launch_ranks<kRanks<T, kBytes>, rec_forward_kernel<T, kBytes>>(cols, 4 * kTile * (int)sizeof(T) + pad, p, stream);
+}
+
+template <typename T, int kBytes> cudaError_t backward_ranks(const RecArgs& p, cudaStream_t stream)
+{
+    constexpr int cols = kApart<kBytes> ? kTileCols<kBytes> : 0, pad = kBytes < 0 ? 16 : 0;
+    return launch_ranks<kRanks<T, kBytes>, rec_backward_kernel<T, kBytes>>(cols, 6 * kTile * (int)sizeof(T) + pad, p, stream);
+}
+
 }  // namespace
 
 template <typename T> cudaError_t rec_split_forward(const RecArgs& p, int by, cudaStream_t stream)
 {
-    constexpr int shared = 4 * kSpan * kCols * (int)sizeof(T);
-    if (by == 16) return launch_ranks<kRanks<T, 16>, rec_forward_kernel<T, 16>>(true, shared, p, stream);
+    if (by == 16) return forward_ranks<T, 16>(p, stream);
+    if (by_granules<T>(p, {&p.z, &p.x, &p.y})) return forward_ranks<T, -(int)sizeof(T)>(p, stream);
     if constexpr (sizeof(T) == 2)
-        if (by == 2) return launch_ranks<kRanks<T, 2>, rec_forward_kernel<T, 2>>(false, shared, p, stream);
-    return launch_ranks<kRanks<T, 4>, rec_forward_kernel<T, 4>>(false, shared, p, stream);
+        if (by == 2) return forward_ranks<T, 2>(p, stream);
+    return forward_ranks<T, 4>(p, stream);
 }
 
 template <typename T> cudaError_t rec_split_backward(const RecArgs& p, int by, cudaStream_t stream)
 {
-    constexpr int shared = 6 * kSpan * kCols * (int)sizeof(T);
-    if (by == 16) return launch_ranks<kRanks<T, 16>, rec_backward_kernel<T, 16>>(true, shared, p, stream);
+    if (by == 16) return backward_ranks<T, 16>(p, stream);
+    if (by_granules<T>(p, {&p.z, &p.x, &p.dy, &p.dz, &p.dx})) return backward_ranks<T, -(int)sizeof(T)>(p, stream);
     if constexpr (sizeof(T) == 2)
-        if (by == 2) return launch_ranks<kRanks<T, 2>, rec_backward_kernel<T, 2>>(false, shared, p, stream);
-    return launch_ranks<kRanks<T, 4>, rec_backward_kernel<T, 4>>(false, shared, p, stream);
+        if (by == 2) return backward_ranks<T, 2>(p, stream);
+    return backward_ranks<T, 4>(p, stream);
 }
 
 template cudaError_t rec_split_forward<float>(const RecArgs&, int, cudaStream_t);

@@ -124,6 +124,31 @@ def test_layouts(layout, ch, dt):
         assert torch.equal(g, p)
 
 
+@pytest.mark.parametrize("dt", [F, B])
+@pytest.mark.parametrize("batch,steps,ch", [(2, 150, 33), (3, 200, 57), (2, 129, 58), (2, 300, 61), (2, 700, 62),
+                                            (1, 1100, 121), (2, 257, 123), (40, 140, 61), (3, 140, 1001)])
+def test_rows_off_every_alignment(batch, steps, ch, dt):
+    """Rows that begin at any element, among values that are not numbers and stay as they are."""
+    z, x, h0, dy, dh = _inputs(ch + steps, batch, steps, ch, dt)
+
+    def among(t, shift, gap):
+        whole = torch.full((shift + batch * steps * (ch + gap) + 9,), float("nan"), dtype=dt, device="cuda")
+        view = whole[shift:shift + batch * steps * (ch + gap)].view(batch, steps, ch + gap)[..., :ch]
+        if t is not None:
+            view.copy_(t)
+        return whole, view
+
+    for shift in range(0, 8, 3):
+        ins = [among(t, shift + i, shift + 2 * i) for i, t in enumerate((z, x, dy))]
+        outs = [among(None, shift + i, 1 + shift + i) for i in range(3)]
+        (_, z2), (_, x2), (_, dy2) = ins
+        _check(_run(z2, x2, h0, None, dy2, dh, *(v for _, v in outs)), z, x, h0, None, dy, dh)
+        for whole, view in outs:
+            assert not bool(view.isnan().any())
+            view.fill_(float("nan"))
+            assert bool(whole.isnan().all())
+
+
 def test_what_lies_between_the_rows_is_kept():
     batch, steps, ch = 2, 40, 21
     z, x, h0, dy, dh = _inputs(1, batch, steps, ch, B)
