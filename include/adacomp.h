@@ -361,7 +361,8 @@ adacomp_status adacomp_materialize_group(adacomp_layer_t h, float* const* residu
  * The conventions above hold, with these differences: tensors of layer norm and the
  * recurrence are strided (strides count elements; the last axis is contiguous) and
  * aligned to their element type only (ADACOMP_ERR_ALIGNMENT otherwise); aligned to
- * 16 bytes, with strides that keep every row so, they are read and written faster.
+ * 16 bytes, with strides that keep every row so, they are read and written faster. What shares
+ * 16 bytes, aligned to as many, with a row's elements may be read with them and is not used.
  * Outputs may not overlap inputs or each other unless a call says so. Sums, statistics
  * and states are fp32 or wider; results are rounded to the output's type once. Calls
  * are deterministic. Non-finite inputs reach only the results that depend on them.
@@ -385,8 +386,8 @@ adacomp_status adacomp_layer_norm_forward(adacomp_layer_norm_t h, int64_t rows, 
                                           const void* w, const void* b, void* y, int64_t y_stride, float* mean,
                                           float* rstd, cudaStream_t stream);
 
-/* Workspace bytes of a backward pass over `rows` rows (the partial sums of dw and db;
- * needs no initialisation). */
+/* Workspace bytes of a backward pass over `rows` rows (partial sums; needs no
+ * initialisation). */
 size_t adacomp_layer_norm_backward_ws_bytes(adacomp_layer_norm_t h, int64_t rows);
 
 /* From dy and the forward pass's x, mean and rstd, with xh = (x - mean) * rstd and g = dy * w:
