@@ -67,9 +67,7 @@ __device__ __forceinline__ void take_over(int barrier)
     asm volatile("bar.sync %0, 64;" ::"r"(barrier) : "memory");
 }
 
-// A column of a tile. Where a sequence's rows are read 16 bytes at a time (kBytes), a tile is
-// kCols channels of one sequence; otherwise the channels of all sequences are numbered
-// through, so that few channels fill a tile too.
+// A column of a tile.
 template <int kBytes, int kCols> struct Column {
     int64_t b, c;
     int32_t len;  // of its sequence; 0 past the last column
@@ -77,7 +75,7 @@ template <int kBytes, int kCols> struct Column {
 
     __device__ __forceinline__ Column(const RecArgs& p, uint32_t tile, int j)
     {
-        if (kBytes == 16) {
+        if (kApart<kBytes>) {
             const uint32_t blocks = (uint32_t)((p.channels + kCols - 1) / kCols);
             b = tile / blocks;
             c = (int64_t)(tile - (uint32_t)b * blocks) * kCols + j;
@@ -104,7 +102,8 @@ template <typename T, int kBytes, int kCols, int kChunk, int kTensors> struct Co
     static constexpr int kPlaces = kCols * (int)sizeof(T) / kBytes;
     static constexpr int kStride = 32 / kPlaces < kChunk ? 32 / kPlaces : kChunk;
     static constexpr int kEach = kBytes / (int)sizeof(T);  // elements at a time
-    static constexpr int kElements = kChunk * kCols;       // of one tensor
+    static constexpr int kPitch = kCols;
+    static constexpr int kElements = kChunk * kPitch;      // of one tensor
     static_assert(kPlaces <= 32 && kChunk % kStride == 0, "whole rows");
     const T* from[kTensors];
     Distance<kBytes> step[kTensors];
@@ -154,6 +153,65 @@ template <typename T, int kBytes, int kCols, int kChunk, int kTensors> struct Co
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
 };
+
+// Rows without alignment, by the aligned 16 bytes that hold them (a copy of four bytes costs as
+// much as one of 16): the first and the last of these may hold a neighbour's elements too, and a
+// row's first element lies `before` bytes into its place.
+template <typename T, int kBytes, int kCols, int kChunk, int kTensors> struct CopierOff {
+    static constexpr int kGranules = (kCols * (int)sizeof(T) + 16 - (int)sizeof(T) + 15) / 16;  // of a row, at most
+    static constexpr int kPitch = kGranules * 16 / (int)sizeof(T);
+    static constexpr int kElements = kChunk * kPitch;
+    const T* from[kTensors];
+    int32_t step[kTensors];
+    int32_t len, bytes;
+
+    __device__ __forceinline__ CopierOff(const RecArgs& p, uint32_t tile, const RecSeq* const (&s)[kTensors])
+    {
+        const Column<kBytes, kCols> col(p, tile, 0);
+        const int64_t rest = p.channels - col.c;
+        bytes = (rest < kCols ? (int32_t)rest : kCols) * (int)sizeof(T);
+        len = col.len;
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i) {
+            from[i] = at<const T>(*s[i], col.b, 0, col.c);
+            step[i] = (int32_t)s[i]->step * (int)sizeof(T);
+        }
+    }
+
+    __device__ __forceinline__ void copy(T* to, int32_t t0) const
+    {
+        const int lane = threadIdx.x & 31, left = len - t0;
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(to) + lane * 16;
+#pragma unroll
+        for (int k = 0; k < (kChunk * kGranules + 31) / 32; ++k) {
+            const int row = (k * 32 + lane) / kGranules, place = (k * 32 + lane - row * kGranules) * 16;
+            if (row >= left || row >= kChunk) continue;
+#pragma unroll
+            for (int i = 0; i < kTensors; ++i) {
+                const uintptr_t g = reinterpret_cast<uintptr_t>(from[i]) + (int64_t)(t0 + row) * step[i];
+                const int before = (int)(g & 15), n = min(16, before + bytes - place);
+                if (n > 0)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     d + i * kElements * (int)sizeof(T) + k * 512),
+                                 "l"(g - before + place), "r"(n)
+                                 : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+};
+
+template <typename T, int kBytes, int kCols, int kChunk, int kTensors>
+using CopierOf = typename std::conditional<kBytes < 0, CopierOff<T, kBytes, kCols, kChunk, kTensors>,
+                                           Copier<T, kBytes < 0 ? 4 : kBytes, kCols, kChunk, kTensors>>::type;
+
+// How many bytes lie before a row's first element in its place: none, but in rows without alignment.
+template <int kBytes, typename Copy> __device__ __forceinline__ uint32_t before(const Copy& c, int tensor, int32_t t)
+{
+    if constexpr (kBytes < 0)
+        return ((uint32_t)reinterpret_cast<uintptr_t>(c.from[tensor]) + (uint32_t)t * (uint32_t)c.step[tensor]) & 15;
+    else return 0;
+}
 
 __device__ __forceinline__ void copies_wait()
 {
@@ -207,7 +265,7 @@ __global__ void __launch_bounds__(32 * kWarps, kV == 2 ? 2 : 4) rec_forward_kern
 {
     constexpr int kCols = 32 * kV, S = kForward;
     static_assert(kV == 1 || kBytes == 16, "neighbours lie in one row");
-    using Copy = Copier<T, kBytes, kCols, S, 2>;
+    using Copy = CopierOf<T, kBytes, kCols, S, 2>;
     extern __shared__ __align__(16) uint8_t shared_bytes[];
     __shared__ float state[kWarps][kCols];  // after a warp's chunk
     ptx::griddep_wait();
@@ -224,9 +282,12 @@ __global__ void __launch_bounds__(32 * kWarps, kV == 2 ? 2 : 4) rec_forward_kern
     for (int slot = 0; t0 < steps; t0 += turn, slot ^= 1) {
         copies_wait();
         if (t0 + turn < steps) copier.copy(ring + (slot ^ 1) * (2 * Copy::kElements), t0 + turn);
-        const T* z = ring + slot * (2 * Copy::kElements) + j;
+        const T* const first = ring + slot * (2 * Copy::kElements) + j;
+        const auto place = [&](int tensor, int k) {  // step k's
+            return moved(first + tensor * Copy::kElements + k * Copy::kPitch, before<kBytes>(copier, tensor, t0 + k));
+        };
         const int32_t live = col.len - t0;
-        const bool all = __all_sync(0xffffffffu, live >= S && on == kV);
+        const bool all = __all_sync(0xffffffffu, (live >= S && on == kV) || (kBytes < 0 && on == 0));
         float a[S][kV], u[S][kV], h[kV], after[kV];
         Step own[kV];
 #pragma unroll
@@ -235,8 +296,8 @@ __global__ void __launch_bounds__(32 * kWarps, kV == 2 ? 2 : 4) rec_forward_kern
 #pragma unroll
             for (int k = 0; k < S; ++k) {
                 float zv[kV], xv[kV];
-                values(z + k * kCols, zv);
-                values(z + k * kCols + Copy::kElements, xv);
+                values(place(0, k), zv);
+                values(place(1, k), xv);
 #pragma unroll
                 for (int v = 0; v < kV; ++v) {
                     float r;
@@ -278,7 +339,7 @@ __global__ void __launch_bounds__(32 * kWarps, kV == 2 ? 2 : 4) rec_forward_kern
             for (int k = 0; k < S; ++k) {
 #pragma unroll
                 for (int v = 0; v < kV; ++v) h[v] = fmaf(a[k][v], h[v], u[k][v]);
-                put(moved(y, k * step), h);
+                if (kBytes > 0 || on) put(moved(y, k * step), h);
             }
         } else {
 #pragma unroll
@@ -304,7 +365,7 @@ template <typename T, int kBytes, int kV>
 __global__ void __launch_bounds__(32 * kBackWarps<kV>, kV == 2 ? 2 : kBytes == 16 ? 6 : 5) rec_backward_kernel(const __grid_constant__ RecArgs p)
 {
     constexpr int kCols = 32 * kV, S = kBackward<kV>, W = kBackWarps<kV>;
-    using Copy = Copier<T, kBytes, kCols, S, 3>;
+    using Copy = CopierOf<T, kBytes, kCols, S, 3>;
     extern __shared__ __align__(16) uint8_t shared_bytes[];
     __shared__ float state[W][kCols];  // after a warp's chunk
     __shared__ float grad[W][kCols];   // the gradient before it
@@ -334,10 +395,12 @@ __global__ void __launch_bounds__(32 * kBackWarps<kV>, kV == 2 ? 2 : kBytes == 1
         for (int v = 0; v < kV; ++v) h[v] = warp == 0 && v < on ? p.carry[col.kept(p, t0) + v] : 0.0f;
         copies_wait();
         if (t0 >= kRecChunk) copier.copy(ring + (slot ^ 1) * (3 * Copy::kElements), t0 - kRecChunk);
-        const T* z = ring + slot * (3 * Copy::kElements) + j;
-        const T *x = z + Copy::kElements, *d = x + Copy::kElements;
+        const T* const first = ring + slot * (3 * Copy::kElements) + j;
+        const auto place = [&](int tensor, int k) {  // step k's
+            return moved(first + tensor * Copy::kElements + k * Copy::kPitch, before<kBytes>(copier, tensor, t0 + k));
+        };
         const int32_t live = col.len - t0;
-        const bool all = __all_sync(0xffffffffu, live >= S && on == kV);
+        const bool all = __all_sync(0xffffffffu, (live >= S && on == kV) || (kBytes < 0 && on == 0));
         float a[S][kV], b[S][kV], from_x[S][kV];  // from_x: x_t, later h_{t-1} - x_t
         Step own[kV];
         float P[kV];
@@ -347,9 +410,9 @@ __global__ void __launch_bounds__(32 * kBackWarps<kV>, kV == 2 ? 2 : kBytes == 1
 #pragma unroll
             for (int k = 0; k < S; ++k) {
                 float zv[kV], dv[kV];
-                values(z + k * kCols, zv);
-                values(x + k * kCols, from_x[k]);
-                values(d + k * kCols, dv);
+                values(place(0, k), zv);
+                values(place(1, k), from_x[k]);
+                values(place(2, k), dv);
 #pragma unroll
                 for (int v = 0; v < kV; ++v) {
                     gate(zv[v], &a[k][v], &b[k][v]);
@@ -406,7 +469,7 @@ __global__ void __launch_bounds__(32 * kBackWarps<kV>, kV == 2 ? 2 : kBytes == 1
 #pragma unroll
             for (int k = S - 1; k >= 0; --k) {
                 float dv[kV], gx[kV], gz[kV];
-                values(d + k * kCols, dv);
+                values(place(2, k), dv);
 #pragma unroll
                 for (int v = 0; v < kV; ++v) {
                     const float G = __fadd_rn(q[v], masked.value && k >= live ? 0.0f : dv[v]);
@@ -415,8 +478,10 @@ __global__ void __launch_bounds__(32 * kBackWarps<kV>, kV == 2 ? 2 : kBytes == 1
                     q[v] = __fmul_rn(a[k][v], G);
                 }
                 if (!masked.value) {
-                    put(moved(dx, k * step_x), gx);
-                    put(moved(dz, k * step_z), gz);
+                    if (kBytes > 0 || on) {
+                        put(moved(dx, k * step_x), gx);
+                        put(moved(dz, k * step_z), gz);
+                    }
                 } else if (t0 + k < steps) {
 #pragma unroll
                     for (int v = 0; v < kV; ++v)
@@ -448,10 +513,10 @@ int row_bytes(const RecArgs& p, int e, std::initializer_list<const RecSeq*> seqs
 
 // A kernel with a CTA of `warps` per tile of `cols` columns; per_warp: shared bytes of a warp.
 template <void (*kern)(RecArgs)>
-cudaError_t launch_tiles(const RecArgs& p, bool rows16, int cols, int most, int warps, int per_warp, cudaStream_t stream)
+cudaError_t launch_tiles(const RecArgs& p, bool apart, int cols, int most, int warps, int per_warp, cudaStream_t stream)
 {
     static bool set[64] = {};  // the kernel's shared memory, once per device
-    const int64_t tiles = rows16 ? p.batch * ((p.channels + cols - 1) / cols) : (p.batch * p.channels + cols - 1) / cols;
+    const int64_t tiles = apart ? p.batch * ((p.channels + cols - 1) / cols) : (p.batch * p.channels + cols - 1) / cols;
     if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -467,15 +532,16 @@ cudaError_t launch_tiles(const RecArgs& p, bool rows16, int cols, int most, int 
 template <typename T, int kBytes, int kV> cudaError_t forward_v(const RecArgs& p, cudaStream_t stream)
 {
     const int64_t chunks = (p.steps + kForward - 1) / kForward;
-    return launch_tiles<rec_forward_kernel<T, kBytes, kV>>(p, kBytes == 16, 32 * kV, kWarps,
-                                                           chunks < kWarps ? (int)chunks : kWarps,
-                                                           2 * 2 * kForward * 32 * kV * (int)sizeof(T), stream);
+    return launch_tiles<rec_forward_kernel<T, kBytes, kV>>(
+        p, kApart<kBytes>, 32 * kV, kWarps, chunks < kWarps ? (int)chunks : kWarps,
+        2 * 2 * CopierOf<T, kBytes, 32 * kV, kForward, 2>::kElements * (int)sizeof(T), stream);
 }
 
 template <typename T, int kBytes, int kV> cudaError_t backward_v(const RecArgs& p, cudaStream_t stream)
 {
-    return launch_tiles<rec_backward_kernel<T, kBytes, kV>>(p, kBytes == 16, 32 * kV, kBackWarps<kV>, kBackWarps<kV>,
-                                                            2 * 3 * kBackward<kV> * 32 * kV * (int)sizeof(T), stream);
+    return launch_tiles<rec_backward_kernel<T, kBytes, kV>>(
+        p, kApart<kBytes>, 32 * kV, kBackWarps<kV>, kBackWarps<kV>,
+        2 * 3 * CopierOf<T, kBytes, 32 * kV, kBackward<kV>, 3>::kElements * (int)sizeof(T), stream);
 }
 
 // How a call is split. Many columns: a CTA for 64 or 32 of them, if that makes one for every
@@ -483,6 +549,11 @@ template <typename T, int kBytes, int kV> cudaError_t backward_v(const RecArgs& 
 // forward 56 us with clusters, 89 without, backward 124 and 297).
 constexpr int64_t kManyColumns = 152 * 32;
 constexpr int64_t kSplitSteps = 128;
+
+// Rows without alignment (forward and backward us by 16 bytes, and by four or two): 16 x 2048 x 1023
+// fp32 79 and 146, 141 and 208; bf16 58 and 115, 79 and 172. But rows of pairs of bf16 elements
+// take as many copies of four bytes as there are lanes: 16 x 2048 x 1022 58 and 114, 54 and 95.
+template <typename T> constexpr int kPairs = sizeof(T) == 2 ? 4 : 0;
 
 template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
 {
@@ -495,6 +566,7 @@ template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
     const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.y});
     if (n < kManyColumns && p.steps > kSplitSteps) return rec_split_forward<T>(p, by, stream);
     if (by == 16) return n >= 2 * kManyColumns ? forward_v<T, 16, 2>(p, stream) : forward_v<T, 16, 1>(p, stream);
+    if (by != kPairs<T> && by_granules(p, 32, 32, 0, {&p.z, &p.x, &p.y})) return forward_v<T, -(int)sizeof(T), 1>(p, stream);
     if constexpr (sizeof(T) == 2)
         if (by == 2) return forward_v<T, 2, 1>(p, stream);
     return forward_v<T, 4, 1>(p, stream);
@@ -509,9 +581,13 @@ template <typename T> cudaError_t backward(const RecArgs& p, cudaStream_t stream
         // two columns per lane save instructions (16x2048x1024 bf16: 71 us against 84); with fp32
         // tensors, which are bound by memory, one is faster (104 us against 115)
         if (by == 16 && n >= 2 * kManyColumns) return backward_v<T, 16, 2>(p, stream);
-        if (by == 2) return backward_v<T, 2, 1>(p, stream);
     }
-    return by == 16 ? backward_v<T, 16, 1>(p, stream) : backward_v<T, 4, 1>(p, stream);
+    if (by == 16) return backward_v<T, 16, 1>(p, stream);
+    if (by != kPairs<T> && by_granules(p, 32, 32, 0, {&p.z, &p.x, &p.dy, &p.dz, &p.dx}))
+        return backward_v<T, -(int)sizeof(T), 1>(p, stream);
+    if constexpr (sizeof(T) == 2)
+        if (by == 2) return backward_v<T, 2, 1>(p, stream);
+    return backward_v<T, 4, 1>(p, stream);
 }
 
 bool rec_seq_ok(const RecSeq& s, int64_t batch, int64_t steps, int64_t channels, bool written)

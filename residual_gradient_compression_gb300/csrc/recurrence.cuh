@@ -1,6 +1,7 @@
 // Shared by the recurrence's kernels: their arguments, the gate, and addresses of rows.
 #pragma once
 
+#include <initializer_list>
 #include <type_traits>
 
 #include "train_common.cuh"
@@ -61,10 +62,28 @@ template <typename T> __device__ __forceinline__ T* moved(T* p, int64_t bytes)
     return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + bytes);
 }
 
+// kBytes, by which the kernels take a tensor's rows: 16, 4 or 2 bytes at a time as they are
+// aligned, or less than zero: rows of elements of -kBytes bytes without alignment, by the
+// aligned 16 bytes that hold them (a copy of four bytes costs as much as one of 16).
+// Tiles are then of one sequence's channels (kApart), and otherwise of all sequences'
+// numbered through, so that few channels fill a tile too.
+template <int kBytes> constexpr bool kApart = kBytes == 16 || kBytes < 0;
+
 // Distances between rows, in bytes: in 32 bits where the rows are read 16 bytes at a time
 // (the host sees to it), so that an address is one instruction.
-template <int kBytes>
-using Distance = typename std::conditional<kBytes == 16 || kBytes < 0, int32_t, int64_t>::type;
+template <int kBytes> using Distance = typename std::conditional<kApart<kBytes>, int32_t, int64_t>::type;
+
+// Whether rows without alignment are taken by the aligned 16 bytes that hold them, in tiles of
+// `cols` of one sequence's channels: unless that makes more tiles than channels that are numbered
+// through do by `through`, and more than `most`.
+inline bool by_granules(const RecArgs& p, int64_t cols, int64_t through, int64_t most,
+                        std::initializer_list<const RecSeq*> seqs)
+{
+    const int64_t apart = p.batch * ((p.channels + cols - 1) / cols), tiles = (p.batch * p.channels + through - 1) / through;
+    bool fits = p.channels >= 32 && (4 * apart <= 5 * tiles || apart <= most);
+    for (const RecSeq* s : seqs) fits = fits && s->step < (int64_t)1 << 22;  // a tile's steps span less than 2^31 bytes
+    return fits;
+}
 
 }  // namespace
 }  // namespace adacomp

@@ -1,6 +1,5 @@
 // The recurrence where there are few columns: the steps split over warps, CTAs and clusters.
 #include <cmath>
-#include <initializer_list>
 
 #include "recurrence.cuh"
 
@@ -38,14 +37,9 @@ constexpr int kCols = 64, kSteps = 8, kWarps = 8, kThreads = 32 * kWarps, kSpan 
 constexpr int kTile = kSpan * kCols;  // elements of a tensor that a CTA has in a round
 static_assert(kRecChunk == kSpan, "a kept state for every CTA");
 
-// kBytes, by which the kernels take the rows: 16, 4 or 2 bytes at a time as they are aligned, or
-// less than zero: rows of elements of -kBytes bytes without alignment, by the aligned 16 bytes
-// that hold them, the first and last of which may hold a neighbour's elements too (a copy of four
-// bytes costs as much as one of 16). Such a tile has as many columns as 64 elements hold wherever
-// its row begins in the first 16 bytes.
+// A tile's columns: of rows without alignment, as many as 64 elements hold wherever the row
+// begins in the first 16 bytes.
 template <int kBytes> constexpr int kTileCols = kBytes > 0 ? kCols : kCols + 1 + 16 / kBytes;
-// Tiles of one sequence's channels, or of all sequences' numbered through.
-template <int kBytes> constexpr bool kApart = kBytes == 16 || kBytes < 0;
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -625,18 +619,10 @@ cudaError_t launch_ranks(int cols, int shared, const RecArgs& p, cudaStream_t st
     return cudaLaunchKernelEx(&cfg, kern, p, ranks);
 }
 
-// Whether rows without alignment are taken by the aligned 16 bytes that hold them: unless that
-// makes more tiles, as it does of few channels beyond a tile's, and more than run at once.
-// Training step, us with it and without: 4 x 20011 x 501 fp32 289 and 417, 4 x 4096 x 1001 bf16
-// 120 and 174, 32 x 4096 x 33 fp32 55 and 70; 32 x 4096 x 62 fp32 (two tiles for one) 115 and 93.
-template <typename T> bool by_granules(const RecArgs& p, std::initializer_list<const RecSeq*> seqs)
-{
-    constexpr int64_t cols = kTileCols<-(int)sizeof(T)>;
-    const int64_t apart = p.batch * ((p.channels + cols - 1) / cols), through = (p.batch * p.channels + kCols - 1) / kCols;
-    bool fits = p.channels >= 32 && (4 * apart <= 5 * through || apart <= 38);
-    for (const RecSeq* s : seqs) fits = fits && s->step < (int64_t)1 << 22;  // a tile's steps span less than 2^31 bytes
-    return fits;
-}
+// Rows without alignment (a training step's us by 16 bytes and by four or two): 4 x 20011 x 501
+// fp32 290 and 417, 4 x 4096 x 1001 bf16 121 and 174; 32 x 4096 x 33 fp32, twice as many tiles but
+// all running at once, 55 and 70; 32 x 4096 x 62 fp32, more than that, 115 and 93.
+constexpr int64_t kAtOnce = 38;
 
 template <typename T, int kBytes> cudaError_t forward_ranks(const RecArgs& p, cudaStream_t stream)
 {
@@ -655,7 +641,8 @@ template <typename T, int kBytes> cudaError_t backward_ranks(const RecArgs& p, c
 template <typename T> cudaError_t rec_split_forward(const RecArgs& p, int by, cudaStream_t stream)
 {
     if (by == 16) return forward_ranks<T, 16>(p, stream);
-    if (by_granules<T>(p, {&p.z, &p.x, &p.y})) return forward_ranks<T, -(int)sizeof(T)>(p, stream);
+    if (by_granules(p, kTileCols<-(int)sizeof(T)>, kCols, kAtOnce, {&p.z, &p.x, &p.y}))
+        return forward_ranks<T, -(int)sizeof(T)>(p, stream);
     if constexpr (sizeof(T) == 2)
         if (by == 2) return forward_ranks<T, 2>(p, stream);
     return forward_ranks<T, 4>(p, stream);
@@ -664,7 +651,8 @@ template <typename T> cudaError_t rec_split_forward(const RecArgs& p, int by, cu
 template <typename T> cudaError_t rec_split_backward(const RecArgs& p, int by, cudaStream_t stream)
 {
     if (by == 16) return backward_ranks<T, 16>(p, stream);
-    if (by_granules<T>(p, {&p.z, &p.x, &p.dy, &p.dz, &p.dx})) return backward_ranks<T, -(int)sizeof(T)>(p, stream);
+    if (by_granules(p, kTileCols<-(int)sizeof(T)>, kCols, kAtOnce, {&p.z, &p.x, &p.dy, &p.dz, &p.dx}))
+        return backward_ranks<T, -(int)sizeof(T)>(p, stream);
     if constexpr (sizeof(T) == 2)
         if (by == 2) return backward_ranks<T, 2>(p, stream);
     return backward_ranks<T, 4>(p, stream);
