@@ -50,9 +50,8 @@ template <typename T> __global__ void __launch_bounds__(kRecThreads) rec_forward
 // Bound by memory and, in bf16, nearly as much by instructions (23 per element forward, 43
 // backward). Measured over 16 sequences of 2048 steps and 1024 channels: forward 35 us in bf16
 // (5.7 TB/s) and 65 in fp32 (6.2), backward 71 (4.7) and 104 (6.4). Rows that are not aligned
-// to 16 bytes are copied by 4 bytes, or, for bf16 at odd places, loaded by 2: with 1023
-// channels 80 and 173 us in bf16, 141 and 209 in fp32. Loading them to registers instead
-// measured 132 and 281 us in bf16.
+// to 16 bytes: with 1023 channels 58 and 115 us in bf16, 79 and 146 in fp32; there each row's
+// place in its 16 bytes is found again for every tensor, and its results are written one by one.
 constexpr int kWarps = 8;
 
 __device__ __forceinline__ void hand_on(int barrier)
@@ -544,11 +543,19 @@ template <typename T, int kBytes, int kV> cudaError_t backward_v(const RecArgs& 
         2 * 3 * CopierOf<T, kBytes, 32 * kV, kBackward<kV>, 3>::kElements * (int)sizeof(T), stream);
 }
 
-// How a call is split. Many columns: a CTA for 64 or 32 of them, if that makes one for every
-// SM; otherwise, if there are steps to split, clusters (recurrence_split.cu; 4x4096x1001 bf16:
-// forward 56 us with clusters, 89 without, backward 124 and 297).
+// How a call is split, by the columns n = batch * channels, in us with the choice and without. Many
+// columns: a CTA for 64 or 32 of them, if that makes one for every SM; otherwise, if there are
+// steps to split, clusters (4x4096x1001 bf16: forward 34 with clusters, 62 without, backward 86
+// and 151). The backward pass, whose chain from one kept state to the next is longer, wants
+// clusters also where there are up to twice as many columns and the chain is long (5x4096x1000
+// bf16 70 and 141, 6x1500x1024 fp32 42 and 49; but 8x1000x1024 fp32 40 and 36), fewer where rows
+// are off alignment (5x4096x1001 fp32 101 and 147; but 9x4096x1001 164 and 147).
 constexpr int64_t kManyColumns = 152 * 32;
 constexpr int64_t kSplitSteps = 128;
+constexpr int64_t kLongSteps = 1200;
+// A CTA for 64 columns, two per lane, saves instructions and halves the CTAs (forward: 16x2048x1024
+// fp32 65, with 32 columns 69; but 12x2048x1024 58 and 47).
+constexpr int64_t kTwoColumns = 3 * kManyColumns;
 
 // Rows without alignment (forward and backward us by 16 bytes, and by four or two): 16 x 2048 x 1023
 // fp32 79 and 146, 141 and 208; bf16 58 and 115, 79 and 172. But rows of pairs of bf16 elements
@@ -565,7 +572,7 @@ template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
     }
     const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.y});
     if (n < kManyColumns && p.steps > kSplitSteps) return rec_split_forward<T>(p, by, stream);
-    if (by == 16) return n >= 2 * kManyColumns ? forward_v<T, 16, 2>(p, stream) : forward_v<T, 16, 1>(p, stream);
+    if (by == 16) return n >= kTwoColumns ? forward_v<T, 16, 2>(p, stream) : forward_v<T, 16, 1>(p, stream);
     if (by != kPairs<T> && by_granules(p, 32, 32, 0, {&p.z, &p.x, &p.y})) return forward_v<T, -(int)sizeof(T), 1>(p, stream);
     if constexpr (sizeof(T) == 2)
         if (by == 2) return forward_v<T, 2, 1>(p, stream);
@@ -576,11 +583,12 @@ template <typename T> cudaError_t backward(const RecArgs& p, cudaStream_t stream
 {
     const int64_t n = p.batch * p.channels;
     const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.dy, &p.dz, &p.dx});
-    if (n < kManyColumns && p.steps > kSplitSteps) return rec_split_backward<T>(p, by, stream);
+    const int64_t many = p.steps < kLongSteps ? kManyColumns : by == 16 ? 2 * kManyColumns : kManyColumns * 3 / 2;
+    if (n < many && p.steps > kSplitSteps) return rec_split_backward<T>(p, by, stream);
     if constexpr (sizeof(T) == 2) {
         // two columns per lane save instructions (16x2048x1024 bf16: 71 us against 84); with fp32
         // tensors, which are bound by memory, one is faster (104 us against 115)
-        if (by == 16 && n >= 2 * kManyColumns) return backward_v<T, 16, 2>(p, stream);
+        if (by == 16 && n >= kTwoColumns) return backward_v<T, 16, 2>(p, stream);
     }
     if (by == 16) return backward_v<T, 16, 1>(p, stream);
     if (by != kPairs<T> && by_granules(p, 32, 32, 0, {&p.z, &p.x, &p.dy, &p.dz, &p.dx}))
