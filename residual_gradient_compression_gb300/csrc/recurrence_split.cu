@@ -318,7 +318,189 @@ template <int kBytes> __device__ __forceinline__ float* kept(const RecArgs& p, c
     return p.carry + (col.b * p.chunks + t / kRecChunk) * p.channels + col.c;
 }
 
-template <typename T, int kBytes>
+// ---------------------------------------------------------------- chunks at once
+// Few columns of many steps leave most SMs without work even so. There every chunk of 64 steps
+// has a CTA of its own, in three kernels: what each chunk does to a state; the states before the
+// chunks (the gradients after them), by the columns; and each chunk's results from these, for
+// which the inputs are read again, mostly from L2. The first two hand on through the rows of
+// the chunk's own outputs, which the third writes last: no workspace is needed for them.
+template <typename T> struct Place {  // of an fp32 value in two rows, of which fp32 rows need one
+    T *high, *low;
+    __device__ __forceinline__ void put(float v) const
+    {
+        if constexpr (sizeof(T) == 4) {
+            *high = v;
+        } else {
+            *reinterpret_cast<uint16_t*>(high) = (uint16_t)(__float_as_uint(v) >> 16);
+            *reinterpret_cast<uint16_t*>(low) = (uint16_t)__float_as_uint(v);
+        }
+    }
+    __device__ __forceinline__ float get() const
+    {
+        if constexpr (sizeof(T) == 4) return *high;
+        else
+            return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(high) << 16 |
+                                   *reinterpret_cast<const uint16_t*>(low));
+    }
+};
+
+// The places of values at a chunk's first steps: the two that the first kernel leaves, and the one
+// that the third begins with, apart from them, as the second writes it while it reads them; but
+// the last chunk may be short, and has one place for both. The forward pass has them in the rows of
+// y, the backward pass in those of dz and dx, where one of each holds a value.
+__device__ __forceinline__ int begin_place(bool last) { return last ? 0 : 2; }
+
+template <typename T, bool kBack> __device__ __forceinline__ Place<T> place_at(const RecArgs& p, int64_t b, int64_t c, int64_t t, int i)
+{
+    if constexpr (kBack) {
+        if constexpr (sizeof(T) == 4) return {at<T>(i & 1 ? p.dx : p.dz, b, t + i / 2, c), nullptr};
+        else return {at<T>(p.dz, b, t + i, c), at<T>(p.dx, b, t + i, c)};
+    } else {
+        if constexpr (sizeof(T) == 4) return {at<T>(p.y, b, t + i, c), nullptr};
+        else return {at<T>(p.y, b, t + 2 * i, c), at<T>(p.y, b, t + 2 * i + 1, c)};
+    }
+}
+
+template <typename T, bool kBack, int kBytes>
+__device__ __forceinline__ Two begin_of(const RecArgs& p, const Column<kBytes> (&col)[2], int32_t t, bool last)
+{
+    const int place = begin_place(last);
+    float v[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (col[j].on) v[j] = place_at<T, kBack>(p, col[j].b, col[j].c, t, place).get();
+    return two_of(v[0], v[1]);
+}
+
+// The first kernel: a CTA's chunk, h -> A h + H (not of the last chunk), or p -> A p + P (not of
+// the first; of the last, p itself).
+template <typename T, int kBytes, bool kBack>
+__global__ void __launch_bounds__(kThreads, 4) rec_totals_kernel(const __grid_constant__ RecArgs p, const uint32_t chunks)
+{
+    extern __shared__ __align__(16) uint8_t shared_bytes[];
+    __shared__ float4 part[kWarps][32];
+    T* const tile_at = reinterpret_cast<T*>(shared_bytes);
+    ptx::griddep_wait();
+    const uint32_t tile = blockIdx.x / (chunks - 1);
+    const int32_t tc = (int32_t)(blockIdx.x - tile * (chunks - 1) + (kBack ? 1 : 0)) * kSpan;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Column<kBytes> col[2] = {Column<kBytes>(p, tile, place_of<kBytes>(lane, 0)),
+                                  Column<kBytes>(p, tile, place_of<kBytes>(lane, 1))};
+    const Copier<T, kBytes, 2> copier(p, tile, {&p.z, kBack ? &p.dy : &p.x});
+    copier.copy(tile_at, tc);
+    copies_wait();
+    __syncthreads();
+    const int32_t ts = tc + warp * kSteps;
+    const Live at_hand(p, col, ts);
+    const T* const first = tile_at + warp * kSteps * kCols + place_of<kBytes>(lane, 0);
+    Two A = two_of(1.0f), H = two_of(0.0f);
+    const auto form = [&](auto masked) {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            float v[2][2], a0, a1, b0, b1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const T* q = first + i * kTile + k * kCols;
+                two<kBytes>(kBytes < 0 ? moved(q, copier.before(i, ts + k)) : q, v[i][0], v[i][1]);
+            }
+            gate(v[0][0], &a0, &b0);
+            gate(v[0][1], &a1, &b1);
+            if (masked.value) {
+                if (k >= at_hand.live0) a0 = 1.0f, b0 = v[1][0] = 0.0f;
+                if (k >= at_hand.live1) a1 = 1.0f, b1 = v[1][1] = 0.0f;
+            }
+            const Two a = two_of(a0, a1), u = two_of(v[1][0], v[1][1]);
+            A = A * a;
+            if (kBack) H = fma2(A, u, H);
+            else H = fma2(a, H, two_of(b0, b1) * u);
+        }
+    };
+    if (at_hand.all) form(std::false_type());
+    else form(std::true_type());
+    part[warp][lane] = quad(A, H);
+    __syncthreads();
+    if (warp != 0) return;
+    A = two_of(1.0f), H = two_of(0.0f);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        const float4 q = part[kBack ? kWarps - 1 - i : i][lane];
+        H = fma2(low(q), H, high(q));
+        A = A * low(q);
+    }
+    const bool last = kBack && tc + kSpan >= (int32_t)p.steps;
+    if (last) A = fma2(A, load_state(p.dh_last, p, col), H);
+    const float v[2][2] = {{A.x, H.x}, {A.y, H.y}};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (!col[j].on) continue;
+        place_at<T, kBack>(p, col[j].b, col[j].c, tc, 0).put(v[j][0]);
+        if (!last) place_at<T, kBack>(p, col[j].b, col[j].c, tc, 1).put(v[j][1]);
+    }
+}
+
+// The second: 32 columns per CTA, whose warps have consecutive chunks each.
+constexpr int kStateWarps = 32;
+
+template <typename T, bool kBack>
+__global__ void __launch_bounds__(32 * kStateWarps) rec_states_kernel(const __grid_constant__ RecArgs p, const uint32_t chunks)
+{
+    __shared__ float2 part[kStateWarps][32];
+    ptx::griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+    const bool on = i < p.batch * p.channels;
+    const int64_t b = on ? i / p.channels : 0, c = on ? i - b * p.channels : 0;
+    // Turn k: the step from chunk k to k + 1, or back from chunk `chunks - 1 - k` (its gradient
+    // is given) to the one before it.
+    const int32_t turns = (int32_t)chunks - 1, each = (turns + kStateWarps - 1) / kStateWarps;
+    const int32_t begin = min(turns, warp * each), end = min(turns, begin + each);
+    const auto chunk_of = [&](int32_t k) { return kBack ? (int32_t)chunks - 1 - k : k; };
+    const auto step_of = [&](int32_t k) {
+        const int64_t t = (int64_t)chunk_of(k) * kSpan;
+        float2 v = make_float2(1.0f, 0.0f);
+        if (on) {
+            v.x = place_at<T, kBack>(p, b, c, t, 0).get();
+            if (kBack && k == 0) v = make_float2(0.0f, v.x);
+            else v.y = place_at<T, kBack>(p, b, c, t, 1).get();
+        }
+        return v;
+    };
+    float2 own = make_float2(1.0f, 0.0f);
+#pragma unroll 8
+    for (int32_t k = begin; k < end; ++k) {
+        const float2 v = step_of(k);
+        own.y = fmaf(v.x, own.y, v.y);
+        own.x *= v.x;
+    }
+    part[warp][lane] = own;
+    __syncthreads();
+    float h = !kBack && p.h0 && on ? p.h0[i] : 0.0f;
+    const auto hand = [&](int32_t chunk, float v) {
+        if (!kBack && p.carry) p.carry[(b * p.chunks + chunk) * p.channels + c] = v;
+        else place_at<T, kBack>(p, b, c, (int64_t)chunk * kSpan, begin_place(chunk + 1 == (int32_t)chunks)).put(v);
+    };
+    if (!kBack && on && warp == 0) hand(0, h);
+    for (int w = 0; w < warp; ++w) h = fmaf(part[w][lane].x, h, part[w][lane].y);
+    for (int32_t k0 = begin; k0 < end; k0 += 8) {
+        float2 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (k0 + j < end) v[j] = step_of(k0 + j);
+        if (!on) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int32_t k = k0 + j;
+            if (k >= end) break;
+            h = fmaf(v[j].x, h, v[j].y);
+            // (where dh0 is dh_last itself, the third kernel cannot read it)
+            if (kBack && k == 0) hand((int32_t)chunks - 1, p.dh_last ? p.dh_last[i] : 0.0f);
+            hand(chunk_of(k) + (kBack ? -1 : 1), h);
+        }
+    }
+}
+
+// ranks: the CTAs of a cluster, or (kChunks) the chunks of a sequence, with their states at hand.
+template <typename T, int kBytes, bool kChunks>
 __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
 {
     extern __shared__ __align__(16) uint8_t shared_bytes[];
@@ -327,19 +509,22 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
     __shared__ Exchange<kRanks<T, kBytes>> exchange[2];
     const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (2 * kTile); };
     ptx::griddep_wait();
-    if (ranks > 1) {
+    if (!kChunks && ranks > 1) {
         exchange_init(exchange);
         cluster_sync();  // all CTAs run, and their barriers are there, before one writes to another
     }
-    const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
+    const uint32_t tile = blockIdx.x / ranks, rank = kChunks ? blockIdx.x - tile * ranks : ranks > 1 ? cluster_rank() : 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Column<kBytes> col[2] = {Column<kBytes>(p, tile, place_of<kBytes>(lane, 0)),
                                   Column<kBytes>(p, tile, place_of<kBytes>(lane, 1))};
     const Copier<T, kBytes, 2> copier(p, tile, {&p.z, &p.x});
     const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
-    Two h0 = load_state(p.h0, p, col);  // before the round's first step (the joining warp's)
-    bool given_up = false;
     int32_t tc = (int32_t)rank * kSpan;
+    Two h0;  // before the round's first step (the joining warp's)
+    if (!kChunks) h0 = load_state(p.h0, p, col);
+    else if (p.carry) h0 = two_of(col[0].on ? *kept(p, col[0], tc) : 0.0f, col[1].on ? *kept(p, col[1], tc) : 0.0f);
+    else if (warp == 0) h0 = begin_of<T, false>(p, col, tc, rank + 1 == ranks);
+    bool given_up = false;
     copier.copy(tile_of(0), tc);
     for (int32_t t0 = 0, round = 0; t0 < steps; t0 += span, tc += span, ++round) {
         const int par = round & 1;
@@ -378,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
         __syncthreads();
         if (warp == 0) {
             Two h = h0;  // before the CTA's first step
-            if (ranks > 1) {
+            if (!kChunks && ranks > 1) {
                 Exchange<kRanks<T, kBytes>>& x = exchange[par];
                 if (lane == 0) exchange_expect(&x, ranks * 512);
                 Two tA = two_of(1.0f), tH = two_of(0.0f);
@@ -397,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
                 }
                 if (given_up) h = h0 = two_of(NAN);
             }
-            if (p.carry && tc < steps) {
+            if (!kChunks && p.carry && tc < steps) {
                 const Two v = h;
                 if (col[0].on) *kept(p, col[0], tc) = v.x;
                 if (col[1].on) *kept(p, col[1], tc) = v.y;
@@ -408,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
                 const float4 q = part[w][lane];
                 h = fma2(low(q), h, high(q));
             }
-            if (ranks == 1) h0 = h;
+            if (kChunks || ranks == 1) h0 = h;
         }
         __syncthreads();
         Two h = begin[warp][lane];
@@ -429,15 +614,15 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
             }
         }
     }
-    if (rank == 0 && warp == 0) store_state(p.h_last, p, col, h0);
-    if (ranks > 1) cluster_meet();  // no CTA ends while another may write to it
+    if (rank == (kChunks ? ranks - 1 : 0) && warp == 0) store_state(p.h_last, p, col, h0);
+    if (!kChunks && ranks > 1) cluster_meet();  // no CTA ends while another may write to it
 }
 
 // The reverse of it: p, the gradient that reaches a state from the steps after it, goes
 // through a warp's steps as p -> A p + P, P = sum of dy_k times the gates up to and with
 // step k. The states are formed again from the one that the forward pass kept for the CTA's
 // steps: that is less to read than y, and not rounded.
-template <typename T, int kBytes>
+template <typename T, int kBytes, bool kChunks>
 __global__ void __launch_bounds__(kThreads, kBytes == 4 || kBytes == -4 ? 2 : 3) rec_backward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
 {
     extern __shared__ __align__(16) uint8_t shared_bytes[];
@@ -447,18 +632,20 @@ __global__ void __launch_bounds__(kThreads, kBytes == 4 || kBytes == -4 ? 2 : 3)
     __shared__ Exchange<kRanks<T, kBytes>> exchange[2];
     const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (3 * kTile); };
     ptx::griddep_wait();
-    if (ranks > 1) {
+    if (!kChunks && ranks > 1) {
         exchange_init(exchange);
         cluster_sync();  // all CTAs run, and their barriers are there, before one writes to another
     }
-    const uint32_t rank = ranks > 1 ? cluster_rank() : 0, tile = blockIdx.x / ranks;
+    const uint32_t tile = blockIdx.x / ranks, rank = kChunks ? blockIdx.x - tile * ranks : ranks > 1 ? cluster_rank() : 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Column<kBytes> col[2] = {Column<kBytes>(p, tile, place_of<kBytes>(lane, 0)),
                                   Column<kBytes>(p, tile, place_of<kBytes>(lane, 1))};
     const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
     int32_t t0 = steps > 0 ? (steps - 1) / span * span : -1, tc = t0 + (int32_t)rank * kSpan;
     const Copier<T, kBytes, 3> copier(p, tile, {&p.z, &p.x, &p.dy});
-    Two p0 = load_state(p.dh_last, p, col);  // after the round's last step (the joining warp's)
+    Two p0;  // after the round's last step (the joining warp's)
+    if (!kChunks) p0 = load_state(p.dh_last, p, col);
+    else if (warp == kWarps - 1) p0 = begin_of<T, true>(p, col, tc, rank + 1 == ranks);
     bool given_up = false;
     if (t0 >= 0) copier.copy(tile_of(0), tc);
     for (int32_t round = 0; t0 >= 0; t0 -= span, tc -= span, ++round) {
@@ -529,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, kBytes == 4 || kBytes == -4 ? 2 : 3)
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w)
                 tP = fma2(low(part[w][lane]), tP, grad[w][lane]);
-            if (ranks > 1) {
+            if (!kChunks && ranks > 1) {
                 Exchange<kRanks<T, kBytes>>& x = exchange[par];
                 if (lane == 0) exchange_expect(&x, ranks * 512);
                 for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tP));
@@ -577,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, kBytes == 4 || kBytes == -4 ? 2 : 3)
         else finish(std::true_type());
     }
     if (rank == 0 && warp == kWarps - 1) store_state(p.dh0, p, col, p0);
-    if (ranks > 1) cluster_meet();  // no CTA ends while another may write to it
+    if (!kChunks && ranks > 1) cluster_meet();  // no CTA ends while another may write to it
 }
 
 // Launches a kernel of clusters, behind the kernel ahead of it as launch_after does.
@@ -624,38 +811,77 @@ cudaError_t launch_ranks(int cols, int shared, const RecArgs& p, cudaStream_t st
 // all running at once, 55 and 70; 32 x 4096 x 62 fp32, more than that, 115 and 93.
 constexpr int64_t kAtOnce = 38;
 
-template <typename T, int kBytes> cudaError_t forward_ranks(const RecArgs& p, cudaStream_t stream)
+// Whether every chunk has a CTA of its own, which costs their number, and three launches, where
+// clusters cost the number of their rounds: forward and backward us with it and without, 1 x 9918
+// x 3 fp32 14 and 15, 44 and 53; 233 x 1500 x 1 16 and 20, 19 and 34; 1 x 32768 x 1024 117 and
+// 167, 147 and 214 (bf16, with clusters of 16, 98 and 144, 87 and 131); 16 x 9656 x 133 98 and
+// 150, 76 and 146; 1 x 1000000 x 8 372 and 661, 4095 and 4996.
+template <typename T, int kBytes> bool by_chunks(const RecArgs& p, int64_t tiles, int64_t chunks)
 {
-    constexpr int cols = kApart<kBytes> ? kTileCols<kBytes> : 0, pad = kBytes < 0 ? 16 : 0;
-    return launch_ranks<kRanks<T, kBytes>, rec_forward_kernel<T, kBytes>>(cols, 4 * kTile * (int)sizeof(T) + pad, p, stream);
+    // the last chunk's beginning needs two rows of bf16 elements, if it is not in the carry
+    if (!p.carry && sizeof(T) == 2 && p.steps % kSpan == 1) return false;
+    return kRanks<T, kBytes> > 8 ? tiles * chunks + 800 <= 15 * chunks : tiles * chunks + 400 <= 22 * chunks;
 }
 
-template <typename T, int kBytes> cudaError_t backward_ranks(const RecArgs& p, cudaStream_t stream)
+// Launches a kernel with a CTA for each of `chunks` chunks of every tile.
+template <void (*kern)(RecArgs, uint32_t)>
+cudaError_t launch_chunks(int64_t tiles, uint32_t grid, uint32_t chunks, int shared, const RecArgs& p, cudaStream_t stream)
+{
+    static bool set[64] = {};  // the kernel's shared memory, once per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+    if (e == cudaSuccess && !set[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+        set[dev] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess) return e;
+    return launch_after(kern, dim3((unsigned)(tiles * grid)), dim3(kThreads), (size_t)shared, stream, p, chunks);
+}
+
+template <typename T, int kBytes, bool kBack> cudaError_t run(const RecArgs& p, cudaStream_t stream)
 {
     constexpr int cols = kApart<kBytes> ? kTileCols<kBytes> : 0, pad = kBytes < 0 ? 16 : 0;
-    return launch_ranks<kRanks<T, kBytes>, rec_backward_kernel<T, kBytes>>(cols, 6 * kTile * (int)sizeof(T) + pad, p, stream);
+    constexpr int one = kTile * (int)sizeof(T), tensors = kBack ? 3 : 2;
+    const int64_t tiles = cols ? p.batch * ((p.channels + cols - 1) / cols) : (p.batch * p.channels + kCols - 1) / kCols;
+    const int64_t chunks = (p.steps + kSpan - 1) / kSpan;
+    if (by_chunks<T, kBytes>(p, tiles, chunks)) {
+        const uint32_t n = (uint32_t)chunks;
+        cudaError_t e =
+            launch_chunks<rec_totals_kernel<T, kBytes, kBack>>(tiles, n - 1, n, 2 * one + pad, p, stream);
+        if (e != cudaSuccess) return e;
+        e = launch_after(rec_states_kernel<T, kBack>, dim3((unsigned)((p.batch * p.channels + 31) / 32)),
+                         dim3(32 * kStateWarps), 0, stream, p, n);
+        if (e != cudaSuccess) return e;
+        if constexpr (kBack)
+            return launch_chunks<rec_backward_kernel<T, kBytes, true>>(tiles, n, n, tensors * one + pad, p, stream);
+        else return launch_chunks<rec_forward_kernel<T, kBytes, true>>(tiles, n, n, tensors * one + pad, p, stream);
+    }
+    if constexpr (kBack)
+        return launch_ranks<kRanks<T, kBytes>, rec_backward_kernel<T, kBytes, false>>(cols, 2 * tensors * one + pad, p, stream);
+    else return launch_ranks<kRanks<T, kBytes>, rec_forward_kernel<T, kBytes, false>>(cols, 2 * tensors * one + pad, p, stream);
 }
 
 }  // namespace
 
 template <typename T> cudaError_t rec_split_forward(const RecArgs& p, int by, cudaStream_t stream)
 {
-    if (by == 16) return forward_ranks<T, 16>(p, stream);
+    if (by == 16) return run<T, 16, false>(p, stream);
     if (by_granules(p, kTileCols<-(int)sizeof(T)>, kCols, kAtOnce, {&p.z, &p.x, &p.y}))
-        return forward_ranks<T, -(int)sizeof(T)>(p, stream);
+        return run<T, -(int)sizeof(T), false>(p, stream);
     if constexpr (sizeof(T) == 2)
-        if (by == 2) return forward_ranks<T, 2>(p, stream);
-    return forward_ranks<T, 4>(p, stream);
+        if (by == 2) return run<T, 2, false>(p, stream);
+    return run<T, 4, false>(p, stream);
 }
 
 template <typename T> cudaError_t rec_split_backward(const RecArgs& p, int by, cudaStream_t stream)
 {
-    if (by == 16) return backward_ranks<T, 16>(p, stream);
+    if (by == 16) return run<T, 16, true>(p, stream);
     if (by_granules(p, kTileCols<-(int)sizeof(T)>, kCols, kAtOnce, {&p.z, &p.x, &p.dy, &p.dz, &p.dx}))
-        return backward_ranks<T, -(int)sizeof(T)>(p, stream);
+        return run<T, -(int)sizeof(T), true>(p, stream);
     if constexpr (sizeof(T) == 2)
-        if (by == 2) return backward_ranks<T, 2>(p, stream);
-    return backward_ranks<T, 4>(p, stream);
+        if (by == 2) return run<T, 2, true>(p, stream);
+    return run<T, 4, true>(p, stream);
 }
 
 template cudaError_t rec_split_forward<float>(const RecArgs&, int, cudaStream_t);

@@ -149,6 +149,29 @@ def test_rows_off_every_alignment(batch, steps, ch, dt):
             assert bool(whole.isnan().all())
 
 
+@pytest.mark.parametrize("dt", [F, B])
+@pytest.mark.parametrize("batch,steps,ch", [(1, 2000, 5), (1, 3713, 33), (30, 1345, 1), (2, 1700, 130)])
+def test_long_sequences_of_few_channels(batch, steps, ch, dt):
+    """Ragged, with and without the kept states, and with the states replaced in place."""
+    z, x, h0, dy, dh = _inputs(steps + ch, batch, steps, ch, dt)
+    lengths = torch.tensor([steps - 700 * (b % 3) for b in range(batch)], dtype=torch.int32, device="cuda")
+    got = _run(z, x, h0, lengths, dy, dh)
+    ref, bound = recurrence(z, x, h0, lengths, dy, dh)
+    for name, g, r, e in zip(("y", "h_last", "dz", "dx", "dh0"), got, ref, bound):
+        assert_within(g, r, e, name)
+    h = ac.adacomp_recurrence_init(ch, CODE[dt])
+    y, dz, dx = (torch.full_like(z, -9.0) for _ in range(3))
+    state, carry, grad = h0.clone(), _carry(h, batch, steps), dh.clone()
+    ac.adacomp_recurrence_forward(h, z, x, y, h0=state, lengths=lengths, h_last=state)
+    for g, r, e, name in zip((y, state), ref, bound, ("y without carry", "h_last in place")):
+        assert_within(g, r, e, name)
+    ac.adacomp_recurrence_forward(h, z, x, y, h0=h0, lengths=lengths, carry=carry)
+    assert torch.equal(y, got[0])
+    ac.adacomp_recurrence_backward(h, z, x, dy, carry, dz, dx, lengths=lengths, dh_last=grad, dh0=grad)
+    for g, e in zip((dz, dx, grad), got[2:]):
+        assert torch.equal(g, e)
+
+
 def test_what_lies_between_the_rows_is_kept():
     batch, steps, ch = 2, 40, 21
     z, x, h0, dy, dh = _inputs(1, batch, steps, ch, B)
