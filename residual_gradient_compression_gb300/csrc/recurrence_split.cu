@@ -623,7 +623,8 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
 // step k. The states are formed again from the one that the forward pass kept for the CTA's
 // steps: that is less to read than y, and not rounded.
 template <typename T, int kBytes, bool kChunks>
-__global__ void __launch_bounds__(kThreads, kBytes == 4 || kBytes == -4 ? 2 : 3) rec_backward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
+__global__ void __launch_bounds__(kThreads, kBytes == 16 ? 3 : 2)
+    rec_backward_kernel(const __grid_constant__ RecArgs p, const uint32_t ranks)
 {
     extern __shared__ __align__(16) uint8_t shared_bytes[];
     __shared__ float4 part[kWarps][32];  // a warp's (A, H)
