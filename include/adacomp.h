@@ -363,7 +363,8 @@ adacomp_status adacomp_materialize_group(adacomp_layer_t h, float* const* residu
  * aligned to their element type only (ADACOMP_ERR_ALIGNMENT otherwise); aligned to
  * 16 bytes, with strides that keep every row so, they are read and written faster. What shares
  * 16 bytes, aligned to as many, with a row's elements may be read with them and is not used.
- * Outputs may not overlap inputs or each other unless a call says so. Sums, statistics
+ * Outputs may not overlap inputs or each other unless a call says so, and hold
+ * intermediate values while a call runs. Sums, statistics
  * and states are fp32 or wider; results are rounded to the output's type once. Calls
  * are deterministic. Non-finite inputs reach only the results that depend on them.
  * A handle holds sizes and types only and may be used by several host threads.
