@@ -165,7 +165,15 @@ template <typename X, typename W, int N> cudaError_t ln_forward_n(LnArgs a, cuda
     // next best. Aligned rows want many elements for each of few threads (16384 x 2048 bf16: two
     // warps 25, one warp of 64 each 28, four of 16 each 27; 32768 x 1024 bf16: one warp 24, 64
     // each 32), fp32 rows of 2049 to 4096 less so (8192 x 4096: 41, four warps of 32 each 43).
-    if (a.dim > 8192) return with(ln_forward_row_kernel<X, W, M, 64, 8>, 256, 256);
+    // Few rows: as many threads as there can be, for the loads' latency (one row of 12745 fp32, caches
+    // cold: 15, eight warps 33; of 16384: 11 and 17), and so wide rows of two-byte pieces (4000 x
+    // 16383 bf16: 146 and 166, but fp32 169 and 150).
+    constexpr bool kShort = Piece<X, N>::kBytes == 2;
+    if (a.dim > 2048 && (a.rows <= 152 || (kShort && a.dim > 8192)))
+        return with(ln_forward_row_kernel<X, W, M, 16, 32>, 1024, 1024);
+    if constexpr (!kShort) {
+        if (a.dim > 8192) return with(ln_forward_row_kernel<X, W, M, 64, 8>, 256, 256);
+    }
     if (a.dim > 4096) return with(ln_forward_row_kernel<X, W, M, 32, 8>, 256, 256);
     if (a.dim > 2048) {
         if constexpr (kWhole && sizeof(X) == 2) return with(ln_forward_row_kernel<X, W, M, 32, 4>, 128, 128);

@@ -538,8 +538,11 @@ template <typename T, int kBytes, int kV> cudaError_t forward_v(const RecArgs& p
 
 template <typename T, int kBytes, int kV> cudaError_t backward_v(const RecArgs& p, cudaStream_t stream)
 {
+    // no warps without a chunk (135 x 11 x 2833 fp32: 52 us, and 74 with the others)
+    const int64_t chunks = (p.steps + kBackward<kV> - 1) / kBackward<kV>;
+    const int warps = chunks < 1 ? 1 : chunks < kBackWarps<kV> ? (int)chunks : kBackWarps<kV>;
     return launch_tiles<rec_backward_kernel<T, kBytes, kV>>(
-        p, kApart<kBytes>, 32 * kV, kBackWarps<kV>, kBackWarps<kV>,
+        p, kApart<kBytes>, 32 * kV, kBackWarps<kV>, warps,
         2 * 3 * CopierOf<T, kBytes, 32 * kV, kBackward<kV>, 3>::kElements * (int)sizeof(T), stream);
 }
 

@@ -90,7 +90,7 @@ WIDTHS = [w + d for w in (128, 256, 512, 1024, 2048, 4096, 8192, 16384) for d in
 @pytest.mark.parametrize("xt,wt", [(F, F), (B, F), (B, B)])
 @pytest.mark.parametrize("dim", WIDTHS)
 def test_widths(dim, xt, wt):
-    gen, rows = _gen(dim), 309
+    gen, rows = _gen(dim), 309  # more than SMs; below, in test_forward_and_backward, fewer
     h = ac.adacomp_layer_norm_init(dim, CODE[xt], CODE[wt], EPS)
     x = _rand(gen, rows, dim, dtype=xt, offset=0.5)
     w, b = _params(gen, dim, wt)
