@@ -14,10 +14,17 @@ namespace adacomp {
 namespace {
 
 constexpr int kRecThreads = 128;
-constexpr int kRecFew = 4;  // steps up to which a thread takes all of them
+// Steps up to which a thread takes all of a column's, and those up to which it does so where there
+// are many columns (32 forward; in the backward pass, which keeps them in registers, half of that).
+constexpr int kRecFew = 4, kRecSome = 32;
+constexpr int64_t kRecColumns = 152 * 128;
 
 // ---------------------------------------------------------------- few steps
-// One thread per column (a channel of a sequence), step after step.
+// One thread per column (a channel of a sequence), step after step; bound by memory where there
+// are many. A warp for 32 columns, as below, has a CTA of its own for so few steps, and the
+// CTAs' starts are what that waits for. us with this and with that, forward and backward:
+// 135 x 11 x 2833 fp32 10 and 15, 38 and 52; 1000 x 4 x 1024 fp32 13 and 13, the backward pass 136; 100 x 16 x
+// 4096 fp32 13 and 28, 22 and 60; forward 100 x 32 x 4096 fp32 34 and 36, 100 x 64 x 4096 63 and 58.
 template <typename T> __global__ void __launch_bounds__(kRecThreads) rec_forward_few_kernel(const RecArgs p)
 {
     ptx::griddep_wait();
@@ -25,16 +32,76 @@ template <typename T> __global__ void __launch_bounds__(kRecThreads) rec_forward
     if (i >= p.batch * p.channels) return;
     const int64_t b = i / p.channels, c = i - b * p.channels, len = length_of(p, b);
     float h = p.h0 ? p.h0[i] : 0.0f;
-    for (int64_t t = 0; t < p.steps; ++t) {
-        if (p.carry && t % kRecChunk == 0) p.carry[(b * p.chunks + t / kRecChunk) * p.channels + c] = h;
-        if (t < len) {
-            float a, r;
-            gate(to_f32(*at<T>(p.z, b, t, c)), &a, &r);
-            h = fmaf(a, h, r * to_f32(*at<T>(p.x, b, t, c)));
+    constexpr int S = 4;  // steps' loads on their way
+    const T* z = at<const T>(p.z, b, 0, c);
+    const T* x = at<const T>(p.x, b, 0, c);
+    T* y = at<T>(p.y, b, 0, c);
+    for (int64_t t0 = 0; t0 < p.steps; t0 += S) {
+        T zv[S], xv[S];
+#pragma unroll
+        for (int k = 0; k < S; ++k)
+            if (t0 + k < len) {
+                zv[k] = z[(t0 + k) * p.z.step];
+                xv[k] = x[(t0 + k) * p.x.step];
+            }
+        if (p.carry && t0 % kRecChunk == 0) p.carry[(b * p.chunks + t0 / kRecChunk) * p.channels + c] = h;
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+            if (t0 + k < len) {
+                float a, r;
+                gate(to_f32(zv[k]), &a, &r);
+                h = fmaf(a, h, r * to_f32(xv[k]));
+            }
+            if (t0 + k < p.steps) y[(t0 + k) * p.y.step] = from_f32<T>(t0 + k < len ? h : 0.0f);
         }
-        *at<T>(p.y, b, t, c) = from_f32<T>(t < len ? h : 0.0f);
     }
     if (p.h_last) p.h_last[i] = h;
+}
+
+template <typename T, int S> __global__ void __launch_bounds__(kRecThreads) rec_backward_few_kernel(const RecArgs p)
+{
+    ptx::griddep_wait();
+    const int64_t i = (int64_t)blockIdx.x * kRecThreads + threadIdx.x;
+    if (i >= p.batch * p.channels) return;
+    const int64_t b = i / p.channels, c = i - b * p.channels;
+    const int len = (int)length_of(p, b), steps = (int)p.steps;
+    const T* z = at<const T>(p.z, b, 0, c);
+    const T* x = at<const T>(p.x, b, 0, c);
+    const T* dy = at<const T>(p.dy, b, 0, c);
+    float h = p.carry[b * p.chunks * p.channels + c], q = p.dh_last ? p.dh_last[i] : 0.0f;
+    T zv[S], xv[S], dv[S];
+#pragma unroll
+    for (int k = 0; k < S; ++k)
+        if (k < len) {
+            zv[k] = z[k * p.z.step];
+            xv[k] = x[k * p.x.step];
+            dv[k] = dy[k * p.dy.step];
+        }
+    float a[S], r[S], before[S];  // before: h_{t-1} - x_t
+#pragma unroll
+    for (int k = 0; k < S; ++k)
+        if (k < len) {
+            gate(to_f32(zv[k]), &a[k], &r[k]);
+            const float v = to_f32(xv[k]);
+            before[k] = h - v;
+            h = fmaf(a[k], h, r[k] * v);
+        }
+    T* dz = at<T>(p.dz, b, 0, c);
+    T* dx = at<T>(p.dx, b, 0, c);
+#pragma unroll
+    for (int k = S - 1; k >= 0; --k) {
+        if (k >= steps) continue;
+        float gx = 0.0f, gz = 0.0f;
+        if (k < len) {
+            const float G = __fadd_rn(q, to_f32(dv[k]));
+            gx = r[k] * G;
+            gz = a[k] * gx * before[k];
+            q = __fmul_rn(a[k], G);
+        }
+        dx[k * p.dx.step] = from_f32<T>(gx);
+        dz[k * p.dz.step] = from_f32<T>(gz);
+    }
+    if (p.dh0) p.dh0[i] = q;
 }
 
 // ---------------------------------------------------------------- many steps
@@ -568,7 +635,7 @@ template <typename T> constexpr int kPairs = sizeof(T) == 2 ? 4 : 0;
 template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
 {
     const int64_t n = p.batch * p.channels;
-    if (p.steps <= kRecFew) {
+    if (p.steps <= kRecFew || (p.steps <= kRecSome && n >= kRecColumns)) {
         if (n > (int64_t)0x7fffffff * kRecThreads) return cudaErrorInvalidConfiguration;
         return launch_after(rec_forward_few_kernel<T>, dim3((unsigned)((n + kRecThreads - 1) / kRecThreads)),
                             dim3(kRecThreads), 0, stream, p);
@@ -585,6 +652,12 @@ template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
 template <typename T> cudaError_t backward(const RecArgs& p, cudaStream_t stream)
 {
     const int64_t n = p.batch * p.channels;
+    if (p.steps >= 1 && (p.steps <= kRecFew || (p.steps <= kRecSome / 2 && n >= kRecColumns))) {
+        if (n > (int64_t)0x7fffffff * kRecThreads) return cudaErrorInvalidConfiguration;
+        const dim3 grid((unsigned)((n + kRecThreads - 1) / kRecThreads));
+        return launch_after(p.steps <= kRecFew ? rec_backward_few_kernel<T, kRecFew> : rec_backward_few_kernel<T, kRecSome / 2>,
+                            grid, dim3(kRecThreads), 0, stream, p);
+    }
     const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.dy, &p.dz, &p.dx});
     const int64_t many = p.steps < kLongSteps ? kManyColumns : by == 16 ? 2 * kManyColumns : kManyColumns * 3 / 2;
     if (n < many && p.steps > kSplitSteps) return rec_split_backward<T>(p, by, stream);

@@ -62,7 +62,7 @@ def _check(got, z, x, h0, lengths, dy, dh_last):
 SIZES = [(1, 1, 1), (3, 1, 70), (64, 1, 1024), (2, 2, 3), (1, 7, 33), (5, 15, 64), (2, 16, 65), (3, 17, 2), (1, 31, 130),
          (2, 63, 32), (2, 64, 64), (1, 65, 66), (2, 127, 5), (2, 128, 96), (1, 129, 63), (1, 255, 64), (3, 257, 40),
          (1, 512, 31), (1, 1000, 129), (1, 1023, 64), (2, 1025, 68), (1, 2049, 7), (1, 4500, 1), (20, 300, 200),
-         (300, 40, 33), (2, 130, 4096)]
+         (300, 40, 33), (2, 130, 4096), (21, 9, 1001), (40, 16, 700), (25, 17, 900), (30, 32, 800), (2, 3, 9)]
 
 
 @pytest.mark.parametrize("dt", [F, B])
