@@ -15,16 +15,19 @@ namespace {
 
 constexpr int kRecThreads = 128;
 // Steps up to which a thread takes all of a column's, and those up to which it does so where there
-// are many columns (32 forward; in the backward pass, which keeps them in registers, half of that).
+// are many columns; the backward pass keeps them in registers (300 x 20 x 1000 fp32: 35 us, by
+// warps 50; but bf16 32 and 21).
 constexpr int kRecFew = 4, kRecSome = 32;
+template <typename T> constexpr int kRecSomeBack = sizeof(T) == 4 ? 32 : 16;
 constexpr int64_t kRecColumns = 152 * 128;
 
 // ---------------------------------------------------------------- few steps
 // One thread per column (a channel of a sequence), step after step; bound by memory where there
 // are many. A warp for 32 columns, as below, has a CTA of its own for so few steps, and the
 // CTAs' starts are what that waits for. us with this and with that, forward and backward:
-// 135 x 11 x 2833 fp32 10 and 15, 38 and 52; 1000 x 4 x 1024 fp32 13 and 13, the backward pass 136; 100 x 16 x
-// 4096 fp32 13 and 28, 22 and 60; forward 100 x 32 x 4096 fp32 34 and 36, 100 x 64 x 4096 63 and 58.
+// 135 x 11 x 2833 fp32 10 and 15, 38 and 52; 1000 x 4 x 1024 fp32 13 and 13, backward 136;
+// 100 x 16 x 4096 fp32 13 and 28, 22 and 60; forward 100 x 32 x 4096 fp32 34 and 36, 100 x 64 x
+// 4096 63 and 58.
 template <typename T> __global__ void __launch_bounds__(kRecThreads) rec_forward_few_kernel(const RecArgs p)
 {
     ptx::griddep_wait();
@@ -652,11 +655,13 @@ template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
 template <typename T> cudaError_t backward(const RecArgs& p, cudaStream_t stream)
 {
     const int64_t n = p.batch * p.channels;
-    if (p.steps >= 1 && (p.steps <= kRecFew || (p.steps <= kRecSome / 2 && n >= kRecColumns))) {
+    if (p.steps >= 1 && (p.steps <= kRecFew || (p.steps <= kRecSomeBack<T> && n >= kRecColumns))) {
         if (n > (int64_t)0x7fffffff * kRecThreads) return cudaErrorInvalidConfiguration;
         const dim3 grid((unsigned)((n + kRecThreads - 1) / kRecThreads));
-        return launch_after(p.steps <= kRecFew ? rec_backward_few_kernel<T, kRecFew> : rec_backward_few_kernel<T, kRecSome / 2>,
-                            grid, dim3(kRecThreads), 0, stream, p);
+        const auto kern = p.steps <= kRecFew ? rec_backward_few_kernel<T, kRecFew>
+                          : p.steps <= 16    ? rec_backward_few_kernel<T, 16>
+                                             : rec_backward_few_kernel<T, kRecSomeBack<T>>;
+        return launch_after(kern, grid, dim3(kRecThreads), 0, stream, p);
     }
     const int by = row_bytes(p, (int)sizeof(T), {&p.z, &p.x, &p.dy, &p.dz, &p.dx});
     const int64_t many = p.steps < kLongSteps ? kManyColumns : by == 16 ? 2 * kManyColumns : kManyColumns * 3 / 2;
