@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_backward_kernel(const LnArgs
     constexpr bool kRing = Ring::kRing;
     using Raw = typename Piece<X, N>::Raw;
     extern __shared__ __align__(16) uint8_t shared_bytes[];
-    __shared__ float2 sums[2][kLnThreads / 32];
+    __shared__ __align__(16) float2 sums[2][kLnThreads / 32];  // read two at a time
     ptx::griddep_wait();
     const int group = kWarps ? 32 * kWarps : a.group, place = threadIdx.x & (group - 1), dim = (int)a.dim;
     const int groups = kLnThreads / group, which = threadIdx.x / group;

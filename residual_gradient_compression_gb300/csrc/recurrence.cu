@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(32 * kWarps, kV == 2 ? 2 : 4) rec_forward_kern
     static_assert(kV == 1 || kBytes == 16, "neighbours lie in one row");
     using Copy = CopierOf<T, kBytes, kCols, S, 2>;
     extern __shared__ __align__(16) uint8_t shared_bytes[];
-    __shared__ float state[kWarps][kCols];  // after a warp's chunk
+    __shared__ __align__(8) float state[kWarps][kCols];  // after a warp's chunk; a lane's columns at a time
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, j = lane * kV;
     T* const ring = reinterpret_cast<T*>(shared_bytes) + warp * (4 * Copy::kElements);  // two chunks
@@ -436,8 +436,8 @@ __global__ void __launch_bounds__(32 * kBackWarps<kV>, kV == 2 ? 2 : kBytes == 1
     constexpr int kCols = 32 * kV, S = kBackward<kV>, W = kBackWarps<kV>;
     using Copy = CopierOf<T, kBytes, kCols, S, 3>;
     extern __shared__ __align__(16) uint8_t shared_bytes[];
-    __shared__ float state[W][kCols];  // after a warp's chunk
-    __shared__ float grad[W][kCols];   // the gradient before it
+    __shared__ __align__(8) float state[W][kCols];  // after a warp's chunk; a lane's columns at a time
+    __shared__ __align__(8) float grad[W][kCols];   // the gradient before it
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane * kV;
     T* const ring = reinterpret_cast<T*>(shared_bytes) + warp * (6 * Copy::kElements);  // two chunks
