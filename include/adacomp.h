@@ -367,7 +367,7 @@ adacomp_status adacomp_materialize_group(adacomp_layer_t h, float* const* residu
  * intermediate values while a call runs. Sums, statistics
  * and states are fp32 or wider; results are rounded to the output's type once. Calls
  * are deterministic. Non-finite inputs reach only the results that depend on them.
- * A handle holds sizes and types only and may be used by several host threads.
+ * A handle holds sizes, types and settings only and may be used by several host threads.
  * ------------------------------------------------------------------------------ */
 
 /* Layer norm over rows of dim elements (dim >= 1) of type x_dtype, with a weight and
@@ -446,6 +446,20 @@ adacomp_status adacomp_recurrence_backward(adacomp_recurrence_t h, int64_t batch
                                            const float* carry, const int32_t* lengths, const float* dh_last,
                                            void* dz, int64_t dz_batch, int64_t dz_step, void* dx, int64_t dx_batch,
                                            int64_t dx_step, float* dh0, cudaStream_t stream);
+
+/* Calls over few channels of many steps split a sequence over CTAs of a cluster that wait for
+ * each other's totals. Such a wait is bounded by a timeout in nanoseconds (default 2e9, rounded up
+ * to microseconds, and begun after some 250 tries). The CTAs run together and each writes before
+ * it waits, so none is expected to run out. On expiry the call still ends as usual, with the
+ * status ADACOMP_OK that it returned: what the CTA computes from there on, y, dz and dx of its
+ * steps and the states, is NaN, as there is no workspace to record ADACOMP_ERR_TIMEOUT in.
+ * Nothing traps. Not to be set while another host thread calls with the handle. */
+adacomp_status adacomp_recurrence_set_timeout_ns(adacomp_recurrence_t h, uint64_t timeout_ns);
+
+/* Fault injection for tests of that timeout (not part of the operator): the given CTA of every
+ * cluster writes nothing to the others, so that all of the cluster's waits run out. 0xFFFFFFFF
+ * switches it off (the default). Nothing faults or hangs. */
+adacomp_status adacomp_recurrence_set_fault_injection(adacomp_recurrence_t h, uint32_t silent_cta);
 void adacomp_recurrence_free(adacomp_recurrence_t h);
 
 /* AdamW over many tensors at once, and the norm of their gradients. Tensor i has n[i]

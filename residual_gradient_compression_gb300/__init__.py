@@ -86,6 +86,8 @@ def lib() -> ctypes.CDLL:
         seq = [vp, i64, i64]
         L.adacomp_recurrence_forward.argtypes = [vp, i64, i64] + seq * 2 + [vp, vp] + seq + [vp, vp, vp]
         L.adacomp_recurrence_backward.argtypes = [vp, i64, i64] + seq * 3 + [vp, vp, vp] + seq * 2 + [vp, vp]
+        L.adacomp_recurrence_set_timeout_ns.argtypes = [vp, u64]
+        L.adacomp_recurrence_set_fault_injection.argtypes = [vp, ctypes.c_uint32]
         L.adacomp_adamw_init.argtypes = [P(vp), i32, P(i64), P(i32), P(i32), P(f32), i32, P(sz)]
         L.adacomp_grad_norm.argtypes = [vp, vp, f32, f32, vp, vp, sz, vp]
         L.adacomp_adamw_step.argtypes = [vp] * 8 + [f32] * 7 + [vp, vp]
@@ -103,6 +105,7 @@ def lib() -> ctypes.CDLL:
                      "adacomp_decode_adam", "adacomp_decode_adam_group", "adacomp_materialize_group",
                      "adacomp_layer_norm_init", "adacomp_layer_norm_forward", "adacomp_layer_norm_backward",
                      "adacomp_recurrence_init", "adacomp_recurrence_forward", "adacomp_recurrence_backward",
+                     "adacomp_recurrence_set_timeout_ns", "adacomp_recurrence_set_fault_injection",
                      "adacomp_adamw_init", "adacomp_grad_norm", "adacomp_adamw_step"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -476,6 +479,16 @@ def adacomp_recurrence_backward(h, z, x, dy, carry, dz, dx, lengths=None, dh_las
         *_sequence(dy, h, shape, "dy"), _carry(h, carry, batch, steps), _array(lengths, batch, torch.int32, "lengths"),
         _array(dh_last, n, torch.float32, "dh_last"), *_sequence(dz, h, shape, "dz"), *_sequence(dx, h, shape, "dx"),
         _array(dh0, n, torch.float32, "dh0"), _stream(stream)), "adacomp_recurrence_backward")
+
+
+def adacomp_recurrence_set_timeout_ns(h, ns: int):
+    """Bound on a wait within a cluster; results behind one that runs out are NaN."""
+    _check(lib().adacomp_recurrence_set_timeout_ns(h.ptr, ns), "adacomp_recurrence_set_timeout_ns")
+
+
+def adacomp_recurrence_set_fault_injection(h, silent_cta: int = 0xFFFFFFFF):
+    """Test hook: the given CTA of every cluster writes nothing to the others, whose waits run out."""
+    _check(lib().adacomp_recurrence_set_fault_injection(h.ptr, silent_cta), "adacomp_recurrence_set_fault_injection")
 
 
 def adacomp_recurrence_free(h):

@@ -8,6 +8,8 @@
 struct adacomp_recurrence {
     int64_t channels = 0;
     int32_t dtype = ADACOMP_F32;
+    uint64_t timeout_ns = 2000000000ull;
+    uint32_t inject_silent_cta = 0xffffffffu;  // test-only fault injection
 };
 
 namespace adacomp {
@@ -747,6 +749,8 @@ adacomp_status adacomp_recurrence_forward(adacomp_recurrence_t h, int64_t batch,
     p.steps = steps;
     p.channels = h->channels;
     p.chunks = (steps + adacomp::kRecChunk - 1) / adacomp::kRecChunk;
+    p.timeout = (uint32_t)(h->timeout_ns < (uint64_t)1 << 41 ? (h->timeout_ns + 1023) >> 10 : 1u << 31);
+    p.silent = h->inject_silent_cta;
     const cudaError_t err = h->dtype == ADACOMP_BF16 ? adacomp::forward<adacomp::bf16>(p, stream)
                                                      : adacomp::forward<float>(p, stream);
     return adacomp::launch_result(err, stream);
@@ -786,9 +790,25 @@ adacomp_status adacomp_recurrence_backward(adacomp_recurrence_t h, int64_t batch
     p.steps = steps;
     p.channels = h->channels;
     p.chunks = (steps + adacomp::kRecChunk - 1) / adacomp::kRecChunk;
+    p.timeout = (uint32_t)(h->timeout_ns < (uint64_t)1 << 41 ? (h->timeout_ns + 1023) >> 10 : 1u << 31);
+    p.silent = h->inject_silent_cta;
     const cudaError_t err = h->dtype == ADACOMP_BF16 ? adacomp::backward<adacomp::bf16>(p, stream)
                                                      : adacomp::backward<float>(p, stream);
     return adacomp::launch_result(err, stream);
+}
+
+adacomp_status adacomp_recurrence_set_timeout_ns(adacomp_recurrence_t h, uint64_t timeout_ns)
+{
+    if (!h || timeout_ns == 0) return ADACOMP_ERR_INVALID_ARG;
+    h->timeout_ns = timeout_ns;
+    return ADACOMP_OK;
+}
+
+adacomp_status adacomp_recurrence_set_fault_injection(adacomp_recurrence_t h, uint32_t silent_cta)
+{
+    if (!h) return ADACOMP_ERR_INVALID_ARG;
+    h->inject_silent_cta = silent_cta;
+    return ADACOMP_OK;
 }
 
 void adacomp_recurrence_free(adacomp_recurrence_t h) { delete h; }

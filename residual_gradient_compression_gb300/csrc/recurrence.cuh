@@ -21,6 +21,8 @@ struct RecArgs {
     const int32_t* lengths;
     float *h_last, *dh0, *carry;
     int64_t batch, steps, channels, chunks;
+    uint32_t timeout;  // of a wait for the other CTAs of a cluster, in 1024 ns
+    uint32_t silent;   // test only: the CTA of every cluster that writes nothing to the others
 };
 
 // The kernels that split the steps over clusters (recurrence_split.cu), for few columns. `by`:

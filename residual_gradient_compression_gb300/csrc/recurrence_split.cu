@@ -103,20 +103,54 @@ template <int R> __device__ __forceinline__ void push(Exchange<R>* x, float4* p,
                  : "memory");
 }
 
-// Waits for a barrier's phase. The CTAs of a cluster run together and each writes before it
-// waits, so the wait ends; were it not to, it is given up after some seconds.
-template <int R> __device__ __forceinline__ bool exchange_wait(Exchange<R>* x, uint32_t phase)
+__device__ __forceinline__ uint32_t clock_1024ns() { return (uint32_t)(ptx::globaltimer() >> 10); }
+
+// Whether a barrier's phase is complete; kSleep: the thread may be suspended until it is, for some
+// microseconds.
+template <bool kSleep, int R> __device__ __forceinline__ bool exchange_done(Exchange<R>* x, uint32_t phase)
 {
-    for (uint32_t i = 0; i < (1u << 22); ++i) {
-        uint32_t done;
+    uint32_t done;
+    if constexpr (kSleep)
         asm volatile(
             "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
             : "=r"(done)
             : "r"(shared_address(&x->barrier)), "r"(phase)
             : "memory");
-        if (done) return true;
+    else
+        asm volatile(
+            "{ .reg .pred p; mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+            : "=r"(done)
+            : "r"(shared_address(&x->barrier)), "r"(phase)
+            : "memory");
+    return done != 0;
+}
+
+// Waits for a barrier's phase: some hundred tries, and then for `timeout` times 1024 ns at most. The
+// CTAs of a cluster run together and each writes before it waits, so the wait ends. Were it not
+// to, the CTA exchanges nothing any more, as its barrier's phase is still open, and its results
+// from there on are NaN: so each CTA runs into one timeout at most. (The lanes vote, so that the
+// way past the tries is the warp's: with a timer in a lane's own loop 4x20011x501 takes 7 us more.)
+template <int R> __device__ __forceinline__ bool exchange_wait(Exchange<R>* x, uint32_t phase, uint32_t timeout)
+{
+    bool done = false;
+    for (uint32_t i = 0; i < 256 && !done; ++i) done = exchange_done<true>(x, phase);
+    if (__all_sync(0xffffffffu, done)) return true;
+    const uint32_t start = clock_1024ns();
+    do {
+        done = __all_sync(0xffffffffu, exchange_done<false>(x, phase));
+    } while (!done && clock_1024ns() - start <= timeout);
+    return __all_sync(0xffffffffu, done);
+}
+
+// The end of a cluster's kernel: no CTA ends while another may write to it. What a CTA that gave
+// up was written by then and has not waited for lands within far less than a millisecond.
+__device__ __forceinline__ void exchange_end(bool given_up)
+{
+    cluster_meet();
+    if (!given_up) return;
+    const uint32_t start = clock_1024ns();
+    while (clock_1024ns() - start < 1024) {
     }
-    return false;
 }
 
 // The columns of a tile. Where a sequence's rows are read 16 bytes at a time, a tile is of one
@@ -565,16 +599,19 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
             Two h = h0;  // before the CTA's first step
             if (!kChunks && ranks > 1) {
                 Exchange<kRanks<T, kBytes>>& x = exchange[par];
-                if (lane == 0) exchange_expect(&x, ranks * 512);
-                Two tA = two_of(1.0f), tH = two_of(0.0f);
+                if (!given_up) {
+                    if (lane == 0) exchange_expect(&x, ranks * 512);
+                    Two tA = two_of(1.0f), tH = two_of(0.0f);
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float4 q = part[w][lane];
-                    tH = fma2(low(q), tH, high(q));
-                    tA = tA * low(q);
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float4 q = part[w][lane];
+                        tH = fma2(low(q), tH, high(q));
+                        tA = tA * low(q);
+                    }
+                    if (rank != p.silent)
+                        for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tH));
+                    given_up = !exchange_wait(&x, (round >> 1) & 1, p.timeout);
                 }
-                for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tH));
-                if (!given_up) given_up = !exchange_wait(&x, (round >> 1) & 1);
                 for (uint32_t r = 0; r < ranks; ++r) {
                     if (r == rank) h = h0;
                     const float4 q = x.value[r][lane];
@@ -615,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
         }
     }
     if (rank == (kChunks ? ranks - 1 : 0) && warp == 0) store_state(p.h_last, p, col, h0);
-    if (!kChunks && ranks > 1) cluster_meet();  // no CTA ends while another may write to it
+    if (!kChunks && ranks > 1) exchange_end(given_up);
 }
 
 // The reverse of it: p, the gradient that reaches a state from the steps after it, goes
@@ -719,9 +756,12 @@ __global__ void __launch_bounds__(kThreads, kBytes == 16 ? 3 : 2)
                 tP = fma2(low(part[w][lane]), tP, grad[w][lane]);
             if (!kChunks && ranks > 1) {
                 Exchange<kRanks<T, kBytes>>& x = exchange[par];
-                if (lane == 0) exchange_expect(&x, ranks * 512);
-                for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tP));
-                if (!given_up) given_up = !exchange_wait(&x, (round >> 1) & 1);
+                if (!given_up) {
+                    if (lane == 0) exchange_expect(&x, ranks * 512);
+                    if (rank != p.silent)
+                        for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tP));
+                    given_up = !exchange_wait(&x, (round >> 1) & 1, p.timeout);
+                }
                 for (uint32_t r = ranks; r-- > 0;) {
                     if (r == rank) q = p0;
                     const float4 v = x.value[r][lane];
@@ -765,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, kBytes == 16 ? 3 : 2)
         else finish(std::true_type());
     }
     if (rank == 0 && warp == kWarps - 1) store_state(p.dh0, p, col, p0);
-    if (!kChunks && ranks > 1) cluster_meet();  // no CTA ends while another may write to it
+    if (!kChunks && ranks > 1) exchange_end(given_up);
 }
 
 // Launches a kernel of clusters, behind the kernel ahead of it as launch_after does.

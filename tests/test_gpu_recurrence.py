@@ -323,3 +323,30 @@ def test_same_bits_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, r) for a, r in zip(out, ref))
+
+
+@pytest.mark.parametrize("silent", [0, 1])
+@pytest.mark.parametrize("dt,batch,steps,ch", [(F, 3, 1500, 200), (B, 3, 1500, 200), (F, 3, 1100, 301)])
+def test_a_wait_within_a_cluster_that_runs_out(dt, batch, steps, ch, silent):
+    """One CTA of every cluster writes nothing to the others: every wait ends at its timeout, in the
+    first of several rounds, all results are NaN, and the next calls are as they were."""
+    z, x, h0, dy, dh = _inputs(3, batch, steps, ch, dt)
+    h = ac.adacomp_recurrence_init(ch, CODE[dt])
+    carry, kept = _carry(h, batch, steps), _carry(h, batch, steps)
+
+    def run(carry_in, carry_out):
+        y, dz, dx = (torch.full_like(z, -9.0) for _ in range(3))
+        last, dh0 = torch.zeros_like(h0), torch.zeros_like(h0)
+        ac.adacomp_recurrence_forward(h, z, x, y, h0=h0, h_last=last, carry=carry_out)
+        ac.adacomp_recurrence_backward(h, z, x, dy, carry_in, dz, dx, dh_last=dh, dh0=dh0)
+        return y, last, dz, dx, dh0
+
+    before = run(carry, carry)
+    ac.adacomp_recurrence_set_timeout_ns(h, 20_000_000)  # 20 ms
+    ac.adacomp_recurrence_set_fault_injection(h, silent)
+    for t in run(carry, kept):
+        assert bool(t.isnan().all())
+    ac.adacomp_recurrence_set_fault_injection(h)
+    for got, want in zip(run(carry, kept), before):
+        assert torch.equal(got, want)
+    assert torch.equal(kept, carry)

@@ -209,3 +209,12 @@ def test_free_takes_null_and_twice():
     h = ac.adacomp_recurrence_init(10, ac.F32)
     ac.adacomp_recurrence_free(h)
     ac.adacomp_recurrence_free(h)
+
+
+def test_recurrence_settings_refuse():
+    L, h = ac.lib(), ac.adacomp_recurrence_init(10, ac.F32)
+    assert L.adacomp_recurrence_set_timeout_ns(None, 5) == ac.ERR_INVALID_ARG
+    assert L.adacomp_recurrence_set_fault_injection(None, 0) == ac.ERR_INVALID_ARG
+    assert _status(ac.adacomp_recurrence_set_timeout_ns, h, 0) == ac.ERR_INVALID_ARG
+    ac.adacomp_recurrence_set_timeout_ns(h, 10 ** 9)
+    ac.adacomp_recurrence_set_fault_injection(h)
