@@ -407,7 +407,9 @@ void adacomp_layer_norm_free(adacomp_layer_norm_t h);
  * [batch, steps, channels] in `dtype`: with the gate a_t = 1 / (1 + exp(-z_t)),
  *     h_t = a_t * h_{t-1} + (1 - a_t) * x_t,   y_t = h_t,   t = 0 .. length-1.
  * The state is fp32 throughout; y is it rounded once. steps = 1 is the form for one new
- * token. Host only. */
+ * token. Steps may be composed, h -> A h + H, in an order that depends on the sizes. An infinite
+ * state, or gradient in the backward pass, stays infinite through gates that are not 0 in fp32
+ * (z > -87.3); one of 0 makes it infinite or NaN. Host only. */
 typedef struct adacomp_recurrence* adacomp_recurrence_t;
 adacomp_status adacomp_recurrence_init(adacomp_recurrence_t* out, int64_t channels, adacomp_dtype dtype);
 

@@ -382,6 +382,13 @@ __global__ void __launch_bounds__(32 * kWarps, kV == 2 ? 2 : 4) rec_forward_kern
         };
         if (all) form(std::false_type());
         else form(std::true_type());
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {  // as product() of them all
+            float least = kLeast;
+#pragma unroll
+            for (int k = 0; k < S; k += 2) least = least3(least, a[k][v], a[k + 1][v]);
+            own[v].A = not_below(own[v].A, least);
+        }
         if (t0 == 0) {
 #pragma unroll
             for (int v = 0; v < kV; ++v) h[v] = p.h0 && v < on ? p.h0[col.state(p) + v] : 0.0f;
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(32 * kBackWarps<kV>, kV == 2 ? 2 : kBytes == 1
                     gate(zv[v], &a[k][v], &b[k][v]);
                     if (masked.value && k >= live) a[k][v] = 1.0f, b[k][v] = from_x[k][v] = dv[v] = 0.0f;
                     own[v].H = fmaf(a[k][v], own[v].H, b[k][v] * from_x[k][v]);
-                    own[v].A *= a[k][v];
+                    own[v].A = product(own[v].A, a[k][v]);
                     P[v] = fmaf(own[v].A, dv[v], P[v]);
                 }
             }

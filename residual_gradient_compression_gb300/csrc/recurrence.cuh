@@ -47,6 +47,27 @@ __device__ __forceinline__ void gate(float z, float* a, float* b)
     *b = open ? s : r;
 }
 
+__device__ __forceinline__ float least3(float x, float y, float z)
+{
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+__device__ __forceinline__ float not_below(float x, float least)  // NaN stays NaN
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(least));
+    return r;
+}
+
+// The product of gates, which is 0 only if one of them is: what vanishes in fp32 is rounded up to
+// kLeast and not down to 0, so that an infinite state stays infinite behind it, as it does step
+// by step (0 * infinity is not a number). The states wait for nothing that this adds.
+constexpr float kLeast = 0x1p-149f;
+
+__device__ __forceinline__ float product(float A, float a) { return not_below(A * a, least3(A, a, kLeast)); }
+
 __device__ __forceinline__ int64_t length_of(const RecArgs& p, int64_t b)
 {
     if (!p.lengths) return p.steps;

@@ -18,6 +18,7 @@ __device__ __forceinline__ Two operator*(Two a, Two b) { return {__fmul_rn(a.x, 
 __device__ __forceinline__ Two operator+(Two a, Two b) { return {__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)}; }
 __device__ __forceinline__ Two operator-(Two a, Two b) { return {__fsub_rn(a.x, b.x), __fsub_rn(a.y, b.y)}; }
 __device__ __forceinline__ Two fma2(Two a, Two b, Two c) { return {fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)}; }
+__device__ __forceinline__ Two product(Two A, Two a) { return {product(A.x, a.x), product(A.y, a.y)}; }
 
 // ---------------------------------------------------------------- many steps
 // The steps are split: a warp has 64 columns (two per lane) and eight consecutive steps, a
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_totals_kernel(const __grid_co
                 if (k >= at_hand.live1) a1 = 1.0f, b1 = v[1][1] = 0.0f;
             }
             const Two a = two_of(a0, a1), u = two_of(v[1][0], v[1][1]);
-            A = A * a;
+            A = product(A, a);
             if (kBack) H = fma2(A, u, H);
             else H = fma2(a, H, two_of(b0, b1) * u);
         }
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_totals_kernel(const __grid_co
     for (int i = 0; i < kWarps; ++i) {
         const float4 q = part[kBack ? kWarps - 1 - i : i][lane];
         H = fma2(low(q), H, high(q));
-        A = A * low(q);
+        A = product(A, low(q));
     }
     const bool last = kBack && tc + kSpan >= (int32_t)p.steps;
     if (last) A = fma2(A, load_state(p.dh_last, p, col), H);
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(32 * kStateWarps) rec_states_kernel(const __gr
     for (int32_t k = begin; k < end; ++k) {
         const float2 v = step_of(k);
         own.y = fmaf(v.x, own.y, v.y);
-        own.x *= v.x;
+        own.x = product(own.x, v.x);
     }
     part[warp][lane] = own;
     __syncthreads();
@@ -593,6 +594,11 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
         };
         if (at_hand.all) form(std::false_type());
         else form(std::true_type());
+        Two least = two_of(kLeast);  // as product() of them all
+#pragma unroll
+        for (int k = 0; k < kSteps; k += 2)
+            least = two_of(least3(least.x, a[k].x, a[k + 1].x), least3(least.y, a[k].y, a[k + 1].y));
+        A = two_of(not_below(A.x, least.x), not_below(A.y, least.y));
         part[warp][lane] = quad(A, H);
         __syncthreads();
         if (warp == 0) {
@@ -606,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
                     for (int w = 0; w < kWarps; ++w) {
                         const float4 q = part[w][lane];
                         tH = fma2(low(q), tH, high(q));
-                        tA = tA * low(q);
+                        tA = product(tA, low(q));
                     }
                     if (rank != p.silent)
                         for (uint32_t r = 0; r < ranks; ++r) push(&x, &x.value[rank][lane], r, quad(tA, tH));
@@ -725,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, kBytes == 16 ? 3 : 2)
                 a[k] = two_of(a0, a1);
                 b[k] = two_of(b0, b1);
                 H = fma2(a[k], H, b[k] * inputs(masked, 1, k));
-                A = A * a[k];
+                A = product(A, a[k]);
                 P = fma2(A, inputs(masked, 2, k), P);
             }
         };
@@ -738,18 +744,18 @@ __global__ void __launch_bounds__(kThreads, kBytes == 16 ? 3 : 2)
         for (int w = 0; w < warp; ++w) {
             const float4 v = part[w][lane];
             H = fma2(low(v), H, high(v));
-            A = A * low(v);
+            A = product(A, low(v));
         }
         Two B = two_of(1.0f);  // and from the CTA's end back to the warp's
         P = two_of(0.0f);
         for (int w = kWarps - 1; w > warp; --w) {
             const Two v = low(part[w][lane]);
             P = fma2(v, P, grad[w][lane]);
-            B = B * v;
+            B = product(B, v);
         }
         if (warp == kWarps - 1) {
             const float4 own = part[warp][lane];
-            const Two tA = A * low(own);
+            const Two tA = product(A, low(own));
             Two tP = two_of(0.0f), q = p0;  // q: after the CTA's last step
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w)

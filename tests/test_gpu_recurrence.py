@@ -350,3 +350,31 @@ def test_a_wait_within_a_cluster_that_runs_out(dt, batch, steps, ch, silent):
     for got, want in zip(run(carry, kept), before):
         assert torch.equal(got, want)
     assert torch.equal(kept, carry)
+
+
+def _kind(t):
+    """0 where finite, 1 and 2 where an infinity of either sign, 3 where not a number."""
+    return torch.isposinf(t) + 2 * torch.isneginf(t) + 3 * torch.isnan(t)
+
+
+@pytest.mark.parametrize("dt", [F, B])
+@pytest.mark.parametrize("batch,steps,ch", [(3, 3, 50), (25, 14, 900), (3, 40, 70), (5, 200, 1000), (5, 200, 1001),
+                                            (16, 150, 1024), (3, 1500, 200), (3, 1100, 301), (1, 2000, 37),
+                                            (1, 4000, 64), (30, 1345, 9)])
+def test_infinite_states_and_gradients_stay_infinite(batch, steps, ch, dt):
+    """Infinities in h0, x, dh_last and dy, behind gates whose product over a chunk of steps vanishes
+    in fp32 although none of them does: as by the definition, a state or gradient stays infinite,
+    and only two infinities of unlike sign make a value that is not a number."""
+    z, x, h0, dy, dh = _inputs(batch + steps, batch, steps, ch, dt)
+    z.copy_((torch.rand(z.shape, generator=_gen(1), device="cuda") - 7.5).to(dt))
+    inf, early, late = float("inf"), min(1, steps - 1), steps - 1 - (steps > 8)
+    h0[:, 0], h0[:, 1], h0[:, 3], h0[0, 4] = inf, -inf, inf, -inf
+    x[:, early, 2], x[:, late, 3], x[:, early, 4] = inf, -inf, -inf
+    dh[:, 5], dh[:, 6], dh[:, 8] = inf, -inf, inf
+    dy[:, late, 7], dy[:, early, 8] = -inf, -inf
+    got = _run(z, x, h0, None, dy, dh)
+    ref, bound = recurrence(z, x, h0, None, dy, dh)
+    for name, g, r, e in zip(("y", "h_last", "dz", "dx", "dh0"), got, ref, bound):
+        same = _kind(g) == _kind(r)
+        assert bool(same.all()), (name, (~same).nonzero()[:3].tolist(), g[~same][:3], r[~same][:3])
+        assert_within(g[..., 9:], r[..., 9:], e[..., 9:], name)
