@@ -113,8 +113,9 @@ __global__ void __launch_bounds__(kLnRowThreads<kWarps>,
 }
 
 // Rows too wide for registers: a CTA per row, three passes over it (the second and third
-// from L2).
-template <typename X, typename W> __global__ void __launch_bounds__(kLnThreads) ln_forward_long_kernel(const LnArgs a)
+// from L2). kRuns: of more than a run's elements per thread.
+template <typename X, typename W, bool kRuns>
+__global__ void __launch_bounds__(kLnThreads) ln_forward_long_kernel(const LnArgs a)
 {
     __shared__ float shared[2][kLnThreads / 32];
     ptx::griddep_wait();
@@ -131,15 +132,24 @@ template <typename X, typename W> __global__ void __launch_bounds__(kLnThreads) 
         for (int i = 0; i < kLnThreads / 32; ++i) v += shared[turn][i];
         return v;
     };
-    float s = 0.0f;
-    for (int64_t i = threadIdx.x; i < a.dim; i += kLnThreads) s += to_f32(x[i]);
-    const float mean = sum(s, 0) / (float)a.dim;
-    s = 0.0f;
-    for (int64_t i = threadIdx.x; i < a.dim; i += kLnThreads) {
-        const float d = to_f32(x[i]) - mean;
-        s = fmaf(d, d, s);
-    }
-    const float rstd = 1.0f / sqrtf(sum(s, 1) / (float)a.dim + a.eps);
+    const auto runs = [&](auto&& add) {
+        if constexpr (!kRuns) {
+            float s = 0.0f;
+            for (int64_t i = threadIdx.x; i < a.dim; i += kLnThreads) s = add(to_f32(x[i]), s);
+            return s;
+        }
+        RunSum r;
+        for (int64_t i = threadIdx.x; i < a.dim;) {
+            const int64_t end = i + kLnRun * kLnThreads < a.dim ? i + kLnRun * kLnThreads : a.dim;
+            float s = 0.0f;
+            for (; i < end; i += kLnThreads) s = add(to_f32(x[i]), s);
+            r.add(s);
+        }
+        return r.value();
+    };
+    const float mean = sum(runs([](float v, float s) { return s + v; }), 0) / (float)a.dim;
+    const float squares = runs([mean](float v, float s) { return fmaf(v - mean, v - mean, s); });
+    const float rstd = 1.0f / sqrtf(sum(squares, 1) / (float)a.dim + a.eps);
     for (int64_t i = threadIdx.x; i < a.dim; i += kLnThreads)
         y[i] = from_f32<X>(fmaf((to_f32(x[i]) - mean) * rstd, to_f32(w[i]), b ? to_f32(b[i]) : 0.0f));
     if (threadIdx.x == 0) {
@@ -152,7 +162,8 @@ template <typename X, typename W> __global__ void __launch_bounds__(kLnThreads) 
 template <typename X, typename W, int N> cudaError_t ln_forward_n(LnArgs a, cudaStream_t stream)
 {
     const dim3 one((unsigned)a.rows), threads(kLnThreads);
-    if (a.dim > 64 * kLnThreads) return launch_after(ln_forward_long_kernel<X, W>, one, threads, 0, stream, a);
+    if (a.dim > kLnRun * kLnThreads) return launch_after(ln_forward_long_kernel<X, W, true>, one, threads, 0, stream, a);
+    if (a.dim > 64 * kLnThreads) return launch_after(ln_forward_long_kernel<X, W, false>, one, threads, 0, stream, a);
     // the elements of a piece: no more than four weights of 32 bits
     constexpr bool kWhole = Piece<X, N>::kBytes == 16;
     constexpr int M = kWhole && sizeof(W) == 4 ? 4 : N;

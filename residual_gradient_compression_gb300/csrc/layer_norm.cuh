@@ -124,6 +124,22 @@ template <int N> __device__ __forceinline__ void weights(const bf16* p, float (&
     }
 }
 
+// Where rows are long a thread adds runs of kLnRun terms, and the runs' sums with what their
+// additions round off: a sum of millions of terms in sequence would lose their last bits, all in
+// one direction if they are alike. (fp64 sums instead: 4096 x 12288 bf16 backward 145 us, not 98.)
+constexpr int kLnRun = 256;
+
+struct RunSum {
+    float sum = 0.0f, rest = 0.0f;
+    __device__ __forceinline__ void add(float v)  // D. Knuth's exact sum of two
+    {
+        const float t = sum + v, from_v = t - sum;
+        rest += (sum - (t - from_v)) + (v - from_v);
+        sum = t;
+    }
+    __device__ __forceinline__ float value() const { return sum + rest; }
+};
+
 // The sum over the lanes of a group of up to 32 (a power of two).
 __device__ __forceinline__ float group_sum(float v, int group)
 {

@@ -238,6 +238,7 @@ constexpr int kLnStrip = 256;        // threads of a CTA where rows are too wide
 template <int N> constexpr int kLnStripCols = N == 1 ? 4 : 8;      // columns of a thread there
 constexpr int kLnStripCtas = 3;      // per SM
 constexpr int kLnStripSlices = 128;  // of the rows, at most
+constexpr int64_t kLnSpan = 2 * kLnRun * kLnStrip;  // elements of a row that its threads add in one run (two sums each)
 
 // The rows' two sums, behind the column sums.
 __device__ __forceinline__ float2* row_sums(const LnArgs& a)
@@ -273,18 +274,21 @@ template <typename W> __global__ void __launch_bounds__(kLnJoin) ln_join_kernel(
 // memory: x and dy are read twice, the second time from the last row upwards, of which L2 has
 // the more the fewer there are (4096 x 12288 bf16: 99 us, downwards 106; 5.1 TB/s of the five
 // passes). fp32 4096 x 16000: 195 us (6.7 TB/s). Pieces of two bytes: 4096 x 12289 148 us.
-template <typename X, typename W, int N> __global__ void __launch_bounds__(kLnStrip) ln_sums_kernel(const LnArgs a)
+// kRuns: rows of more than kLnSpan elements.
+template <typename X, typename W, int N, bool kRuns>
+__global__ void __launch_bounds__(kLnStrip) ln_sums_kernel(const LnArgs a)
 {
     __shared__ float2 shared[kLnStrip / 32];
     ptx::griddep_wait();
     constexpr int M = N == 1 ? 32 / (int)sizeof(X) : 8;  // elements of a turn
+    static_assert(2 * kLnRun % M == 0, "whole turns");
     const int64_t row = blockIdx.x;
     const X* x = static_cast<const X*>(a.x) + row * a.x_stride;
     const X* dy = static_cast<const X*>(a.dy) + row * a.dy_stride;
     const W* w = static_cast<const W*>(a.w);
     const float mean = a.mean_in[row];
     Pair t0 = pair(0.0f), t1 = pair(0.0f);
-    for (int64_t c = threadIdx.x * N; c < a.dim; c += kLnStrip * M) {
+    const auto turn = [&](int64_t c) {
         Piece<X, N> px[M / N], pd[M / N];
         float wv[M] = {};
 #pragma unroll
@@ -303,8 +307,19 @@ template <typename X, typename W, int N> __global__ void __launch_bounds__(kLnSt
             t0 = t0 + g;
             t1 = fma2(g, pair_of(px, i) + pair(-mean), t1);
         }
+    };
+    RunSum r0, r1;
+    if constexpr (!kRuns) {
+        for (int64_t c = threadIdx.x * N; c < a.dim; c += kLnStrip * M) turn(c);
+    } else {
+        for (int64_t c = threadIdx.x * N; c < a.dim;) {
+            for (int i = 0; i < kLnSpan / (kLnStrip * M) && c < a.dim; ++i, c += kLnStrip * M) turn(c);
+            r0.add(both(t0));
+            r1.add(both(t1));
+            t0 = t1 = pair(0.0f);
+        }
     }
-    float s0 = warp_sum(both(t0)), s1 = warp_sum(both(t1));
+    float s0 = warp_sum(kRuns ? r0.value() : both(t0)), s1 = warp_sum(kRuns ? r1.value() : both(t1));
     if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = make_float2(s0, s1);
     __syncthreads();
     if (threadIdx.x) return;
@@ -446,7 +461,8 @@ template <typename X, typename W, int N> cudaError_t ln_backward_wide(LnArgs a, 
     int64_t most = kLnStripCtas * sms / strips;  // one wave
     most = most < 1 ? 1 : most < kLnStripSlices ? most : kLnStripSlices;
     a.slices = (int)(a.rows < most ? a.rows : most);
-    e = launch_after(ln_sums_kernel<X, W, N>, dim3((unsigned)a.rows), dim3(kLnStrip), 0, stream, a);
+    e = launch_after(a.dim > kLnSpan ? ln_sums_kernel<X, W, N, true> : ln_sums_kernel<X, W, N, false>,
+                     dim3((unsigned)a.rows), dim3(kLnStrip), 0, stream, a);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)strips, (unsigned)a.slices);
     e = launch_after(ln_strip_kernel<X, W, N>, grid, dim3(kLnStrip), 0, stream, a);
