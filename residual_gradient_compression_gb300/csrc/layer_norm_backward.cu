@@ -6,7 +6,7 @@ namespace {
 
 constexpr int kLnCols = 16;      // columns of a thread
 constexpr int kLnThreads = 512;  // a CTA's
-constexpr int kLnParts = 304;    // CTAs at most, each with partial sums of dw and db
+constexpr int kLnParts = 152;    // CTAs at most (one per SM), each with partial sums of dw and db
 constexpr int64_t kLnDim = (int64_t)kLnThreads * kLnCols;
 
 __device__ __forceinline__ void group_barrier(int id, int threads)
@@ -243,7 +243,7 @@ constexpr int64_t kLnSpan = 2 * kLnRun * kLnStrip;  // elements of a row that it
 // The rows' two sums, behind the column sums.
 __device__ __forceinline__ float2* row_sums(const LnArgs& a)
 {
-    return reinterpret_cast<float2*>(a.part + (int64_t)kLnStripSlices * 2 * a.dim);
+    return reinterpret_cast<float2*>(a.part + (a.rows < kLnStripSlices ? a.rows : kLnStripSlices) * 2 * a.dim);
 }
 
 // Adds the partial sums: 32 columns per CTA, 32 rows of threads that each add every 32nd. Bound by
@@ -475,8 +475,9 @@ size_t ln_backward_bytes(int64_t rows, int64_t dim)
 {
     // whichever way a call's alignment takes
     const size_t sums = (size_t)dim * 2 * 4;
-    const size_t group = dim <= kLnDim ? (rows < 1 ? 1 : rows < kLnParts ? rows : kLnParts) * sums : sums;
-    const size_t wide = dim > kLnDim / 2 ? kLnStripSlices * sums + (size_t)rows * sizeof(float2) : sums;
+    const auto parts = [&](int64_t most) { return (size_t)(rows < 1 ? 1 : rows < most ? rows : most) * sums; };
+    const size_t group = dim <= kLnDim ? parts(kLnParts) : sums;
+    const size_t wide = dim > kLnDim / 2 ? parts(kLnStripSlices) + (size_t)rows * sizeof(float2) : sums;
     return group > wide ? group : wide;
 }
 

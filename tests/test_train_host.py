@@ -218,3 +218,15 @@ def test_recurrence_settings_refuse():
     assert _status(ac.adacomp_recurrence_set_timeout_ns, h, 0) == ac.ERR_INVALID_ARG
     ac.adacomp_recurrence_set_timeout_ns(h, 10 ** 9)
     ac.adacomp_recurrence_set_fault_injection(h)
+
+
+@pytest.mark.parametrize("dim", [1, 100, 2048, 4097, 8192, 8193, 2 ** 23 + 3])
+@pytest.mark.parametrize("rows", [0, 1, 2, 151, 100_000])
+def test_layer_norm_workspace_is_what_a_call_can_write(rows, dim):
+    """Partial sums of the weight's and the bias's gradients: one per SM (152) where rows fit in
+    registers, or up to 128 and a pair of sums per row; never more than there are rows."""
+    h = ac.adacomp_layer_norm_init(dim, ac.BF16, ac.F32)
+    sums = 8 * dim
+    narrow = min(max(rows, 1), 152) * sums if dim <= 8192 else sums
+    wide = min(max(rows, 1), 128) * sums + 8 * rows if dim > 4096 else sums
+    assert ac.adacomp_layer_norm_backward_ws_bytes(h, rows) == max(narrow, wide)
