@@ -510,8 +510,10 @@ class Pointers:
 
 
 def adacomp_pointers(tensors) -> Pointers:
-    """Tensors to pass to adacomp_grad_norm or adacomp_adamw_step (which also take plain lists)."""
-    return Pointers(tensors)
+    """Tensors to pass to adacomp_grad_norm or adacomp_adamw_step (which also take plain lists).
+    Their addresses are taken here, and their memory is kept: a tensor that is given other memory
+    afterwards (t.data = ..., resize_) is not followed, and wants new pointers."""
+    return Pointers(None if t is None else t.detach() for t in tensors)
 
 
 def _pointers(tensors, expect, what: str, may_miss: bool = False):

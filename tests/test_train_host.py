@@ -230,3 +230,16 @@ def test_layer_norm_workspace_is_what_a_call_can_write(rows, dim):
     narrow = min(max(rows, 1), 152) * sums if dim <= 8192 else sums
     wide = min(max(rows, 1), 128) * sums + 8 * rows if dim > 4096 else sums
     assert ac.adacomp_layer_norm_backward_ws_bytes(h, rows) == max(narrow, wide)
+
+
+def test_pointers_keep_the_memory_that_they_point_to():
+    """A tensor whose memory is replaced afterwards (t.data = ...) is not followed, and what its
+    address was taken of is not freed."""
+    class OnGpu(torch.Tensor):  # passes for one; no call below reaches the GPU
+        is_cuda = True
+
+    t = torch.zeros(100).as_subclass(OnGpu)
+    p = ac.adacomp_pointers([t, None])
+    t.data = torch.ones(50)
+    assert p.tensors[0].data_ptr() == p.array[0] != t.data_ptr()
+    assert p.tensors[0].numel() == 100 and p.tensors[1] is None and not p.tensors[0].any()
