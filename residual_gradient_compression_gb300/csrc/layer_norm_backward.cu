@@ -420,15 +420,10 @@ template <typename W> cudaError_t ln_join(const LnArgs& a, cudaStream_t stream)
 
 template <typename X, typename W, int N, int kWarps> cudaError_t ln_backward_group(LnArgs a, cudaStream_t stream)
 {
-    static bool set[64] = {};
     constexpr int sums = 2 * (int)kLnDim * 4, ring = LnRing<X, N>::kBytes, shared = ring > sums ? ring : sums;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = sm_count(&sms);
-    if (e == cudaSuccess && !set[dev]) {
-        e = cudaFuncSetAttribute(ln_backward_kernel<X, W, N, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
-        set[dev] = e == cudaSuccess;
-    }
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e == cudaSuccess) e = allow<ln_backward_kernel<X, W, N, kWarps>>(shared);
     if (e != cudaSuccess) return e;
     const int64_t per = kLnThreads / a.group, need = (a.rows + per - 1) / per;
     const int64_t most = sms < kLnParts ? sms : kLnParts;

@@ -593,16 +593,9 @@ int row_bytes(const RecArgs& p, int e, std::initializer_list<const RecSeq*> seqs
 template <void (*kern)(RecArgs)>
 cudaError_t launch_tiles(const RecArgs& p, bool apart, int cols, int most, int warps, int per_warp, cudaStream_t stream)
 {
-    static bool set[64] = {};  // the kernel's shared memory, once per device
     const int64_t tiles = apart ? p.batch * ((p.channels + cols - 1) / cols) : (p.batch * p.channels + cols - 1) / cols;
     if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
-    if (e == cudaSuccess && !set[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most * per_warp);
-        set[dev] = e == cudaSuccess;
-    }
+    const cudaError_t e = allow<kern>(most * per_warp);
     if (e != cudaSuccess) return e;
     return launch_after(kern, dim3((unsigned)tiles), dim3(32 * (unsigned)warps), (size_t)(warps * per_warp), stream, p);
 }

@@ -818,8 +818,6 @@ __global__ void __launch_bounds__(kThreads, kBytes == 16 ? 3 : 2)
 template <int kRanks, void (*kern)(RecArgs, uint32_t)>
 cudaError_t launch_ranks(int cols, int shared, const RecArgs& p, cudaStream_t stream)
 {
-    static bool set[64] = {};  // the kernel's shared memory, once per device
-
     uint32_t ranks = 1;
     const int64_t tiles = cols ? p.batch * ((p.channels + cols - 1) / cols) : (p.batch * p.channels + kCols - 1) / kCols;
     // a CTA more in a cluster is worth its exchange where the GPU is not full without it; more
@@ -827,15 +825,7 @@ cudaError_t launch_ranks(int cols, int shared, const RecArgs& p, cudaStream_t st
     const uint32_t most = tiles <= 19 ? (uint32_t)kRanks : 8;
     while (ranks < most && (int64_t)ranks * kSpan < p.steps && tiles * ranks < 1024) ranks *= 2;
     if (tiles > 0x7fffffff / (int64_t)ranks) return cudaErrorInvalidConfiguration;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
-    if (e == cudaSuccess && !set[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
-        if (e == cudaSuccess && kRanks > 8)
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        set[dev] = e == cudaSuccess;
-    }
+    const cudaError_t e = allow<kern, (kRanks > 8)>(shared);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * ranks));
@@ -874,14 +864,7 @@ template <typename T, int kBytes> bool by_chunks(const RecArgs& p, int64_t tiles
 template <void (*kern)(RecArgs, uint32_t)>
 cudaError_t launch_chunks(int64_t tiles, uint32_t grid, uint32_t chunks, int shared, const RecArgs& p, cudaStream_t stream)
 {
-    static bool set[64] = {};  // the kernel's shared memory, once per device
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
-    if (e == cudaSuccess && !set[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
-        set[dev] = e == cudaSuccess;
-    }
+    const cudaError_t e = allow<kern>(shared);
     if (e != cudaSuccess) return e;
     return launch_after(kern, dim3((unsigned)(tiles * grid)), dim3(kThreads), (size_t)shared, stream, p, chunks);
 }

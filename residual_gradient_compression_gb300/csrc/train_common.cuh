@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -29,22 +30,38 @@ inline bool is_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<ui
 inline bool known_dtype(int32_t t) { return t == ADACOMP_F32 || t == ADACOMP_BF16; }
 inline int dtype_bytes(int32_t t) { return t == ADACOMP_BF16 ? 2 : 4; }
 
-// Multiprocessors of the current device, looked up once per device.
+// Multiprocessors of the current device, looked up once per device (by any of several host threads).
 inline cudaError_t sm_count(int* out)
 {
-    static int known[64] = {};
+    static std::atomic<int> known[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (known[dev] == 0) {
-        int n = 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
         e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
-        known[dev] = n;
+        known[dev].store(n, std::memory_order_relaxed);
     }
-    *out = known[dev];
+    *out = n;
     return cudaSuccess;
+}
+
+// Lets a kernel have `shared` bytes of dynamic shared memory, and (kClusters) clusters of more than
+// eight CTAs, once per device; of several host threads that come first, each does.
+template <auto kern, bool kClusters = false> cudaError_t allow(int shared)
+{
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+    if (kClusters && e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
 }
 
 // ---------------------------------------------------------------- device
