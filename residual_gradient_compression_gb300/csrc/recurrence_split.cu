@@ -544,11 +544,11 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
     __shared__ Exchange<kRanks<T, kBytes>> exchange[2];
     const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (2 * kTile); };
     ptx::griddep_wait();
-    if (!kChunks && ranks > 1) {
+    if constexpr (!kChunks) {
         exchange_init(exchange);
         cluster_sync();  // all CTAs run, and their barriers are there, before one writes to another
     }
-    const uint32_t tile = blockIdx.x / ranks, rank = kChunks ? blockIdx.x - tile * ranks : ranks > 1 ? cluster_rank() : 0;
+    const uint32_t tile = blockIdx.x / ranks, rank = kChunks ? blockIdx.x - tile * ranks : cluster_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Column<kBytes> col[2] = {Column<kBytes>(p, tile, place_of<kBytes>(lane, 0)),
                                   Column<kBytes>(p, tile, place_of<kBytes>(lane, 1))};
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
         const int par = round & 1;
         copies_wait();
         __syncthreads();
-        if (t0 + span < steps) copier.copy(tile_of(par ^ 1), tc + span);
+        if (!kChunks && t0 + span < steps) copier.copy(tile_of(par ^ 1), tc + span);
         const int32_t ts = tc + warp * kSteps;
         const Live at_hand(p, col, ts);
         const T* const first = tile_of(par) + warp * kSteps * kCols + place_of<kBytes>(lane, 0);
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
         __syncthreads();
         if (warp == 0) {
             Two h = h0;  // before the CTA's first step
-            if (!kChunks && ranks > 1) {
+            if constexpr (!kChunks) {
                 Exchange<kRanks<T, kBytes>>& x = exchange[par];
                 if (!given_up) {
                     if (lane == 0) exchange_expect(&x, ranks * 512);
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
                 const float4 q = part[w][lane];
                 h = fma2(low(q), h, high(q));
             }
-            if (kChunks || ranks == 1) h0 = h;
+            if (kChunks) h0 = h;
         }
         __syncthreads();
         Two h = begin[warp][lane];
@@ -656,9 +656,10 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(const __grid_c
                     y.put(k, k < at_hand.live0 ? v.x : 0.0f, k < at_hand.live1 ? v.y : 0.0f, col[0].on, col[1].on);
             }
         }
+        if (kChunks) break;  // one round (the next one's first step may not be a 32-bit number)
     }
     if (rank == (kChunks ? ranks - 1 : 0) && warp == 0) store_state(p.h_last, p, col, h0);
-    if (!kChunks && ranks > 1) exchange_end(given_up);
+    if constexpr (!kChunks) exchange_end(given_up);
 }
 
 // The reverse of it: p, the gradient that reaches a state from the steps after it, goes
@@ -676,22 +677,22 @@ __global__ void __launch_bounds__(kThreads, kBytes == 16 ? 3 : 2)
     __shared__ Exchange<kRanks<T, kBytes>> exchange[2];
     const auto tile_of = [&](int i) { return reinterpret_cast<T*>(shared_bytes) + i * (3 * kTile); };
     ptx::griddep_wait();
-    if (!kChunks && ranks > 1) {
+    if constexpr (!kChunks) {
         exchange_init(exchange);
         cluster_sync();  // all CTAs run, and their barriers are there, before one writes to another
     }
-    const uint32_t tile = blockIdx.x / ranks, rank = kChunks ? blockIdx.x - tile * ranks : ranks > 1 ? cluster_rank() : 0;
+    const uint32_t tile = blockIdx.x / ranks, rank = kChunks ? blockIdx.x - tile * ranks : cluster_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Column<kBytes> col[2] = {Column<kBytes>(p, tile, place_of<kBytes>(lane, 0)),
                                   Column<kBytes>(p, tile, place_of<kBytes>(lane, 1))};
     const int32_t steps = (int32_t)p.steps, span = (int32_t)ranks * kSpan;
-    int32_t t0 = steps > 0 ? (steps - 1) / span * span : -1, tc = t0 + (int32_t)rank * kSpan;
+    int32_t t0 = (steps - 1) / span * span, tc = t0 + (int32_t)rank * kSpan;
     const Copier<T, kBytes, 3> copier(p, tile, {&p.z, &p.x, &p.dy});
     Two p0;  // after the round's last step (the joining warp's)
     if (!kChunks) p0 = load_state(p.dh_last, p, col);
     else if (warp == kWarps - 1) p0 = begin_of<T, true>(p, col, tc, rank + 1 == ranks);
     bool given_up = false;
-    if (t0 >= 0) copier.copy(tile_of(0), tc);
+    copier.copy(tile_of(0), tc);
     for (int32_t round = 0; t0 >= 0; t0 -= span, tc -= span, ++round) {
         const int par = round & 1;
         Two h = two_of(0.0f);  // before the CTA's first step
@@ -699,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, kBytes == 16 ? 3 : 2)
             h = two_of(col[0].on ? *kept(p, col[0], tc) : 0.0f, col[1].on ? *kept(p, col[1], tc) : 0.0f);
         copies_wait();
         __syncthreads();
-        if (t0 > 0) copier.copy(tile_of(par ^ 1), tc - span);
+        if (!kChunks && t0 > 0) copier.copy(tile_of(par ^ 1), tc - span);
         const int32_t ts = tc + warp * kSteps;
         const Live at_hand(p, col, ts);
         const T* const first = tile_of(par) + warp * kSteps * kCols + place_of<kBytes>(lane, 0);
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, kBytes == 16 ? 3 : 2)
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w)
                 tP = fma2(low(part[w][lane]), tP, grad[w][lane]);
-            if (!kChunks && ranks > 1) {
+            if constexpr (!kChunks) {
                 Exchange<kRanks<T, kBytes>>& x = exchange[par];
                 if (!given_up) {
                     if (lane == 0) exchange_expect(&x, ranks * 512);
@@ -809,22 +810,22 @@ __global__ void __launch_bounds__(kThreads, kBytes == 16 ? 3 : 2)
         };
         if (at_hand.all) finish(std::false_type());
         else finish(std::true_type());
+        if (kChunks) break;
     }
     if (rank == 0 && warp == kWarps - 1) store_state(p.dh0, p, col, p0);
-    if (!kChunks && ranks > 1) exchange_end(given_up);
+    if constexpr (!kChunks) exchange_end(given_up);
 }
 
 // Launches a kernel of clusters, behind the kernel ahead of it as launch_after does.
 template <int kRanks, void (*kern)(RecArgs, uint32_t)>
 cudaError_t launch_ranks(int cols, int shared, const RecArgs& p, cudaStream_t stream)
 {
-    uint32_t ranks = 1;
     const int64_t tiles = cols ? p.batch * ((p.channels + cols - 1) / cols) : (p.batch * p.channels + kCols - 1) / kCols;
     // a CTA more in a cluster is worth its exchange where the GPU is not full without it; more
     // than eight where all clusters still run at once
     const uint32_t most = tiles <= 19 ? (uint32_t)kRanks : 8;
+    uint32_t ranks = 2;  // at least, as there are more than 128 steps and less than 512 tiles
     while (ranks < most && (int64_t)ranks * kSpan < p.steps && tiles * ranks < 1024) ranks *= 2;
-    if (tiles > 0x7fffffff / (int64_t)ranks) return cudaErrorInvalidConfiguration;
     const cudaError_t e = allow<kern, (kRanks > 8)>(shared);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
