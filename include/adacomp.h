@@ -407,9 +407,11 @@ void adacomp_layer_norm_free(adacomp_layer_norm_t h);
  * [batch, steps, channels] in `dtype`: with the gate a_t = 1 / (1 + exp(-z_t)),
  *     h_t = a_t * h_{t-1} + (1 - a_t) * x_t,   y_t = h_t,   t = 0 .. length-1.
  * The state is fp32 throughout; y is it rounded once. steps = 1 is the form for one new
- * token. Steps may be composed, h -> A h + H, in an order that depends on the sizes. An infinite
- * state, or gradient in the backward pass, stays infinite through gates that are not 0 in fp32
- * (z > -87.3); one of 0 makes it infinite or NaN. Host only. */
+ * token. The smaller of a_t and 1 - a_t has an error of up to 6 + 1.2 |z_t| units in its last
+ * place, the larger of up to 6, and what is below 2^-126 (|z_t| > 87.3) is 0. Steps may be
+ * composed, h -> A h + H, in an order that depends on the sizes. An infinite state, or gradient
+ * in the backward pass, stays infinite through gates that are not 0; one of 0 makes it infinite
+ * or NaN. Host only. */
 typedef struct adacomp_recurrence* adacomp_recurrence_t;
 adacomp_status adacomp_recurrence_init(adacomp_recurrence_t* out, int64_t channels, adacomp_dtype dtype);
 
@@ -499,7 +501,8 @@ adacomp_status adacomp_grad_norm(adacomp_adamw_t h, const void* const* grad, flo
  * The three constants are formed in fp64 and rounded once. With 8-bit states m and v enter
  * as (e4m3 * scale) and (e4m3 * scale)^2, and leave as the block's new scale = max/448 and
  * the e4m3 nearest to value * (448/max) (to even; a positive u never becomes 0 but the
- * smallest e4m3; a block whose max is below 2^-96 becomes zeros with scale 0).
+ * smallest e4m3; a block whose max is below 2^-96 has scale 0, and so stands for zeros). A value
+ * that is not finite reaches its whole block through the scale.
  *   weight, grad, m, v   host arrays of num_tensors device pointers, 16-byte aligned;
  *                        weight, m and v are in/out. State starts as zeros.
  *   m_scale, v_scale     8-bit states: device fp32[ceil(n/256)] per tensor; otherwise NULL

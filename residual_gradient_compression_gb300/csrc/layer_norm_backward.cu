@@ -44,8 +44,9 @@ template <typename X, int N> struct LnRing {
 //
 // With 32-bit weights, all in us, both kernels: 16384 x 2048 bf16 42 (4.8 TB/s; 65536 rows 132,
 // 6.1 TB/s), fp32 66 (6.1 TB/s); 8192 x 8192 bf16 79, fp32 128 (6.3 TB/s); 32768 x 1001 fp32 75
-// (5.2 TB/s), bf16 56. Short runs are bound by the start, the column sums and the join; bf16 rows
-// also by the instructions (63 % of the issue slots at four warps per scheduler).
+// (5.2 TB/s), bf16 56. Short runs are bound by the start, the column sums and the join, and bf16
+// rows by latency: at four warps per scheduler half of the issue slots are used (49.5 % at 16384 x
+// 2048) and 56 % of the DRAM's rate.
 template <typename X, typename W, int N, int kWarps>
 __global__ void __launch_bounds__(kLnThreads, 1) ln_backward_kernel(const LnArgs a)
 {

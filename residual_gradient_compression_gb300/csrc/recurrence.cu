@@ -119,10 +119,10 @@ template <typename T, int S> __global__ void __launch_bounds__(kRecThreads) rec_
 // for one that may not be running. A hand-over is a named barrier of the two warps. The warp's
 // next chunk is copied to shared memory meanwhile.
 //
-// Bound by memory and, in bf16, nearly as much by instructions (23 per element forward, 43
+// Bound by memory and, in bf16, nearly as much by instructions (23 per element forward, 45
 // backward). Measured over 16 sequences of 2048 steps and 1024 channels: forward 35 us in bf16
-// (5.7 TB/s) and 65 in fp32 (6.2), backward 71 (4.7) and 104 (6.4). Rows that are not aligned
-// to 16 bytes: with 1023 channels 58 and 115 us in bf16, 79 and 146 in fp32; there each row's
+// (5.7 TB/s) and 65 in fp32 (6.2), backward 73 (4.6) and 104 (6.4). Rows that are not aligned
+// to 16 bytes: with 1023 channels 59 and 112 us in bf16, 78 and 146 in fp32; there each row's
 // place in its 16 bytes is found again for every tensor, and its results are written one by one.
 constexpr int kWarps = 8;
 
@@ -620,11 +620,11 @@ template <typename T, int kBytes, int kV> cudaError_t backward_v(const RecArgs& 
 
 // How a call is split, by the columns n = batch * channels, in us with the choice and without. Many
 // columns: a CTA for 64 or 32 of them, if that makes one for every SM; otherwise, if there are
-// steps to split, clusters (4x4096x1001 bf16: forward 34 with clusters, 62 without, backward 86
-// and 151). The backward pass, whose chain from one kept state to the next is longer, wants
+// steps to split, clusters (4x4096x1001 bf16: forward 35 with clusters, 41 without, backward 69
+// and 124). The backward pass, whose chain from one kept state to the next is longer, wants
 // clusters also where there are up to twice as many columns and the chain is long (5x4096x1000
-// bf16 70 and 141, 6x1500x1024 fp32 42 and 49; but 8x1000x1024 fp32 40 and 36), fewer where rows
-// are off alignment (5x4096x1001 fp32 101 and 147; but 9x4096x1001 164 and 147).
+// bf16 74 and 143, 6x1500x1024 fp32 42 and 49; but 8x1000x1024 fp32 41 and 36), fewer where rows
+// are off alignment (5x4096x1001 fp32 102 and 147; but 9x4096x1001 167 and 148).
 constexpr int64_t kManyColumns = 152 * 32;
 constexpr int64_t kSplitSteps = 128;
 constexpr int64_t kLongSteps = 1200;
@@ -633,8 +633,8 @@ constexpr int64_t kLongSteps = 1200;
 constexpr int64_t kTwoColumns = 3 * kManyColumns;
 
 // Rows without alignment (forward and backward us by 16 bytes, and by four or two): 16 x 2048 x 1023
-// fp32 79 and 146, 141 and 208; bf16 58 and 115, 79 and 172. But rows of pairs of bf16 elements
-// take as many copies of four bytes as there are lanes: 16 x 2048 x 1022 58 and 114, 54 and 95.
+// fp32 78 and 146, 142 and 209; bf16 59 and 112, 81 and 174. But rows of pairs of bf16 elements
+// take as many copies of four bytes as there are lanes: 16 x 2048 x 1022 58 and 114, 55 and 96.
 template <typename T> constexpr int kPairs = sizeof(T) == 2 ? 4 : 0;
 
 template <typename T> cudaError_t forward(const RecArgs& p, cudaStream_t stream)
@@ -669,7 +669,7 @@ template <typename T> cudaError_t backward(const RecArgs& p, cudaStream_t stream
     const int64_t many = p.steps < kLongSteps ? kManyColumns : by == 16 ? 2 * kManyColumns : kManyColumns * 3 / 2;
     if (n < many && p.steps > kSplitSteps) return rec_split_backward<T>(p, by, stream);
     if constexpr (sizeof(T) == 2) {
-        // two columns per lane save instructions (16x2048x1024 bf16: 71 us against 84); with fp32
+        // two columns per lane save instructions (16x2048x1024 bf16: 73 us against 86); with fp32
         // tensors, which are bound by memory, one is faster (104 us against 115)
         if (by == 16 && n >= kTwoColumns) return backward_v<T, 16, 2>(p, stream);
     }

@@ -32,8 +32,8 @@ __device__ __forceinline__ Two product(Two A, Two a) { return {product(A.x, a.x)
 //
 // Bound by the rounds' latency (some 3 us each: the gates, one exchange, the results), as a
 // few columns leave an SM one or two CTAs. Measured: one sequence of 32768 steps of 1024 bf16
-// channels 87 us forward (2.3 TB/s), 131 backward (2.6); four ragged ones of up to 20011 steps
-// of 501 fp32 channels 115 (2.7 TB/s) and 174 (3.2).
+// channels 92 us forward (2.2 TB/s), 137 backward (2.5); four ragged ones of up to 20011 steps
+// of 501 fp32 channels 116 (2.7 TB/s) and 179 (3.1).
 constexpr int kCols = 64, kSteps = 8, kWarps = 8, kThreads = 32 * kWarps, kSpan = kSteps * kWarps;
 constexpr int kTile = kSpan * kCols;  // elements of a tensor that a CTA has in a round
 static_assert(kRecChunk == kSpan, "a kept state for every CTA");
@@ -845,15 +845,16 @@ cudaError_t launch_ranks(int cols, int shared, const RecArgs& p, cudaStream_t st
 }
 
 // Rows without alignment (a training step's us by 16 bytes and by four or two): 4 x 20011 x 501
-// fp32 290 and 417, 4 x 4096 x 1001 bf16 121 and 174; 32 x 4096 x 33 fp32, twice as many tiles but
-// all running at once, 55 and 70; 32 x 4096 x 62 fp32, more than that, 115 and 93.
+// fp32 295 and 440, 4 x 4096 x 1001 bf16 104 and 159; 32 x 4096 x 33 fp32, twice as many tiles but
+// all running at once, 56 and 72; 32 x 4096 x 62 fp32, more than that, 115 and 94.
 constexpr int64_t kAtOnce = 38;
 
 // Whether every chunk has a CTA of its own, which costs their number, and three launches, where
 // clusters cost the number of their rounds: forward and backward us with it and without, 1 x 9918
-// x 3 fp32 14 and 15, 44 and 53; 233 x 1500 x 1 16 and 20, 19 and 34; 1 x 32768 x 1024 117 and
-// 167, 147 and 214 (bf16, with clusters of 16, 98 and 144, 87 and 131); 16 x 9656 x 133 98 and
-// 150, 76 and 146; 1 x 1000000 x 8 372 and 661, 4095 and 4996.
+// x 3 fp32 13 and 22, 45 and 56; 233 x 1500 x 1 15 and 22, 20 and 34; 1 x 32768 x 1024 122 and
+// 170, 152 and 222 (bf16, with clusters of 16, 101 and 145, 92 and 137); 16 x 9656 x 133 bf16 106
+// and 168, 94 and 121; 1 x 1000000 x 8 382 and 682, 4162 and 5191. The numbers in by_chunks lie
+// between such pairs.
 template <typename T, int kBytes> bool by_chunks(const RecArgs& p, int64_t tiles, int64_t chunks)
 {
     // the last chunk's beginning needs two rows of bf16 elements, if it is not in the carry
