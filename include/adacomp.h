@@ -519,6 +519,122 @@ adacomp_status adacomp_adamw_step(adacomp_adamw_t h, void* const* weight, const 
                                   cudaStream_t stream);
 void adacomp_adamw_free(adacomp_adamw_t h);
 
+/* ------------------------------------------------------------------------------
+ * Linear layers and losses over a vocabulary: the matrix products of a training step. The
+ * conventions of the training operators above hold. Matrices are strided by rows: inputs
+ * by any stride >= 0 (0: one row read for all), outputs by at least a row. With 16-byte aligned
+ * pointers and row strides that are multiples of 16 bytes they are used as they lie; others are
+ * first copied into the workspace. Workspaces are 16-byte aligned, need no initialisation, and
+ * serve one call at a time.
+ *
+ * bf16 products are exact and summed in fp32. fp32 numbers are split into three bf16 numbers that
+ * add up to them (what is below 2^-133 is lost), and of the nine products of parts the six
+ * largest are summed, which leaves out less than 2^-22 of a product. Sums may add the terms
+ * in any order that depends on the sizes alone, and round or truncate each partial sum.
+ *
+ * The kernels wait for their own copies and products. Such a wait is bounded by 2 s; on expiry the call
+ * still ends, and the results that it had not computed are NaN. Nothing traps.
+ * ------------------------------------------------------------------------------ */
+
+/* A linear layer from in_dim to out_dim (each 1..2^30), all of its tensors of one dtype:
+ *     z = x w^T + bias,  y = act(z) + residual,   w[out_dim][in_dim].
+ * Activations, of fp32 z: relu(z) = max(z, 0) (slope 0 at 0); gelu(z) = z (1 + erf(z / sqrt 2)) / 2;
+ * gelu_tanh(z) = z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2; silu(z) = z / (1 + exp(-z)).
+ * Host only. */
+typedef enum {
+    ADACOMP_ACT_NONE = 0,
+    ADACOMP_ACT_RELU = 1,
+    ADACOMP_ACT_GELU = 2,
+    ADACOMP_ACT_GELU_TANH = 3,
+    ADACOMP_ACT_SILU = 4
+} adacomp_activation;
+typedef struct adacomp_linear* adacomp_linear_t;
+adacomp_status adacomp_linear_init(adacomp_linear_t* out, int64_t in_dim, int64_t out_dim, adacomp_dtype dtype,
+                                   adacomp_activation activation);
+
+/* Workspace bytes of a forward or backward pass over up to `rows` rows, whatever their alignment. */
+size_t adacomp_linear_forward_ws_bytes(adacomp_linear_t h, int64_t rows);
+size_t adacomp_linear_backward_ws_bytes(adacomp_linear_t h, int64_t rows);
+
+/* y of `rows` rows (0 does nothing; one row, or a few, is the form for new tokens). bias[out_dim]
+ * and residual may be NULL; y may be residual itself with the same stride. pre (may be NULL)
+ * receives z rounded to dtype, which the backward pass of an activation needs. */
+adacomp_status adacomp_linear_forward(adacomp_linear_t h, int64_t rows, const void* x, int64_t x_stride, const void* w,
+                                      int64_t w_stride, const void* bias, const void* residual, int64_t residual_stride,
+                                      void* y, int64_t y_stride, void* pre, int64_t pre_stride, void* ws,
+                                      size_t ws_bytes, cudaStream_t stream);
+
+/* From dy, with dz = dy * act'(pre) (dy itself without an activation; pre may then be NULL):
+ *     dx = dz w,  dw = dz^T x,  db = sum over rows of dz;   the residual's gradient is dy.
+ * For the products dz is rounded to bf16 where dtype is bf16; db is summed from the unrounded dz. dx, dw and
+ * db may each be NULL (not wanted; x is needed for dw only, w for dx only) and are overwritten
+ * (dw and db with zeros for 0 rows). */
+adacomp_status adacomp_linear_backward(adacomp_linear_t h, int64_t rows, const void* dy, int64_t dy_stride,
+                                       const void* x, int64_t x_stride, const void* w, int64_t w_stride,
+                                       const void* pre, int64_t pre_stride, void* dx, int64_t dx_stride, void* dw,
+                                       int64_t dw_stride, void* db, void* ws, size_t ws_bytes, cudaStream_t stream);
+void adacomp_linear_free(adacomp_linear_t h);
+
+/* A vocabulary of `vocab` tokens (1..2^30) with weights w[vocab][dim] (dim 1..2^30), and the losses of
+ * hidden states x[rows][dim] against it, x, w, dx and dw of one dtype. The logits z = x w^T stay in
+ * fp32 and are not kept: a backward pass forms them again, a piece of the vocabulary at a time. Host only. */
+typedef struct adacomp_vocab* adacomp_vocab_t;
+adacomp_status adacomp_vocab_init(adacomp_vocab_t* out, int64_t dim, int64_t vocab, adacomp_dtype dtype);
+
+/* Workspace bytes over up to `rows` rows, whatever their alignment; k as below. */
+size_t adacomp_vocab_loss_forward_ws_bytes(adacomp_vocab_t h, int64_t rows);
+size_t adacomp_vocab_loss_backward_ws_bytes(adacomp_vocab_t h, int64_t rows);
+size_t adacomp_distill_forward_ws_bytes(adacomp_vocab_t h, int64_t rows, int32_t k);
+size_t adacomp_distill_backward_ws_bytes(adacomp_vocab_t h, int64_t rows, int32_t k);
+
+/* Softmax cross entropy:  lse = log(sum over v of exp(z_v)),  loss = lse - z_target.
+ *   target   device int32[rows] or int64[rows] (target_bytes 4 or 8). A row whose target is negative
+ *            has no loss: its loss and lse are 0, its x is not used (it may hold anything), and
+ *            takes no time in the products. One of vocab or more makes the row's loss NaN.
+ *   loss     device fp32[rows];  lse  device fp32[rows], for the backward pass
+ * rows = 0 does nothing. */
+adacomp_status adacomp_vocab_loss_forward(adacomp_vocab_t h, int64_t rows, const void* x, int64_t x_stride,
+                                          const void* w, int64_t w_stride, const void* target, int32_t target_bytes,
+                                          float* loss, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The gradients, from the gradient dloss of loss (device fp32; row r's is dloss[r * dloss_stride], so 0 is one
+ * value for all rows; not used for rows without a loss):
+ *     dz = (exp(z - lse) - [v = target]) * dloss,  dx = dz w,  dw = dz^T x.
+ * For the products dz is rounded to bf16 where dtype is bf16. dx and dw may each be NULL (not both) and are overwritten: dx is 0
+ * in rows without a loss, dw is 0 if no row has one. A target of vocab or more makes the row's
+ * dx, and dw, NaN. */
+adacomp_status adacomp_vocab_loss_backward(adacomp_vocab_t h, int64_t rows, const void* x, int64_t x_stride,
+                                           const void* w, int64_t w_stride, const void* target, int32_t target_bytes,
+                                           const float* lse, const float* dloss, int64_t dloss_stride, void* dx,
+                                           int64_t dx_stride, void* dw, int64_t dw_stride, void* ws, size_t ws_bytes,
+                                           cudaStream_t stream);
+
+/* Distillation from a teacher's k logits per row (1 <= k <= ADACOMP_MAX_TEACHER), of the tokens
+ * index: with t = temperature, q = softmax(logit / t) over the row's listed tokens and
+ * p = softmax(z / t) over the vocabulary,
+ *     lse = log(sum over v of exp(z_v / t)),
+ *     loss = t^2 * sum over the list of q * (log q - log p).
+ *   index    device int32[rows][k], rows index_stride apart. A negative one is no token (a shorter
+ *            list); a row without any has no loss, as above. One of vocab or more makes the row's loss NaN.
+ *            A token that is listed twice counts twice.
+ *   logit    device, of logit_dtype, [rows][k], rows logit_stride apart; not used where index is
+ *            negative. -inf is a probability of 0; a row of nothing else has a loss of NaN.
+ * temperature is finite and positive. The vocabulary's gradients as above, with
+ *     dz = t * (p - sum of q over the token's places in the list) * dloss. */
+#define ADACOMP_MAX_TEACHER 256
+adacomp_status adacomp_distill_forward(adacomp_vocab_t h, int64_t rows, const void* x, int64_t x_stride, const void* w,
+                                       int64_t w_stride, int32_t k, const int32_t* index, int64_t index_stride,
+                                       const void* logit, int64_t logit_stride, adacomp_dtype logit_dtype,
+                                       float temperature, float* loss, float* lse, void* ws, size_t ws_bytes,
+                                       cudaStream_t stream);
+adacomp_status adacomp_distill_backward(adacomp_vocab_t h, int64_t rows, const void* x, int64_t x_stride, const void* w,
+                                        int64_t w_stride, int32_t k, const int32_t* index, int64_t index_stride,
+                                        const void* logit, int64_t logit_stride, adacomp_dtype logit_dtype,
+                                        float temperature, const float* lse, const float* dloss, int64_t dloss_stride,
+                                        void* dx, int64_t dx_stride, void* dw, int64_t dw_stride, void* ws,
+                                        size_t ws_bytes, cudaStream_t stream);
+void adacomp_vocab_free(adacomp_vocab_t h);
+
 /* Releases the handle. adacomp_free(NULL) does nothing. */
 void adacomp_free(adacomp_layer_t h);
 

@@ -26,11 +26,13 @@ OK, ERR_INVALID_ARG, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_CAPACITY, ERR_CUDA, ERR_T
     ERR_BAD_MESSAGE = range(8)
 F32, BF16 = 0, 1
 RULE_ADACOMP, RULE_LOCAL_SELECTION = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
 MAX_GROUP = 128
 MAX_LEARNERS = 256
 DECODE_WS_FIXED = 10240
 RECURRENCE_CHUNK = 64   # steps between the states that the recurrence's forward pass keeps
 ADAMW_BLOCK = 256       # elements that share a scale of 8-bit optimiser states
+MAX_TEACHER = 256       # tokens of a teacher's list
 STATIC_WS_BYTES = 1 << 20  # ADACOMP_STATIC_WS_BYTES: the largest workspace adacomp_compress_static_ws holds
 
 _lib = None
@@ -91,7 +93,23 @@ def lib() -> ctypes.CDLL:
         L.adacomp_adamw_init.argtypes = [P(vp), i32, P(i64), P(i32), P(i32), P(f32), i32, P(sz)]
         L.adacomp_grad_norm.argtypes = [vp, vp, f32, f32, vp, vp, sz, vp]
         L.adacomp_adamw_step.argtypes = [vp] * 8 + [f32] * 7 + [vp, vp]
-        for name in ("adacomp_layer_norm_free", "adacomp_recurrence_free", "adacomp_adamw_free"):
+        L.adacomp_linear_init.argtypes = [P(vp), i64, i64, ctypes.c_int, ctypes.c_int]
+        row = [vp, i64]
+        L.adacomp_linear_forward.argtypes = [vp, i64] + row * 2 + [vp] + row * 3 + [vp, sz, vp]
+        L.adacomp_linear_backward.argtypes = [vp, i64] + row * 6 + [vp, vp, sz, vp]
+        L.adacomp_vocab_init.argtypes = [P(vp), i64, i64, ctypes.c_int]
+        L.adacomp_vocab_loss_forward.argtypes = [vp, i64] + row * 2 + [vp, i32, vp, vp, vp, sz, vp]
+        L.adacomp_vocab_loss_backward.argtypes = [vp, i64] + row * 2 + [vp, i32, vp] + row * 3 + [vp, sz, vp]
+        lists = [i32] + row * 2 + [ctypes.c_int, f32]
+        L.adacomp_distill_forward.argtypes = [vp, i64] + row * 2 + lists + [vp, vp, vp, sz, vp]
+        L.adacomp_distill_backward.argtypes = [vp, i64] + row * 2 + lists + [vp] + row * 3 + [vp, sz, vp]
+        for name, more in (("linear_forward", []), ("linear_backward", []), ("vocab_loss_forward", []),
+                           ("vocab_loss_backward", []), ("distill_forward", [i32]), ("distill_backward", [i32])):
+            getattr(L, f"adacomp_{name}").restype = ctypes.c_int
+            size = getattr(L, f"adacomp_{name}_ws_bytes")
+            size.argtypes, size.restype = [vp, i64] + more, sz
+        for name in ("adacomp_layer_norm_free", "adacomp_recurrence_free", "adacomp_adamw_free", "adacomp_linear_free",
+                     "adacomp_vocab_free"):
             getattr(L, name).argtypes = [vp]
             getattr(L, name).restype = None
         L.adacomp_status_string.argtypes = [ctypes.c_int]
@@ -106,7 +124,8 @@ def lib() -> ctypes.CDLL:
                      "adacomp_layer_norm_init", "adacomp_layer_norm_forward", "adacomp_layer_norm_backward",
                      "adacomp_recurrence_init", "adacomp_recurrence_forward", "adacomp_recurrence_backward",
                      "adacomp_recurrence_set_timeout_ns", "adacomp_recurrence_set_fault_injection",
-                     "adacomp_adamw_init", "adacomp_grad_norm", "adacomp_adamw_step"):
+                     "adacomp_adamw_init", "adacomp_grad_norm", "adacomp_adamw_step",
+                     "adacomp_linear_init", "adacomp_vocab_init"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -575,4 +594,168 @@ def adacomp_adamw_step(h, weights, grads, m, v, lr: float, beta1: float, beta2: 
 
 
 def adacomp_adamw_free(h):
+    h.__del__()
+
+
+# ---------------------------------------------------------------------------------------
+# Linear layers and losses over a vocabulary.
+
+_CODES = {v: k for k, v in _DTYPES.items()}
+
+
+def _rows(t, dtype, rows: int, cols: int, what: str):
+    """(address, row stride) of a tensor of rows x cols elements: a matrix with contiguous rows, or
+    anything contiguous whose last axis is a row. None stays None."""
+    if t is None:
+        return None, 0
+    shape = t.shape
+    if t.dtype is not dtype or not t.is_cuda or not shape or shape[-1] != cols or t.numel() != rows * cols:
+        _bad(f"{what} must be a CUDA tensor of {dtype}, {rows} rows of {cols}")
+    if len(shape) == 2:
+        stride, one = t.stride()
+        if one != 1 and cols > 1:
+            _bad(f"{what}: the elements of a row must be contiguous")
+        return t.data_ptr(), stride
+    if not t.is_contiguous():
+        _bad(f"{what}: a tensor that is not a matrix must be contiguous")
+    return t.data_ptr(), cols
+
+
+def _count(t, cols: int, what: str) -> int:
+    if not t.dim() or t.shape[-1] != cols:
+        _bad(f"{what} must have rows of {cols}")
+    return t.numel() // cols
+
+
+def adacomp_linear_init(in_dim: int, out_dim: int, dtype: int = F32, activation: int = ACT_NONE) -> _TrainHandle:
+    p = ctypes.c_void_p()
+    _check(lib().adacomp_linear_init(ctypes.byref(p), in_dim, out_dim, dtype, activation), "adacomp_linear_init")
+    h = _TrainHandle(p.value, "adacomp_linear_free")
+    h.in_dim, h.out_dim, h.torch_dtype, h.activation = in_dim, out_dim, _DTYPES[dtype], activation
+    return h
+
+
+def adacomp_linear_forward_ws_bytes(h, rows: int) -> int:
+    return lib().adacomp_linear_forward_ws_bytes(h.ptr, rows)
+
+
+def adacomp_linear_backward_ws_bytes(h, rows: int) -> int:
+    return lib().adacomp_linear_backward_ws_bytes(h.ptr, rows)
+
+
+def adacomp_linear_forward(h, x, w, y, ws, bias=None, residual=None, pre=None, stream=None):
+    """y = act(x w^T + bias) + residual; pre receives the value before the activation, for the backward pass."""
+    t, n = h.torch_dtype, h.out_dim
+    rows = _count(x, h.in_dim, "x")
+    _check(lib().adacomp_linear_forward(
+        h.ptr, rows, *_rows(x, t, rows, h.in_dim, "x"), *_rows(w, t, n, h.in_dim, "w"), _array(bias, n, t, "bias"),
+        *_rows(residual, t, rows, n, "residual"), *_rows(y, t, rows, n, "y"), *_rows(pre, t, rows, n, "pre"), _ptr(ws),
+        _nbytes(ws), _stream(stream)), "adacomp_linear_forward")
+
+
+def adacomp_linear_backward(h, dy, x, w, ws, pre=None, dx=None, dw=None, db=None, stream=None):
+    """dx, dw and db (those that are given) from dy and the forward pass's x, w and pre. x may be None
+    without dw, w without dx."""
+    t, n, k = h.torch_dtype, h.out_dim, h.in_dim
+    rows = _count(dy, n, "dy")
+    _check(lib().adacomp_linear_backward(
+        h.ptr, rows, *_rows(dy, t, rows, n, "dy"), *_rows(x, t, rows, k, "x"), *_rows(w, t, n, k, "w"),
+        *_rows(pre, t, rows, n, "pre"), *_rows(dx, t, rows, k, "dx"), *_rows(dw, t, n, k, "dw"),
+        _array(db, n, t, "db"), _ptr(ws), _nbytes(ws), _stream(stream)), "adacomp_linear_backward")
+
+
+def adacomp_linear_free(h):
+    h.__del__()
+
+
+def adacomp_vocab_init(dim: int, vocab: int, dtype: int = F32) -> _TrainHandle:
+    p = ctypes.c_void_p()
+    _check(lib().adacomp_vocab_init(ctypes.byref(p), dim, vocab, dtype), "adacomp_vocab_init")
+    h = _TrainHandle(p.value, "adacomp_vocab_free")
+    h.dim, h.vocab, h.torch_dtype = dim, vocab, _DTYPES[dtype]
+    return h
+
+
+def adacomp_vocab_loss_forward_ws_bytes(h, rows: int) -> int:
+    return lib().adacomp_vocab_loss_forward_ws_bytes(h.ptr, rows)
+
+
+def adacomp_vocab_loss_backward_ws_bytes(h, rows: int) -> int:
+    return lib().adacomp_vocab_loss_backward_ws_bytes(h.ptr, rows)
+
+
+def adacomp_distill_forward_ws_bytes(h, rows: int, k: int) -> int:
+    return lib().adacomp_distill_forward_ws_bytes(h.ptr, rows, k)
+
+
+def adacomp_distill_backward_ws_bytes(h, rows: int, k: int) -> int:
+    return lib().adacomp_distill_backward_ws_bytes(h.ptr, rows, k)
+
+
+def _target(target, rows: int):
+    if target.dtype not in (torch.int32, torch.int64):
+        _bad("target must be a tensor of int32 or int64")
+    return _array(target, rows, target.dtype, "target"), target.dtype.itemsize
+
+
+def _teacher(index, logit, rows: int):
+    if index.dim() < 2 or logit.shape != index.shape or logit.dtype not in _CODES:
+        _bad("index and logit must be [rows, k], logit of float32 or bfloat16")
+    k = index.shape[-1]
+    return (k, *_rows(index, torch.int32, rows, k, "index"), *_rows(logit, logit.dtype, rows, k, "logit"),
+            _CODES[logit.dtype])
+
+
+def _dloss(dloss, rows: int):
+    """(address, stride): one value per row, or one for all."""
+    if dloss.numel() == 1 and rows != 1:
+        return _array(dloss, 1, torch.float32, "dloss"), 0
+    return _array(dloss, rows, torch.float32, "dloss"), 1
+
+
+def _hidden(h, x, w):
+    rows = _count(x, h.dim, "x")
+    return rows, (*_rows(x, h.torch_dtype, rows, h.dim, "x"), *_rows(w, h.torch_dtype, h.vocab, h.dim, "w"))
+
+
+def _vocab_gradients(h, rows, dx, dw):
+    return (*_rows(dx, h.torch_dtype, rows, h.dim, "dx"), *_rows(dw, h.torch_dtype, h.vocab, h.dim, "dw"))
+
+
+def adacomp_vocab_loss_forward(h, x, w, target, loss, lse, ws, stream=None):
+    """Each row's softmax cross entropy of the logits x w^T; a negative target is a row without a loss.
+    loss and lse: fp32, one value per row."""
+    rows, operands = _hidden(h, x, w)
+    _check(lib().adacomp_vocab_loss_forward(
+        h.ptr, rows, *operands, *_target(target, rows), _array(loss, rows, torch.float32, "loss"),
+        _array(lse, rows, torch.float32, "lse"), _ptr(ws), _nbytes(ws), _stream(stream)), "adacomp_vocab_loss_forward")
+
+
+def adacomp_vocab_loss_backward(h, x, w, target, lse, dloss, ws, dx=None, dw=None, stream=None):
+    """dx and dw (those that are given) from dloss (fp32, one per row or one for all) and the forward pass's lse."""
+    rows, operands = _hidden(h, x, w)
+    _check(lib().adacomp_vocab_loss_backward(
+        h.ptr, rows, *operands, *_target(target, rows), _array(lse, rows, torch.float32, "lse"), *_dloss(dloss, rows),
+        *_vocab_gradients(h, rows, dx, dw), _ptr(ws), _nbytes(ws), _stream(stream)), "adacomp_vocab_loss_backward")
+
+
+def adacomp_distill_forward(h, x, w, index, logit, temperature: float, loss, lse, ws, stream=None):
+    """Each row's temperature^2 KL(teacher || student), the teacher given by the logits of the tokens index
+    (int32 [rows, k]; a negative one is none). loss and lse: fp32, one value per row."""
+    rows, operands = _hidden(h, x, w)
+    _check(lib().adacomp_distill_forward(
+        h.ptr, rows, *operands, *_teacher(index, logit, rows), temperature, _array(loss, rows, torch.float32, "loss"),
+        _array(lse, rows, torch.float32, "lse"), _ptr(ws), _nbytes(ws), _stream(stream)), "adacomp_distill_forward")
+
+
+def adacomp_distill_backward(h, x, w, index, logit, temperature: float, lse, dloss, ws, dx=None, dw=None, stream=None):
+    """dx and dw (those that are given) from dloss (fp32, one per row or one for all) and the forward pass's lse."""
+    rows, operands = _hidden(h, x, w)
+    _check(lib().adacomp_distill_backward(
+        h.ptr, rows, *operands, *_teacher(index, logit, rows), temperature, _array(lse, rows, torch.float32, "lse"),
+        *_dloss(dloss, rows), *_vocab_gradients(h, rows, dx, dw), _ptr(ws), _nbytes(ws), _stream(stream)),
+        "adacomp_distill_backward")
+
+
+def adacomp_vocab_free(h):
     h.__del__()

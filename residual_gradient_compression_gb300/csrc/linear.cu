@@ -1,0 +1,280 @@
+// Linear layers: the forward and backward pass and their C entry points (adacomp.h).
+#include <initializer_list>
+#include <new>
+
+#include "product.cuh"
+
+struct adacomp_linear {
+    int64_t in = 0, out = 0;
+    int32_t dtype = ADACOMP_F32, act = ADACOMP_ACT_NONE;
+};
+
+namespace adacomp {
+namespace {
+
+constexpr int kDzThreads = 128;
+constexpr int kDzSlices = 152;  // partial sums of db: one per slice of the rows
+
+struct LinearArgs {
+    int64_t rows, in, out;
+    int32_t act;
+    const void *x, *w, *bias, *residual, *dy, *pre_in;
+    void *y, *pre, *dx, *dw, *db;
+    int64_t x_stride, w_stride, residual_stride, dy_stride, pre_in_stride, y_stride, pre_stride, dx_stride, dw_stride;
+};
+
+struct LinearParts {  // of a backward pass's workspace
+    void* dz;
+    int64_t dz_stride;
+    float* sums;
+};
+
+LinearParts linear_parts(Carve& c, int64_t rows, int64_t out, int32_t dtype, int32_t act)
+{
+    LinearParts p = {};
+    p.sums = c.take<float>(kDzSlices * out);
+    p.dz_stride = round_up(out, 16 / dtype_bytes(dtype));
+    if (act != ADACOMP_ACT_NONE) p.dz = c.take<char>(rows * p.dz_stride * dtype_bytes(dtype));
+    return p;
+}
+
+struct DzArgs {
+    const void *dy, *pre;
+    void* dz;
+    float* sums;
+    int64_t rows, n, dy_stride, pre_stride, dz_stride;
+    int32_t act, slices;
+};
+
+// dz = dy * act'(pre), and its sums over slices of the rows. A thread has a column.
+template <typename T> __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a)
+{
+    ptx::griddep_wait();
+    const int64_t c = (int64_t)blockIdx.x * kDzThreads + threadIdx.x;
+    if (c >= a.n) return;
+    float sum = 0.0f;
+    for (int64_t r = blockIdx.y; r < a.rows; r += a.slices) {
+        float v = to_f32(static_cast<const T*>(a.dy)[r * a.dy_stride + c]);
+        if (a.act != ADACOMP_ACT_NONE) {
+            v *= slope(to_f32(static_cast<const T*>(a.pre)[r * a.pre_stride + c]), a.act);
+            if (a.dz) static_cast<T*>(a.dz)[r * a.dz_stride + c] = from_f32<T>(v);
+        }
+        sum += v;
+    }
+    a.sums[(int64_t)blockIdx.y * a.n + c] = sum;
+}
+
+template <typename T> __global__ void __launch_bounds__(kDzThreads) linear_db_kernel(const float* sums, T* db, int64_t n, int32_t slices)
+{
+    ptx::griddep_wait();
+    const int64_t c = (int64_t)blockIdx.x * kDzThreads + threadIdx.x;
+    if (c >= n) return;
+    float s = 0.0f;
+    for (int i = 0; i < slices; ++i) s += sums[(int64_t)i * n + c];
+    db[c] = from_f32<T>(s);
+}
+
+template <typename T> cudaError_t linear_forward(const LinearArgs& a, cudaStream_t stream)
+{
+    EpiLinear<T> epi = {};
+    epi.y = static_cast<T*>(a.y);
+    epi.pre = static_cast<T*>(a.pre);
+    epi.bias = static_cast<const T*>(a.bias);
+    epi.residual = static_cast<const T*>(a.residual);
+    epi.y_stride = a.y_stride;
+    epi.pre_stride = a.pre_stride;
+    epi.residual_stride = a.residual_stride;
+    epi.n = a.out;
+    epi.act = a.act;
+    epi.y_whole = whole_rows(a.y, a.y_stride, a.rows, sizeof(T));
+    epi.pre_whole = whole_rows(a.pre, a.pre_stride, a.rows, sizeof(T));
+    epi.bias_whole = is_aligned(a.bias, 16);
+    epi.residual_whole = whole_rows(a.residual, a.residual_stride, a.rows, sizeof(T));
+    SimpleArgs g = {};
+    g.a = {a.x, a.x_stride, 1};
+    g.b = {a.w, a.w_stride, 1};
+    g.m = a.rows;
+    g.n = a.out;
+    g.k = a.in;
+    g.strip = kCols;
+    return product_simple<T>(g, epi, stream);
+}
+
+template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws, cudaStream_t stream)
+{
+    Carve carve{static_cast<char*>(ws)};
+    const LinearParts p = linear_parts(carve, a.rows, a.out, sizeof(T) == 2 ? ADACOMP_BF16 : ADACOMP_F32, a.act);
+    const bool act = a.act != ADACOMP_ACT_NONE;
+    cudaError_t e = cudaSuccess;
+    if ((act && (a.dx || a.dw)) || a.db) {
+        DzArgs d = {};
+        d.dy = a.dy;
+        d.pre = a.pre_in;
+        d.dz = a.dx || a.dw ? p.dz : nullptr;
+        d.sums = p.sums;
+        d.rows = a.rows;
+        d.n = a.out;
+        d.dy_stride = a.dy_stride;
+        d.pre_stride = a.pre_in_stride;
+        d.dz_stride = p.dz_stride;
+        d.act = a.act;
+        d.slices = (int32_t)(a.rows < kDzSlices ? a.rows : kDzSlices);
+        const unsigned blocks = (unsigned)((a.out + kDzThreads - 1) / kDzThreads);
+        if (d.slices) e = launch_after(linear_dz_kernel<T>, dim3(blocks, d.slices), dim3(kDzThreads), 0, stream, d);
+        if (e == cudaSuccess && a.db)
+            e = launch_after(linear_db_kernel<T>, dim3(blocks), dim3(kDzThreads), 0, stream, p.sums, static_cast<T*>(a.db), a.out, d.slices);
+        if (e != cudaSuccess) return e;
+    }
+    const Operand dz = act ? Operand{p.dz, p.dz_stride, 1} : Operand{a.dy, a.dy_stride, 1};
+    SimpleArgs g = {};
+    EpiStore<T> epi = {};
+    epi.first = epi.last = true;
+    g.strip = kCols;
+    if (a.dx) {
+        g.a = dz;
+        g.b = {a.w, 1, a.w_stride};
+        g.m = a.rows;
+        g.n = epi.n = a.in;
+        g.k = a.out;
+        epi.out = static_cast<T*>(a.dx);
+        epi.stride = a.dx_stride;
+        epi.whole = whole_rows(a.dx, a.dx_stride, a.rows, sizeof(T));
+        e = product_simple<T>(g, epi, stream);
+        if (e != cudaSuccess) return e;
+    }
+    if (a.dw) {
+        g.a = {dz.p, 1, dz.outer};
+        g.b = {a.x, 1, a.x_stride};
+        g.m = a.out;
+        g.n = epi.n = a.in;
+        g.k = a.rows;
+        epi.out = static_cast<T*>(a.dw);
+        epi.stride = a.dw_stride;
+        epi.whole = whole_rows(a.dw, a.dw_stride, a.out, sizeof(T));
+        e = product_simple<T>(g, epi, stream);
+    }
+    return e;
+}
+
+constexpr int64_t kMostDim = (int64_t)1 << 30, kMostRows = (int64_t)1 << 31;
+
+}  // namespace
+}  // namespace adacomp
+
+using adacomp::is_aligned;
+
+extern "C" {
+
+adacomp_status adacomp_linear_init(adacomp_linear_t* out, int64_t in_dim, int64_t out_dim, adacomp_dtype dtype,
+                                   adacomp_activation activation)
+{
+    if (!out) return ADACOMP_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (in_dim < 1 || in_dim > adacomp::kMostDim || out_dim < 1 || out_dim > adacomp::kMostDim ||
+        !adacomp::known_dtype(dtype) || (int)activation < ADACOMP_ACT_NONE || (int)activation > ADACOMP_ACT_SILU)
+        return ADACOMP_ERR_INVALID_ARG;
+    adacomp_linear* h = new (std::nothrow) adacomp_linear;
+    if (!h) return ADACOMP_ERR_INVALID_ARG;
+    h->in = in_dim;
+    h->out = out_dim;
+    h->dtype = dtype;
+    h->act = activation;
+    *out = h;
+    return ADACOMP_OK;
+}
+
+size_t adacomp_linear_forward_ws_bytes(adacomp_linear_t h, int64_t rows)
+{
+    (void)h;
+    (void)rows;
+    return 0;
+}
+
+size_t adacomp_linear_backward_ws_bytes(adacomp_linear_t h, int64_t rows)
+{
+    if (!h || rows < 0 || rows >= adacomp::kMostRows) return 0;
+    adacomp::Carve c;
+    adacomp::linear_parts(c, rows, h->out, h->dtype, h->act);
+    return c.at;
+}
+
+adacomp_status adacomp_linear_forward(adacomp_linear_t h, int64_t rows, const void* x, int64_t x_stride, const void* w,
+                                      int64_t w_stride, const void* bias, const void* residual, int64_t residual_stride,
+                                      void* y, int64_t y_stride, void* pre, int64_t pre_stride, void* ws,
+                                      size_t ws_bytes, cudaStream_t stream)
+{
+    adacomp::TrainRange range("adacomp_linear_forward");
+    if (!h || rows < 0 || rows >= adacomp::kMostRows) return ADACOMP_ERR_INVALID_ARG;
+    if (rows == 0) return ADACOMP_OK;
+    if (!x || !w || !y || !ws || x_stride < 0 || w_stride < 0 || (residual && residual_stride < 0) ||
+        (rows > 1 && (y_stride < h->out || (pre && pre_stride < h->out))))
+        return ADACOMP_ERR_INVALID_ARG;
+    const uintptr_t e = adacomp::dtype_bytes(h->dtype);
+    if (!is_aligned(x, e) || !is_aligned(w, e) || !is_aligned(bias, e) || !is_aligned(residual, e) || !is_aligned(y, e) ||
+        !is_aligned(pre, e) || !is_aligned(ws, 16))
+        return ADACOMP_ERR_ALIGNMENT;
+    if (ws_bytes < adacomp_linear_forward_ws_bytes(h, rows)) return ADACOMP_ERR_WORKSPACE;
+    adacomp::LinearArgs a = {};
+    a.rows = rows;
+    a.in = h->in;
+    a.out = h->out;
+    a.act = h->act;
+    a.x = x;
+    a.w = w;
+    a.bias = bias;
+    a.residual = residual;
+    a.y = y;
+    a.pre = pre;
+    a.x_stride = x_stride;
+    a.w_stride = w_stride;
+    a.residual_stride = residual_stride;
+    a.y_stride = y_stride;
+    a.pre_stride = pre_stride;
+    const cudaError_t err = h->dtype == ADACOMP_BF16 ? adacomp::linear_forward<adacomp::bf16>(a, stream)
+                                                     : adacomp::linear_forward<float>(a, stream);
+    return adacomp::launch_result(err, stream);
+}
+
+adacomp_status adacomp_linear_backward(adacomp_linear_t h, int64_t rows, const void* dy, int64_t dy_stride,
+                                       const void* x, int64_t x_stride, const void* w, int64_t w_stride,
+                                       const void* pre, int64_t pre_stride, void* dx, int64_t dx_stride, void* dw,
+                                       int64_t dw_stride, void* db, void* ws, size_t ws_bytes, cudaStream_t stream)
+{
+    adacomp::TrainRange range("adacomp_linear_backward");
+    if (!h || rows < 0 || rows >= adacomp::kMostRows) return ADACOMP_ERR_INVALID_ARG;
+    if ((!dx && !dw && !db) || !ws) return ADACOMP_ERR_INVALID_ARG;
+    if (dw && h->out > 1 && dw_stride < h->in) return ADACOMP_ERR_INVALID_ARG;
+    if (rows > 0 && (!dy || dy_stride < 0 || (h->act != ADACOMP_ACT_NONE && (!pre || pre_stride < 0)) ||
+                     (dw && (!x || x_stride < 0)) || (dx && (!w || w_stride < 0 || (rows > 1 && dx_stride < h->in)))))
+        return ADACOMP_ERR_INVALID_ARG;
+    const uintptr_t e = adacomp::dtype_bytes(h->dtype);
+    for (const void* p : {dy, x, w, pre, (const void*)dx, (const void*)dw, (const void*)db})
+        if (!is_aligned(p, e)) return ADACOMP_ERR_ALIGNMENT;
+    if (!is_aligned(ws, 16)) return ADACOMP_ERR_ALIGNMENT;
+    if (ws_bytes < adacomp_linear_backward_ws_bytes(h, rows)) return ADACOMP_ERR_WORKSPACE;
+    adacomp::LinearArgs a = {};
+    a.rows = rows;
+    a.in = h->in;
+    a.out = h->out;
+    a.act = h->act;
+    a.dy = dy;
+    a.x = x;
+    a.w = w;
+    a.pre_in = pre;
+    a.dx = dx;
+    a.dw = dw;
+    a.db = db;
+    a.dy_stride = dy_stride;
+    a.x_stride = x_stride;
+    a.w_stride = w_stride;
+    a.pre_in_stride = pre_stride;
+    a.dx_stride = dx_stride;
+    a.dw_stride = dw_stride;
+    const cudaError_t err = h->dtype == ADACOMP_BF16 ? adacomp::linear_backward<adacomp::bf16>(a, ws, stream)
+                                                     : adacomp::linear_backward<float>(a, ws, stream);
+    return adacomp::launch_result(err, stream);
+}
+
+void adacomp_linear_free(adacomp_linear_t h) { delete h; }
+
+}  // extern "C"

@@ -1,0 +1,650 @@
+// Losses over a vocabulary (softmax cross entropy, distillation from a teacher's top logits): forward and
+// backward passes and their C entry points (adacomp.h).
+#include <new>
+
+#include "product.cuh"
+
+struct adacomp_vocab {
+    int64_t dim = 0, vocab = 0;
+    int32_t dtype = ADACOMP_F32;
+};
+
+namespace adacomp {
+namespace {
+
+constexpr int kListThreads = 256;
+constexpr int kScanThreads = 1024;
+constexpr int kPackThreads = 256;
+
+struct VocabArgs {
+    int64_t rows, dim, vocab;
+    const void *x, *w;
+    int64_t x_stride, w_stride;
+    const void *target;            // cross entropy; or
+    int32_t target_bytes;
+    const int32_t* index;          // a teacher's lists
+    const void* logit;
+    int64_t index_stride, logit_stride;
+    int32_t logit_dtype, k;
+    float temperature;
+    float *loss, *lse_out;         // forward
+    const float *lse, *dloss;      // backward
+    int64_t dloss_stride;
+    void *dx, *dw;
+    int64_t dx_stride, dw_stride;
+};
+
+struct VocabParts {
+    int32_t *index, *map, *count;
+    float *q, *given;      // weights; sum of q log q: -inf for a row without a loss, NaN for one without a value
+    float2* part;          // forward
+    float* picked;
+    float* acc;            // backward: dx so far
+    void *x, *dz;          // the rows that have a loss, one behind the other; a piece's gradient
+    int64_t x_stride, dz_stride, piece;
+};
+
+// Columns of a piece: so many that the piece's gradient has some 2^27 elements, and no fewer than 2048.
+int64_t piece_of(int64_t rows, int64_t vocab)
+{
+    int64_t n = rows > 0 ? ((int64_t)1 << 27) / rows / kStrip * kStrip : vocab;
+    if (n < 2048) n = 2048;
+    return n < vocab ? n : vocab;
+}
+
+VocabParts vocab_parts(Carve& c, int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, int32_t k, bool backward)
+{
+    VocabParts p = {};
+    const int64_t e = dtype_bytes(dtype), padded = round_up(rows, kRows);
+    p.index = c.take<int32_t>(rows * k);
+    p.q = c.take<float>(rows * k);
+    p.given = c.take<float>(rows);
+    p.map = c.take<int32_t>(rows);
+    p.count = c.take<int32_t>(1);
+    p.x_stride = round_up(dim, 16 / e);
+    p.x = c.take<char>(padded * p.x_stride * e);
+    if (backward) {
+        p.piece = piece_of(rows, vocab);
+        p.dz_stride = round_up(p.piece, kStrip);
+        p.dz = c.take<char>(padded * p.dz_stride * e);
+        p.acc = c.take<float>(rows * round_up(dim, 4));
+    } else {
+        p.part = c.take<float2>(rows * ((vocab + kStrip - 1) / kStrip));
+        p.picked = c.take<float>(rows * k);
+    }
+    return p;
+}
+
+// ---------------------------------------------------------------- rows
+struct ListArgs {
+    const void* target;
+    const int32_t* index;
+    const void* logit;
+    int64_t rows, vocab, index_stride, logit_stride;
+    int32_t target_bytes, logit_dtype, k;
+    float scale;
+    int32_t* to_index;
+    float *to_q, *given;
+};
+
+// One token of weight 1 for each row that has a target.
+__global__ void __launch_bounds__(kListThreads) vocab_target_kernel(const ListArgs a)
+{
+    ptx::griddep_wait();
+    for (int64_t r = (int64_t)blockIdx.x * kListThreads + threadIdx.x; r < a.rows; r += (int64_t)gridDim.x * kListThreads) {
+        const int64_t t = a.target_bytes == 8 ? static_cast<const int64_t*>(a.target)[r]
+                                              : static_cast<const int32_t*>(a.target)[r];
+        a.to_index[r] = t >= 0 && t < a.vocab ? (int32_t)t : INT32_MAX;
+        a.to_q[r] = 1.0f;
+        a.given[r] = t < 0 ? -INFINITY : t < a.vocab ? 0.0f : NAN;
+    }
+}
+
+// A teacher's list of a row by a warp: softmax of its logits, and the tokens in ascending order (each place is
+// the number of places before it, so equal tokens keep their order).
+template <typename L> __global__ void __launch_bounds__(kListThreads) vocab_teacher_kernel(const ListArgs a)
+{
+    __shared__ int32_t keys[kListThreads / 32][ADACOMP_MAX_TEACHER];
+    ptx::griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int64_t r = (int64_t)blockIdx.x * (kListThreads / 32) + warp; r < a.rows;
+         r += (int64_t)gridDim.x * (kListThreads / 32)) {
+        const int32_t* index = a.index + r * a.index_stride;
+        const L* logit = static_cast<const L*>(a.logit) + r * a.logit_stride;
+        float u[ADACOMP_MAX_TEACHER / 32], top = -INFINITY;
+        bool some = false, bad = false, none = false;  // none: a logit that is NaN
+#pragma unroll
+        for (int i = 0; i < ADACOMP_MAX_TEACHER / 32; ++i) {
+            const int j = i * 32 + lane;
+            u[i] = -INFINITY;
+            if (j >= a.k) continue;
+            const int32_t t = index[j];
+            keys[warp][j] = t >= 0 ? t : INT32_MAX;
+            if (t < 0) continue;
+            some = true;
+            bad = bad || t >= a.vocab;
+            u[i] = to_f32(logit[j]) * a.scale;
+            none = none || u[i] != u[i];
+            top = fmaxf(top, u[i]);
+        }
+        some = __any_sync(0xffffffffu, some);
+        bad = __any_sync(0xffffffffu, bad);
+        none = __any_sync(0xffffffffu, none);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (bad || none || top == -INFINITY || top == INFINITY) {  // no list, or none that has a value
+            for (int j = lane; j < a.k; j += 32) {
+                a.to_index[r * a.k + j] = INT32_MAX;
+                a.to_q[r * a.k + j] = 0.0f;
+            }
+            if (lane == 0) a.given[r] = some ? NAN : -INFINITY;
+            __syncwarp();
+            continue;
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < ADACOMP_MAX_TEACHER / 32; ++i) sum += u[i] > -INFINITY ? expf(u[i] - top) : 0.0f;
+        sum = warp_sum(sum);
+        const float log_sum = logf(sum);
+        float given = 0.0f;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < ADACOMP_MAX_TEACHER / 32; ++i) {
+            const int j = i * 32 + lane;
+            if (j >= a.k) continue;
+            const float q = u[i] > -INFINITY ? expf(u[i] - top) / sum : 0.0f;
+            if (q > 0.0f) given += q * (u[i] - top - log_sum);
+            const int32_t key = keys[warp][j];
+            int place = 0;
+            for (int o = 0; o < a.k; ++o) place += keys[warp][o] < key || (keys[warp][o] == key && o < j);
+            a.to_index[r * a.k + place] = key;
+            a.to_q[r * a.k + place] = q;
+        }
+        given = warp_sum(given);
+        if (lane == 0) a.given[r] = given;
+        __syncwarp();
+    }
+}
+
+// The rows that have a loss, in their order, and how many there are. One CTA.
+__global__ void __launch_bounds__(kScanThreads) vocab_rows_kernel(const float* given, int64_t rows, int32_t* map, int32_t* count)
+{
+    constexpr int kEach = 8;
+    __shared__ int32_t sums[kScanThreads / 32];
+    ptx::griddep_wait();
+    int32_t before = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int64_t r0 = 0; r0 < rows; r0 += kScanThreads * kEach) {
+        bool there[kEach];
+        int32_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int64_t r = r0 + threadIdx.x * kEach + i;
+            there[i] = r < rows && given[r] != -INFINITY;
+            mine += there[i];
+        }
+        int32_t sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane == 31) sums[warp] = sum;
+        __syncthreads();
+        int32_t at = before + sum - mine, all = 0;
+        for (int i = 0; i < kScanThreads / 32; ++i) {
+            if (i < warp) at += sums[i];
+            all += sums[i];
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (there[i]) map[at++] = (int32_t)(r0 + threadIdx.x * kEach + i);
+        before += all;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) *count = before;
+}
+
+struct GatherArgs {
+    const void* x;
+    void *to, *dx;
+    const float* given;
+    const int32_t *map, *count;
+    int64_t rows, dim, x_stride, to_stride, dx_stride;
+};
+
+// The rows that have a loss one behind the other, and zeros up to a whole tile; the other rows of dx are zeros.
+template <typename T> __global__ void __launch_bounds__(kPackThreads) vocab_gather_kernel(const GatherArgs a)
+{
+    ptx::griddep_wait();
+    const int64_t count = *a.count, end = (count + kRows - 1) / kRows * kRows;
+    const T zero = from_f32<T>(0.0f);
+    for (int64_t r = blockIdx.x; r < end; r += gridDim.x) {
+        const T* x = r < count ? static_cast<const T*>(a.x) + (int64_t)a.map[r] * a.x_stride : nullptr;
+        T* to = static_cast<T*>(a.to) + r * a.to_stride;
+        for (int64_t i = threadIdx.x; i < a.dim; i += kPackThreads) to[i] = x ? x[i] : zero;
+    }
+    if (!a.dx) return;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        if (a.given[r] != -INFINITY) continue;
+        T* dx = static_cast<T*>(a.dx) + r * a.dx_stride;
+        for (int64_t i = threadIdx.x; i < a.dim; i += kPackThreads) dx[i] = zero;
+    }
+}
+
+struct JoinArgs {
+    const float2* part;
+    const float *picked, *q, *given;
+    const int32_t *map, *count;
+    float *loss, *lse;
+    int64_t rows, strips;
+    int32_t k;
+    float temperature;
+};
+
+// A row's strips joined, and its loss, by a warp; rows without a loss are 0.
+__global__ void __launch_bounds__(kListThreads) vocab_join_kernel(const JoinArgs a)
+{
+    ptx::griddep_wait();
+    const int lane = threadIdx.x & 31, warps = kListThreads / 32;
+    const int64_t count = *a.count, first = (int64_t)blockIdx.x * warps + (threadIdx.x >> 5);
+    for (int64_t r = first; r < count; r += (int64_t)gridDim.x * warps) {
+        float top = -INFINITY, sum = 0.0f;
+        for (int64_t i = lane; i < a.strips; i += 32) top = fmaxf(top, a.part[i * a.rows + r].x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float from = top == -INFINITY ? 0.0f : top;
+        for (int64_t i = lane; i < a.strips; i += 32) {
+            const float2 p = a.part[i * a.rows + r];
+            sum += p.y * expf(p.x - from);
+        }
+        sum = warp_sum(sum);
+        const float lse = top + logf(sum);
+        const int64_t row = a.map[r];
+        const float given = a.given[row];
+        float mean = 0.0f;  // of the logits under q
+        if (given == given)
+            for (int j = lane; j < a.k; j += 32) {
+                const float q = a.q[row * a.k + j];
+                if (q > 0.0f) mean += q * a.picked[row * a.k + j];
+            }
+        mean = warp_sum(mean);
+        if (lane == 0) {
+            a.lse[row] = lse;
+            a.loss[row] = a.temperature * a.temperature * (given + (lse - mean));
+        }
+    }
+    for (int64_t r = first; r < a.rows; r += (int64_t)gridDim.x * warps)
+        if (a.given[r] == -INFINITY && lane == 0) a.loss[r] = a.lse[r] = 0.0f;
+}
+
+// ---------------------------------------------------------------- passes
+unsigned blocks_of(int64_t n, int64_t each, int64_t most)
+{
+    const int64_t b = (n + each - 1) / each;
+    return (unsigned)(b < 1 ? 1 : b < most ? b : most);
+}
+
+// The lists, the rows that have a loss, and their copies.
+template <typename T> cudaError_t vocab_rows(const VocabArgs& a, const VocabParts& p, cudaStream_t stream)
+{
+    ListArgs l = {};
+    l.target = a.target;
+    l.index = a.index;
+    l.logit = a.logit;
+    l.rows = a.rows;
+    l.vocab = a.vocab;
+    l.index_stride = a.index_stride;
+    l.logit_stride = a.logit_stride;
+    l.target_bytes = a.target_bytes;
+    l.logit_dtype = a.logit_dtype;
+    l.k = a.k;
+    l.scale = 1.0f / a.temperature;
+    l.to_index = p.index;
+    l.to_q = p.q;
+    l.given = p.given;
+    cudaError_t e;
+    if (a.target) e = launch_after(vocab_target_kernel, dim3(blocks_of(a.rows, kListThreads, 1024)), dim3(kListThreads), 0, stream, l);
+    else
+        e = launch_after(a.logit_dtype == ADACOMP_BF16 ? vocab_teacher_kernel<bf16> : vocab_teacher_kernel<float>,
+                         dim3(blocks_of(a.rows, kListThreads / 32, 4096)), dim3(kListThreads), 0, stream, l);
+    if (e != cudaSuccess) return e;
+    e = launch_after(vocab_rows_kernel, dim3(1), dim3(kScanThreads), 0, stream, (const float*)p.given, a.rows, p.map, p.count);
+    if (e != cudaSuccess) return e;
+    GatherArgs g = {};
+    g.x = a.x;
+    g.to = p.x;
+    g.dx = a.dx;
+    g.given = p.given;
+    g.map = p.map;
+    g.count = p.count;
+    g.rows = a.rows;
+    g.dim = a.dim;
+    g.x_stride = a.x_stride;
+    g.to_stride = p.x_stride;
+    g.dx_stride = a.dx_stride;
+    return launch_after(vocab_gather_kernel<T>, dim3(blocks_of(a.rows, 1, 4096)), dim3(kPackThreads), 0, stream, g);
+}
+
+template <typename T> cudaError_t vocab_forward(const VocabArgs& a, void* ws, cudaStream_t stream)
+{
+    Carve carve{static_cast<char*>(ws)};
+    const VocabParts p = vocab_parts(carve, a.rows, a.dim, a.vocab, sizeof(T) == 2 ? ADACOMP_BF16 : ADACOMP_F32, a.k, false);
+    cudaError_t e = vocab_rows<T>(a, p, stream);
+    if (e != cudaSuccess) return e;
+    EpiSoftmax<T> epi = {};
+    epi.part = p.part;
+    epi.picked = p.picked;
+    epi.lists = {p.index, p.q, p.map, a.k};
+    epi.n = a.vocab;
+    epi.rows = a.rows;
+    epi.scale = 1.0f / a.temperature;
+    SimpleArgs g = {};
+    g.a = {p.x, p.x_stride, 1};
+    g.b = {a.w, a.w_stride, 1};
+    g.m = a.rows;
+    g.n = a.vocab;
+    g.k = a.dim;
+    g.m_count = p.count;
+    g.strip = kStrip;
+    e = product_simple<T>(g, epi, stream);
+    if (e != cudaSuccess) return e;
+    JoinArgs j = {};
+    j.part = p.part;
+    j.picked = p.picked;
+    j.q = p.q;
+    j.given = p.given;
+    j.map = p.map;
+    j.count = p.count;
+    j.loss = a.loss;
+    j.lse = a.lse_out;
+    j.rows = a.rows;
+    j.strips = (a.vocab + kStrip - 1) / kStrip;
+    j.k = a.k;
+    j.temperature = a.temperature;
+    return launch_after(vocab_join_kernel, dim3(blocks_of(a.rows, kListThreads / 32, 4096)), dim3(kListThreads), 0, stream, j);
+}
+
+template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, cudaStream_t stream)
+{
+    Carve carve{static_cast<char*>(ws)};
+    const VocabParts p = vocab_parts(carve, a.rows, a.dim, a.vocab, sizeof(T) == 2 ? ADACOMP_BF16 : ADACOMP_F32, a.k, true);
+    cudaError_t e = vocab_rows<T>(a, p, stream);
+    EpiGradient<T> grad = {};
+    grad.dz = static_cast<T*>(p.dz);
+    grad.lists = {p.index, p.q, p.map, a.k};
+    grad.lse = a.lse;
+    grad.dloss = a.dloss;
+    grad.given = p.given;
+    grad.stride = p.dz_stride;
+    grad.dloss_stride = a.dloss_stride;
+    grad.scale = 1.0f / a.temperature;
+    grad.temperature = a.temperature;
+    EpiStore<T> store = {};
+    store.n = a.dim;
+    for (int64_t at = 0; at < a.vocab && e == cudaSuccess; at += p.piece) {
+        const int64_t n = a.vocab - at < p.piece ? a.vocab - at : p.piece;
+        const T* w = static_cast<const T*>(a.w) + at * a.w_stride;
+        grad.n = n;
+        grad.first = at;
+        SimpleArgs g = {};
+        g.a = {p.x, p.x_stride, 1};
+        g.b = {w, a.w_stride, 1};
+        g.m = a.rows;
+        g.n = n;
+        g.k = a.dim;
+        g.m_count = p.count;
+        g.strip = kCols;
+        e = product_simple<T>(g, grad, stream);
+        if (a.dx && e == cudaSuccess) {
+            store.out = static_cast<T*>(a.dx);
+            store.acc = p.acc;
+            store.map = p.map;
+            store.stride = a.dx_stride;
+            store.acc_stride = round_up(a.dim, 4);
+            store.first = at == 0;
+            store.last = at + n == a.vocab;
+            store.whole = whole_rows(a.dx, a.dx_stride, a.rows, sizeof(T));
+            g.a = {p.dz, p.dz_stride, 1};
+            g.b = {w, 1, a.w_stride};
+            g.n = a.dim;
+            g.k = n;
+            e = product_simple<T>(g, store, stream);
+        }
+        if (a.dw && e == cudaSuccess) {
+            store.out = static_cast<T*>(a.dw) + at * a.dw_stride;
+            store.map = nullptr;
+            store.stride = a.dw_stride;
+            store.first = store.last = true;
+            store.whole = whole_rows(a.dw, a.dw_stride, a.vocab, sizeof(T));
+            g = {};
+            g.a = {p.dz, 1, p.dz_stride};
+            g.b = {p.x, 1, p.x_stride};
+            g.m = n;
+            g.n = a.dim;
+            g.k = a.rows;
+            g.k_count = p.count;
+            g.strip = kCols;
+            e = product_simple<T>(g, store, stream);
+        }
+    }
+    return e;
+}
+
+template <typename T> cudaError_t zero_rows(const VocabArgs& a, cudaStream_t stream)  // dw of no rows
+{
+    if (!a.dw) return cudaSuccess;
+    EpiStore<T> store = {};
+    store.out = static_cast<T*>(a.dw);
+    store.stride = a.dw_stride;
+    store.n = a.dim;
+    store.first = store.last = true;
+    store.whole = whole_rows(a.dw, a.dw_stride, a.vocab, sizeof(T));
+    SimpleArgs g = {};
+    g.m = a.vocab;
+    g.n = a.dim;
+    g.strip = kCols;
+    return product_simple<T>(g, store, stream);  // a product of no terms
+}
+
+constexpr int64_t kMostDim = (int64_t)1 << 30, kMostRows = (int64_t)1 << 31;
+
+// What both losses and both passes ask of their arguments.
+adacomp_status vocab_check(adacomp_vocab_t h, const VocabArgs& a, const void* ws)
+{
+    if (!a.x || !a.w || !ws || a.x_stride < 0 || a.w_stride < 0) return ADACOMP_ERR_INVALID_ARG;
+    const uintptr_t e = dtype_bytes(h->dtype);
+    if (!is_aligned(a.x, e) || !is_aligned(a.w, e) || !is_aligned(a.loss, 4) || !is_aligned(a.lse_out, 4) ||
+        !is_aligned(a.lse, 4) || !is_aligned(a.dloss, 4) || !is_aligned(a.dx, e) || !is_aligned(a.dw, e) ||
+        (a.target && !is_aligned(a.target, a.target_bytes)) || !is_aligned(a.index, 4) ||
+        (a.logit && !is_aligned(a.logit, dtype_bytes(a.logit_dtype))) || !is_aligned(ws, 16))
+        return ADACOMP_ERR_ALIGNMENT;
+    return ADACOMP_OK;
+}
+
+adacomp_status vocab_pass(adacomp_vocab_t h, VocabArgs& a, bool backward, void* ws, size_t ws_bytes, cudaStream_t stream)
+{
+    a.dim = h->dim;
+    a.vocab = h->vocab;
+    if (a.rows > 0) {
+        const adacomp_status s = vocab_check(h, a, ws);
+        if (s != ADACOMP_OK) return s;
+    }
+    const bool narrow = h->dtype == ADACOMP_BF16;
+    if (backward) {
+        if ((!a.dx && !a.dw) || a.dloss_stride < 0 || (a.rows > 0 && (!a.lse || !a.dloss)) ||
+            (a.dx && a.rows > 1 && a.dx_stride < a.dim) || (a.dw && a.vocab > 1 && a.dw_stride < a.dim))
+            return ADACOMP_ERR_INVALID_ARG;
+        if (!is_aligned(a.dw, dtype_bytes(h->dtype))) return ADACOMP_ERR_ALIGNMENT;
+        if (a.rows == 0) return launch_result(narrow ? zero_rows<bf16>(a, stream) : zero_rows<float>(a, stream), stream);
+    } else {
+        if (a.rows == 0) return ADACOMP_OK;
+        if (!a.loss || !a.lse_out) return ADACOMP_ERR_INVALID_ARG;
+    }
+    Carve need;
+    vocab_parts(need, a.rows, a.dim, a.vocab, h->dtype, a.k, backward);
+    if (ws_bytes < need.at) return ADACOMP_ERR_WORKSPACE;
+    const cudaError_t e = backward ? (narrow ? vocab_backward<bf16>(a, ws, stream) : vocab_backward<float>(a, ws, stream))
+                                   : (narrow ? vocab_forward<bf16>(a, ws, stream) : vocab_forward<float>(a, ws, stream));
+    return launch_result(e, stream);
+}
+
+size_t vocab_bytes(adacomp_vocab_t h, int64_t rows, int32_t k, bool backward)
+{
+    if (!h || rows < 0 || rows >= kMostRows || k < 1 || k > ADACOMP_MAX_TEACHER) return 0;
+    Carve c;
+    vocab_parts(c, rows, h->dim, h->vocab, h->dtype, k, backward);
+    return c.at;
+}
+
+bool target_fits(const VocabArgs& a)
+{
+    return (a.target_bytes == 4 || a.target_bytes == 8) && (a.rows == 0 || a.target);
+}
+
+bool teacher_fits(const VocabArgs& a)
+{
+    return a.k >= 1 && a.k <= ADACOMP_MAX_TEACHER && known_dtype(a.logit_dtype) && a.temperature > 0.0f &&
+           std::isfinite(a.temperature) &&
+           (a.rows == 0 || (a.index && a.logit && a.index_stride >= 0 && a.logit_stride >= 0));
+}
+
+}  // namespace
+}  // namespace adacomp
+
+extern "C" {
+
+adacomp_status adacomp_vocab_init(adacomp_vocab_t* out, int64_t dim, int64_t vocab, adacomp_dtype dtype)
+{
+    if (!out) return ADACOMP_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (dim < 1 || dim > adacomp::kMostDim || vocab < 1 || vocab > adacomp::kMostDim || !adacomp::known_dtype(dtype))
+        return ADACOMP_ERR_INVALID_ARG;
+    adacomp_vocab* h = new (std::nothrow) adacomp_vocab;
+    if (!h) return ADACOMP_ERR_INVALID_ARG;
+    h->dim = dim;
+    h->vocab = vocab;
+    h->dtype = dtype;
+    *out = h;
+    return ADACOMP_OK;
+}
+
+size_t adacomp_vocab_loss_forward_ws_bytes(adacomp_vocab_t h, int64_t rows) { return adacomp::vocab_bytes(h, rows, 1, false); }
+size_t adacomp_vocab_loss_backward_ws_bytes(adacomp_vocab_t h, int64_t rows) { return adacomp::vocab_bytes(h, rows, 1, true); }
+size_t adacomp_distill_forward_ws_bytes(adacomp_vocab_t h, int64_t rows, int32_t k) { return adacomp::vocab_bytes(h, rows, k, false); }
+size_t adacomp_distill_backward_ws_bytes(adacomp_vocab_t h, int64_t rows, int32_t k) { return adacomp::vocab_bytes(h, rows, k, true); }
+
+adacomp_status adacomp_vocab_loss_forward(adacomp_vocab_t h, int64_t rows, const void* x, int64_t x_stride,
+                                          const void* w, int64_t w_stride, const void* target, int32_t target_bytes,
+                                          float* loss, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream)
+{
+    adacomp::TrainRange range("adacomp_vocab_loss_forward");
+    if (!h || rows < 0 || rows >= adacomp::kMostRows) return ADACOMP_ERR_INVALID_ARG;
+    adacomp::VocabArgs a = {};
+    a.rows = rows;
+    a.x = x;
+    a.x_stride = x_stride;
+    a.w = w;
+    a.w_stride = w_stride;
+    a.target = target;
+    a.target_bytes = target_bytes;
+    a.k = 1;
+    a.temperature = 1.0f;
+    a.loss = loss;
+    a.lse_out = lse;
+    if (!adacomp::target_fits(a)) return ADACOMP_ERR_INVALID_ARG;
+    return adacomp::vocab_pass(h, a, false, ws, ws_bytes, stream);
+}
+
+adacomp_status adacomp_vocab_loss_backward(adacomp_vocab_t h, int64_t rows, const void* x, int64_t x_stride,
+                                           const void* w, int64_t w_stride, const void* target, int32_t target_bytes,
+                                           const float* lse, const float* dloss, int64_t dloss_stride, void* dx,
+                                           int64_t dx_stride, void* dw, int64_t dw_stride, void* ws, size_t ws_bytes,
+                                           cudaStream_t stream)
+{
+    adacomp::TrainRange range("adacomp_vocab_loss_backward");
+    if (!h || rows < 0 || rows >= adacomp::kMostRows) return ADACOMP_ERR_INVALID_ARG;
+    adacomp::VocabArgs a = {};
+    a.rows = rows;
+    a.x = x;
+    a.x_stride = x_stride;
+    a.w = w;
+    a.w_stride = w_stride;
+    a.target = target;
+    a.target_bytes = target_bytes;
+    a.k = 1;
+    a.temperature = 1.0f;
+    a.lse = lse;
+    a.dloss = dloss;
+    a.dloss_stride = dloss_stride;
+    a.dx = dx;
+    a.dx_stride = dx_stride;
+    a.dw = dw;
+    a.dw_stride = dw_stride;
+    if (!adacomp::target_fits(a)) return ADACOMP_ERR_INVALID_ARG;
+    return adacomp::vocab_pass(h, a, true, ws, ws_bytes, stream);
+}
+
+adacomp_status adacomp_distill_forward(adacomp_vocab_t h, int64_t rows, const void* x, int64_t x_stride, const void* w,
+                                       int64_t w_stride, int32_t k, const int32_t* index, int64_t index_stride,
+                                       const void* logit, int64_t logit_stride, adacomp_dtype logit_dtype,
+                                       float temperature, float* loss, float* lse, void* ws, size_t ws_bytes,
+                                       cudaStream_t stream)
+{
+    adacomp::TrainRange range("adacomp_distill_forward");
+    if (!h || rows < 0 || rows >= adacomp::kMostRows) return ADACOMP_ERR_INVALID_ARG;
+    adacomp::VocabArgs a = {};
+    a.rows = rows;
+    a.x = x;
+    a.x_stride = x_stride;
+    a.w = w;
+    a.w_stride = w_stride;
+    a.k = k;
+    a.index = index;
+    a.index_stride = index_stride;
+    a.logit = logit;
+    a.logit_stride = logit_stride;
+    a.logit_dtype = logit_dtype;
+    a.temperature = temperature;
+    a.loss = loss;
+    a.lse_out = lse;
+    if (!adacomp::teacher_fits(a)) return ADACOMP_ERR_INVALID_ARG;
+    return adacomp::vocab_pass(h, a, false, ws, ws_bytes, stream);
+}
+
+adacomp_status adacomp_distill_backward(adacomp_vocab_t h, int64_t rows, const void* x, int64_t x_stride, const void* w,
+                                        int64_t w_stride, int32_t k, const int32_t* index, int64_t index_stride,
+                                        const void* logit, int64_t logit_stride, adacomp_dtype logit_dtype,
+                                        float temperature, const float* lse, const float* dloss, int64_t dloss_stride,
+                                        void* dx, int64_t dx_stride, void* dw, int64_t dw_stride, void* ws,
+                                        size_t ws_bytes, cudaStream_t stream)
+{
+    adacomp::TrainRange range("adacomp_distill_backward");
+    if (!h || rows < 0 || rows >= adacomp::kMostRows) return ADACOMP_ERR_INVALID_ARG;
+    adacomp::VocabArgs a = {};
+    a.rows = rows;
+    a.x = x;
+    a.x_stride = x_stride;
+    a.w = w;
+    a.w_stride = w_stride;
+    a.k = k;
+    a.index = index;
+    a.index_stride = index_stride;
+    a.logit = logit;
+    a.logit_stride = logit_stride;
+    a.logit_dtype = logit_dtype;
+    a.temperature = temperature;
+    a.lse = lse;
+    a.dloss = dloss;
+    a.dloss_stride = dloss_stride;
+    a.dx = dx;
+    a.dx_stride = dx_stride;
+    a.dw = dw;
+    a.dw_stride = dw_stride;
+    if (!adacomp::teacher_fits(a)) return ADACOMP_ERR_INVALID_ARG;
+    return adacomp::vocab_pass(h, a, true, ws, ws_bytes, stream);
+}
+
+void adacomp_vocab_free(adacomp_vocab_t h) { delete h; }
+
+}  // extern "C"
