@@ -2,7 +2,7 @@
 #include <initializer_list>
 #include <new>
 
-#include "product.cuh"
+#include "product_tc.cuh"
 
 struct adacomp_linear {
     int64_t in = 0, out = 0;
@@ -23,26 +23,33 @@ struct LinearArgs {
     int64_t x_stride, w_stride, residual_stride, dy_stride, pre_in_stride, y_stride, pre_stride, dx_stride, dw_stride;
 };
 
-struct LinearParts {  // of a backward pass's workspace
-    void* dz;
-    int64_t dz_stride;
-    float* sums;
+struct LinearParts {  // of a pass's workspace
+    float* sums;            // backward: of dz, over slices of the rows
+    bf16 *dz, *x, *w;       // copies of what cannot be read as it lies
+    float* parts;           // of products whose terms are split
 };
 
-LinearParts linear_parts(Carve& c, int64_t rows, int64_t out, int32_t dtype, int32_t act)
+LinearParts linear_parts(Carve& c, int64_t rows, int64_t in, int64_t out, int bytes, bool backward)
 {
     LinearParts p = {};
-    p.sums = c.take<float>(kDzSlices * out);
-    p.dz_stride = round_up(out, 16 / dtype_bytes(dtype));
-    if (act != ADACOMP_ACT_NONE) p.dz = c.take<char>(rows * p.dz_stride * dtype_bytes(dtype));
+    p.x = c.take<bf16>(packed_elements(rows, in, bytes));
+    p.w = c.take<bf16>(packed_elements(out, in, bytes));
+    int64_t most = parts_elements(rows, out);
+    if (backward) {
+        p.sums = c.take<float>(kDzSlices * out);
+        p.dz = c.take<bf16>(packed_elements(rows, out, bytes));
+        const int64_t x = parts_elements(rows, in), w = parts_elements(out, in);
+        most = x > w ? x : w;
+    }
+    p.parts = c.take<float>(most);
     return p;
 }
 
 struct DzArgs {
     const void *dy, *pre;
-    void* dz;
+    bf16* dz;
     float* sums;
-    int64_t rows, n, dy_stride, pre_stride, dz_stride;
+    int64_t rows, n, dy_stride, pre_stride, dz_stride, dz_plane;
     int32_t act, slices;
 };
 
@@ -57,7 +64,17 @@ template <typename T> __global__ void __launch_bounds__(kDzThreads) linear_dz_ke
         float v = to_f32(static_cast<const T*>(a.dy)[r * a.dy_stride + c]);
         if (a.act != ADACOMP_ACT_NONE) {
             v *= slope(to_f32(static_cast<const T*>(a.pre)[r * a.pre_stride + c]), a.act);
-            if (a.dz) static_cast<T*>(a.dz)[r * a.dz_stride + c] = from_f32<T>(v);
+            if (a.dz) {
+                bf16* dz = a.dz + r * a.dz_stride + c;
+                if constexpr (sizeof(T) == 4) {
+                    bf16 part[kPlanes];
+                    split_parts(v, part);
+#pragma unroll
+                    for (int p = 0; p < kPlanes; ++p) dz[p * a.dz_plane] = part[p];
+                } else {
+                    *dz = from_f32<bf16>(v);
+                }
+            }
         }
         sum += v;
     }
@@ -74,7 +91,7 @@ template <typename T> __global__ void __launch_bounds__(kDzThreads) linear_db_ke
     db[c] = from_f32<T>(s);
 }
 
-template <typename T> cudaError_t linear_forward(const LinearArgs& a, cudaStream_t stream)
+template <typename T> cudaError_t linear_forward(const LinearArgs& a, void* ws, cudaStream_t stream)
 {
     EpiLinear<T> epi = {};
     epi.y = static_cast<T*>(a.y);
@@ -90,68 +107,70 @@ template <typename T> cudaError_t linear_forward(const LinearArgs& a, cudaStream
     epi.pre_whole = whole_rows(a.pre, a.pre_stride, a.rows, sizeof(T));
     epi.bias_whole = is_aligned(a.bias, 16);
     epi.residual_whole = whole_rows(a.residual, a.residual_stride, a.rows, sizeof(T));
-    SimpleArgs g = {};
-    g.a = {a.x, a.x_stride, 1};
-    g.b = {a.w, a.w_stride, 1};
+    Carve carve{static_cast<char*>(ws)};
+    const LinearParts p = linear_parts(carve, a.rows, a.in, a.out, sizeof(T), false);
+    Matrix x, w;
+    cudaError_t e = take_matrix<T>(&x, a.x, a.x_stride, a.rows, a.in, p.x, stream);
+    if (e == cudaSuccess) e = take_matrix<T>(&w, a.w, a.w_stride, a.out, a.in, p.w, stream);
+    if (e != cudaSuccess) return e;
+    TcArgs g = {};
     g.m = a.rows;
     g.n = a.out;
     g.k = a.in;
-    g.strip = kCols;
-    return product_simple<T>(g, epi, stream);
+    return product_tc<T>(x, false, w, false, g, p.parts, epi, stream);
 }
 
 template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws, cudaStream_t stream)
 {
     Carve carve{static_cast<char*>(ws)};
-    const LinearParts p = linear_parts(carve, a.rows, a.out, sizeof(T) == 2 ? ADACOMP_BF16 : ADACOMP_F32, a.act);
-    const bool act = a.act != ADACOMP_ACT_NONE;
+    const LinearParts p = linear_parts(carve, a.rows, a.in, a.out, sizeof(T), true);
+    const bool act = a.act != ADACOMP_ACT_NONE, products = a.dx || a.dw;
     cudaError_t e = cudaSuccess;
-    if ((act && (a.dx || a.dw)) || a.db) {
+    Matrix dz = {p.dz, a.rows, a.out, round_up(a.out, 8), a.rows * round_up(a.out, 8)}, x, w;
+    if ((act && products) || a.db) {
         DzArgs d = {};
         d.dy = a.dy;
         d.pre = a.pre_in;
-        d.dz = a.dx || a.dw ? p.dz : nullptr;
+        d.dz = products ? p.dz : nullptr;
         d.sums = p.sums;
         d.rows = a.rows;
         d.n = a.out;
         d.dy_stride = a.dy_stride;
         d.pre_stride = a.pre_in_stride;
-        d.dz_stride = p.dz_stride;
+        d.dz_stride = dz.stride;
+        d.dz_plane = dz.plane;
         d.act = a.act;
         d.slices = (int32_t)(a.rows < kDzSlices ? a.rows : kDzSlices);
         const unsigned blocks = (unsigned)((a.out + kDzThreads - 1) / kDzThreads);
         if (d.slices) e = launch_after(linear_dz_kernel<T>, dim3(blocks, d.slices), dim3(kDzThreads), 0, stream, d);
         if (e == cudaSuccess && a.db)
-            e = launch_after(linear_db_kernel<T>, dim3(blocks), dim3(kDzThreads), 0, stream, p.sums, static_cast<T*>(a.db), a.out, d.slices);
-        if (e != cudaSuccess) return e;
+            e = launch_after(linear_db_kernel<T>, dim3(blocks), dim3(kDzThreads), 0, stream, (const float*)p.sums, static_cast<T*>(a.db), a.out, d.slices);
     }
-    const Operand dz = act ? Operand{p.dz, p.dz_stride, 1} : Operand{a.dy, a.dy_stride, 1};
-    SimpleArgs g = {};
+    if (e == cudaSuccess && !act && products) e = take_matrix<T>(&dz, a.dy, a.dy_stride, a.rows, a.out, p.dz, stream);
+    TcArgs g = {};
     EpiStore<T> epi = {};
     epi.first = epi.last = true;
-    g.strip = kCols;
-    if (a.dx) {
-        g.a = dz;
-        g.b = {a.w, 1, a.w_stride};
+    if (a.dx && a.rows && e == cudaSuccess) {
+        e = take_matrix<T>(&w, a.w, a.w_stride, a.out, a.in, p.w, stream);
+        if (e != cudaSuccess) return e;
         g.m = a.rows;
         g.n = epi.n = a.in;
         g.k = a.out;
         epi.out = static_cast<T*>(a.dx);
         epi.stride = a.dx_stride;
         epi.whole = whole_rows(a.dx, a.dx_stride, a.rows, sizeof(T));
-        e = product_simple<T>(g, epi, stream);
-        if (e != cudaSuccess) return e;
+        e = product_tc<T>(dz, false, w, true, g, p.parts, epi, stream);
     }
-    if (a.dw) {
-        g.a = {dz.p, 1, dz.outer};
-        g.b = {a.x, 1, a.x_stride};
+    if (a.dw && e == cudaSuccess) {
         g.m = a.out;
         g.n = epi.n = a.in;
         g.k = a.rows;
         epi.out = static_cast<T*>(a.dw);
         epi.stride = a.dw_stride;
         epi.whole = whole_rows(a.dw, a.dw_stride, a.out, sizeof(T));
-        e = product_simple<T>(g, epi, stream);
+        if (a.rows == 0) return product_none<T>(g.m, g.n, epi, stream);
+        e = take_matrix<T>(&x, a.x, a.x_stride, a.rows, a.in, p.x, stream);
+        if (e == cudaSuccess) e = product_tc<T>(dz, true, x, true, g, p.parts, epi, stream);
     }
     return e;
 }
@@ -185,16 +204,17 @@ adacomp_status adacomp_linear_init(adacomp_linear_t* out, int64_t in_dim, int64_
 
 size_t adacomp_linear_forward_ws_bytes(adacomp_linear_t h, int64_t rows)
 {
-    (void)h;
-    (void)rows;
-    return 0;
+    if (!h || rows < 0 || rows >= adacomp::kMostRows) return 0;
+    adacomp::Carve c;
+    adacomp::linear_parts(c, rows, h->in, h->out, adacomp::dtype_bytes(h->dtype), false);
+    return c.at;
 }
 
 size_t adacomp_linear_backward_ws_bytes(adacomp_linear_t h, int64_t rows)
 {
     if (!h || rows < 0 || rows >= adacomp::kMostRows) return 0;
     adacomp::Carve c;
-    adacomp::linear_parts(c, rows, h->out, h->dtype, h->act);
+    adacomp::linear_parts(c, rows, h->in, h->out, adacomp::dtype_bytes(h->dtype), true);
     return c.at;
 }
 
@@ -230,8 +250,8 @@ adacomp_status adacomp_linear_forward(adacomp_linear_t h, int64_t rows, const vo
     a.residual_stride = residual_stride;
     a.y_stride = y_stride;
     a.pre_stride = pre_stride;
-    const cudaError_t err = h->dtype == ADACOMP_BF16 ? adacomp::linear_forward<adacomp::bf16>(a, stream)
-                                                     : adacomp::linear_forward<float>(a, stream);
+    const cudaError_t err = h->dtype == ADACOMP_BF16 ? adacomp::linear_forward<adacomp::bf16>(a, ws, stream)
+                                                     : adacomp::linear_forward<float>(a, ws, stream);
     return adacomp::launch_result(err, stream);
 }
 

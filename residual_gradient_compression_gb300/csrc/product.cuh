@@ -3,7 +3,8 @@
 //
 // A product is C(m, n) = sum over k of A(m, k) B(n, k). Whichever kernel forms it hands an epilogue
 // the sums of one row, 32 columns at a time and in ascending order within a strip, in one thread's
-// registers: begin(row), chunk(columns) for the strip's columns, end(strip).
+// registers: begin(row), chunk(columns) for the strip's columns, end(strip). kZeros: rows past the last one, up to
+// a tile's end, are set to zeros.
 #pragma once
 
 #include "train_common.cuh"
@@ -25,7 +26,7 @@ struct Carve {
 namespace {
 
 constexpr int kCols = 32;    // columns of a chunk
-constexpr int kStrip = 256;  // of a strip: what a softmax's partial sums are kept for
+constexpr int kStrip = 128;  // of a strip: what a softmax's partial sums are kept for
 constexpr int kRows = 128;   // rows of a tile
 
 inline int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
@@ -88,6 +89,43 @@ inline bool whole_rows(const void* p, int64_t stride, int64_t rows, int bytes)
     return is_aligned(p, 16) && (rows < 2 || stride * bytes % 16 == 0);
 }
 
+// ---------------------------------------------------------------- fp32 numbers in parts
+constexpr int kPlanes = 4;  // of bf16 numbers for an fp32 matrix
+
+// x = top + mid + low exactly (but for what is below 2^-133), each a bf16 number. A value that is not finite has only a
+// top; the fourth plane is the top without such values, for the products with the other operand's lower parts
+// (infinity times a part that is 0 would be NaN).
+__device__ __forceinline__ void split_parts(float x, bf16 (&part)[kPlanes])
+{
+    part[0] = __float2bfloat16_rn(x);
+    part[1] = part[2] = part[3] = __float2bfloat16_rn(0.0f);
+    if (!(fabsf(x) <= 3.402823466e38f)) return;
+    if (__hisinf(part[0])) part[0] = __float2bfloat16_rz(x);  // rounded past the largest bf16 number
+    const float rest = x - __bfloat162float(part[0]);
+    part[1] = __float2bfloat16_rn(rest);
+    part[2] = __float2bfloat16_rn(rest - __bfloat162float(part[1]));
+    part[3] = part[0];
+}
+
+// A row's columns as operands of another product: bf16 numbers, or, of an fp32 matrix, planes of them.
+template <typename T> __device__ __forceinline__ void put_parts(bf16* p, int64_t plane, const float (&v)[kCols], int64_t left)
+{
+    if constexpr (sizeof(T) == 2) {
+        put_chunk(p, v, left, true);
+    } else {
+        float part[kPlanes][kCols];
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+            bf16 each[kPlanes];
+            split_parts(v[i], each);
+#pragma unroll
+            for (int j = 0; j < kPlanes; ++j) part[j][i] = __bfloat162float(each[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kPlanes; ++j) put_chunk(p + j * plane, part[j], left, true);
+    }
+}
+
 // ---------------------------------------------------------------- activations
 __device__ __forceinline__ float activate(float z, int kind)
 {
@@ -126,8 +164,9 @@ template <typename T> struct EpiLinear {
     int64_t y_stride, pre_stride, residual_stride, n;
     int32_t act;
     bool y_whole, pre_whole, bias_whole, residual_whole;
+    static constexpr bool kZeros = false;
     struct State {};
-    __device__ __forceinline__ void begin(State&, int64_t, int64_t) const {}
+    __device__ __forceinline__ void begin(State&, int64_t, int64_t, int) const {}
     __device__ __forceinline__ void chunk(State&, int64_t r, int64_t c, float (&v)[kCols]) const
     {
         if (c >= n) return;
@@ -152,6 +191,7 @@ template <typename T> struct EpiLinear {
         put_chunk(y + r * y_stride + c, v, left, y_whole);
     }
     __device__ __forceinline__ void end(State&, int64_t, int64_t) const {}
+    __device__ __forceinline__ void zeros(int64_t, int64_t) const {}
 };
 
 // The sums themselves, in rows that `map` may move; with acc, added up over several products in
@@ -160,12 +200,16 @@ template <typename T> struct EpiStore {
     T* out;
     float* acc;
     const int32_t* map;
-    int64_t stride, acc_stride, n;
+    int64_t stride, acc_stride, n, split_stride;  // split_stride: between the parts of a product whose terms are split
     bool first, last, whole;
+    static constexpr bool kZeros = false;
     struct State {
-        int64_t to;
+        T* to;
     };
-    __device__ __forceinline__ void begin(State& s, int64_t r, int64_t) const { s.to = map ? map[r] : r; }
+    __device__ __forceinline__ void begin(State& s, int64_t r, int64_t, int split) const
+    {
+        s.to = out + split * split_stride + (map ? map[r] : r) * stride;
+    }
     __device__ __forceinline__ void chunk(State& s, int64_t r, int64_t c, float (&v)[kCols]) const
     {
         if (c >= n) return;
@@ -176,10 +220,11 @@ template <typename T> struct EpiStore {
 #pragma unroll
             for (int i = 0; i < kCols; ++i) v[i] += b[i];
         }
-        if (last) put_chunk(out + s.to * stride + c, v, left, whole);
+        if (last) put_chunk(s.to + c, v, left, whole);
         else put_chunk(acc + r * acc_stride + c, v, left, true);
     }
     __device__ __forceinline__ void end(State&, int64_t, int64_t) const {}
+    __device__ __forceinline__ void zeros(int64_t, int64_t) const {}
 };
 
 // exp of differences from a row's maximum or logarithm: the quick form's error (2 + 1.2 |x| units
@@ -211,7 +256,7 @@ __device__ __forceinline__ int first_place(const int32_t* index, int k, int64_t 
     return lo;
 }
 
-// Of each strip of 256 logits of a row: their maximum and the sum of exp(z - maximum), in one pass
+// Of each strip of 128 logits of a row: their maximum and the sum of exp(z - maximum), in one pass
 // over the sums as they come; and the logits of the listed tokens.
 template <typename T> struct EpiSoftmax {
     float2* part;  // [strips][rows]
@@ -219,13 +264,14 @@ template <typename T> struct EpiSoftmax {
     Lists lists;
     int64_t n, rows;
     float scale;  // of the logits: 1 / temperature
+    static constexpr bool kZeros = false;
     struct State {
         float top, sum;
         const int32_t* index;
         float* picked;
         int at, next;
     };
-    __device__ __forceinline__ void begin(State& s, int64_t r, int64_t c) const
+    __device__ __forceinline__ void begin(State& s, int64_t r, int64_t c, int) const
     {
         const int64_t row = lists.map[r];
         s.top = -INFINITY;
@@ -265,15 +311,18 @@ template <typename T> struct EpiSoftmax {
     {
         part[strip * rows + r] = make_float2(s.top, s.sum);
     }
+    __device__ __forceinline__ void zeros(int64_t, int64_t) const {}
 };
 
-// The logits' gradient (p - q) * dloss * temperature of columns first .. first + n - 1, rounded to T.
+// The logits' gradient (p - q) * dloss * temperature of columns first .. first + n - 1: rounded to
+// bf16, or, of fp32 operands, in parts.
 template <typename T> struct EpiGradient {
-    T* dz;  // [rows][stride]
+    bf16* dz;  // [planes][rows][stride]
     Lists lists;
     const float *lse, *dloss, *given;
-    int64_t stride, n, first, dloss_stride;
+    int64_t stride, plane, rows, n, first, dloss_stride;  // rows: that there is room for
     float scale, temperature;
+    static constexpr bool kZeros = true;
     struct State {
         float lse, factor;
         const int32_t* index;
@@ -281,7 +330,7 @@ template <typename T> struct EpiGradient {
         int at;
         int64_t next;
     };
-    __device__ __forceinline__ void begin(State& s, int64_t r, int64_t c) const
+    __device__ __forceinline__ void begin(State& s, int64_t r, int64_t c, int) const
     {
         const int64_t row = lists.map[r];
         s.lse = lse[row];
@@ -305,9 +354,15 @@ template <typename T> struct EpiGradient {
         }
 #pragma unroll
         for (int i = 0; i < kCols; ++i) v[i] *= s.factor;
-        put_chunk(dz + r * stride + c, v, n - c, true);
+        put_parts<T>(dz + r * stride + c, plane, v, n - c);
     }
     __device__ __forceinline__ void end(State&, int64_t, int64_t) const {}
+    __device__ __forceinline__ void zeros(int64_t r, int64_t c) const
+    {
+        if (r >= rows || c >= n) return;
+        float v[kCols] = {};
+        put_parts<T>(dz + r * stride + c, plane, v, n - c);
+    }
 };
 
 // ---------------------------------------------------------------- operands of any layout
@@ -349,7 +404,7 @@ __global__ void __launch_bounds__(kRows) product_simple_kernel(const SimpleArgs 
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t strip = tile % strips, r0 = tile / strips * kRows, r = r0 + threadIdx.x, c0 = strip * g.strip;
         typename Epi::State state;
-        if (r < m) epi.begin(state, r, c0);
+        if (r < m) epi.begin(state, r, c0, 0);
         for (int64_t c = c0; c < c0 + g.strip && c < g.n; c += kCols) {
             float v[kCols] = {};
             for (int64_t k = 0; k < terms; k += kDepth) {

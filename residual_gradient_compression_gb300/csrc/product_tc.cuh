@@ -1,0 +1,578 @@
+// Products on the tensor cores: C(m, n) = sum over k of A(m, k) B(n, k), bf16 operands, fp32 sums.
+//
+// A pair of CTAs (a cluster of two SMs) has tiles of 256 x kN; each loads its 128 rows of A and its half of
+// B's rows for 64 terms at a time, by TMA, into a ring of stages; one thread of the first CTA issues the
+// products (tcgen05.mma, cta_group::2) on both CTAs' shared memory; the sums lie in tensor memory, 128
+// rows in each CTA, in two buffers, so that eight warps hand a tile to the epilogue while the next one
+// is computed. Each operand lies by rows of terms ("k major") or by terms of rows ("mn major", the transposed
+// operands of the gradients): both are copied as they lie and told apart by the matrix descriptors.
+//
+// fp32 operands are four planes of bf16 numbers (split_parts), and their product is the sum of six products of
+// planes, the smallest first.
+#pragma once
+
+#include <cuda.h>
+
+#include "product.cuh"
+
+namespace adacomp {
+namespace {
+
+constexpr int kTcThreads = 384;      // warps 0..3: copies, products, tensor memory, none; 4..11: epilogue
+constexpr int kTcEpilogue = 4;       // the epilogue's first warp
+constexpr int kTcDepth = 64;         // terms of a stage: 128 bytes of bf16
+constexpr int kTcM = 256;            // rows of a pair's tile
+constexpr uint64_t kTcLimit = 2000000000ull;  // ns: of every wait
+
+template <int kN> struct TcShape {
+    static constexpr int kA = 128 * kTcDepth * 2, kB = kN / 2 * kTcDepth * 2;  // bytes of a CTA's stage
+    static constexpr int kStages = 196608 / (kA + kB) < 8 ? 196608 / (kA + kB) : 8;
+    static constexpr int kShared = kStages * (kA + kB) + 1024 + 256;  // 1024: to begin on such a boundary
+};
+
+// ---------------------------------------------------------------- operands
+// A matrix as a product takes it: rows of `cols` bf16 numbers that are contiguous, 16-byte aligned rows `stride`
+// apart, and planes `plane` apart.
+struct Matrix {
+    const bf16* p;
+    int64_t rows, cols, stride, plane;
+};
+
+struct TcArgs {
+    int64_t m, n, k;
+    const int32_t *m_count, *k_count;  // how many of the rows m, or terms k, there are; NULL: all
+    int32_t planes;                    // 1, or kPlanes
+    int32_t splits;                    // of the terms, each a product of its own
+    int32_t a_mn, b_mn;                // operands that lie by terms
+    int32_t group;                     // tiles of rows that are taken before the next column's
+};
+
+struct PackArgs {
+    const void* from;
+    bf16* to;
+    const int32_t *map, *count;  // which rows, and how many; NULL: all
+    int64_t rows, cols, from_stride, to_stride, plane;
+};
+
+// A matrix of any layout by rows of contiguous elements as aligned rows of bf16 numbers (planes of them for fp32); with
+// `count`, zeros from there to a whole tile. A thread takes eight elements at a time.
+constexpr int kTcPack = 256;
+template <typename T> __global__ void __launch_bounds__(kTcPack) pack_kernel(const PackArgs a)
+{
+    ptx::griddep_wait();
+    const int64_t count = a.count ? *a.count : a.rows, rows = a.count ? (count + kRows - 1) / kRows * kRows : count;
+    const int64_t each = (a.cols + 7) / 8, all = rows * each;
+    for (int64_t i = (int64_t)blockIdx.x * kTcPack + threadIdx.x; i < all; i += (int64_t)gridDim.x * kTcPack) {
+        const int64_t r = i / each, c = (i - r * each) * 8;
+        const T* from = static_cast<const T*>(a.from) + (r < count ? (a.map ? (int64_t)a.map[r] : r) * a.from_stride : 0) + c;
+        bf16 v[sizeof(T) == 4 ? kPlanes : 1][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const T x = r < count && c + j < a.cols ? from[j] : from_f32<T>(0.0f);
+            if constexpr (sizeof(T) == 4) {
+                bf16 part[kPlanes];
+                split_parts(x, part);
+#pragma unroll
+                for (int p = 0; p < kPlanes; ++p) v[p][j] = part[p];
+            } else {
+                v[0][j] = x;
+            }
+        }
+        bf16* to = a.to + r * a.to_stride + c;
+#pragma unroll
+        for (int p = 0; p < (sizeof(T) == 4 ? kPlanes : 1); ++p)
+            *reinterpret_cast<uint4*>(to + p * a.plane) = *reinterpret_cast<const uint4*>(v[p]);
+    }
+}
+
+// ---------------------------------------------------------------- instructions
+namespace tc {
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t map_shared(const void* p, uint32_t rank)  // where p is in a CTA of the cluster
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_addr(p)), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t bar)  // an address of the cluster
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A wait on a barrier that other CTAs arrive at, bounded in time; false when it ran out, here or
+// in another warp (dead).
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(ptx::smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead)
+{
+    if (try_wait_cluster(bar, parity)) return true;
+    const uint64_t from = ptx::globaltimer();
+    for (uint32_t i = 1;; ++i) {
+        if (try_wait_cluster(bar, parity)) return true;
+        if ((i & 31) == 0) {
+            if (*dead) return false;
+            if (ptx::globaltimer() - from > kTcLimit) {
+                *dead = 1;
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void load(uint32_t to, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void prefetch(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// Of a tile in shared memory, in the 128-byte swizzle that TMA writes: where it begins, and the distances (bytes) of
+// 64-element blocks along the rows (mn major only) and of groups of eight 128-byte lines.
+__device__ __forceinline__ uint64_t descriptor(uint32_t at, uint32_t block, uint32_t group)
+{
+    return (uint64_t)((at & 0x3ffff) >> 4) | (uint64_t)(block >> 4) << 16 | (uint64_t)(group >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+        : "memory");
+}
+
+// Arrives at the barrier in both CTAs once the products issued so far are done.
+__device__ __forceinline__ void commit(uint64_t* bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            ptx::smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void read_chunk(uint32_t at, uint32_t (&v)[32])  // 32 lanes' rows, 32 columns each
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(at)
+        : "memory");
+}
+
+__device__ __forceinline__ void read_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+}  // namespace tc
+
+// The pairs of planes whose products are summed, the smallest first.
+__device__ __forceinline__ int plane_a(int pass) { return (0x231130 >> 4 * (5 - pass)) & 15; }
+__device__ __forceinline__ int plane_b(int pass) { return (0x321310 >> 4 * (5 - pass)) & 15; }
+
+// ---------------------------------------------------------------- kernel
+template <int kN, typename Epi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+    product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const TcArgs g,
+                      const Epi epi)
+{
+    using Shape = TcShape<kN>;
+    constexpr int kStages = Shape::kStages;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2], drained;
+    __shared__ uint32_t tmem_at;
+    __shared__ int dead_flag;
+    volatile int* dead = &dead_flag;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const uint32_t base = (ptx::smem_addr(raw) + 1023) & ~1023u;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sums_full[i], 1);
+            ptx::mbar_init(&sums_empty[i], 2 * 8);  // a thread of each of both CTAs' epilogue warps
+        }
+        ptx::mbar_init(&drained, 1);
+        dead_flag = 0;
+        ptx::fence_mbar_init();
+        tc::prefetch(&map_a);
+        tc::prefetch(&map_b);
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_addr(&tmem_at)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        tc::fence_before();
+    }
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = tmem_at;
+    ptx::griddep_wait();
+
+    const int64_t m = g.m_count ? *g.m_count : g.m, terms = g.k_count ? *g.k_count : g.k;
+    const int64_t tiles_m = (m + kTcM - 1) / kTcM, tiles_n = (g.n + kN - 1) / kN, tiles = tiles_m * tiles_n;
+    const int64_t blocks = (terms + kTcDepth - 1) / kTcDepth, per_split = (blocks + g.splits - 1) / g.splits;
+    const int passes = g.planes == 1 ? 1 : 6;
+    const int64_t units = tiles * g.splits, first = blockIdx.x / 2, step = gridDim.x / 2;
+    struct Unit {
+        int64_t m0, n0, from, count;
+        int split;
+    };
+    const auto unit_of = [&](int64_t u) {
+        Unit t;
+        t.split = (int)(u / tiles);
+        const int64_t tile = u - t.split * tiles, whole = (int64_t)g.group * tiles_n, band = tile / whole, in = tile - band * whole;
+        const int64_t rows = tiles_m - band * g.group < g.group ? tiles_m - band * g.group : g.group;
+        t.n0 = in / rows * kN;
+        t.m0 = (band * g.group + in % rows) * kTcM;
+        t.from = t.split * per_split;
+        t.count = blocks - t.from < per_split ? blocks - t.from : per_split;
+        if (t.count < 0) t.count = 0;
+        return t;
+    };
+
+    if (warp == 0 && lane == 0) {  // copies
+        uint32_t n = 0;  // stages so far
+        const uint32_t leader = rank & ~1u;
+        bool alive = true;
+        for (int64_t u = first; u < units && alive; u += step) {
+            const Unit t = unit_of(u);
+            const int32_t ma = (int32_t)(t.m0 + rank * 128), nb = (int32_t)(t.n0 + rank * (kN / 2));
+            for (int pass = 0; pass < passes && alive; ++pass) {
+                const int pa = passes == 1 ? 0 : plane_a(pass), pb = passes == 1 ? 0 : plane_b(pass);
+                for (int64_t k = 0; k < t.count; ++k, ++n) {
+                    const int s = (int)(n % kStages);
+                    alive = tc::wait(&empty[s], (n / kStages & 1) ^ 1, dead);
+                    if (!alive) break;
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * (Shape::kA + Shape::kB));
+                    const uint32_t bar = tc::map_shared(&full[s], leader), at = base + s * (Shape::kA + Shape::kB);
+                    const int32_t k0 = (int32_t)((t.from + k) * kTcDepth);
+                    if (g.a_mn) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) tc::load(at + i * 8192, &map_a, ma + 64 * i, k0, pa, bar);
+                    } else {
+                        tc::load(at, &map_a, k0, ma, pa, bar);
+                    }
+                    if (g.b_mn) {
+#pragma unroll
+                        for (int i = 0; i < kN / 128; ++i) tc::load(at + Shape::kA + i * 8192, &map_b, nb + 64 * i, k0, pb, bar);
+                    } else {
+                        tc::load(at + Shape::kA, &map_b, k0, nb, pb, bar);
+                    }
+                }
+            }
+        }
+        if (!alive) {  // the copies in flight end before the CTA does: each stage's last one
+            int none = 0;
+            if (rank == 0)
+                for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+                    tc::wait(&full[i % kStages], i / kStages & 1, &none);
+            else {
+                const uint64_t from = ptx::globaltimer();
+                while (ptx::globaltimer() - from < 10000000ull) {}  // 10 ms, as their barrier is the other CTA's
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {  // products
+        const uint32_t kind = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(g.a_mn != 0) << 15 | (uint32_t)(g.b_mn != 0) << 16 |
+                              (uint32_t)(kN / 8) << 17 | (uint32_t)(kTcM / 16) << 24;
+        // 16 terms further: 32 bytes along a line, or 16 lines
+        const uint32_t step_a = g.a_mn ? 2048 : 32, step_b = g.b_mn ? 2048 : 32;
+        const uint32_t block_a = g.a_mn ? 8192 : 16, block_b = g.b_mn ? 8192 : 16;
+        uint32_t n = 0, done = 0;
+        bool alive = true;
+        for (int64_t u = first; u < units && alive; u += step) {
+            const Unit t = unit_of(u);
+            if (t.count == 0) continue;
+            const int buffer = (int)(done & 1);
+            alive = tc::wait(&sums_empty[buffer], (done / 2 & 1) ^ 1, dead);
+            if (!alive) break;
+            tc::fence_after();
+            const uint32_t d = tmem + buffer * 256;
+            const int64_t all = t.count * passes;
+            for (int64_t i = 0; i < all; ++i, ++n) {
+                const int s = (int)(n % kStages);
+                alive = tc::wait(&full[s], (n / kStages & 1), dead);
+                if (!alive) break;
+                tc::fence_after();
+                const uint32_t at = base + s * (Shape::kA + Shape::kB);
+#pragma unroll
+                for (int j = 0; j < kTcDepth / 16; ++j)
+                    tc::mma(d, tc::descriptor(at + j * step_a, block_a, 1024),
+                            tc::descriptor(at + Shape::kA + j * step_b, block_b, 1024), kind, i > 0 || j > 0);
+                tc::commit(&empty[s]);
+            }
+            if (!alive) break;
+            tc::commit(&sums_full[buffer]);
+            ++done;
+        }
+        if (!alive) {  // the products in flight end before the tensor memory is given back
+            int none = 0;
+            tc::commit(&drained);
+            tc::wait(&drained, 0, &none);
+        }
+    } else if (warp >= kTcEpilogue) {
+        const int quarter = warp & 3, half = (warp - kTcEpilogue) / 4;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        constexpr int kStrips = kN / kStrip, kMine = (kStrips + 1) / 2;  // strips of a tile, and of a half of the warps
+        uint32_t done = 0;
+        bool alive = true;
+        for (int64_t u = first; u < units; u += step) {
+            const Unit t = unit_of(u);
+            const int64_t r = t.m0 + rank * 128 + quarter * 32 + lane;
+            const int buffer = (int)(done & 1);
+            if (t.count && alive) {
+                alive = tc::wait(&sums_full[buffer], (done / 2 & 1), dead);
+                tc::fence_after();
+            }
+            alive = __all_sync(0xffffffffu, alive);
+#pragma unroll 1
+            for (int strip = half * kMine; strip < kStrips && strip < (half + 1) * kMine; ++strip) {
+                const int64_t c0 = t.n0 + strip * kStrip;
+                if (c0 >= g.n) break;
+                typename Epi::State state;
+                if (r < m) epi.begin(state, r, c0, t.split);
+#pragma unroll 1
+                for (int c = 0; c < kStrip; c += kCols) {
+                    float v[kCols];
+                    __syncwarp();
+                    if (t.count && alive) {
+                        uint32_t w[kCols];
+                        tc::read_chunk(lanes + buffer * 256 + strip * kStrip + c, w);
+                        tc::read_wait();
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i) v[i] = __uint_as_float(w[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i) v[i] = alive ? 0.0f : NAN;
+                    }
+                    if (r < m) epi.chunk(state, r, c0 + c, v);
+                    else if (Epi::kZeros) epi.zeros(r, c0 + c);
+                }
+                if (r < m) epi.end(state, r, c0 / kStrip);
+            }
+            if (t.count) {
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::arrive_at(tc::map_shared(&sums_empty[buffer], 0));
+                ++done;
+            }
+        }
+    }
+    __syncthreads();
+    tc::cluster_sync();
+    if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    tc::cluster_sync();
+}
+
+// ---------------------------------------------------------------- host
+// The sums of the parts that the terms were split into, one after the other, handed to an epilogue. A thread has a row's 32
+// columns.
+struct JoinPartsArgs {
+    const float* part;  // [splits][m][stride]
+    int64_t m, n, stride;
+    const int32_t* m_count;
+    int32_t splits;
+};
+
+template <typename Epi> __global__ void __launch_bounds__(kRows) join_parts_kernel(const JoinPartsArgs a, const Epi epi)
+{
+    ptx::griddep_wait();
+    const int64_t m = a.m_count ? *a.m_count : a.m;
+    const int64_t chunks = (a.n + kCols - 1) / kCols, i = (int64_t)blockIdx.x * kRows + threadIdx.x;
+    if (i >= chunks * m) return;
+    const int64_t r = i / chunks, c = (i - r * chunks) * kCols;
+    float v[kCols] = {};
+    for (int s = 0; s < a.splits; ++s) {
+        float b[kCols];
+        get_chunk(a.part + ((int64_t)s * a.m + r) * a.stride + c, b, a.n - c, true);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) v[j] += b[j];
+    }
+    typename Epi::State state;
+    epi.begin(state, r, c, 0);
+    epi.chunk(state, r, c, v);
+    epi.end(state, r, c / kStrip);
+}
+
+// A product of no terms: the epilogue of zeros.
+template <typename T, typename Epi> cudaError_t product_none(int64_t m, int64_t n, const Epi& epi, cudaStream_t stream)
+{
+    const JoinPartsArgs j = {nullptr, m, n, 0, nullptr, 0};
+    const int64_t all = (n + kCols - 1) / kCols * m;
+    return launch_after(join_parts_kernel<Epi>, dim3((unsigned)((all + kRows - 1) / kRows)), dim3(kRows), 0, stream, j, epi);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled()
+{
+    static std::atomic<EncodeTiled> known{nullptr};
+    EncodeTiled f = known.load(std::memory_order_acquire);
+    if (!f) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        f = reinterpret_cast<EncodeTiled>(p);
+        known.store(f, std::memory_order_release);
+    }
+    return f;
+}
+
+// How TMA reads a matrix: 64 numbers of each of `box` rows at a time; zeros past its ends.
+inline cudaError_t tensor_map(CUtensorMap* map, const Matrix& a, int planes, int box)
+{
+    const EncodeTiled f = encode_tiled();
+    if (!f) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.cols, (cuuint64_t)a.rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.stride * 2, (cuuint64_t)(planes > 1 ? a.plane : a.stride) * 2};
+    const cuuint32_t boxes[3] = {(cuuint32_t)kTcDepth, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16*>(a.p), dims, strides, boxes, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+// Whether a bf16 matrix can be read as it lies.
+inline bool as_it_lies(const void* p, int64_t stride, int64_t rows, int64_t cols)
+{
+    return is_aligned(p, 16) && (rows < 2 ? true : stride % 8 == 0 && stride >= cols);
+}
+
+inline Matrix matrix_of(const void* p, int64_t stride, int64_t rows, int64_t cols)
+{
+    return {static_cast<const bf16*>(p), rows, cols, rows < 2 ? round_up(cols, 8) : stride, 0};
+}
+
+inline int64_t packed_elements(int64_t rows, int64_t cols, int bytes)  // of a workspace
+{
+    return rows * round_up(cols, 8) * (bytes == 4 ? kPlanes : 1);
+}
+
+// A matrix of T's as a product takes it: as it lies, or copied to `room` (packed_elements).
+template <typename T>
+cudaError_t take_matrix(Matrix* out, const void* p, int64_t stride, int64_t rows, int64_t cols, bf16* room, cudaStream_t stream,
+                        const int32_t* map = nullptr, const int32_t* count = nullptr, int64_t out_rows = 0)
+{
+    if (sizeof(T) == 2 && !count && as_it_lies(p, stride, rows, cols)) {
+        *out = matrix_of(p, stride, rows, cols);
+        return cudaSuccess;
+    }
+    const int64_t to_rows = count ? out_rows : rows;
+    *out = {room, to_rows, cols, round_up(cols, 8), to_rows * round_up(cols, 8)};
+    PackArgs a = {p, room, map, count, rows, cols, stride, out->stride, out->plane};
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const int64_t need = (to_rows * (out->stride / 8) + kTcPack - 1) / kTcPack, most = (int64_t)sms * 16;
+    if (need == 0) return cudaSuccess;
+    return launch_after(pack_kernel<T>, dim3((unsigned)(need < most ? need : most)), dim3(kTcPack), 0, stream, a);
+}
+
+template <int kN, typename Epi>
+cudaError_t product_tc_n(const Matrix& a, const Matrix& b, const TcArgs& g, const Epi& epi, cudaStream_t stream)
+{
+    CUtensorMap map_a, map_b;
+    cudaError_t e = tensor_map(&map_a, a, g.planes, g.a_mn ? kTcDepth : 128);
+    if (e == cudaSuccess) e = tensor_map(&map_b, b, g.planes, g.b_mn ? kTcDepth : kN / 2);
+    if (e == cudaSuccess) e = allow<product_tc_kernel<kN, Epi>>(TcShape<kN>::kShared);
+    int sms = 0;
+    if (e == cudaSuccess) e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const int64_t units = (g.m + kTcM - 1) / kTcM * ((g.n + kN - 1) / kN) * g.splits, pairs = sms / 2;
+    return launch_after(product_tc_kernel<kN, Epi>, dim3((unsigned)(2 * (units < pairs ? units : pairs))), dim3(kTcThreads),
+                        TcShape<kN>::kShared, stream, map_a, map_b, g, epi);
+}
+
+// The terms of a product with few tiles are split, so that more of the SMs have some; the parts' sums are joined by a
+// kernel of their own.
+constexpr int64_t kMostPairs = 76;
+
+inline int splits_of(int64_t m, int64_t n, int64_t k)
+{
+    const int64_t tiles = (m + kTcM - 1) / kTcM * ((n + 255) / 256), blocks = (k + kTcDepth - 1) / kTcDepth;
+    int64_t s = kMostPairs / (tiles < 1 ? 1 : tiles);
+    if (s > blocks / 4) s = blocks / 4;
+    return (int)(s < 1 ? 1 : s);
+}
+
+inline int64_t parts_elements(int64_t m, int64_t n)  // of a workspace: tiles x splits are at most kMostPairs
+{
+    const int64_t whole = kMostPairs * kTcM * 256, all = kMostPairs * m * round_up(n, 4);
+    return all < whole ? all : whole;
+}
+
+// A product of matrices of T's planes. a_mn, b_mn: the matrix lies by terms (its rows are terms). parts: room for
+// parts_elements, or NULL.
+template <typename T, typename Epi>
+cudaError_t product_tc(const Matrix& a, bool a_mn, const Matrix& b, bool b_mn, TcArgs g, float* parts, const Epi& epi,
+                       cudaStream_t stream)
+{
+    if (g.m <= 0 || g.n <= 0) return cudaSuccess;
+    g.planes = sizeof(T) == 4 ? kPlanes : 1;
+    g.a_mn = a_mn;
+    g.b_mn = b_mn;
+    g.splits = parts ? splits_of(g.m, g.n, g.k) : 1;
+    g.group = 8;
+    if (g.splits == 1) return product_tc_n<256>(a, b, g, epi, stream);
+    EpiStore<float> each = {};
+    each.out = parts;
+    each.stride = round_up(g.n, 4);
+    each.split_stride = g.m * each.stride;
+    each.n = g.n;
+    each.first = each.last = each.whole = true;
+    const cudaError_t e = product_tc_n<256>(a, b, g, each, stream);
+    if (e != cudaSuccess) return e;
+    const JoinPartsArgs j = {parts, g.m, g.n, each.stride, g.m_count, g.splits};
+    const int64_t all = (g.n + kCols - 1) / kCols * g.m;
+    return launch_after(join_parts_kernel<Epi>, dim3((unsigned)((all + kRows - 1) / kRows)), dim3(kRows), 0, stream, j, epi);
+}
+
+}  // namespace
+}  // namespace adacomp

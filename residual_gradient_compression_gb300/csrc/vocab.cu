@@ -2,7 +2,7 @@
 // backward passes and their C entry points (adacomp.h).
 #include <new>
 
-#include "product.cuh"
+#include "product_tc.cuh"
 
 struct adacomp_vocab {
     int64_t dim = 0, vocab = 0;
@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kListThreads = 256;
 constexpr int kScanThreads = 1024;
-constexpr int kPackThreads = 256;
+constexpr int kZeroThreads = 256;
 
 struct VocabArgs {
     int64_t rows, dim, vocab;
@@ -40,8 +40,9 @@ struct VocabParts {
     float2* part;          // forward
     float* picked;
     float* acc;            // backward: dx so far
-    void *x, *dz;          // the rows that have a loss, one behind the other; a piece's gradient
-    int64_t x_stride, dz_stride, piece;
+    bf16 *x, *w, *dz;      // the rows that have a loss, one behind the other; a copy of w; a piece's gradient
+    float* parts;          // of products whose terms are split
+    int64_t padded, dz_stride, piece;
 };
 
 // Columns of a piece: so many that the piece's gradient has some 2^27 elements, and no fewer than 2048.
@@ -52,22 +53,24 @@ int64_t piece_of(int64_t rows, int64_t vocab)
     return n < vocab ? n : vocab;
 }
 
-VocabParts vocab_parts(Carve& c, int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, int32_t k, bool backward)
+VocabParts vocab_parts(Carve& c, int64_t rows, int64_t dim, int64_t vocab, int bytes, int32_t k, bool backward)
 {
     VocabParts p = {};
-    const int64_t e = dtype_bytes(dtype), padded = round_up(rows, kRows);
     p.index = c.take<int32_t>(rows * k);
     p.q = c.take<float>(rows * k);
     p.given = c.take<float>(rows);
     p.map = c.take<int32_t>(rows);
     p.count = c.take<int32_t>(1);
-    p.x_stride = round_up(dim, 16 / e);
-    p.x = c.take<char>(padded * p.x_stride * e);
+    p.padded = round_up(rows, kRows);
+    p.x = c.take<bf16>(packed_elements(p.padded, dim, bytes));
+    p.w = c.take<bf16>(packed_elements(vocab, dim, bytes));
     if (backward) {
         p.piece = piece_of(rows, vocab);
-        p.dz_stride = round_up(p.piece, kStrip);
-        p.dz = c.take<char>(padded * p.dz_stride * e);
+        p.dz_stride = round_up(p.piece, 8);
+        p.dz = c.take<bf16>(packed_elements(p.padded, p.piece, bytes));
         p.acc = c.take<float>(rows * round_up(dim, 4));
+        const int64_t x = parts_elements(rows, dim), w = parts_elements(p.piece, dim);
+        p.parts = c.take<float>(x > w ? x : w);
     } else {
         p.part = c.take<float2>(rows * ((vocab + kStrip - 1) / kStrip));
         p.picked = c.take<float>(rows * k);
@@ -205,30 +208,14 @@ __global__ void __launch_bounds__(kScanThreads) vocab_rows_kernel(const float* g
     if (threadIdx.x == 0) *count = before;
 }
 
-struct GatherArgs {
-    const void* x;
-    void *to, *dx;
-    const float* given;
-    const int32_t *map, *count;
-    int64_t rows, dim, x_stride, to_stride, dx_stride;
-};
-
-// The rows that have a loss one behind the other, and zeros up to a whole tile; the other rows of dx are zeros.
-template <typename T> __global__ void __launch_bounds__(kPackThreads) vocab_gather_kernel(const GatherArgs a)
+// The rows of dx without a loss.
+template <typename T>
+__global__ void __launch_bounds__(kZeroThreads) vocab_zero_kernel(T* dx, int64_t stride, const float* given, int64_t rows, int64_t dim)
 {
     ptx::griddep_wait();
-    const int64_t count = *a.count, end = (count + kRows - 1) / kRows * kRows;
-    const T zero = from_f32<T>(0.0f);
-    for (int64_t r = blockIdx.x; r < end; r += gridDim.x) {
-        const T* x = r < count ? static_cast<const T*>(a.x) + (int64_t)a.map[r] * a.x_stride : nullptr;
-        T* to = static_cast<T*>(a.to) + r * a.to_stride;
-        for (int64_t i = threadIdx.x; i < a.dim; i += kPackThreads) to[i] = x ? x[i] : zero;
-    }
-    if (!a.dx) return;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        if (a.given[r] != -INFINITY) continue;
-        T* dx = static_cast<T*>(a.dx) + r * a.dx_stride;
-        for (int64_t i = threadIdx.x; i < a.dim; i += kPackThreads) dx[i] = zero;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        if (given[r] != -INFINITY) continue;
+        for (int64_t i = threadIdx.x; i < dim; i += kZeroThreads) dx[r * stride + i] = from_f32<T>(0.0f);
     }
 }
 
@@ -285,8 +272,8 @@ unsigned blocks_of(int64_t n, int64_t each, int64_t most)
     return (unsigned)(b < 1 ? 1 : b < most ? b : most);
 }
 
-// The lists, the rows that have a loss, and their copies.
-template <typename T> cudaError_t vocab_rows(const VocabArgs& a, const VocabParts& p, cudaStream_t stream)
+// The lists, the rows that have a loss, and the operands.
+template <typename T> cudaError_t vocab_rows(const VocabArgs& a, const VocabParts& p, Matrix* x, Matrix* w, cudaStream_t stream)
 {
     ListArgs l = {};
     l.target = a.target;
@@ -311,26 +298,16 @@ template <typename T> cudaError_t vocab_rows(const VocabArgs& a, const VocabPart
     if (e != cudaSuccess) return e;
     e = launch_after(vocab_rows_kernel, dim3(1), dim3(kScanThreads), 0, stream, (const float*)p.given, a.rows, p.map, p.count);
     if (e != cudaSuccess) return e;
-    GatherArgs g = {};
-    g.x = a.x;
-    g.to = p.x;
-    g.dx = a.dx;
-    g.given = p.given;
-    g.map = p.map;
-    g.count = p.count;
-    g.rows = a.rows;
-    g.dim = a.dim;
-    g.x_stride = a.x_stride;
-    g.to_stride = p.x_stride;
-    g.dx_stride = a.dx_stride;
-    return launch_after(vocab_gather_kernel<T>, dim3(blocks_of(a.rows, 1, 4096)), dim3(kPackThreads), 0, stream, g);
+    e = take_matrix<T>(x, a.x, a.x_stride, a.rows, a.dim, p.x, stream, p.map, p.count, p.padded);
+    return e == cudaSuccess ? take_matrix<T>(w, a.w, a.w_stride, a.vocab, a.dim, p.w, stream) : e;
 }
 
 template <typename T> cudaError_t vocab_forward(const VocabArgs& a, void* ws, cudaStream_t stream)
 {
     Carve carve{static_cast<char*>(ws)};
-    const VocabParts p = vocab_parts(carve, a.rows, a.dim, a.vocab, sizeof(T) == 2 ? ADACOMP_BF16 : ADACOMP_F32, a.k, false);
-    cudaError_t e = vocab_rows<T>(a, p, stream);
+    const VocabParts p = vocab_parts(carve, a.rows, a.dim, a.vocab, sizeof(T), a.k, false);
+    Matrix x, w;
+    cudaError_t e = vocab_rows<T>(a, p, &x, &w, stream);
     if (e != cudaSuccess) return e;
     EpiSoftmax<T> epi = {};
     epi.part = p.part;
@@ -339,15 +316,12 @@ template <typename T> cudaError_t vocab_forward(const VocabArgs& a, void* ws, cu
     epi.n = a.vocab;
     epi.rows = a.rows;
     epi.scale = 1.0f / a.temperature;
-    SimpleArgs g = {};
-    g.a = {p.x, p.x_stride, 1};
-    g.b = {a.w, a.w_stride, 1};
+    TcArgs g = {};
     g.m = a.rows;
     g.n = a.vocab;
     g.k = a.dim;
     g.m_count = p.count;
-    g.strip = kStrip;
-    e = product_simple<T>(g, epi, stream);
+    e = product_tc<T>(x, false, w, false, g, nullptr, epi, stream);
     if (e != cudaSuccess) return e;
     JoinArgs j = {};
     j.part = p.part;
@@ -368,64 +342,63 @@ template <typename T> cudaError_t vocab_forward(const VocabArgs& a, void* ws, cu
 template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, cudaStream_t stream)
 {
     Carve carve{static_cast<char*>(ws)};
-    const VocabParts p = vocab_parts(carve, a.rows, a.dim, a.vocab, sizeof(T) == 2 ? ADACOMP_BF16 : ADACOMP_F32, a.k, true);
-    cudaError_t e = vocab_rows<T>(a, p, stream);
+    const VocabParts p = vocab_parts(carve, a.rows, a.dim, a.vocab, sizeof(T), a.k, true);
+    Matrix x, w;
+    cudaError_t e = vocab_rows<T>(a, p, &x, &w, stream);
+    if (a.dx && e == cudaSuccess)
+        e = launch_after(vocab_zero_kernel<T>, dim3(blocks_of(a.rows, 1, 4096)), dim3(kZeroThreads), 0, stream, static_cast<T*>(a.dx),
+                         a.dx_stride, (const float*)p.given, a.rows, a.dim);
     EpiGradient<T> grad = {};
-    grad.dz = static_cast<T*>(p.dz);
+    grad.dz = p.dz;
     grad.lists = {p.index, p.q, p.map, a.k};
     grad.lse = a.lse;
     grad.dloss = a.dloss;
     grad.given = p.given;
     grad.stride = p.dz_stride;
+    grad.plane = p.padded * p.dz_stride;
+    grad.rows = p.padded;
     grad.dloss_stride = a.dloss_stride;
     grad.scale = 1.0f / a.temperature;
     grad.temperature = a.temperature;
-    EpiStore<T> store = {};
-    store.n = a.dim;
     for (int64_t at = 0; at < a.vocab && e == cudaSuccess; at += p.piece) {
         const int64_t n = a.vocab - at < p.piece ? a.vocab - at : p.piece;
-        const T* w = static_cast<const T*>(a.w) + at * a.w_stride;
+        const Matrix here = {w.p + at * w.stride, n, a.dim, w.stride, w.plane}, dz = {p.dz, p.padded, n, p.dz_stride, grad.plane};
         grad.n = n;
         grad.first = at;
-        SimpleArgs g = {};
-        g.a = {p.x, p.x_stride, 1};
-        g.b = {w, a.w_stride, 1};
+        TcArgs g = {};
         g.m = a.rows;
         g.n = n;
         g.k = a.dim;
         g.m_count = p.count;
-        g.strip = kCols;
-        e = product_simple<T>(g, grad, stream);
+        e = product_tc<T>(x, false, here, false, g, nullptr, grad, stream);
         if (a.dx && e == cudaSuccess) {
+            EpiStore<T> store = {};
             store.out = static_cast<T*>(a.dx);
             store.acc = p.acc;
             store.map = p.map;
             store.stride = a.dx_stride;
             store.acc_stride = round_up(a.dim, 4);
+            store.n = a.dim;
             store.first = at == 0;
             store.last = at + n == a.vocab;
             store.whole = whole_rows(a.dx, a.dx_stride, a.rows, sizeof(T));
-            g.a = {p.dz, p.dz_stride, 1};
-            g.b = {w, 1, a.w_stride};
             g.n = a.dim;
             g.k = n;
-            e = product_simple<T>(g, store, stream);
+            e = product_tc<T>(dz, false, here, true, g, p.parts, store, stream);
         }
         if (a.dw && e == cudaSuccess) {
+            EpiStore<T> store = {};
             store.out = static_cast<T*>(a.dw) + at * a.dw_stride;
-            store.map = nullptr;
             store.stride = a.dw_stride;
+            store.n = a.dim;
             store.first = store.last = true;
             store.whole = whole_rows(a.dw, a.dw_stride, a.vocab, sizeof(T));
             g = {};
-            g.a = {p.dz, 1, p.dz_stride};
-            g.b = {p.x, 1, p.x_stride};
             g.m = n;
             g.n = a.dim;
             g.k = a.rows;
             g.k_count = p.count;
-            g.strip = kCols;
-            e = product_simple<T>(g, store, stream);
+            e = product_tc<T>(dz, true, x, true, g, p.parts, store, stream);
         }
     }
     return e;
@@ -440,11 +413,7 @@ template <typename T> cudaError_t zero_rows(const VocabArgs& a, cudaStream_t str
     store.n = a.dim;
     store.first = store.last = true;
     store.whole = whole_rows(a.dw, a.dw_stride, a.vocab, sizeof(T));
-    SimpleArgs g = {};
-    g.m = a.vocab;
-    g.n = a.dim;
-    g.strip = kCols;
-    return product_simple<T>(g, store, stream);  // a product of no terms
+    return product_none<T>(a.vocab, a.dim, store, stream);
 }
 
 constexpr int64_t kMostDim = (int64_t)1 << 30, kMostRows = (int64_t)1 << 31;
@@ -482,7 +451,7 @@ adacomp_status vocab_pass(adacomp_vocab_t h, VocabArgs& a, bool backward, void* 
         if (!a.loss || !a.lse_out) return ADACOMP_ERR_INVALID_ARG;
     }
     Carve need;
-    vocab_parts(need, a.rows, a.dim, a.vocab, h->dtype, a.k, backward);
+    vocab_parts(need, a.rows, a.dim, a.vocab, dtype_bytes(h->dtype), a.k, backward);
     if (ws_bytes < need.at) return ADACOMP_ERR_WORKSPACE;
     const cudaError_t e = backward ? (narrow ? vocab_backward<bf16>(a, ws, stream) : vocab_backward<float>(a, ws, stream))
                                    : (narrow ? vocab_forward<bf16>(a, ws, stream) : vocab_forward<float>(a, ws, stream));
@@ -493,7 +462,7 @@ size_t vocab_bytes(adacomp_vocab_t h, int64_t rows, int32_t k, bool backward)
 {
     if (!h || rows < 0 || rows >= kMostRows || k < 1 || k > ADACOMP_MAX_TEACHER) return 0;
     Carve c;
-    vocab_parts(c, rows, h->dim, h->vocab, h->dtype, k, backward);
+    vocab_parts(c, rows, h->dim, h->vocab, dtype_bytes(h->dtype), k, backward);
     return c.at;
 }
 
