@@ -12,8 +12,9 @@ struct adacomp_linear {
 namespace adacomp {
 namespace {
 
-constexpr int kDzThreads = 128;
-constexpr int kDzSlices = 152;  // partial sums of db: one per slice of the rows
+constexpr int kDzCols = 256, kDzRows = 8;  // of a CTA: a warp has 256 columns of a row
+constexpr int kDzSlices = 152;             // partial sums of db: one per slice of the rows
+constexpr int kDbCols = 32, kDbRows = 16;
 
 struct LinearArgs {
     int64_t rows, in, out;
@@ -51,43 +52,73 @@ struct DzArgs {
     float* sums;
     int64_t rows, n, dy_stride, pre_stride, dz_stride, dz_plane;
     int32_t act, slices;
+    bool dy_whole, pre_whole;
 };
 
-// dz = dy * act'(pre), and its sums over slices of the rows. A thread has a column.
-template <typename T> __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a)
+// dz = dy * act'(pre), and its sums over slices of the rows. Bound by memory: a thread has eight columns of every
+// kDzRows-th row of a slice, four rows under way at a time; the CTA's sums meet in shared memory, the slices' in a
+// second kernel, in a fixed order.
+template <typename T, int kAct> __device__ __forceinline__ void dz_rows(const DzArgs& a, int32_t c, float (&sum)[8])
 {
-    ptx::griddep_wait();
-    const int64_t c = (int64_t)blockIdx.x * kDzThreads + threadIdx.x;
-    if (c >= a.n) return;
-    float sum = 0.0f;
-    for (int64_t r = blockIdx.y; r < a.rows; r += a.slices) {
-        float v = to_f32(static_cast<const T*>(a.dy)[r * a.dy_stride + c]);
-        if (a.act != ADACOMP_ACT_NONE) {
-            v *= slope(to_f32(static_cast<const T*>(a.pre)[r * a.pre_stride + c]), a.act);
-            if (a.dz) {
-                bf16* dz = a.dz + r * a.dz_stride + c;
-                if constexpr (sizeof(T) == 4) {
-                    bf16 part[kPlanes];
-                    split_parts(v, part);
+    const T *dy = static_cast<const T*>(a.dy) + c, *pre = static_cast<const T*>(a.pre) + c;
+    const int64_t left = a.n - c, step = (int64_t)a.slices * kDzRows;
+#pragma unroll 4
+    for (int64_t r = blockIdx.y * kDzRows + threadIdx.y; r < a.rows; r += step) {
+        float v[8];
+        get_chunk(dy + r * a.dy_stride, v, left, a.dy_whole);
+        if constexpr (kAct != ADACOMP_ACT_NONE) {
+            float z[8];
+            get_chunk(pre + r * a.pre_stride, z, left, a.pre_whole);
 #pragma unroll
-                    for (int p = 0; p < kPlanes; ++p) dz[p * a.dz_plane] = part[p];
-                } else {
-                    *dz = from_f32<bf16>(v);
-                }
-            }
+            for (int j = 0; j < 8; ++j) v[j] *= slope<T, kAct>(z[j]);
+            if (a.dz) put_parts<T>(a.dz + r * a.dz_stride + c, a.dz_plane, v, left);
         }
-        sum += v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += v[j];
     }
-    a.sums[(int64_t)blockIdx.y * a.n + c] = sum;
 }
 
-template <typename T> __global__ void __launch_bounds__(kDzThreads) linear_db_kernel(const float* sums, T* db, int64_t n, int32_t slices)
+template <typename T> __global__ void __launch_bounds__(kDzCols / 8 * kDzRows) linear_dz_kernel(const DzArgs a)
 {
+    __shared__ float sums[kDzRows][kDzCols];
     ptx::griddep_wait();
-    const int64_t c = (int64_t)blockIdx.x * kDzThreads + threadIdx.x;
-    if (c >= n) return;
+    const int32_t c = blockIdx.x * kDzCols + threadIdx.x * 8;
+    float sum[8] = {};
+    if (c < a.n) switch (a.act) {
+        case ADACOMP_ACT_RELU: dz_rows<T, ADACOMP_ACT_RELU>(a, c, sum); break;
+        case ADACOMP_ACT_GELU: dz_rows<T, ADACOMP_ACT_GELU>(a, c, sum); break;
+        case ADACOMP_ACT_GELU_TANH: dz_rows<T, ADACOMP_ACT_GELU_TANH>(a, c, sum); break;
+        case ADACOMP_ACT_SILU: dz_rows<T, ADACOMP_ACT_SILU>(a, c, sum); break;
+        default: dz_rows<T, ADACOMP_ACT_NONE>(a, c, sum);
+        }
+    if (!a.sums) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[threadIdx.y][threadIdx.x * 8 + j] = sum[j];
+    __syncthreads();
+    const int i = threadIdx.y * (kDzCols / 8) + threadIdx.x;
+    const int64_t at = (int64_t)blockIdx.x * kDzCols + i;
+    if (i >= kDzCols || at >= a.n) return;
     float s = 0.0f;
-    for (int i = 0; i < slices; ++i) s += sums[(int64_t)i * n + c];
+#pragma unroll
+    for (int j = 0; j < kDzRows; ++j) s += sums[j][i];
+    a.sums[blockIdx.y * a.n + at] = s;
+}
+
+template <typename T> __global__ void __launch_bounds__(kDbCols * kDbRows) linear_db_kernel(const float* part, T* db, int64_t n, int32_t slices)
+{
+    __shared__ float sums[kDbRows][kDbCols];
+    ptx::griddep_wait();
+    const int64_t c = (int64_t)blockIdx.x * kDbCols + threadIdx.x;
+    float s = 0.0f;
+    if (c < n)
+#pragma unroll 4
+        for (int i = threadIdx.y; i < slices; i += kDbRows) s += part[i * n + c];
+    sums[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y || c >= n) return;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kDbRows; ++i) s += sums[i][threadIdx.x];
     db[c] = from_f32<T>(s);
 }
 
@@ -101,7 +132,7 @@ template <typename T> cudaError_t linear_forward(const LinearArgs& a, void* ws, 
     epi.y_stride = a.y_stride;
     epi.pre_stride = a.pre_stride;
     epi.residual_stride = a.residual_stride;
-    epi.n = a.out;
+    epi.n = (int32_t)a.out;
     epi.act = a.act;
     epi.y_whole = whole_rows(a.y, a.y_stride, a.rows, sizeof(T));
     epi.pre_whole = whole_rows(a.pre, a.pre_stride, a.rows, sizeof(T));
@@ -132,7 +163,7 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
         d.dy = a.dy;
         d.pre = a.pre_in;
         d.dz = products ? p.dz : nullptr;
-        d.sums = p.sums;
+        d.sums = a.db ? p.sums : nullptr;
         d.rows = a.rows;
         d.n = a.out;
         d.dy_stride = a.dy_stride;
@@ -140,11 +171,18 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
         d.dz_stride = dz.stride;
         d.dz_plane = dz.plane;
         d.act = a.act;
-        d.slices = (int32_t)(a.rows < kDzSlices ? a.rows : kDzSlices);
-        const unsigned blocks = (unsigned)((a.out + kDzThreads - 1) / kDzThreads);
-        if (d.slices) e = launch_after(linear_dz_kernel<T>, dim3(blocks, d.slices), dim3(kDzThreads), 0, stream, d);
+        d.dy_whole = whole_rows(a.dy, a.dy_stride, a.rows, sizeof(T));
+        d.pre_whole = whole_rows(a.pre_in, a.pre_in_stride, a.rows, sizeof(T));
+        // CTAs for eight on each SM, of no fewer than two rows a thread
+        const int64_t blocks = (a.out + kDzCols - 1) / kDzCols, most = (a.rows + 2 * kDzRows - 1) / (2 * kDzRows);
+        int64_t slices = 8 * kDzSlices / blocks;
+        slices = slices < 1 ? 1 : slices < kDzSlices ? slices : kDzSlices;
+        d.slices = (int32_t)(slices < most ? slices : most);
+        if (d.slices)
+            e = launch_after(linear_dz_kernel<T>, dim3((unsigned)blocks, d.slices), dim3(kDzCols / 8, kDzRows), 0, stream, d);
         if (e == cudaSuccess && a.db)
-            e = launch_after(linear_db_kernel<T>, dim3(blocks), dim3(kDzThreads), 0, stream, (const float*)p.sums, static_cast<T*>(a.db), a.out, d.slices);
+            e = launch_after(linear_db_kernel<T>, dim3((unsigned)((a.out + kDbCols - 1) / kDbCols)), dim3(kDbCols, kDbRows), 0, stream,
+                             (const float*)p.sums, static_cast<T*>(a.db), a.out, d.slices);
     }
     if (e == cudaSuccess && !act && products) e = take_matrix<T>(&dz, a.dy, a.dy_stride, a.rows, a.out, p.dz, stream);
     TcArgs g = {};
@@ -154,7 +192,8 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
         e = take_matrix<T>(&w, a.w, a.w_stride, a.out, a.in, p.w, stream);
         if (e != cudaSuccess) return e;
         g.m = a.rows;
-        g.n = epi.n = a.in;
+        g.n = a.in;
+        epi.n = (int32_t)a.in;
         g.k = a.out;
         epi.out = static_cast<T*>(a.dx);
         epi.stride = a.dx_stride;
@@ -163,7 +202,8 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
     }
     if (a.dw && e == cudaSuccess) {
         g.m = a.out;
-        g.n = epi.n = a.in;
+        g.n = a.in;
+        epi.n = (int32_t)a.in;
         g.k = a.rows;
         epi.out = static_cast<T*>(a.dw);
         epi.stride = a.dw_stride;
@@ -175,7 +215,7 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
     return e;
 }
 
-constexpr int64_t kMostDim = (int64_t)1 << 30, kMostRows = (int64_t)1 << 31;
+constexpr int64_t kMostDim = (int64_t)1 << 30, kMostRows = ((int64_t)1 << 30) + 1;
 
 }  // namespace
 }  // namespace adacomp

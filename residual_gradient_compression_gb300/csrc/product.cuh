@@ -1,10 +1,13 @@
 // Shared by the linear layers and the losses over a vocabulary: what is done with a product's
-// sums (the epilogues), a product for operands of any layout, and rows that are copied together.
+// sums (the epilogues).
 //
-// A product is C(m, n) = sum over k of A(m, k) B(n, k). Whichever kernel forms it hands an epilogue
-// the sums of one row, 32 columns at a time and in ascending order within a strip, in one thread's
-// registers: begin(row), chunk(columns) for the strip's columns, end(strip). kZeros: rows past the last one, up to
-// a tile's end, are set to zeros.
+// A product is C(m, n) = sum over k of A(m, k) B(n, k). A warp of the kernel that forms it has 32 rows' sums in registers,
+// 128 columns of a row per thread, and hands them to an epilogue in two steps: rows(), a thread its row, with
+// what begin() loaded before the sums were there; and chunk(), the warp 32 columns at a time through shared memory, so that
+// what it reads and writes in global memory are whole pieces of rows (a thread that writes its own row takes 32 cache
+// lines at a time: a linear layer's forward product of 8192 x 2048 x 16384 bf16 took 369 us so, and 313 without its
+// stores). kExact: the results are held in fp32, so the sums are formed in short runs.
+// kPieces: a thread may also hand over four columns on their own, piece().
 #pragma once
 
 #include "train_common.cuh"
@@ -25,25 +28,24 @@ struct Carve {
 
 namespace {
 
-constexpr int kCols = 32;    // columns of a chunk
-constexpr int kStrip = 128;  // of a strip: what a softmax's partial sums are kept for
+constexpr int kStrip = 128;  // columns of a row that a thread has; a softmax's partial sums are kept for each
 constexpr int kRows = 128;   // rows of a tile
 
 inline int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// ---------------------------------------------------------------- rows of 32 columns
-template <typename T> __device__ __forceinline__ void put_chunk(T* p, const float (&v)[kCols], int64_t left, bool whole)
+// ---------------------------------------------------------------- a row's columns, eight or a multiple of them
+template <typename T, int N> __device__ __forceinline__ void put_chunk(T* p, const float (&v)[N], int64_t left, bool whole)
 {
-    if (whole && left >= kCols) {
+    if (whole && left >= N) {
         uint4* q = reinterpret_cast<uint4*>(p);
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < kCols; i += 4)
+            for (int i = 0; i < N; i += 4)
                 q[i / 4] = make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
                                       __float_as_uint(v[i + 3]));
         } else {
 #pragma unroll
-            for (int i = 0; i < kCols; i += 8) {
+            for (int i = 0; i < N; i += 8) {
                 uint32_t w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -56,16 +58,16 @@ template <typename T> __device__ __forceinline__ void put_chunk(T* p, const floa
         return;
     }
 #pragma unroll
-    for (int i = 0; i < kCols; ++i)
+    for (int i = 0; i < N; ++i)
         if (i < left) p[i] = from_f32<T>(v[i]);
 }
 
-template <typename T> __device__ __forceinline__ void get_chunk(const T* p, float (&v)[kCols], int64_t left, bool whole)
+template <typename T, int N> __device__ __forceinline__ void get_chunk(const T* p, float (&v)[N], int64_t left, bool whole)
 {
-    if (whole && left >= kCols) {
+    if (whole && left >= N) {
         const uint4* q = reinterpret_cast<const uint4*>(p);
 #pragma unroll
-        for (int i = 0; i < kCols * (int)sizeof(T) / 16; ++i) {
+        for (int i = 0; i < N * (int)sizeof(T) / 16; ++i) {
             const uint4 u = q[i];
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -81,8 +83,53 @@ template <typename T> __device__ __forceinline__ void get_chunk(const T* p, floa
         return;
     }
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) v[i] = i < left ? to_f32(p[i]) : 0.0f;
+    for (int i = 0; i < N; ++i) v[i] = i < left ? to_f32(p[i]) : 0.0f;
 }
+
+// Four columns of a row.
+template <typename T> __device__ __forceinline__ void put4(T* p, const float4& v, int64_t left, bool whole)
+{
+    if (whole && left >= 4) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(p) = v;
+        } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+        return;
+    }
+    if (left > 0) p[0] = from_f32<T>(v.x);
+    if (left > 1) p[1] = from_f32<T>(v.y);
+    if (left > 2) p[2] = from_f32<T>(v.z);
+    if (left > 3) p[3] = from_f32<T>(v.w);
+}
+
+template <typename T> __device__ __forceinline__ float4 get4(const T* p, int64_t left, bool whole)
+{
+    if (whole && left >= 4) {
+        if constexpr (sizeof(T) == 4) {
+            return *reinterpret_cast<const float4*>(p);
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(p);
+            return make_float4(bf16_low(w.x), bf16_high(w.x), bf16_low(w.y), bf16_high(w.y));
+        }
+    }
+    return make_float4(left > 0 ? to_f32(p[0]) : 0.0f, left > 1 ? to_f32(p[1]) : 0.0f, left > 2 ? to_f32(p[2]) : 0.0f,
+                       left > 3 ? to_f32(p[3]) : 0.0f);
+}
+
+__device__ __forceinline__ float4 operator+(const float4& a, const float4& b)
+{
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+// A warp's 32 rows of 32 columns in shared memory; a row's 16-byte pieces lie where no two rows of eight share banks.
+struct Stage {
+    float4* p;
+    __device__ __forceinline__ float4& at(int row, int piece) const { return p[row * 8 + (piece ^ (row & 7))]; }
+};
+
+constexpr int kTurns = 8;  // a chunk in turns of four rows, of which a lane has four columns
 
 inline bool whole_rows(const void* p, int64_t stride, int64_t rows, int bytes)
 {
@@ -108,123 +155,219 @@ __device__ __forceinline__ void split_parts(float x, bf16 (&part)[kPlanes])
 }
 
 // A row's columns as operands of another product: bf16 numbers, or, of an fp32 matrix, planes of them.
-template <typename T> __device__ __forceinline__ void put_parts(bf16* p, int64_t plane, const float (&v)[kCols], int64_t left)
+template <typename T, int N> __device__ __forceinline__ void put_parts(bf16* p, int64_t plane, const float (&v)[N], int64_t left)
 {
     if constexpr (sizeof(T) == 2) {
         put_chunk(p, v, left, true);
     } else {
-        float part[kPlanes][kCols];
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) {
-            bf16 each[kPlanes];
-            split_parts(v[i], each);
+        for (int i = 0; i < N; i += 8) {
+            float part[kPlanes][8];
 #pragma unroll
-            for (int j = 0; j < kPlanes; ++j) part[j][i] = __bfloat162float(each[j]);
+            for (int c = 0; c < 8; ++c) {
+                bf16 each[kPlanes];
+                split_parts(v[i + c], each);
+#pragma unroll
+                for (int j = 0; j < kPlanes; ++j) part[j][c] = __bfloat162float(each[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < kPlanes; ++j) put_chunk(p + j * plane + i, part[j], left - i, true);
         }
-#pragma unroll
-        for (int j = 0; j < kPlanes; ++j) put_chunk(p + j * plane, part[j], left, true);
     }
 }
 
 // ---------------------------------------------------------------- activations
-__device__ __forceinline__ float activate(float z, int kind)
+// Of bf16 layers by quick functions, whose error is some 2^-22 of z, far below the results' rounding: the epilogue of a
+// product of 2048 terms has no time for more. 1 + erf(x), and exp(-x^2), by the rational approximation of Abramowitz and
+// Stegun (7.1.26; error 1.5e-7).
+__device__ __forceinline__ float quick_erfc_minus(float x, float& bell)
 {
-    switch (kind) {
-    case ADACOMP_ACT_RELU: return z < 0.0f ? 0.0f : z;
-    case ADACOMP_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case ADACOMP_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
-    case ADACOMP_ACT_SILU: return z / (1.0f + expf(-z));
-    default: return z;
+    const float a = fabsf(x), t = __fdividef(1.0f, fmaf(0.3275911f, a, 1.0f));
+    bell = __expf(-x * x);
+    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+    const float tail = p * bell;  // erfc(|x|)
+    return x < 0.0f ? tail : 2.0f - tail;
+}
+
+__device__ __forceinline__ float quick_sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+template <typename T, int kKind> __device__ __forceinline__ float activate(float z)
+{
+    constexpr bool kQuick = sizeof(T) == 2;
+    if constexpr (kKind == ADACOMP_ACT_RELU) {
+        return z < 0.0f ? 0.0f : z;
+    } else if constexpr (kKind == ADACOMP_ACT_GELU) {
+        float bell;
+        if (kQuick) return 0.5f * z * quick_erfc_minus(z * 0.70710678f, bell);
+        return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    } else if constexpr (kKind == ADACOMP_ACT_GELU_TANH) {  // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
+        const float u = 0.79788456f * (z + 0.044715f * z * z * z);
+        if (kQuick) return z * quick_sigmoid(2.0f * u);
+        return 0.5f * z * (1.0f + tanhf(u));
+    } else if constexpr (kKind == ADACOMP_ACT_SILU) {
+        if (kQuick) return z * quick_sigmoid(z);
+        return z / (1.0f + expf(-z));
+    } else {
+        return z;
     }
 }
 
-__device__ __forceinline__ float slope(float z, int kind)
+template <typename T, int kKind> __device__ __forceinline__ float slope(float z)
 {
-    switch (kind) {
-    case ADACOMP_ACT_RELU: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;  // NaN stays NaN
-    case ADACOMP_ACT_GELU:
+    constexpr bool kQuick = sizeof(T) == 2;
+    if constexpr (kKind == ADACOMP_ACT_RELU) {
+        return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;  // NaN stays NaN
+    } else if constexpr (kKind == ADACOMP_ACT_GELU) {
+        if (kQuick) {
+            float bell;
+            const float c = 0.5f * quick_erfc_minus(z * 0.70710678f, bell);
+            return fmaf(z * 0.39894228f, bell, c);
+        }
         return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * expf(-0.5f * z * z) * 0.39894228f;
-    case ADACOMP_ACT_GELU_TANH: {
-        const float t = tanhf(0.79788456f * (z + 0.044715f * z * z * z));
+    } else if constexpr (kKind == ADACOMP_ACT_GELU_TANH) {
+        const float u = 0.79788456f * (z + 0.044715f * z * z * z);
+        const float t = kQuick ? fmaf(2.0f, quick_sigmoid(2.0f * u), -1.0f) : tanhf(u);
         return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456f * (1.0f + 0.134145f * z * z);
-    }
-    case ADACOMP_ACT_SILU: {
-        const float g = 1.0f / (1.0f + expf(-z));
+    } else if constexpr (kKind == ADACOMP_ACT_SILU) {
+        const float g = kQuick ? quick_sigmoid(z) : 1.0f / (1.0f + expf(-z));
         return g * (1.0f + z * (1.0f - g));
-    }
-    default: return 1.0f;
+    } else {
+        return 1.0f;
     }
 }
 
 // ---------------------------------------------------------------- epilogues
 // y = act(sum + bias) + residual, and the value before the activation.
 template <typename T> struct EpiLinear {
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true;
     T *y, *pre;
     const T *bias, *residual;
-    int64_t y_stride, pre_stride, residual_stride, n;
-    int32_t act;
+    int64_t y_stride, pre_stride, residual_stride;
+    int32_t n, act;
     bool y_whole, pre_whole, bias_whole, residual_whole;
-    static constexpr bool kZeros = false;
     struct State {};
-    __device__ __forceinline__ void begin(State&, int64_t, int64_t, int) const {}
-    __device__ __forceinline__ void chunk(State&, int64_t r, int64_t c, float (&v)[kCols]) const
+    __device__ __forceinline__ State begin(int32_t, int32_t) const { return {}; }
+    __device__ __forceinline__ void rows(const State&, int32_t, int32_t, bool, float (&)[kStrip]) const {}
+
+    template <typename F> __device__ __forceinline__ void turns(const Stage& stage, int32_t r0, int32_t end, int32_t c0, F f) const
     {
-        if (c >= n) return;
-        const int64_t left = n - c;
-        if (bias) {
-            float b[kCols];
-            get_chunk(bias + c, b, left, bias_whole);
+        const int lane = threadIdx.x & 31, piece = lane & 7, first = lane / 8;
+        const int32_t c = c0 + piece * 4, left = n - c;
+        const float4 b = bias ? get4(bias + c, left, bias_whole) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (pre) {
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) v[i] += b[i];
+            for (int i = 0; i < kTurns; ++i) {
+                const int32_t r = r0 + i * 4 + first;
+                if (r < end) put4(pre + r * pre_stride + c, stage.at(i * 4 + first, piece) + b, left, pre_whole);
+            }
         }
-        if (pre) put_chunk(pre + r * pre_stride + c, v, left, pre_whole);
-        if (act != ADACOMP_ACT_NONE) {
+        if (!residual) {
+#pragma unroll 2
+            for (int i = 0; i < kTurns; ++i) {
+                const int32_t r = r0 + i * 4 + first;
+                if (r < end) put4(y + r * y_stride + c, f(stage.at(i * 4 + first, piece) + b), left, y_whole);
+            }
+            return;
+        }
+#pragma unroll 2
+        for (int i = 0; i < kTurns; ++i) {
+            float4& v = stage.at(i * 4 + first, piece);
+            v = f(v + b);
+        }
+        float4 more[kTurns];  // loads that wait together
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) v[i] = activate(v[i], act);
+        for (int i = 0; i < kTurns; ++i) {
+            const int32_t r = r0 + i * 4 + first;
+            more[i] = get4(residual + r * residual_stride + c, r < end ? left : 0, residual_whole);
         }
-        if (residual) {
-            float b[kCols];
-            get_chunk(residual + r * residual_stride + c, b, left, residual_whole);
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) v[i] += b[i];
+        for (int i = 0; i < kTurns; ++i) {
+            const int32_t r = r0 + i * 4 + first;
+            if (r < end) put4(y + r * y_stride + c, stage.at(i * 4 + first, piece) + more[i], left, y_whole);
         }
-        put_chunk(y + r * y_stride + c, v, left, y_whole);
     }
-    __device__ __forceinline__ void end(State&, int64_t, int64_t) const {}
-    __device__ __forceinline__ void zeros(int64_t, int64_t) const {}
+
+    template <int kKind> static __device__ __forceinline__ float4 each(const float4& v)
+    {
+        return make_float4(activate<T, kKind>(v.x), activate<T, kKind>(v.y), activate<T, kKind>(v.z), activate<T, kKind>(v.w));
+    }
+
+    template <typename G> __device__ __forceinline__ void with_act(G g) const
+    {
+        switch (act) {
+        case ADACOMP_ACT_RELU: g([](const float4& v) { return each<ADACOMP_ACT_RELU>(v); }); break;
+        case ADACOMP_ACT_GELU: g([](const float4& v) { return each<ADACOMP_ACT_GELU>(v); }); break;
+        case ADACOMP_ACT_GELU_TANH: g([](const float4& v) { return each<ADACOMP_ACT_GELU_TANH>(v); }); break;
+        case ADACOMP_ACT_SILU: g([](const float4& v) { return each<ADACOMP_ACT_SILU>(v); }); break;
+        default: g([](const float4& v) { return v; });
+        }
+    }
+
+    __device__ __forceinline__ void chunk(const Stage& stage, int32_t r0, int32_t end, int32_t c) const
+    {
+        with_act([&](auto f) { turns(stage, r0, end, c, f); });
+    }
+
+    // four columns, by a thread on its own
+    __device__ __forceinline__ void piece(int32_t r, int32_t c, float4 v) const
+    {
+        const int32_t left = n - c;
+        if (bias) v = v + get4(bias + c, left, bias_whole);
+        if (pre) put4(pre + r * pre_stride + c, v, left, pre_whole);
+        with_act([&](auto f) { v = f(v); });
+        if (residual) v = v + get4(residual + r * residual_stride + c, left, residual_whole);
+        put4(y + r * y_stride + c, v, left, y_whole);
+    }
 };
 
 // The sums themselves, in rows that `map` may move; with acc, added up over several products in
 // fp32 (first: nothing to add to yet) and rounded by the last one only.
 template <typename T> struct EpiStore {
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true;
     T* out;
     float* acc;
     const int32_t* map;
-    int64_t stride, acc_stride, n, split_stride;  // split_stride: between the parts of a product whose terms are split
+    int64_t stride, acc_stride, split_stride;  // split_stride: between the parts of a product whose terms are split
+    int32_t n;
     bool first, last, whole;
-    static constexpr bool kZeros = false;
-    struct State {
-        T* to;
-    };
-    __device__ __forceinline__ void begin(State& s, int64_t r, int64_t, int split) const
+    struct State {};
+    __device__ __forceinline__ State begin(int32_t, int32_t) const { return {}; }
+    __device__ __forceinline__ void rows(const State&, int32_t, int32_t, bool, float (&)[kStrip]) const {}
+
+    __device__ __forceinline__ EpiStore of_split(int split) const
     {
-        s.to = out + split * split_stride + (map ? map[r] : r) * stride;
+        EpiStore e = *this;
+        e.out += split * split_stride;
+        return e;
     }
-    __device__ __forceinline__ void chunk(State& s, int64_t r, int64_t c, float (&v)[kCols]) const
+
+    __device__ __forceinline__ void chunk(const Stage& stage, int32_t r0, int32_t end, int32_t c0) const
     {
-        if (c >= n) return;
-        const int64_t left = n - c;
-        if (!first) {
-            float b[kCols];
-            get_chunk(acc + r * acc_stride + c, b, left, true);
+        const int lane = threadIdx.x & 31, piece = lane & 7, at = lane / 8;
+        const int32_t c = c0 + piece * 4, left = n - c;
+        float4 v[kTurns];
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) v[i] += b[i];
+        for (int i = 0; i < kTurns; ++i) {
+            const int32_t r = r0 + i * 4 + at;
+            v[i] = stage.at(i * 4 + at, piece);
+            if (!first) v[i] = v[i] + get4(acc + r * acc_stride + c, r < end ? left : 0, true);
         }
-        if (last) put_chunk(s.to + c, v, left, whole);
-        else put_chunk(acc + r * acc_stride + c, v, left, true);
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const int32_t r = r0 + i * 4 + at;
+            if (r >= end) continue;
+            if (last) put4(out + (map ? map[r] : r) * stride + c, v[i], left, whole);
+            else put4(acc + r * acc_stride + c, v[i], left, true);
+        }
     }
-    __device__ __forceinline__ void end(State&, int64_t, int64_t) const {}
-    __device__ __forceinline__ void zeros(int64_t, int64_t) const {}
+
+    __device__ __forceinline__ void piece(int32_t r, int32_t c, float4 v) const
+    {
+        const int32_t left = n - c;
+        if (!first) v = v + get4(acc + r * acc_stride + c, left, true);
+        if (last) put4(out + (map ? map[r] : r) * stride + c, v, left, whole);
+        else put4(acc + r * acc_stride + c, v, left, true);
+    }
 };
 
 // exp of differences from a row's maximum or logarithm: the quick form's error (2 + 1.2 |x| units
@@ -233,6 +376,15 @@ template <typename T> __device__ __forceinline__ float exp_of(float x)
 {
     if constexpr (sizeof(T) == 4) return expf(x);
     else return __expf(x);
+}
+
+// yes ? a : b, by an instruction: of a series of them over an array the compiler makes an index, and so puts the
+// array into local memory.
+__device__ __forceinline__ float select(bool yes, float a, float b)
+{
+    float v;
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tselp.f32 %0, %1, %2, p;\n\t}" : "=f"(v) : "f"(a), "f"(b), "r"((uint32_t)yes));
+    return v;
 }
 
 // What each row is compared with: k tokens in ascending order (those past the list's end are
@@ -244,204 +396,134 @@ struct Lists {
     int32_t k;
 };
 
-// A row's first place in its list that is not before column c.
-__device__ __forceinline__ int first_place(const int32_t* index, int k, int64_t c)
+// Where a row's list begins, its first place that is not before column c, and the token there.
+struct Place {
+    int64_t list;
+    int32_t at, token;
+};
+
+__device__ __forceinline__ Place place_of(const Lists& l, int64_t row, int32_t c)
 {
-    int lo = 0, hi = k;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (index[mid] < c) lo = mid + 1;
+    Place p = {row * l.k, 0, INT32_MAX};
+    const int32_t* index = l.index + p.list;
+    for (int hi = l.k; p.at < hi;) {
+        const int mid = (p.at + hi) / 2;
+        if (index[mid] < c) p.at = mid + 1;
         else hi = mid;
     }
-    return lo;
+    if (p.at < l.k) p.token = index[p.at];
+    return p;
 }
 
-// Of each strip of 128 logits of a row: their maximum and the sum of exp(z - maximum), in one pass
-// over the sums as they come; and the logits of the listed tokens.
+__device__ __forceinline__ int32_t next_token(const Lists& l, const Place& p, int32_t at)
+{
+    return at < l.k ? l.index[p.list + at] : INT32_MAX;
+}
+
+// Of each strip of 128 logits of a row: their maximum and the sum of exp(z - maximum); and the logits
+// of the listed tokens.
 template <typename T> struct EpiSoftmax {
-    float2* part;  // [strips][rows]
+    static constexpr bool kExact = true, kChunks = false, kPieces = false;
+    float2* part;  // [strips][row_stride]
     float* picked;
     Lists lists;
-    int64_t n, rows;
+    int64_t row_stride;
+    int32_t n;
     float scale;  // of the logits: 1 / temperature
-    static constexpr bool kZeros = false;
-    struct State {
-        float top, sum;
-        const int32_t* index;
-        float* picked;
-        int at, next;
-    };
-    __device__ __forceinline__ void begin(State& s, int64_t r, int64_t c, int) const
+    using State = Place;
+    __device__ __forceinline__ State begin(int32_t r, int32_t c) const { return place_of(lists, lists.map[r], c); }
+    __device__ __forceinline__ void rows(const State& s, int32_t r, int32_t c, bool live, float (&v)[kStrip]) const
     {
-        const int64_t row = lists.map[r];
-        s.top = -INFINITY;
-        s.sum = 0.0f;
-        s.index = lists.index + row * lists.k;
-        s.picked = picked + row * lists.k;
-        s.at = first_place(s.index, lists.k, c);
-        s.next = s.at < lists.k ? s.index[s.at] : INT32_MAX;
-    }
-    __device__ __forceinline__ void chunk(State& s, int64_t, int64_t c, float (&v)[kCols]) const
-    {
-        if (c >= n) return;
+        if (!live) return;
+        const int32_t end = n - c < kStrip ? n : c + kStrip;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) v[i] *= scale;
-        while (s.next < c + kCols && s.next < n) {
+        for (int i = 0; i < kStrip; ++i) v[i] *= scale;
+        for (int32_t at = s.at, token = s.token; token < end; token = next_token(lists, s, ++at)) {
             float z = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) z = s.next == c + i ? v[i] : z;
-            s.picked[s.at] = z;
-            s.next = ++s.at < lists.k ? s.index[s.at] : INT32_MAX;
+            for (int i = 0; i < kStrip; ++i) z = select(token - c == i, v[i], z);
+            picked[s.list + at] = z;
         }
-        if (n - c < kCols) {
+        if (end < c + kStrip) {
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) v[i] = i < n - c ? v[i] : -INFINITY;
+            for (int i = 0; i < kStrip; ++i) v[i] = i < end - c ? v[i] : -INFINITY;
         }
-        float top = s.top;
+        float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) top = fmaxf(top, v[i]);
-        const float from = top == -INFINITY ? 0.0f : top;  // nothing but -inf so far: all terms are 0
-        float sum[4] = {s.sum * exp_of<T>(s.top - from), 0.0f, 0.0f, 0.0f};
+        for (int i = 4; i < kStrip; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
+        top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const float less = top[0] == -INFINITY ? 0.0f : top[0];  // nothing but -inf: all terms are 0
+        float sum[4] = {};
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) sum[i & 3] += exp_of<T>(v[i] - from);
-        s.sum = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        s.top = top;
+        for (int i = 0; i < kStrip; ++i) sum[i & 3] += exp_of<T>(v[i] - less);
+        part[c / kStrip * row_stride + r] = make_float2(top[0], (sum[0] + sum[1]) + (sum[2] + sum[3]));
     }
-    __device__ __forceinline__ void end(State& s, int64_t r, int64_t strip) const
-    {
-        part[strip * rows + r] = make_float2(s.top, s.sum);
-    }
-    __device__ __forceinline__ void zeros(int64_t, int64_t) const {}
+    __device__ __forceinline__ void chunk(const Stage&, int32_t, int32_t, int32_t) const {}
 };
 
 // The logits' gradient (p - q) * dloss * temperature of columns first .. first + n - 1: rounded to
-// bf16, or, of fp32 operands, in parts.
+// bf16, or, of fp32 operands, in parts. Rows past the last one, up to a tile's end, are zeros: they are terms of a product.
 template <typename T> struct EpiGradient {
-    bf16* dz;  // [planes][rows][stride]
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = false;
+    bf16* dz;  // [planes][room][stride]
     Lists lists;
     const float *lse, *dloss, *given;
-    int64_t stride, plane, rows, n, first, dloss_stride;  // rows: that there is room for
+    int64_t stride, plane, dloss_stride;
+    int32_t room, n, first;
     float scale, temperature;
-    static constexpr bool kZeros = true;
     struct State {
+        Place place;
         float lse, factor;
-        const int32_t* index;
-        const float* q;
-        int at;
-        int64_t next;
     };
-    __device__ __forceinline__ void begin(State& s, int64_t r, int64_t c, int) const
+    __device__ __forceinline__ State begin(int32_t r, int32_t c) const
     {
         const int64_t row = lists.map[r];
-        s.lse = lse[row];
-        s.factor = dloss[row * dloss_stride] * temperature;
+        State s = {place_of(lists, row, first + c), lse[row], dloss[row * dloss_stride] * temperature};
         if (given[row] != given[row]) s.factor = given[row];  // a row that has no value
-        s.index = lists.index + row * lists.k;
-        s.q = lists.q + row * lists.k;
-        s.at = first_place(s.index, lists.k, first + c);
-        s.next = s.at < lists.k ? s.index[s.at] - first : INT64_MAX;
+        return s;
     }
-    __device__ __forceinline__ void chunk(State& s, int64_t r, int64_t c, float (&v)[kCols]) const
+    __device__ __forceinline__ void rows(const State& s, int32_t, int32_t c, bool live, float (&v)[kStrip]) const
     {
-        if (c >= n) return;
+        if (!live) {
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) v[i] = exp_of<T>(fmaf(v[i], scale, -s.lse));
-        while (s.next < c + kCols) {
-            const float q = s.q[s.at];
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) v[i] -= s.next == c + i ? q : 0.0f;
-            s.next = ++s.at < lists.k ? s.index[s.at] - first : INT64_MAX;
+            for (int i = 0; i < kStrip; ++i) v[i] = 0.0f;
+            return;
         }
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) v[i] *= s.factor;
-        put_parts<T>(dz + r * stride + c, plane, v, n - c);
+        for (int i = 0; i < kStrip; ++i) v[i] = exp_of<T>(fmaf(v[i], scale, -s.lse));
+        for (int32_t at = s.place.at, token = s.place.token; token < first + c + kStrip; token = next_token(lists, s.place, ++at)) {
+            const float q = lists.q[s.place.list + at];
+#pragma unroll
+            for (int i = 0; i < kStrip; ++i) v[i] -= select(token - first - c == i, q, 0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < kStrip; ++i) v[i] *= s.factor;
     }
-    __device__ __forceinline__ void end(State&, int64_t, int64_t) const {}
-    __device__ __forceinline__ void zeros(int64_t r, int64_t c) const
+    __device__ __forceinline__ void chunk(const Stage& stage, int32_t r0, int32_t, int32_t c0) const
     {
-        if (r >= rows || c >= n) return;
-        float v[kCols] = {};
-        put_parts<T>(dz + r * stride + c, plane, v, n - c);
-    }
-};
-
-// ---------------------------------------------------------------- operands of any layout
-struct Operand {
-    const void* p;
-    int64_t outer, inner;  // strides between rows, and along a row
-};
-
-struct SimpleArgs {
-    Operand a, b;
-    int64_t m, n, k;
-    const int32_t *m_count, *k_count;  // how many of the rows m, or terms k, there are; NULL: all
-    int64_t strip;                     // columns of a CTA's tile: a multiple of kCols
-};
-
-template <typename T, bool kInner>
-__device__ __forceinline__ void simple_load(float* to, int row_pitch, const Operand& o, int rows, int64_t r0, int64_t r_end,
-                                            int64_t k0, int64_t k_end)
-{
-    constexpr int kDepth = 16;
-    const T* p = static_cast<const T*>(o.p);
-    for (int i = threadIdx.x; i < rows * kDepth; i += kRows) {
-        const int k = kInner ? i % kDepth : i / rows, r = kInner ? i / kDepth : i % rows;
-        const bool there = r0 + r < r_end && k0 + k < k_end;
-        to[k * row_pitch + r] = there ? to_f32(p[(r0 + r) * o.outer + (k0 + k) * o.inner]) : 0.0f;
-    }
-}
-
-// A thread has a row and 32 columns; 16 terms at a time in shared memory, summed in fp32 one after the
-// other.
-template <typename T, typename Epi>
-__global__ void __launch_bounds__(kRows) product_simple_kernel(const SimpleArgs g, const Epi epi)
-{
-    constexpr int kDepth = 16;
-    __shared__ __align__(16) float sa[kDepth][kRows + 1], sb[kDepth][kCols + 4];
-    ptx::griddep_wait();
-    const int64_t m = g.m_count ? *g.m_count : g.m, terms = g.k_count ? *g.k_count : g.k;
-    const int64_t strips = (g.n + g.strip - 1) / g.strip, tiles = (m + kRows - 1) / kRows * strips;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t strip = tile % strips, r0 = tile / strips * kRows, r = r0 + threadIdx.x, c0 = strip * g.strip;
-        typename Epi::State state;
-        if (r < m) epi.begin(state, r, c0, 0);
-        for (int64_t c = c0; c < c0 + g.strip && c < g.n; c += kCols) {
-            float v[kCols] = {};
-            for (int64_t k = 0; k < terms; k += kDepth) {
-                if (g.a.inner == 1) simple_load<T, true>(&sa[0][0], kRows + 1, g.a, kRows, r0, m, k, terms);
-                else simple_load<T, false>(&sa[0][0], kRows + 1, g.a, kRows, r0, m, k, terms);
-                if (g.b.inner == 1) simple_load<T, true>(&sb[0][0], kCols + 4, g.b, kCols, c, g.n, k, terms);
-                else simple_load<T, false>(&sb[0][0], kCols + 4, g.b, kCols, c, g.n, k, terms);
-                __syncthreads();
+        const int lane = threadIdx.x & 31, piece = lane & 7, at = lane / 8;
+        const int32_t c = c0 + piece * 4, left = n - c;
 #pragma unroll
-                for (int i = 0; i < kDepth; ++i) {
-                    const float x = sa[i][threadIdx.x];
+        for (int i = 0; i < kTurns; ++i) {
+            const int32_t r = r0 + i * 4 + at;
+            if (r >= room) continue;
+            const float4 v = stage.at(i * 4 + at, piece);
+            bf16* to = dz + r * stride + c;
+            if constexpr (sizeof(T) == 2) {
+                put4(to, v, left, true);
+            } else {
+                bf16 x[kPlanes], y[kPlanes], z[kPlanes], w[kPlanes];
+                split_parts(v.x, x);
+                split_parts(v.y, y);
+                split_parts(v.z, z);
+                split_parts(v.w, w);
 #pragma unroll
-                    for (int j = 0; j < kCols; j += 4) {
-                        const float4 w = *reinterpret_cast<const float4*>(&sb[i][j]);
-                        v[j] = fmaf(x, w.x, v[j]);
-                        v[j + 1] = fmaf(x, w.y, v[j + 1]);
-                        v[j + 2] = fmaf(x, w.z, v[j + 2]);
-                        v[j + 3] = fmaf(x, w.w, v[j + 3]);
-                    }
-                }
-                __syncthreads();
+                for (int j = 0; j < kPlanes; ++j)
+                    put4(to + j * plane, make_float4(__bfloat162float(x[j]), __bfloat162float(y[j]), __bfloat162float(z[j]), __bfloat162float(w[j])), left, true);
             }
-            if (r < m) epi.chunk(state, r, c, v);
         }
-        if (r < m) epi.end(state, r, strip);
     }
-}
-
-template <typename T, typename Epi> cudaError_t product_simple(const SimpleArgs& g, const Epi& epi, cudaStream_t stream)
-{
-    if (g.m <= 0 || g.n <= 0) return cudaSuccess;
-    int sms = 0;
-    const cudaError_t e = sm_count(&sms);
-    if (e != cudaSuccess) return e;
-    const int64_t tiles = (g.m + kRows - 1) / kRows * ((g.n + g.strip - 1) / g.strip), most = (int64_t)sms * 8;
-    return launch_after(product_simple_kernel<T, Epi>, dim3((unsigned)(tiles < most ? tiles : most)), dim3(kRows), 0, stream, g, epi);
-}
+};
 
 }  // namespace
 }  // namespace adacomp

@@ -3,8 +3,11 @@
 // A pair of CTAs (a cluster of two SMs) has tiles of 256 x kN; each loads its 128 rows of A and its half of
 // B's rows for 64 terms at a time, by TMA, into a ring of stages; one thread of the first CTA issues the
 // products (tcgen05.mma, cta_group::2) on both CTAs' shared memory; the sums lie in tensor memory, 128
-// rows in each CTA, in two buffers, so that eight warps hand a tile to the epilogue while the next one
-// is computed. Each operand lies by rows of terms ("k major") or by terms of rows ("mn major", the transposed
+// rows in each CTA, in two buffers. Eight warps take them over into registers, 128 columns of a row per thread, and hand
+// them to the epilogue while the next tile is computed (sixteen with 64 columns each were slower, by the stores that
+// they have under way at once). Where results are held in fp32 they do so every
+// `run` blocks of terms and add the runs up: tensor memory's sums are truncated at every step, all in one
+// direction, which over 2048 terms is 8e-7 of a sum. Each operand lies by rows of terms ("k major") or by terms of rows ("mn major", the transposed
 // operands of the gradients): both are copied as they lie and told apart by the matrix descriptors.
 //
 // fp32 operands are four planes of bf16 numbers (split_parts), and their product is the sum of six products of
@@ -27,7 +30,8 @@ constexpr uint64_t kTcLimit = 2000000000ull;  // ns: of every wait
 template <int kN> struct TcShape {
     static constexpr int kA = 128 * kTcDepth * 2, kB = kN / 2 * kTcDepth * 2;  // bytes of a CTA's stage
     static constexpr int kStages = 196608 / (kA + kB) < 8 ? 196608 / (kA + kB) : 8;
-    static constexpr int kShared = kStages * (kA + kB) + 1024 + 256;  // 1024: to begin on such a boundary
+    static constexpr int kStage = 4096;  // of an epilogue warp
+    static constexpr int kShared = kStages * (kA + kB) + 8 * kStage + 1024;  // 1024: to begin on such a boundary
 };
 
 // ---------------------------------------------------------------- operands
@@ -44,6 +48,7 @@ struct TcArgs {
     int32_t planes;                    // 1, or kPlanes
     int32_t splits;                    // of the terms, each a product of its own
     int32_t a_mn, b_mn;                // operands that lie by terms
+    int32_t run;                       // blocks of terms whose sums are formed in tensor memory
     int32_t group;                     // tiles of rows that are taken before the next column's
 };
 
@@ -52,6 +57,7 @@ struct PackArgs {
     bf16* to;
     const int32_t *map, *count;  // which rows, and how many; NULL: all
     int64_t rows, cols, from_stride, to_stride, plane;
+    bool whole;  // rows that can be read 16 bytes at a time
 };
 
 // A matrix of any layout by rows of contiguous elements as aligned rows of bf16 numbers (planes of them for fp32); with
@@ -65,17 +71,18 @@ template <typename T> __global__ void __launch_bounds__(kTcPack) pack_kernel(con
     for (int64_t i = (int64_t)blockIdx.x * kTcPack + threadIdx.x; i < all; i += (int64_t)gridDim.x * kTcPack) {
         const int64_t r = i / each, c = (i - r * each) * 8;
         const T* from = static_cast<const T*>(a.from) + (r < count ? (a.map ? (int64_t)a.map[r] : r) * a.from_stride : 0) + c;
-        bf16 v[sizeof(T) == 4 ? kPlanes : 1][8];
+        float x[8];
+        get_chunk(from, x, r < count ? a.cols - c : 0, a.whole);
+        __align__(16) bf16 v[sizeof(T) == 4 ? kPlanes : 1][8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const T x = r < count && c + j < a.cols ? from[j] : from_f32<T>(0.0f);
             if constexpr (sizeof(T) == 4) {
                 bf16 part[kPlanes];
-                split_parts(x, part);
+                split_parts(x[j], part);
 #pragma unroll
                 for (int p = 0; p < kPlanes; ++p) v[p][j] = part[p];
             } else {
-                v[0][j] = x;
+                v[0][j] = __float2bfloat16_rn(x[j]);
             }
         }
         bf16* to = a.to + r * a.to_stride + c;
@@ -95,6 +102,16 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
+// One lane of a converged warp. The instructions that a single thread issues take their operands from uniform
+// registers, and under this predicate, in loops of the whole warp, the compiler keeps them there (with a branch for
+// one lane they are moved there each time: 8192 x 2048 x 16384 bf16 took 369 us, and 287 so).
+__device__ __forceinline__ bool elect()
+{
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
@@ -109,38 +126,28 @@ __device__ __forceinline__ uint32_t map_shared(const void* p, uint32_t rank)  //
 
 __device__ __forceinline__ void arrive_at(uint32_t bar)  // an address of the cluster
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// A wait on a barrier that other CTAs arrive at, bounded in time; false when it ran out, here or
-// in another warp (dead).
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
+// A wait bounded in time; false when it ran out, here or in another warp (dead).
+// The clock is looked at after many tries only: a look takes longer than most waits.
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* dead)
 {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(ptx::smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
+    const uint64_t from = ptx::globaltimer();
+    while (!*dead && ptx::globaltimer() - from <= kTcLimit) {
+        for (int i = 0; i < 64; ++i)
+            if (ptx::mbar_try_wait(bar, parity)) return true;
+    }
+    *dead = 1;
+    return false;
 }
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead)
 {
-    if (try_wait_cluster(bar, parity)) return true;
-    const uint64_t from = ptx::globaltimer();
-    for (uint32_t i = 1;; ++i) {
-        if (try_wait_cluster(bar, parity)) return true;
-        if ((i & 31) == 0) {
-            if (*dead) return false;
-            if (ptx::globaltimer() - from > kTcLimit) {
-                *dead = 1;
-                return false;
-            }
-        }
-    }
+#pragma unroll 1
+    for (int i = 0; i < 4096; ++i)
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+    return wait_long(bar, parity, dead);
 }
 
 __device__ __forceinline__ void load(uint32_t to, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint32_t bar)
@@ -186,15 +193,12 @@ __device__ __forceinline__ void commit(uint64_t* bar)
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void read_chunk(uint32_t at, uint32_t (&v)[32])  // 32 lanes' rows, 32 columns each
+__device__ __forceinline__ void read_chunk(uint32_t at, uint32_t (&v)[16])  // 32 lanes' rows, 16 columns each
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(at)
         : "memory");
 }
@@ -208,20 +212,20 @@ __device__ __forceinline__ int plane_a(int pass) { return (0x231130 >> 4 * (5 - 
 __device__ __forceinline__ int plane_b(int pass) { return (0x321310 >> 4 * (5 - pass)) & 15; }
 
 // ---------------------------------------------------------------- kernel
-template <int kN, typename Epi>
+template <int kN, bool kSplit, typename Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const TcArgs g,
                       const Epi epi)
 {
     using Shape = TcShape<kN>;
     constexpr int kStages = Shape::kStages;
-    extern __shared__ uint8_t raw[];
+    extern __shared__ __align__(1024) uint8_t raw[];
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2], drained;
     __shared__ uint32_t tmem_at;
     __shared__ int dead_flag;
     volatile int* dead = &dead_flag;
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const uint32_t base = (ptx::smem_addr(raw) + 1023) & ~1023u;
     if (threadIdx.x == 0) {
@@ -251,20 +255,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     const uint32_t tmem = tmem_at;
     ptx::griddep_wait();
 
-    const int64_t m = g.m_count ? *g.m_count : g.m, terms = g.k_count ? *g.k_count : g.k;
-    const int64_t tiles_m = (m + kTcM - 1) / kTcM, tiles_n = (g.n + kN - 1) / kN, tiles = tiles_m * tiles_n;
-    const int64_t blocks = (terms + kTcDepth - 1) / kTcDepth, per_split = (blocks + g.splits - 1) / g.splits;
+    const int32_t m = (int32_t)(g.m_count ? *g.m_count : g.m), terms = (int32_t)(g.k_count ? *g.k_count : g.k), n = (int32_t)g.n;
+    const int32_t tiles_m = (m + kTcM - 1) / kTcM, tiles_n = (n + kN - 1) / kN;
+    const int32_t blocks = (terms + kTcDepth - 1) / kTcDepth, per_split = (blocks + g.splits - 1) / g.splits;
     const int passes = g.planes == 1 ? 1 : 6;
-    const int64_t units = tiles * g.splits, first = blockIdx.x / 2, step = gridDim.x / 2;
+    const int64_t tiles = (int64_t)tiles_m * tiles_n, units = tiles * g.splits, first = blockIdx.x / 2, step = gridDim.x / 2;
     struct Unit {
-        int64_t m0, n0, from, count;
-        int split;
+        int32_t m0, n0, from, count, split;
     };
     const auto unit_of = [&](int64_t u) {
         Unit t;
-        t.split = (int)(u / tiles);
-        const int64_t tile = u - t.split * tiles, whole = (int64_t)g.group * tiles_n, band = tile / whole, in = tile - band * whole;
-        const int64_t rows = tiles_m - band * g.group < g.group ? tiles_m - band * g.group : g.group;
+        t.split = (int32_t)(u / tiles);
+        const int64_t tile = u - t.split * tiles, whole = (int64_t)g.group * tiles_n;
+        const int32_t band = (int32_t)(tile / whole), in = (int32_t)(tile - band * whole);
+        const int32_t rows = tiles_m - band * g.group < g.group ? tiles_m - band * g.group : g.group;
         t.n0 = in / rows * kN;
         t.m0 = (band * g.group + in % rows) * kTcM;
         t.from = t.split * per_split;
@@ -273,130 +277,151 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         return t;
     };
 
-    if (warp == 0 && lane == 0) {  // copies
-        uint32_t n = 0;  // stages so far
-        const uint32_t leader = rank & ~1u;
-        bool alive = true;
-        for (int64_t u = first; u < units && alive; u += step) {
-            const Unit t = unit_of(u);
-            const int32_t ma = (int32_t)(t.m0 + rank * 128), nb = (int32_t)(t.n0 + rank * (kN / 2));
-            for (int pass = 0; pass < passes && alive; ++pass) {
-                const int pa = passes == 1 ? 0 : plane_a(pass), pb = passes == 1 ? 0 : plane_b(pass);
-                for (int64_t k = 0; k < t.count; ++k, ++n) {
-                    const int s = (int)(n % kStages);
-                    alive = tc::wait(&empty[s], (n / kStages & 1) ^ 1, dead);
-                    if (!alive) break;
-                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * (Shape::kA + Shape::kB));
-                    const uint32_t bar = tc::map_shared(&full[s], leader), at = base + s * (Shape::kA + Shape::kB);
-                    const int32_t k0 = (int32_t)((t.from + k) * kTcDepth);
-                    if (g.a_mn) {
+    // 384 threads of 168 registers: 128 with 40 and 256 with 232 are as many
+    if (warp < kTcEpilogue) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0) {  // copies
+            uint32_t at_stage = 0, turn = 0, issued = 0;
+            const uint32_t full_at = tc::map_shared(full, 0);  // the first CTA's
+            bool alive = true;
+            for (int64_t u = first; u < units && alive; u += step) {
+                const Unit t = unit_of(u);
+                const int32_t ma = t.m0 + (int32_t)rank * 128, nb = t.n0 + (int32_t)rank * (kN / 2);
+                for (int32_t from = 0; from < t.count && alive; from += g.run) {
+                    const int32_t end = t.count - from < g.run ? t.count : from + g.run;
+                    for (int pass = 0; pass < passes && alive; ++pass) {
+                        const int pa = passes == 1 ? 0 : plane_a(pass), pb = passes == 1 ? 0 : plane_b(pass);
+                        for (int32_t k = from; k < end; ++k) {
+                            alive = __all_sync(0xffffffffu, tc::wait(&empty[at_stage], turn ^ 1, dead));
+                            if (!alive) break;
+                            const uint32_t bar = full_at + at_stage * 8, at = base + at_stage * (Shape::kA + Shape::kB);
+                            const int32_t k0 = (t.from + k) * kTcDepth;
+                            if (tc::elect()) {
+                                if (rank == 0) ptx::mbar_arrive_expect_tx(&full[at_stage], 2 * (Shape::kA + Shape::kB));
+                                if (g.a_mn) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) tc::load(at + i * 8192, &map_a, ma + 64 * i, k0, pa, bar);
-                    } else {
-                        tc::load(at, &map_a, k0, ma, pa, bar);
-                    }
-                    if (g.b_mn) {
+                                    for (int i = 0; i < 2; ++i) tc::load(at + i * 8192, &map_a, ma + 64 * i, k0, pa, bar);
+                                } else {
+                                    tc::load(at, &map_a, k0, ma, pa, bar);
+                                }
+                                if (g.b_mn) {
 #pragma unroll
-                        for (int i = 0; i < kN / 128; ++i) tc::load(at + Shape::kA + i * 8192, &map_b, nb + 64 * i, k0, pb, bar);
-                    } else {
-                        tc::load(at + Shape::kA, &map_b, k0, nb, pb, bar);
+                                    for (int i = 0; i < kN / 128; ++i) tc::load(at + Shape::kA + i * 8192, &map_b, nb + 64 * i, k0, pb, bar);
+                                } else {
+                                    tc::load(at + Shape::kA, &map_b, k0, nb, pb, bar);
+                                }
+                            }
+                            ++issued;
+                            if (++at_stage == kStages) at_stage = 0, turn ^= 1;
+                        }
                     }
                 }
             }
-        }
-        if (!alive) {  // the copies in flight end before the CTA does: each stage's last one
-            int none = 0;
-            if (rank == 0)
-                for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
-                    tc::wait(&full[i % kStages], i / kStages & 1, &none);
-            else {
-                const uint64_t from = ptx::globaltimer();
-                while (ptx::globaltimer() - from < 10000000ull) {}  // 10 ms, as their barrier is the other CTA's
+            if (!alive) {  // the copies in flight end before the CTA does: each stage's last one
+                int none = 0;
+                if (rank == 0) {
+                    for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                        tc::wait(&full[i % kStages], i / kStages & 1, &none);
+                } else {  // their barrier is the other CTA's: 10 ms
+                    const uint64_t from = ptx::globaltimer();
+                    while (ptx::globaltimer() - from < 10000000ull) {}
+                }
             }
-        }
-    } else if (warp == 1 && lane == 0 && rank == 0) {  // products
-        const uint32_t kind = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(g.a_mn != 0) << 15 | (uint32_t)(g.b_mn != 0) << 16 |
-                              (uint32_t)(kN / 8) << 17 | (uint32_t)(kTcM / 16) << 24;
-        // 16 terms further: 32 bytes along a line, or 16 lines
-        const uint32_t step_a = g.a_mn ? 2048 : 32, step_b = g.b_mn ? 2048 : 32;
-        const uint32_t block_a = g.a_mn ? 8192 : 16, block_b = g.b_mn ? 8192 : 16;
-        uint32_t n = 0, done = 0;
-        bool alive = true;
-        for (int64_t u = first; u < units && alive; u += step) {
-            const Unit t = unit_of(u);
-            if (t.count == 0) continue;
-            const int buffer = (int)(done & 1);
-            alive = tc::wait(&sums_empty[buffer], (done / 2 & 1) ^ 1, dead);
-            if (!alive) break;
-            tc::fence_after();
-            const uint32_t d = tmem + buffer * 256;
-            const int64_t all = t.count * passes;
-            for (int64_t i = 0; i < all; ++i, ++n) {
-                const int s = (int)(n % kStages);
-                alive = tc::wait(&full[s], (n / kStages & 1), dead);
-                if (!alive) break;
-                tc::fence_after();
-                const uint32_t at = base + s * (Shape::kA + Shape::kB);
+        } else if (warp == 1 && rank == 0) {  // products
+            const uint32_t kind = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(g.a_mn != 0) << 15 | (uint32_t)(g.b_mn != 0) << 16 |
+                                  (uint32_t)(kN / 8) << 17 | (uint32_t)(kTcM / 16) << 24;
+            // 16 terms further: 32 bytes along a line, or 16 lines
+            const uint32_t step_a = (g.a_mn ? 2048 : 32) >> 4, step_b = (g.b_mn ? 2048 : 32) >> 4;
+            const uint64_t first_a = tc::descriptor(base, g.a_mn ? 8192 : 16, 1024);
+            const uint64_t first_b = tc::descriptor(base + Shape::kA, g.b_mn ? 8192 : 16, 1024);
+            uint32_t at_stage = 0, turn = 0, done = 0;
+            bool alive = true;
+            for (int64_t u = first; u < units && alive; u += step) {
+                const Unit t = unit_of(u);
+                for (int32_t from = 0; from < t.count && alive; from += g.run) {
+                    const int buffer = (int)(done & 1);
+                    alive = __all_sync(0xffffffffu, tc::wait(&sums_empty[buffer], (done / 2 & 1) ^ 1, dead));
+                    if (!alive) break;
+                    tc::fence_after();
+                    const uint32_t d = tmem + buffer * 256;
+                    const int32_t all = (t.count - from < g.run ? t.count - from : g.run) * passes;
+                    for (int32_t i = 0; i < all; ++i) {
+                        alive = __all_sync(0xffffffffu, tc::wait(&full[at_stage], turn, dead));
+                        if (!alive) break;
+                        tc::fence_after();
+                        const uint32_t at = at_stage * ((Shape::kA + Shape::kB) >> 4);
+                        if (tc::elect()) {
 #pragma unroll
-                for (int j = 0; j < kTcDepth / 16; ++j)
-                    tc::mma(d, tc::descriptor(at + j * step_a, block_a, 1024),
-                            tc::descriptor(at + Shape::kA + j * step_b, block_b, 1024), kind, i > 0 || j > 0);
-                tc::commit(&empty[s]);
+                            for (int j = 0; j < kTcDepth / 16; ++j)
+                                tc::mma(d, first_a + at + j * step_a, first_b + at + j * step_b, kind, i > 0 || j > 0);
+                            tc::commit(&empty[at_stage]);
+                        }
+                        if (++at_stage == kStages) at_stage = 0, turn ^= 1;
+                    }
+                    if (!alive) break;
+                    if (tc::elect()) tc::commit(&sums_full[buffer]);
+                    ++done;
+                }
             }
-            if (!alive) break;
-            tc::commit(&sums_full[buffer]);
-            ++done;
+            if (!alive) {  // the products in flight end before the tensor memory is given back
+                int none = 0;
+                if (tc::elect()) tc::commit(&drained);
+                tc::wait(&drained, 0, &none);
+            }
         }
-        if (!alive) {  // the products in flight end before the tensor memory is given back
-            int none = 0;
-            tc::commit(&drained);
-            tc::wait(&drained, 0, &none);
-        }
-    } else if (warp >= kTcEpilogue) {
-        const int quarter = warp & 3, half = (warp - kTcEpilogue) / 4;
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        constexpr int kStrips = kN / kStrip, kMine = (kStrips + 1) / 2;  // strips of a tile, and of a half of the warps
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int quarter = warp & 3, strip = (warp - kTcEpilogue) / 4;
+        const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + strip * kStrip;
+        const Stage stage = {reinterpret_cast<float4*>(raw + (base - ptx::smem_addr(raw)) + kStages * (Shape::kA + Shape::kB) +
+                                                       (warp - kTcEpilogue) * Shape::kStage)};
+        const uint32_t freed[2] = {tc::map_shared(&sums_empty[0], 0), tc::map_shared(&sums_empty[1], 0)};
         uint32_t done = 0;
         bool alive = true;
         for (int64_t u = first; u < units; u += step) {
             const Unit t = unit_of(u);
-            const int64_t r = t.m0 + rank * 128 + quarter * 32 + lane;
-            const int buffer = (int)(done & 1);
-            if (t.count && alive) {
-                alive = tc::wait(&sums_full[buffer], (done / 2 & 1), dead);
+            const int32_t r = t.m0 + (int32_t)rank * 128 + quarter * 32 + lane, c0 = t.n0 + strip * kStrip;
+            typename Epi::State state = {};
+            if (r < m && c0 < n) state = epi.begin(r, c0);
+            float v[kStrip];
+#pragma unroll
+            for (int i = 0; i < kStrip; ++i) v[i] = 0.0f;
+#pragma unroll 1
+            for (int32_t from = 0; from < t.count; from += g.run, ++done) {
+                const int buffer = (int)(done & 1);
+                alive = __all_sync(0xffffffffu, alive && tc::wait(&sums_full[buffer], done / 2 & 1, dead));
+                if (!alive) break;
                 tc::fence_after();
-            }
-            alive = __all_sync(0xffffffffu, alive);
-#pragma unroll 1
-            for (int strip = half * kMine; strip < kStrips && strip < (half + 1) * kMine; ++strip) {
-                const int64_t c0 = t.n0 + strip * kStrip;
-                if (c0 >= g.n) break;
-                typename Epi::State state;
-                if (r < m) epi.begin(state, r, c0, t.split);
-#pragma unroll 1
-                for (int c = 0; c < kStrip; c += kCols) {
-                    float v[kCols];
-                    __syncwarp();
-                    if (t.count && alive) {
-                        uint32_t w[kCols];
-                        tc::read_chunk(lanes + buffer * 256 + strip * kStrip + c, w);
-                        tc::read_wait();
 #pragma unroll
-                        for (int i = 0; i < kCols; ++i) v[i] = __uint_as_float(w[i]);
-                    } else {
+                for (int c = 0; c < kStrip; c += 16) {
+                    uint32_t w[16];
+                    tc::read_chunk(mine + buffer * 256 + c, w);
+                    tc::read_wait();
 #pragma unroll
-                        for (int i = 0; i < kCols; ++i) v[i] = alive ? 0.0f : NAN;
-                    }
-                    if (r < m) epi.chunk(state, r, c0 + c, v);
-                    else if (Epi::kZeros) epi.zeros(r, c0 + c);
+                    for (int i = 0; i < 16; ++i) v[c + i] += __uint_as_float(w[i]);
                 }
-                if (r < m) epi.end(state, r, c0 / kStrip);
-            }
-            if (t.count) {
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) tc::arrive_at(tc::map_shared(&sums_empty[buffer], 0));
-                ++done;
+                if (lane == 0) tc::arrive_at(freed[buffer]);
+            }
+            if (!alive) {
+#pragma unroll
+                for (int i = 0; i < kStrip; ++i) v[i] = NAN;
+            }
+            if (c0 >= n) continue;
+            epi.rows(state, r, c0, r < m, v);
+            __syncwarp();
+            if constexpr (Epi::kChunks) {
+#pragma unroll
+                for (int c = 0; c < kStrip; c += 32) {
+                    if (c0 + c >= n) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) stage.at(lane, i) = make_float4(v[c + 4 * i], v[c + 4 * i + 1], v[c + 4 * i + 2], v[c + 4 * i + 3]);
+                    __syncwarp();
+                    if constexpr (kSplit) epi.of_split(t.split).chunk(stage, r - lane, m, c0 + c);
+                    else epi.chunk(stage, r - lane, m, c0 + c);
+                    __syncwarp();
+                }
             }
         }
     }
@@ -407,8 +432,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 }
 
 // ---------------------------------------------------------------- host
-// The sums of the parts that the terms were split into, one after the other, handed to an epilogue. A thread has a row's 32
+// The sums of the parts that the terms were split into, one after the other, handed to an epilogue. A thread has four of a row's
 // columns.
+constexpr int kJoin = 4;
 struct JoinPartsArgs {
     const float* part;  // [splits][m][stride]
     int64_t m, n, stride;
@@ -420,27 +446,20 @@ template <typename Epi> __global__ void __launch_bounds__(kRows) join_parts_kern
 {
     ptx::griddep_wait();
     const int64_t m = a.m_count ? *a.m_count : a.m;
-    const int64_t chunks = (a.n + kCols - 1) / kCols, i = (int64_t)blockIdx.x * kRows + threadIdx.x;
+    const int64_t chunks = (a.n + kJoin - 1) / kJoin, i = (int64_t)blockIdx.x * kRows + threadIdx.x;
     if (i >= chunks * m) return;
-    const int64_t r = i / chunks, c = (i - r * chunks) * kCols;
-    float v[kCols] = {};
-    for (int s = 0; s < a.splits; ++s) {
-        float b[kCols];
-        get_chunk(a.part + ((int64_t)s * a.m + r) * a.stride + c, b, a.n - c, true);
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) v[j] += b[j];
-    }
-    typename Epi::State state;
-    epi.begin(state, r, c, 0);
-    epi.chunk(state, r, c, v);
-    epi.end(state, r, c / kStrip);
+    const int64_t r = i / chunks, c = (i - r * chunks) * kJoin;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) v = v + get4(a.part + ((int64_t)s * a.m + r) * a.stride + c, 4, true);
+    epi.piece((int32_t)r, (int32_t)c, v);
 }
 
 // A product of no terms: the epilogue of zeros.
 template <typename T, typename Epi> cudaError_t product_none(int64_t m, int64_t n, const Epi& epi, cudaStream_t stream)
 {
     const JoinPartsArgs j = {nullptr, m, n, 0, nullptr, 0};
-    const int64_t all = (n + kCols - 1) / kCols * m;
+    const int64_t all = (n + kJoin - 1) / kJoin * m;
     return launch_after(join_parts_kernel<Epi>, dim3((unsigned)((all + kRows - 1) / kRows)), dim3(kRows), 0, stream, j, epi);
 }
 
@@ -506,7 +525,7 @@ cudaError_t take_matrix(Matrix* out, const void* p, int64_t stride, int64_t rows
     }
     const int64_t to_rows = count ? out_rows : rows;
     *out = {room, to_rows, cols, round_up(cols, 8), to_rows * round_up(cols, 8)};
-    PackArgs a = {p, room, map, count, rows, cols, stride, out->stride, out->plane};
+    PackArgs a = {p, room, map, count, rows, cols, stride, out->stride, out->plane, whole_rows(p, stride, rows, sizeof(T))};
     int sms = 0;
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
@@ -515,18 +534,18 @@ cudaError_t take_matrix(Matrix* out, const void* p, int64_t stride, int64_t rows
     return launch_after(pack_kernel<T>, dim3((unsigned)(need < most ? need : most)), dim3(kTcPack), 0, stream, a);
 }
 
-template <int kN, typename Epi>
+template <int kN, bool kSplit, typename Epi>
 cudaError_t product_tc_n(const Matrix& a, const Matrix& b, const TcArgs& g, const Epi& epi, cudaStream_t stream)
 {
     CUtensorMap map_a, map_b;
     cudaError_t e = tensor_map(&map_a, a, g.planes, g.a_mn ? kTcDepth : 128);
     if (e == cudaSuccess) e = tensor_map(&map_b, b, g.planes, g.b_mn ? kTcDepth : kN / 2);
-    if (e == cudaSuccess) e = allow<product_tc_kernel<kN, Epi>>(TcShape<kN>::kShared);
+    if (e == cudaSuccess) e = allow<product_tc_kernel<kN, kSplit, Epi>>(TcShape<kN>::kShared);
     int sms = 0;
     if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     const int64_t units = (g.m + kTcM - 1) / kTcM * ((g.n + kN - 1) / kN) * g.splits, pairs = sms / 2;
-    return launch_after(product_tc_kernel<kN, Epi>, dim3((unsigned)(2 * (units < pairs ? units : pairs))), dim3(kTcThreads),
+    return launch_after(product_tc_kernel<kN, kSplit, Epi>, dim3((unsigned)(2 * (units < pairs ? units : pairs))), dim3(kTcThreads),
                         TcShape<kN>::kShared, stream, map_a, map_b, g, epi);
 }
 
@@ -558,20 +577,25 @@ cudaError_t product_tc(const Matrix& a, bool a_mn, const Matrix& b, bool b_mn, T
     g.planes = sizeof(T) == 4 ? kPlanes : 1;
     g.a_mn = a_mn;
     g.b_mn = b_mn;
-    g.splits = parts ? splits_of(g.m, g.n, g.k) : 1;
+    g.splits = Epi::kPieces ? splits_of(g.m, g.n, g.k) : 1;
     g.group = 8;
-    if (g.splits == 1) return product_tc_n<256>(a, b, g, epi, stream);
+    g.run = sizeof(T) == 4 ? 4 : Epi::kExact ? 8 : 1 << 30;
+    if constexpr (Epi::kPieces) {
+    if (g.splits > 1) {
     EpiStore<float> each = {};
     each.out = parts;
     each.stride = round_up(g.n, 4);
     each.split_stride = g.m * each.stride;
-    each.n = g.n;
+    each.n = (int32_t)g.n;
     each.first = each.last = each.whole = true;
-    const cudaError_t e = product_tc_n<256>(a, b, g, each, stream);
+    const cudaError_t e = product_tc_n<256, true>(a, b, g, each, stream);
     if (e != cudaSuccess) return e;
     const JoinPartsArgs j = {parts, g.m, g.n, each.stride, g.m_count, g.splits};
-    const int64_t all = (g.n + kCols - 1) / kCols * g.m;
+    const int64_t all = (g.n + kJoin - 1) / kJoin * g.m;
     return launch_after(join_parts_kernel<Epi>, dim3((unsigned)((all + kRows - 1) / kRows)), dim3(kRows), 0, stream, j, epi);
+    }
+    }
+    return product_tc_n<256, false>(a, b, g, epi, stream);
 }
 
 }  // namespace

@@ -13,7 +13,8 @@ namespace adacomp {
 namespace {
 
 constexpr int kListThreads = 256;
-constexpr int kScanThreads = 1024;
+constexpr int kScanThreads = 256, kScanRows = 1024;
+constexpr int kJoinThreads = 1024;
 constexpr int kZeroThreads = 256;
 
 struct VocabArgs {
@@ -90,19 +91,6 @@ struct ListArgs {
     float *to_q, *given;
 };
 
-// One token of weight 1 for each row that has a target.
-__global__ void __launch_bounds__(kListThreads) vocab_target_kernel(const ListArgs a)
-{
-    ptx::griddep_wait();
-    for (int64_t r = (int64_t)blockIdx.x * kListThreads + threadIdx.x; r < a.rows; r += (int64_t)gridDim.x * kListThreads) {
-        const int64_t t = a.target_bytes == 8 ? static_cast<const int64_t*>(a.target)[r]
-                                              : static_cast<const int32_t*>(a.target)[r];
-        a.to_index[r] = t >= 0 && t < a.vocab ? (int32_t)t : INT32_MAX;
-        a.to_q[r] = 1.0f;
-        a.given[r] = t < 0 ? -INFINITY : t < a.vocab ? 0.0f : NAN;
-    }
-}
-
 // A teacher's list of a row by a warp: softmax of its logits, and the tokens in ascending order (each place is
 // the number of places before it, so equal tokens keep their order).
 template <typename L> __global__ void __launch_bounds__(kListThreads) vocab_teacher_kernel(const ListArgs a)
@@ -169,53 +157,68 @@ template <typename L> __global__ void __launch_bounds__(kListThreads) vocab_teac
     }
 }
 
-// The rows that have a loss, in their order, and how many there are. One CTA.
-__global__ void __launch_bounds__(kScanThreads) vocab_rows_kernel(const float* given, int64_t rows, int32_t* map, int32_t* count)
+// The rows that have a loss, in their order, and how many there are. A CTA has kScanRows rows, and counts those
+// before them itself. kTarget: of one token each, which become lists of one, of weight 1.
+template <bool kTarget> __global__ void __launch_bounds__(kScanThreads) vocab_rows_kernel(const ListArgs a, int32_t* map, int32_t* count)
 {
-    constexpr int kEach = 8;
-    __shared__ int32_t sums[kScanThreads / 32];
+    constexpr int kEach = kScanRows / kScanThreads, kWarps = kScanThreads / 32;
+    __shared__ int32_t sums[2][kWarps];
     ptx::griddep_wait();
-    int32_t before = 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int64_t r0 = 0; r0 < rows; r0 += kScanThreads * kEach) {
-        bool there[kEach];
-        int32_t mine = 0;
+    const auto target = [&](int64_t r) {
+        return a.target_bytes == 8 ? static_cast<const int64_t*>(a.target)[r] : (int64_t) static_cast<const int32_t*>(a.target)[r];
+    };
+    const auto valid = [&](int64_t r) { return kTarget ? target(r) >= 0 : a.given[r] != -INFINITY; };
+    const int64_t r0 = (int64_t)blockIdx.x * kScanRows;
+    int32_t before = 0, mine = 0;
+    for (int64_t r = threadIdx.x; r < r0; r += kScanThreads) before += valid(r);
+    bool there[kEach];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int64_t r = r0 + threadIdx.x * kEach + i;
-            there[i] = r < rows && given[r] != -INFINITY;
-            mine += there[i];
+    for (int i = 0; i < kEach; ++i) {
+        const int64_t r = r0 + threadIdx.x * kEach + i;
+        there[i] = r < a.rows && valid(r);
+        mine += there[i];
+        if (kTarget && r < a.rows) {
+            const int64_t t = target(r);
+            a.to_index[r] = t >= 0 && t < a.vocab ? (int32_t)t : INT32_MAX;
+            a.to_q[r] = 1.0f;
+            a.given[r] = t < 0 ? -INFINITY : t < a.vocab ? 0.0f : NAN;
         }
-        int32_t sum = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int32_t v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
-        }
-        if (lane == 31) sums[warp] = sum;
-        __syncthreads();
-        int32_t at = before + sum - mine, all = 0;
-        for (int i = 0; i < kScanThreads / 32; ++i) {
-            if (i < warp) at += sums[i];
-            all += sums[i];
-        }
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (there[i]) map[at++] = (int32_t)(r0 + threadIdx.x * kEach + i);
-        before += all;
-        __syncthreads();
     }
-    if (threadIdx.x == 0) *count = before;
+    int32_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    if (lane == 31) {
+        sums[0][warp] = sum;
+        sums[1][warp] = before;
+    }
+    __syncthreads();
+    int32_t at = sum - mine, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        at += sums[1][i] + (i < warp ? sums[0][i] : 0);
+        all += sums[1][i] + sums[0][i];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+        if (there[i]) map[at++] = (int32_t)(r0 + threadIdx.x * kEach + i);
+    if (threadIdx.x == 0 && blockIdx.x == gridDim.x - 1) *count = all;
 }
 
-// The rows of dx without a loss.
+// The rows of dx without a loss, a warp each.
 template <typename T>
 __global__ void __launch_bounds__(kZeroThreads) vocab_zero_kernel(T* dx, int64_t stride, const float* given, int64_t rows, int64_t dim)
 {
     ptx::griddep_wait();
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int64_t warps = kZeroThreads / 32;
+    for (int64_t r = blockIdx.x * warps + threadIdx.x / 32; r < rows; r += gridDim.x * warps) {
         if (given[r] != -INFINITY) continue;
-        for (int64_t i = threadIdx.x; i < dim; i += kZeroThreads) dx[r * stride + i] = from_f32<T>(0.0f);
+        for (int64_t i = threadIdx.x & 31; i < dim; i += 32) dx[r * stride + i] = from_f32<T>(0.0f);
     }
 }
 
@@ -229,40 +232,54 @@ struct JoinArgs {
     float temperature;
 };
 
-// A row's strips joined, and its loss, by a warp; rows without a loss are 0.
-__global__ void __launch_bounds__(kListThreads) vocab_join_kernel(const JoinArgs a)
+// Rows' strips joined, and their losses; rows without a loss are 0. A CTA has 32 rows, a warp each 32nd of
+// their strips, a lane a row; then a warp a row, for its list.
+__global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinArgs a)
 {
+    constexpr int kWarps = kJoinThreads / 32;
+    __shared__ float2 sums[kWarps][33];
     ptx::griddep_wait();
-    const int lane = threadIdx.x & 31, warps = kListThreads / 32;
-    const int64_t count = *a.count, first = (int64_t)blockIdx.x * warps + (threadIdx.x >> 5);
-    for (int64_t r = first; r < count; r += (int64_t)gridDim.x * warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t count = *a.count;
+    for (int64_t r0 = (int64_t)blockIdx.x * 32; r0 < count; r0 += (int64_t)gridDim.x * 32) {
+        const int64_t r = r0 + lane;
         float top = -INFINITY, sum = 0.0f;
-        for (int64_t i = lane; i < a.strips; i += 32) top = fmaxf(top, a.part[i * a.rows + r].x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float from = top == -INFINITY ? 0.0f : top;
-        for (int64_t i = lane; i < a.strips; i += 32) {
-            const float2 p = a.part[i * a.rows + r];
-            sum += p.y * expf(p.x - from);
-        }
-        sum = warp_sum(sum);
-        const float lse = top + logf(sum);
-        const int64_t row = a.map[r];
-        const float given = a.given[row];
-        float mean = 0.0f;  // of the logits under q
-        if (given == given)
-            for (int j = lane; j < a.k; j += 32) {
-                const float q = a.q[row * a.k + j];
-                if (q > 0.0f) mean += q * a.picked[row * a.k + j];
+        if (r < count) {
+#pragma unroll 4
+            for (int64_t i = warp; i < a.strips; i += kWarps) {
+                const float2 p = a.part[i * a.rows + r];
+                const float more = fmaxf(top, p.x), less = more == -INFINITY ? 0.0f : more;
+                sum = sum * expf(top - less) + p.y * expf(p.x - less);
+                top = more;
             }
-        mean = warp_sum(mean);
-        if (lane == 0) {
-            a.lse[row] = lse;
-            a.loss[row] = a.temperature * a.temperature * (given + (lse - mean));
         }
+        sums[warp][lane] = make_float2(top, sum);
+        __syncthreads();
+        if (const int i = warp; r0 + i < count) {
+            const float2 p = sums[lane][i];
+            float most = p.x;
+#pragma unroll
+            for (int o = kWarps / 2; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const float all = warp_sum(p.y * expf(p.x - (most == -INFINITY ? 0.0f : most)));
+            const float lse = most + logf(all);
+            const int64_t row = a.map[r0 + i];
+            const float given = a.given[row];
+            float mean = 0.0f;  // of the logits under q
+            if (given == given)
+                for (int j = lane; j < a.k; j += 32) {
+                    const float q = a.q[row * a.k + j];
+                    if (q > 0.0f) mean += q * a.picked[row * a.k + j];
+                }
+            mean = warp_sum(mean);
+            if (lane == 0) {
+                a.lse[row] = lse;
+                a.loss[row] = a.temperature * a.temperature * (given + (lse - mean));
+            }
+        }
+        __syncthreads();
     }
-    for (int64_t r = first; r < a.rows; r += (int64_t)gridDim.x * warps)
-        if (a.given[r] == -INFINITY && lane == 0) a.loss[r] = a.lse[r] = 0.0f;
+    for (int64_t r = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; r < a.rows; r += (int64_t)gridDim.x * kJoinThreads)
+        if (a.given[r] == -INFINITY) a.loss[r] = a.lse[r] = 0.0f;
 }
 
 // ---------------------------------------------------------------- passes
@@ -290,13 +307,15 @@ template <typename T> cudaError_t vocab_rows(const VocabArgs& a, const VocabPart
     l.to_index = p.index;
     l.to_q = p.q;
     l.given = p.given;
-    cudaError_t e;
-    if (a.target) e = launch_after(vocab_target_kernel, dim3(blocks_of(a.rows, kListThreads, 1024)), dim3(kListThreads), 0, stream, l);
-    else
+    cudaError_t e = cudaSuccess;
+    const dim3 scan((unsigned)((a.rows + kScanRows - 1) / kScanRows)), threads(kScanThreads);
+    if (a.target) {
+        e = launch_after(vocab_rows_kernel<true>, scan, threads, 0, stream, l, p.map, p.count);
+    } else {
         e = launch_after(a.logit_dtype == ADACOMP_BF16 ? vocab_teacher_kernel<bf16> : vocab_teacher_kernel<float>,
                          dim3(blocks_of(a.rows, kListThreads / 32, 4096)), dim3(kListThreads), 0, stream, l);
-    if (e != cudaSuccess) return e;
-    e = launch_after(vocab_rows_kernel, dim3(1), dim3(kScanThreads), 0, stream, (const float*)p.given, a.rows, p.map, p.count);
+        if (e == cudaSuccess) e = launch_after(vocab_rows_kernel<false>, scan, threads, 0, stream, l, p.map, p.count);
+    }
     if (e != cudaSuccess) return e;
     e = take_matrix<T>(x, a.x, a.x_stride, a.rows, a.dim, p.x, stream, p.map, p.count, p.padded);
     return e == cudaSuccess ? take_matrix<T>(w, a.w, a.w_stride, a.vocab, a.dim, p.w, stream) : e;
@@ -313,8 +332,8 @@ template <typename T> cudaError_t vocab_forward(const VocabArgs& a, void* ws, cu
     epi.part = p.part;
     epi.picked = p.picked;
     epi.lists = {p.index, p.q, p.map, a.k};
-    epi.n = a.vocab;
-    epi.rows = a.rows;
+    epi.n = (int32_t)a.vocab;
+    epi.row_stride = a.rows;
     epi.scale = 1.0f / a.temperature;
     TcArgs g = {};
     g.m = a.rows;
@@ -336,7 +355,7 @@ template <typename T> cudaError_t vocab_forward(const VocabArgs& a, void* ws, cu
     j.strips = (a.vocab + kStrip - 1) / kStrip;
     j.k = a.k;
     j.temperature = a.temperature;
-    return launch_after(vocab_join_kernel, dim3(blocks_of(a.rows, kListThreads / 32, 4096)), dim3(kListThreads), 0, stream, j);
+    return launch_after(vocab_join_kernel, dim3(blocks_of(a.rows, 32, 4096)), dim3(kJoinThreads), 0, stream, j);
 }
 
 template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, cudaStream_t stream)
@@ -346,7 +365,7 @@ template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, c
     Matrix x, w;
     cudaError_t e = vocab_rows<T>(a, p, &x, &w, stream);
     if (a.dx && e == cudaSuccess)
-        e = launch_after(vocab_zero_kernel<T>, dim3(blocks_of(a.rows, 1, 4096)), dim3(kZeroThreads), 0, stream, static_cast<T*>(a.dx),
+        e = launch_after(vocab_zero_kernel<T>, dim3(blocks_of(a.rows, kZeroThreads / 32, 1216)), dim3(kZeroThreads), 0, stream, static_cast<T*>(a.dx),
                          a.dx_stride, (const float*)p.given, a.rows, a.dim);
     EpiGradient<T> grad = {};
     grad.dz = p.dz;
@@ -356,15 +375,15 @@ template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, c
     grad.given = p.given;
     grad.stride = p.dz_stride;
     grad.plane = p.padded * p.dz_stride;
-    grad.rows = p.padded;
+    grad.room = (int32_t)p.padded;
     grad.dloss_stride = a.dloss_stride;
     grad.scale = 1.0f / a.temperature;
     grad.temperature = a.temperature;
     for (int64_t at = 0; at < a.vocab && e == cudaSuccess; at += p.piece) {
         const int64_t n = a.vocab - at < p.piece ? a.vocab - at : p.piece;
         const Matrix here = {w.p + at * w.stride, n, a.dim, w.stride, w.plane}, dz = {p.dz, p.padded, n, p.dz_stride, grad.plane};
-        grad.n = n;
-        grad.first = at;
+        grad.n = (int32_t)n;
+        grad.first = (int32_t)at;
         TcArgs g = {};
         g.m = a.rows;
         g.n = n;
@@ -378,7 +397,7 @@ template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, c
             store.map = p.map;
             store.stride = a.dx_stride;
             store.acc_stride = round_up(a.dim, 4);
-            store.n = a.dim;
+            store.n = (int32_t)a.dim;
             store.first = at == 0;
             store.last = at + n == a.vocab;
             store.whole = whole_rows(a.dx, a.dx_stride, a.rows, sizeof(T));
@@ -390,7 +409,7 @@ template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, c
             EpiStore<T> store = {};
             store.out = static_cast<T*>(a.dw) + at * a.dw_stride;
             store.stride = a.dw_stride;
-            store.n = a.dim;
+            store.n = (int32_t)a.dim;
             store.first = store.last = true;
             store.whole = whole_rows(a.dw, a.dw_stride, a.vocab, sizeof(T));
             g = {};
@@ -410,13 +429,13 @@ template <typename T> cudaError_t zero_rows(const VocabArgs& a, cudaStream_t str
     EpiStore<T> store = {};
     store.out = static_cast<T*>(a.dw);
     store.stride = a.dw_stride;
-    store.n = a.dim;
+    store.n = (int32_t)a.dim;
     store.first = store.last = true;
     store.whole = whole_rows(a.dw, a.dw_stride, a.vocab, sizeof(T));
     return product_none<T>(a.vocab, a.dim, store, stream);
 }
 
-constexpr int64_t kMostDim = (int64_t)1 << 30, kMostRows = (int64_t)1 << 31;
+constexpr int64_t kMostDim = (int64_t)1 << 30, kMostRows = ((int64_t)1 << 30) + 1;
 
 // What both losses and both passes ask of their arguments.
 adacomp_status vocab_check(adacomp_vocab_t h, const VocabArgs& a, const void* ws)
