@@ -2,6 +2,7 @@
 #include <initializer_list>
 #include <new>
 
+#include "product_few.cuh"
 #include "product_tc.cuh"
 
 struct adacomp_linear {
@@ -15,6 +16,7 @@ namespace {
 constexpr int kDzCols = 256, kDzRows = 8;  // of a CTA: a warp has 256 columns of a row
 constexpr int kDzSlices = 152;             // partial sums of db: one per slice of the rows
 constexpr int kDbCols = 32, kDbRows = 16;
+constexpr int64_t kOneSlice = 128;         // rows that one slice has, without a second kernel
 
 struct LinearArgs {
     int64_t rows, in, out;
@@ -46,13 +48,22 @@ LinearParts linear_parts(Carve& c, int64_t rows, int64_t in, int64_t out, int by
     return p;
 }
 
+// Which products are for the kernel of small matrices. us with it and without: fp32 256 x 512 x 512 12 and 21, 512 x 512 x 512
+// 21 and 21; bf16 256 x 256 x 256 8 and 10, 256 x 512 x 512 14 and 12.
+template <typename T> bool is_small(int64_t rows, int64_t in, int64_t out)
+{
+    constexpr int64_t most = (int64_t)1 << (sizeof(T) == 4 ? 26 : 24);
+    return rows * in <= most && rows * in * out <= most;
+}
+
 struct DzArgs {
     const void *dy, *pre;
-    bf16* dz;
+    void* dz;       // planes of bf16 numbers, or (plain) T's
+    void* db;       // of one slice alone
     float* sums;
     int64_t rows, n, dy_stride, pre_stride, dz_stride, dz_plane;
     int32_t act, slices;
-    bool dy_whole, pre_whole;
+    bool plain, dy_whole, pre_whole;
 };
 
 // dz = dy * act'(pre), and its sums over slices of the rows. Bound by memory: a thread has eight columns of every
@@ -71,7 +82,8 @@ template <typename T, int kAct> __device__ __forceinline__ void dz_rows(const Dz
             get_chunk(pre + r * a.pre_stride, z, left, a.pre_whole);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] *= slope<T, kAct>(z[j]);
-            if (a.dz) put_parts<T>(a.dz + r * a.dz_stride + c, a.dz_plane, v, left);
+            if (a.dz && a.plain) put_chunk(static_cast<T*>(a.dz) + r * a.dz_stride + c, v, left, true);
+            else if (a.dz) put_parts<T>(static_cast<bf16*>(a.dz) + r * a.dz_stride + c, a.dz_plane, v, left);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] += v[j];
@@ -91,7 +103,7 @@ template <typename T> __global__ void __launch_bounds__(kDzCols / 8 * kDzRows) l
         case ADACOMP_ACT_SILU: dz_rows<T, ADACOMP_ACT_SILU>(a, c, sum); break;
         default: dz_rows<T, ADACOMP_ACT_NONE>(a, c, sum);
         }
-    if (!a.sums) return;
+    if (!a.sums && !a.db) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sums[threadIdx.y][threadIdx.x * 8 + j] = sum[j];
     __syncthreads();
@@ -101,7 +113,8 @@ template <typename T> __global__ void __launch_bounds__(kDzCols / 8 * kDzRows) l
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < kDzRows; ++j) s += sums[j][i];
-    a.sums[blockIdx.y * a.n + at] = s;
+    if (a.db) static_cast<T*>(a.db)[at] = from_f32<T>(s);
+    else a.sums[blockIdx.y * a.n + at] = s;
 }
 
 template <typename T> __global__ void __launch_bounds__(kDbCols * kDbRows) linear_db_kernel(const float* part, T* db, int64_t n, int32_t slices)
@@ -138,24 +151,25 @@ template <typename T> cudaError_t linear_forward(const LinearArgs& a, void* ws, 
     epi.pre_whole = whole_rows(a.pre, a.pre_stride, a.rows, sizeof(T));
     epi.bias_whole = is_aligned(a.bias, 16);
     epi.residual_whole = whole_rows(a.residual, a.residual_stride, a.rows, sizeof(T));
+    if (a.rows <= (sizeof(T) == 2 ? kFewBf16 : kFewF32))
+        return product_few<T>(FewArgs{a.x, a.w, a.x_stride, a.w_stride, (int32_t)a.rows, (int32_t)a.out, (int32_t)a.in}, epi, stream);
+    if (is_small<T>(a.rows, a.in, a.out))
+        return product_small<T>(SmallArgs{{a.x, a.x_stride, 1}, {a.w, a.w_stride, 1}, (int32_t)a.rows, (int32_t)a.out, (int32_t)a.in}, epi, stream);
     Carve carve{static_cast<char*>(ws)};
     const LinearParts p = linear_parts(carve, a.rows, a.in, a.out, sizeof(T), false);
     Matrix x, w;
     cudaError_t e = take_matrix<T>(&x, a.x, a.x_stride, a.rows, a.in, p.x, stream);
     if (e == cudaSuccess) e = take_matrix<T>(&w, a.w, a.w_stride, a.out, a.in, p.w, stream);
     if (e != cudaSuccess) return e;
-    TcArgs g = {};
-    g.m = a.rows;
-    g.n = a.out;
-    g.k = a.in;
-    return product_tc<T>(x, false, w, false, g, p.parts, epi, stream);
+    const TcProduct product = {x, w, false, false, a.rows, a.out, a.in, nullptr, nullptr};
+    return product_tc<T>(product, p.parts, epi, stream);
 }
 
 template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws, cudaStream_t stream)
 {
     Carve carve{static_cast<char*>(ws)};
     const LinearParts p = linear_parts(carve, a.rows, a.in, a.out, sizeof(T), true);
-    const bool act = a.act != ADACOMP_ACT_NONE, products = a.dx || a.dw;
+    const bool act = a.act != ADACOMP_ACT_NONE, products = a.dx || a.dw, small = is_small<T>(a.rows, a.in, a.out);
     cudaError_t e = cudaSuccess;
     Matrix dz = {p.dz, a.rows, a.out, round_up(a.out, 8), a.rows * round_up(a.out, 8)}, x, w;
     if ((act && products) || a.db) {
@@ -171,48 +185,52 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
         d.dz_stride = dz.stride;
         d.dz_plane = dz.plane;
         d.act = a.act;
+        d.plain = small;
         d.dy_whole = whole_rows(a.dy, a.dy_stride, a.rows, sizeof(T));
         d.pre_whole = whole_rows(a.pre_in, a.pre_in_stride, a.rows, sizeof(T));
         // CTAs for eight on each SM, of no fewer than two rows a thread
         const int64_t blocks = (a.out + kDzCols - 1) / kDzCols, most = (a.rows + 2 * kDzRows - 1) / (2 * kDzRows);
         int64_t slices = 8 * kDzSlices / blocks;
         slices = slices < 1 ? 1 : slices < kDzSlices ? slices : kDzSlices;
-        d.slices = (int32_t)(slices < most ? slices : most);
-        if (d.slices)
-            e = launch_after(linear_dz_kernel<T>, dim3((unsigned)blocks, d.slices), dim3(kDzCols / 8, kDzRows), 0, stream, d);
-        if (e == cudaSuccess && a.db)
+        d.slices = (int32_t)(a.rows <= kOneSlice ? 1 : slices < most ? slices : most);
+        if (d.slices == 1 || a.rows == 0) {
+            d.db = a.db;
+            d.sums = nullptr;
+        }
+        e = launch_after(linear_dz_kernel<T>, dim3((unsigned)blocks, d.slices), dim3(kDzCols / 8, kDzRows), 0, stream, d);
+        if (e == cudaSuccess && a.db && !d.db)
             e = launch_after(linear_db_kernel<T>, dim3((unsigned)((a.out + kDbCols - 1) / kDbCols)), dim3(kDbCols, kDbRows), 0, stream,
                              (const float*)p.sums, static_cast<T*>(a.db), a.out, d.slices);
     }
-    if (e == cudaSuccess && !act && products) e = take_matrix<T>(&dz, a.dy, a.dy_stride, a.rows, a.out, p.dz, stream);
-    TcArgs g = {};
-    EpiStore<T> epi = {};
-    epi.first = epi.last = true;
-    if (a.dx && a.rows && e == cudaSuccess) {
-        e = take_matrix<T>(&w, a.w, a.w_stride, a.out, a.in, p.w, stream);
-        if (e != cudaSuccess) return e;
-        g.m = a.rows;
-        g.n = a.in;
+    if (e != cudaSuccess) return e;
+    const auto store = [&](void* out, int64_t stride, int64_t rows) {
+        EpiStore<T> epi = {};
+        epi.out = static_cast<T*>(out);
+        epi.stride = stride;
         epi.n = (int32_t)a.in;
-        g.k = a.out;
-        epi.out = static_cast<T*>(a.dx);
-        epi.stride = a.dx_stride;
-        epi.whole = whole_rows(a.dx, a.dx_stride, a.rows, sizeof(T));
-        e = product_tc<T>(dz, false, w, true, g, p.parts, epi, stream);
+        epi.first = epi.last = true;
+        epi.whole = whole_rows(out, stride, rows, sizeof(T));
+        return epi;
+    };
+    const EpiStore<T> to_dx = store(a.dx, a.dx_stride, a.rows), to_dw = store(a.dw, a.dw_stride, a.out);
+    if (a.rows == 0) return a.dw ? product_none<T>(a.out, a.in, to_dw, stream) : cudaSuccess;
+    const int32_t rows = (int32_t)a.rows, in = (int32_t)a.in, out = (int32_t)a.out;
+    if (small) {
+        const Operand by_row = act ? Operand{p.dz, dz.stride, 1} : Operand{a.dy, a.dy_stride, 1};
+        if (a.dx) e = product_small<T>(SmallArgs{by_row, {a.w, 1, a.w_stride}, rows, in, out}, to_dx, stream);
+        if (a.dw && e == cudaSuccess)
+            e = product_small<T>(SmallArgs{{by_row.p, 1, by_row.row}, {a.x, 1, a.x_stride}, out, in, rows}, to_dw, stream);
+        return e;
     }
-    if (a.dw && e == cudaSuccess) {
-        g.m = a.out;
-        g.n = a.in;
-        epi.n = (int32_t)a.in;
-        g.k = a.rows;
-        epi.out = static_cast<T*>(a.dw);
-        epi.stride = a.dw_stride;
-        epi.whole = whole_rows(a.dw, a.dw_stride, a.out, sizeof(T));
-        if (a.rows == 0) return product_none<T>(g.m, g.n, epi, stream);
-        e = take_matrix<T>(&x, a.x, a.x_stride, a.rows, a.in, p.x, stream);
-        if (e == cudaSuccess) e = product_tc<T>(dz, true, x, true, g, p.parts, epi, stream);
-    }
-    return e;
+    if (!act && products) e = take_matrix<T>(&dz, a.dy, a.dy_stride, a.rows, a.out, p.dz, stream);
+    if (a.dx && e == cudaSuccess) e = take_matrix<T>(&w, a.w, a.w_stride, a.out, a.in, p.w, stream);
+    if (a.dw && e == cudaSuccess) e = take_matrix<T>(&x, a.x, a.x_stride, a.rows, a.in, p.x, stream);
+    if (e != cudaSuccess) return e;
+    const TcProduct dx = {dz, w, false, true, a.rows, a.in, a.out, nullptr, nullptr};
+    const TcProduct dw = {dz, x, true, true, a.out, a.in, a.rows, nullptr, nullptr};
+    if (a.dx && a.dw) return product_tc_both<T>(dx, to_dx, dw, to_dw, p.parts, stream);
+    if (a.dx) return product_tc<T>(dx, p.parts, to_dx, stream);
+    return a.dw ? product_tc<T>(dw, p.parts, to_dw, stream) : cudaSuccess;
 }
 
 constexpr int64_t kMostDim = (int64_t)1 << 30, kMostRows = ((int64_t)1 << 30) + 1;

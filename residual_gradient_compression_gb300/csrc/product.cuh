@@ -7,7 +7,8 @@
 // what it reads and writes in global memory are whole pieces of rows (a thread that writes its own row takes 32 cache
 // lines at a time: a linear layer's forward product of 8192 x 2048 x 16384 bf16 took 369 us so, and 313 without its
 // stores). kExact: the results are held in fp32, so the sums are formed in short runs.
-// kPieces: a thread may also hand over four columns on their own, piece().
+// kPieces: a thread may also hand over four columns on their own, piece(). kAdds: there may be a matrix that
+// the sums are added to, which take() loads before they are there.
 #pragma once
 
 #include "train_common.cuh"
@@ -239,7 +240,7 @@ template <typename T, int kKind> __device__ __forceinline__ float slope(float z)
 // ---------------------------------------------------------------- epilogues
 // y = act(sum + bias) + residual, and the value before the activation.
 template <typename T> struct EpiLinear {
-    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true;
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kAdds = false;
     T *y, *pre;
     const T *bias, *residual;
     int64_t y_stride, pre_stride, residual_stride;
@@ -303,7 +304,7 @@ template <typename T> struct EpiLinear {
         }
     }
 
-    __device__ __forceinline__ void chunk(const Stage& stage, int32_t r0, int32_t end, int32_t c) const
+    __device__ __forceinline__ void chunk(const Stage& stage, const State&, int32_t r0, int32_t end, int32_t c) const
     {
         with_act([&](auto f) { turns(stage, r0, end, c, f); });
     }
@@ -323,15 +324,18 @@ template <typename T> struct EpiLinear {
 // The sums themselves, in rows that `map` may move; with acc, added up over several products in
 // fp32 (first: nothing to add to yet) and rounded by the last one only.
 template <typename T> struct EpiStore {
-    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true;
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kAdds = true;
     T* out;
     float* acc;
     const int32_t* map;
     int64_t stride, acc_stride, split_stride;  // split_stride: between the parts of a product whose terms are split
     int32_t n;
     bool first, last, whole;
-    struct State {};
-    __device__ __forceinline__ State begin(int32_t, int32_t) const { return {}; }
+    struct State {
+        int32_t to;
+    };
+    __device__ __forceinline__ State begin(int32_t r, int32_t) const { return {map ? map[r] : r}; }
+    __device__ __forceinline__ bool adds() const { return !first; }
     __device__ __forceinline__ void rows(const State&, int32_t, int32_t, bool, float (&)[kStrip]) const {}
 
     __device__ __forceinline__ EpiStore of_split(int split) const
@@ -341,7 +345,7 @@ template <typename T> struct EpiStore {
         return e;
     }
 
-    __device__ __forceinline__ void chunk(const Stage& stage, int32_t r0, int32_t end, int32_t c0) const
+    __device__ __forceinline__ void take(const Stage& stage, int32_t r0, int32_t end, int32_t c0) const
     {
         const int lane = threadIdx.x & 31, piece = lane & 7, at = lane / 8;
         const int32_t c = c0 + piece * 4, left = n - c;
@@ -349,15 +353,23 @@ template <typename T> struct EpiStore {
 #pragma unroll
         for (int i = 0; i < kTurns; ++i) {
             const int32_t r = r0 + i * 4 + at;
-            v[i] = stage.at(i * 4 + at, piece);
-            if (!first) v[i] = v[i] + get4(acc + r * acc_stride + c, r < end ? left : 0, true);
+            v[i] = get4(acc + r * acc_stride + c, r < end ? left : 0, true);
         }
 #pragma unroll
+        for (int i = 0; i < kTurns; ++i) stage.at(i * 4 + at, piece) = v[i];
+    }
+
+    __device__ __forceinline__ void chunk(const Stage& stage, const State& s, int32_t r0, int32_t end, int32_t c0) const
+    {
+        const int lane = threadIdx.x & 31, piece = lane & 7, at = lane / 8;
+        const int32_t c = c0 + piece * 4, left = n - c;
+#pragma unroll
         for (int i = 0; i < kTurns; ++i) {
-            const int32_t r = r0 + i * 4 + at;
+            const int32_t r = r0 + i * 4 + at, to = __shfl_sync(0xffffffffu, s.to, i * 4 + at);
             if (r >= end) continue;
-            if (last) put4(out + (map ? map[r] : r) * stride + c, v[i], left, whole);
-            else put4(acc + r * acc_stride + c, v[i], left, true);
+            const float4 v = stage.at(i * 4 + at, piece);
+            if (last) put4(out + to * stride + c, v, left, whole);
+            else put4(acc + r * acc_stride + c, v, left, true);
         }
     }
 
@@ -423,7 +435,7 @@ __device__ __forceinline__ int32_t next_token(const Lists& l, const Place& p, in
 // Of each strip of 128 logits of a row: their maximum and the sum of exp(z - maximum); and the logits
 // of the listed tokens.
 template <typename T> struct EpiSoftmax {
-    static constexpr bool kExact = true, kChunks = false, kPieces = false;
+    static constexpr bool kExact = true, kChunks = false, kPieces = false, kAdds = false;
     float2* part;  // [strips][row_stride]
     float* picked;
     Lists lists;
@@ -458,13 +470,13 @@ template <typename T> struct EpiSoftmax {
         for (int i = 0; i < kStrip; ++i) sum[i & 3] += exp_of<T>(v[i] - less);
         part[c / kStrip * row_stride + r] = make_float2(top[0], (sum[0] + sum[1]) + (sum[2] + sum[3]));
     }
-    __device__ __forceinline__ void chunk(const Stage&, int32_t, int32_t, int32_t) const {}
+    __device__ __forceinline__ void chunk(const Stage&, const State&, int32_t, int32_t, int32_t) const {}
 };
 
 // The logits' gradient (p - q) * dloss * temperature of columns first .. first + n - 1: rounded to
 // bf16, or, of fp32 operands, in parts. Rows past the last one, up to a tile's end, are zeros: they are terms of a product.
 template <typename T> struct EpiGradient {
-    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = false;
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = false, kAdds = false;
     bf16* dz;  // [planes][room][stride]
     Lists lists;
     const float *lse, *dloss, *given;
@@ -499,7 +511,7 @@ template <typename T> struct EpiGradient {
 #pragma unroll
         for (int i = 0; i < kStrip; ++i) v[i] *= s.factor;
     }
-    __device__ __forceinline__ void chunk(const Stage& stage, int32_t r0, int32_t, int32_t c0) const
+    __device__ __forceinline__ void chunk(const Stage& stage, const State&, int32_t r0, int32_t, int32_t c0) const
     {
         const int lane = threadIdx.x & 31, piece = lane & 7, at = lane / 8;
         const int32_t c = c0 + piece * 4, left = n - c;

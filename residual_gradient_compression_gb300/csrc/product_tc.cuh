@@ -212,10 +212,95 @@ __device__ __forceinline__ int plane_a(int pass) { return (0x231130 >> 4 * (5 - 
 __device__ __forceinline__ int plane_b(int pass) { return (0x321310 >> 4 * (5 - pass)) & 15; }
 
 // ---------------------------------------------------------------- kernel
-template <int kN, bool kSplit, typename Epi>
+enum TcMode { kTcOne, kTcSplit, kTcBoth };
+
+// One product, one whose terms are split, or two products at once, of which the first has the longer sums.
+struct TcMaps {
+    CUtensorMap a[2], b[2];
+};
+
+template <typename Epi> struct TcParams {
+    TcArgs g[2];
+    Epi epi[2];
+};
+
+// What a pair of CTAs does: its i-th tile. Of one product: every pairs-th. Of two: the first one's tiles in the same way,
+// then of the second one's so many that all pairs have about as much to do: those with a tile more of the first product
+// (the first `more` pairs) `few` of them, the others `many`.
+struct TcUnit {
+    int32_t m0, n0, from, count, split, which;
+};
+
+template <int kN, int kMode> struct TcSchedule {
+    int32_t m[2], n[2], tiles_m[2], tiles_n[2], blocks[2], group[2], splits, per_split, pairs, pair;
+    int64_t tiles[2], more, few, many, mine;  // mine: of the first product
+
+    __device__ __forceinline__ TcSchedule(const TcArgs (&g)[2])
+    {
+        pairs = gridDim.x / 2;
+        pair = blockIdx.x / 2;
+#pragma unroll
+        for (int i = 0; i < (kMode == kTcBoth ? 2 : 1); ++i) {
+            m[i] = (int32_t)(g[i].m_count ? *g[i].m_count : g[i].m);
+            n[i] = (int32_t)g[i].n;
+            const int32_t terms = (int32_t)(g[i].k_count ? *g[i].k_count : g[i].k);
+            tiles_m[i] = (m[i] + kTcM - 1) / kTcM;
+            tiles_n[i] = (n[i] + kN - 1) / kN;
+            blocks[i] = (terms + kTcDepth - 1) / kTcDepth;
+            group[i] = g[i].group;
+            tiles[i] = (int64_t)tiles_m[i] * tiles_n[i];
+        }
+        splits = kMode == kTcSplit ? g[0].splits : 1;
+        per_split = (blocks[0] + splits - 1) / splits;
+        if constexpr (kMode == kTcBoth) {
+            const int64_t a = blocks[0], b = blocks[1] > 0 ? blocks[1] : 1, each = tiles[0] / pairs;
+            more = tiles[0] - each * pairs;
+            mine = each + (pair < more);
+            for (int64_t t = (a * tiles[0] + b * tiles[1] + pairs - 1) / pairs;; t += b) {
+                few = t > a * (each + 1) ? (t - a * (each + 1)) / b : 0;
+                many = t > a * each ? (t - a * each) / b : 0;
+                if (more * few + (pairs - more) * many >= tiles[1]) break;
+            }
+        }
+    }
+
+    __device__ __forceinline__ bool at(int64_t i, TcUnit& t) const
+    {
+        int64_t tile = pair + i * pairs;
+        t.which = 0;
+        t.split = 0;
+        if constexpr (kMode == kTcSplit) {
+            if (tile >= tiles[0] * splits) return false;
+            t.split = (int32_t)(tile / tiles[0]);
+            tile -= t.split * tiles[0];
+        } else if constexpr (kMode == kTcBoth) {
+            if (i >= mine) {
+                const int64_t j = i - mine;
+                t.which = 1;
+                if (j >= (pair < more ? few : many)) return false;
+                tile = pair < more ? j * more + pair : more * few + j * (pairs - more) + (pair - more);
+                if (tile >= tiles[1]) return false;
+            }
+        } else {
+            if (tile >= tiles[0]) return false;
+        }
+        const int w = kMode == kTcBoth ? t.which : 0;
+        const int32_t tm = w ? tiles_m[1] : tiles_m[0], tn = w ? tiles_n[1] : tiles_n[0], gr = w ? group[1] : group[0];
+        const int64_t whole = (int64_t)gr * tn;
+        const int32_t band = (int32_t)(tile / whole), in = (int32_t)(tile - band * whole);
+        const int32_t rows = tm - band * gr < gr ? tm - band * gr : gr;
+        t.n0 = in / rows * kN;
+        t.m0 = (band * gr + in % rows) * kTcM;
+        t.from = t.split * per_split;
+        t.count = w ? blocks[1] : blocks[0] - t.from < per_split ? blocks[0] - t.from : per_split;
+        if (t.count < 0) t.count = 0;
+        return true;
+    }
+};
+
+template <int kN, int kMode, typename Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
-    product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const TcArgs g,
-                      const Epi epi)
+    product_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcParams<Epi> params)
 {
     using Shape = TcShape<kN>;
     constexpr int kStages = Shape::kStages;
@@ -240,8 +325,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         ptx::mbar_init(&drained, 1);
         dead_flag = 0;
         ptx::fence_mbar_init();
-        tc::prefetch(&map_a);
-        tc::prefetch(&map_b);
+#pragma unroll
+        for (int i = 0; i < (kMode == kTcBoth ? 2 : 1); ++i) {
+            tc::prefetch(&maps.a[i]);
+            tc::prefetch(&maps.b[i]);
+        }
     }
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_addr(&tmem_at)), "r"(512)
@@ -254,28 +342,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     tc::fence_after();
     const uint32_t tmem = tmem_at;
     ptx::griddep_wait();
-
-    const int32_t m = (int32_t)(g.m_count ? *g.m_count : g.m), terms = (int32_t)(g.k_count ? *g.k_count : g.k), n = (int32_t)g.n;
-    const int32_t tiles_m = (m + kTcM - 1) / kTcM, tiles_n = (n + kN - 1) / kN;
-    const int32_t blocks = (terms + kTcDepth - 1) / kTcDepth, per_split = (blocks + g.splits - 1) / g.splits;
-    const int passes = g.planes == 1 ? 1 : 6;
-    const int64_t tiles = (int64_t)tiles_m * tiles_n, units = tiles * g.splits, first = blockIdx.x / 2, step = gridDim.x / 2;
-    struct Unit {
-        int32_t m0, n0, from, count, split;
-    };
-    const auto unit_of = [&](int64_t u) {
-        Unit t;
-        t.split = (int32_t)(u / tiles);
-        const int64_t tile = u - t.split * tiles, whole = (int64_t)g.group * tiles_n;
-        const int32_t band = (int32_t)(tile / whole), in = (int32_t)(tile - band * whole);
-        const int32_t rows = tiles_m - band * g.group < g.group ? tiles_m - band * g.group : g.group;
-        t.n0 = in / rows * kN;
-        t.m0 = (band * g.group + in % rows) * kTcM;
-        t.from = t.split * per_split;
-        t.count = blocks - t.from < per_split ? blocks - t.from : per_split;
-        if (t.count < 0) t.count = 0;
-        return t;
-    };
+    const TcSchedule<kN, kMode> schedule(params.g);
+    TcUnit t;
 
     // 384 threads of 168 registers: 128 with 40 and 256 with 232 are as many
     if (warp < kTcEpilogue) {
@@ -284,8 +352,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             uint32_t at_stage = 0, turn = 0, issued = 0;
             const uint32_t full_at = tc::map_shared(full, 0);  // the first CTA's
             bool alive = true;
-            for (int64_t u = first; u < units && alive; u += step) {
-                const Unit t = unit_of(u);
+            for (int64_t u = 0; alive && schedule.at(u, t); ++u) {
+                const TcArgs& g = params.g[kMode == kTcBoth ? t.which : 0];
+                const CUtensorMap *map_a = &maps.a[kMode == kTcBoth ? t.which : 0], *map_b = &maps.b[kMode == kTcBoth ? t.which : 0];
+                const int passes = g.planes == 1 ? 1 : 6;
                 const int32_t ma = t.m0 + (int32_t)rank * 128, nb = t.n0 + (int32_t)rank * (kN / 2);
                 for (int32_t from = 0; from < t.count && alive; from += g.run) {
                     const int32_t end = t.count - from < g.run ? t.count : from + g.run;
@@ -300,15 +370,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                                 if (rank == 0) ptx::mbar_arrive_expect_tx(&full[at_stage], 2 * (Shape::kA + Shape::kB));
                                 if (g.a_mn) {
 #pragma unroll
-                                    for (int i = 0; i < 2; ++i) tc::load(at + i * 8192, &map_a, ma + 64 * i, k0, pa, bar);
+                                    for (int i = 0; i < 2; ++i) tc::load(at + i * 8192, map_a, ma + 64 * i, k0, pa, bar);
                                 } else {
-                                    tc::load(at, &map_a, k0, ma, pa, bar);
+                                    tc::load(at, map_a, k0, ma, pa, bar);
                                 }
                                 if (g.b_mn) {
 #pragma unroll
-                                    for (int i = 0; i < kN / 128; ++i) tc::load(at + Shape::kA + i * 8192, &map_b, nb + 64 * i, k0, pb, bar);
+                                    for (int i = 0; i < kN / 128; ++i) tc::load(at + Shape::kA + i * 8192, map_b, nb + 64 * i, k0, pb, bar);
                                 } else {
-                                    tc::load(at + Shape::kA, &map_b, k0, nb, pb, bar);
+                                    tc::load(at + Shape::kA, map_b, k0, nb, pb, bar);
                                 }
                             }
                             ++issued;
@@ -328,16 +398,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 }
             }
         } else if (warp == 1 && rank == 0) {  // products
-            const uint32_t kind = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(g.a_mn != 0) << 15 | (uint32_t)(g.b_mn != 0) << 16 |
-                                  (uint32_t)(kN / 8) << 17 | (uint32_t)(kTcM / 16) << 24;
-            // 16 terms further: 32 bytes along a line, or 16 lines
-            const uint32_t step_a = (g.a_mn ? 2048 : 32) >> 4, step_b = (g.b_mn ? 2048 : 32) >> 4;
-            const uint64_t first_a = tc::descriptor(base, g.a_mn ? 8192 : 16, 1024);
-            const uint64_t first_b = tc::descriptor(base + Shape::kA, g.b_mn ? 8192 : 16, 1024);
             uint32_t at_stage = 0, turn = 0, done = 0;
             bool alive = true;
-            for (int64_t u = first; u < units && alive; u += step) {
-                const Unit t = unit_of(u);
+            for (int64_t u = 0; alive && schedule.at(u, t); ++u) {
+                const TcArgs& g = params.g[kMode == kTcBoth ? t.which : 0];
+                const int passes = g.planes == 1 ? 1 : 6;
+                const uint32_t kind = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(g.a_mn != 0) << 15 | (uint32_t)(g.b_mn != 0) << 16 |
+                                      (uint32_t)(kN / 8) << 17 | (uint32_t)(kTcM / 16) << 24;
+                // 16 terms further: 32 bytes along a line, or 16 lines
+                const uint32_t step_a = (g.a_mn ? 2048 : 32) >> 4, step_b = (g.b_mn ? 2048 : 32) >> 4;
+                const uint64_t first_a = tc::descriptor(base, g.a_mn ? 8192 : 16, 1024);
+                const uint64_t first_b = tc::descriptor(base + Shape::kA, g.b_mn ? 8192 : 16, 1024);
                 for (int32_t from = 0; from < t.count && alive; from += g.run) {
                     const int buffer = (int)(done & 1);
                     alive = __all_sync(0xffffffffu, tc::wait(&sums_empty[buffer], (done / 2 & 1) ^ 1, dead));
@@ -378,14 +449,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const uint32_t freed[2] = {tc::map_shared(&sums_empty[0], 0), tc::map_shared(&sums_empty[1], 0)};
         uint32_t done = 0;
         bool alive = true;
-        for (int64_t u = first; u < units; u += step) {
-            const Unit t = unit_of(u);
+        for (int64_t u = 0; schedule.at(u, t); ++u) {
+            const TcArgs& g = params.g[kMode == kTcBoth ? t.which : 0];
+            const Epi& epi = params.epi[kMode == kTcBoth ? t.which : 0];
+            const int32_t m = kMode == kTcBoth && t.which ? schedule.m[1] : schedule.m[0], n = (int32_t)g.n;
             const int32_t r = t.m0 + (int32_t)rank * 128 + quarter * 32 + lane, c0 = t.n0 + strip * kStrip;
             typename Epi::State state = {};
             if (r < m && c0 < n) state = epi.begin(r, c0);
             float v[kStrip];
 #pragma unroll
             for (int i = 0; i < kStrip; ++i) v[i] = 0.0f;
+            if constexpr (Epi::kAdds) {
+                if (epi.adds()) {  // what the sums are added to, while they are computed
+#pragma unroll
+                    for (int c = 0; c < kStrip; c += 32) {
+                        if (c0 + c >= n) break;
+                        epi.take(stage, r - lane, m, c0 + c);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 more = stage.at(lane, i);
+                            v[c + 4 * i] = more.x, v[c + 4 * i + 1] = more.y, v[c + 4 * i + 2] = more.z, v[c + 4 * i + 3] = more.w;
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
 #pragma unroll 1
             for (int32_t from = 0; from < t.count; from += g.run, ++done) {
                 const int buffer = (int)(done & 1);
@@ -418,8 +507,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) stage.at(lane, i) = make_float4(v[c + 4 * i], v[c + 4 * i + 1], v[c + 4 * i + 2], v[c + 4 * i + 3]);
                     __syncwarp();
-                    if constexpr (kSplit) epi.of_split(t.split).chunk(stage, r - lane, m, c0 + c);
-                    else epi.chunk(stage, r - lane, m, c0 + c);
+                    if constexpr (kMode == kTcSplit) epi.of_split(t.split).chunk(stage, state, r - lane, m, c0 + c);
+                    else epi.chunk(stage, state, r - lane, m, c0 + c);
                     __syncwarp();
                 }
             }
@@ -534,19 +623,48 @@ cudaError_t take_matrix(Matrix* out, const void* p, int64_t stride, int64_t rows
     return launch_after(pack_kernel<T>, dim3((unsigned)(need < most ? need : most)), dim3(kTcPack), 0, stream, a);
 }
 
-template <int kN, bool kSplit, typename Epi>
-cudaError_t product_tc_n(const Matrix& a, const Matrix& b, const TcArgs& g, const Epi& epi, cudaStream_t stream)
+template <int kN, int kMode, typename Epi>
+cudaError_t launch_tc(const TcMaps& maps, const TcParams<Epi>& p, cudaStream_t stream)
 {
-    CUtensorMap map_a, map_b;
-    cudaError_t e = tensor_map(&map_a, a, g.planes, g.a_mn ? kTcDepth : 128);
-    if (e == cudaSuccess) e = tensor_map(&map_b, b, g.planes, g.b_mn ? kTcDepth : kN / 2);
-    if (e == cudaSuccess) e = allow<product_tc_kernel<kN, kSplit, Epi>>(TcShape<kN>::kShared);
+    cudaError_t e = allow<product_tc_kernel<kN, kMode, Epi>>(TcShape<kN>::kShared);
     int sms = 0;
     if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const int64_t units = (g.m + kTcM - 1) / kTcM * ((g.n + kN - 1) / kN) * g.splits, pairs = sms / 2;
-    return launch_after(product_tc_kernel<kN, kSplit, Epi>, dim3((unsigned)(2 * (units < pairs ? units : pairs))), dim3(kTcThreads),
-                        TcShape<kN>::kShared, stream, map_a, map_b, g, epi);
+    int64_t units = 0;
+    for (int i = 0; i < (kMode == kTcBoth ? 2 : 1); ++i)
+        units += (p.g[i].m + kTcM - 1) / kTcM * ((p.g[i].n + kN - 1) / kN) * (kMode == kTcSplit ? p.g[i].splits : 1);
+    const int64_t pairs = sms / 2;
+    return launch_after(product_tc_kernel<kN, kMode, Epi>, dim3((unsigned)(2 * (units < pairs ? units : pairs))), dim3(kTcThreads),
+                        TcShape<kN>::kShared, stream, maps, p);
+}
+
+// A product's operands. a_mn, b_mn: the matrix lies by terms (its rows are terms).
+struct TcProduct {
+    Matrix a, b;
+    bool a_mn, b_mn;
+    int64_t m, n, k;
+    const int32_t *m_count, *k_count;
+};
+
+template <typename T, typename Epi> cudaError_t set_tc(TcMaps& maps, TcParams<Epi>& p, int i, const TcProduct& x, const Epi& epi)
+{
+    constexpr int kN = 256;
+    TcArgs g = {};
+    g.m = x.m;
+    g.n = x.n;
+    g.k = x.k;
+    g.m_count = x.m_count;
+    g.k_count = x.k_count;
+    g.planes = sizeof(T) == 4 ? kPlanes : 1;
+    g.splits = 1;
+    g.a_mn = x.a_mn;
+    g.b_mn = x.b_mn;
+    g.group = 8;
+    g.run = sizeof(T) == 4 ? 4 : Epi::kExact ? 8 : 1 << 30;
+    p.g[i] = g;
+    p.epi[i] = epi;
+    const cudaError_t e = tensor_map(&maps.a[i], x.a, g.planes, x.a_mn ? kTcDepth : 128);
+    return e == cudaSuccess ? tensor_map(&maps.b[i], x.b, g.planes, x.b_mn ? kTcDepth : kN / 2) : e;
 }
 
 // The terms of a product with few tiles are split, so that more of the SMs have some; the parts' sums are joined by a
@@ -567,35 +685,52 @@ inline int64_t parts_elements(int64_t m, int64_t n)  // of a workspace: tiles x 
     return all < whole ? all : whole;
 }
 
-// A product of matrices of T's planes. a_mn, b_mn: the matrix lies by terms (its rows are terms). parts: room for
-// parts_elements, or NULL.
-template <typename T, typename Epi>
-cudaError_t product_tc(const Matrix& a, bool a_mn, const Matrix& b, bool b_mn, TcArgs g, float* parts, const Epi& epi,
-                       cudaStream_t stream)
+// A product of matrices of T's planes. parts: room for parts_elements.
+template <typename T, typename Epi> cudaError_t product_tc(const TcProduct& x, float* parts, const Epi& epi, cudaStream_t stream)
 {
-    if (g.m <= 0 || g.n <= 0) return cudaSuccess;
-    g.planes = sizeof(T) == 4 ? kPlanes : 1;
-    g.a_mn = a_mn;
-    g.b_mn = b_mn;
-    g.splits = Epi::kPieces ? splits_of(g.m, g.n, g.k) : 1;
-    g.group = 8;
-    g.run = sizeof(T) == 4 ? 4 : Epi::kExact ? 8 : 1 << 30;
+    if (x.m <= 0 || x.n <= 0) return cudaSuccess;
+    TcMaps maps = {};
     if constexpr (Epi::kPieces) {
-    if (g.splits > 1) {
-    EpiStore<float> each = {};
-    each.out = parts;
-    each.stride = round_up(g.n, 4);
-    each.split_stride = g.m * each.stride;
-    each.n = (int32_t)g.n;
-    each.first = each.last = each.whole = true;
-    const cudaError_t e = product_tc_n<256, true>(a, b, g, each, stream);
-    if (e != cudaSuccess) return e;
-    const JoinPartsArgs j = {parts, g.m, g.n, each.stride, g.m_count, g.splits};
-    const int64_t all = (g.n + kJoin - 1) / kJoin * g.m;
-    return launch_after(join_parts_kernel<Epi>, dim3((unsigned)((all + kRows - 1) / kRows)), dim3(kRows), 0, stream, j, epi);
+        const int splits = splits_of(x.m, x.n, x.k);
+        if (splits > 1) {
+            EpiStore<float> each = {};
+            each.out = parts;
+            each.stride = round_up(x.n, 4);
+            each.split_stride = x.m * each.stride;
+            each.n = (int32_t)x.n;
+            each.first = each.last = each.whole = true;
+            TcParams<EpiStore<float>> p = {};
+            cudaError_t e = set_tc<T>(maps, p, 0, x, each);
+            if (e != cudaSuccess) return e;
+            p.g[0].splits = splits;
+            if (!Epi::kExact) p.g[0].run = 1 << 30;
+            e = launch_tc<256, kTcSplit>(maps, p, stream);
+            if (e != cudaSuccess) return e;
+            const JoinPartsArgs j = {parts, x.m, x.n, each.stride, x.m_count, splits};
+            const int64_t all = (x.n + kJoin - 1) / kJoin * x.m;
+            return launch_after(join_parts_kernel<Epi>, dim3((unsigned)((all + kRows - 1) / kRows)), dim3(kRows), 0, stream, j, epi);
+        }
     }
+    TcParams<Epi> p = {};
+    const cudaError_t e = set_tc<T>(maps, p, 0, x, epi);
+    return e == cudaSuccess ? launch_tc<256, kTcOne>(maps, p, stream) : e;
+}
+
+// Two products, neither of which needs the other: in one launch, so that the tiles of one fill the SMs that the other's last
+// ones leave idle (8192 rows, 16384 tokens of a vocabulary, width 2048, bf16: 608 -> 5xx us), unless they are small.
+template <typename T, typename Epi>
+cudaError_t product_tc_both(const TcProduct& x, const Epi& epi_x, const TcProduct& y, const Epi& epi_y, float* parts, cudaStream_t stream)
+{
+    if (splits_of(x.m, x.n, x.k) > 1 || splits_of(y.m, y.n, y.k) > 1) {
+        const cudaError_t e = product_tc<T>(x, parts, epi_x, stream);
+        return e == cudaSuccess ? product_tc<T>(y, parts, epi_y, stream) : e;
     }
-    return product_tc_n<256, false>(a, b, g, epi, stream);
+    const bool turned = y.k > x.k;  // the longer sums first
+    TcMaps maps = {};
+    TcParams<Epi> p = {};
+    cudaError_t e = set_tc<T>(maps, p, turned, x, epi_x);
+    if (e == cudaSuccess) e = set_tc<T>(maps, p, !turned, y, epi_y);
+    return e == cudaSuccess ? launch_tc<256, kTcBoth>(maps, p, stream) : e;
 }
 
 }  // namespace

@@ -335,12 +335,8 @@ template <typename T> cudaError_t vocab_forward(const VocabArgs& a, void* ws, cu
     epi.n = (int32_t)a.vocab;
     epi.row_stride = a.rows;
     epi.scale = 1.0f / a.temperature;
-    TcArgs g = {};
-    g.m = a.rows;
-    g.n = a.vocab;
-    g.k = a.dim;
-    g.m_count = p.count;
-    e = product_tc<T>(x, false, w, false, g, nullptr, epi, stream);
+    const TcProduct product = {x, w, false, false, a.rows, a.vocab, a.dim, p.count, nullptr};
+    e = product_tc<T>(product, nullptr, epi, stream);
     if (e != cudaSuccess) return e;
     JoinArgs j = {};
     j.part = p.part;
@@ -384,41 +380,27 @@ template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, c
         const Matrix here = {w.p + at * w.stride, n, a.dim, w.stride, w.plane}, dz = {p.dz, p.padded, n, p.dz_stride, grad.plane};
         grad.n = (int32_t)n;
         grad.first = (int32_t)at;
-        TcArgs g = {};
-        g.m = a.rows;
-        g.n = n;
-        g.k = a.dim;
-        g.m_count = p.count;
-        e = product_tc<T>(x, false, here, false, g, nullptr, grad, stream);
-        if (a.dx && e == cudaSuccess) {
-            EpiStore<T> store = {};
-            store.out = static_cast<T*>(a.dx);
-            store.acc = p.acc;
-            store.map = p.map;
-            store.stride = a.dx_stride;
-            store.acc_stride = round_up(a.dim, 4);
-            store.n = (int32_t)a.dim;
-            store.first = at == 0;
-            store.last = at + n == a.vocab;
-            store.whole = whole_rows(a.dx, a.dx_stride, a.rows, sizeof(T));
-            g.n = a.dim;
-            g.k = n;
-            e = product_tc<T>(dz, false, here, true, g, p.parts, store, stream);
-        }
-        if (a.dw && e == cudaSuccess) {
-            EpiStore<T> store = {};
-            store.out = static_cast<T*>(a.dw) + at * a.dw_stride;
-            store.stride = a.dw_stride;
-            store.n = (int32_t)a.dim;
-            store.first = store.last = true;
-            store.whole = whole_rows(a.dw, a.dw_stride, a.vocab, sizeof(T));
-            g = {};
-            g.m = n;
-            g.n = a.dim;
-            g.k = a.rows;
-            g.k_count = p.count;
-            e = product_tc<T>(dz, true, x, true, g, p.parts, store, stream);
-        }
+        const TcProduct logits = {x, here, false, false, a.rows, n, a.dim, p.count, nullptr};
+        e = product_tc<T>(logits, nullptr, grad, stream);
+        if (e != cudaSuccess) break;
+        EpiStore<T> to_dx = {}, to_dw = {};
+        to_dx.out = static_cast<T*>(a.dx);
+        to_dx.acc = p.acc;
+        to_dx.map = p.map;
+        to_dx.stride = a.dx_stride;
+        to_dx.acc_stride = round_up(a.dim, 4);
+        to_dx.first = at == 0;
+        to_dx.last = at + n == a.vocab;
+        to_dx.whole = whole_rows(a.dx, a.dx_stride, a.rows, sizeof(T));
+        to_dw.out = static_cast<T*>(a.dw) + (a.dw ? at * a.dw_stride : 0);
+        to_dw.stride = a.dw_stride;
+        to_dw.first = to_dw.last = true;
+        to_dw.whole = whole_rows(a.dw, a.dw_stride, a.vocab, sizeof(T));
+        to_dx.n = to_dw.n = (int32_t)a.dim;
+        const TcProduct dx = {dz, here, false, true, a.rows, a.dim, n, p.count, nullptr};
+        const TcProduct dw = {dz, x, true, true, n, a.dim, a.rows, nullptr, p.count};
+        if (a.dx && a.dw) e = product_tc_both<T>(dx, to_dx, dw, to_dw, p.parts, stream);
+        else e = a.dx ? product_tc<T>(dx, p.parts, to_dx, stream) : product_tc<T>(dw, p.parts, to_dw, stream);
     }
     return e;
 }
