@@ -41,8 +41,7 @@ LinearParts linear_parts(Carve& c, int64_t rows, int64_t in, int64_t out, int by
     if (backward) {
         p.sums = c.take<float>(kDzSlices * out);
         p.dz = c.take<bf16>(packed_elements(rows, out, bytes));
-        const int64_t x = parts_elements(rows, in), w = parts_elements(out, in);
-        most = x > w ? x : w;
+        most = parts_elements(rows, in) + parts_elements(out, in);
     }
     p.parts = c.take<float>(most);
     return p;
@@ -66,31 +65,71 @@ struct DzArgs {
     bool plain, dy_whole, pre_whole;
 };
 
+// Eight columns of a row as they lie in memory, until they are used.
+template <typename T> struct Eight {
+    uint32_t w[2 * sizeof(T)];
+    __device__ __forceinline__ void load(const T* p, int64_t left, bool whole)
+    {
+        if (whole && left >= 8) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+                const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+            }
+            return;
+        }
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = i < left ? __float_as_uint(p[i]) : 0u;
+        } else {
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = (2 * i < left ? q[2 * i] : 0u) | (2 * i + 1 < left ? (uint32_t)q[2 * i + 1] << 16 : 0u);
+        }
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return i & 1 ? bf16_high(w[i / 2]) : bf16_low(w[i / 2]);
+    }
+};
+
 // dz = dy * act'(pre), and its sums over slices of the rows. Bound by memory: a thread has eight columns of every
-// kDzRows-th row of a slice, four rows under way at a time; the CTA's sums meet in shared memory, the slices' in a
+// kDzRows-th row of a slice, several rows under way at a time; the CTA's sums meet in shared memory, the slices' in a
 // second kernel, in a fixed order.
 template <typename T, int kAct> __device__ __forceinline__ void dz_rows(const DzArgs& a, int32_t c, float (&sum)[8])
 {
+    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
     const T *dy = static_cast<const T*>(a.dy) + c, *pre = static_cast<const T*>(a.pre) + c;
     const int64_t left = a.n - c, step = (int64_t)a.slices * kDzRows;
-#pragma unroll 4
-    for (int64_t r = blockIdx.y * kDzRows + threadIdx.y; r < a.rows; r += step) {
-        float v[8];
-        get_chunk(dy + r * a.dy_stride, v, left, a.dy_whole);
-        if constexpr (kAct != ADACOMP_ACT_NONE) {
-            float z[8];
-            get_chunk(pre + r * a.pre_stride, z, left, a.pre_whole);
+    for (int64_t r0 = blockIdx.y * kDzRows + threadIdx.y; r0 < a.rows; r0 += kAhead * step) {
+        Eight<T> v[kAhead], z[kAhead];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= slope<T, kAct>(z[j]);
-            if (a.dz && a.plain) put_chunk(static_cast<T*>(a.dz) + r * a.dz_stride + c, v, left, true);
-            else if (a.dz) put_parts<T>(static_cast<bf16*>(a.dz) + r * a.dz_stride + c, a.dz_plane, v, left);
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t r = r0 + i * step, here = r < a.rows ? left : 0;
+            v[i].load(dy + r * a.dy_stride, here, a.dy_whole);
+            if constexpr (kAct != ADACOMP_ACT_NONE) z[i].load(pre + r * a.pre_stride, here, a.pre_whole);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t r = r0 + i * step;
+            if (r >= a.rows) break;
+            float d[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                d[j] = v[i].get(j);
+                // one rounding whatever is asked for: db is the sum of what dz would be rounded from
+                if constexpr (kAct != ADACOMP_ACT_NONE) d[j] = __fmul_rn(d[j], slope<T, kAct>(z[i].get(j)));
+                sum[j] += d[j];
+            }
+            if (kAct == ADACOMP_ACT_NONE || !a.dz) continue;
+            if (a.plain) put_chunk(static_cast<T*>(a.dz) + r * a.dz_stride + c, d, left, true);
+            else put_parts<T>(static_cast<bf16*>(a.dz) + r * a.dz_stride + c, a.dz_plane, d, left);
+        }
     }
 }
 
-template <typename T> __global__ void __launch_bounds__(kDzCols / 8 * kDzRows) linear_dz_kernel(const DzArgs a)
+template <typename T> __global__ void __launch_bounds__(kDzCols / 8 * kDzRows, sizeof(T) == 2 ? 4 : 3) linear_dz_kernel(const DzArgs a)
 {
     __shared__ float sums[kDzRows][kDzCols];
     ptx::griddep_wait();
@@ -147,10 +186,8 @@ template <typename T> cudaError_t linear_forward(const LinearArgs& a, void* ws, 
     epi.residual_stride = a.residual_stride;
     epi.n = (int32_t)a.out;
     epi.act = a.act;
-    epi.y_whole = whole_rows(a.y, a.y_stride, a.rows, sizeof(T));
-    epi.pre_whole = whole_rows(a.pre, a.pre_stride, a.rows, sizeof(T));
-    epi.bias_whole = is_aligned(a.bias, 16);
-    epi.residual_whole = whole_rows(a.residual, a.residual_stride, a.rows, sizeof(T));
+    epi.whole = whole_rows(a.y, a.y_stride, a.rows, sizeof(T)) && whole_rows(a.pre, a.pre_stride, a.rows, sizeof(T)) &&
+                is_aligned(a.bias, 16) && whole_rows(a.residual, a.residual_stride, a.rows, sizeof(T));
     if (a.rows <= (sizeof(T) == 2 ? kFewBf16 : kFewF32))
         return product_few<T>(FewArgs{a.x, a.w, a.x_stride, a.w_stride, (int32_t)a.rows, (int32_t)a.out, (int32_t)a.in}, epi, stream);
     if (is_small<T>(a.rows, a.in, a.out))
@@ -171,7 +208,7 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
     const LinearParts p = linear_parts(carve, a.rows, a.in, a.out, sizeof(T), true);
     const bool act = a.act != ADACOMP_ACT_NONE, products = a.dx || a.dw, small = is_small<T>(a.rows, a.in, a.out);
     cudaError_t e = cudaSuccess;
-    Matrix dz = {p.dz, a.rows, a.out, round_up(a.out, 8), a.rows * round_up(a.out, 8)}, x, w;
+    Matrix dz = {p.dz, a.rows, a.out, pitch_of(a.out), a.rows * pitch_of(a.out)}, x, w;
     if ((act && products) || a.db) {
         DzArgs d = {};
         d.dy = a.dy;
@@ -213,7 +250,7 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
         return epi;
     };
     const EpiStore<T> to_dx = store(a.dx, a.dx_stride, a.rows), to_dw = store(a.dw, a.dw_stride, a.out);
-    if (a.rows == 0) return a.dw ? product_none<T>(a.out, a.in, to_dw, stream) : cudaSuccess;
+    if (a.rows == 0) return a.dw ? product_none(a.out, a.in, to_dw, stream) : cudaSuccess;
     const int32_t rows = (int32_t)a.rows, in = (int32_t)a.in, out = (int32_t)a.out;
     if (small) {
         const Operand by_row = act ? Operand{p.dz, dz.stride, 1} : Operand{a.dy, a.dy_stride, 1};

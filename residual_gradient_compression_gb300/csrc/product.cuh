@@ -7,7 +7,7 @@
 // what it reads and writes in global memory are whole pieces of rows (a thread that writes its own row takes 32 cache
 // lines at a time: a linear layer's forward product of 8192 x 2048 x 16384 bf16 took 369 us so, and 313 without its
 // stores). kExact: the results are held in fp32, so the sums are formed in short runs.
-// kPieces: a thread may also hand over four columns on their own, piece(). kAdds: there may be a matrix that
+// kPieces: a thread may also hand over columns on their own, piece(). kAdds: there may be a matrix that
 // the sums are added to, which take() loads before they are there.
 #pragma once
 
@@ -87,41 +87,54 @@ template <typename T, int N> __device__ __forceinline__ void get_chunk(const T* 
     for (int i = 0; i < N; ++i) v[i] = i < left ? to_f32(p[i]) : 0.0f;
 }
 
-// Four columns of a row.
-template <typename T> __device__ __forceinline__ void put4(T* p, const float4& v, int64_t left, bool whole)
-{
-    if (whole && left >= 4) {
-        if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<float4*>(p) = v;
-        } else {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-            *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        }
-        return;
+// N columns of a row: four that are aligned to as many, or one.
+template <int N> struct Cols {
+    float v[N];
+    __device__ __forceinline__ Cols operator+(const Cols& o) const
+    {
+        Cols s;
+#pragma unroll
+        for (int i = 0; i < N; ++i) s.v[i] = v[i] + o.v[i];
+        return s;
     }
-    if (left > 0) p[0] = from_f32<T>(v.x);
-    if (left > 1) p[1] = from_f32<T>(v.y);
-    if (left > 2) p[2] = from_f32<T>(v.z);
-    if (left > 3) p[3] = from_f32<T>(v.w);
-}
+};
 
-template <typename T> __device__ __forceinline__ float4 get4(const T* p, int64_t left, bool whole)
+template <typename T, int N> __device__ __forceinline__ void put(T* p, const Cols<N>& c, int32_t left)
 {
-    if (whole && left >= 4) {
-        if constexpr (sizeof(T) == 4) {
-            return *reinterpret_cast<const float4*>(p);
-        } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(p);
-            return make_float4(bf16_low(w.x), bf16_high(w.x), bf16_low(w.y), bf16_high(w.y));
+    if constexpr (N == 4) {
+        if (left >= 4) {
+            if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<float4*>(p) = make_float4(c.v[0], c.v[1], c.v[2], c.v[3]);
+            } else {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(c.v[0], c.v[1]), hi = __floats2bfloat162_rn(c.v[2], c.v[3]);
+                *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            }
+            return;
         }
     }
-    return make_float4(left > 0 ? to_f32(p[0]) : 0.0f, left > 1 ? to_f32(p[1]) : 0.0f, left > 2 ? to_f32(p[2]) : 0.0f,
-                       left > 3 ? to_f32(p[3]) : 0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < left) p[i] = from_f32<T>(c.v[i]);
 }
 
-__device__ __forceinline__ float4 operator+(const float4& a, const float4& b)
+template <int N, typename T> __device__ __forceinline__ Cols<N> get(const T* p, int32_t left)
 {
-    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+    Cols<N> c;
+    if constexpr (N == 4) {
+        if (left >= 4) {
+            if constexpr (sizeof(T) == 4) {
+                const float4 w = *reinterpret_cast<const float4*>(p);
+                c.v[0] = w.x, c.v[1] = w.y, c.v[2] = w.z, c.v[3] = w.w;
+            } else {
+                const uint2 w = *reinterpret_cast<const uint2*>(p);
+                c.v[0] = bf16_low(w.x), c.v[1] = bf16_high(w.x), c.v[2] = bf16_low(w.y), c.v[3] = bf16_high(w.y);
+            }
+            return c;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) c.v[i] = i < left ? to_f32(p[i]) : 0.0f;
+    return c;
 }
 
 // A warp's 32 rows of 32 columns in shared memory; a row's 16-byte pieces lie where no two rows of eight share banks.
@@ -130,12 +143,41 @@ struct Stage {
     __device__ __forceinline__ float4& at(int row, int piece) const { return p[row * 8 + (piece ^ (row & 7))]; }
 };
 
-constexpr int kTurns = 8;  // a chunk in turns of four rows, of which a lane has four columns
+// How a warp takes a chunk: in turns of four rows, of which a lane has four columns, or, where rows do not begin at such
+// places, of one row, of which it has one.
+template <int N> struct Turns {
+    static constexpr int kCount = N == 4 ? 8 : 32;
+    int row, col;
+    __device__ __forceinline__ Turns()
+    {
+        const int lane = threadIdx.x & 31;
+        row = N == 4 ? lane / 8 : 0;
+        col = N == 4 ? (lane & 7) * 4 : lane;
+    }
+    __device__ __forceinline__ int row_of(int turn) const { return turn * (32 / kCount) + row; }
+    __device__ __forceinline__ Cols<N> read(const Stage& s, int turn) const
+    {
+        const float4& v = s.at(row_of(turn), col / 4);
+        Cols<N> c;
+        if constexpr (N == 4) c.v[0] = v.x, c.v[1] = v.y, c.v[2] = v.z, c.v[3] = v.w;
+        else c.v[0] = reinterpret_cast<const float*>(&v)[col & 3];
+        return c;
+    }
+    __device__ __forceinline__ void write(const Stage& s, int turn, const Cols<N>& c) const
+    {
+        float4& v = s.at(row_of(turn), col / 4);
+        if constexpr (N == 4) v = make_float4(c.v[0], c.v[1], c.v[2], c.v[3]);
+        else reinterpret_cast<float*>(&v)[col & 3] = c.v[0];
+    }
+};
 
 inline bool whole_rows(const void* p, int64_t stride, int64_t rows, int bytes)
 {
     return is_aligned(p, 16) && (rows < 2 || stride * bytes % 16 == 0);
 }
+
+// Of a matrix in a workspace: rows begin with a cache line, unless they are shorter than one.
+inline int64_t pitch_of(int64_t cols) { return round_up(cols, cols < 64 ? 8 : 64); }
 
 // ---------------------------------------------------------------- fp32 numbers in parts
 constexpr int kPlanes = 4;  // of bf16 numbers for an fp32 matrix
@@ -245,90 +287,95 @@ template <typename T> struct EpiLinear {
     const T *bias, *residual;
     int64_t y_stride, pre_stride, residual_stride;
     int32_t n, act;
-    bool y_whole, pre_whole, bias_whole, residual_whole;
+    bool whole;  // all of them
     struct State {};
     __device__ __forceinline__ State begin(int32_t, int32_t) const { return {}; }
     __device__ __forceinline__ void rows(const State&, int32_t, int32_t, bool, float (&)[kStrip]) const {}
 
-    template <typename F> __device__ __forceinline__ void turns(const Stage& stage, int32_t r0, int32_t end, int32_t c0, F f) const
+    template <int N, typename F> __device__ __forceinline__ void turns(const Stage& stage, int32_t r0, int32_t end, int32_t c0, F f) const
     {
-        const int lane = threadIdx.x & 31, piece = lane & 7, first = lane / 8;
-        const int32_t c = c0 + piece * 4, left = n - c;
-        const float4 b = bias ? get4(bias + c, left, bias_whole) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (pre) {
-#pragma unroll
-            for (int i = 0; i < kTurns; ++i) {
-                const int32_t r = r0 + i * 4 + first;
-                if (r < end) put4(pre + r * pre_stride + c, stage.at(i * 4 + first, piece) + b, left, pre_whole);
-            }
-        }
+        constexpr int kCount = Turns<N>::kCount;
+        const Turns<N> turn;
+        const int32_t c = c0 + turn.col, left = n - c;
+        Cols<N> b = {};
+        if (bias) b = get<N>(bias + c, left);
         if (!residual) {
-#pragma unroll 2
-            for (int i = 0; i < kTurns; ++i) {
-                const int32_t r = r0 + i * 4 + first;
-                if (r < end) put4(y + r * y_stride + c, f(stage.at(i * 4 + first, piece) + b), left, y_whole);
+#pragma unroll(N == 4 ? 4 : 8)
+            for (int i = 0; i < kCount; ++i) {
+                const int32_t r = r0 + turn.row_of(i);
+                const Cols<N> z = turn.read(stage, i) + b;
+                if (pre && r < end) put(pre + r * pre_stride + c, z, left);
+                const Cols<N> v = f(z);
+                if (r < end) put(y + r * y_stride + c, v, left);
             }
             return;
         }
-#pragma unroll 2
-        for (int i = 0; i < kTurns; ++i) {
-            float4& v = stage.at(i * 4 + first, piece);
-            v = f(v + b);
-        }
-        float4 more[kTurns];  // loads that wait together
+        Cols<N> more[kCount];  // loads that wait together, while the activation is computed
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-            const int32_t r = r0 + i * 4 + first;
-            more[i] = get4(residual + r * residual_stride + c, r < end ? left : 0, residual_whole);
+        for (int i = 0; i < kCount; ++i) {
+            const int32_t r = r0 + turn.row_of(i);
+            more[i] = get<N>(residual + r * residual_stride + c, r < end ? left : 0);
+        }
+#pragma unroll(N == 4 ? 4 : 8)
+        for (int i = 0; i < kCount; ++i) {
+            const int32_t r = r0 + turn.row_of(i);
+            const Cols<N> z = turn.read(stage, i) + b;
+            if (pre && r < end) put(pre + r * pre_stride + c, z, left);
+            turn.write(stage, i, f(z));
         }
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-            const int32_t r = r0 + i * 4 + first;
-            if (r < end) put4(y + r * y_stride + c, stage.at(i * 4 + first, piece) + more[i], left, y_whole);
+        for (int i = 0; i < kCount; ++i) {
+            const int32_t r = r0 + turn.row_of(i);
+            const Cols<N> v = turn.read(stage, i) + more[i];
+            if (r < end) put(y + r * y_stride + c, v, left);
         }
     }
 
-    template <int kKind> static __device__ __forceinline__ float4 each(const float4& v)
+    template <int kKind, int N> static __device__ __forceinline__ Cols<N> each(Cols<N> c)
     {
-        return make_float4(activate<T, kKind>(v.x), activate<T, kKind>(v.y), activate<T, kKind>(v.z), activate<T, kKind>(v.w));
+#pragma unroll
+        for (int i = 0; i < N; ++i) c.v[i] = activate<T, kKind>(c.v[i]);
+        return c;
     }
 
     template <typename G> __device__ __forceinline__ void with_act(G g) const
     {
         switch (act) {
-        case ADACOMP_ACT_RELU: g([](const float4& v) { return each<ADACOMP_ACT_RELU>(v); }); break;
-        case ADACOMP_ACT_GELU: g([](const float4& v) { return each<ADACOMP_ACT_GELU>(v); }); break;
-        case ADACOMP_ACT_GELU_TANH: g([](const float4& v) { return each<ADACOMP_ACT_GELU_TANH>(v); }); break;
-        case ADACOMP_ACT_SILU: g([](const float4& v) { return each<ADACOMP_ACT_SILU>(v); }); break;
-        default: g([](const float4& v) { return v; });
+        case ADACOMP_ACT_RELU: g([](auto v) { return each<ADACOMP_ACT_RELU>(v); }); break;
+        case ADACOMP_ACT_GELU: g([](auto v) { return each<ADACOMP_ACT_GELU>(v); }); break;
+        case ADACOMP_ACT_GELU_TANH: g([](auto v) { return each<ADACOMP_ACT_GELU_TANH>(v); }); break;
+        case ADACOMP_ACT_SILU: g([](auto v) { return each<ADACOMP_ACT_SILU>(v); }); break;
+        default: g([](auto v) { return v; });
         }
     }
 
     __device__ __forceinline__ void chunk(const Stage& stage, const State&, int32_t r0, int32_t end, int32_t c) const
     {
-        with_act([&](auto f) { turns(stage, r0, end, c, f); });
+        if (whole) with_act([&](auto f) { turns<4>(stage, r0, end, c, f); });
+        else with_act([&](auto f) { turns<1>(stage, r0, end, c, f); });
     }
 
-    // four columns, by a thread on its own
-    __device__ __forceinline__ void piece(int32_t r, int32_t c, float4 v) const
+    // columns, by a thread on its own
+    template <int N> __device__ __forceinline__ void piece(int32_t r, int32_t c, Cols<N> v) const
     {
         const int32_t left = n - c;
-        if (bias) v = v + get4(bias + c, left, bias_whole);
-        if (pre) put4(pre + r * pre_stride + c, v, left, pre_whole);
+        if (bias) v = v + get<N>(bias + c, left);
+        if (pre) put(pre + r * pre_stride + c, v, left);
         with_act([&](auto f) { v = f(v); });
-        if (residual) v = v + get4(residual + r * residual_stride + c, left, residual_whole);
-        put4(y + r * y_stride + c, v, left, y_whole);
+        if (residual) v = v + get<N>(residual + r * residual_stride + c, left);
+        put(y + r * y_stride + c, v, left);
     }
 };
 
 // The sums themselves, in rows that `map` may move; with acc, added up over several products in
-// fp32 (first: nothing to add to yet) and rounded by the last one only.
+// fp32 (first: nothing to add to yet) and rounded by the last one only. Of a product whose terms are split, the parts'
+// sums go to acc, split_stride apart (and neither first nor last is asked).
 template <typename T> struct EpiStore {
     static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kAdds = true;
     T* out;
     float* acc;
     const int32_t* map;
-    int64_t stride, acc_stride, split_stride;  // split_stride: between the parts of a product whose terms are split
+    int64_t stride, acc_stride, split_stride;
     int32_t n;
     bool first, last, whole;
     struct State {
@@ -338,47 +385,50 @@ template <typename T> struct EpiStore {
     __device__ __forceinline__ bool adds() const { return !first; }
     __device__ __forceinline__ void rows(const State&, int32_t, int32_t, bool, float (&)[kStrip]) const {}
 
-    __device__ __forceinline__ EpiStore of_split(int split) const
-    {
-        EpiStore e = *this;
-        e.out += split * split_stride;
-        return e;
-    }
-
     __device__ __forceinline__ void take(const Stage& stage, int32_t r0, int32_t end, int32_t c0) const
     {
-        const int lane = threadIdx.x & 31, piece = lane & 7, at = lane / 8;
-        const int32_t c = c0 + piece * 4, left = n - c;
-        float4 v[kTurns];
+        const Turns<4> turn;
+        const int32_t c = c0 + turn.col, left = n - c;
+        Cols<4> v[8];
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-            const int32_t r = r0 + i * 4 + at;
-            v[i] = get4(acc + r * acc_stride + c, r < end ? left : 0, true);
+        for (int i = 0; i < 8; ++i) {
+            const int32_t r = r0 + turn.row_of(i);
+            v[i] = get<4>(acc + r * acc_stride + c, r < end ? left : 0);
         }
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i) stage.at(i * 4 + at, piece) = v[i];
+        for (int i = 0; i < 8; ++i) turn.write(stage, i, v[i]);
+    }
+
+    template <int N, typename O>
+    __device__ __forceinline__ void turns(const Stage& stage, int32_t to, O* p, int64_t pitch, int32_t r0, int32_t end, int32_t c0) const
+    {
+        const Turns<N> turn;
+        const int32_t c = c0 + turn.col, left = n - c;
+#pragma unroll
+        for (int i = 0; i < Turns<N>::kCount; ++i) {
+            const int32_t r = __shfl_sync(0xffffffffu, to, turn.row_of(i));
+            if (r0 + turn.row_of(i) < end) put(p + r * pitch + c, turn.read(stage, i), left);
+        }
+    }
+
+    __device__ __forceinline__ void part(const Stage& stage, int split, int32_t r0, int32_t end, int32_t c0) const
+    {
+        turns<4>(stage, r0 + (int32_t)(threadIdx.x & 31), acc + split * split_stride, acc_stride, r0, end, c0);
     }
 
     __device__ __forceinline__ void chunk(const Stage& stage, const State& s, int32_t r0, int32_t end, int32_t c0) const
     {
-        const int lane = threadIdx.x & 31, piece = lane & 7, at = lane / 8;
-        const int32_t c = c0 + piece * 4, left = n - c;
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-            const int32_t r = r0 + i * 4 + at, to = __shfl_sync(0xffffffffu, s.to, i * 4 + at);
-            if (r >= end) continue;
-            const float4 v = stage.at(i * 4 + at, piece);
-            if (last) put4(out + to * stride + c, v, left, whole);
-            else put4(acc + r * acc_stride + c, v, left, true);
-        }
+        if (!last) turns<4>(stage, r0 + (int32_t)(threadIdx.x & 31), acc, acc_stride, r0, end, c0);
+        else if (whole) turns<4>(stage, s.to, out, stride, r0, end, c0);
+        else turns<1>(stage, s.to, out, stride, r0, end, c0);
     }
 
-    __device__ __forceinline__ void piece(int32_t r, int32_t c, float4 v) const
+    template <int N> __device__ __forceinline__ void piece(int32_t r, int32_t c, Cols<N> v) const
     {
         const int32_t left = n - c;
-        if (!first) v = v + get4(acc + r * acc_stride + c, left, true);
-        if (last) put4(out + (map ? map[r] : r) * stride + c, v, left, whole);
-        else put4(acc + r * acc_stride + c, v, left, true);
+        if (!first) v = v + get<N>(acc + r * acc_stride + c, left);
+        if (last) put(out + (map ? map[r] : r) * stride + c, v, left);
+        else put(acc + r * acc_stride + c, v, left);
     }
 };
 
@@ -513,25 +563,27 @@ template <typename T> struct EpiGradient {
     }
     __device__ __forceinline__ void chunk(const Stage& stage, const State&, int32_t r0, int32_t, int32_t c0) const
     {
-        const int lane = threadIdx.x & 31, piece = lane & 7, at = lane / 8;
-        const int32_t c = c0 + piece * 4, left = n - c;
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-            const int32_t r = r0 + i * 4 + at;
+        const Turns<4> turn;
+        const int32_t c = c0 + turn.col, left = n - c;
+#pragma unroll(sizeof(T) == 2 ? 8 : 2)
+        for (int i = 0; i < 8; ++i) {
+            const int32_t r = r0 + turn.row_of(i);
             if (r >= room) continue;
-            const float4 v = stage.at(i * 4 + at, piece);
+            const Cols<4> v = turn.read(stage, i);
             bf16* to = dz + r * stride + c;
             if constexpr (sizeof(T) == 2) {
-                put4(to, v, left, true);
+                put(to, v, left);
             } else {
-                bf16 x[kPlanes], y[kPlanes], z[kPlanes], w[kPlanes];
-                split_parts(v.x, x);
-                split_parts(v.y, y);
-                split_parts(v.z, z);
-                split_parts(v.w, w);
+                Cols<4> part[kPlanes];
 #pragma unroll
-                for (int j = 0; j < kPlanes; ++j)
-                    put4(to + j * plane, make_float4(__bfloat162float(x[j]), __bfloat162float(y[j]), __bfloat162float(z[j]), __bfloat162float(w[j])), left, true);
+                for (int j = 0; j < 4; ++j) {
+                    bf16 each[kPlanes];
+                    split_parts(v.v[j], each);
+#pragma unroll
+                    for (int p = 0; p < kPlanes; ++p) part[p].v[j] = __bfloat162float(each[p]);
+                }
+#pragma unroll
+                for (int p = 0; p < kPlanes; ++p) put(to + p * plane, part[p], left);
             }
         }
     }

@@ -7,6 +7,18 @@
 namespace adacomp {
 namespace {
 
+// Four columns to an epilogue, one by one where its rows are not aligned.
+template <typename Epi> __device__ __forceinline__ void put_piece(const Epi& epi, int32_t r, int32_t c, const Cols<4>& v)
+{
+    if (epi.whole) {
+        epi.piece(r, c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < epi.n) epi.piece(r, c + i, Cols<1>{{v.v[i]}});
+    }
+}
+
 // ---------------------------------------------------------------- few rows
 constexpr int kFewBf16 = 16, kFewF32 = 8;  // rows, at most
 
@@ -75,10 +87,10 @@ __global__ void __launch_bounds__(kWarps * 32) few_bf16_kernel(const FewArgs g, 
     if (threadIdx.x >= kTokens * 4) return;
     const int32_t r = threadIdx.x / 4, c = threadIdx.x % 4 * 4;
     if (r >= g.rows || c0 + c >= g.n) return;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    Cols<4> v = {};
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) v = v + *reinterpret_cast<const float4*>(&sums[i][r][c]);
-    epi.piece(r, c0 + c, v);
+    for (int i = 0; i < kWarps; ++i) v = v + get<4>(&sums[i][r][c], 4);
+    put_piece(epi, r, c0 + c, v);
 }
 
 // The same of fp32 numbers: a warp has four rows of the weights, its lanes four terms each at a time.
@@ -94,21 +106,33 @@ __global__ void __launch_bounds__(256, 2) few_f32_kernel(const FewArgs g, const 
     float d[kTokens][4] = {};
 #pragma unroll 1
     for (int32_t k = lane * 4; k < g.k; k += 128) {
-        float4 a[4];
+        const auto load = [&](const float* p, int32_t left) {
+            if constexpr (kWhole) {
+                return get<4>(p, left);
+            } else {
+                Cols<4> v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = get4(w + (c0 + i) * g.w_stride + k, c0 + i < g.n ? g.k - k : 0, kWhole);
+                for (int i = 0; i < 4; ++i) v.v[i] = i < left ? p[i] : 0.0f;
+                return v;
+            }
+        };
+        Cols<4> a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = load(w + (c0 + i) * g.w_stride + k, c0 + i < g.n ? g.k - k : 0);
 #pragma unroll
         for (int t = 0; t < kTokens; ++t) {
-            const float4 b = get4(x + t * g.x_stride + k, t < g.rows ? g.k - k : 0, kWhole);
+            const Cols<4> b = load(x + t * g.x_stride + k, t < g.rows ? g.k - k : 0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[t][i] = fmaf(a[i].w, b.w, fmaf(a[i].z, b.z, fmaf(a[i].y, b.y, fmaf(a[i].x, b.x, d[t][i]))));
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[t][i] = fmaf(a[i].v[j], b.v[j], d[t][i]);
         }
     }
 #pragma unroll
     for (int t = 0; t < kTokens; ++t) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[t][i] = warp_sum(d[t][i]);
-        if (lane == t && t < g.rows) epi.piece(t, c0, make_float4(d[t][0], d[t][1], d[t][2], d[t][3]));
+        if (lane == t && t < g.rows) put_piece(epi, t, c0, Cols<4>{{d[t][0], d[t][1], d[t][2], d[t][3]}});
     }
 }
 
@@ -222,10 +246,10 @@ template <typename T, typename Epi> __global__ void __launch_bounds__(256) produ
     __syncthreads();
     const int row = threadIdx.x / 8, col = threadIdx.x % 8 * 4;
     if (m0 + row >= g.m || n0 + col >= g.n) return;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    Cols<4> v = {};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v = v + *reinterpret_cast<const float4*>(tile + (i * kSmallTile + row) * kPitch + col);
-    epi.piece(m0 + row, n0 + col, v);
+    for (int i = 0; i < 8; ++i) v = v + get<4>(tile + (i * kSmallTile + row) * kPitch + col, 4);
+    put_piece(epi, m0 + row, n0 + col, v);
 }
 
 template <typename T, typename Epi> cudaError_t product_small(const SmallArgs& g, const Epi& epi, cudaStream_t stream)

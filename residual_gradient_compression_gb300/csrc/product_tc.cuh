@@ -212,9 +212,7 @@ __device__ __forceinline__ int plane_a(int pass) { return (0x231130 >> 4 * (5 - 
 __device__ __forceinline__ int plane_b(int pass) { return (0x321310 >> 4 * (5 - pass)) & 15; }
 
 // ---------------------------------------------------------------- kernel
-enum TcMode { kTcOne, kTcSplit, kTcBoth };
-
-// One product, one whose terms are split, or two products at once, of which the first has the longer sums.
+// One product, or two at once, of which the first has the longer sums.
 struct TcMaps {
     CUtensorMap a[2], b[2];
 };
@@ -224,81 +222,86 @@ template <typename Epi> struct TcParams {
     Epi epi[2];
 };
 
-// What a pair of CTAs does: its i-th tile. Of one product: every pairs-th. Of two: the first one's tiles in the same way,
-// then of the second one's so many that all pairs have about as much to do: those with a tile more of the first product
-// (the first `more` pairs) `few` of them, the others `many`.
+// What each pair of CTAs does when two products are computed at once: of the first one's units (tiles, or parts of
+// their sums) every pairs-th; then of the second one's so many that all pairs have about as much to do: those with
+// a unit more of the first (the first `more` pairs) `few` of them, the others `many`. Also on the host, which compares
+// ways to split the sums by it.
+struct TcShares {
+    int64_t more, each, few, many, blocks;  // blocks: what the busiest pair has to do
+    __host__ __device__ TcShares(int64_t pairs, int64_t units_a, int64_t a, int64_t units_b, int64_t b)
+    {
+        each = units_a / pairs;
+        more = units_a - each * pairs;
+        b = b > 0 ? b : 1;
+        for (blocks = (a * units_a + b * units_b + pairs - 1) / pairs;; blocks += b) {
+            few = blocks > a * (each + 1) ? (blocks - a * (each + 1)) / b : 0;
+            many = blocks > a * each ? (blocks - a * each) / b : 0;
+            if (more * few + (pairs - more) * many >= units_b) break;
+        }
+        if (more && blocks < a * (each + 1)) blocks = a * (each + 1);
+    }
+};
+
 struct TcUnit {
     int32_t m0, n0, from, count, split, which;
 };
 
-template <int kN, int kMode> struct TcSchedule {
-    int32_t m[2], n[2], tiles_m[2], tiles_n[2], blocks[2], group[2], splits, per_split, pairs, pair;
-    int64_t tiles[2], more, few, many, mine;  // mine: of the first product
+// (Counts of units fit in 32 bits: 2^31 tiles would be a result of 2^47 elements.)
+template <int kN, bool kBoth> struct TcSchedule {
+    int32_t m[2], tiles_m[2], tiles_n[2], blocks[2], per_split[2], tiles[2], units[2], more, few, many, mine;
 
     __device__ __forceinline__ TcSchedule(const TcArgs (&g)[2])
     {
-        pairs = gridDim.x / 2;
-        pair = blockIdx.x / 2;
+        const int32_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
 #pragma unroll
-        for (int i = 0; i < (kMode == kTcBoth ? 2 : 1); ++i) {
+        for (int i = 0; i < (kBoth ? 2 : 1); ++i) {
             m[i] = (int32_t)(g[i].m_count ? *g[i].m_count : g[i].m);
-            n[i] = (int32_t)g[i].n;
             const int32_t terms = (int32_t)(g[i].k_count ? *g[i].k_count : g[i].k);
             tiles_m[i] = (m[i] + kTcM - 1) / kTcM;
-            tiles_n[i] = (n[i] + kN - 1) / kN;
+            tiles_n[i] = ((int32_t)g[i].n + kN - 1) / kN;
             blocks[i] = (terms + kTcDepth - 1) / kTcDepth;
-            group[i] = g[i].group;
-            tiles[i] = (int64_t)tiles_m[i] * tiles_n[i];
+            per_split[i] = (blocks[i] + g[i].splits - 1) / g[i].splits;
+            tiles[i] = tiles_m[i] * tiles_n[i];
+            units[i] = tiles[i] * g[i].splits;
         }
-        splits = kMode == kTcSplit ? g[0].splits : 1;
-        per_split = (blocks[0] + splits - 1) / splits;
-        if constexpr (kMode == kTcBoth) {
-            const int64_t a = blocks[0], b = blocks[1] > 0 ? blocks[1] : 1, each = tiles[0] / pairs;
-            more = tiles[0] - each * pairs;
-            mine = each + (pair < more);
-            for (int64_t t = (a * tiles[0] + b * tiles[1] + pairs - 1) / pairs;; t += b) {
-                few = t > a * (each + 1) ? (t - a * (each + 1)) / b : 0;
-                many = t > a * each ? (t - a * each) / b : 0;
-                if (more * few + (pairs - more) * many >= tiles[1]) break;
-            }
+        if constexpr (kBoth) {
+            const TcShares shares(pairs, units[0], per_split[0], units[1], per_split[1]);
+            more = (int32_t)shares.more;
+            few = (int32_t)shares.few;
+            many = (int32_t)shares.many;
+            mine = (int32_t)shares.each + (pair < more);  // of the first product
         }
     }
 
-    __device__ __forceinline__ bool at(int64_t i, TcUnit& t) const
+    __device__ __forceinline__ bool at(const TcArgs (&g)[2], int32_t i, TcUnit& t) const
     {
-        int64_t tile = pair + i * pairs;
-        t.which = 0;
-        t.split = 0;
-        if constexpr (kMode == kTcSplit) {
-            if (tile >= tiles[0] * splits) return false;
-            t.split = (int32_t)(tile / tiles[0]);
-            tile -= t.split * tiles[0];
-        } else if constexpr (kMode == kTcBoth) {
-            if (i >= mine) {
-                const int64_t j = i - mine;
-                t.which = 1;
-                if (j >= (pair < more ? few : many)) return false;
-                tile = pair < more ? j * more + pair : more * few + j * (pairs - more) + (pair - more);
-                if (tile >= tiles[1]) return false;
-            }
-        } else {
-            if (tile >= tiles[0]) return false;
+        const int32_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+        int32_t unit = pair + i * pairs;
+        bool second = false;
+        if (kBoth && i >= mine) {
+            const int32_t j = i - mine;
+            second = true;
+            if (j >= (pair < more ? few : many)) return false;
+            unit = pair < more ? j * more + pair : more * few + j * (pairs - more) + (pair - more);
         }
-        const int w = kMode == kTcBoth ? t.which : 0;
-        const int32_t tm = w ? tiles_m[1] : tiles_m[0], tn = w ? tiles_n[1] : tiles_n[0], gr = w ? group[1] : group[0];
-        const int64_t whole = (int64_t)gr * tn;
-        const int32_t band = (int32_t)(tile / whole), in = (int32_t)(tile - band * whole);
+        if (unit >= (second ? units[1] : units[0])) return false;
+        t.which = second;
+        const int32_t tm = second ? tiles_m[1] : tiles_m[0], tn = second ? tiles_n[1] : tiles_n[0], gr = g[second].group;
+        const int32_t all = second ? blocks[1] : blocks[0], part = second ? per_split[1] : per_split[0];
+        const int32_t count = second ? tiles[1] : tiles[0];
+        t.split = unit / count;
+        const int32_t tile = unit - t.split * count, whole = gr * tn, band = tile / whole, in = tile - band * whole;
         const int32_t rows = tm - band * gr < gr ? tm - band * gr : gr;
         t.n0 = in / rows * kN;
         t.m0 = (band * gr + in % rows) * kTcM;
-        t.from = t.split * per_split;
-        t.count = w ? blocks[1] : blocks[0] - t.from < per_split ? blocks[0] - t.from : per_split;
+        t.from = t.split * part;
+        t.count = all - t.from < part ? all - t.from : part;
         if (t.count < 0) t.count = 0;
         return true;
     }
 };
 
-template <int kN, int kMode, typename Epi>
+template <int kN, bool kBoth, typename Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     product_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcParams<Epi> params)
 {
@@ -326,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         dead_flag = 0;
         ptx::fence_mbar_init();
 #pragma unroll
-        for (int i = 0; i < (kMode == kTcBoth ? 2 : 1); ++i) {
+        for (int i = 0; i < (kBoth ? 2 : 1); ++i) {
             tc::prefetch(&maps.a[i]);
             tc::prefetch(&maps.b[i]);
         }
@@ -342,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     tc::fence_after();
     const uint32_t tmem = tmem_at;
     ptx::griddep_wait();
-    const TcSchedule<kN, kMode> schedule(params.g);
+    const TcSchedule<kN, kBoth> schedule(params.g);
     TcUnit t;
 
     // 384 threads of 168 registers: 128 with 40 and 256 with 232 are as many
@@ -352,9 +355,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             uint32_t at_stage = 0, turn = 0, issued = 0;
             const uint32_t full_at = tc::map_shared(full, 0);  // the first CTA's
             bool alive = true;
-            for (int64_t u = 0; alive && schedule.at(u, t); ++u) {
-                const TcArgs& g = params.g[kMode == kTcBoth ? t.which : 0];
-                const CUtensorMap *map_a = &maps.a[kMode == kTcBoth ? t.which : 0], *map_b = &maps.b[kMode == kTcBoth ? t.which : 0];
+            for (int32_t u = 0; alive && schedule.at(params.g, u, t); ++u) {
+                const TcArgs& g = params.g[kBoth ? t.which : 0];
+                const CUtensorMap *map_a = &maps.a[kBoth ? t.which : 0], *map_b = &maps.b[kBoth ? t.which : 0];
                 const int passes = g.planes == 1 ? 1 : 6;
                 const int32_t ma = t.m0 + (int32_t)rank * 128, nb = t.n0 + (int32_t)rank * (kN / 2);
                 for (int32_t from = 0; from < t.count && alive; from += g.run) {
@@ -400,8 +403,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         } else if (warp == 1 && rank == 0) {  // products
             uint32_t at_stage = 0, turn = 0, done = 0;
             bool alive = true;
-            for (int64_t u = 0; alive && schedule.at(u, t); ++u) {
-                const TcArgs& g = params.g[kMode == kTcBoth ? t.which : 0];
+            for (int32_t u = 0; alive && schedule.at(params.g, u, t); ++u) {
+                const TcArgs& g = params.g[kBoth ? t.which : 0];
                 const int passes = g.planes == 1 ? 1 : 6;
                 const uint32_t kind = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(g.a_mn != 0) << 15 | (uint32_t)(g.b_mn != 0) << 16 |
                                       (uint32_t)(kN / 8) << 17 | (uint32_t)(kTcM / 16) << 24;
@@ -449,10 +452,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const uint32_t freed[2] = {tc::map_shared(&sums_empty[0], 0), tc::map_shared(&sums_empty[1], 0)};
         uint32_t done = 0;
         bool alive = true;
-        for (int64_t u = 0; schedule.at(u, t); ++u) {
-            const TcArgs& g = params.g[kMode == kTcBoth ? t.which : 0];
-            const Epi& epi = params.epi[kMode == kTcBoth ? t.which : 0];
-            const int32_t m = kMode == kTcBoth && t.which ? schedule.m[1] : schedule.m[0], n = (int32_t)g.n;
+        for (int32_t u = 0; schedule.at(params.g, u, t); ++u) {
+            const TcArgs& g = params.g[kBoth ? t.which : 0];
+            const Epi& epi = params.epi[kBoth ? t.which : 0];
+            const int32_t m = kBoth && t.which ? schedule.m[1] : schedule.m[0], n = (int32_t)g.n;
             const int32_t r = t.m0 + (int32_t)rank * 128 + quarter * 32 + lane, c0 = t.n0 + strip * kStrip;
             typename Epi::State state = {};
             if (r < m && c0 < n) state = epi.begin(r, c0);
@@ -460,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int i = 0; i < kStrip; ++i) v[i] = 0.0f;
             if constexpr (Epi::kAdds) {
-                if (epi.adds()) {  // what the sums are added to, while they are computed
+                if (epi.adds() && g.splits == 1) {  // what the sums are added to, while they are computed
 #pragma unroll
                     for (int c = 0; c < kStrip; c += 32) {
                         if (c0 + c >= n) break;
@@ -507,8 +510,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) stage.at(lane, i) = make_float4(v[c + 4 * i], v[c + 4 * i + 1], v[c + 4 * i + 2], v[c + 4 * i + 3]);
                     __syncwarp();
-                    if constexpr (kMode == kTcSplit) epi.of_split(t.split).chunk(stage, state, r - lane, m, c0 + c);
-                    else epi.chunk(stage, state, r - lane, m, c0 + c);
+                    if constexpr (Epi::kAdds) {
+                        if (g.splits > 1) {
+                            epi.part(stage, t.split, r - lane, m, c0 + c);
+                            __syncwarp();
+                            continue;
+                        }
+                    }
+                    epi.chunk(stage, state, r - lane, m, c0 + c);
                     __syncwarp();
                 }
             }
@@ -521,9 +530,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 }
 
 // ---------------------------------------------------------------- host
-// The sums of the parts that the terms were split into, one after the other, handed to an epilogue. A thread has four of a row's
-// columns.
-constexpr int kJoin = 4;
+// The sums of the parts that the terms were split into, one after the other, handed to an epilogue. A thread has four of a
+// row's columns, or one.
 struct JoinPartsArgs {
     const float* part;  // [splits][m][stride]
     int64_t m, n, stride;
@@ -531,25 +539,30 @@ struct JoinPartsArgs {
     int32_t splits;
 };
 
-template <typename Epi> __global__ void __launch_bounds__(kRows) join_parts_kernel(const JoinPartsArgs a, const Epi epi)
+template <int N, typename Epi> __global__ void __launch_bounds__(kRows) join_parts_kernel(const JoinPartsArgs a, const Epi epi)
 {
     ptx::griddep_wait();
     const int64_t m = a.m_count ? *a.m_count : a.m;
-    const int64_t chunks = (a.n + kJoin - 1) / kJoin, i = (int64_t)blockIdx.x * kRows + threadIdx.x;
+    const int64_t chunks = (a.n + N - 1) / N, i = (int64_t)blockIdx.x * kRows + threadIdx.x;
     if (i >= chunks * m) return;
-    const int64_t r = i / chunks, c = (i - r * chunks) * kJoin;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int64_t r = i / chunks, c = (i - r * chunks) * N;
+    Cols<N> v = {};
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) v = v + get4(a.part + ((int64_t)s * a.m + r) * a.stride + c, 4, true);
+    for (int s = 0; s < a.splits; ++s) v = v + get<N>(a.part + ((int64_t)s * a.m + r) * a.stride + c, 4);
     epi.piece((int32_t)r, (int32_t)c, v);
 }
 
-// A product of no terms: the epilogue of zeros.
-template <typename T, typename Epi> cudaError_t product_none(int64_t m, int64_t n, const Epi& epi, cudaStream_t stream)
+template <typename Epi> cudaError_t join_parts(const JoinPartsArgs& j, const Epi& epi, cudaStream_t stream)
 {
-    const JoinPartsArgs j = {nullptr, m, n, 0, nullptr, 0};
-    const int64_t all = (n + kJoin - 1) / kJoin * m;
-    return launch_after(join_parts_kernel<Epi>, dim3((unsigned)((all + kRows - 1) / kRows)), dim3(kRows), 0, stream, j, epi);
+    const int64_t all = (j.n + (epi.whole ? 3 : 0)) / (epi.whole ? 4 : 1) * j.m;
+    return launch_after(epi.whole ? join_parts_kernel<4, Epi> : join_parts_kernel<1, Epi>, dim3((unsigned)((all + kRows - 1) / kRows)),
+                        dim3(kRows), 0, stream, j, epi);
+}
+
+// A product of no terms: the epilogue of zeros.
+template <typename Epi> cudaError_t product_none(int64_t m, int64_t n, const Epi& epi, cudaStream_t stream)
+{
+    return join_parts(JoinPartsArgs{nullptr, m, n, 0, nullptr, 0}, epi, stream);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -595,12 +608,12 @@ inline bool as_it_lies(const void* p, int64_t stride, int64_t rows, int64_t cols
 
 inline Matrix matrix_of(const void* p, int64_t stride, int64_t rows, int64_t cols)
 {
-    return {static_cast<const bf16*>(p), rows, cols, rows < 2 ? round_up(cols, 8) : stride, 0};
+    return {static_cast<const bf16*>(p), rows, cols, rows < 2 ? pitch_of(cols) : stride, 0};
 }
 
 inline int64_t packed_elements(int64_t rows, int64_t cols, int bytes)  // of a workspace
 {
-    return rows * round_up(cols, 8) * (bytes == 4 ? kPlanes : 1);
+    return rows * pitch_of(cols) * (bytes == 4 ? kPlanes : 1);
 }
 
 // A matrix of T's as a product takes it: as it lies, or copied to `room` (packed_elements).
@@ -613,28 +626,28 @@ cudaError_t take_matrix(Matrix* out, const void* p, int64_t stride, int64_t rows
         return cudaSuccess;
     }
     const int64_t to_rows = count ? out_rows : rows;
-    *out = {room, to_rows, cols, round_up(cols, 8), to_rows * round_up(cols, 8)};
+    *out = {room, to_rows, cols, pitch_of(cols), to_rows * pitch_of(cols)};
     PackArgs a = {p, room, map, count, rows, cols, stride, out->stride, out->plane, whole_rows(p, stride, rows, sizeof(T))};
     int sms = 0;
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const int64_t need = (to_rows * (out->stride / 8) + kTcPack - 1) / kTcPack, most = (int64_t)sms * 16;
+    const int64_t need = (to_rows * ((cols + 7) / 8) + kTcPack - 1) / kTcPack, most = (int64_t)sms * 16;
     if (need == 0) return cudaSuccess;
     return launch_after(pack_kernel<T>, dim3((unsigned)(need < most ? need : most)), dim3(kTcPack), 0, stream, a);
 }
 
-template <int kN, int kMode, typename Epi>
+template <int kN, bool kBoth, typename Epi>
 cudaError_t launch_tc(const TcMaps& maps, const TcParams<Epi>& p, cudaStream_t stream)
 {
-    cudaError_t e = allow<product_tc_kernel<kN, kMode, Epi>>(TcShape<kN>::kShared);
+    cudaError_t e = allow<product_tc_kernel<kN, kBoth, Epi>>(TcShape<kN>::kShared);
     int sms = 0;
     if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     int64_t units = 0;
-    for (int i = 0; i < (kMode == kTcBoth ? 2 : 1); ++i)
-        units += (p.g[i].m + kTcM - 1) / kTcM * ((p.g[i].n + kN - 1) / kN) * (kMode == kTcSplit ? p.g[i].splits : 1);
+    for (int i = 0; i < (kBoth ? 2 : 1); ++i)
+        units += (p.g[i].m + kTcM - 1) / kTcM * ((p.g[i].n + kN - 1) / kN) * p.g[i].splits;
     const int64_t pairs = sms / 2;
-    return launch_after(product_tc_kernel<kN, kMode, Epi>, dim3((unsigned)(2 * (units < pairs ? units : pairs))), dim3(kTcThreads),
+    return launch_after(product_tc_kernel<kN, kBoth, Epi>, dim3((unsigned)(2 * (units < pairs ? units : pairs))), dim3(kTcThreads),
                         TcShape<kN>::kShared, stream, maps, p);
 }
 
@@ -667,22 +680,39 @@ template <typename T, typename Epi> cudaError_t set_tc(TcMaps& maps, TcParams<Ep
     return e == cudaSuccess ? tensor_map(&maps.b[i], x.b, g.planes, x.b_mn ? kTcDepth : kN / 2) : e;
 }
 
-// The terms of a product with few tiles are split, so that more of the SMs have some; the parts' sums are joined by a
-// kernel of their own.
-constexpr int64_t kMostPairs = 76;
+// ---------------------------------------------------------------- which way
+// The terms of a product with few tiles, or of a few more than go round, are split, and the parts' sums joined by a kernel
+// of their own. By estimate, us: a block of 64 terms takes a pair 0.3 (fp32: six times that), a tile's end 2 more (its
+// epilogue's last part, which nothing covers), the parts' sums are written and read at 4 bytes each, and the joining kernel
+// begins 3 later.
+constexpr int64_t kPairs = 76, kMostParts = 2 * kPairs;  // tiles x splits are at most kMostParts, if split
 
-inline int splits_of(int64_t m, int64_t n, int64_t k)
+struct TcSize {
+    int64_t m, n, k;
+    int64_t tiles() const { return (m + kTcM - 1) / kTcM * ((n + 255) / 256); }
+    int64_t blocks(int s) const { return ((k + kTcDepth - 1) / kTcDepth + s - 1) / s; }
+    bool may(int s) const { return s == 1 || (tiles() * s <= kMostParts && blocks(1) >= 4 * s); }
+    double join(int s) const { return s == 1 ? 0.0 : 3.0 + (double)s * m * n * 8 / 5e6; }
+};
+
+inline int64_t parts_elements(int64_t m, int64_t n)  // of a workspace
 {
-    const int64_t tiles = (m + kTcM - 1) / kTcM * ((n + 255) / 256), blocks = (k + kTcDepth - 1) / kTcDepth;
-    int64_t s = kMostPairs / (tiles < 1 ? 1 : tiles);
-    if (s > blocks / 4) s = blocks / 4;
-    return (int)(s < 1 ? 1 : s);
+    const int64_t whole = kMostParts * kTcM * 256, all = kMostParts * m * round_up(n, 4);
+    return all < whole ? all : whole;
 }
 
-inline int64_t parts_elements(int64_t m, int64_t n)  // of a workspace: tiles x splits are at most kMostPairs
+inline double cost_of(const TcSize& x, int s, double block)
 {
-    const int64_t whole = kMostPairs * kTcM * 256, all = kMostPairs * m * round_up(n, 4);
-    return all < whole ? all : whole;
+    const int64_t waves = (x.tiles() * s + kPairs - 1) / kPairs;
+    return waves * (x.blocks(s) * block + 2.0) + x.join(s);
+}
+
+inline int splits_of(const TcSize& x, double block)
+{
+    int best = 1;
+    for (int s = 2; x.may(s); ++s)
+        if (cost_of(x, s, block) < 0.95 * cost_of(x, best, block)) best = s;
+    return best;
 }
 
 // A product of matrices of T's planes. parts: room for parts_elements.
@@ -691,46 +721,70 @@ template <typename T, typename Epi> cudaError_t product_tc(const TcProduct& x, f
     if (x.m <= 0 || x.n <= 0) return cudaSuccess;
     TcMaps maps = {};
     if constexpr (Epi::kPieces) {
-        const int splits = splits_of(x.m, x.n, x.k);
+        const int splits = splits_of(TcSize{x.m, x.n, x.k}, sizeof(T) == 4 ? 1.8 : 0.3);
         if (splits > 1) {
-            EpiStore<float> each = {};
-            each.out = parts;
-            each.stride = round_up(x.n, 4);
-            each.split_stride = x.m * each.stride;
+            EpiStore<T> each = {};
+            each.acc = parts;
+            each.acc_stride = round_up(x.n, 4);
+            each.split_stride = x.m * each.acc_stride;
             each.n = (int32_t)x.n;
-            each.first = each.last = each.whole = true;
-            TcParams<EpiStore<float>> p = {};
+            each.first = true;
+            TcParams<EpiStore<T>> p = {};
             cudaError_t e = set_tc<T>(maps, p, 0, x, each);
             if (e != cudaSuccess) return e;
             p.g[0].splits = splits;
-            if (!Epi::kExact) p.g[0].run = 1 << 30;
-            e = launch_tc<256, kTcSplit>(maps, p, stream);
-            if (e != cudaSuccess) return e;
-            const JoinPartsArgs j = {parts, x.m, x.n, each.stride, x.m_count, splits};
-            const int64_t all = (x.n + kJoin - 1) / kJoin * x.m;
-            return launch_after(join_parts_kernel<Epi>, dim3((unsigned)((all + kRows - 1) / kRows)), dim3(kRows), 0, stream, j, epi);
+            e = launch_tc<256, false>(maps, p, stream);
+            return e == cudaSuccess ? join_parts(JoinPartsArgs{parts, x.m, x.n, each.acc_stride, x.m_count, splits}, epi, stream) : e;
         }
     }
     TcParams<Epi> p = {};
     const cudaError_t e = set_tc<T>(maps, p, 0, x, epi);
-    return e == cudaSuccess ? launch_tc<256, kTcOne>(maps, p, stream) : e;
+    return e == cudaSuccess ? launch_tc<256, false>(maps, p, stream) : e;
 }
 
-// Two products, neither of which needs the other: in one launch, so that the tiles of one fill the SMs that the other's last
-// ones leave idle (8192 rows, 16384 tokens of a vocabulary, width 2048, bf16: 608 -> 5xx us), unless they are small.
+// Two products, neither of which needs the other, in one launch, so that the units of one fill the SMs that the other's last
+// ones leave idle. parts: room for both's parts_elements, the first's first.
 template <typename T, typename Epi>
 cudaError_t product_tc_both(const TcProduct& x, const Epi& epi_x, const TcProduct& y, const Epi& epi_y, float* parts, cudaStream_t stream)
 {
-    if (splits_of(x.m, x.n, x.k) > 1 || splits_of(y.m, y.n, y.k) > 1) {
-        const cudaError_t e = product_tc<T>(x, parts, epi_x, stream);
-        return e == cudaSuccess ? product_tc<T>(y, parts, epi_y, stream) : e;
+    constexpr double block = sizeof(T) == 4 ? 1.8 : 0.3;
+    const TcSize size[2] = {{x.m, x.n, x.k}, {y.m, y.n, y.k}};
+    int best[2] = {1, 1};
+    double least = -1.0;
+    const int alone[2] = {splits_of(size[0], block), splits_of(size[1], block)};
+    for (int i = 0; i < 9; ++i) {  // each whole, as it would be alone, and half of that
+        const int s = i % 3 == 0 ? 1 : (alone[0] + i % 3 - 1) / (i % 3), t = i / 3 == 0 ? 1 : (alone[1] + i / 3 - 1) / (i / 3);
+        const bool turned = size[1].blocks(t) > size[0].blocks(s);  // the longer sums first
+        const TcSize &a = size[turned], &b = size[!turned];
+        const int sa = turned ? t : s, sb = turned ? s : t;
+        const int64_t units_a = a.tiles() * sa, units_b = b.tiles() * sb;
+        const TcShares shares(kPairs, units_a, a.blocks(sa), units_b, b.blocks(sb));
+        const double cost = shares.blocks * block + 2.0 * ((units_a + units_b + kPairs - 1) / kPairs) + size[0].join(s) + size[1].join(t);
+        if (least < 0.0 || cost < 0.98 * least) least = cost, best[0] = s, best[1] = t;
     }
-    const bool turned = y.k > x.k;  // the longer sums first
+    const bool turned = size[1].blocks(best[1]) > size[0].blocks(best[0]);
     TcMaps maps = {};
     TcParams<Epi> p = {};
-    cudaError_t e = set_tc<T>(maps, p, turned, x, epi_x);
-    if (e == cudaSuccess) e = set_tc<T>(maps, p, !turned, y, epi_y);
-    return e == cudaSuccess ? launch_tc<256, kTcBoth>(maps, p, stream) : e;
+    JoinPartsArgs joins[2] = {};
+    float* room[2] = {parts, parts + parts_elements(x.m, x.n)};
+    for (int i = 0; i < 2; ++i) {
+        const TcProduct& g = i ? y : x;
+        Epi epi = i ? epi_y : epi_x;
+        if (best[i] > 1) {
+            epi.acc = room[i];
+            epi.acc_stride = round_up(g.n, 4);
+            epi.split_stride = g.m * epi.acc_stride;
+            joins[i] = {room[i], g.m, g.n, epi.acc_stride, g.m_count, best[i]};
+        }
+        const int at = turned ? !i : i;
+        const cudaError_t e = set_tc<T>(maps, p, at, g, epi);
+        if (e != cudaSuccess) return e;
+        p.g[at].splits = best[i];
+    }
+    cudaError_t e = launch_tc<256, true>(maps, p, stream);
+    if (e == cudaSuccess && best[0] > 1) e = join_parts(joins[0], epi_x, stream);
+    if (e == cudaSuccess && best[1] > 1) e = join_parts(joins[1], epi_y, stream);
+    return e;
 }
 
 }  // namespace

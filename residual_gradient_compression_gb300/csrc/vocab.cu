@@ -67,11 +67,10 @@ VocabParts vocab_parts(Carve& c, int64_t rows, int64_t dim, int64_t vocab, int b
     p.w = c.take<bf16>(packed_elements(vocab, dim, bytes));
     if (backward) {
         p.piece = piece_of(rows, vocab);
-        p.dz_stride = round_up(p.piece, 8);
+        p.dz_stride = pitch_of(p.piece);
         p.dz = c.take<bf16>(packed_elements(p.padded, p.piece, bytes));
         p.acc = c.take<float>(rows * round_up(dim, 4));
-        const int64_t x = parts_elements(rows, dim), w = parts_elements(p.piece, dim);
-        p.parts = c.take<float>(x > w ? x : w);
+        p.parts = c.take<float>(parts_elements(rows, dim) + parts_elements(p.piece, dim));
     } else {
         p.part = c.take<float2>(rows * ((vocab + kStrip - 1) / kStrip));
         p.picked = c.take<float>(rows * k);
@@ -414,7 +413,7 @@ template <typename T> cudaError_t zero_rows(const VocabArgs& a, cudaStream_t str
     store.n = (int32_t)a.dim;
     store.first = store.last = true;
     store.whole = whole_rows(a.dw, a.dw_stride, a.vocab, sizeof(T));
-    return product_none<T>(a.vocab, a.dim, store, stream);
+    return product_none(a.vocab, a.dim, store, stream);
 }
 
 constexpr int64_t kMostDim = (int64_t)1 << 30, kMostRows = ((int64_t)1 << 30) + 1;
