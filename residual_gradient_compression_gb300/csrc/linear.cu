@@ -14,6 +14,7 @@ namespace adacomp {
 namespace {
 
 constexpr int kDzCols = 256, kDzRows = 8;  // of a CTA: a warp has 256 columns of a row
+constexpr int kDzFew = 32;                 // columns of one for few rows, of which it has 64 at a time
 constexpr int kDzSlices = 152;             // partial sums of db: one per slice of the rows
 constexpr int kDbCols = 32, kDbRows = 16;
 constexpr int64_t kOneSlice = 128;         // rows that one slice has, without a second kernel
@@ -47,12 +48,17 @@ LinearParts linear_parts(Carve& c, int64_t rows, int64_t in, int64_t out, int by
     return p;
 }
 
-// Which products are for the kernel of small matrices. us with it and without: fp32 256 x 512 x 512 12 and 21, 512 x 512 x 512
-// 21 and 21; bf16 256 x 256 x 256 8 and 10, 256 x 512 x 512 14 and 12.
-template <typename T> bool is_small(int64_t rows, int64_t in, int64_t out)
+// Which products are for the kernel of small matrices, by what its whole tiles of 32 x 32 and 128 terms compute. us with it
+// and without: fp32 256 x 512 x 512 12 and 17, 512 x 512 x 512 17 and 17, 2048 x 2048 of one term 66 and 14; bf16
+// 256 x 256 x 256 7 and 10, 128 x 512 x 512 12 and 9.
+template <typename T> bool is_small(int64_t m, int64_t n, int64_t k)
 {
-    constexpr int64_t most = (int64_t)1 << (sizeof(T) == 4 ? 26 : 24);
-    return rows * in <= most && rows * in * out <= most;
+    constexpr int64_t most = (int64_t)1 << (sizeof(T) == 4 ? 27 : 24);
+    const auto at_least = [](int64_t x, int64_t least) { return x > least ? x : least; };
+    m = at_least(m, kSmallTile);
+    n = at_least(n, kSmallTile);
+    k = at_least(k, kSmallDepth);
+    return m <= most / n && m * n <= most / k;
 }
 
 struct DzArgs {
@@ -97,7 +103,7 @@ template <typename T> struct Eight {
 // dz = dy * act'(pre), and its sums over slices of the rows. Bound by memory: a thread has eight columns of every
 // kDzRows-th row of a slice, several rows under way at a time; the CTA's sums meet in shared memory, the slices' in a
 // second kernel, in a fixed order.
-template <typename T, int kAct> __device__ __forceinline__ void dz_rows(const DzArgs& a, int32_t c, float (&sum)[8])
+template <typename T, int kAct, int kDzRows> __device__ __forceinline__ void dz_rows(const DzArgs& a, int32_t c, float (&sum)[8])
 {
     constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
     const T *dy = static_cast<const T*>(a.dy) + c, *pre = static_cast<const T*>(a.pre) + c;
@@ -129,18 +135,19 @@ template <typename T, int kAct> __device__ __forceinline__ void dz_rows(const Dz
     }
 }
 
-template <typename T> __global__ void __launch_bounds__(kDzCols / 8 * kDzRows, sizeof(T) == 2 ? 4 : 3) linear_dz_kernel(const DzArgs a)
+template <typename T, int kDzCols, int kDzRows>
+__global__ void __launch_bounds__(kDzCols / 8 * kDzRows, sizeof(T) == 2 ? 4 : 3) linear_dz_kernel(const DzArgs a)
 {
     __shared__ float sums[kDzRows][kDzCols];
     ptx::griddep_wait();
     const int32_t c = blockIdx.x * kDzCols + threadIdx.x * 8;
     float sum[8] = {};
     if (c < a.n) switch (a.act) {
-        case ADACOMP_ACT_RELU: dz_rows<T, ADACOMP_ACT_RELU>(a, c, sum); break;
-        case ADACOMP_ACT_GELU: dz_rows<T, ADACOMP_ACT_GELU>(a, c, sum); break;
-        case ADACOMP_ACT_GELU_TANH: dz_rows<T, ADACOMP_ACT_GELU_TANH>(a, c, sum); break;
-        case ADACOMP_ACT_SILU: dz_rows<T, ADACOMP_ACT_SILU>(a, c, sum); break;
-        default: dz_rows<T, ADACOMP_ACT_NONE>(a, c, sum);
+        case ADACOMP_ACT_RELU: dz_rows<T, ADACOMP_ACT_RELU, kDzRows>(a, c, sum); break;
+        case ADACOMP_ACT_GELU: dz_rows<T, ADACOMP_ACT_GELU, kDzRows>(a, c, sum); break;
+        case ADACOMP_ACT_GELU_TANH: dz_rows<T, ADACOMP_ACT_GELU_TANH, kDzRows>(a, c, sum); break;
+        case ADACOMP_ACT_SILU: dz_rows<T, ADACOMP_ACT_SILU, kDzRows>(a, c, sum); break;
+        default: dz_rows<T, ADACOMP_ACT_NONE, kDzRows>(a, c, sum);
         }
     if (!a.sums && !a.db) return;
 #pragma unroll
@@ -190,7 +197,7 @@ template <typename T> cudaError_t linear_forward(const LinearArgs& a, void* ws, 
                 is_aligned(a.bias, 16) && whole_rows(a.residual, a.residual_stride, a.rows, sizeof(T));
     if (a.rows <= (sizeof(T) == 2 ? kFewBf16 : kFewF32))
         return product_few<T>(FewArgs{a.x, a.w, a.x_stride, a.w_stride, (int32_t)a.rows, (int32_t)a.out, (int32_t)a.in}, epi, stream);
-    if (is_small<T>(a.rows, a.in, a.out))
+    if (is_small<T>(a.rows, a.out, a.in))
         return product_small<T>(SmallArgs{{a.x, a.x_stride, 1}, {a.w, a.w_stride, 1}, (int32_t)a.rows, (int32_t)a.out, (int32_t)a.in}, epi, stream);
     Carve carve{static_cast<char*>(ws)};
     const LinearParts p = linear_parts(carve, a.rows, a.in, a.out, sizeof(T), false);
@@ -206,7 +213,7 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
 {
     Carve carve{static_cast<char*>(ws)};
     const LinearParts p = linear_parts(carve, a.rows, a.in, a.out, sizeof(T), true);
-    const bool act = a.act != ADACOMP_ACT_NONE, products = a.dx || a.dw, small = is_small<T>(a.rows, a.in, a.out);
+    const bool act = a.act != ADACOMP_ACT_NONE, products = a.dx || a.dw, small = is_small<T>(a.rows, a.in, a.out) && is_small<T>(a.out, a.in, a.rows);
     cudaError_t e = cudaSuccess;
     Matrix dz = {p.dz, a.rows, a.out, pitch_of(a.out), a.rows * pitch_of(a.out)}, x, w;
     if ((act && products) || a.db) {
@@ -234,7 +241,8 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
             d.db = a.db;
             d.sums = nullptr;
         }
-        e = launch_after(linear_dz_kernel<T>, dim3((unsigned)blocks, d.slices), dim3(kDzCols / 8, kDzRows), 0, stream, d);
+        e = d.slices == 1 ? launch_after(linear_dz_kernel<T, kDzFew, 64>, dim3((unsigned)((a.out + kDzFew - 1) / kDzFew)), dim3(kDzFew / 8, 64), 0, stream, d)
+                          : launch_after(linear_dz_kernel<T, kDzCols, kDzRows>, dim3((unsigned)blocks, d.slices), dim3(kDzCols / 8, kDzRows), 0, stream, d);
         if (e == cudaSuccess && a.db && !d.db)
             e = launch_after(linear_db_kernel<T>, dim3((unsigned)((a.out + kDbCols - 1) / kDbCols)), dim3(kDbCols, kDbRows), 0, stream,
                              (const float*)p.sums, static_cast<T*>(a.db), a.out, d.slices);

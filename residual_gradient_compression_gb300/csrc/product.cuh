@@ -2,8 +2,8 @@
 // sums (the epilogues).
 //
 // A product is C(m, n) = sum over k of A(m, k) B(n, k). A warp of the kernel that forms it has 32 rows' sums in registers,
-// 128 columns of a row per thread, and hands them to an epilogue in two steps: rows(), a thread its row, with
-// what begin() loaded before the sums were there; and chunk(), the warp 32 columns at a time through shared memory, so that
+// 128 columns of a row per thread, and hands them to an epilogue in two steps: rows(), a thread its row (from
+// column c up to `last`, the strip-th of the row), with what begin() loaded before the sums were there; and chunk(), the warp 32 columns at a time through shared memory, so that
 // what it reads and writes in global memory are whole pieces of rows (a thread that writes its own row takes 32 cache
 // lines at a time: a linear layer's forward product of 8192 x 2048 x 16384 bf16 took 369 us so, and 313 without its
 // stores). kExact: the results are held in fp32, so the sums are formed in short runs.
@@ -290,7 +290,7 @@ template <typename T> struct EpiLinear {
     bool whole;  // all of them
     struct State {};
     __device__ __forceinline__ State begin(int32_t, int32_t) const { return {}; }
-    __device__ __forceinline__ void rows(const State&, int32_t, int32_t, bool, float (&)[kStrip]) const {}
+    __device__ __forceinline__ void rows(const State&, int32_t, int32_t, int32_t, int32_t, bool, float (&)[kStrip]) const {}
 
     template <int N, typename F> __device__ __forceinline__ void turns(const Stage& stage, int32_t r0, int32_t end, int32_t c0, F f) const
     {
@@ -383,7 +383,7 @@ template <typename T> struct EpiStore {
     };
     __device__ __forceinline__ State begin(int32_t r, int32_t) const { return {map ? map[r] : r}; }
     __device__ __forceinline__ bool adds() const { return !first; }
-    __device__ __forceinline__ void rows(const State&, int32_t, int32_t, bool, float (&)[kStrip]) const {}
+    __device__ __forceinline__ void rows(const State&, int32_t, int32_t, int32_t, int32_t, bool, float (&)[kStrip]) const {}
 
     __device__ __forceinline__ void take(const Stage& stage, int32_t r0, int32_t end, int32_t c0) const
     {
@@ -482,7 +482,7 @@ __device__ __forceinline__ int32_t next_token(const Lists& l, const Place& p, in
     return at < l.k ? l.index[p.list + at] : INT32_MAX;
 }
 
-// Of each strip of 128 logits of a row: their maximum and the sum of exp(z - maximum); and the logits
+// Of each strip of up to 128 logits of a row: their maximum and the sum of exp(z - maximum); and the logits
 // of the listed tokens.
 template <typename T> struct EpiSoftmax {
     static constexpr bool kExact = true, kChunks = false, kPieces = false, kAdds = false;
@@ -490,14 +490,13 @@ template <typename T> struct EpiSoftmax {
     float* picked;
     Lists lists;
     int64_t row_stride;
-    int32_t n;
     float scale;  // of the logits: 1 / temperature
     using State = Place;
     __device__ __forceinline__ State begin(int32_t r, int32_t c) const { return place_of(lists, lists.map[r], c); }
-    __device__ __forceinline__ void rows(const State& s, int32_t r, int32_t c, bool live, float (&v)[kStrip]) const
+    __device__ __forceinline__ void rows(const State& s, int32_t r, int32_t c, int32_t last, int32_t strip, bool live, float (&v)[kStrip]) const
     {
         if (!live) return;
-        const int32_t end = n - c < kStrip ? n : c + kStrip;
+        const int32_t end = last - c < kStrip ? last : c + kStrip;
 #pragma unroll
         for (int i = 0; i < kStrip; ++i) v[i] *= scale;
         for (int32_t at = s.at, token = s.token; token < end; token = next_token(lists, s, ++at)) {
@@ -518,7 +517,7 @@ template <typename T> struct EpiSoftmax {
         float sum[4] = {};
 #pragma unroll
         for (int i = 0; i < kStrip; ++i) sum[i & 3] += exp_of<T>(v[i] - less);
-        part[c / kStrip * row_stride + r] = make_float2(top[0], (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        part[strip * row_stride + r] = make_float2(top[0], (sum[0] + sum[1]) + (sum[2] + sum[3]));
     }
     __device__ __forceinline__ void chunk(const Stage&, const State&, int32_t, int32_t, int32_t) const {}
 };
@@ -544,7 +543,7 @@ template <typename T> struct EpiGradient {
         if (given[row] != given[row]) s.factor = given[row];  // a row that has no value
         return s;
     }
-    __device__ __forceinline__ void rows(const State& s, int32_t, int32_t c, bool live, float (&v)[kStrip]) const
+    __device__ __forceinline__ void rows(const State& s, int32_t, int32_t c, int32_t, int32_t, bool live, float (&v)[kStrip]) const
     {
         if (!live) {
 #pragma unroll

@@ -93,18 +93,20 @@ __global__ void __launch_bounds__(kWarps * 32) few_bf16_kernel(const FewArgs g, 
     put_piece(epi, r, c0 + c, v);
 }
 
-// The same of fp32 numbers: a warp has four rows of the weights, its lanes four terms each at a time.
+// The same of fp32 numbers: a warp has four rows of the weights, its lanes four terms each at a time. (8 x 2048 x 8192 32 us,
+// bound by the tokens' loads from L1, of which there are two for one of the weights'; two rows a warp 44.)
 template <typename Epi, int kTokens, bool kWhole>
 __global__ void __launch_bounds__(256, 2) few_f32_kernel(const FewArgs g, const Epi epi)
 {
+    constexpr int kOut = 4;
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int32_t c0 = (blockIdx.x * 8 + threadIdx.x / 32) * 4;
+    const int32_t c0 = (blockIdx.x * 8 + threadIdx.x / 32) * kOut;
     if (c0 >= g.n) return;
     const float* w = static_cast<const float*>(g.w);
     const float* x = static_cast<const float*>(g.x);
-    float d[kTokens][4] = {};
-#pragma unroll 1
+    float d[kTokens][kOut] = {};
+#pragma unroll(kTokens == 8 ? 1 : 2)
     for (int32_t k = lane * 4; k < g.k; k += 128) {
         const auto load = [&](const float* p, int32_t left) {
             if constexpr (kWhole) {
@@ -116,23 +118,25 @@ __global__ void __launch_bounds__(256, 2) few_f32_kernel(const FewArgs g, const 
                 return v;
             }
         };
-        Cols<4> a[4];
+        Cols<4> a[kOut];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = load(w + (c0 + i) * g.w_stride + k, c0 + i < g.n ? g.k - k : 0);
+        for (int i = 0; i < kOut; ++i) a[i] = load(w + (c0 + i) * g.w_stride + k, c0 + i < g.n ? g.k - k : 0);
 #pragma unroll
         for (int t = 0; t < kTokens; ++t) {
             const Cols<4> b = load(x + t * g.x_stride + k, t < g.rows ? g.k - k : 0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kOut; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[t][i] = fmaf(a[i].v[j], b.v[j], d[t][i]);
         }
     }
 #pragma unroll
     for (int t = 0; t < kTokens; ++t) {
+        Cols<4> v = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[t][i] = warp_sum(d[t][i]);
-        if (lane == t && t < g.rows) put_piece(epi, t, c0, Cols<4>{{d[t][0], d[t][1], d[t][2], d[t][3]}});
+        for (int i = 0; i < kOut; ++i) v.v[i] = warp_sum(d[t][i]);
+        if (lane != t || t >= g.rows) continue;
+        put_piece(epi, t, c0, v);
     }
 }
 
@@ -163,13 +167,15 @@ struct Operand {
 
 struct SmallArgs {
     Operand a, b;
-    int32_t m, n, k;
+    int32_t m, n, k, parts;
 };
 
 constexpr int kSmallTile = 32, kSmallDepth = 128;
 
 // A CTA has a tile of 32 x 32, 128 terms at a time in shared memory, of which a warp has 16; a thread has 4 x 8 of the
-// tile's sums, fp32, in its warp's terms; the warps' sums meet in shared memory.
+// tile's sums, fp32, in its warp's terms; the warps' sums meet in shared memory. A block of terms takes over a
+// microsecond, most of it waiting for loads, so where tiles are few the terms are split over the CTAs of a cluster, whose sums the
+// first one reads from the others' shared memory.
 template <typename T, typename Epi> __global__ void __launch_bounds__(256) product_small_kernel(const SmallArgs g, const Epi epi)
 {
     constexpr int kPitch = kSmallTile + 4, kEach = kSmallTile * kSmallDepth / 256;
@@ -177,7 +183,10 @@ template <typename T, typename Epi> __global__ void __launch_bounds__(256) produ
     float *sa = tile, *sb = tile + kSmallDepth * kPitch;
     ptx::griddep_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, r = lane / 4 * 4, c = lane % 4 * 8;
-    const int32_t tiles_n = (g.n + kSmallTile - 1) / kSmallTile, m0 = blockIdx.x / tiles_n * kSmallTile, n0 = blockIdx.x % tiles_n * kSmallTile;
+    const int32_t place = blockIdx.x / g.parts, part = blockIdx.x % g.parts, tiles_n = (g.n + kSmallTile - 1) / kSmallTile;
+    const int32_t m0 = place / tiles_n * kSmallTile, n0 = place % tiles_n * kSmallTile;
+    const int32_t blocks = (g.k + kSmallDepth - 1) / kSmallDepth, each = (blocks + g.parts - 1) / g.parts;
+    const int32_t first = part * each * kSmallDepth, end = g.k - first < each * kSmallDepth ? g.k : first + each * kSmallDepth;
     // A thread's elements of an operand's block are kEach places `step` apart, along its rows or its terms.
     struct Mine {
         const T* p;
@@ -194,14 +203,14 @@ template <typename T, typename Epi> __global__ void __launch_bounds__(256) produ
         m.each = m.by_terms ? 256 / kSmallDepth : 256 / kSmallTile;
         m.step = m.each * (m.by_terms ? o.row : o.term);
         m.next = kSmallDepth * o.term;
-        m.p = static_cast<const T*>(o.p) + (r0 + m.row) * o.row + m.term * o.term;
+        m.p = static_cast<const T*>(o.p) + (r0 + m.row) * o.row + (int64_t)(first + m.term) * o.term;
         m.left = rows - r0 - m.row;
         m.at = m.term * kPitch + m.row;
         m.at_step = m.each * (m.by_terms ? 1 : kPitch);
         return m;
     };
     const auto load = [&](Mine& m, int32_t k0, float (&v)[kEach]) {
-        const int32_t terms = g.k - k0 - m.term;
+        const int32_t terms = end - k0 - m.term;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const bool there = m.by_terms ? terms > 0 && i * m.each < m.left : m.left > 0 && i * m.each < terms;
@@ -215,13 +224,13 @@ template <typename T, typename Epi> __global__ void __launch_bounds__(256) produ
     };
     float va[kEach], vb[kEach], d[4][8] = {};
     Mine ma = mine(g.a, m0, g.m), mb = mine(g.b, n0, g.n);
-    load(ma, 0, va);
-    load(mb, 0, vb);
-    for (int32_t k0 = 0; k0 < g.k; k0 += kSmallDepth) {
+    load(ma, first, va);
+    load(mb, first, vb);
+    for (int32_t k0 = first; k0 < end; k0 += kSmallDepth) {
         store(ma, sa, va);
         store(mb, sb, vb);
         __syncthreads();
-        if (k0 + kSmallDepth < g.k) {
+        if (k0 + kSmallDepth < end) {
             load(ma, k0 + kSmallDepth, va);
             load(mb, k0 + kSmallDepth, vb);
         }
@@ -245,17 +254,49 @@ template <typename T, typename Epi> __global__ void __launch_bounds__(256) produ
             *reinterpret_cast<float4*>(tile + (warp * kSmallTile + r + p) * kPitch + c + q) = make_float4(d[p][q], d[p][q + 1], d[p][q + 2], d[p][q + 3]);
     __syncthreads();
     const int row = threadIdx.x / 8, col = threadIdx.x % 8 * 4;
-    if (m0 + row >= g.m || n0 + col >= g.n) return;
     Cols<4> v = {};
 #pragma unroll
     for (int i = 0; i < 8; ++i) v = v + get<4>(tile + (i * kSmallTile + row) * kPitch + col, 4);
-    put_piece(epi, m0 + row, n0 + col, v);
+    if (g.parts > 1) {
+        float* mine_at = tile + row * kPitch + col;
+        __syncthreads();
+        put(mine_at, v, 4);
+        asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+        if (part == 0) {
+            for (int i = 1; i < g.parts; ++i) {
+                uint32_t at;
+                Cols<4> more;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_addr(mine_at)), "r"(i));
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(more.v[0]), "=f"(more.v[1]), "=f"(more.v[2]), "=f"(more.v[3])
+                             : "r"(at)
+                             : "memory");
+                v = v + more;
+            }
+        }
+        asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    }
+    if (part == 0 && m0 + row < g.m && n0 + col < g.n) put_piece(epi, m0 + row, n0 + col, v);
 }
 
-template <typename T, typename Epi> cudaError_t product_small(const SmallArgs& g, const Epi& epi, cudaStream_t stream)
+template <typename T, typename Epi> cudaError_t product_small(SmallArgs g, const Epi& epi, cudaStream_t stream)
 {
     const int64_t tiles = (int64_t)((g.n + kSmallTile - 1) / kSmallTile) * ((g.m + kSmallTile - 1) / kSmallTile);
-    return launch_after(product_small_kernel<T, Epi>, dim3((unsigned)tiles), dim3(256), 0, stream, g, epi);
+    // up to two CTAs an SM, of no fewer than a block of terms
+    for (g.parts = 1; g.parts < 8 && tiles * g.parts * 2 <= 304 && g.k >= g.parts * 2 * kSmallDepth;) g.parts *= 2;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)g.parts;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * g.parts));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = g.parts > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, product_small_kernel<T, Epi>, (const SmallArgs)g, epi);
 }
 
 }  // namespace

@@ -1,6 +1,6 @@
 // Products on the tensor cores: C(m, n) = sum over k of A(m, k) B(n, k), bf16 operands, fp32 sums.
 //
-// A pair of CTAs (a cluster of two SMs) has tiles of 256 x kN; each loads its 128 rows of A and its half of
+// A pair of CTAs (a cluster of two SMs) has tiles of 256 rows and up to 256 columns; each loads its 128 rows of A and its half of
 // B's rows for 64 terms at a time, by TMA, into a ring of stages; one thread of the first CTA issues the
 // products (tcgen05.mma, cta_group::2) on both CTAs' shared memory; the sums lie in tensor memory, 128
 // rows in each CTA, in two buffers. Eight warps take them over into registers, 128 columns of a row per thread, and hand
@@ -25,14 +25,13 @@ constexpr int kTcThreads = 384;      // warps 0..3: copies, products, tensor mem
 constexpr int kTcEpilogue = 4;       // the epilogue's first warp
 constexpr int kTcDepth = 64;         // terms of a stage: 128 bytes of bf16
 constexpr int kTcM = 256;            // rows of a pair's tile
+constexpr int kTcN = 256;            // and columns, at most: a multiple of 32
 constexpr uint64_t kTcLimit = 2000000000ull;  // ns: of every wait
 
-template <int kN> struct TcShape {
-    static constexpr int kA = 128 * kTcDepth * 2, kB = kN / 2 * kTcDepth * 2;  // bytes of a CTA's stage
-    static constexpr int kStages = 196608 / (kA + kB) < 8 ? 196608 / (kA + kB) : 8;
-    static constexpr int kStage = 4096;  // of an epilogue warp
-    static constexpr int kShared = kStages * (kA + kB) + 8 * kStage + 1024;  // 1024: to begin on such a boundary
-};
+constexpr int kTcStageA = 128 * kTcDepth * 2, kTcStageB = kTcN / 2 * kTcDepth * 2;  // bytes of a CTA's stage
+constexpr int kTcStages = 196608 / (kTcStageA + kTcStageB);
+constexpr int kTcStage = 4096;  // of an epilogue warp
+constexpr int kTcShared = kTcStages * (kTcStageA + kTcStageB) + 8 * kTcStage + 1024;  // 1024: to begin on such a boundary
 
 // ---------------------------------------------------------------- operands
 // A matrix as a product takes it: rows of `cols` bf16 numbers that are contiguous, 16-byte aligned rows `stride`
@@ -49,6 +48,7 @@ struct TcArgs {
     int32_t splits;                    // of the terms, each a product of its own
     int32_t a_mn, b_mn;                // operands that lie by terms
     int32_t run;                       // blocks of terms whose sums are formed in tensor memory
+    int32_t width;                     // columns of a tile
     int32_t group;                     // tiles of rows that are taken before the next column's
 };
 
@@ -247,7 +247,7 @@ struct TcUnit {
 };
 
 // (Counts of units fit in 32 bits: 2^31 tiles would be a result of 2^47 elements.)
-template <int kN, bool kBoth> struct TcSchedule {
+template <bool kBoth> struct TcSchedule {
     int32_t m[2], tiles_m[2], tiles_n[2], blocks[2], per_split[2], tiles[2], units[2], more, few, many, mine;
 
     __device__ __forceinline__ TcSchedule(const TcArgs (&g)[2])
@@ -258,14 +258,14 @@ template <int kN, bool kBoth> struct TcSchedule {
             m[i] = (int32_t)(g[i].m_count ? *g[i].m_count : g[i].m);
             const int32_t terms = (int32_t)(g[i].k_count ? *g[i].k_count : g[i].k);
             tiles_m[i] = (m[i] + kTcM - 1) / kTcM;
-            tiles_n[i] = ((int32_t)g[i].n + kN - 1) / kN;
+            tiles_n[i] = ((int32_t)g[i].n + g[i].width - 1) / g[i].width;
             blocks[i] = (terms + kTcDepth - 1) / kTcDepth;
             per_split[i] = (blocks[i] + g[i].splits - 1) / g[i].splits;
             tiles[i] = tiles_m[i] * tiles_n[i];
             units[i] = tiles[i] * g[i].splits;
         }
         if constexpr (kBoth) {
-            const TcShares shares(pairs, units[0], per_split[0], units[1], per_split[1]);
+            const TcShares shares(pairs, units[0], (int64_t)per_split[0] * g[0].width, units[1], (int64_t)per_split[1] * g[1].width);
             more = (int32_t)shares.more;
             few = (int32_t)shares.few;
             many = (int32_t)shares.many;
@@ -292,7 +292,7 @@ template <int kN, bool kBoth> struct TcSchedule {
         t.split = unit / count;
         const int32_t tile = unit - t.split * count, whole = gr * tn, band = tile / whole, in = tile - band * whole;
         const int32_t rows = tm - band * gr < gr ? tm - band * gr : gr;
-        t.n0 = in / rows * kN;
+        t.n0 = in / rows * g[second].width;
         t.m0 = (band * gr + in % rows) * kTcM;
         t.from = t.split * part;
         t.count = all - t.from < part ? all - t.from : part;
@@ -301,14 +301,12 @@ template <int kN, bool kBoth> struct TcSchedule {
     }
 };
 
-template <int kN, bool kBoth, typename Epi>
+template <bool kBoth, typename Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     product_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcParams<Epi> params)
 {
-    using Shape = TcShape<kN>;
-    constexpr int kStages = Shape::kStages;
     extern __shared__ __align__(1024) uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2], drained;
+    __shared__ __align__(8) uint64_t full[kTcStages], empty[kTcStages], sums_full[2], sums_empty[2], drained;
     __shared__ uint32_t tmem_at;
     __shared__ int dead_flag;
     volatile int* dead = &dead_flag;
@@ -317,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     const uint32_t rank = tc::cluster_rank();
     const uint32_t base = (ptx::smem_addr(raw) + 1023) & ~1023u;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kTcStages; ++i) {
             ptx::mbar_init(&full[i], 1);
             ptx::mbar_init(&empty[i], 1);
         }
@@ -345,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     tc::fence_after();
     const uint32_t tmem = tmem_at;
     ptx::griddep_wait();
-    const TcSchedule<kN, kBoth> schedule(params.g);
+    const TcSchedule<kBoth> schedule(params.g);
     TcUnit t;
 
     // 384 threads of 168 registers: 128 with 40 and 256 with 232 are as many
@@ -359,7 +357,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 const TcArgs& g = params.g[kBoth ? t.which : 0];
                 const CUtensorMap *map_a = &maps.a[kBoth ? t.which : 0], *map_b = &maps.b[kBoth ? t.which : 0];
                 const int passes = g.planes == 1 ? 1 : 6;
-                const int32_t ma = t.m0 + (int32_t)rank * 128, nb = t.n0 + (int32_t)rank * (kN / 2);
+                const int32_t ma = t.m0 + (int32_t)rank * 128, nb = t.n0 + (int32_t)rank * (g.width / 2);
+                const uint32_t bytes = kTcStageA + (g.b_mn ? (g.width + 127) / 128 * 8192 : g.width * kTcDepth);
                 for (int32_t from = 0; from < t.count && alive; from += g.run) {
                     const int32_t end = t.count - from < g.run ? t.count : from + g.run;
                     for (int pass = 0; pass < passes && alive; ++pass) {
@@ -367,10 +366,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                         for (int32_t k = from; k < end; ++k) {
                             alive = __all_sync(0xffffffffu, tc::wait(&empty[at_stage], turn ^ 1, dead));
                             if (!alive) break;
-                            const uint32_t bar = full_at + at_stage * 8, at = base + at_stage * (Shape::kA + Shape::kB);
+                            const uint32_t bar = full_at + at_stage * 8, at = base + at_stage * (kTcStageA + kTcStageB);
                             const int32_t k0 = (t.from + k) * kTcDepth;
                             if (tc::elect()) {
-                                if (rank == 0) ptx::mbar_arrive_expect_tx(&full[at_stage], 2 * (Shape::kA + Shape::kB));
+                                if (rank == 0) ptx::mbar_arrive_expect_tx(&full[at_stage], 2 * bytes);
                                 if (g.a_mn) {
 #pragma unroll
                                     for (int i = 0; i < 2; ++i) tc::load(at + i * 8192, map_a, ma + 64 * i, k0, pa, bar);
@@ -378,14 +377,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                                     tc::load(at, map_a, k0, ma, pa, bar);
                                 }
                                 if (g.b_mn) {
-#pragma unroll
-                                    for (int i = 0; i < kN / 128; ++i) tc::load(at + Shape::kA + i * 8192, map_b, nb + 64 * i, k0, pb, bar);
+                                    tc::load(at + kTcStageA, map_b, nb, k0, pb, bar);
+                                    if (g.width > 128) tc::load(at + kTcStageA + 8192, map_b, nb + 64, k0, pb, bar);
                                 } else {
-                                    tc::load(at + Shape::kA, map_b, k0, nb, pb, bar);
+                                    tc::load(at + kTcStageA, map_b, k0, nb, pb, bar);
                                 }
                             }
                             ++issued;
-                            if (++at_stage == kStages) at_stage = 0, turn ^= 1;
+                            if (++at_stage == kTcStages) at_stage = 0, turn ^= 1;
                         }
                     }
                 }
@@ -393,8 +392,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             if (!alive) {  // the copies in flight end before the CTA does: each stage's last one
                 int none = 0;
                 if (rank == 0) {
-                    for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                        tc::wait(&full[i % kStages], i / kStages & 1, &none);
+                    for (uint32_t i = issued > kTcStages ? issued - kTcStages : 0; i < issued; ++i)
+                        tc::wait(&full[i % kTcStages], i / kTcStages & 1, &none);
                 } else {  // their barrier is the other CTA's: 10 ms
                     const uint64_t from = ptx::globaltimer();
                     while (ptx::globaltimer() - from < 10000000ull) {}
@@ -407,11 +406,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 const TcArgs& g = params.g[kBoth ? t.which : 0];
                 const int passes = g.planes == 1 ? 1 : 6;
                 const uint32_t kind = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(g.a_mn != 0) << 15 | (uint32_t)(g.b_mn != 0) << 16 |
-                                      (uint32_t)(kN / 8) << 17 | (uint32_t)(kTcM / 16) << 24;
+                                      (uint32_t)(g.width / 8) << 17 | (uint32_t)(kTcM / 16) << 24;
                 // 16 terms further: 32 bytes along a line, or 16 lines
                 const uint32_t step_a = (g.a_mn ? 2048 : 32) >> 4, step_b = (g.b_mn ? 2048 : 32) >> 4;
                 const uint64_t first_a = tc::descriptor(base, g.a_mn ? 8192 : 16, 1024);
-                const uint64_t first_b = tc::descriptor(base + Shape::kA, g.b_mn ? 8192 : 16, 1024);
+                const uint64_t first_b = tc::descriptor(base + kTcStageA, g.b_mn ? 8192 : 16, 1024);
                 for (int32_t from = 0; from < t.count && alive; from += g.run) {
                     const int buffer = (int)(done & 1);
                     alive = __all_sync(0xffffffffu, tc::wait(&sums_empty[buffer], (done / 2 & 1) ^ 1, dead));
@@ -423,14 +422,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                         alive = __all_sync(0xffffffffu, tc::wait(&full[at_stage], turn, dead));
                         if (!alive) break;
                         tc::fence_after();
-                        const uint32_t at = at_stage * ((Shape::kA + Shape::kB) >> 4);
+                        const uint32_t at = at_stage * ((kTcStageA + kTcStageB) >> 4);
                         if (tc::elect()) {
 #pragma unroll
                             for (int j = 0; j < kTcDepth / 16; ++j)
                                 tc::mma(d, first_a + at + j * step_a, first_b + at + j * step_b, kind, i > 0 || j > 0);
                             tc::commit(&empty[at_stage]);
                         }
-                        if (++at_stage == kStages) at_stage = 0, turn ^= 1;
+                        if (++at_stage == kTcStages) at_stage = 0, turn ^= 1;
                     }
                     if (!alive) break;
                     if (tc::elect()) tc::commit(&sums_full[buffer]);
@@ -447,15 +446,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int quarter = warp & 3, strip = (warp - kTcEpilogue) / 4;
         const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + strip * kStrip;
-        const Stage stage = {reinterpret_cast<float4*>(raw + (base - ptx::smem_addr(raw)) + kStages * (Shape::kA + Shape::kB) +
-                                                       (warp - kTcEpilogue) * Shape::kStage)};
+        const Stage stage = {reinterpret_cast<float4*>(raw + (base - ptx::smem_addr(raw)) + kTcStages * (kTcStageA + kTcStageB) +
+                                                       (warp - kTcEpilogue) * kTcStage)};
         const uint32_t freed[2] = {tc::map_shared(&sums_empty[0], 0), tc::map_shared(&sums_empty[1], 0)};
         uint32_t done = 0;
         bool alive = true;
         for (int32_t u = 0; schedule.at(params.g, u, t); ++u) {
             const TcArgs& g = params.g[kBoth ? t.which : 0];
             const Epi& epi = params.epi[kBoth ? t.which : 0];
-            const int32_t m = kBoth && t.which ? schedule.m[1] : schedule.m[0], n = (int32_t)g.n;
+            const int32_t m = kBoth && t.which ? schedule.m[1] : schedule.m[0], n = t.n0 + g.width < g.n ? t.n0 + g.width : (int32_t)g.n;
             const int32_t r = t.m0 + (int32_t)rank * 128 + quarter * 32 + lane, c0 = t.n0 + strip * kStrip;
             typename Epi::State state = {};
             if (r < m && c0 < n) state = epi.begin(r, c0);
@@ -501,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 for (int i = 0; i < kStrip; ++i) v[i] = NAN;
             }
             if (c0 >= n) continue;
-            epi.rows(state, r, c0, r < m, v);
+            epi.rows(state, r, c0, n, t.n0 / g.width * ((g.width + kStrip - 1) / kStrip) + strip, r < m, v);
             __syncwarp();
             if constexpr (Epi::kChunks) {
 #pragma unroll
@@ -636,19 +635,19 @@ cudaError_t take_matrix(Matrix* out, const void* p, int64_t stride, int64_t rows
     return launch_after(pack_kernel<T>, dim3((unsigned)(need < most ? need : most)), dim3(kTcPack), 0, stream, a);
 }
 
-template <int kN, bool kBoth, typename Epi>
+template <bool kBoth, typename Epi>
 cudaError_t launch_tc(const TcMaps& maps, const TcParams<Epi>& p, cudaStream_t stream)
 {
-    cudaError_t e = allow<product_tc_kernel<kN, kBoth, Epi>>(TcShape<kN>::kShared);
+    cudaError_t e = allow<product_tc_kernel<kBoth, Epi>>(kTcShared);
     int sms = 0;
     if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     int64_t units = 0;
     for (int i = 0; i < (kBoth ? 2 : 1); ++i)
-        units += (p.g[i].m + kTcM - 1) / kTcM * ((p.g[i].n + kN - 1) / kN) * p.g[i].splits;
+        units += (p.g[i].m + kTcM - 1) / kTcM * ((p.g[i].n + p.g[i].width - 1) / p.g[i].width) * p.g[i].splits;
     const int64_t pairs = sms / 2;
-    return launch_after(product_tc_kernel<kN, kBoth, Epi>, dim3((unsigned)(2 * (units < pairs ? units : pairs))), dim3(kTcThreads),
-                        TcShape<kN>::kShared, stream, maps, p);
+    return launch_after(product_tc_kernel<kBoth, Epi>, dim3((unsigned)(2 * (units < pairs ? units : pairs))), dim3(kTcThreads),
+                        kTcShared, stream, maps, p);
 }
 
 // A product's operands. a_mn, b_mn: the matrix lies by terms (its rows are terms).
@@ -659,9 +658,9 @@ struct TcProduct {
     const int32_t *m_count, *k_count;
 };
 
-template <typename T, typename Epi> cudaError_t set_tc(TcMaps& maps, TcParams<Epi>& p, int i, const TcProduct& x, const Epi& epi)
+template <typename T, typename Epi>
+cudaError_t set_tc(TcMaps& maps, TcParams<Epi>& p, int i, const TcProduct& x, int width, int splits, const Epi& epi)
 {
-    constexpr int kN = 256;
     TcArgs g = {};
     g.m = x.m;
     g.n = x.n;
@@ -669,7 +668,8 @@ template <typename T, typename Epi> cudaError_t set_tc(TcMaps& maps, TcParams<Ep
     g.m_count = x.m_count;
     g.k_count = x.k_count;
     g.planes = sizeof(T) == 4 ? kPlanes : 1;
-    g.splits = 1;
+    g.splits = splits;
+    g.width = width;
     g.a_mn = x.a_mn;
     g.b_mn = x.b_mn;
     g.group = 8;
@@ -677,22 +677,50 @@ template <typename T, typename Epi> cudaError_t set_tc(TcMaps& maps, TcParams<Ep
     p.g[i] = g;
     p.epi[i] = epi;
     const cudaError_t e = tensor_map(&maps.a[i], x.a, g.planes, x.a_mn ? kTcDepth : 128);
-    return e == cudaSuccess ? tensor_map(&maps.b[i], x.b, g.planes, x.b_mn ? kTcDepth : kN / 2) : e;
+    return e == cudaSuccess ? tensor_map(&maps.b[i], x.b, g.planes, x.b_mn ? kTcDepth : width / 2) : e;
 }
 
 // ---------------------------------------------------------------- which way
-// The terms of a product with few tiles, or of a few more than go round, are split, and the parts' sums joined by a kernel
-// of their own. By estimate, us: a block of 64 terms takes a pair 0.3 (fp32: six times that), a tile's end 2 more (its
-// epilogue's last part, which nothing covers), the parts' sums are written and read at 4 bytes each, and the joining kernel
-// begins 3 later.
+// How wide the tiles are, and into how many parts the terms are split (which a kernel of its own joins), so that the last
+// tiles leave few SMs idle. By estimate, us: a block of 64 terms and 256 columns takes a pair kTcBlock (six times that in
+// fp32), a narrower one more than its share, as the rows of A are loaded all the same (tiles of 32 blocks, bf16: 256 columns
+// 11.2, 224 9.7, 192 8.7, 160 7.8, 128 7.2, 96 6.7); the last tile's end 2 more, which nothing covers; the parts' sums are
+// written and read, and the joining kernel begins 3 later. With it, and with 256 columns and whole sums: the logits of 512
+// rows over 50304 tokens 75 and 84; a layer's gradients 3001 x 1001 x 777 fp32 102 and 111.
 constexpr int64_t kPairs = 76, kMostParts = 2 * kPairs;  // tiles x splits are at most kMostParts, if split
+constexpr double kTcBlock = 0.32;
+
+struct TcWay {
+    int width, splits;
+};
 
 struct TcSize {
     int64_t m, n, k;
-    int64_t tiles() const { return (m + kTcM - 1) / kTcM * ((n + 255) / 256); }
+    bool fp32, may_split;
+    int64_t tiles(int width) const { return (m + kTcM - 1) / kTcM * ((n + width - 1) / width); }
     int64_t blocks(int s) const { return ((k + kTcDepth - 1) / kTcDepth + s - 1) / s; }
-    bool may(int s) const { return s == 1 || (tiles() * s <= kMostParts && blocks(1) >= 4 * s); }
-    double join(int s) const { return s == 1 ? 0.0 : 3.0 + (double)s * m * n * 8 / 5e6; }
+    bool may(TcWay w) const { return w.splits == 1 || (may_split && tiles(w.width) * w.splits <= kMostParts && blocks(1) >= 4 * w.splits); }
+    double join(TcWay w) const { return w.splits == 1 ? 0.0 : 3.0 + (double)w.splits * m * n * 8 / 5e6; }
+    double unit(TcWay w) const
+    {
+        const double share = w.width / 256.0, least = 0.45 + 0.38 * share;
+        return blocks(w.splits) * kTcBlock * (fp32 ? 6 : 1) * (share > least ? share : least);
+    }
+    double cost(TcWay w) const
+    {
+        const int64_t waves = (tiles(w.width) * w.splits + kPairs - 1) / kPairs;
+        return waves * unit(w) + 2.0 + join(w);
+    }
+    // the narrowest that gives as few tiles as 256 columns
+    int even() const { return (int)round_up((n + (n + 255) / 256 - 1) / ((n + 255) / 256), 32); }
+    TcWay best() const
+    {
+        TcWay best = {even(), 1};
+        for (int width = even(); width >= 32 && (width >= 96 || width == even()); width -= 32)
+            for (TcWay w = {width, 1}; may(w); ++w.splits)
+                if (cost(w) < 0.97 * cost(best)) best = w;
+        return best;
+    }
 };
 
 inline int64_t parts_elements(int64_t m, int64_t n)  // of a workspace
@@ -701,45 +729,45 @@ inline int64_t parts_elements(int64_t m, int64_t n)  // of a workspace
     return all < whole ? all : whole;
 }
 
-inline double cost_of(const TcSize& x, int s, double block)
+template <typename T, typename Epi> TcSize size_of(const TcProduct& x) { return {x.m, x.n, x.k, sizeof(T) == 4, Epi::kPieces}; }
+
+// The epilogue of a product whose terms are split: its parts' sums.
+template <typename T> EpiStore<T> to_parts(EpiStore<T> epi, float* parts, const TcProduct& x)
 {
-    const int64_t waves = (x.tiles() * s + kPairs - 1) / kPairs;
-    return waves * (x.blocks(s) * block + 2.0) + x.join(s);
+    epi.acc = parts;
+    epi.acc_stride = round_up(x.n, 4);
+    epi.split_stride = x.m * epi.acc_stride;
+    epi.n = (int32_t)x.n;
+    return epi;
 }
 
-inline int splits_of(const TcSize& x, double block)
+inline JoinPartsArgs joining(float* parts, const TcProduct& x, int splits)
 {
-    int best = 1;
-    for (int s = 2; x.may(s); ++s)
-        if (cost_of(x, s, block) < 0.95 * cost_of(x, best, block)) best = s;
-    return best;
+    return {parts, x.m, x.n, round_up(x.n, 4), x.m_count, splits};
 }
 
 // A product of matrices of T's planes. parts: room for parts_elements.
-template <typename T, typename Epi> cudaError_t product_tc(const TcProduct& x, float* parts, const Epi& epi, cudaStream_t stream)
+template <typename T, typename Epi>
+cudaError_t product_tc(const TcProduct& x, TcWay way, float* parts, const Epi& epi, cudaStream_t stream)
 {
     if (x.m <= 0 || x.n <= 0) return cudaSuccess;
     TcMaps maps = {};
     if constexpr (Epi::kPieces) {
-        const int splits = splits_of(TcSize{x.m, x.n, x.k}, sizeof(T) == 4 ? 1.8 : 0.3);
-        if (splits > 1) {
-            EpiStore<T> each = {};
-            each.acc = parts;
-            each.acc_stride = round_up(x.n, 4);
-            each.split_stride = x.m * each.acc_stride;
-            each.n = (int32_t)x.n;
-            each.first = true;
+        if (way.splits > 1) {
             TcParams<EpiStore<T>> p = {};
-            cudaError_t e = set_tc<T>(maps, p, 0, x, each);
-            if (e != cudaSuccess) return e;
-            p.g[0].splits = splits;
-            e = launch_tc<256, false>(maps, p, stream);
-            return e == cudaSuccess ? join_parts(JoinPartsArgs{parts, x.m, x.n, each.acc_stride, x.m_count, splits}, epi, stream) : e;
+            cudaError_t e = set_tc<T>(maps, p, 0, x, way.width, way.splits, to_parts(EpiStore<T>{}, parts, x));
+            if (e == cudaSuccess) e = launch_tc<false>(maps, p, stream);
+            return e == cudaSuccess ? join_parts(joining(parts, x, way.splits), epi, stream) : e;
         }
     }
     TcParams<Epi> p = {};
-    const cudaError_t e = set_tc<T>(maps, p, 0, x, epi);
-    return e == cudaSuccess ? launch_tc<256, false>(maps, p, stream) : e;
+    const cudaError_t e = set_tc<T>(maps, p, 0, x, way.width, 1, epi);
+    return e == cudaSuccess ? launch_tc<false>(maps, p, stream) : e;
+}
+
+template <typename T, typename Epi> cudaError_t product_tc(const TcProduct& x, float* parts, const Epi& epi, cudaStream_t stream)
+{
+    return product_tc<T>(x, size_of<T, Epi>(x).best(), parts, epi, stream);
 }
 
 // Two products, neither of which needs the other, in one launch, so that the units of one fill the SMs that the other's last
@@ -747,43 +775,41 @@ template <typename T, typename Epi> cudaError_t product_tc(const TcProduct& x, f
 template <typename T, typename Epi>
 cudaError_t product_tc_both(const TcProduct& x, const Epi& epi_x, const TcProduct& y, const Epi& epi_y, float* parts, cudaStream_t stream)
 {
-    constexpr double block = sizeof(T) == 4 ? 1.8 : 0.3;
-    const TcSize size[2] = {{x.m, x.n, x.k}, {y.m, y.n, y.k}};
-    int best[2] = {1, 1};
-    double least = -1.0;
-    const int alone[2] = {splits_of(size[0], block), splits_of(size[1], block)};
-    for (int i = 0; i < 9; ++i) {  // each whole, as it would be alone, and half of that
-        const int s = i % 3 == 0 ? 1 : (alone[0] + i % 3 - 1) / (i % 3), t = i / 3 == 0 ? 1 : (alone[1] + i / 3 - 1) / (i / 3);
-        const bool turned = size[1].blocks(t) > size[0].blocks(s);  // the longer sums first
-        const TcSize &a = size[turned], &b = size[!turned];
-        const int sa = turned ? t : s, sb = turned ? s : t;
-        const int64_t units_a = a.tiles() * sa, units_b = b.tiles() * sb;
-        const TcShares shares(kPairs, units_a, a.blocks(sa), units_b, b.blocks(sb));
-        const double cost = shares.blocks * block + 2.0 * ((units_a + units_b + kPairs - 1) / kPairs) + size[0].join(s) + size[1].join(t);
-        if (least < 0.0 || cost < 0.98 * least) least = cost, best[0] = s, best[1] = t;
+    const TcProduct* const product[2] = {&x, &y};
+    const Epi* const epi[2] = {&epi_x, &epi_y};
+    const TcSize size[2] = {size_of<T, Epi>(x), size_of<T, Epi>(y)};
+    float* const room[2] = {parts, parts + parts_elements(x.m, x.n)};
+    const int width[2] = {size[0].even(), size[1].even()};
+    int alone[2];
+    for (int i = 0; i < 2; ++i) {
+        TcWay best = {width[i], 1};
+        for (TcWay w = best; size[i].may(w); ++w.splits)
+            if (size[i].cost(w) < 0.97 * size[i].cost(best)) best = w;
+        alone[i] = best.splits;
     }
-    const bool turned = size[1].blocks(best[1]) > size[0].blocks(best[0]);
+    TcWay best[2] = {{width[0], 1}, {width[1], 1}};
+    bool turned = false;
+    double least = -1.0;
+    for (int i = 0; i < 9; ++i) {  // each whole, as it would be alone, and half of that
+        const TcWay way[2] = {{width[0], i % 3 == 0 ? 1 : (alone[0] + i % 3 - 1) / (i % 3)},
+                              {width[1], i / 3 == 0 ? 1 : (alone[1] + i / 3 - 1) / (i / 3)}};
+        const double unit[2] = {size[0].unit(way[0]), size[1].unit(way[1])};
+        const int a = unit[1] > unit[0], b = !a;  // the longer sums first
+        const TcShares shares(kPairs, size[a].tiles(width[a]) * way[a].splits, (int64_t)(unit[a] * 1000),
+                              size[b].tiles(width[b]) * way[b].splits, (int64_t)(unit[b] * 1000));
+        const double cost = shares.blocks / 1000.0 + 2.0 + size[0].join(way[0]) + size[1].join(way[1]);
+        if (least < 0.0 || cost < 0.98 * least) least = cost, best[0] = way[0], best[1] = way[1], turned = a;
+    }
     TcMaps maps = {};
     TcParams<Epi> p = {};
-    JoinPartsArgs joins[2] = {};
-    float* room[2] = {parts, parts + parts_elements(x.m, x.n)};
     for (int i = 0; i < 2; ++i) {
-        const TcProduct& g = i ? y : x;
-        Epi epi = i ? epi_y : epi_x;
-        if (best[i] > 1) {
-            epi.acc = room[i];
-            epi.acc_stride = round_up(g.n, 4);
-            epi.split_stride = g.m * epi.acc_stride;
-            joins[i] = {room[i], g.m, g.n, epi.acc_stride, g.m_count, best[i]};
-        }
-        const int at = turned ? !i : i;
-        const cudaError_t e = set_tc<T>(maps, p, at, g, epi);
+        const TcProduct& g = *product[i];
+        const cudaError_t e = set_tc<T>(maps, p, turned ? !i : i, g, width[i], best[i].splits, best[i].splits > 1 ? to_parts(*epi[i], room[i], g) : *epi[i]);
         if (e != cudaSuccess) return e;
-        p.g[at].splits = best[i];
     }
-    cudaError_t e = launch_tc<256, true>(maps, p, stream);
-    if (e == cudaSuccess && best[0] > 1) e = join_parts(joins[0], epi_x, stream);
-    if (e == cudaSuccess && best[1] > 1) e = join_parts(joins[1], epi_y, stream);
+    cudaError_t e = launch_tc<true>(maps, p, stream);
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+        if (best[i].splits > 1) e = join_parts(joining(room[i], *product[i], best[i].splits), *epi[i], stream);
     return e;
 }
 

@@ -54,6 +54,15 @@ int64_t piece_of(int64_t rows, int64_t vocab)
     return n < vocab ? n : vocab;
 }
 
+// Strips of a row's logits, in tiles of `width` columns; and at most, whatever the tiles (of which all but narrow
+// vocabularies' have 96 columns or more).
+int64_t strips_of(int64_t vocab, int width)
+{
+    const int64_t tiles = (vocab + width - 1) / width, rest = vocab - (tiles - 1) * width;
+    return (tiles - 1) * ((width + kStrip - 1) / kStrip) + (rest + kStrip - 1) / kStrip;
+}
+int64_t most_strips(int64_t vocab) { return vocab / 80 + 2; }
+
 VocabParts vocab_parts(Carve& c, int64_t rows, int64_t dim, int64_t vocab, int bytes, int32_t k, bool backward)
 {
     VocabParts p = {};
@@ -72,7 +81,7 @@ VocabParts vocab_parts(Carve& c, int64_t rows, int64_t dim, int64_t vocab, int b
         p.acc = c.take<float>(rows * round_up(dim, 4));
         p.parts = c.take<float>(parts_elements(rows, dim) + parts_elements(p.piece, dim));
     } else {
-        p.part = c.take<float2>(rows * ((vocab + kStrip - 1) / kStrip));
+        p.part = c.take<float2>(rows * most_strips(vocab));
         p.picked = c.take<float>(rows * k);
     }
     return p;
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinArgs
         const int64_t r = r0 + lane;
         float top = -INFINITY, sum = 0.0f;
         if (r < count) {
-#pragma unroll 4
+#pragma unroll 8
             for (int64_t i = warp; i < a.strips; i += kWarps) {
                 const float2 p = a.part[i * a.rows + r];
                 const float more = fmaxf(top, p.x), less = more == -INFINITY ? 0.0f : more;
@@ -331,11 +340,11 @@ template <typename T> cudaError_t vocab_forward(const VocabArgs& a, void* ws, cu
     epi.part = p.part;
     epi.picked = p.picked;
     epi.lists = {p.index, p.q, p.map, a.k};
-    epi.n = (int32_t)a.vocab;
     epi.row_stride = a.rows;
     epi.scale = 1.0f / a.temperature;
     const TcProduct product = {x, w, false, false, a.rows, a.vocab, a.dim, p.count, nullptr};
-    e = product_tc<T>(product, nullptr, epi, stream);
+    const TcWay way = size_of<T, EpiSoftmax<T>>(product).best();
+    e = product_tc<T>(product, way, nullptr, epi, stream);
     if (e != cudaSuccess) return e;
     JoinArgs j = {};
     j.part = p.part;
@@ -347,7 +356,7 @@ template <typename T> cudaError_t vocab_forward(const VocabArgs& a, void* ws, cu
     j.loss = a.loss;
     j.lse = a.lse_out;
     j.rows = a.rows;
-    j.strips = (a.vocab + kStrip - 1) / kStrip;
+    j.strips = strips_of(a.vocab, way.width);
     j.k = a.k;
     j.temperature = a.temperature;
     return launch_after(vocab_join_kernel, dim3(blocks_of(a.rows, 32, 4096)), dim3(kJoinThreads), 0, stream, j);
