@@ -1,8 +1,9 @@
 """A small recurrent language model trained data-parallel with compressed gradients.
 
-The whole step runs through this library, but for the matrix products (torch):
+The whole step runs through this library:
 
-    layer norm -> gates and inputs (product) -> gated recurrence -> product, in residual blocks
+    layer norm -> gates and inputs (adacomp_linear) -> gated recurrence -> adacomp_linear onto the residual stream
+    softmax cross entropy over the vocabulary, whose logits are not kept (adacomp_vocab_loss)
     every learner compresses its gradients (adacomp_compress_group)
     the learners' messages are summed (adacomp_decode_accumulate_group)
     the sum's norm clips it (adacomp_grad_norm), and AdamW takes the step (adacomp_adamw_step)
@@ -68,6 +69,52 @@ class Recurrence(torch.autograd.Function):
         return dzx, None
 
 
+class Linear(torch.autograd.Function):
+    """x w^T, onto a residual if there is one; h: adacomp_linear_init."""
+
+    @staticmethod
+    def forward(ctx, x, w, residual, h):
+        y = torch.empty(*x.shape[:-1], w.shape[0], dtype=x.dtype, device=x.device)
+        ws = scratch(ac.adacomp_linear_forward_ws_bytes(h, x.numel() // x.shape[-1]), x)
+        ac.adacomp_linear_forward(h, x, w, y, ws, residual=residual)
+        ctx.save_for_backward(x, w)
+        ctx.h, ctx.added = h, residual is not None
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w = ctx.saved_tensors
+        dy, dx, dw = dy.contiguous(), torch.empty_like(x), torch.empty_like(w)
+        ws = scratch(ac.adacomp_linear_backward_ws_bytes(ctx.h, x.numel() // x.shape[-1]), x)
+        ac.adacomp_linear_backward(ctx.h, dy, x, w, ws, dx=dx, dw=dw)
+        return dx, dw, dy if ctx.added else None, None
+
+
+class CrossEntropy(torch.autograd.Function):
+    """Each row's loss against the rows of w; negative targets have none. h: adacomp_vocab_init."""
+
+    @staticmethod
+    def forward(ctx, x, w, target, h):
+        rows = target.numel()
+        loss, lse = torch.empty(rows, device=x.device), torch.empty(rows, device=x.device)
+        ac.adacomp_vocab_loss_forward(h, x, w, target, loss, lse, scratch(ac.adacomp_vocab_loss_forward_ws_bytes(h, rows), x))
+        ctx.save_for_backward(x, w, target, lse)
+        ctx.h = h
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        x, w, target, lse = ctx.saved_tensors
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        ws = scratch(ac.adacomp_vocab_loss_backward_ws_bytes(ctx.h, target.numel()), x)
+        ac.adacomp_vocab_loss_backward(ctx.h, x, w, target, lse, dloss.contiguous(), ws, dx=dx, dw=dw)
+        return dx, dw, None, None
+
+
+def scratch(nbytes, like):
+    return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
 class Model:
     """Weights in one flat list: embedding, and per block (norm w, norm b, gates and inputs, output)."""
 
@@ -77,7 +124,7 @@ class Model:
         self.width, self.blocks = width, blocks
         self.weights = [init(vocab, width, scale=0.02)]
         for _ in range(blocks):
-            gates = init(width, 2 * width, scale=width ** -0.5)
+            gates = init(2 * width, width, scale=width ** -0.5)
             self.weights += [torch.ones(width, device="cuda", requires_grad=True),
                              torch.zeros(width, device="cuda", requires_grad=True), gates,
                              init(width, width, scale=width ** -0.5)]
@@ -85,18 +132,24 @@ class Model:
                          torch.zeros(width, device="cuda", requires_grad=True)]
         self.norm = ac.adacomp_layer_norm_init(width, ac.F32, ac.F32, 1e-5)
         self.recurrence = ac.adacomp_recurrence_init(width, ac.F32)
+        self.gates, self.proj = ac.adacomp_linear_init(width, 2 * width), ac.adacomp_linear_init(width, width)
+        self.head, self.vocab = ac.adacomp_linear_init(width, vocab), ac.adacomp_vocab_init(width, vocab)
 
-    def logits(self, tokens):
+    def hidden(self, tokens):
         w = self.weights
         x = w[0][tokens]
         for i in range(self.blocks):
             nw, nb, gates, out = w[1 + 4 * i:5 + 4 * i]
-            x = x + Recurrence.apply(LayerNorm.apply(x, nw, nb, self.norm) @ gates, self.recurrence) @ out
-        return LayerNorm.apply(x, w[-2], w[-1], self.norm) @ w[0].T
+            zx = Linear.apply(LayerNorm.apply(x, nw, nb, self.norm), gates, None, self.gates)
+            x = Linear.apply(Recurrence.apply(zx, self.recurrence), out, x, self.proj)
+        return LayerNorm.apply(x, w[-2], w[-1], self.norm)
+
+    def logits(self, tokens):
+        return Linear.apply(self.hidden(tokens), self.weights[0], None, self.head)
 
     def loss(self, tokens):
-        logits = self.logits(tokens[:, :-1])
-        return torch.nn.functional.cross_entropy(logits.reshape(-1, logits.shape[-1]), tokens[:, 1:].reshape(-1))
+        x = self.hidden(tokens[:, :-1])
+        return CrossEntropy.apply(x.reshape(-1, self.width), self.weights[0], tokens[:, 1:].reshape(-1), self.vocab).mean()
 
     @torch.no_grad()
     def generate(self, tokens, count):
@@ -104,17 +157,19 @@ class Model:
         batch, w, c = tokens.shape[0], self.weights, self.width
         states = [torch.zeros(batch, c, device="cuda") for _ in range(self.blocks)]
         y, n = torch.empty(batch, 1, c, device="cuda"), torch.empty(batch, c, device="cuda")
+        zx, logits = torch.empty(batch, 1, 2 * c, device="cuda"), torch.empty(batch, w[0].shape[0], device="cuda")
+        ws = scratch(max(ac.adacomp_linear_forward_ws_bytes(h, batch) for h in (self.gates, self.proj, self.head)), n)
         out = tokens
         for t in range(tokens.shape[1] + count - 1):
             x = w[0][out[:, t]]
             for i, state in enumerate(states):
                 nw, nb, gates, proj = w[1 + 4 * i:5 + 4 * i]
                 ac.adacomp_layer_norm_forward(self.norm, x, nw, nb, n)
-                zx = (n @ gates)[:, None]
+                ac.adacomp_linear_forward(self.gates, n, gates, zx, ws)
                 ac.adacomp_recurrence_forward(self.recurrence, zx[..., :c], zx[..., c:], y, h0=state, h_last=state)
-                x = x + y[:, 0] @ proj
+                ac.adacomp_linear_forward(self.proj, y, proj, x, ws, residual=x)
             ac.adacomp_layer_norm_forward(self.norm, x, w[-2], w[-1], n)
-            logits = n @ w[0].T
+            ac.adacomp_linear_forward(self.head, n, w[0], logits, ws)
             if t + 1 >= tokens.shape[1]:
                 out = torch.cat([out, logits.argmax(1, keepdim=True)], 1)
         return out, logits
