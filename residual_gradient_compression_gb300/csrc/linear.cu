@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kDzCols / 8 * kDzRows, sizeof(T) == 2 ? 4 : 3)
 {
     __shared__ float sums[kDzRows][kDzCols];
     ptx::griddep_wait();
+    ptx::griddep_launch();
     const int32_t c = blockIdx.x * kDzCols + threadIdx.x * 8;
     float sum[8] = {};
     if (c < a.n) switch (a.act) {
@@ -167,6 +168,7 @@ template <typename T> __global__ void __launch_bounds__(kDbCols * kDbRows) linea
 {
     __shared__ float sums[kDbRows][kDbCols];
     ptx::griddep_wait();
+    ptx::griddep_launch();
     const int64_t c = (int64_t)blockIdx.x * kDbCols + threadIdx.x;
     float s = 0.0f;
     if (c < n)

@@ -8,7 +8,8 @@
 // lines at a time: a linear layer's forward product of 8192 x 2048 x 16384 bf16 took 369 us so, and 313 without its
 // stores). kExact: the results are held in fp32, so the sums are formed in short runs.
 // kPieces: a thread may also hand over columns on their own, piece(). kAdds: there may be a matrix that
-// the sums are added to, which take() loads before they are there.
+// the sums are added to, which take() loads before they are there. kPatches: patch() changes single columns of a chunk in
+// shared memory.
 #pragma once
 
 #include "train_common.cuh"
@@ -142,6 +143,19 @@ struct Stage {
     float4* p;
     __device__ __forceinline__ float4& at(int row, int piece) const { return p[row * 8 + (piece ^ (row & 7))]; }
 };
+
+// A thread's own row: 32 of its columns to shared memory, and one of them there.
+__device__ __forceinline__ void put_row(const Stage& s, const float (&v)[kStrip], int from)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s.at(lane, i) = make_float4(v[from + 4 * i], v[from + 4 * i + 1], v[from + 4 * i + 2], v[from + 4 * i + 3]);
+}
+
+__device__ __forceinline__ float& row_value(const Stage& s, int col)
+{
+    return reinterpret_cast<float*>(&s.at(threadIdx.x & 31, col / 4))[col & 3];
+}
 
 // How a warp takes a chunk: in turns of four rows, of which a lane has four columns, or, where rows do not begin at such
 // places, of one row, of which it has one.
@@ -282,7 +296,7 @@ template <typename T, int kKind> __device__ __forceinline__ float slope(float z)
 // ---------------------------------------------------------------- epilogues
 // y = act(sum + bias) + residual, and the value before the activation.
 template <typename T> struct EpiLinear {
-    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kAdds = false;
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kAdds = false, kPatches = false;
     T *y, *pre;
     const T *bias, *residual;
     int64_t y_stride, pre_stride, residual_stride;
@@ -290,7 +304,7 @@ template <typename T> struct EpiLinear {
     bool whole;  // all of them
     struct State {};
     __device__ __forceinline__ State begin(int32_t, int32_t) const { return {}; }
-    __device__ __forceinline__ void rows(const State&, int32_t, int32_t, int32_t, int32_t, bool, float (&)[kStrip]) const {}
+    __device__ __forceinline__ void rows(const Stage&, const State&, int32_t, int32_t, int32_t, int32_t, bool, float (&)[kStrip]) const {}
 
     template <int N, typename F> __device__ __forceinline__ void turns(const Stage& stage, int32_t r0, int32_t end, int32_t c0, F f) const
     {
@@ -371,7 +385,7 @@ template <typename T> struct EpiLinear {
 // fp32 (first: nothing to add to yet) and rounded by the last one only. Of a product whose terms are split, the parts'
 // sums go to acc, split_stride apart (and neither first nor last is asked).
 template <typename T> struct EpiStore {
-    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kAdds = true;
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kAdds = true, kPatches = false;
     T* out;
     float* acc;
     const int32_t* map;
@@ -383,7 +397,7 @@ template <typename T> struct EpiStore {
     };
     __device__ __forceinline__ State begin(int32_t r, int32_t) const { return {map ? map[r] : r}; }
     __device__ __forceinline__ bool adds() const { return !first; }
-    __device__ __forceinline__ void rows(const State&, int32_t, int32_t, int32_t, int32_t, bool, float (&)[kStrip]) const {}
+    __device__ __forceinline__ void rows(const Stage&, const State&, int32_t, int32_t, int32_t, int32_t, bool, float (&)[kStrip]) const {}
 
     __device__ __forceinline__ void take(const Stage& stage, int32_t r0, int32_t end, int32_t c0) const
     {
@@ -440,15 +454,6 @@ template <typename T> __device__ __forceinline__ float exp_of(float x)
     else return __expf(x);
 }
 
-// yes ? a : b, by an instruction: of a series of them over an array the compiler makes an index, and so puts the
-// array into local memory.
-__device__ __forceinline__ float select(bool yes, float a, float b)
-{
-    float v;
-    asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tselp.f32 %0, %1, %2, p;\n\t}" : "=f"(v) : "f"(a), "f"(b), "r"((uint32_t)yes));
-    return v;
-}
-
 // What each row is compared with: k tokens in ascending order (those past the list's end are
 // INT32_MAX), with their weights, of the rows in their own order; map: the rows that have a loss.
 struct Lists {
@@ -460,13 +465,14 @@ struct Lists {
 
 // Where a row's list begins, its first place that is not before column c, and the token there.
 struct Place {
-    int64_t list;
-    int32_t at, token;
+    int64_t list = 0;
+    int32_t at = 0, token = INT32_MAX;
 };
 
 __device__ __forceinline__ Place place_of(const Lists& l, int64_t row, int32_t c)
 {
-    Place p = {row * l.k, 0, INT32_MAX};
+    Place p;
+    p.list = row * l.k;
     const int32_t* index = l.index + p.list;
     for (int hi = l.k; p.at < hi;) {
         const int mid = (p.at + hi) / 2;
@@ -485,7 +491,7 @@ __device__ __forceinline__ int32_t next_token(const Lists& l, const Place& p, in
 // Of each strip of up to 128 logits of a row: their maximum and the sum of exp(z - maximum); and the logits
 // of the listed tokens.
 template <typename T> struct EpiSoftmax {
-    static constexpr bool kExact = true, kChunks = false, kPieces = false, kAdds = false;
+    static constexpr bool kExact = true, kChunks = false, kPieces = false, kAdds = false, kPatches = false;
     float2* part;  // [strips][row_stride]
     float* picked;
     Lists lists;
@@ -493,18 +499,21 @@ template <typename T> struct EpiSoftmax {
     float scale;  // of the logits: 1 / temperature
     using State = Place;
     __device__ __forceinline__ State begin(int32_t r, int32_t c) const { return place_of(lists, lists.map[r], c); }
-    __device__ __forceinline__ void rows(const State& s, int32_t r, int32_t c, int32_t last, int32_t strip, bool live, float (&v)[kStrip]) const
+    __device__ __forceinline__ void rows(const Stage& stage, const State& s, int32_t r, int32_t c, int32_t last, int32_t strip, bool live,
+                                         float (&v)[kStrip]) const
     {
-        if (!live) return;
-        const int32_t end = last - c < kStrip ? last : c + kStrip;
+        const int32_t end = !live ? c : last - c < kStrip ? last : c + kStrip;
 #pragma unroll
         for (int i = 0; i < kStrip; ++i) v[i] *= scale;
-        for (int32_t at = s.at, token = s.token; token < end; token = next_token(lists, s, ++at)) {
-            float z = 0.0f;
+        if (__any_sync(0xffffffffu, live && s.token < end)) {  // by shared memory, where a column can be an index
+            int32_t at = s.at, token = live ? s.token : INT32_MAX;
 #pragma unroll
-            for (int i = 0; i < kStrip; ++i) z = select(token - c == i, v[i], z);
-            picked[s.list + at] = z;
+            for (int q = 0; q < kStrip; q += 32) {
+                put_row(stage, v, q);
+                for (; token < end && token < c + q + 32; token = next_token(lists, s, ++at)) picked[s.list + at] = row_value(stage, token - c - q);
+            }
         }
+        if (!live) return;
         if (end < c + kStrip) {
 #pragma unroll
             for (int i = 0; i < kStrip; ++i) v[i] = i < end - c ? v[i] : -INFINITY;
@@ -525,7 +534,7 @@ template <typename T> struct EpiSoftmax {
 // The logits' gradient (p - q) * dloss * temperature of columns first .. first + n - 1: rounded to
 // bf16, or, of fp32 operands, in parts. Rows past the last one, up to a tile's end, are zeros: they are terms of a product.
 template <typename T> struct EpiGradient {
-    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = false, kAdds = false;
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = false, kAdds = false, kPatches = true;
     bf16* dz;  // [planes][room][stride]
     Lists lists;
     const float *lse, *dloss, *given;
@@ -543,28 +552,30 @@ template <typename T> struct EpiGradient {
         if (given[row] != given[row]) s.factor = given[row];  // a row that has no value
         return s;
     }
-    __device__ __forceinline__ void rows(const State& s, int32_t, int32_t c, int32_t, int32_t, bool live, float (&v)[kStrip]) const
+    __device__ __forceinline__ void rows(const Stage&, const State& s, int32_t, int32_t, int32_t, int32_t, bool live, float (&v)[kStrip]) const
     {
-        if (!live) {
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < kStrip; ++i) v[i] = exp_of<T>(fmaf(v[i], scale, -s.lse)) * s.factor;
+        } else {
 #pragma unroll
             for (int i = 0; i < kStrip; ++i) v[i] = 0.0f;
-            return;
         }
-#pragma unroll
-        for (int i = 0; i < kStrip; ++i) v[i] = exp_of<T>(fmaf(v[i], scale, -s.lse));
-        for (int32_t at = s.place.at, token = s.place.token; token < first + c + kStrip; token = next_token(lists, s.place, ++at)) {
-            const float q = lists.q[s.place.list + at];
-#pragma unroll
-            for (int i = 0; i < kStrip; ++i) v[i] -= select(token - first - c == i, q, 0.0f);
+    }
+    // The listed tokens among the 32 columns from c on, which lie in shared memory, a thread its row's.
+    __device__ __forceinline__ void patch(const Stage& stage, State& s, int32_t c) const
+    {
+        while (s.place.token < first + c + 32) {
+            float& v = row_value(stage, s.place.token - first - c);
+            v = fmaf(-lists.q[s.place.list + s.place.at], s.factor, v);
+            s.place.token = next_token(lists, s.place, ++s.place.at);
         }
-#pragma unroll
-        for (int i = 0; i < kStrip; ++i) v[i] *= s.factor;
     }
     __device__ __forceinline__ void chunk(const Stage& stage, const State&, int32_t r0, int32_t, int32_t c0) const
     {
         const Turns<4> turn;
         const int32_t c = c0 + turn.col, left = n - c;
-#pragma unroll(sizeof(T) == 2 ? 8 : 2)
+#pragma unroll(sizeof(T) == 2 ? 8 : 1)
         for (int i = 0; i < 8; ++i) {
             const int32_t r = r0 + turn.row_of(i);
             if (r >= room) continue;

@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_bf16_kernel(const FewArgs g, 
     constexpr int kTiles = kTokens / 8, kAhead = kTokens == 8 ? 4 : 2;
     __shared__ __align__(16) float sums[kWarps][kTokens][20];
     ptx::griddep_wait();
+    ptx::griddep_launch();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, row = lane / 4, quad = lane & 3;
     const int32_t c0 = blockIdx.x * 16;
     const int32_t steps = (g.k + 31) / 32, each = (steps + kWarps - 1) / kWarps;
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(256, 2) few_f32_kernel(const FewArgs g, const 
 {
     constexpr int kOut = 4;
     ptx::griddep_wait();
+    ptx::griddep_launch();
     const int lane = threadIdx.x & 31;
     const int32_t c0 = (blockIdx.x * 8 + threadIdx.x / 32) * kOut;
     if (c0 >= g.n) return;
@@ -182,6 +184,7 @@ template <typename T, typename Epi> __global__ void __launch_bounds__(256) produ
     __shared__ __align__(16) float tile[8 * kSmallTile * kPitch];  // both operands' terms; then the warps' sums
     float *sa = tile, *sb = tile + kSmallDepth * kPitch;
     ptx::griddep_wait();
+    ptx::griddep_launch();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, r = lane / 4 * 4, c = lane % 4 * 8;
     const int32_t place = blockIdx.x / g.parts, part = blockIdx.x % g.parts, tiles_n = (g.n + kSmallTile - 1) / kSmallTile;
     const int32_t m0 = place / tiles_n * kSmallTile, n0 = place % tiles_n * kSmallTile;

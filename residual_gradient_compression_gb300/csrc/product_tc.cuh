@@ -66,6 +66,7 @@ constexpr int kTcPack = 256;
 template <typename T> __global__ void __launch_bounds__(kTcPack) pack_kernel(const PackArgs a)
 {
     ptx::griddep_wait();
+    ptx::griddep_launch();
     const int64_t count = a.count ? *a.count : a.rows, rows = a.count ? (count + kRows - 1) / kRows * kRows : count;
     const int64_t each = (a.cols + 7) / 8, all = rows * each;
     for (int64_t i = (int64_t)blockIdx.x * kTcPack + threadIdx.x; i < all; i += (int64_t)gridDim.x * kTcPack) {
@@ -500,14 +501,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 for (int i = 0; i < kStrip; ++i) v[i] = NAN;
             }
             if (c0 >= n) continue;
-            epi.rows(state, r, c0, n, t.n0 / g.width * ((g.width + kStrip - 1) / kStrip) + strip, r < m, v);
+            epi.rows(stage, state, r, c0, n, t.n0 / g.width * ((g.width + kStrip - 1) / kStrip) + strip, r < m, v);
             __syncwarp();
             if constexpr (Epi::kChunks) {
 #pragma unroll
                 for (int c = 0; c < kStrip; c += 32) {
                     if (c0 + c >= n) break;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) stage.at(lane, i) = make_float4(v[c + 4 * i], v[c + 4 * i + 1], v[c + 4 * i + 2], v[c + 4 * i + 3]);
+                    put_row(stage, v, c);
+                    if constexpr (Epi::kPatches) {
+                        if (r < m) epi.patch(stage, state, c0 + c);
+                    }
                     __syncwarp();
                     if constexpr (Epi::kAdds) {
                         if (g.splits > 1) {
@@ -541,6 +544,7 @@ struct JoinPartsArgs {
 template <int N, typename Epi> __global__ void __launch_bounds__(kRows) join_parts_kernel(const JoinPartsArgs a, const Epi epi)
 {
     ptx::griddep_wait();
+    ptx::griddep_launch();
     const int64_t m = a.m_count ? *a.m_count : a.m;
     const int64_t chunks = (a.n + N - 1) / N, i = (int64_t)blockIdx.x * kRows + threadIdx.x;
     if (i >= chunks * m) return;

@@ -105,6 +105,7 @@ template <typename L> __global__ void __launch_bounds__(kListThreads) vocab_teac
 {
     __shared__ int32_t keys[kListThreads / 32][ADACOMP_MAX_TEACHER];
     ptx::griddep_wait();
+    ptx::griddep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t r = (int64_t)blockIdx.x * (kListThreads / 32) + warp; r < a.rows;
          r += (int64_t)gridDim.x * (kListThreads / 32)) {
@@ -172,6 +173,7 @@ template <bool kTarget> __global__ void __launch_bounds__(kScanThreads) vocab_ro
     constexpr int kEach = kScanRows / kScanThreads, kWarps = kScanThreads / 32;
     __shared__ int32_t sums[2][kWarps];
     ptx::griddep_wait();
+    ptx::griddep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const auto target = [&](int64_t r) {
         return a.target_bytes == 8 ? static_cast<const int64_t*>(a.target)[r] : (int64_t) static_cast<const int32_t*>(a.target)[r];
@@ -223,6 +225,7 @@ template <typename T>
 __global__ void __launch_bounds__(kZeroThreads) vocab_zero_kernel(T* dx, int64_t stride, const float* given, int64_t rows, int64_t dim)
 {
     ptx::griddep_wait();
+    ptx::griddep_launch();
     const int64_t warps = kZeroThreads / 32;
     for (int64_t r = blockIdx.x * warps + threadIdx.x / 32; r < rows; r += gridDim.x * warps) {
         if (given[r] != -INFINITY) continue;
@@ -240,37 +243,45 @@ struct JoinArgs {
     float temperature;
 };
 
-// Rows' strips joined, and their losses; rows without a loss are 0. A CTA has 32 rows, a warp each 32nd of
-// their strips, a lane a row; then a warp a row, for its list.
-__global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinArgs a)
+// Rows' strips joined, and their losses; rows without a loss are 0. A CTA has kJoinRows rows: a warp's lanes have a strip of each,
+// or, where rows are few, four strips of eight rows; then a warp has a row, for its list.
+template <int kJoinRows> __global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinArgs a)
 {
-    constexpr int kWarps = kJoinThreads / 32;
-    __shared__ float2 sums[kWarps][33];
+    constexpr int kParts = kJoinThreads / kJoinRows;  // of a row's strips
+    __shared__ float2 sums[kJoinRows][kParts + 1];
     ptx::griddep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    ptx::griddep_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = threadIdx.x / kJoinRows, mine = threadIdx.x % kJoinRows;
     const int64_t count = *a.count;
-    for (int64_t r0 = (int64_t)blockIdx.x * 32; r0 < count; r0 += (int64_t)gridDim.x * 32) {
-        const int64_t r = r0 + lane;
+    for (int64_t r0 = (int64_t)blockIdx.x * kJoinRows; r0 < count; r0 += (int64_t)gridDim.x * kJoinRows) {
+        const int64_t r = r0 + mine;
         float top = -INFINITY, sum = 0.0f;
         if (r < count) {
-#pragma unroll 8
-            for (int64_t i = warp; i < a.strips; i += kWarps) {
+#pragma unroll 4
+            for (int64_t i = part; i < a.strips; i += kParts) {
                 const float2 p = a.part[i * a.rows + r];
                 const float more = fmaxf(top, p.x), less = more == -INFINITY ? 0.0f : more;
                 sum = sum * expf(top - less) + p.y * expf(p.x - less);
                 top = more;
             }
         }
-        sums[warp][lane] = make_float2(top, sum);
+        sums[mine][part] = make_float2(top, sum);
         __syncthreads();
-        if (const int i = warp; r0 + i < count) {
-            const float2 p = sums[lane][i];
-            float most = p.x;
+        if (warp < kJoinRows && r0 + warp < count) {
+            float2 p[kParts / 32];
+            float most = -INFINITY, all = 0.0f;
 #pragma unroll
-            for (int o = kWarps / 2; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            const float all = warp_sum(p.y * expf(p.x - (most == -INFINITY ? 0.0f : most)));
+            for (int i = 0; i < kParts / 32; ++i) {
+                p[i] = sums[warp][i * 32 + lane];
+                most = fmaxf(most, p[i].x);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+#pragma unroll
+            for (int i = 0; i < kParts / 32; ++i) all += p[i].y * expf(p[i].x - (most == -INFINITY ? 0.0f : most));
+            all = warp_sum(all);
             const float lse = most + logf(all);
-            const int64_t row = a.map[r0 + i];
+            const int64_t row = a.map[r0 + warp];
             const float given = a.given[row];
             float mean = 0.0f;  // of the logits under q
             if (given == given)
@@ -359,7 +370,9 @@ template <typename T> cudaError_t vocab_forward(const VocabArgs& a, void* ws, cu
     j.strips = strips_of(a.vocab, way.width);
     j.k = a.k;
     j.temperature = a.temperature;
-    return launch_after(vocab_join_kernel, dim3(blocks_of(a.rows, 32, 4096)), dim3(kJoinThreads), 0, stream, j);
+    // few rows by more CTAs (512 rows of 50304 tokens: 8.2 us, and 12 by 32 rows each)
+    if (a.rows <= 2048) return launch_after(vocab_join_kernel<8>, dim3(blocks_of(a.rows, 8, 4096)), dim3(kJoinThreads), 0, stream, j);
+    return launch_after(vocab_join_kernel<32>, dim3(blocks_of(a.rows, 32, 4096)), dim3(kJoinThreads), 0, stream, j);
 }
 
 template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, cudaStream_t stream)
