@@ -7,9 +7,10 @@
 // what it reads and writes in global memory are whole pieces of rows (a thread that writes its own row takes 32 cache
 // lines at a time: a linear layer's forward product of 8192 x 2048 x 16384 bf16 took 369 us so, and 313 without its
 // stores). kExact: the results are held in fp32, so the sums are formed in short runs.
-// kPieces: a thread may also hand over columns on their own, piece(). kAdds: there may be a matrix that
-// the sums are added to, which take() loads before they are there. kPatches: patch() changes single columns of a chunk in
-// shared memory.
+// kPieces: a thread may also hand over columns on their own, piece(). kFetches: there may be a matrix that
+// the chunks are added to: begin() brings it into L2, and fetch() loads a chunk while the one before is worked on (a chunk's
+// loads in its turn: a layer of 16384 x 2048 x 8192 bf16 with a residual 608 us, and 414 so). kPatches: patch() changes single columns of a chunk in
+// shared memory. kParts: part() takes the sums of a part of the terms.
 #pragma once
 
 #include "train_common.cuh"
@@ -152,6 +153,16 @@ __device__ __forceinline__ void put_row(const Stage& s, const float (&v)[kStrip]
     for (int i = 0; i < 8; ++i) s.at(lane, i) = make_float4(v[from + 4 * i], v[from + 4 * i + 1], v[from + 4 * i + 2], v[from + 4 * i + 3]);
 }
 
+__device__ __forceinline__ void put_chunk_of(const Stage& s, const float (&v)[kStrip], int chunk)  // in loops that are not unrolled
+{
+    switch (chunk) {
+    case 0: put_row(s, v, 0); break;
+    case 1: put_row(s, v, 32); break;
+    case 2: put_row(s, v, 64); break;
+    default: put_row(s, v, 96);
+    }
+}
+
 __device__ __forceinline__ float& row_value(const Stage& s, int col)
 {
     return reinterpret_cast<float*>(&s.at(threadIdx.x & 31, col / 4))[col & 3];
@@ -188,6 +199,68 @@ template <int N> struct Turns {
 inline bool whole_rows(const void* p, int64_t stride, int64_t rows, int bytes)
 {
     return is_aligned(p, 16) && (rows < 2 || stride * bytes % 16 == 0);
+}
+
+// A chunk of a matrix that an epilogue reads, as a warp takes it, on its way while the chunk before is worked on.
+struct Fetched {
+    uint32_t w[32];
+    template <typename T, int N> __device__ __forceinline__ void load(int turn, const T* p, int32_t left)
+    {
+        constexpr int kWords = N == 1 ? 1 : (int)sizeof(T);
+        uint32_t* to = w + turn * kWords;
+        if constexpr (N == 4) {
+            if (left >= 4) {
+                if constexpr (sizeof(T) == 4) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(p);
+                    to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
+                } else {
+                    const uint2 q = *reinterpret_cast<const uint2*>(p);
+                    to[0] = q.x, to[1] = q.y;
+                }
+                return;
+            }
+        }
+        const Cols<N> c = get<N>(p, left);
+        if constexpr (N == 4 && sizeof(T) == 2) {
+            to[0] = __float_as_uint(c.v[0]) >> 16 | (__float_as_uint(c.v[1]) & 0xffff0000u);
+            to[1] = __float_as_uint(c.v[2]) >> 16 | (__float_as_uint(c.v[3]) & 0xffff0000u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) to[i] = __float_as_uint(c.v[i]);
+        }
+    }
+    template <typename T, int N> __device__ __forceinline__ Cols<N> use(int turn) const
+    {
+        constexpr int kWords = N == 1 ? 1 : (int)sizeof(T);
+        const uint32_t* from = w + turn * kWords;
+        Cols<N> c;
+        if constexpr (N == 4 && sizeof(T) == 2) {
+            c.v[0] = bf16_low(from[0]), c.v[1] = bf16_high(from[0]), c.v[2] = bf16_low(from[1]), c.v[3] = bf16_high(from[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) c.v[i] = __uint_as_float(from[i]);
+        }
+        return c;
+    }
+    template <typename T, int N>
+    __device__ __forceinline__ void load_all(const T* p, int64_t stride, int32_t n, int32_t r0, int32_t end, int32_t c0)
+    {
+        const Turns<N> turn;
+        const int32_t c = c0 + turn.col, left = n - c;
+#pragma unroll
+        for (int i = 0; i < Turns<N>::kCount; ++i) {
+            const int32_t r = r0 + turn.row_of(i);
+            load<T, N>(i, p + r * stride + c, r < end ? left : 0);
+        }
+    }
+};
+
+// Brings a row's columns from p on into L2.
+template <typename T> __device__ __forceinline__ void prefetch_row(const T* p, int32_t left)
+{
+    const char* q = reinterpret_cast<const char*>(p);
+    const int32_t bytes = (left < kStrip ? left : kStrip) * (int32_t)sizeof(T);
+    for (int32_t i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i));
 }
 
 // Of a matrix in a workspace: rows begin with a cache line, unless they are shorter than one.
@@ -296,51 +369,53 @@ template <typename T, int kKind> __device__ __forceinline__ float slope(float z)
 // ---------------------------------------------------------------- epilogues
 // y = act(sum + bias) + residual, and the value before the activation.
 template <typename T> struct EpiLinear {
-    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kAdds = false, kPatches = false;
+    // fp32: one copy of the instructions, which a CTA with one or two tiles waits to be loaded (a training step of 3001 x 1001 x 777
+    // 187 and 165 us); bf16: four, whose stores overlap (gelu of 16384 x 2048 x 8192 with both outputs 432 and 378)
+    static constexpr int kUnroll = sizeof(T) == 4 ? 1 : 4;
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kFetches = true, kPatches = false, kParts = false;
     T *y, *pre;
     const T *bias, *residual;
     int64_t y_stride, pre_stride, residual_stride;
     int32_t n, act;
     bool whole;  // all of them
     struct State {};
-    __device__ __forceinline__ State begin(int32_t, int32_t) const { return {}; }
+    __device__ __forceinline__ bool fetches() const { return residual != nullptr; }
+    __device__ __forceinline__ State begin(int32_t r, int32_t c) const
+    {
+        if (residual) prefetch_row(residual + r * residual_stride + c, n - c);
+        return {};
+    }
     __device__ __forceinline__ void rows(const Stage&, const State&, int32_t, int32_t, int32_t, int32_t, bool, float (&)[kStrip]) const {}
 
-    template <int N, typename F> __device__ __forceinline__ void turns(const Stage& stage, int32_t r0, int32_t end, int32_t c0, F f) const
+    __device__ __forceinline__ void fetch(Fetched& f, int32_t r0, int32_t end, int32_t c0) const
+    {
+        if (whole) f.load_all<T, 4>(residual, residual_stride, n, r0, end, c0);
+        else f.load_all<T, 1>(residual, residual_stride, n, r0, end, c0);
+    }
+
+    // (Little unrolled: what a CTA runs once or a few times costs as much as its instructions take to be loaded.)
+    template <int N, typename F>
+    __device__ __forceinline__ void turns(const Stage& stage, const Fetched& fetched, int32_t r0, int32_t end, int32_t c0, F f) const
     {
         constexpr int kCount = Turns<N>::kCount;
         const Turns<N> turn;
         const int32_t c = c0 + turn.col, left = n - c;
         Cols<N> b = {};
         if (bias) b = get<N>(bias + c, left);
-        if (!residual) {
-#pragma unroll(N == 4 ? 4 : 8)
-            for (int i = 0; i < kCount; ++i) {
-                const int32_t r = r0 + turn.row_of(i);
-                const Cols<N> z = turn.read(stage, i) + b;
-                if (pre && r < end) put(pre + r * pre_stride + c, z, left);
-                const Cols<N> v = f(z);
-                if (r < end) put(y + r * y_stride + c, v, left);
-            }
-            return;
-        }
-        Cols<N> more[kCount];  // loads that wait together, while the activation is computed
-#pragma unroll
-        for (int i = 0; i < kCount; ++i) {
-            const int32_t r = r0 + turn.row_of(i);
-            more[i] = get<N>(residual + r * residual_stride + c, r < end ? left : 0);
-        }
-#pragma unroll(N == 4 ? 4 : 8)
+#pragma unroll(N == 4 ? 2 : 4)
         for (int i = 0; i < kCount; ++i) {
             const int32_t r = r0 + turn.row_of(i);
             const Cols<N> z = turn.read(stage, i) + b;
             if (pre && r < end) put(pre + r * pre_stride + c, z, left);
-            turn.write(stage, i, f(z));
+            const Cols<N> v = f(z);
+            if (residual) turn.write(stage, i, v);
+            else if (r < end) put(y + r * y_stride + c, v, left);
         }
+        if (!residual) return;
 #pragma unroll
         for (int i = 0; i < kCount; ++i) {
             const int32_t r = r0 + turn.row_of(i);
-            const Cols<N> v = turn.read(stage, i) + more[i];
+            const Cols<N> v = turn.read(stage, i) + fetched.use<T, N>(i);
             if (r < end) put(y + r * y_stride + c, v, left);
         }
     }
@@ -363,10 +438,10 @@ template <typename T> struct EpiLinear {
         }
     }
 
-    __device__ __forceinline__ void chunk(const Stage& stage, const State&, int32_t r0, int32_t end, int32_t c) const
+    __device__ __forceinline__ void chunk(const Stage& stage, const State&, const Fetched& fetched, int32_t r0, int32_t end, int32_t c) const
     {
-        if (whole) with_act([&](auto f) { turns<4>(stage, r0, end, c, f); });
-        else with_act([&](auto f) { turns<1>(stage, r0, end, c, f); });
+        if (whole) with_act([&](auto f) { turns<4>(stage, fetched, r0, end, c, f); });
+        else with_act([&](auto f) { turns<1>(stage, fetched, r0, end, c, f); });
     }
 
     // columns, by a thread on its own
@@ -385,7 +460,8 @@ template <typename T> struct EpiLinear {
 // fp32 (first: nothing to add to yet) and rounded by the last one only. Of a product whose terms are split, the parts'
 // sums go to acc, split_stride apart (and neither first nor last is asked).
 template <typename T> struct EpiStore {
-    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kAdds = true, kPatches = false;
+    static constexpr int kUnroll = sizeof(T) == 4 ? 1 : 4;
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kFetches = true, kPatches = false, kParts = true;
     T* out;
     float* acc;
     const int32_t* map;
@@ -395,22 +471,17 @@ template <typename T> struct EpiStore {
     struct State {
         int32_t to;
     };
-    __device__ __forceinline__ State begin(int32_t r, int32_t) const { return {map ? map[r] : r}; }
-    __device__ __forceinline__ bool adds() const { return !first; }
+    __device__ __forceinline__ bool fetches() const { return !first; }
+    __device__ __forceinline__ State begin(int32_t r, int32_t c) const
+    {
+        if (!first) prefetch_row(acc + r * acc_stride + c, n - c);
+        return {map ? map[r] : r};
+    }
     __device__ __forceinline__ void rows(const Stage&, const State&, int32_t, int32_t, int32_t, int32_t, bool, float (&)[kStrip]) const {}
 
-    __device__ __forceinline__ void take(const Stage& stage, int32_t r0, int32_t end, int32_t c0) const
+    __device__ __forceinline__ void fetch(Fetched& f, int32_t r0, int32_t end, int32_t c0) const
     {
-        const Turns<4> turn;
-        const int32_t c = c0 + turn.col, left = n - c;
-        Cols<4> v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int32_t r = r0 + turn.row_of(i);
-            v[i] = get<4>(acc + r * acc_stride + c, r < end ? left : 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) turn.write(stage, i, v[i]);
+        f.load_all<float, 4>(acc, acc_stride, n, r0, end, c0);
     }
 
     template <int N, typename O>
@@ -430,8 +501,14 @@ template <typename T> struct EpiStore {
         turns<4>(stage, r0 + (int32_t)(threadIdx.x & 31), acc + split * split_stride, acc_stride, r0, end, c0);
     }
 
-    __device__ __forceinline__ void chunk(const Stage& stage, const State& s, int32_t r0, int32_t end, int32_t c0) const
+    __device__ __forceinline__ void chunk(const Stage& stage, const State& s, const Fetched& fetched, int32_t r0, int32_t end, int32_t c0) const
     {
+        if (!first) {
+            const Turns<4> turn;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) turn.write(stage, i, turn.read(stage, i) + fetched.use<float, 4>(i));
+            __syncwarp();
+        }
         if (!last) turns<4>(stage, r0 + (int32_t)(threadIdx.x & 31), acc, acc_stride, r0, end, c0);
         else if (whole) turns<4>(stage, s.to, out, stride, r0, end, c0);
         else turns<1>(stage, s.to, out, stride, r0, end, c0);
@@ -491,7 +568,8 @@ __device__ __forceinline__ int32_t next_token(const Lists& l, const Place& p, in
 // Of each strip of up to 128 logits of a row: their maximum and the sum of exp(z - maximum); and the logits
 // of the listed tokens.
 template <typename T> struct EpiSoftmax {
-    static constexpr bool kExact = true, kChunks = false, kPieces = false, kAdds = false, kPatches = false;
+    static constexpr int kUnroll = 1;
+    static constexpr bool kExact = true, kChunks = false, kPieces = false, kFetches = false, kPatches = false, kParts = false;
     float2* part;  // [strips][row_stride]
     float* picked;
     Lists lists;
@@ -507,9 +585,9 @@ template <typename T> struct EpiSoftmax {
         for (int i = 0; i < kStrip; ++i) v[i] *= scale;
         if (__any_sync(0xffffffffu, live && s.token < end)) {  // by shared memory, where a column can be an index
             int32_t at = s.at, token = live ? s.token : INT32_MAX;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < kStrip; q += 32) {
-                put_row(stage, v, q);
+                put_chunk_of(stage, v, q / 32);
                 for (; token < end && token < c + q + 32; token = next_token(lists, s, ++at)) picked[s.list + at] = row_value(stage, token - c - q);
             }
         }
@@ -528,13 +606,14 @@ template <typename T> struct EpiSoftmax {
         for (int i = 0; i < kStrip; ++i) sum[i & 3] += exp_of<T>(v[i] - less);
         part[strip * row_stride + r] = make_float2(top[0], (sum[0] + sum[1]) + (sum[2] + sum[3]));
     }
-    __device__ __forceinline__ void chunk(const Stage&, const State&, int32_t, int32_t, int32_t) const {}
+    __device__ __forceinline__ void chunk(const Stage&, const State&, const Fetched&, int32_t, int32_t, int32_t) const {}
 };
 
 // The logits' gradient (p - q) * dloss * temperature of columns first .. first + n - 1: rounded to
 // bf16, or, of fp32 operands, in parts. Rows past the last one, up to a tile's end, are zeros: they are terms of a product.
 template <typename T> struct EpiGradient {
-    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = false, kAdds = false, kPatches = true;
+    static constexpr int kUnroll = sizeof(T) == 4 ? 1 : 4;
+    static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = false, kFetches = false, kPatches = true, kParts = false;
     bf16* dz;  // [planes][room][stride]
     Lists lists;
     const float *lse, *dloss, *given;
@@ -571,7 +650,7 @@ template <typename T> struct EpiGradient {
             s.place.token = next_token(lists, s.place, ++s.place.at);
         }
     }
-    __device__ __forceinline__ void chunk(const Stage& stage, const State&, int32_t r0, int32_t, int32_t c0) const
+    __device__ __forceinline__ void chunk(const Stage& stage, const State&, const Fetched&, int32_t r0, int32_t, int32_t c0) const
     {
         const Turns<4> turn;
         const int32_t c = c0 + turn.col, left = n - c;

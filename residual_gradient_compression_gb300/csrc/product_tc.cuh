@@ -462,21 +462,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             float v[kStrip];
 #pragma unroll
             for (int i = 0; i < kStrip; ++i) v[i] = 0.0f;
-            if constexpr (Epi::kAdds) {
-                if (epi.adds() && g.splits == 1) {  // what the sums are added to, while they are computed
-#pragma unroll
-                    for (int c = 0; c < kStrip; c += 32) {
-                        if (c0 + c >= n) break;
-                        epi.take(stage, r - lane, m, c0 + c);
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 more = stage.at(lane, i);
-                            v[c + 4 * i] = more.x, v[c + 4 * i + 1] = more.y, v[c + 4 * i + 2] = more.z, v[c + 4 * i + 3] = more.w;
-                        }
-                        __syncwarp();
-                    }
-                }
+            Fetched ahead;
+            bool fetches = false;
+            if constexpr (Epi::kFetches) {
+                fetches = c0 < n && g.splits == 1 && epi.fetches();
+                if (fetches) epi.fetch(ahead, r - lane, m, c0);
             }
 #pragma unroll 1
             for (int32_t from = 0; from < t.count; from += g.run, ++done) {
@@ -504,22 +494,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             epi.rows(stage, state, r, c0, n, t.n0 / g.width * ((g.width + kStrip - 1) / kStrip) + strip, r < m, v);
             __syncwarp();
             if constexpr (Epi::kChunks) {
-#pragma unroll
+#pragma unroll(Epi::kUnroll)
                 for (int c = 0; c < kStrip; c += 32) {
                     if (c0 + c >= n) break;
-                    put_row(stage, v, c);
+                    const Fetched now = ahead;
+                    put_chunk_of(stage, v, c / 32);
+                    if constexpr (Epi::kFetches) {
+                        if (fetches && c + 32 < kStrip && c0 + c + 32 < n) epi.fetch(ahead, r - lane, m, c0 + c + 32);
+                    }
                     if constexpr (Epi::kPatches) {
                         if (r < m) epi.patch(stage, state, c0 + c);
                     }
                     __syncwarp();
-                    if constexpr (Epi::kAdds) {
+                    if constexpr (Epi::kParts) {
                         if (g.splits > 1) {
                             epi.part(stage, t.split, r - lane, m, c0 + c);
                             __syncwarp();
                             continue;
                         }
                     }
-                    epi.chunk(stage, state, r - lane, m, c0 + c);
+                    epi.chunk(stage, state, now, r - lane, m, c0 + c);
                     __syncwarp();
                 }
             }
