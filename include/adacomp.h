@@ -522,15 +522,15 @@ void adacomp_adamw_free(adacomp_adamw_t h);
 /* ------------------------------------------------------------------------------
  * Linear layers and losses over a vocabulary: the matrix products of a training step. The
  * conventions of the training operators above hold. Matrices are strided by rows: inputs
- * by any stride >= 0 (0: one row read for all), outputs by at least a row. With 16-byte aligned
+ * by any stride >= 0 (0: one row read for all), outputs by at least a row; up to 2^30 rows. With 16-byte aligned
  * pointers and row strides that are multiples of 16 bytes they are used as they lie; others are
  * first copied into the workspace. Workspaces are 16-byte aligned, need no initialisation, and
  * serve one call at a time.
  *
- * bf16 products are exact and summed in fp32. fp32 numbers are split into three bf16 numbers that
- * add up to them (what is below 2^-133 is lost), and of the nine products of parts the six
- * largest are summed, which leaves out less than 2^-22 of a product. Sums may add the terms
- * in any order that depends on the sizes alone, and round or truncate each partial sum.
+ * bf16 products are exact and summed in fp32. fp32 numbers are, but in small products, split into three
+ * bf16 numbers that add up to them (what is below 2^-126 may be lost), and of the nine products of
+ * parts the six largest are summed, which leaves out less than 2^-22 of a product. Sums add the terms
+ * in an order that depends on sizes and alignment alone, and round or truncate each partial sum.
  *
  * The kernels wait for their own copies and products. Such a wait is bounded by 2 s; on expiry the call
  * still ends, and the results that it had not computed are NaN. Nothing traps.
@@ -619,7 +619,7 @@ adacomp_status adacomp_vocab_loss_backward(adacomp_vocab_t h, int64_t rows, cons
  *            A token that is listed twice counts twice.
  *   logit    device, of logit_dtype, [rows][k], rows logit_stride apart; not used where index is
  *            negative. -inf is a probability of 0; a row of nothing else has a loss of NaN.
- * temperature is finite and positive. The vocabulary's gradients as above, with
+ * temperature is positive, and it, its square and its inverse are finite. The vocabulary's gradients as above, with
  *     dz = t * (p - sum of q over the token's places in the list) * dloss. */
 #define ADACOMP_MAX_TEACHER 256
 adacomp_status adacomp_distill_forward(adacomp_vocab_t h, int64_t rows, const void* x, int64_t x_stride, const void* w,

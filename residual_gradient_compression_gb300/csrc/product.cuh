@@ -568,7 +568,6 @@ __device__ __forceinline__ int32_t next_token(const Lists& l, const Place& p, in
 // Of each strip of up to 128 logits of a row: their maximum and the sum of exp(z - maximum); and the logits
 // of the listed tokens.
 template <typename T> struct EpiSoftmax {
-    static constexpr int kUnroll = 1;
     static constexpr bool kExact = true, kChunks = false, kPieces = false, kFetches = false, kPatches = false, kParts = false;
     float2* part;  // [strips][row_stride]
     float* picked;

@@ -600,7 +600,7 @@ inline cudaError_t tensor_map(CUtensorMap* map, const Matrix& a, int planes, int
 // Whether a bf16 matrix can be read as it lies.
 inline bool as_it_lies(const void* p, int64_t stride, int64_t rows, int64_t cols)
 {
-    return is_aligned(p, 16) && (rows < 2 ? true : stride % 8 == 0 && stride >= cols);
+    return is_aligned(p, 16) && (rows < 2 || (stride % 8 == 0 && stride >= cols && stride < (int64_t)1 << 38));
 }
 
 inline Matrix matrix_of(const void* p, int64_t stride, int64_t rows, int64_t cols)
@@ -732,6 +732,7 @@ template <typename T, typename Epi> TcSize size_of(const TcProduct& x) { return 
 // The epilogue of a product whose terms are split: its parts' sums.
 template <typename T> EpiStore<T> to_parts(EpiStore<T> epi, float* parts, const TcProduct& x)
 {
+    epi.first = true;
     epi.acc = parts;
     epi.acc_stride = round_up(x.n, 4);
     epi.split_stride = x.m * epi.acc_stride;

@@ -46,12 +46,22 @@ struct VocabParts {
     int64_t padded, dz_stride, piece;
 };
 
-// Columns of a piece: so many that the piece's gradient has some 2^27 elements, and no fewer than 2048.
+// Columns of a piece: so many that the piece's gradient, of whole tiles of rows, has up to 2^27 elements, and no fewer than
+// 2048; and the most elements that one of up to `rows` rows has.
+constexpr int64_t kPieceElements = (int64_t)1 << 27, kLeastPiece = 2048;
 int64_t piece_of(int64_t rows, int64_t vocab)
 {
-    int64_t n = rows > 0 ? ((int64_t)1 << 27) / rows / kStrip * kStrip : vocab;
-    if (n < 2048) n = 2048;
+    const int64_t padded = round_up(rows < 1 ? 1 : rows, kRows);
+    if (padded * pitch_of(vocab) <= kPieceElements) return vocab;
+    int64_t n = kPieceElements / padded / kStrip * kStrip;
+    if (n < kLeastPiece) n = kLeastPiece;
     return n < vocab ? n : vocab;
+}
+int64_t piece_elements(int64_t rows, int64_t vocab)
+{
+    const int64_t padded = round_up(rows < 1 ? 1 : rows, kRows), all = padded * pitch_of(vocab);
+    const int64_t least = padded * pitch_of(vocab < kLeastPiece ? vocab : kLeastPiece);
+    return all <= kPieceElements ? all : least > kPieceElements ? least : kPieceElements;
 }
 
 // Strips of a row's logits, in tiles of `width` columns; and at most, whatever the tiles (of which all but narrow
@@ -77,9 +87,9 @@ VocabParts vocab_parts(Carve& c, int64_t rows, int64_t dim, int64_t vocab, int b
     if (backward) {
         p.piece = piece_of(rows, vocab);
         p.dz_stride = pitch_of(p.piece);
-        p.dz = c.take<bf16>(packed_elements(p.padded, p.piece, bytes));
+        p.dz = c.take<bf16>(piece_elements(rows, vocab) * (bytes == 4 ? kPlanes : 1));
         p.acc = c.take<float>(rows * round_up(dim, 4));
-        p.parts = c.take<float>(parts_elements(rows, dim) + parts_elements(p.piece, dim));
+        p.parts = c.take<float>(parts_elements(rows, dim) + parts_elements(vocab, dim));
     } else {
         p.part = c.take<float2>(rows * most_strips(vocab));
         p.picked = c.take<float>(rows * k);
@@ -496,7 +506,7 @@ bool target_fits(const VocabArgs& a)
 bool teacher_fits(const VocabArgs& a)
 {
     return a.k >= 1 && a.k <= ADACOMP_MAX_TEACHER && known_dtype(a.logit_dtype) && a.temperature > 0.0f &&
-           std::isfinite(a.temperature) &&
+           std::isfinite(a.temperature * a.temperature) && std::isfinite(1.0f / a.temperature) &&
            (a.rows == 0 || (a.index && a.logit && a.index_stride >= 0 && a.logit_stride >= 0));
 }
 

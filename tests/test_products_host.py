@@ -128,7 +128,7 @@ def test_distill_refuses_before_launch(dt):
                        [h.ptr, 4, A, 10, A, 10, 5, A, 5, A, 5, dt, 2.0, A, A, 1, A, 10, A, 10, A, backward_need, None])
     inf, nan = float("inf"), float("nan")
     for change in ({"a0": None}, {"a1": -1}, {"a2": None}, {"a4": None}, {"a6": 0}, {"a6": 257}, {"a7": None},
-                   {"a8": -1}, {"a9": None}, {"a10": -1}, {"a11": 2}, {"a12": 0.0}, {"a12": -1.0}, {"a12": inf},
+                   {"a8": -1}, {"a9": None}, {"a10": -1}, {"a11": 2}, {"a12": 0.0}, {"a12": -1.0}, {"a12": inf}, {"a12": 1e-39}, {"a12": 1e20},
                    {"a12": nan}, {"a13": None}, {"a14": None}):
         assert call(**change) == ac.ERR_INVALID_ARG, change
         assert backward(**change) == ac.ERR_INVALID_ARG, change
@@ -162,3 +162,16 @@ def test_free_takes_null_and_twice():
     for _ in range(2):
         ac.adacomp_linear_free(h)
         ac.adacomp_vocab_free(v)
+
+
+@pytest.mark.parametrize("dim,vocab", [(1, 1), (8, 1000), (64, 2047), (2048, 50304), (500, 10007)])
+@pytest.mark.parametrize("dt", [ac.F32, ac.BF16])
+def test_a_workspace_for_more_rows_is_enough_for_fewer(dim, vocab, dt):
+    """Fewer rows take the vocabulary in larger pieces, and split sums into more parts."""
+    v, h = ac.adacomp_vocab_init(dim, vocab, dt), ac.adacomp_linear_init(dim, vocab, dt)
+    rows = sorted({1, 2, 127, 128, 129, 1000, 2500, 4096, 5000, 5120, 8191, 8192, 65536, 65537, 131072, 134016, 134144, 10 ** 6})
+    for size in (lambda r: ac.adacomp_vocab_loss_forward_ws_bytes(v, r), lambda r: ac.adacomp_vocab_loss_backward_ws_bytes(v, r),
+                 lambda r: ac.adacomp_distill_forward_ws_bytes(v, r, 9), lambda r: ac.adacomp_distill_backward_ws_bytes(v, r, 9),
+                 lambda r: ac.adacomp_linear_forward_ws_bytes(h, r), lambda r: ac.adacomp_linear_backward_ws_bytes(h, r)):
+        sizes = [size(r) for r in rows]
+        assert sizes == sorted(sizes) and sizes[0] > 0
