@@ -566,7 +566,8 @@ adacomp_status adacomp_linear_forward(adacomp_linear_t h, int64_t rows, const vo
 
 /* From dy, with dz = dy * act'(pre) (dy itself without an activation; pre may then be NULL):
  *     dx = dz w,  dw = dz^T x,  db = sum over rows of dz;   the residual's gradient is dy.
- * For the products dz is rounded to bf16 where dtype is bf16; db is summed from the unrounded dz. dx, dw and
+ * For the products dz is rounded to bf16 where dtype is bf16 (of up to 32 rows, taken in two parts); db is summed from
+ * the unrounded dz. dx, dw and
  * db may each be NULL (not wanted; x is needed for dw only, w for dx only) and are overwritten
  * (dw and db with zeros for 0 rows). */
 adacomp_status adacomp_linear_backward(adacomp_linear_t h, int64_t rows, const void* dy, int64_t dy_stride,
@@ -600,7 +601,8 @@ adacomp_status adacomp_vocab_loss_forward(adacomp_vocab_t h, int64_t rows, const
 /* The gradients, from the gradient dloss of loss (device fp32; row r's is dloss[r * dloss_stride], so 0 is one
  * value for all rows; not used for rows without a loss):
  *     dz = (exp(z - lse) - [v = target]) * dloss,  dx = dz w,  dw = dz^T x.
- * For the products dz is rounded to bf16 where dtype is bf16. dx and dw may each be NULL (not both) and are overwritten: dx is 0
+ * For the products dz is rounded to bf16 where dtype is bf16 (of up to 32 rows, taken in two
+ * parts). dx and dw may each be NULL (not both) and are overwritten: dx is 0
  * in rows without a loss, dw is 0 if no row has one. A target of vocab or more makes the row's
  * dx, and dw, NaN. */
 adacomp_status adacomp_vocab_loss_backward(adacomp_vocab_t h, int64_t rows, const void* x, int64_t x_stride,

@@ -41,7 +41,9 @@ LinearParts linear_parts(Carve& c, int64_t rows, int64_t in, int64_t out, int by
     int64_t most = parts_elements(rows, out);
     if (backward) {
         p.sums = c.take<float>(kDzSlices * out);
-        p.dz = c.take<bf16>(packed_elements(rows, out, bytes));
+        // in two parts, or as fp32 numbers, of few rows
+        const int64_t few = packed_elements(2 * (rows < kFewRows ? rows : kFewRows), out, bytes), all = packed_elements(rows, out, bytes);
+        p.dz = c.take<bf16>(few > all ? few : all);
         most = parts_elements(rows, in) + parts_elements(out, in);
     }
     p.parts = c.take<float>(most);
@@ -68,7 +70,7 @@ struct DzArgs {
     float* sums;
     int64_t rows, n, dy_stride, pre_stride, dz_stride, dz_plane;
     int32_t act, slices;
-    bool plain, dy_whole, pre_whole;
+    bool plain, two, dy_whole, pre_whole;  // two: parts; with plain, fp32 numbers
 };
 
 // Eight columns of a row as they lie in memory, until they are used.
@@ -129,8 +131,9 @@ template <typename T, int kAct, int kDzRows> __device__ __forceinline__ void dz_
                 sum[j] += d[j];
             }
             if (kAct == ADACOMP_ACT_NONE || !a.dz) continue;
-            if (a.plain) put_chunk(static_cast<T*>(a.dz) + r * a.dz_stride + c, d, left, true);
-            else put_parts<T>(static_cast<bf16*>(a.dz) + r * a.dz_stride + c, a.dz_plane, d, left);
+            if (a.plain && a.two) put_chunk(static_cast<float*>(a.dz) + r * a.dz_stride + c, d, left, true);
+            else if (a.plain) put_chunk(static_cast<T*>(a.dz) + r * a.dz_stride + c, d, left, true);
+            else put_parts<T>(static_cast<bf16*>(a.dz) + r * a.dz_stride + c, a.dz_plane, d, left, a.two);
         }
     }
 }
@@ -200,7 +203,7 @@ template <typename T> cudaError_t linear_forward(const LinearArgs& a, void* ws, 
     if (a.rows <= (sizeof(T) == 2 ? kFewBf16 : kFewF32))
         return product_few<T>(FewArgs{a.x, a.w, a.x_stride, a.w_stride, (int32_t)a.rows, (int32_t)a.out, (int32_t)a.in}, epi, stream);
     if (is_small<T>(a.rows, a.out, a.in))
-        return product_small<T>(SmallArgs{{a.x, a.x_stride, 1}, {a.w, a.w_stride, 1}, (int32_t)a.rows, (int32_t)a.out, (int32_t)a.in}, epi, stream);
+        return product_small<T, T>(SmallArgs{{a.x, a.x_stride, 1}, {a.w, a.w_stride, 1}, (int32_t)a.rows, (int32_t)a.out, (int32_t)a.in}, epi, stream);
     Carve carve{static_cast<char*>(ws)};
     const LinearParts p = linear_parts(carve, a.rows, a.in, a.out, sizeof(T), false);
     Matrix x, w;
@@ -216,6 +219,7 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
     Carve carve{static_cast<char*>(ws)};
     const LinearParts p = linear_parts(carve, a.rows, a.in, a.out, sizeof(T), true);
     const bool act = a.act != ADACOMP_ACT_NONE, products = a.dx || a.dw, small = is_small<T>(a.rows, a.in, a.out) && is_small<T>(a.out, a.in, a.rows);
+    const bool two = sizeof(T) == 2 && act && a.rows <= kFewRows;
     cudaError_t e = cudaSuccess;
     Matrix dz = {p.dz, a.rows, a.out, pitch_of(a.out), a.rows * pitch_of(a.out)}, x, w;
     if ((act && products) || a.db) {
@@ -232,6 +236,7 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
         d.dz_plane = dz.plane;
         d.act = a.act;
         d.plain = small;
+        d.two = two;
         d.dy_whole = whole_rows(a.dy, a.dy_stride, a.rows, sizeof(T));
         d.pre_whole = whole_rows(a.pre_in, a.pre_in_stride, a.rows, sizeof(T));
         // CTAs for eight on each SM, of no fewer than two rows a thread
@@ -264,17 +269,17 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
     const int32_t rows = (int32_t)a.rows, in = (int32_t)a.in, out = (int32_t)a.out;
     if (small) {
         const Operand by_row = act ? Operand{p.dz, dz.stride, 1} : Operand{a.dy, a.dy_stride, 1};
-        if (a.dx) e = product_small<T>(SmallArgs{by_row, {a.w, 1, a.w_stride}, rows, in, out}, to_dx, stream);
-        if (a.dw && e == cudaSuccess)
-            e = product_small<T>(SmallArgs{{by_row.p, 1, by_row.row}, {a.x, 1, a.x_stride}, out, in, rows}, to_dw, stream);
+        const SmallArgs to_x = {by_row, {a.w, 1, a.w_stride}, rows, in, out}, to_w = {{by_row.p, 1, by_row.row}, {a.x, 1, a.x_stride}, out, in, rows};
+        if (a.dx) e = two ? product_small<float, T>(to_x, to_dx, stream) : product_small<T, T>(to_x, to_dx, stream);
+        if (a.dw && e == cudaSuccess) e = two ? product_small<float, T>(to_w, to_dw, stream) : product_small<T, T>(to_w, to_dw, stream);
         return e;
     }
     if (!act && products) e = take_matrix<T>(&dz, a.dy, a.dy_stride, a.rows, a.out, p.dz, stream);
     if (a.dx && e == cudaSuccess) e = take_matrix<T>(&w, a.w, a.w_stride, a.out, a.in, p.w, stream);
     if (a.dw && e == cudaSuccess) e = take_matrix<T>(&x, a.x, a.x_stride, a.rows, a.in, p.x, stream);
     if (e != cudaSuccess) return e;
-    const TcProduct dx = {dz, w, false, true, a.rows, a.in, a.out, nullptr, nullptr};
-    const TcProduct dw = {dz, x, true, true, a.out, a.in, a.rows, nullptr, nullptr};
+    const TcProduct dx = {dz, w, false, true, a.rows, a.in, a.out, nullptr, nullptr, two ? 2 : 1};
+    const TcProduct dw = {dz, x, true, true, a.out, a.in, a.rows, nullptr, nullptr, two ? 2 : 1};
     if (a.dx && a.dw) return product_tc_both<T>(dx, to_dx, dw, to_dw, p.parts, stream);
     if (a.dx) return product_tc<T>(dx, p.parts, to_dx, stream);
     return a.dw ? product_tc<T>(dw, p.parts, to_dw, stream) : cudaSuccess;

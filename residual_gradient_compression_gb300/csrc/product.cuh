@@ -284,11 +284,36 @@ __device__ __forceinline__ void split_parts(float x, bf16 (&part)[kPlanes])
     part[3] = part[0];
 }
 
-// A row's columns as operands of another product: bf16 numbers, or, of an fp32 matrix, planes of them.
-template <typename T, int N> __device__ __forceinline__ void put_parts(bf16* p, int64_t plane, const float (&v)[N], int64_t left)
+// A value in two parts of one sign, so that an infinite factor meets no 0 or other sign in the second: what bf16 has of its
+// bits, and the rest, or where there is none 2^-24 of it.
+__device__ __forceinline__ float first_of(float v) { return __bfloat162float(__float2bfloat16_rz(v)); }
+__device__ __forceinline__ float rest_of(float v)
+{
+    if (isinf(v)) return copysignf(1.0f, v);
+    const float rest = v - first_of(v);
+    return rest == 0.0f ? v * 5.9604645e-8f : rest;
+}
+
+// The gradient of bf16 products is an operand of two more. It is rounded to bf16 for them, by 2^-9 of each value at random, which
+// is less than their results' own rounding where sums of many rows or columns are formed; of up to kFewRows rows, whose few
+// values may share one rounding, it is taken in two parts (the products' time is that of reading and writing the weights).
+constexpr int64_t kFewRows = 32;
+
+// A row's columns as operands of another product: bf16 numbers, two planes of them, or, of an fp32 matrix, four.
+template <typename T, int N> __device__ __forceinline__ void put_parts(bf16* p, int64_t plane, const float (&v)[N], int64_t left, bool two)
 {
     if constexpr (sizeof(T) == 2) {
-        put_chunk(p, v, left, true);
+        if (!two) {
+            put_chunk(p, v, left, true);
+            return;
+        }
+        float part[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) part[i] = first_of(v[i]);
+        put_chunk(p, part, left, true);
+#pragma unroll
+        for (int i = 0; i < N; ++i) part[i] = rest_of(v[i]);
+        put_chunk(p + plane, part, left, true);
     } else {
 #pragma unroll
         for (int i = 0; i < N; i += 8) {
@@ -609,7 +634,7 @@ template <typename T> struct EpiSoftmax {
 };
 
 // The logits' gradient (p - q) * dloss * temperature of columns first .. first + n - 1: rounded to
-// bf16, or, of fp32 operands, in parts. Rows past the last one, up to a tile's end, are zeros: they are terms of a product.
+// bf16, or in parts. Rows past the last one, up to a tile's end, are zeros: they are terms of a product.
 template <typename T> struct EpiGradient {
     static constexpr int kUnroll = sizeof(T) == 4 ? 1 : 4;
     static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = false, kFetches = false, kPatches = true, kParts = false;
@@ -619,6 +644,7 @@ template <typename T> struct EpiGradient {
     int64_t stride, plane, dloss_stride;
     int32_t room, n, first;
     float scale, temperature;
+    bool two;  // parts of bf16 results
     struct State {
         Place place;
         float lse, factor;
@@ -660,7 +686,17 @@ template <typename T> struct EpiGradient {
             const Cols<4> v = turn.read(stage, i);
             bf16* to = dz + r * stride + c;
             if constexpr (sizeof(T) == 2) {
-                put(to, v, left);
+                if (!two) {
+                    put(to, v, left);
+                    continue;
+                }
+                Cols<4> part;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) part.v[j] = first_of(v.v[j]);
+                put(to, part, left);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) part.v[j] = rest_of(v.v[j]);
+                put(to + plane, part, left);
             } else {
                 Cols<4> part[kPlanes];
 #pragma unroll

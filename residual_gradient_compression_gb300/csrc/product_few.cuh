@@ -178,7 +178,7 @@ constexpr int kSmallTile = 32, kSmallDepth = 128;
 // tile's sums, fp32, in its warp's terms; the warps' sums meet in shared memory. A block of terms takes over a
 // microsecond, most of it waiting for loads, so where tiles are few the terms are split over the CTAs of a cluster, whose sums the
 // first one reads from the others' shared memory.
-template <typename T, typename Epi> __global__ void __launch_bounds__(256) product_small_kernel(const SmallArgs g, const Epi epi)
+template <typename A, typename B, typename Epi> __global__ void __launch_bounds__(256) product_small_kernel(const SmallArgs g, const Epi epi)
 {
     constexpr int kPitch = kSmallTile + 4, kEach = kSmallTile * kSmallDepth / 256;
     __shared__ __align__(16) float tile[8 * kSmallTile * kPitch];  // both operands' terms; then the warps' sums
@@ -192,32 +192,32 @@ template <typename T, typename Epi> __global__ void __launch_bounds__(256) produ
     const int32_t first = part * each * kSmallDepth, end = g.k - first < each * kSmallDepth ? g.k : first + each * kSmallDepth;
     // A thread's elements of an operand's block are kEach places `step` apart, along its rows or its terms.
     struct Mine {
-        const T* p;
-        int64_t step, next;         // between a block's elements, and to the next block
+        const char* p;
+        int64_t step, next;         // bytes between a block's elements, and to the next block
         int32_t term, row, left, each;  // its first element; how far the other coordinate may go, in elements of the block
         int32_t at, at_step;        // in shared memory
         bool by_terms;
     };
-    const auto mine = [&](const Operand& o, int32_t r0, int32_t rows) {
+    const auto mine = [&](const Operand& o, int32_t r0, int32_t rows, int32_t bytes) {
         Mine m;
         m.by_terms = o.term == 1;
         m.term = m.by_terms ? threadIdx.x % kSmallDepth : threadIdx.x / kSmallTile;
         m.row = m.by_terms ? threadIdx.x / kSmallDepth : threadIdx.x % kSmallTile;
         m.each = m.by_terms ? 256 / kSmallDepth : 256 / kSmallTile;
-        m.step = m.each * (m.by_terms ? o.row : o.term);
-        m.next = kSmallDepth * o.term;
-        m.p = static_cast<const T*>(o.p) + (r0 + m.row) * o.row + (int64_t)(first + m.term) * o.term;
+        m.step = m.each * (m.by_terms ? o.row : o.term) * bytes;
+        m.next = kSmallDepth * o.term * bytes;
+        m.p = static_cast<const char*>(o.p) + ((r0 + m.row) * o.row + (int64_t)(first + m.term) * o.term) * bytes;
         m.left = rows - r0 - m.row;
         m.at = m.term * kPitch + m.row;
         m.at_step = m.each * (m.by_terms ? 1 : kPitch);
         return m;
     };
-    const auto load = [&](Mine& m, int32_t k0, float (&v)[kEach]) {
+    const auto load = [&](auto type, Mine& m, int32_t k0, float (&v)[kEach]) {
         const int32_t terms = end - k0 - m.term;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const bool there = m.by_terms ? terms > 0 && i * m.each < m.left : m.left > 0 && i * m.each < terms;
-            v[i] = there ? to_f32(m.p[i * m.step]) : 0.0f;
+            v[i] = there ? to_f32(*reinterpret_cast<const decltype(type)*>(m.p + i * m.step)) : 0.0f;
         }
         m.p += m.next;
     };
@@ -226,16 +226,16 @@ template <typename T, typename Epi> __global__ void __launch_bounds__(256) produ
         for (int i = 0; i < kEach; ++i) s[m.at + i * m.at_step] = v[i];
     };
     float va[kEach], vb[kEach], d[4][8] = {};
-    Mine ma = mine(g.a, m0, g.m), mb = mine(g.b, n0, g.n);
-    load(ma, first, va);
-    load(mb, first, vb);
+    Mine ma = mine(g.a, m0, g.m, sizeof(A)), mb = mine(g.b, n0, g.n, sizeof(B));
+    load(A{}, ma, first, va);
+    load(B{}, mb, first, vb);
     for (int32_t k0 = first; k0 < end; k0 += kSmallDepth) {
         store(ma, sa, va);
         store(mb, sb, vb);
         __syncthreads();
         if (k0 + kSmallDepth < end) {
-            load(ma, k0 + kSmallDepth, va);
-            load(mb, k0 + kSmallDepth, vb);
+            load(A{}, ma, k0 + kSmallDepth, va);
+            load(B{}, mb, k0 + kSmallDepth, vb);
         }
 #pragma unroll
         for (int i = 0; i < kSmallDepth / 8; ++i) {
@@ -282,7 +282,7 @@ template <typename T, typename Epi> __global__ void __launch_bounds__(256) produ
     if (part == 0 && m0 + row < g.m && n0 + col < g.n) put_piece(epi, m0 + row, n0 + col, v);
 }
 
-template <typename T, typename Epi> cudaError_t product_small(SmallArgs g, const Epi& epi, cudaStream_t stream)
+template <typename A, typename B, typename Epi> cudaError_t product_small(SmallArgs g, const Epi& epi, cudaStream_t stream)
 {
     const int64_t tiles = (int64_t)((g.n + kSmallTile - 1) / kSmallTile) * ((g.m + kSmallTile - 1) / kSmallTile);
     // up to two CTAs an SM, of no fewer than a block of terms
@@ -299,7 +299,7 @@ template <typename T, typename Epi> cudaError_t product_small(SmallArgs g, const
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = g.parts > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, product_small_kernel<T, Epi>, (const SmallArgs)g, epi);
+    return cudaLaunchKernelEx(&cfg, product_small_kernel<A, B, Epi>, (const SmallArgs)g, epi);
 }
 
 }  // namespace

@@ -44,7 +44,7 @@ struct Matrix {
 struct TcArgs {
     int64_t m, n, k;
     const int32_t *m_count, *k_count;  // how many of the rows m, or terms k, there are; NULL: all
-    int32_t planes;                    // 1, or kPlanes
+    int32_t passes;                    // products of planes that are summed: 1, two of a bf16 A in two parts, or kSix
     int32_t splits;                    // of the terms, each a product of its own
     int32_t a_mn, b_mn;                // operands that lie by terms
     int32_t run;                       // blocks of terms whose sums are formed in tensor memory
@@ -208,7 +208,9 @@ __device__ __forceinline__ void read_wait() { asm volatile("tcgen05.wait::ld.syn
 
 }  // namespace tc
 
-// The pairs of planes whose products are summed, the smallest first.
+// The pairs of planes of fp32 operands whose products are summed, the smallest first. Of a bf16 product A may have two planes,
+// of which the second is what the first leaves of it.
+constexpr int kSix = 6;
 __device__ __forceinline__ int plane_a(int pass) { return (0x231130 >> 4 * (5 - pass)) & 15; }
 __device__ __forceinline__ int plane_b(int pass) { return (0x321310 >> 4 * (5 - pass)) & 15; }
 
@@ -357,13 +359,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             for (int32_t u = 0; alive && schedule.at(params.g, u, t); ++u) {
                 const TcArgs& g = params.g[kBoth ? t.which : 0];
                 const CUtensorMap *map_a = &maps.a[kBoth ? t.which : 0], *map_b = &maps.b[kBoth ? t.which : 0];
-                const int passes = g.planes == 1 ? 1 : 6;
+                const int passes = g.passes;
                 const int32_t ma = t.m0 + (int32_t)rank * 128, nb = t.n0 + (int32_t)rank * (g.width / 2);
                 const uint32_t bytes = kTcStageA + (g.b_mn ? (g.width + 127) / 128 * 8192 : g.width * kTcDepth);
                 for (int32_t from = 0; from < t.count && alive; from += g.run) {
                     const int32_t end = t.count - from < g.run ? t.count : from + g.run;
                     for (int pass = 0; pass < passes && alive; ++pass) {
-                        const int pa = passes == 1 ? 0 : plane_a(pass), pb = passes == 1 ? 0 : plane_b(pass);
+                        const int pa = passes == kSix ? plane_a(pass) : passes - 1 - pass, pb = passes == kSix ? plane_b(pass) : 0;
                         for (int32_t k = from; k < end; ++k) {
                             alive = __all_sync(0xffffffffu, tc::wait(&empty[at_stage], turn ^ 1, dead));
                             if (!alive) break;
@@ -405,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             bool alive = true;
             for (int32_t u = 0; alive && schedule.at(params.g, u, t); ++u) {
                 const TcArgs& g = params.g[kBoth ? t.which : 0];
-                const int passes = g.planes == 1 ? 1 : 6;
+                const int passes = g.passes;
                 const uint32_t kind = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(g.a_mn != 0) << 15 | (uint32_t)(g.b_mn != 0) << 16 |
                                       (uint32_t)(g.width / 8) << 17 | (uint32_t)(kTcM / 16) << 24;
                 // 16 terms further: 32 bytes along a line, or 16 lines
@@ -654,6 +656,7 @@ struct TcProduct {
     bool a_mn, b_mn;
     int64_t m, n, k;
     const int32_t *m_count, *k_count;
+    int parts = 1;  // bf16: of A
 };
 
 template <typename T, typename Epi>
@@ -665,7 +668,8 @@ cudaError_t set_tc(TcMaps& maps, TcParams<Epi>& p, int i, const TcProduct& x, in
     g.k = x.k;
     g.m_count = x.m_count;
     g.k_count = x.k_count;
-    g.planes = sizeof(T) == 4 ? kPlanes : 1;
+    const int planes_a = sizeof(T) == 4 ? kPlanes : x.parts, planes_b = sizeof(T) == 4 ? kPlanes : 1;
+    g.passes = sizeof(T) == 4 ? kSix : x.parts;
     g.splits = splits;
     g.width = width;
     g.a_mn = x.a_mn;
@@ -674,8 +678,8 @@ cudaError_t set_tc(TcMaps& maps, TcParams<Epi>& p, int i, const TcProduct& x, in
     g.run = sizeof(T) == 4 ? 4 : Epi::kExact ? 8 : 1 << 30;
     p.g[i] = g;
     p.epi[i] = epi;
-    const cudaError_t e = tensor_map(&maps.a[i], x.a, g.planes, x.a_mn ? kTcDepth : 128);
-    return e == cudaSuccess ? tensor_map(&maps.b[i], x.b, g.planes, x.b_mn ? kTcDepth : width / 2) : e;
+    const cudaError_t e = tensor_map(&maps.a[i], x.a, planes_a, x.a_mn ? kTcDepth : 128);
+    return e == cudaSuccess ? tensor_map(&maps.b[i], x.b, planes_b, x.b_mn ? kTcDepth : width / 2) : e;
 }
 
 // ---------------------------------------------------------------- which way
@@ -694,7 +698,8 @@ struct TcWay {
 
 struct TcSize {
     int64_t m, n, k;
-    bool fp32, may_split;
+    int passes;
+    bool may_split;
     int64_t tiles(int width) const { return (m + kTcM - 1) / kTcM * ((n + width - 1) / width); }
     int64_t blocks(int s) const { return ((k + kTcDepth - 1) / kTcDepth + s - 1) / s; }
     bool may(TcWay w) const { return w.splits == 1 || (may_split && tiles(w.width) * w.splits <= kMostParts && blocks(1) >= 4 * w.splits); }
@@ -702,7 +707,7 @@ struct TcSize {
     double unit(TcWay w) const
     {
         const double share = w.width / 256.0, least = 0.45 + 0.38 * share;
-        return blocks(w.splits) * kTcBlock * (fp32 ? 6 : 1) * (share > least ? share : least);
+        return blocks(w.splits) * kTcBlock * passes * (share > least ? share : least);
     }
     double cost(TcWay w) const
     {
@@ -727,7 +732,7 @@ inline int64_t parts_elements(int64_t m, int64_t n)  // of a workspace
     return all < whole ? all : whole;
 }
 
-template <typename T, typename Epi> TcSize size_of(const TcProduct& x) { return {x.m, x.n, x.k, sizeof(T) == 4, Epi::kPieces}; }
+template <typename T, typename Epi> TcSize size_of(const TcProduct& x) { return {x.m, x.n, x.k, sizeof(T) == 4 ? kSix : x.parts, Epi::kPieces}; }
 
 // The epilogue of a product whose terms are split: its parts' sums.
 template <typename T> EpiStore<T> to_parts(EpiStore<T> epi, float* parts, const TcProduct& x)

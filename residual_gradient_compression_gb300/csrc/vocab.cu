@@ -87,7 +87,8 @@ VocabParts vocab_parts(Carve& c, int64_t rows, int64_t dim, int64_t vocab, int b
     if (backward) {
         p.piece = piece_of(rows, vocab);
         p.dz_stride = pitch_of(p.piece);
-        p.dz = c.take<bf16>(piece_elements(rows, vocab) * (bytes == 4 ? kPlanes : 1));
+        const int64_t few = 2 * piece_elements(rows < kFewRows ? rows : kFewRows, vocab), all = piece_elements(rows, vocab);
+        p.dz = c.take<bf16>(bytes == 4 ? kPlanes * all : few > all ? few : all);
         p.acc = c.take<float>(rows * round_up(dim, 4));
         p.parts = c.take<float>(parts_elements(rows, dim) + parts_elements(vocab, dim));
     } else {
@@ -406,6 +407,7 @@ template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, c
     grad.dloss_stride = a.dloss_stride;
     grad.scale = 1.0f / a.temperature;
     grad.temperature = a.temperature;
+    grad.two = sizeof(T) == 2 && a.rows <= kFewRows;
     for (int64_t at = 0; at < a.vocab && e == cudaSuccess; at += p.piece) {
         const int64_t n = a.vocab - at < p.piece ? a.vocab - at : p.piece;
         const Matrix here = {w.p + at * w.stride, n, a.dim, w.stride, w.plane}, dz = {p.dz, p.padded, n, p.dz_stride, grad.plane};
@@ -428,8 +430,8 @@ template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, c
         to_dw.first = to_dw.last = true;
         to_dw.whole = whole_rows(a.dw, a.dw_stride, a.vocab, sizeof(T));
         to_dx.n = to_dw.n = (int32_t)a.dim;
-        const TcProduct dx = {dz, here, false, true, a.rows, a.dim, n, p.count, nullptr};
-        const TcProduct dw = {dz, x, true, true, n, a.dim, a.rows, nullptr, p.count};
+        const TcProduct dx = {dz, here, false, true, a.rows, a.dim, n, p.count, nullptr, grad.two ? 2 : 1};
+        const TcProduct dw = {dz, x, true, true, n, a.dim, a.rows, nullptr, p.count, grad.two ? 2 : 1};
         if (a.dx && a.dw) e = product_tc_both<T>(dx, to_dx, dw, to_dw, p.parts, stream);
         else e = a.dx ? product_tc<T>(dx, p.parts, to_dx, stream) : product_tc<T>(dw, p.parts, to_dw, stream);
     }

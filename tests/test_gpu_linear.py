@@ -176,6 +176,35 @@ def test_values_that_are_not_finite(rows, dt):
         assert float(y[0, 3]) == 0.0
 
 
+@pytest.mark.parametrize("rows,din,dout", [(1, 1, 1), (1, 700, 3), (2, 40, 900), (20, 520, 1000), (32, 1000, 2000), (33, 1000, 2000)])
+def test_gradients_of_few_bf16_rows_are_not_rounded_twice(rows, din, dout):
+    """dz of up to 32 rows is taken in two parts, 2^-15 of it apart from its value, and slopes are off by 128 * 2^-24, so that
+    little but the results' own rounding is left; of more rows it is rounded to 2^-8."""
+    x, w, b, _, dy = _inputs(rows, din, dout, BF16, 14)
+    layer = Layer(din, dout, BF16, "silu")
+    _, pre = layer.forward(x, w, b)
+    dx, dw, _ = layer.backward(dy, x, w, pre)
+    dz = dy.double() * act(pre.double(), "silu")[1]
+    e = dz.abs() * (2.0 ** -15 if rows <= 32 else 2.0 ** -8) + dy.double().abs() * 2.0 ** -16
+    for got, ref, size in ((dx, dz @ w.double(), e @ w.double().abs()), (dw, dz.T @ x.double(), e.T @ x.double().abs())):
+        assert_within(got, ref, ref.abs() * 2.0 ** -8 + size * 1.01, "gradient")
+
+
+@pytest.mark.parametrize("rows", [3, 32, 40])
+def test_infinite_factors_of_a_gradient(rows):
+    """bf16, with an activation: an infinite weight or input makes what it meets infinite with the gradient's sign."""
+    for din, dout in ((40, 60), (520, 2000)):
+        x, w, _, _, dy = _inputs(rows, din, dout, BF16, 15)
+        x[1, 2], w[3, 4] = float("inf"), float("-inf")
+        dy[:, 3], dy[1, 5] = 1.0, -2.0
+        pre = torch.full_like(dy, 30.0)  # slopes of 1, exactly
+        dx, dw, _ = Layer(din, dout, BF16, "silu").backward(dy, x, w, pre)
+        ref = dy.double() @ w.double(), dy.double().T @ x.double()
+        for got, want in zip((dx, dw), ref):
+            assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(torch.isinf(got), torch.isinf(want))
+            assert torch.equal(got[torch.isinf(got)].sign().double(), want[torch.isinf(want)].sign())
+
+
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 def test_one_row_for_all(dt):
     """A stride of 0 between rows, of x, the weights, the residual and dy."""
