@@ -284,6 +284,19 @@ __device__ __forceinline__ void split_parts(float x, bf16 (&part)[kPlanes])
     part[3] = part[0];
 }
 
+// The same by cutting bits off instead of rounding, in fewer instructions, for an epilogue (a training step of cross entropy
+// 2003 x 501 x 10007 396 and 378 us); each part the upper half of a word. The other operand's parts are rounded, so what their products
+// leave out has no sign in common.
+__device__ __forceinline__ void cut_parts(float x, uint32_t (&part)[kPlanes])
+{
+    const bool finite = fabsf(x) <= 3.402823466e38f;
+    part[0] = x != x ? 0x7fff0000u : __float_as_uint(x) & 0xffff0000u;
+    const float rest = finite ? x - __uint_as_float(part[0]) : 0.0f;
+    part[1] = __float_as_uint(rest) & 0xffff0000u;
+    part[2] = __float_as_uint(rest - __uint_as_float(part[1])) & 0xffff0000u;
+    part[3] = finite ? part[0] : 0u;
+}
+
 // A value in two parts of one sign, so that an infinite factor meets no 0 or other sign in the second: what bf16 has of its
 // bits, and the rest, or where there is none 2^-24 of it.
 __device__ __forceinline__ float first_of(float v) { return __bfloat162float(__float2bfloat16_rz(v)); }
@@ -698,16 +711,25 @@ template <typename T> struct EpiGradient {
                 for (int j = 0; j < 4; ++j) part.v[j] = rest_of(v.v[j]);
                 put(to + plane, part, left);
             } else {
-                Cols<4> part[kPlanes];
+                uint32_t part[kPlanes][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    bf16 each[kPlanes];
-                    split_parts(v.v[j], each);
+                    uint32_t each[kPlanes];
+                    cut_parts(v.v[j], each);
 #pragma unroll
-                    for (int p = 0; p < kPlanes; ++p) part[p].v[j] = __bfloat162float(each[p]);
+                    for (int p = 0; p < kPlanes; ++p) part[p][j] = each[p];
                 }
 #pragma unroll
-                for (int p = 0; p < kPlanes; ++p) put(to + p * plane, part[p], left);
+                for (int p = 0; p < kPlanes; ++p) {
+                    uint16_t* at = reinterpret_cast<uint16_t*>(to + p * plane);
+                    if (left >= 4) {
+                        *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(part[p][0], part[p][1], 0x7632), __byte_perm(part[p][2], part[p][3], 0x7632));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < left) at[j] = (uint16_t)(part[p][j] >> 16);
+                    }
+                }
             }
         }
     }

@@ -85,3 +85,63 @@ def test_the_error_of_fp32_sums_does_not_grow_with_their_length():
     ac.adacomp_linear_forward(h, x, w, y, workspace(ac.adacomp_linear_forward_ws_bytes(h, 300)))
     ref = x.double() @ w.double().T
     assert ((y.double() - ref).abs() / ref).max() < 16 * 2.0 ** -23 + 32 * 2.0 ** -24 + 2.0 ** -22
+
+
+@DTYPES
+def test_offsets_past_32_bits(dt):
+    """Rows so far apart that the last ones begin past 2^32 elements: the bits of rows that are not."""
+    rows, din, dout, far = 3000, 72, 136, 1_500_008
+    g = torch.Generator(device="cuda").manual_seed(2)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dt)  # noqa: E731
+    code = ac.BF16 if dt == BF16 else ac.F32
+    x, w, dy = n(rows, din), n(dout, din), n(rows, dout)
+    wide = torch.empty(rows * far, dtype=dt, device="cuda").view(rows, far)
+    spread = {}
+    at = 0
+    for name, cols, value in (("x", din, x), ("y", dout, None), ("pre", dout, None), ("dy", dout, dy), ("dx", din, None)):
+        spread[name] = wide[:, at:at + cols]
+        at += (cols + 7) // 8 * 8
+        if value is not None:
+            spread[name].copy_(value)
+    h = ac.adacomp_linear_init(din, dout, code, ac.ACT_SILU)
+    ws = workspace(max(ac.adacomp_linear_forward_ws_bytes(h, rows), ac.adacomp_linear_backward_ws_bytes(h, rows)))
+    near = {"y": torch.empty_like(dy), "pre": torch.empty_like(dy), "dx": torch.empty_like(x)}
+    grads = []
+    for t in (dict(near, x=x, dy=dy), spread):
+        dw = torch.empty_like(w)
+        ac.adacomp_linear_forward(h, t["x"], w, t["y"], ws, pre=t["pre"])
+        ac.adacomp_linear_backward(h, t["dy"], t["x"], w, ws, pre=t["pre"], dx=t["dx"], dw=dw)
+        grads.append(dw)
+    assert torch.equal(*grads)
+    for name in near:
+        assert torch.equal(near[name], spread[name]), name
+    v = ac.adacomp_vocab_init(din, dout, code)
+    target = torch.randint(0, dout, (rows,), generator=g, device="cuda")
+    ws = workspace(max(ac.adacomp_vocab_loss_forward_ws_bytes(v, rows), ac.adacomp_vocab_loss_backward_ws_bytes(v, rows)))
+    results = []
+    for hidden, dx in ((x, torch.empty_like(x)), (spread["x"], spread["dx"])):
+        loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        ac.adacomp_vocab_loss_forward(v, hidden, w, target, loss, lse, ws)
+        ac.adacomp_vocab_loss_backward(v, hidden, w, target, lse, loss, ws, dx=dx)
+        results.append((loss, lse, dx))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_many_short_rows():
+    """So many rows that counting those with a loss takes hundreds of CTAs, and that grids of rows go round."""
+    rows, dim, vocab = 600_000, 16, 96
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, w = (torch.randn(*s, generator=g, device="cuda").bfloat16() for s in ((rows, dim), (vocab, dim)))
+    target = torch.randint(-vocab, vocab, (rows,), generator=g, device="cuda").to(torch.int32)
+    v = ac.adacomp_vocab_init(dim, vocab, ac.BF16)
+    ws = workspace(max(ac.adacomp_vocab_loss_forward_ws_bytes(v, rows), ac.adacomp_vocab_loss_backward_ws_bytes(v, rows))).fill_(255)
+    loss, lse, dx = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.empty_like(x)
+    one = torch.ones(1, device="cuda")
+    ac.adacomp_vocab_loss_forward(v, x, w, target, loss, lse, ws)
+    ac.adacomp_vocab_loss_backward(v, x, w, target, lse, one, ws, dx=dx)
+    for part in (slice(0, 20_000), slice(290_000, 310_000), slice(580_000, 600_000)):
+        ref, bound = loss_ref(x[part], w, target[part].long()[:, None])
+        assert_within(loss[part], ref[0], bound[0], "loss")
+        ref, bound = backward_ref(x[part], w, target[part].long()[:, None], lse[part], one.expand(20_000))
+        assert_within(dx[part], ref[0], bound[0], "dx")
