@@ -50,9 +50,9 @@ LinearParts linear_parts(Carve& c, int64_t rows, int64_t in, int64_t out, int by
     return p;
 }
 
-// Which products are for the kernel of small matrices, by what its whole tiles of 32 x 32 and 128 terms compute. us with it
-// and without: fp32 256 x 512 x 512 12 and 17, 512 x 512 x 512 17 and 17, 2048 x 2048 of one term 66 and 14; bf16
-// 256 x 256 x 256 7 and 10, 128 x 512 x 512 12 and 9.
+// Which products are for the kernel of small matrices, by what its whole tiles of 32 x 32 and 128 terms compute.
+// us with it and without: fp32 256 x 512 x 512 12 and 17, 512 x 512 x 512 17 and 17, 2048 x 2048 of one term 66
+// and 14; bf16 256 x 256 x 256 7 and 10, 128 x 512 x 512 12 and 9.
 template <typename T> bool is_small(int64_t m, int64_t n, int64_t k)
 {
     constexpr int64_t most = (int64_t)1 << (sizeof(T) == 4 ? 27 : 24);
@@ -107,7 +107,7 @@ template <typename T> struct Eight {
 // second kernel, in a fixed order.
 template <typename T, int kAct, int kDzRows> __device__ __forceinline__ void dz_rows(const DzArgs& a, int32_t c, float (&sum)[8])
 {
-    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
+    constexpr int kAhead = sizeof(T) == 2 ? 3 : 2;
     const T *dy = static_cast<const T*>(a.dy) + c, *pre = static_cast<const T*>(a.pre) + c;
     const int64_t left = a.n - c, step = (int64_t)a.slices * kDzRows;
     for (int64_t r0 = blockIdx.y * kDzRows + threadIdx.y; r0 < a.rows; r0 += kAhead * step) {
@@ -122,12 +122,17 @@ template <typename T, int kAct, int kDzRows> __device__ __forceinline__ void dz_
         for (int i = 0; i < kAhead; ++i) {
             const int64_t r = r0 + i * step;
             if (r >= a.rows) break;
-            float d[8];
+            float d[8], s[8];
+            if constexpr (kAct != ADACOMP_ACT_NONE) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] = z[i].get(j);
+                slope_all<T, kAct>(s);
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 d[j] = v[i].get(j);
                 // one rounding whatever is asked for: db is the sum of what dz would be rounded from
-                if constexpr (kAct != ADACOMP_ACT_NONE) d[j] = __fmul_rn(d[j], slope<T, kAct>(z[i].get(j)));
+                if constexpr (kAct != ADACOMP_ACT_NONE) d[j] = __fmul_rn(d[j], s[j]);
                 sum[j] += d[j];
             }
             if (kAct == ADACOMP_ACT_NONE || !a.dz) continue;

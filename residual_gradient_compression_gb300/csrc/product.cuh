@@ -1,16 +1,17 @@
-// Shared by the linear layers and the losses over a vocabulary: what is done with a product's
-// sums (the epilogues).
+// Shared by the linear layers and the losses over a vocabulary: what is done with a product's sums (the
+// epilogues).
 //
-// A product is C(m, n) = sum over k of A(m, k) B(n, k). A warp of the kernel that forms it has 32 rows' sums in registers,
-// 128 columns of a row per thread, and hands them to an epilogue in two steps: rows(), a thread its row (from
-// column c up to `last`, the strip-th of the row), with what begin() loaded before the sums were there; and chunk(), the warp 32 columns at a time through shared memory, so that
-// what it reads and writes in global memory are whole pieces of rows (a thread that writes its own row takes 32 cache
-// lines at a time: a linear layer's forward product of 8192 x 2048 x 16384 bf16 took 369 us so, and 313 without its
-// stores). kExact: the results are held in fp32, so the sums are formed in short runs.
-// kPieces: a thread may also hand over columns on their own, piece(). kFetches: there may be a matrix that
-// the chunks are added to: begin() brings it into L2, and fetch() loads a chunk while the one before is worked on (a chunk's
-// loads in its turn: a layer of 16384 x 2048 x 8192 bf16 with a residual 608 us, and 414 so). kPatches: patch() changes single columns of a chunk in
-// shared memory. kParts: part() takes the sums of a part of the terms.
+// A product is C(m, n) = sum over k of A(m, k) B(n, k). A warp of the kernel that forms it has 32 rows' sums in
+// registers, 128 columns of a row per thread, and hands them to an epilogue in two steps: rows(), a thread its
+// row (from column c up to `last`, the strip-th of the row), with what begin() loaded before the sums were
+// there; and chunk(), the warp 32 columns at a time through shared memory, so that what it reads and writes in
+// global memory are whole pieces of rows (a thread that writes its own row takes 32 cache lines at a time: a
+// linear layer's forward product of 8192 x 2048 x 16384 bf16 took 369 us so, and 313 without its stores).
+// kExact: the results are held in fp32, so the sums are formed in short runs. kPieces: a thread may also hand
+// over columns on their own, piece(). kFetches: there may be a matrix that the chunks are added to: begin()
+// brings it into L2, and fetch() loads a chunk while the one before is worked on (a chunk's loads in its turn: a
+// layer of 16384 x 2048 x 8192 bf16 with a residual 608 us, and 414 so). kPatches: patch() changes single
+// columns of a chunk in shared memory. kParts: part() takes the sums of a part of the terms.
 #pragma once
 
 #include "train_common.cuh"
@@ -168,8 +169,8 @@ __device__ __forceinline__ float& row_value(const Stage& s, int col)
     return reinterpret_cast<float*>(&s.at(threadIdx.x & 31, col / 4))[col & 3];
 }
 
-// How a warp takes a chunk: in turns of four rows, of which a lane has four columns, or, where rows do not begin at such
-// places, of one row, of which it has one.
+// How a warp takes a chunk: in turns of four rows, of which a lane has four columns, or, where rows do not begin
+// at such places, of one row, of which it has one.
 template <int N> struct Turns {
     static constexpr int kCount = N == 4 ? 8 : 32;
     int row, col;
@@ -269,9 +270,9 @@ inline int64_t pitch_of(int64_t cols) { return round_up(cols, cols < 64 ? 8 : 64
 // ---------------------------------------------------------------- fp32 numbers in parts
 constexpr int kPlanes = 4;  // of bf16 numbers for an fp32 matrix
 
-// x = top + mid + low exactly (but for what is below 2^-133), each a bf16 number. A value that is not finite has only a
-// top; the fourth plane is the top without such values, for the products with the other operand's lower parts
-// (infinity times a part that is 0 would be NaN).
+// x = top + mid + low exactly (but for what is below 2^-133), each a bf16 number. A value that is not finite has
+// only a top; the fourth plane is the top without such values, for the products with the other operand's lower
+// parts (infinity times a part that is 0 would be NaN).
 __device__ __forceinline__ void split_parts(float x, bf16 (&part)[kPlanes])
 {
     part[0] = __float2bfloat16_rn(x);
@@ -284,9 +285,9 @@ __device__ __forceinline__ void split_parts(float x, bf16 (&part)[kPlanes])
     part[3] = part[0];
 }
 
-// The same by cutting bits off instead of rounding, in fewer instructions, for an epilogue (a training step of cross entropy
-// 2003 x 501 x 10007 396 and 378 us); each part the upper half of a word. The other operand's parts are rounded, so what their products
-// leave out has no sign in common.
+// The same by cutting bits off instead of rounding, in fewer instructions, for an epilogue (a training step of
+// cross entropy 2003 x 501 x 10007 396 and 378 us); each part the upper half of a word. The other operand's
+// parts are rounded, so what their products leave out has no sign in common.
 __device__ __forceinline__ void cut_parts(float x, uint32_t (&part)[kPlanes])
 {
     const bool finite = fabsf(x) <= 3.402823466e38f;
@@ -297,8 +298,8 @@ __device__ __forceinline__ void cut_parts(float x, uint32_t (&part)[kPlanes])
     part[3] = finite ? part[0] : 0u;
 }
 
-// A value in two parts of one sign, so that an infinite factor meets no 0 or other sign in the second: what bf16 has of its
-// bits, and the rest, or where there is none 2^-24 of it.
+// A value in two parts of one sign, so that an infinite factor meets no 0 or other sign in the second: what bf16
+// has of its bits, and the rest, or where there is none 2^-24 of it.
 __device__ __forceinline__ float first_of(float v) { return __bfloat162float(__float2bfloat16_rz(v)); }
 __device__ __forceinline__ float rest_of(float v)
 {
@@ -307,9 +308,10 @@ __device__ __forceinline__ float rest_of(float v)
     return rest == 0.0f ? v * 5.9604645e-8f : rest;
 }
 
-// The gradient of bf16 products is an operand of two more. It is rounded to bf16 for them, by 2^-9 of each value at random, which
-// is less than their results' own rounding where sums of many rows or columns are formed; of up to kFewRows rows, whose few
-// values may share one rounding, it is taken in two parts (the products' time is that of reading and writing the weights).
+// The gradient of bf16 products is an operand of two more. It is rounded to bf16 for them, by 2^-9 of each value
+// at random, which is less than their results' own rounding where sums of many rows or columns are formed; of up
+// to kFewRows rows, whose few values may share one rounding, it is taken in two parts (the products' time is
+// that of reading and writing the weights).
 constexpr int64_t kFewRows = 32;
 
 // A row's columns as operands of another product: bf16 numbers, two planes of them, or, of an fp32 matrix, four.
@@ -345,16 +347,25 @@ template <typename T, int N> __device__ __forceinline__ void put_parts(bf16* p, 
 }
 
 // ---------------------------------------------------------------- activations
-// Of bf16 layers by quick functions, whose error is some 2^-22 of z, far below the results' rounding: the epilogue of a
-// product of 2048 terms has no time for more. 1 + erf(x), and exp(-x^2), by the rational approximation of Abramowitz and
-// Stegun (7.1.26; error 1.5e-7).
-__device__ __forceinline__ float quick_erfc_minus(float x, float& bell)
+// Of bf16 layers by quick functions, whose error is some 2^-22 of z, far below the results' rounding: the
+// epilogue of a product of 2048 terms has no time for more. 1 + erf(x), and exp(-x^2), of two values at a time,
+// by the rational approximation of Abramowitz and Stegun (7.1.26; error 1.5e-7).
+__device__ __forceinline__ Pair quick_one_plus_erf(Pair x, Pair& bell)
 {
-    const float a = fabsf(x), t = __fdividef(1.0f, fmaf(0.3275911f, a, 1.0f));
-    bell = __expf(-x * x);
-    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
-    const float tail = p * bell;  // erfc(|x|)
-    return x < 0.0f ? tail : 2.0f - tail;
+    float x0, x1, e0, e1, d0, d1, r0, r1;
+    split(x, x0, x1);
+    split(x * x * pair(-1.44269504f), e0, e1);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(e0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(e1));
+    bell = pair(r0, r1);
+    split(fma2(pair(fabsf(x0), fabsf(x1)), pair(0.3275911f), pair(1.0f)), d0, d1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
+    const Pair t = pair(r0, r1);
+    const Pair p = fma2(t, fma2(t, fma2(t, fma2(t, pair(1.061405429f), pair(-1.453152027f)), pair(1.421413741f)), pair(-0.284496736f)),
+                        pair(0.254829592f));
+    split(fma2(t * p, bell * pair(-1.0f), pair(1.0f)), r0, r1);  // erf(|x|)
+    return pair(copysignf(r0, x0), copysignf(r1, x1)) + pair(1.0f);
 }
 
 __device__ __forceinline__ float quick_sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
@@ -365,8 +376,6 @@ template <typename T, int kKind> __device__ __forceinline__ float activate(float
     if constexpr (kKind == ADACOMP_ACT_RELU) {
         return z < 0.0f ? 0.0f : z;
     } else if constexpr (kKind == ADACOMP_ACT_GELU) {
-        float bell;
-        if (kQuick) return 0.5f * z * quick_erfc_minus(z * 0.70710678f, bell);
         return 0.5f * z * (1.0f + erff(z * 0.70710678f));
     } else if constexpr (kKind == ADACOMP_ACT_GELU_TANH) {  // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
         const float u = 0.79788456f * (z + 0.044715f * z * z * z);
@@ -386,11 +395,6 @@ template <typename T, int kKind> __device__ __forceinline__ float slope(float z)
     if constexpr (kKind == ADACOMP_ACT_RELU) {
         return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;  // NaN stays NaN
     } else if constexpr (kKind == ADACOMP_ACT_GELU) {
-        if (kQuick) {
-            float bell;
-            const float c = 0.5f * quick_erfc_minus(z * 0.70710678f, bell);
-            return fmaf(z * 0.39894228f, bell, c);
-        }
         return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * expf(-0.5f * z * z) * 0.39894228f;
     } else if constexpr (kKind == ADACOMP_ACT_GELU_TANH) {
         const float u = 0.79788456f * (z + 0.044715f * z * z * z);
@@ -404,11 +408,47 @@ template <typename T, int kKind> __device__ __forceinline__ float slope(float z)
     }
 }
 
+// N values at a time, an even number of them or one.
+template <typename T, int kKind, int N> __device__ __forceinline__ void activate_all(float (&v)[N])
+{
+    if constexpr (sizeof(T) == 2 && kKind == ADACOMP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const Pair z = pair(v[i], v[N == 1 ? i : i + 1]);
+            Pair bell;
+            float a, b;
+            split(z * pair(0.5f) * quick_one_plus_erf(z * pair(0.70710678f), bell), a, b);
+            v[i] = a;
+            if (N > 1) v[N == 1 ? i : i + 1] = b;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = activate<T, kKind>(v[i]);
+    }
+}
+
+template <typename T, int kKind, int N> __device__ __forceinline__ void slope_all(float (&v)[N])
+{
+    if constexpr (sizeof(T) == 2 && kKind == ADACOMP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const Pair z = pair(v[i], v[i + 1]);
+            Pair bell;
+            const Pair c = quick_one_plus_erf(z * pair(0.70710678f), bell) * pair(0.5f);
+            split(fma2(z * pair(0.39894228f), bell, c), v[i], v[i + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = slope<T, kKind>(v[i]);
+    }
+}
+
 // ---------------------------------------------------------------- epilogues
 // y = act(sum + bias) + residual, and the value before the activation.
 template <typename T> struct EpiLinear {
-    // fp32: one copy of the instructions, which a CTA with one or two tiles waits to be loaded (a training step of 3001 x 1001 x 777
-    // 187 and 165 us); bf16: four, whose stores overlap (gelu of 16384 x 2048 x 8192 with both outputs 432 and 378)
+    // fp32: one copy of the instructions, which a CTA with one or two tiles waits to be loaded (a training step
+    // of 3001 x 1001 x 777 187 and 165 us); bf16: four, whose stores overlap (gelu of 16384 x 2048 x 8192 with
+    // both outputs 432 and 378)
     static constexpr int kUnroll = sizeof(T) == 4 ? 1 : 4;
     static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kFetches = true, kPatches = false, kParts = false;
     T *y, *pre;
@@ -460,8 +500,7 @@ template <typename T> struct EpiLinear {
 
     template <int kKind, int N> static __device__ __forceinline__ Cols<N> each(Cols<N> c)
     {
-#pragma unroll
-        for (int i = 0; i < N; ++i) c.v[i] = activate<T, kKind>(c.v[i]);
+        activate_all<T, kKind>(c.v);
         return c;
     }
 
@@ -494,9 +533,9 @@ template <typename T> struct EpiLinear {
     }
 };
 
-// The sums themselves, in rows that `map` may move; with acc, added up over several products in
-// fp32 (first: nothing to add to yet) and rounded by the last one only. Of a product whose terms are split, the parts'
-// sums go to acc, split_stride apart (and neither first nor last is asked).
+// The sums themselves, in rows that `map` may move; with acc, added up over several products in fp32 (first:
+// nothing to add to yet) and rounded by the last one only. Of a product whose terms are split, the parts' sums
+// go to acc, split_stride apart (and neither first nor last is asked).
 template <typename T> struct EpiStore {
     static constexpr int kUnroll = sizeof(T) == 4 ? 1 : 4;
     static constexpr bool kExact = sizeof(T) == 4, kChunks = true, kPieces = true, kFetches = true, kPatches = false, kParts = true;

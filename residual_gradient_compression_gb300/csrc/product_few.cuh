@@ -28,11 +28,11 @@ struct FewArgs {
     int32_t rows, n, k;
 };
 
-// y of up to kTokens rows: bound by memory, the weights. A CTA has 16 of their rows, its warps a part of the terms each;
-// a lane reads 16 bytes of two of them, and of a token's row, at a time, kAhead times before it computes. The terms of a
-// product (mma of 16 x 8 x 16, of which the tokens are the columns) may come in any order, so a lane's eight
-// consecutive ones are two pairs of two products. The tensor cores' own memory would add a round trip to each of these
-// short sums. The warps' sums meet in shared memory.
+// y of up to kTokens rows: bound by memory, the weights. A CTA has 16 of their rows, its warps a part of the
+// terms each; a lane reads 16 bytes of two of them, and of a token's row, at a time, kAhead times before it
+// computes. The terms of a product (mma of 16 x 8 x 16, of which the tokens are the columns) may come in any
+// order, so a lane's eight consecutive ones are two pairs of two products. The tensor cores' own memory would
+// add a round trip to each of these short sums. The warps' sums meet in shared memory.
 template <typename Epi, int kTokens, int kWarps, bool kWhole>
 __global__ void __launch_bounds__(kWarps * 32) few_bf16_kernel(const FewArgs g, const Epi epi)
 {
@@ -94,8 +94,9 @@ __global__ void __launch_bounds__(kWarps * 32) few_bf16_kernel(const FewArgs g, 
     put_piece(epi, r, c0 + c, v);
 }
 
-// The same of fp32 numbers: a warp has four rows of the weights, its lanes four terms each at a time. (8 x 2048 x 8192 32 us,
-// bound by the tokens' loads from L1, of which there are two for one of the weights'; two rows a warp 44.)
+// The same of fp32 numbers: a warp has four rows of the weights, its lanes four terms each at a time. (8 x 2048
+// x 8192 32 us, bound by the tokens' loads from L1, of which there are two for one of the weights'; two rows a
+// warp 44.)
 template <typename Epi, int kTokens, bool kWhole>
 __global__ void __launch_bounds__(256, 2) few_f32_kernel(const FewArgs g, const Epi epi)
 {
@@ -174,10 +175,10 @@ struct SmallArgs {
 
 constexpr int kSmallTile = 32, kSmallDepth = 128;
 
-// A CTA has a tile of 32 x 32, 128 terms at a time in shared memory, of which a warp has 16; a thread has 4 x 8 of the
-// tile's sums, fp32, in its warp's terms; the warps' sums meet in shared memory. A block of terms takes over a
-// microsecond, most of it waiting for loads, so where tiles are few the terms are split over the CTAs of a cluster, whose sums the
-// first one reads from the others' shared memory.
+// A CTA has a tile of 32 x 32, 128 terms at a time in shared memory, of which a warp has 16; a thread has 4 x 8
+// of the tile's sums, fp32, in its warp's terms; the warps' sums meet in shared memory. A block of terms takes
+// over a microsecond, most of it waiting for loads, so where tiles are few the terms are split over the CTAs of
+// a cluster, whose sums the first one reads from the others' shared memory.
 template <typename A, typename B, typename Epi> __global__ void __launch_bounds__(256) product_small_kernel(const SmallArgs g, const Epi epi)
 {
     constexpr int kPitch = kSmallTile + 4, kEach = kSmallTile * kSmallDepth / 256;

@@ -1,14 +1,15 @@
 // Products on the tensor cores: C(m, n) = sum over k of A(m, k) B(n, k), bf16 operands, fp32 sums.
 //
-// A pair of CTAs (a cluster of two SMs) has tiles of 256 rows and up to 256 columns; each loads its 128 rows of A and its half of
-// B's rows for 64 terms at a time, by TMA, into a ring of stages; one thread of the first CTA issues the
-// products (tcgen05.mma, cta_group::2) on both CTAs' shared memory; the sums lie in tensor memory, 128
-// rows in each CTA, in two buffers. Eight warps take them over into registers, 128 columns of a row per thread, and hand
-// them to the epilogue while the next tile is computed (sixteen with 64 columns each were slower, by the stores that
-// they have under way at once). Where results are held in fp32 they do so every
-// `run` blocks of terms and add the runs up: tensor memory's sums are truncated at every step, all in one
-// direction, which over 2048 terms is 8e-7 of a sum. Each operand lies by rows of terms ("k major") or by terms of rows ("mn major", the transposed
-// operands of the gradients): both are copied as they lie and told apart by the matrix descriptors.
+// A pair of CTAs (a cluster of two SMs) has tiles of 256 rows and up to 256 columns; each loads its 128 rows of
+// A and its half of B's rows for 64 terms at a time, by TMA, into a ring of stages; one thread of the first CTA
+// issues the products (tcgen05.mma, cta_group::2) on both CTAs' shared memory; the sums lie in tensor memory,
+// 128 rows in each CTA, in two buffers. Eight warps take them over into registers, 128 columns of a row per
+// thread, and hand them to the epilogue while the next tile is computed (sixteen with 64 columns each were
+// slower, by the stores that they have under way at once). Where results are held in fp32 they do so every `run`
+// blocks of terms and add the runs up: tensor memory's sums are truncated at every step, all in one direction,
+// which over 2048 terms is 8e-7 of a sum. Each operand lies by rows of terms ("k major") or by terms of rows
+// ("mn major", the transposed operands of the gradients): both are copied as they lie and told apart by the
+// matrix descriptors.
 //
 // fp32 operands are four planes of bf16 numbers (split_parts), and their product is the sum of six products of
 // planes, the smallest first.
@@ -60,8 +61,8 @@ struct PackArgs {
     bool whole;  // rows that can be read 16 bytes at a time
 };
 
-// A matrix of any layout by rows of contiguous elements as aligned rows of bf16 numbers (planes of them for fp32); with
-// `count`, zeros from there to a whole tile. A thread takes eight elements at a time.
+// A matrix of any layout by rows of contiguous elements as aligned rows of bf16 numbers (planes of them for
+// fp32); with `count`, zeros from there to a whole tile. A thread takes eight elements at a time.
 constexpr int kTcPack = 256;
 template <typename T> __global__ void __launch_bounds__(kTcPack) pack_kernel(const PackArgs a)
 {
@@ -208,8 +209,8 @@ __device__ __forceinline__ void read_wait() { asm volatile("tcgen05.wait::ld.syn
 
 }  // namespace tc
 
-// The pairs of planes of fp32 operands whose products are summed, the smallest first. Of a bf16 product A may have two planes,
-// of which the second is what the first leaves of it.
+// The pairs of planes of fp32 operands whose products are summed, the smallest first. Of a bf16 product A may
+// have two planes, of which the second is what the first leaves of it.
 constexpr int kSix = 6;
 __device__ __forceinline__ int plane_a(int pass) { return (0x231130 >> 4 * (5 - pass)) & 15; }
 __device__ __forceinline__ int plane_b(int pass) { return (0x321310 >> 4 * (5 - pass)) & 15; }
@@ -225,10 +226,10 @@ template <typename Epi> struct TcParams {
     Epi epi[2];
 };
 
-// What each pair of CTAs does when two products are computed at once: of the first one's units (tiles, or parts of
-// their sums) every pairs-th; then of the second one's so many that all pairs have about as much to do: those with
-// a unit more of the first (the first `more` pairs) `few` of them, the others `many`. Also on the host, which compares
-// ways to split the sums by it.
+// What each pair of CTAs does when two products are computed at once: of the first one's units (tiles, or parts
+// of their sums) every pairs-th; then of the second one's so many that all pairs have about as much to do: those
+// with a unit more of the first (the first `more` pairs) `few` of them, the others `many`. Also on the host,
+// which compares ways to split the sums by it.
 struct TcShares {
     int64_t more, each, few, many, blocks;  // blocks: what the busiest pair has to do
     __host__ __device__ TcShares(int64_t pairs, int64_t units_a, int64_t a, int64_t units_b, int64_t b)
@@ -528,8 +529,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 }
 
 // ---------------------------------------------------------------- host
-// The sums of the parts that the terms were split into, one after the other, handed to an epilogue. A thread has four of a
-// row's columns, or one.
+// The sums of the parts that the terms were split into, one after the other, handed to an epilogue. A thread has
+// four of a row's columns, or one.
 struct JoinPartsArgs {
     const float* part;  // [splits][m][stride]
     int64_t m, n, stride;
@@ -683,12 +684,13 @@ cudaError_t set_tc(TcMaps& maps, TcParams<Epi>& p, int i, const TcProduct& x, in
 }
 
 // ---------------------------------------------------------------- which way
-// How wide the tiles are, and into how many parts the terms are split (which a kernel of its own joins), so that the last
-// tiles leave few SMs idle. By estimate, us: a block of 64 terms and 256 columns takes a pair kTcBlock (six times that in
-// fp32), a narrower one more than its share, as the rows of A are loaded all the same (tiles of 32 blocks, bf16: 256 columns
-// 11.2, 224 9.7, 192 8.7, 160 7.8, 128 7.2, 96 6.7); the last tile's end 2 more, which nothing covers; the parts' sums are
-// written and read, and the joining kernel begins 3 later. With it, and with 256 columns and whole sums: the logits of 512
-// rows over 50304 tokens 75 and 84; a layer's gradients 3001 x 1001 x 777 fp32 102 and 111.
+// How wide the tiles are, and into how many parts the terms are split (which a kernel of its own joins), so that
+// the last tiles leave few SMs idle. By estimate, us: a block of 64 terms and 256 columns takes a pair kTcBlock
+// (six times that in fp32), a narrower one more than its share, as the rows of A are loaded all the same (tiles
+// of 32 blocks, bf16: 256 columns 11.2, 224 9.7, 192 8.7, 160 7.8, 128 7.2, 96 6.7); the last tile's end 2 more,
+// which nothing covers; the parts' sums are written and read, and the joining kernel begins 3 later. With it,
+// and with 256 columns and whole sums: the logits of 512 rows over 50304 tokens 75 and 84; a layer's gradients
+// 3001 x 1001 x 777 fp32 102 and 111.
 constexpr int64_t kPairs = 76, kMostParts = 2 * kPairs;  // tiles x splits are at most kMostParts, if split
 constexpr double kTcBlock = 0.32;
 
@@ -774,8 +776,8 @@ template <typename T, typename Epi> cudaError_t product_tc(const TcProduct& x, f
     return product_tc<T>(x, size_of<T, Epi>(x).best(), parts, epi, stream);
 }
 
-// Two products, neither of which needs the other, in one launch, so that the units of one fill the SMs that the other's last
-// ones leave idle. parts: room for both's parts_elements, the first's first.
+// Two products, neither of which needs the other, in one launch, so that the units of one fill the SMs that the
+// other's last ones leave idle. parts: room for both's parts_elements, the first's first.
 template <typename T, typename Epi>
 cudaError_t product_tc_both(const TcProduct& x, const Epi& epi_x, const TcProduct& y, const Epi& epi_y, float* parts, cudaStream_t stream)
 {

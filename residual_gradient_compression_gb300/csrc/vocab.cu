@@ -46,8 +46,8 @@ struct VocabParts {
     int64_t padded, dz_stride, piece;
 };
 
-// Columns of a piece: so many that the piece's gradient, of whole tiles of rows, has up to 2^27 elements, and no fewer than
-// 2048; and the most elements that one of up to `rows` rows has.
+// Columns of a piece: so many that the piece's gradient, of whole tiles of rows, has up to 2^27 elements, and no
+// fewer than 2048; and the most elements that one of up to `rows` rows has.
 constexpr int64_t kPieceElements = (int64_t)1 << 27, kLeastPiece = 2048;
 int64_t piece_of(int64_t rows, int64_t vocab)
 {
@@ -254,8 +254,8 @@ struct JoinArgs {
     float temperature;
 };
 
-// Rows' strips joined, and their losses; rows without a loss are 0. A CTA has kJoinRows rows: a warp's lanes have a strip of each,
-// or, where rows are few, four strips of eight rows; then a warp has a row, for its list.
+// Rows' strips joined, and their losses; rows without a loss are 0. A CTA has kJoinRows rows: a warp's lanes
+// have a strip of each, or, where rows are few, four strips of eight rows; then a warp has a row, for its list.
 template <int kJoinRows> __global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinArgs a)
 {
     constexpr int kParts = kJoinThreads / kJoinRows;  // of a row's strips
