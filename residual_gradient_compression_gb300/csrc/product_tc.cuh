@@ -64,15 +64,13 @@ struct PackArgs {
 // A matrix of any layout by rows of contiguous elements as aligned rows of bf16 numbers (planes of them for
 // fp32); with `count`, zeros from there to a whole tile. A thread takes eight elements at a time.
 constexpr int kTcPack = 256;
-template <typename T> __global__ void __launch_bounds__(kTcPack) pack_kernel(const PackArgs a)
+template <typename T>
+__device__ __forceinline__ void pack_rows(const PackArgs& a, const int32_t* map, int64_t count, int64_t rows)
 {
-    ptx::griddep_wait();
-    ptx::griddep_launch();
-    const int64_t count = a.count ? *a.count : a.rows, rows = a.count ? (count + kRows - 1) / kRows * kRows : count;
     const int64_t each = (a.cols + 7) / 8, all = rows * each;
     for (int64_t i = (int64_t)blockIdx.x * kTcPack + threadIdx.x; i < all; i += (int64_t)gridDim.x * kTcPack) {
         const int64_t r = i / each, c = (i - r * each) * 8;
-        const T* from = static_cast<const T*>(a.from) + (r < count ? (a.map ? (int64_t)a.map[r] : r) * a.from_stride : 0) + c;
+        const T* from = static_cast<const T*>(a.from) + (r < count ? (map ? (int64_t)map[r] : r) * a.from_stride : 0) + c;
         float x[8];
         get_chunk(from, x, r < count ? a.cols - c : 0, a.whole);
         __align__(16) bf16 v[sizeof(T) == 4 ? kPlanes : 1][8];
@@ -92,6 +90,14 @@ template <typename T> __global__ void __launch_bounds__(kTcPack) pack_kernel(con
         for (int p = 0; p < (sizeof(T) == 4 ? kPlanes : 1); ++p)
             *reinterpret_cast<uint4*>(to + p * a.plane) = *reinterpret_cast<const uint4*>(v[p]);
     }
+}
+
+template <typename T> __global__ void __launch_bounds__(kTcPack) pack_kernel(const PackArgs a)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch();
+    const int64_t count = a.count ? *a.count : a.rows;
+    pack_rows<T>(a, a.map, count, a.count ? (count + kRows - 1) / kRows * kRows : count);
 }
 
 // ---------------------------------------------------------------- instructions

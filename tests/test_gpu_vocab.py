@@ -156,6 +156,21 @@ def test_rows_without_a_loss_may_hold_anything(dt):
 
 
 @DTYPES
+@pytest.mark.parametrize("rows", [1023, 1024, 1025, 2049])
+def test_rows_with_a_loss_around_the_sizes_that_one_block_lists(rows, dt):
+    """Few of them, none of the first, the last one among them; all of them; and those of lists."""
+    x, w, target, dloss, g = _inputs(rows, 24, 300, dt, 21)
+    _check(x, w, target, dloss)
+    some = torch.full_like(target, -1)
+    some[rows // 2 + 3::37] = target[rows // 2 + 3::37]
+    some[-1] = target[-1]
+    _check(x, w, some.to(torch.int32), dloss)
+    index, logit = _teacher(rows, 7, 300, g, True)
+    index[:rows // 3] = -1
+    _check(x, w, target, dloss, (index, logit))
+
+
+@DTYPES
 def test_no_row_has_a_loss(dt):
     x, w, target, dloss, _ = _inputs(150, 40, 300, dt, 5)
     head = Head(40, 300, dt)
