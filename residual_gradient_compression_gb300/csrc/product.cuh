@@ -347,25 +347,29 @@ template <typename T, int N> __device__ __forceinline__ void put_parts(bf16* p, 
 }
 
 // ---------------------------------------------------------------- activations
-// Of bf16 layers by quick functions, whose error is some 2^-22 of z, far below the results' rounding: the
-// epilogue of a product of 2048 terms has no time for more. 1 + erf(x), and exp(-x^2), of two values at a time,
-// by the rational approximation of Abramowitz and Stegun (7.1.26; error 1.5e-7).
-__device__ __forceinline__ Pair quick_one_plus_erf(Pair x, Pair& bell)
+// None of them is formed as a difference that cancels: far below 0 each is right relative to itself. Of bf16 layers by
+// quick functions, as the epilogue of a product of 2048 terms has no time for more. 1 + erf(x) of x = z / sqrt 2, and exp(-x^2), of
+// two values at a time: erfc(|x|) = exp(-x^2) t p(t) with t = 1 / (1 + 0.411 |x|), whose coefficients are fitted here
+// (linear program over 0 <= x <= 9.4: 1.1e-7 at most, and 7.3e-5 of erfc where that is less). With the exponential's
+// argument it is off by 3.5e-7 or 1.2e-4 of erfc, whichever is less: far below what bf16 results are rounded to.
+__device__ __forceinline__ Pair quick_one_plus_erf(Pair z, Pair& bell)
 {
-    float x0, x1, e0, e1, d0, d1, r0, r1;
-    split(x, x0, x1);
-    split(x * x * pair(-1.44269504f), e0, e1);
+    float z0, z1, e0, e1, d0, d1, r0, r1;
+    split(z, z0, z1);
+    split(z * z * pair(-0.72134752f), e0, e1);
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(e0));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(e1));
     bell = pair(r0, r1);
-    split(fma2(pair(fabsf(x0), fabsf(x1)), pair(0.3275911f), pair(1.0f)), d0, d1);
+    split(fma2(pair(fabsf(z0), fabsf(z1)), pair(0.29062089f), pair(1.0f)), d0, d1);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
     const Pair t = pair(r0, r1);
-    const Pair p = fma2(t, fma2(t, fma2(t, fma2(t, pair(1.061405429f), pair(-1.453152027f)), pair(1.421413741f)), pair(-0.284496736f)),
-                        pair(0.254829592f));
-    split(fma2(t * p, bell * pair(-1.0f), pair(1.0f)), r0, r1);  // erf(|x|)
-    return pair(copysignf(r0, x0), copysignf(r1, x1)) + pair(1.0f);
+    const Pair p = fma2(t, fma2(t, fma2(t, fma2(t, fma2(t, pair(-0.17731535f), pair(0.56442744f)), pair(-0.18067640f)), pair(0.35698659f)),
+                                pair(0.20235198f)), pair(0.23422568f));
+    const Pair tail = t * p * bell;  // erfc(|x|)
+    split(tail, e0, e1);
+    split(fma2(tail, pair(-1.0f), pair(2.0f)), r0, r1);
+    return pair(z0 < 0.0f ? e0 : r0, z1 < 0.0f ? e1 : r1);
 }
 
 __device__ __forceinline__ float quick_sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
@@ -376,11 +380,11 @@ template <typename T, int kKind> __device__ __forceinline__ float activate(float
     if constexpr (kKind == ADACOMP_ACT_RELU) {
         return z < 0.0f ? 0.0f : z;
     } else if constexpr (kKind == ADACOMP_ACT_GELU) {
-        return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+        return 0.5f * z * erfcf(-0.70710678f * z);
     } else if constexpr (kKind == ADACOMP_ACT_GELU_TANH) {  // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
         const float u = 0.79788456f * (z + 0.044715f * z * z * z);
         if (kQuick) return z * quick_sigmoid(2.0f * u);
-        return 0.5f * z * (1.0f + tanhf(u));
+        return z / (1.0f + expf(-2.0f * u));
     } else if constexpr (kKind == ADACOMP_ACT_SILU) {
         if (kQuick) return z * quick_sigmoid(z);
         return z / (1.0f + expf(-z));
@@ -395,11 +399,11 @@ template <typename T, int kKind> __device__ __forceinline__ float slope(float z)
     if constexpr (kKind == ADACOMP_ACT_RELU) {
         return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;  // NaN stays NaN
     } else if constexpr (kKind == ADACOMP_ACT_GELU) {
-        return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * expf(-0.5f * z * z) * 0.39894228f;
-    } else if constexpr (kKind == ADACOMP_ACT_GELU_TANH) {
+        return 0.5f * erfcf(-0.70710678f * z) + z * expf(-0.5f * z * z) * 0.39894228f;
+    } else if constexpr (kKind == ADACOMP_ACT_GELU_TANH) {  // s = (1 + tanh u) / 2: s + 2 z s (1 - s) du/dz
         const float u = 0.79788456f * (z + 0.044715f * z * z * z);
-        const float t = kQuick ? fmaf(2.0f, quick_sigmoid(2.0f * u), -1.0f) : tanhf(u);
-        return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456f * (1.0f + 0.134145f * z * z);
+        const float s = kQuick ? quick_sigmoid(2.0f * u) : 1.0f / (1.0f + expf(-2.0f * u));
+        return s * (1.0f + z * (1.0f - s) * 1.5957691f * (1.0f + 0.134145f * z * z));
     } else if constexpr (kKind == ADACOMP_ACT_SILU) {
         const float g = kQuick ? quick_sigmoid(z) : 1.0f / (1.0f + expf(-z));
         return g * (1.0f + z * (1.0f - g));
@@ -417,7 +421,7 @@ template <typename T, int kKind, int N> __device__ __forceinline__ void activate
             const Pair z = pair(v[i], v[N == 1 ? i : i + 1]);
             Pair bell;
             float a, b;
-            split(z * pair(0.5f) * quick_one_plus_erf(z * pair(0.70710678f), bell), a, b);
+            split(z * pair(0.5f) * quick_one_plus_erf(z, bell), a, b);
             v[i] = a;
             if (N > 1) v[N == 1 ? i : i + 1] = b;
         }
@@ -434,7 +438,7 @@ template <typename T, int kKind, int N> __device__ __forceinline__ void slope_al
         for (int i = 0; i < N; i += 2) {
             const Pair z = pair(v[i], v[i + 1]);
             Pair bell;
-            const Pair c = quick_one_plus_erf(z * pair(0.70710678f), bell) * pair(0.5f);
+            const Pair c = quick_one_plus_erf(z, bell) * pair(0.5f);
             split(fma2(z * pair(0.39894228f), bell, c), v[i], v[i + 1]);
         }
     } else {
