@@ -530,7 +530,8 @@ void adacomp_adamw_free(adacomp_adamw_t h);
  * bf16 products are exact and summed in fp32. fp32 numbers are, but in small products, split into three
  * bf16 numbers that add up to them (what is below 2^-126 may be lost), and of the nine products of
  * parts the six largest are summed, which leaves out less than 2^-22 of a product. Sums add the terms
- * in an order that depends on sizes and alignment alone, and round or truncate each partial sum.
+ * in an order that depends on sizes and alignment alone, not on which outputs are asked for (over a vocabulary the terms
+ * of dw are the rows that have a loss, so there it depends on which they are), and round or truncate each partial sum.
  *
  * The kernels wait for their own copies and products. Such a wait is bounded by 2 s; on expiry the call
  * still ends, and the results that it had not computed are NaN. Nothing traps.

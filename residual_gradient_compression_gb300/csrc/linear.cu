@@ -285,9 +285,7 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
     if (e != cudaSuccess) return e;
     const TcProduct dx = {dz, w, false, true, a.rows, a.in, a.out, nullptr, nullptr, two ? 2 : 1};
     const TcProduct dw = {dz, x, true, true, a.out, a.in, a.rows, nullptr, nullptr, two ? 2 : 1};
-    if (a.dx && a.dw) return product_tc_both<T>(dx, to_dx, dw, to_dw, p.parts, stream);
-    if (a.dx) return product_tc<T>(dx, p.parts, to_dx, stream);
-    return a.dw ? product_tc<T>(dw, p.parts, to_dw, stream) : cudaSuccess;
+    return product_tc_both<T>(dx, to_dx, a.dx, dw, to_dw, a.dw, p.parts, stream);
 }
 
 constexpr int64_t kMostDim = (int64_t)1 << 30, kMostRows = ((int64_t)1 << 30) + 1;

@@ -732,7 +732,45 @@ struct TcSize {
                 if (cost(w) < 0.97 * cost(best)) best = w;
         return best;
     }
+    TcWay split(int splits) const  // the terms in so many parts: how wide
+    {
+        TcWay best = {even(), splits};
+        for (TcWay w = best; w.width >= 96; w.width -= 32)
+            if (may(w) && cost(w) < 0.97 * cost(best)) best = w;
+        return best;
+    }
 };
+
+// The ways of two products, neither of which needs the other, in one launch, and whether the second has the longer sums.
+struct TcBoth {
+    TcWay way[2];
+    bool turned;
+};
+
+inline TcBoth best_of_both(const TcSize (&size)[2])
+{
+    const int width[2] = {size[0].even(), size[1].even()};
+    int alone[2];
+    for (int i = 0; i < 2; ++i) {
+        TcWay best = {width[i], 1};
+        for (TcWay w = best; size[i].may(w); ++w.splits)
+            if (size[i].cost(w) < 0.97 * size[i].cost(best)) best = w;
+        alone[i] = best.splits;
+    }
+    TcBoth best = {};
+    double least = -1.0;
+    for (int i = 0; i < 9; ++i) {  // each whole, as it would be alone, and half of that
+        const TcWay way[2] = {{width[0], i % 3 == 0 ? 1 : (alone[0] + i % 3 - 1) / (i % 3)},
+                              {width[1], i / 3 == 0 ? 1 : (alone[1] + i / 3 - 1) / (i / 3)}};
+        const double unit[2] = {size[0].unit(way[0]), size[1].unit(way[1])};
+        const int a = unit[1] > unit[0], b = !a;  // the longer sums first
+        const TcShares shares(kPairs, size[a].tiles(width[a]) * way[a].splits, (int64_t)(unit[a] * 1000),
+                              size[b].tiles(width[b]) * way[b].splits, (int64_t)(unit[b] * 1000));
+        const double cost = shares.blocks / 1000.0 + 2.0 + size[0].join(way[0]) + size[1].join(way[1]);
+        if (least < 0.0 || cost < 0.98 * least) least = cost, best = {{way[0], way[1]}, a != 0};
+    }
+    return best;
+}
 
 inline int64_t parts_elements(int64_t m, int64_t n)  // of a workspace
 {
@@ -783,45 +821,32 @@ template <typename T, typename Epi> cudaError_t product_tc(const TcProduct& x, f
 }
 
 // Two products, neither of which needs the other, in one launch, so that the units of one fill the SMs that the
-// other's last ones leave idle. parts: room for both's parts_elements, the first's first.
+// other's last ones leave idle; or the one of them that is wanted (the other's operands may be missing), whose terms are
+// split as beside the other, so that its sums are the same. parts: room for both's parts_elements, the first's first.
 template <typename T, typename Epi>
-cudaError_t product_tc_both(const TcProduct& x, const Epi& epi_x, const TcProduct& y, const Epi& epi_y, float* parts, cudaStream_t stream)
+cudaError_t product_tc_both(const TcProduct& x, const Epi& epi_x, bool want_x, const TcProduct& y, const Epi& epi_y, bool want_y,
+                            float* parts, cudaStream_t stream)
 {
     const TcProduct* const product[2] = {&x, &y};
     const Epi* const epi[2] = {&epi_x, &epi_y};
     const TcSize size[2] = {size_of<T, Epi>(x), size_of<T, Epi>(y)};
     float* const room[2] = {parts, parts + parts_elements(x.m, x.n)};
-    const int width[2] = {size[0].even(), size[1].even()};
-    int alone[2];
-    for (int i = 0; i < 2; ++i) {
-        TcWay best = {width[i], 1};
-        for (TcWay w = best; size[i].may(w); ++w.splits)
-            if (size[i].cost(w) < 0.97 * size[i].cost(best)) best = w;
-        alone[i] = best.splits;
-    }
-    TcWay best[2] = {{width[0], 1}, {width[1], 1}};
-    bool turned = false;
-    double least = -1.0;
-    for (int i = 0; i < 9; ++i) {  // each whole, as it would be alone, and half of that
-        const TcWay way[2] = {{width[0], i % 3 == 0 ? 1 : (alone[0] + i % 3 - 1) / (i % 3)},
-                              {width[1], i / 3 == 0 ? 1 : (alone[1] + i / 3 - 1) / (i / 3)}};
-        const double unit[2] = {size[0].unit(way[0]), size[1].unit(way[1])};
-        const int a = unit[1] > unit[0], b = !a;  // the longer sums first
-        const TcShares shares(kPairs, size[a].tiles(width[a]) * way[a].splits, (int64_t)(unit[a] * 1000),
-                              size[b].tiles(width[b]) * way[b].splits, (int64_t)(unit[b] * 1000));
-        const double cost = shares.blocks / 1000.0 + 2.0 + size[0].join(way[0]) + size[1].join(way[1]);
-        if (least < 0.0 || cost < 0.98 * least) least = cost, best[0] = way[0], best[1] = way[1], turned = a;
+    const TcBoth best = best_of_both(size);
+    if (!want_x || !want_y) {
+        const int i = want_y;
+        return want_x || want_y ? product_tc<T>(*product[i], size[i].split(best.way[i].splits), room[i], *epi[i], stream) : cudaSuccess;
     }
     TcMaps maps = {};
     TcParams<Epi> p = {};
     for (int i = 0; i < 2; ++i) {
         const TcProduct& g = *product[i];
-        const cudaError_t e = set_tc<T>(maps, p, turned ? !i : i, g, width[i], best[i].splits, best[i].splits > 1 ? to_parts(*epi[i], room[i], g) : *epi[i]);
+        const TcWay way = best.way[i];
+        const cudaError_t e = set_tc<T>(maps, p, best.turned ? !i : i, g, way.width, way.splits, way.splits > 1 ? to_parts(*epi[i], room[i], g) : *epi[i]);
         if (e != cudaSuccess) return e;
     }
     cudaError_t e = launch_tc<true>(maps, p, stream);
     for (int i = 0; i < 2 && e == cudaSuccess; ++i)
-        if (best[i].splits > 1) e = join_parts(joining(room[i], *product[i], best[i].splits), *epi[i], stream);
+        if (best.way[i].splits > 1) e = join_parts(joining(room[i], *product[i], best.way[i].splits), *epi[i], stream);
     return e;
 }
 

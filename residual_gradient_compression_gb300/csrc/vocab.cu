@@ -470,8 +470,7 @@ template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, c
         to_dx.n = to_dw.n = (int32_t)a.dim;
         const TcProduct dx = {dz, here, false, true, a.rows, a.dim, n, p.count, nullptr, grad.two ? 2 : 1};
         const TcProduct dw = {dz, x, true, true, n, a.dim, a.rows, nullptr, p.count, grad.two ? 2 : 1};
-        if (a.dx && a.dw) e = product_tc_both<T>(dx, to_dx, dw, to_dw, p.parts, stream);
-        else e = a.dx ? product_tc<T>(dx, p.parts, to_dx, stream) : product_tc<T>(dw, p.parts, to_dw, stream);
+        e = product_tc_both<T>(dx, to_dx, a.dx, dw, to_dw, a.dw, p.parts, stream);
     }
     return e;
 }
