@@ -51,6 +51,7 @@ struct TcArgs {
     int32_t run;                       // blocks of terms whose sums are formed in tensor memory
     int32_t width;                     // columns of a tile
     int32_t group;                     // tiles of rows that are taken before the next column's
+    int32_t least;                     // blocks of terms whose time a tile's end takes
 };
 
 struct PackArgs {
@@ -215,6 +216,12 @@ __device__ __forceinline__ void read_wait() { asm volatile("tcgen05.wait::ld.syn
 
 }  // namespace tc
 
+constexpr double kTcBlock = 0.32;  // us, by estimate: a block of terms and 256 columns, per pass
+// A tile's end, which goes on while the next one's sums are formed: where pairs have several units, none is counted as
+// shorter than that (64 rows' gradients of 2048 x 8192 bf16 85 us without this, a few pairs having most of dw's tiles, and
+// 31 so; the gradients of 32 rows against 50304 tokens 540 and 286).
+constexpr double kTcEnd = 4.0;
+
 // The pairs of planes of fp32 operands whose products are summed, the smallest first. Of a bf16 product A may
 // have two planes, of which the second is what the first leaves of it.
 constexpr int kSix = 6;
@@ -275,7 +282,13 @@ template <bool kBoth> struct TcSchedule {
             units[i] = tiles[i] * g[i].splits;
         }
         if constexpr (kBoth) {
-            const TcShares shares(pairs, units[0], (int64_t)per_split[0] * g[0].width, units[1], (int64_t)per_split[1] * g[1].width);
+            int64_t unit[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int32_t least = units[0] + units[1] > pairs ? g[i].least : 0;
+                unit[i] = (int64_t)(per_split[i] > least ? per_split[i] : least) * g[i].width;
+            }
+            const TcShares shares(pairs, units[0], unit[0], units[1], unit[1]);
             more = (int32_t)shares.more;
             few = (int32_t)shares.few;
             many = (int32_t)shares.many;
@@ -682,6 +695,7 @@ cudaError_t set_tc(TcMaps& maps, TcParams<Epi>& p, int i, const TcProduct& x, in
     g.a_mn = x.a_mn;
     g.b_mn = x.b_mn;
     g.group = 8;
+    g.least = (int32_t)(kTcEnd / (kTcBlock * g.passes)) + 1;
     g.run = sizeof(T) == 4 ? 4 : Epi::kExact ? 8 : 1 << 30;
     p.g[i] = g;
     p.epi[i] = epi;
@@ -698,8 +712,6 @@ cudaError_t set_tc(TcMaps& maps, TcParams<Epi>& p, int i, const TcProduct& x, in
 // and with 256 columns and whole sums: the logits of 512 rows over 50304 tokens 75 and 84; a layer's gradients
 // 3001 x 1001 x 777 fp32 102 and 111.
 constexpr int64_t kPairs = 76, kMostParts = 2 * kPairs;  // tiles x splits are at most kMostParts, if split
-constexpr double kTcBlock = 0.32;
-
 struct TcWay {
     int width, splits;
 };
@@ -762,10 +774,12 @@ inline TcBoth best_of_both(const TcSize (&size)[2])
     for (int i = 0; i < 9; ++i) {  // each whole, as it would be alone, and half of that
         const TcWay way[2] = {{width[0], i % 3 == 0 ? 1 : (alone[0] + i % 3 - 1) / (i % 3)},
                               {width[1], i / 3 == 0 ? 1 : (alone[1] + i / 3 - 1) / (i / 3)}};
-        const double unit[2] = {size[0].unit(way[0]), size[1].unit(way[1])};
+        const int64_t units[2] = {size[0].tiles(width[0]) * way[0].splits, size[1].tiles(width[1]) * way[1].splits};
+        double unit[2] = {size[0].unit(way[0]), size[1].unit(way[1])};
+        for (double& u : unit)
+            if (units[0] + units[1] > kPairs && u < kTcEnd) u = kTcEnd;
         const int a = unit[1] > unit[0], b = !a;  // the longer sums first
-        const TcShares shares(kPairs, size[a].tiles(width[a]) * way[a].splits, (int64_t)(unit[a] * 1000),
-                              size[b].tiles(width[b]) * way[b].splits, (int64_t)(unit[b] * 1000));
+        const TcShares shares(kPairs, units[a], (int64_t)(unit[a] * 1000), units[b], (int64_t)(unit[b] * 1000));
         const double cost = shares.blocks / 1000.0 + 2.0 + size[0].join(way[0]) + size[1].join(way[1]);
         if (least < 0.0 || cost < 0.98 * least) least = cost, best = {{way[0], way[1]}, a != 0};
     }
