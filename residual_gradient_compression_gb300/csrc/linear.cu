@@ -33,23 +33,6 @@ struct LinearParts {  // of a pass's workspace
     float* parts;           // of products whose terms are split
 };
 
-LinearParts linear_parts(Carve& c, int64_t rows, int64_t in, int64_t out, int bytes, bool backward)
-{
-    LinearParts p = {};
-    p.x = c.take<bf16>(packed_elements(rows, in, bytes));
-    p.w = c.take<bf16>(packed_elements(out, in, bytes));
-    int64_t most = parts_elements(rows, out);
-    if (backward) {
-        p.sums = c.take<float>(kDzSlices * out);
-        // in two parts, or as fp32 numbers, of few rows
-        const int64_t few = packed_elements(2 * (rows < kFewRows ? rows : kFewRows), out, bytes), all = packed_elements(rows, out, bytes);
-        p.dz = c.take<bf16>(few > all ? few : all);
-        most = parts_elements(rows, in) + parts_elements(out, in);
-    }
-    p.parts = c.take<float>(most);
-    return p;
-}
-
 // Which products are for the kernel of small matrices, by what its whole tiles of 32 x 32 and 128 terms compute.
 // us with it and without: fp32 256 x 512 x 512 12 and 17, 512 x 512 x 512 17 and 17, 2048 x 2048 of one term 66
 // and 14; bf16 256 x 256 x 256 7 and 10, 128 x 512 x 512 12 and 9.
@@ -61,6 +44,38 @@ template <typename T> bool is_small(int64_t m, int64_t n, int64_t k)
     n = at_least(n, kSmallTile);
     k = at_least(k, kSmallDepth);
     return m <= most / n && m * n <= most / k;
+}
+template <typename T> bool both_small(int64_t rows, int64_t in, int64_t out) { return is_small<T>(rows, in, out) && is_small<T>(out, in, rows); }
+template <typename T> constexpr int64_t few_of() { return sizeof(T) == 2 ? kFewBf16 : kFewF32; }
+
+// What the kernels of few rows and of small matrices do not use is not in it: of fewer rows a pass takes those if it
+// does of more, so that a workspace for more rows is enough for fewer.
+template <typename T> LinearParts linear_parts(Carve& c, int64_t rows, int64_t in, int64_t out, bool backward)
+{
+    constexpr int bytes = sizeof(T);
+    LinearParts p = {};
+    if (backward) {
+        p.sums = c.take<float>(kDzSlices * out);
+        // in two parts, or as fp32 numbers, of few rows
+        const int64_t few = packed_elements(2 * (rows < kFewRows ? rows : kFewRows), out, bytes), all = packed_elements(rows, out, bytes);
+        p.dz = c.take<bf16>(few > all ? few : all);
+        if (both_small<T>(rows, in, out)) return p;
+    } else if (rows <= few_of<T>() || is_small<T>(rows, out, in)) {
+        c.take<float>(1);  // sizes are not 0
+        return p;
+    }
+    p.x = c.take<bf16>(packed_elements(rows, in, bytes));
+    p.w = c.take<bf16>(packed_elements(out, in, bytes));
+    p.parts = c.take<float>(backward ? parts_elements(rows, in) + parts_elements(out, in) : parts_elements(rows, out));
+    return p;
+}
+
+inline size_t linear_bytes(int32_t dtype, int64_t rows, int64_t in, int64_t out, bool backward)
+{
+    Carve c;
+    if (dtype == ADACOMP_BF16) linear_parts<bf16>(c, rows, in, out, backward);
+    else linear_parts<float>(c, rows, in, out, backward);
+    return c.at;
 }
 
 struct DzArgs {
@@ -205,12 +220,12 @@ template <typename T> cudaError_t linear_forward(const LinearArgs& a, void* ws, 
     epi.act = a.act;
     epi.whole = whole_rows(a.y, a.y_stride, a.rows, sizeof(T)) && whole_rows(a.pre, a.pre_stride, a.rows, sizeof(T)) &&
                 is_aligned(a.bias, 16) && whole_rows(a.residual, a.residual_stride, a.rows, sizeof(T));
-    if (a.rows <= (sizeof(T) == 2 ? kFewBf16 : kFewF32))
+    if (a.rows <= few_of<T>())
         return product_few<T>(FewArgs{a.x, a.w, a.x_stride, a.w_stride, (int32_t)a.rows, (int32_t)a.out, (int32_t)a.in}, epi, stream);
     if (is_small<T>(a.rows, a.out, a.in))
         return product_small<T, T>(SmallArgs{{a.x, a.x_stride, 1}, {a.w, a.w_stride, 1}, (int32_t)a.rows, (int32_t)a.out, (int32_t)a.in}, epi, stream);
     Carve carve{static_cast<char*>(ws)};
-    const LinearParts p = linear_parts(carve, a.rows, a.in, a.out, sizeof(T), false);
+    const LinearParts p = linear_parts<T>(carve, a.rows, a.in, a.out, false);
     Matrix x, w;
     cudaError_t e = take_matrix<T>(&x, a.x, a.x_stride, a.rows, a.in, p.x, stream);
     if (e == cudaSuccess) e = take_matrix<T>(&w, a.w, a.w_stride, a.out, a.in, p.w, stream);
@@ -222,8 +237,8 @@ template <typename T> cudaError_t linear_forward(const LinearArgs& a, void* ws, 
 template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws, cudaStream_t stream)
 {
     Carve carve{static_cast<char*>(ws)};
-    const LinearParts p = linear_parts(carve, a.rows, a.in, a.out, sizeof(T), true);
-    const bool act = a.act != ADACOMP_ACT_NONE, products = a.dx || a.dw, small = is_small<T>(a.rows, a.in, a.out) && is_small<T>(a.out, a.in, a.rows);
+    const LinearParts p = linear_parts<T>(carve, a.rows, a.in, a.out, true);
+    const bool act = a.act != ADACOMP_ACT_NONE, products = a.dx || a.dw, small = both_small<T>(a.rows, a.in, a.out);
     const bool two = sizeof(T) == 2 && act && a.rows <= kFewRows;
     cudaError_t e = cudaSuccess;
     Matrix dz = {p.dz, a.rows, a.out, pitch_of(a.out), a.rows * pitch_of(a.out)}, x, w;
@@ -317,18 +332,12 @@ adacomp_status adacomp_linear_init(adacomp_linear_t* out, int64_t in_dim, int64_
 
 size_t adacomp_linear_forward_ws_bytes(adacomp_linear_t h, int64_t rows)
 {
-    if (!h || rows < 0 || rows >= adacomp::kMostRows) return 0;
-    adacomp::Carve c;
-    adacomp::linear_parts(c, rows, h->in, h->out, adacomp::dtype_bytes(h->dtype), false);
-    return c.at;
+    return h && rows >= 0 && rows < adacomp::kMostRows ? adacomp::linear_bytes(h->dtype, rows, h->in, h->out, false) : 0;
 }
 
 size_t adacomp_linear_backward_ws_bytes(adacomp_linear_t h, int64_t rows)
 {
-    if (!h || rows < 0 || rows >= adacomp::kMostRows) return 0;
-    adacomp::Carve c;
-    adacomp::linear_parts(c, rows, h->in, h->out, adacomp::dtype_bytes(h->dtype), true);
-    return c.at;
+    return h && rows >= 0 && rows < adacomp::kMostRows ? adacomp::linear_bytes(h->dtype, rows, h->in, h->out, true) : 0;
 }
 
 adacomp_status adacomp_linear_forward(adacomp_linear_t h, int64_t rows, const void* x, int64_t x_stride, const void* w,
