@@ -533,8 +533,9 @@ void adacomp_adamw_free(adacomp_adamw_t h);
  * in an order that depends on sizes and alignment alone, not on which outputs are asked for (over a vocabulary the terms
  * of dw are the rows that have a loss, so there it depends on which they are), and round or truncate each partial sum.
  *
- * The kernels wait for their own copies and products. Such a wait is bounded by 2 s; on expiry the call
- * still ends, and the results that it had not computed are NaN. Nothing traps.
+ * The kernels of larger products wait for their own copies and products. Such a wait is bounded (below); each is
+ * ended by what its own pair of CTAs does, so none is expected to run out. On expiry the call still ends as usual,
+ * with the status ADACOMP_OK that it returned, and the results that it had not computed are NaN. Nothing traps.
  * ------------------------------------------------------------------------------ */
 
 /* A linear layer from in_dim to out_dim (each 1..2^30), all of its tensors of one dtype:
@@ -575,6 +576,14 @@ adacomp_status adacomp_linear_backward(adacomp_linear_t h, int64_t rows, const v
                                        const void* x, int64_t x_stride, const void* w, int64_t w_stride,
                                        const void* pre, int64_t pre_stride, void* dx, int64_t dx_stride, void* dw,
                                        int64_t dw_stride, void* db, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The bound of the waits, in nanoseconds (1 to 6e10, default 2e9), begun after some 17 ms of tries, of the calls made with the
+ * handle from then on. Not to be set while another host thread calls with the handle. */
+adacomp_status adacomp_linear_set_timeout_ns(adacomp_linear_t h, uint64_t timeout_ns);
+
+/* Fault injection for tests of that bound (not part of the operator): the given CTA (0 or 1) of every pair copies
+ * nothing, so that the pair's waits run out. 0xFFFFFFFF switches it off (the default). Nothing faults or hangs. */
+adacomp_status adacomp_linear_set_fault_injection(adacomp_linear_t h, uint32_t silent_cta);
 void adacomp_linear_free(adacomp_linear_t h);
 
 /* A vocabulary of `vocab` tokens (1..2^30) with weights w[vocab][dim] (dim 1..2^30), and the losses of
@@ -636,6 +645,10 @@ adacomp_status adacomp_distill_backward(adacomp_vocab_t h, int64_t rows, const v
                                         float temperature, const float* lse, const float* dloss, int64_t dloss_stride,
                                         void* dx, int64_t dx_stride, void* dw, int64_t dw_stride, void* ws,
                                         size_t ws_bytes, cudaStream_t stream);
+
+/* As adacomp_linear_set_timeout_ns and adacomp_linear_set_fault_injection. */
+adacomp_status adacomp_vocab_set_timeout_ns(adacomp_vocab_t h, uint64_t timeout_ns);
+adacomp_status adacomp_vocab_set_fault_injection(adacomp_vocab_t h, uint32_t silent_cta);
 void adacomp_vocab_free(adacomp_vocab_t h);
 
 /* Releases the handle. adacomp_free(NULL) does nothing. */

@@ -108,6 +108,10 @@ def lib() -> ctypes.CDLL:
             getattr(L, f"adacomp_{name}").restype = ctypes.c_int
             size = getattr(L, f"adacomp_{name}_ws_bytes")
             size.argtypes, size.restype = [vp, i64] + more, sz
+        for kind in ("linear", "vocab"):
+            for name, value in (("set_timeout_ns", u64), ("set_fault_injection", ctypes.c_uint32)):
+                call = getattr(L, f"adacomp_{kind}_{name}")
+                call.argtypes, call.restype = [vp, value], ctypes.c_int
         for name in ("adacomp_layer_norm_free", "adacomp_recurrence_free", "adacomp_adamw_free", "adacomp_linear_free",
                      "adacomp_vocab_free"):
             getattr(L, name).argtypes = [vp]
@@ -664,6 +668,16 @@ def adacomp_linear_backward(h, dy, x, w, ws, pre=None, dx=None, dw=None, db=None
         _array(db, n, t, "db"), _ptr(ws), _nbytes(ws), _stream(stream)), "adacomp_linear_backward")
 
 
+def adacomp_linear_set_timeout_ns(h, ns: int):
+    """Bound on a wait within a product; results behind one that runs out are NaN."""
+    _check(lib().adacomp_linear_set_timeout_ns(h.ptr, ns), "adacomp_linear_set_timeout_ns")
+
+
+def adacomp_linear_set_fault_injection(h, silent_cta: int = 0xFFFFFFFF):
+    """Test hook: the given CTA (0 or 1) of every pair copies nothing, so that the pair's waits run out."""
+    _check(lib().adacomp_linear_set_fault_injection(h.ptr, silent_cta), "adacomp_linear_set_fault_injection")
+
+
 def adacomp_linear_free(h):
     h.__del__()
 
@@ -755,6 +769,16 @@ def adacomp_distill_backward(h, x, w, index, logit, temperature: float, lse, dlo
         h.ptr, rows, *operands, *_teacher(index, logit, rows), temperature, _array(lse, rows, torch.float32, "lse"),
         *_dloss(dloss, rows), *_vocab_gradients(h, rows, dx, dw), _ptr(ws), _nbytes(ws), _stream(stream)),
         "adacomp_distill_backward")
+
+
+def adacomp_vocab_set_timeout_ns(h, ns: int):
+    """As adacomp_linear_set_timeout_ns."""
+    _check(lib().adacomp_vocab_set_timeout_ns(h.ptr, ns), "adacomp_vocab_set_timeout_ns")
+
+
+def adacomp_vocab_set_fault_injection(h, silent_cta: int = 0xFFFFFFFF):
+    """As adacomp_linear_set_fault_injection."""
+    _check(lib().adacomp_vocab_set_fault_injection(h.ptr, silent_cta), "adacomp_vocab_set_fault_injection")
 
 
 def adacomp_vocab_free(h):

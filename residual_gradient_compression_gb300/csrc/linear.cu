@@ -8,6 +8,7 @@
 struct adacomp_linear {
     int64_t in = 0, out = 0;
     int32_t dtype = ADACOMP_F32, act = ADACOMP_ACT_NONE;
+    adacomp::TcWaits waits;
 };
 
 namespace adacomp {
@@ -25,6 +26,7 @@ struct LinearArgs {
     const void *x, *w, *bias, *residual, *dy, *pre_in;
     void *y, *pre, *dx, *dw, *db;
     int64_t x_stride, w_stride, residual_stride, dy_stride, pre_in_stride, y_stride, pre_stride, dx_stride, dw_stride;
+    TcWaits waits;
 };
 
 struct LinearParts {  // of a pass's workspace
@@ -230,7 +232,7 @@ template <typename T> cudaError_t linear_forward(const LinearArgs& a, void* ws, 
     cudaError_t e = take_matrix<T>(&x, a.x, a.x_stride, a.rows, a.in, p.x, stream);
     if (e == cudaSuccess) e = take_matrix<T>(&w, a.w, a.w_stride, a.out, a.in, p.w, stream);
     if (e != cudaSuccess) return e;
-    const TcProduct product = {x, w, false, false, a.rows, a.out, a.in, nullptr, nullptr};
+    const TcProduct product = {x, w, false, false, a.rows, a.out, a.in, nullptr, nullptr, 1, a.waits};
     return product_tc<T>(product, p.parts, epi, stream);
 }
 
@@ -298,8 +300,8 @@ template <typename T> cudaError_t linear_backward(const LinearArgs& a, void* ws,
     if (a.dx && e == cudaSuccess) e = take_matrix<T>(&w, a.w, a.w_stride, a.out, a.in, p.w, stream);
     if (a.dw && e == cudaSuccess) e = take_matrix<T>(&x, a.x, a.x_stride, a.rows, a.in, p.x, stream);
     if (e != cudaSuccess) return e;
-    const TcProduct dx = {dz, w, false, true, a.rows, a.in, a.out, nullptr, nullptr, two ? 2 : 1};
-    const TcProduct dw = {dz, x, true, true, a.out, a.in, a.rows, nullptr, nullptr, two ? 2 : 1};
+    const TcProduct dx = {dz, w, false, true, a.rows, a.in, a.out, nullptr, nullptr, two ? 2 : 1, a.waits};
+    const TcProduct dw = {dz, x, true, true, a.out, a.in, a.rows, nullptr, nullptr, two ? 2 : 1, a.waits};
     return product_tc_both<T>(dx, to_dx, a.dx, dw, to_dw, a.dw, p.parts, stream);
 }
 
@@ -361,6 +363,7 @@ adacomp_status adacomp_linear_forward(adacomp_linear_t h, int64_t rows, const vo
     a.in = h->in;
     a.out = h->out;
     a.act = h->act;
+    a.waits = h->waits;
     a.x = x;
     a.w = w;
     a.bias = bias;
@@ -399,6 +402,7 @@ adacomp_status adacomp_linear_backward(adacomp_linear_t h, int64_t rows, const v
     a.in = h->in;
     a.out = h->out;
     a.act = h->act;
+    a.waits = h->waits;
     a.dy = dy;
     a.x = x;
     a.w = w;
@@ -415,6 +419,18 @@ adacomp_status adacomp_linear_backward(adacomp_linear_t h, int64_t rows, const v
     const cudaError_t err = h->dtype == ADACOMP_BF16 ? adacomp::linear_backward<adacomp::bf16>(a, ws, stream)
                                                      : adacomp::linear_backward<float>(a, ws, stream);
     return adacomp::launch_result(err, stream);
+}
+
+adacomp_status adacomp_linear_set_timeout_ns(adacomp_linear_t h, uint64_t timeout_ns)
+{
+    return h ? adacomp::set_timeout(h->waits, timeout_ns) : ADACOMP_ERR_INVALID_ARG;
+}
+
+adacomp_status adacomp_linear_set_fault_injection(adacomp_linear_t h, uint32_t silent_cta)
+{
+    if (!h) return ADACOMP_ERR_INVALID_ARG;
+    h->waits.silent = silent_cta;
+    return ADACOMP_OK;
 }
 
 void adacomp_linear_free(adacomp_linear_t h) { delete h; }

@@ -27,7 +27,13 @@ constexpr int kTcEpilogue = 4;       // the epilogue's first warp
 constexpr int kTcDepth = 64;         // terms of a stage: 128 bytes of bf16
 constexpr int kTcM = 256;            // rows of a pair's tile
 constexpr int kTcN = 256;            // and columns, at most: a multiple of 32
-constexpr uint64_t kTcLimit = 2000000000ull;  // ns: of every wait
+
+// How long a wait goes on after its first tries (some 17 ms), and a CTA of every pair that makes no copies
+// (0 or 1; tests only).
+struct TcWaits {
+    uint64_t limit_ns = 2000000000ull;
+    uint32_t silent = 0xffffffffu;
+};
 
 constexpr int kTcStageA = 128 * kTcDepth * 2, kTcStageB = kTcN / 2 * kTcDepth * 2;  // bytes of a CTA's stage
 constexpr int kTcStages = 196608 / (kTcStageA + kTcStageB);
@@ -138,12 +144,12 @@ __device__ __forceinline__ void arrive_at(uint32_t bar)  // an address of the cl
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// A wait bounded in time; false when it ran out, here or in another warp (dead).
-// The clock is looked at after many tries only: a look takes longer than most waits.
-__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* dead)
+// A wait bounded in time; false when it ran out, here or in another warp (dead). A try that fails takes 4 us, and the
+// clock is looked at after many tries only.
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* dead, uint64_t limit)
 {
     const uint64_t from = ptx::globaltimer();
-    while (!*dead && ptx::globaltimer() - from <= kTcLimit) {
+    while (!*dead && ptx::globaltimer() - from <= limit) {
         for (int i = 0; i < 64; ++i)
             if (ptx::mbar_try_wait(bar, parity)) return true;
     }
@@ -151,12 +157,12 @@ __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volati
     return false;
 }
 
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead)
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead, uint64_t limit)
 {
 #pragma unroll 1
     for (int i = 0; i < 4096; ++i)
         if (ptx::mbar_try_wait(bar, parity)) return true;
-    return wait_long(bar, parity, dead);
+    return wait_long(bar, parity, dead, limit);
 }
 
 __device__ __forceinline__ void load(uint32_t to, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint32_t bar)
@@ -237,6 +243,7 @@ struct TcMaps {
 template <typename Epi> struct TcParams {
     TcArgs g[2];
     Epi epi[2];
+    TcWaits waits;
 };
 
 // What each pair of CTAs does when two products are computed at once: of the first one's units (tiles, or parts
@@ -333,6 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     __shared__ uint32_t tmem_at;
     __shared__ int dead_flag;
     volatile int* dead = &dead_flag;
+    const uint64_t limit = params.waits.limit_ns;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
@@ -387,23 +395,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                     for (int pass = 0; pass < passes && alive; ++pass) {
                         const int pa = passes == kSix ? plane_a(pass) : passes - 1 - pass, pb = passes == kSix ? plane_b(pass) : 0;
                         for (int32_t k = from; k < end; ++k) {
-                            alive = __all_sync(0xffffffffu, tc::wait(&empty[at_stage], turn ^ 1, dead));
+                            alive = __all_sync(0xffffffffu, tc::wait(&empty[at_stage], turn ^ 1, dead, limit));
                             if (!alive) break;
                             const uint32_t bar = full_at + at_stage * 8, at = base + at_stage * (kTcStageA + kTcStageB);
                             const int32_t k0 = (t.from + k) * kTcDepth;
                             if (tc::elect()) {
                                 if (rank == 0) ptx::mbar_arrive_expect_tx(&full[at_stage], 2 * bytes);
-                                if (g.a_mn) {
+                                if (rank != params.waits.silent) {
+                                    if (g.a_mn) {
 #pragma unroll
-                                    for (int i = 0; i < 2; ++i) tc::load(at + i * 8192, map_a, ma + 64 * i, k0, pa, bar);
-                                } else {
-                                    tc::load(at, map_a, k0, ma, pa, bar);
-                                }
-                                if (g.b_mn) {
-                                    tc::load(at + kTcStageA, map_b, nb, k0, pb, bar);
-                                    if (g.width > 128) tc::load(at + kTcStageA + 8192, map_b, nb + 64, k0, pb, bar);
-                                } else {
-                                    tc::load(at + kTcStageA, map_b, k0, nb, pb, bar);
+                                        for (int i = 0; i < 2; ++i) tc::load(at + i * 8192, map_a, ma + 64 * i, k0, pa, bar);
+                                    } else {
+                                        tc::load(at, map_a, k0, ma, pa, bar);
+                                    }
+                                    if (g.b_mn) {
+                                        tc::load(at + kTcStageA, map_b, nb, k0, pb, bar);
+                                        if (g.width > 128) tc::load(at + kTcStageA + 8192, map_b, nb + 64, k0, pb, bar);
+                                    } else {
+                                        tc::load(at + kTcStageA, map_b, k0, nb, pb, bar);
+                                    }
                                 }
                             }
                             ++issued;
@@ -416,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 int none = 0;
                 if (rank == 0) {
                     for (uint32_t i = issued > kTcStages ? issued - kTcStages : 0; i < issued; ++i)
-                        tc::wait(&full[i % kTcStages], i / kTcStages & 1, &none);
+                        tc::wait(&full[i % kTcStages], i / kTcStages & 1, &none, limit);
                 } else {  // their barrier is the other CTA's: 10 ms
                     const uint64_t from = ptx::globaltimer();
                     while (ptx::globaltimer() - from < 10000000ull) {}
@@ -436,13 +446,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 const uint64_t first_b = tc::descriptor(base + kTcStageA, g.b_mn ? 8192 : 16, 1024);
                 for (int32_t from = 0; from < t.count && alive; from += g.run) {
                     const int buffer = (int)(done & 1);
-                    alive = __all_sync(0xffffffffu, tc::wait(&sums_empty[buffer], (done / 2 & 1) ^ 1, dead));
+                    alive = __all_sync(0xffffffffu, tc::wait(&sums_empty[buffer], (done / 2 & 1) ^ 1, dead, limit));
                     if (!alive) break;
                     tc::fence_after();
                     const uint32_t d = tmem + buffer * 256;
                     const int32_t all = (t.count - from < g.run ? t.count - from : g.run) * passes;
                     for (int32_t i = 0; i < all; ++i) {
-                        alive = __all_sync(0xffffffffu, tc::wait(&full[at_stage], turn, dead));
+                        alive = __all_sync(0xffffffffu, tc::wait(&full[at_stage], turn, dead, limit));
                         if (!alive) break;
                         tc::fence_after();
                         const uint32_t at = at_stage * ((kTcStageA + kTcStageB) >> 4);
@@ -462,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             if (!alive) {  // the products in flight end before the tensor memory is given back
                 int none = 0;
                 if (tc::elect()) tc::commit(&drained);
-                tc::wait(&drained, 0, &none);
+                tc::wait(&drained, 0, &none, limit);
             }
         }
     } else {
@@ -493,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
             for (int32_t from = 0; from < t.count; from += g.run, ++done) {
                 const int buffer = (int)(done & 1);
-                alive = __all_sync(0xffffffffu, alive && tc::wait(&sums_full[buffer], done / 2 & 1, dead));
+                alive = __all_sync(0xffffffffu, alive && tc::wait(&sums_full[buffer], done / 2 & 1, dead, limit));
                 if (!alive) break;
                 tc::fence_after();
 #pragma unroll
@@ -541,6 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             }
         }
     }
+    __syncwarp();  // lanes that left a wait one by one
     __syncthreads();
     tc::cluster_sync();
     if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
@@ -677,7 +688,15 @@ struct TcProduct {
     int64_t m, n, k;
     const int32_t *m_count, *k_count;
     int parts = 1;  // bf16: of A
+    TcWaits waits = {};
 };
+
+inline adacomp_status set_timeout(TcWaits& waits, uint64_t timeout_ns)
+{
+    if (timeout_ns == 0 || timeout_ns > 60000000000ull) return ADACOMP_ERR_INVALID_ARG;
+    waits.limit_ns = timeout_ns;
+    return ADACOMP_OK;
+}
 
 template <typename T, typename Epi>
 cudaError_t set_tc(TcMaps& maps, TcParams<Epi>& p, int i, const TcProduct& x, int width, int splits, const Epi& epi)
@@ -699,6 +718,7 @@ cudaError_t set_tc(TcMaps& maps, TcParams<Epi>& p, int i, const TcProduct& x, in
     g.run = sizeof(T) == 4 ? 4 : Epi::kExact ? 8 : 1 << 30;
     p.g[i] = g;
     p.epi[i] = epi;
+    p.waits = x.waits;
     const cudaError_t e = tensor_map(&maps.a[i], x.a, planes_a, x.a_mn ? kTcDepth : 128);
     return e == cudaSuccess ? tensor_map(&maps.b[i], x.b, planes_b, x.b_mn ? kTcDepth : width / 2) : e;
 }

@@ -7,6 +7,7 @@
 struct adacomp_vocab {
     int64_t dim = 0, vocab = 0;
     int32_t dtype = ADACOMP_F32;
+    adacomp::TcWaits waits;
 };
 
 namespace adacomp {
@@ -35,6 +36,7 @@ struct VocabArgs {
     int64_t dloss_stride;
     void *dx, *dw;
     int64_t dx_stride, dw_stride;
+    TcWaits waits;
 };
 
 struct VocabParts {
@@ -465,7 +467,7 @@ template <typename T> cudaError_t vocab_forward(const VocabArgs& a, void* ws, cu
     epi.lists = {p.index, p.q, p.map, a.k};
     epi.row_stride = a.rows;
     epi.scale = 1.0f / a.temperature;
-    const TcProduct product = {x, w, false, false, a.rows, a.vocab, a.dim, p.count, nullptr};
+    const TcProduct product = {x, w, false, false, a.rows, a.vocab, a.dim, p.count, nullptr, 1, a.waits};
     const TcWay way = size_of<T, EpiSoftmax<T>>(product).best();
     e = product_tc<T>(product, way, nullptr, epi, stream);
     if (e != cudaSuccess) return e;
@@ -514,7 +516,7 @@ template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, c
         const Matrix here = {w.p + at * w.stride, n, a.dim, w.stride, w.plane}, dz = {p.dz, p.padded, n, p.dz_stride, grad.plane};
         grad.n = (int32_t)n;
         grad.first = (int32_t)at;
-        const TcProduct logits = {x, here, false, false, a.rows, n, a.dim, p.count, nullptr};
+        const TcProduct logits = {x, here, false, false, a.rows, n, a.dim, p.count, nullptr, 1, a.waits};
         e = product_tc<T>(logits, nullptr, grad, stream);
         if (e != cudaSuccess) break;
         EpiStore<T> to_dx = {}, to_dw = {};
@@ -531,8 +533,8 @@ template <typename T> cudaError_t vocab_backward(const VocabArgs& a, void* ws, c
         to_dw.first = to_dw.last = true;
         to_dw.whole = whole_rows(a.dw, a.dw_stride, a.vocab, sizeof(T));
         to_dx.n = to_dw.n = (int32_t)a.dim;
-        const TcProduct dx = {dz, here, false, true, a.rows, a.dim, n, p.count, nullptr, grad.two ? 2 : 1};
-        const TcProduct dw = {dz, x, true, true, n, a.dim, a.rows, nullptr, p.count, grad.two ? 2 : 1};
+        const TcProduct dx = {dz, here, false, true, a.rows, a.dim, n, p.count, nullptr, grad.two ? 2 : 1, a.waits};
+        const TcProduct dw = {dz, x, true, true, n, a.dim, a.rows, nullptr, p.count, grad.two ? 2 : 1, a.waits};
         e = product_tc_both<T>(dx, to_dx, a.dx, dw, to_dw, a.dw, p.parts, stream);
     }
     return e;
@@ -569,6 +571,7 @@ adacomp_status vocab_pass(adacomp_vocab_t h, VocabArgs& a, bool backward, void* 
 {
     a.dim = h->dim;
     a.vocab = h->vocab;
+    a.waits = h->waits;
     if (a.rows > 0) {
         const adacomp_status s = vocab_check(h, a, ws);
         if (s != ADACOMP_OK) return s;
@@ -746,6 +749,18 @@ adacomp_status adacomp_distill_backward(adacomp_vocab_t h, int64_t rows, const v
     a.dw_stride = dw_stride;
     if (!adacomp::teacher_fits(a)) return ADACOMP_ERR_INVALID_ARG;
     return adacomp::vocab_pass(h, a, true, ws, ws_bytes, stream);
+}
+
+adacomp_status adacomp_vocab_set_timeout_ns(adacomp_vocab_t h, uint64_t timeout_ns)
+{
+    return h ? adacomp::set_timeout(h->waits, timeout_ns) : ADACOMP_ERR_INVALID_ARG;
+}
+
+adacomp_status adacomp_vocab_set_fault_injection(adacomp_vocab_t h, uint32_t silent_cta)
+{
+    if (!h) return ADACOMP_ERR_INVALID_ARG;
+    h->waits.silent = silent_cta;
+    return ADACOMP_OK;
 }
 
 void adacomp_vocab_free(adacomp_vocab_t h) { delete h; }
