@@ -120,14 +120,14 @@ template <typename T> struct Eight {
 };
 
 // dz = dy * act'(pre), and its sums over slices of the rows. Bound by memory: a thread has eight columns of every
-// kDzRows-th row of a slice, several rows under way at a time; the CTA's sums meet in shared memory, the slices' in a
+// kRowsOfCta-th row of a slice, several rows under way at a time; the CTA's sums meet in shared memory, the slices' in a
 // second kernel, in a fixed order.
-template <typename T, int kAct, int kDzRows> __device__ __forceinline__ void dz_rows(const DzArgs& a, int32_t c, float (&sum)[8])
+template <typename T, int kAct, int kRowsOfCta> __device__ __forceinline__ void dz_rows(const DzArgs& a, int32_t c, float (&sum)[8])
 {
     constexpr int kAhead = sizeof(T) == 2 ? 3 : 2;
     const T *dy = static_cast<const T*>(a.dy) + c, *pre = static_cast<const T*>(a.pre) + c;
-    const int64_t left = a.n - c, step = (int64_t)a.slices * kDzRows;
-    for (int64_t r0 = blockIdx.y * kDzRows + threadIdx.y; r0 < a.rows; r0 += kAhead * step) {
+    const int64_t left = a.n - c, step = (int64_t)a.slices * kRowsOfCta;
+    for (int64_t r0 = blockIdx.y * kRowsOfCta + threadIdx.y; r0 < a.rows; r0 += kAhead * step) {
         Eight<T> v[kAhead], z[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -160,31 +160,31 @@ template <typename T, int kAct, int kDzRows> __device__ __forceinline__ void dz_
     }
 }
 
-template <typename T, int kDzCols, int kDzRows>
-__global__ void __launch_bounds__(kDzCols / 8 * kDzRows, sizeof(T) == 2 ? 4 : 3) linear_dz_kernel(const DzArgs a)
+template <typename T, int kColsOfCta, int kRowsOfCta>
+__global__ void __launch_bounds__(kColsOfCta / 8 * kRowsOfCta, sizeof(T) == 2 ? 4 : 3) linear_dz_kernel(const DzArgs a)
 {
-    __shared__ float sums[kDzRows][kDzCols];
+    __shared__ float sums[kRowsOfCta][kColsOfCta];
     ptx::griddep_wait();
     ptx::griddep_launch();
-    const int32_t c = blockIdx.x * kDzCols + threadIdx.x * 8;
+    const int32_t c = blockIdx.x * kColsOfCta + threadIdx.x * 8;
     float sum[8] = {};
     if (c < a.n) switch (a.act) {
-        case ADACOMP_ACT_RELU: dz_rows<T, ADACOMP_ACT_RELU, kDzRows>(a, c, sum); break;
-        case ADACOMP_ACT_GELU: dz_rows<T, ADACOMP_ACT_GELU, kDzRows>(a, c, sum); break;
-        case ADACOMP_ACT_GELU_TANH: dz_rows<T, ADACOMP_ACT_GELU_TANH, kDzRows>(a, c, sum); break;
-        case ADACOMP_ACT_SILU: dz_rows<T, ADACOMP_ACT_SILU, kDzRows>(a, c, sum); break;
-        default: dz_rows<T, ADACOMP_ACT_NONE, kDzRows>(a, c, sum);
+        case ADACOMP_ACT_RELU: dz_rows<T, ADACOMP_ACT_RELU, kRowsOfCta>(a, c, sum); break;
+        case ADACOMP_ACT_GELU: dz_rows<T, ADACOMP_ACT_GELU, kRowsOfCta>(a, c, sum); break;
+        case ADACOMP_ACT_GELU_TANH: dz_rows<T, ADACOMP_ACT_GELU_TANH, kRowsOfCta>(a, c, sum); break;
+        case ADACOMP_ACT_SILU: dz_rows<T, ADACOMP_ACT_SILU, kRowsOfCta>(a, c, sum); break;
+        default: dz_rows<T, ADACOMP_ACT_NONE, kRowsOfCta>(a, c, sum);
         }
     if (!a.sums && !a.db) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sums[threadIdx.y][threadIdx.x * 8 + j] = sum[j];
     __syncthreads();
-    const int i = threadIdx.y * (kDzCols / 8) + threadIdx.x;
-    const int64_t at = (int64_t)blockIdx.x * kDzCols + i;
-    if (i >= kDzCols || at >= a.n) return;
+    const int i = threadIdx.y * (kColsOfCta / 8) + threadIdx.x;
+    const int64_t at = (int64_t)blockIdx.x * kColsOfCta + i;
+    if (i >= kColsOfCta || at >= a.n) return;
     float s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kDzRows; ++j) s += sums[j][i];
+    for (int j = 0; j < kRowsOfCta; ++j) s += sums[j][i];
     if (a.db) static_cast<T*>(a.db)[at] = from_f32<T>(s);
     else a.sums[blockIdx.y * a.n + at] = s;
 }

@@ -108,7 +108,7 @@ struct ListArgs {
     const int32_t* index;
     const void* logit;
     int64_t rows, vocab, index_stride, logit_stride;
-    int32_t target_bytes, logit_dtype, k;
+    int32_t target_bytes, k;
     float scale;
     int32_t* to_index;
     float *to_q, *given;
@@ -416,7 +416,6 @@ template <typename T> cudaError_t vocab_rows(const VocabArgs& a, const VocabPart
     l.index_stride = a.index_stride;
     l.logit_stride = a.logit_stride;
     l.target_bytes = a.target_bytes;
-    l.logit_dtype = a.logit_dtype;
     l.k = a.k;
     l.scale = 1.0f / a.temperature;
     l.to_index = p.index;
