@@ -403,7 +403,8 @@ template <typename T, int kKind> __device__ __forceinline__ float slope(float z)
     } else if constexpr (kKind == ADACOMP_ACT_GELU_TANH) {  // s = (1 + tanh u) / 2: s + 2 z s (1 - s) du/dz
         const float u = 0.79788456f * (z + 0.044715f * z * z * z);
         const float s = kQuick ? quick_sigmoid(2.0f * u) : 1.0f / (1.0f + expf(-2.0f * u));
-        return s * (1.0f + z * (1.0f - s) * 1.5957691f * (1.0f + 0.134145f * z * z));
+        const float c = fmaxf(fminf(z, 100.0f), -100.0f);  // where s is 0 or 1, and z z might overflow
+        return s * (1.0f + c * (1.0f - s) * 1.5957691f * (1.0f + 0.134145f * c * c));
     } else if constexpr (kKind == ADACOMP_ACT_SILU) {
         const float g = kQuick ? quick_sigmoid(z) : 1.0f / (1.0f + expf(-z));
         return g * (1.0f + z * (1.0f - g));

@@ -55,3 +55,22 @@ def test_far_below_zero(rows, kind, lowest, dt):
         over = ((got.double() - ref).abs() - bound).max(0).values if got.dim() > 1 else (got.double() - ref).abs() - bound
         at = int(over.argmax())
         assert float(over.max()) <= 0, (name, float(z[at]), got[..., at].flatten()[:1].tolist(), float(ref[at]))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("rows", [1, 300])
+def test_far_from_zero(rows, kind, dt):
+    """Values whose squares or cubes overflow: the activation is z or 0, its slope 1 or 0."""
+    z = torch.tensor([s * 10.0 ** e for s in (1, -1) for e in (3, 6, 10, 14, 19, 20, 30, 38)], device="cuda").to(dt).repeat(64)
+    n = z.numel()
+    h = ac.adacomp_linear_init(1, n, ac.BF16 if dt == BF16 else ac.F32, getattr(ac, "ACT_" + kind.upper()))
+    x, w = torch.ones(rows, 1, dtype=dt, device="cuda"), z[:, None].contiguous()
+    y, pre = (torch.full((rows, n), math.nan, dtype=dt, device="cuda") for _ in range(2))
+    ac.adacomp_linear_forward(h, x, w, y, workspace(ac.adacomp_linear_forward_ws_bytes(h, rows)), pre=pre)
+    on = (z > 0) | (kind == "none")
+    assert torch.equal(y, torch.where(on, z, 0.0).expand_as(y))
+    dy, db = torch.zeros_like(y), torch.full((n,), math.nan, dtype=dt, device="cuda")
+    dy[rows // 2] = 1.0
+    ac.adacomp_linear_backward(h, dy, x, w, workspace(ac.adacomp_linear_backward_ws_bytes(h, rows)), pre=pre, db=db)
+    assert torch.equal(db, on.to(dt))
