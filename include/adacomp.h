@@ -527,7 +527,8 @@ void adacomp_adamw_free(adacomp_adamw_t h);
  * first copied into the workspace. Workspaces are 16-byte aligned, need no initialisation, and
  * serve one call at a time.
  *
- * bf16 products are exact and summed in fp32. fp32 numbers are, but in small products, split into three
+ * bf16 products are exact and summed in fp32; the tensor cores cut off a partial sum's last bits every 16 terms, so where
+ * results are fp32 they sum runs of up to 512 terms, which are added up. fp32 numbers are, but in small products, split into three
  * bf16 numbers that add up to them (what is below 2^-126 may be lost), and of the nine products of
  * parts the six largest are summed, which leaves out less than 2^-22 of a product. Sums add the terms
  * in an order that depends on sizes and alignment alone, not on which outputs are asked for (over a vocabulary the terms
@@ -540,7 +541,8 @@ void adacomp_adamw_free(adacomp_adamw_t h);
 
 /* A linear layer from in_dim to out_dim (each 1..2^30), all of its tensors of one dtype:
  *     z = x w^T + bias,  y = act(z) + residual,   w[out_dim][in_dim].
- * Activations, of fp32 z: relu(z) = max(z, 0) (slope 0 at 0); gelu(z) = z (1 + erf(z / sqrt 2)) / 2;
+ * Activations, of fp32 z (of bf16 layers by quick functions, off by no more than 2^-12 of the value and 2^-20 of z):
+ * relu(z) = max(z, 0) (slope 0 at 0); gelu(z) = z (1 + erf(z / sqrt 2)) / 2;
  * gelu_tanh(z) = z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2; silu(z) = z / (1 + exp(-z)).
  * Host only. */
 typedef enum {
@@ -568,9 +570,8 @@ adacomp_status adacomp_linear_forward(adacomp_linear_t h, int64_t rows, const vo
 
 /* From dy, with dz = dy * act'(pre) (dy itself without an activation; pre may then be NULL):
  *     dx = dz w,  dw = dz^T x,  db = sum over rows of dz;   the residual's gradient is dy.
- * For the products dz is rounded to bf16 where dtype is bf16 (of up to 32 rows, taken in two parts); db is summed from
- * the unrounded dz. dx, dw and
- * db may each be NULL (not wanted; x is needed for dw only, w for dx only) and are overwritten
+ * For the products dz is rounded to bf16 where dtype is bf16 (in calls of up to 32 rows, taken in two parts); db is summed
+ * from the unrounded dz. dx, dw and db may each be NULL (not wanted; x is needed for dw only, w for dx only) and are overwritten
  * (dw and db with zeros for 0 rows). */
 adacomp_status adacomp_linear_backward(adacomp_linear_t h, int64_t rows, const void* dy, int64_t dy_stride,
                                        const void* x, int64_t x_stride, const void* w, int64_t w_stride,
@@ -611,8 +612,8 @@ adacomp_status adacomp_vocab_loss_forward(adacomp_vocab_t h, int64_t rows, const
 /* The gradients, from the gradient dloss of loss (device fp32; row r's is dloss[r * dloss_stride], so 0 is one
  * value for all rows; not used for rows without a loss):
  *     dz = (exp(z - lse) - [v = target]) * dloss,  dx = dz w,  dw = dz^T x.
- * For the products dz is rounded to bf16 where dtype is bf16 (of up to 32 rows, taken in two
- * parts). dx and dw may each be NULL (not both) and are overwritten: dx is 0
+ * For the products dz is rounded to bf16 where dtype is bf16 (in calls of up to 32 rows,
+ * with a loss or without, taken in two parts). dx and dw may each be NULL (not both) and are overwritten: dx is 0
  * in rows without a loss, dw is 0 if no row has one. A target of vocab or more makes the row's
  * dx, and dw, NaN. */
 adacomp_status adacomp_vocab_loss_backward(adacomp_vocab_t h, int64_t rows, const void* x, int64_t x_stride,
