@@ -522,9 +522,9 @@ void adacomp_adamw_free(adacomp_adamw_t h);
 /* ------------------------------------------------------------------------------
  * Linear layers and losses over a vocabulary: the matrix products of a training step. The
  * conventions of the training operators above hold. Matrices are strided by rows: inputs
- * by any stride >= 0 (0: one row read for all), outputs by at least a row; up to 2^30 rows. With 16-byte aligned
- * pointers and row strides that are multiples of 16 bytes they are used as they lie; others are
- * first copied into the workspace. Workspaces are 16-byte aligned, need no initialisation, and
+ * by any stride >= 0 (0: one row read for all), outputs by at least a row; up to 2^30 rows. Products of few rows and
+ * small ones read them as they lie, larger ones bf16 matrices with 16-byte aligned pointers and rows that are multiples
+ * of 16 bytes, and no less than a row, apart; others, and hidden states, are first copied into the workspace. Workspaces are 16-byte aligned, need no initialisation, and
  * serve one call at a time.
  *
  * bf16 products are exact and summed in fp32; the tensor cores cut off a partial sum's last bits every 16 terms, so where
