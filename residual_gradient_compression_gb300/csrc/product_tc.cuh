@@ -383,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         if (warp == 0) {  // copies
             uint32_t at_stage = 0, turn = 0, issued = 0;
             const uint32_t full_at = tc::map_shared(full, 0);  // the first CTA's
-            bool alive = true;
+            bool alive = rank != params.waits.silent;
             for (int32_t u = 0; alive && schedule.at(params.g, u, t); ++u) {
                 const TcArgs& g = params.g[kBoth ? t.which : 0];
                 const CUtensorMap *map_a = &maps.a[kBoth ? t.which : 0], *map_b = &maps.b[kBoth ? t.which : 0];
@@ -401,19 +401,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                             const int32_t k0 = (t.from + k) * kTcDepth;
                             if (tc::elect()) {
                                 if (rank == 0) ptx::mbar_arrive_expect_tx(&full[at_stage], 2 * bytes);
-                                if (rank != params.waits.silent) {
-                                    if (g.a_mn) {
+                                if (g.a_mn) {
 #pragma unroll
-                                        for (int i = 0; i < 2; ++i) tc::load(at + i * 8192, map_a, ma + 64 * i, k0, pa, bar);
-                                    } else {
-                                        tc::load(at, map_a, k0, ma, pa, bar);
-                                    }
-                                    if (g.b_mn) {
-                                        tc::load(at + kTcStageA, map_b, nb, k0, pb, bar);
-                                        if (g.width > 128) tc::load(at + kTcStageA + 8192, map_b, nb + 64, k0, pb, bar);
-                                    } else {
-                                        tc::load(at + kTcStageA, map_b, k0, nb, pb, bar);
-                                    }
+                                    for (int i = 0; i < 2; ++i) tc::load(at + i * 8192, map_a, ma + 64 * i, k0, pa, bar);
+                                } else {
+                                    tc::load(at, map_a, k0, ma, pa, bar);
+                                }
+                                if (g.b_mn) {
+                                    tc::load(at + kTcStageA, map_b, nb, k0, pb, bar);
+                                    if (g.width > 128) tc::load(at + kTcStageA + 8192, map_b, nb + 64, k0, pb, bar);
+                                } else {
+                                    tc::load(at + kTcStageA, map_b, k0, nb, pb, bar);
                                 }
                             }
                             ++issued;
