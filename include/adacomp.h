@@ -524,12 +524,12 @@ void adacomp_adamw_free(adacomp_adamw_t h);
  * conventions of the training operators above hold. Matrices are strided by rows: inputs
  * by any stride >= 0 (0: one row read for all), outputs by at least a row; up to 2^30 rows. Products of few rows and
  * small ones read them as they lie, larger ones bf16 matrices with 16-byte aligned pointers and rows that are multiples
- * of 16 bytes, and no less than a row, apart; others, and hidden states, are first copied into the workspace. Workspaces are 16-byte aligned, need no initialisation, and
- * serve one call at a time.
+ * of 16 bytes, and no less than a row, apart; others, and hidden states, are first copied into the workspace. Workspaces
+ * are 16-byte aligned, need no initialisation, and serve one call at a time.
  *
  * bf16 products are exact and summed in fp32; the tensor cores cut off a partial sum's last bits every 16 terms, so where
- * results are fp32 they sum runs of up to 512 terms, which are added up. fp32 numbers are, but in small products, split into three
- * bf16 numbers that add up to them (what is below 2^-126 may be lost), and of the nine products of
+ * results are fp32 they sum runs of up to 512 terms, which are added up. fp32 numbers are, but in small products, split
+ * into three bf16 numbers that add up to them (what is below 2^-126 may be lost), and of the nine products of
  * parts the six largest are summed, which leaves out less than 2^-22 of a product. Sums add the terms
  * in an order that depends on sizes and alignment alone, not on which outputs are asked for (over a vocabulary the terms
  * of dw are the rows that have a loss, so there it depends on which they are), and round or truncate each partial sum.

@@ -75,3 +75,35 @@ def test_the_time_grows_as_the_rows_do():
             least = min(least, start.elapsed_time(end))
         times.append(least)
     assert times[1] < 7 * times[0], times
+
+
+def test_a_graph_replayed_with_other_rows():
+    """The number of rows with a loss, and which, are read when the graph runs."""
+    rows = 40_000
+    x, w, target, g, h = _case(rows)
+    none = torch.rand(rows, generator=g, device="cuda") < 0.3
+    wanted = torch.where(none, -1, target)
+    ws = workspace(max(ac.adacomp_vocab_loss_forward_ws_bytes(h, rows), ac.adacomp_vocab_loss_backward_ws_bytes(h, rows)))
+    loss, lse, one = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.ones(1, device="cuda")
+    dx, dw, now = torch.empty_like(x), torch.empty_like(w), torch.full_like(target, -1)
+
+    def step():
+        ac.adacomp_vocab_loss_forward(h, x, w, now, loss, lse, ws)
+        ac.adacomp_vocab_loss_backward(h, x, w, now, lse, one, ws, dx=dx, dw=dw)
+
+    results = []
+    for values in (wanted, target):
+        now.copy_(values)
+        step()
+        results.append([t.clone() for t in (loss, lse, dx, dw)])
+    now.fill_(-1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    graph.replay()
+    assert not loss.any() and not dx.any() and not dw.any()
+    for values, want in zip((wanted, target), results):
+        now.copy_(values)
+        graph.replay()
+        for a, b in zip((loss, lse, dx, dw), want):
+            assert torch.equal(a, b)
