@@ -602,6 +602,50 @@ size_t vocab_bytes(adacomp_vocab_t h, int64_t rows, int32_t k, bool backward)
     return c.at;
 }
 
+// The entry points' arguments, those of each kind together.
+VocabArgs vocab_args(int64_t rows, const void* x, int64_t x_stride, const void* w, int64_t w_stride)
+{
+    VocabArgs a = {};
+    a.rows = rows;
+    a.x = x;
+    a.x_stride = x_stride;
+    a.w = w;
+    a.w_stride = w_stride;
+    return a;
+}
+
+void set_target(VocabArgs& a, const void* target, int32_t target_bytes)
+{
+    a.target = target;
+    a.target_bytes = target_bytes;
+    a.k = 1;
+    a.temperature = 1.0f;
+}
+
+void set_teacher(VocabArgs& a, int32_t k, const int32_t* index, int64_t index_stride, const void* logit, int64_t logit_stride,
+                 int32_t logit_dtype, float temperature)
+{
+    a.k = k;
+    a.index = index;
+    a.index_stride = index_stride;
+    a.logit = logit;
+    a.logit_stride = logit_stride;
+    a.logit_dtype = logit_dtype;
+    a.temperature = temperature;
+}
+
+void set_gradients(VocabArgs& a, const float* lse, const float* dloss, int64_t dloss_stride, void* dx, int64_t dx_stride, void* dw,
+                   int64_t dw_stride)
+{
+    a.lse = lse;
+    a.dloss = dloss;
+    a.dloss_stride = dloss_stride;
+    a.dx = dx;
+    a.dx_stride = dx_stride;
+    a.dw = dw;
+    a.dw_stride = dw_stride;
+}
+
 bool target_fits(const VocabArgs& a)
 {
     return (a.target_bytes == 4 || a.target_bytes == 8) && (a.rows == 0 || a.target);
@@ -645,16 +689,8 @@ adacomp_status adacomp_vocab_loss_forward(adacomp_vocab_t h, int64_t rows, const
 {
     adacomp::TrainRange range("adacomp_vocab_loss_forward");
     if (!h || rows < 0 || rows >= adacomp::kMostRows) return ADACOMP_ERR_INVALID_ARG;
-    adacomp::VocabArgs a = {};
-    a.rows = rows;
-    a.x = x;
-    a.x_stride = x_stride;
-    a.w = w;
-    a.w_stride = w_stride;
-    a.target = target;
-    a.target_bytes = target_bytes;
-    a.k = 1;
-    a.temperature = 1.0f;
+    adacomp::VocabArgs a = adacomp::vocab_args(rows, x, x_stride, w, w_stride);
+    adacomp::set_target(a, target, target_bytes);
     a.loss = loss;
     a.lse_out = lse;
     if (!adacomp::target_fits(a)) return ADACOMP_ERR_INVALID_ARG;
@@ -669,23 +705,9 @@ adacomp_status adacomp_vocab_loss_backward(adacomp_vocab_t h, int64_t rows, cons
 {
     adacomp::TrainRange range("adacomp_vocab_loss_backward");
     if (!h || rows < 0 || rows >= adacomp::kMostRows) return ADACOMP_ERR_INVALID_ARG;
-    adacomp::VocabArgs a = {};
-    a.rows = rows;
-    a.x = x;
-    a.x_stride = x_stride;
-    a.w = w;
-    a.w_stride = w_stride;
-    a.target = target;
-    a.target_bytes = target_bytes;
-    a.k = 1;
-    a.temperature = 1.0f;
-    a.lse = lse;
-    a.dloss = dloss;
-    a.dloss_stride = dloss_stride;
-    a.dx = dx;
-    a.dx_stride = dx_stride;
-    a.dw = dw;
-    a.dw_stride = dw_stride;
+    adacomp::VocabArgs a = adacomp::vocab_args(rows, x, x_stride, w, w_stride);
+    adacomp::set_target(a, target, target_bytes);
+    adacomp::set_gradients(a, lse, dloss, dloss_stride, dx, dx_stride, dw, dw_stride);
     if (!adacomp::target_fits(a)) return ADACOMP_ERR_INVALID_ARG;
     return adacomp::vocab_pass(h, a, true, ws, ws_bytes, stream);
 }
@@ -698,19 +720,8 @@ adacomp_status adacomp_distill_forward(adacomp_vocab_t h, int64_t rows, const vo
 {
     adacomp::TrainRange range("adacomp_distill_forward");
     if (!h || rows < 0 || rows >= adacomp::kMostRows) return ADACOMP_ERR_INVALID_ARG;
-    adacomp::VocabArgs a = {};
-    a.rows = rows;
-    a.x = x;
-    a.x_stride = x_stride;
-    a.w = w;
-    a.w_stride = w_stride;
-    a.k = k;
-    a.index = index;
-    a.index_stride = index_stride;
-    a.logit = logit;
-    a.logit_stride = logit_stride;
-    a.logit_dtype = logit_dtype;
-    a.temperature = temperature;
+    adacomp::VocabArgs a = adacomp::vocab_args(rows, x, x_stride, w, w_stride);
+    adacomp::set_teacher(a, k, index, index_stride, logit, logit_stride, logit_dtype, temperature);
     a.loss = loss;
     a.lse_out = lse;
     if (!adacomp::teacher_fits(a)) return ADACOMP_ERR_INVALID_ARG;
@@ -726,26 +737,9 @@ adacomp_status adacomp_distill_backward(adacomp_vocab_t h, int64_t rows, const v
 {
     adacomp::TrainRange range("adacomp_distill_backward");
     if (!h || rows < 0 || rows >= adacomp::kMostRows) return ADACOMP_ERR_INVALID_ARG;
-    adacomp::VocabArgs a = {};
-    a.rows = rows;
-    a.x = x;
-    a.x_stride = x_stride;
-    a.w = w;
-    a.w_stride = w_stride;
-    a.k = k;
-    a.index = index;
-    a.index_stride = index_stride;
-    a.logit = logit;
-    a.logit_stride = logit_stride;
-    a.logit_dtype = logit_dtype;
-    a.temperature = temperature;
-    a.lse = lse;
-    a.dloss = dloss;
-    a.dloss_stride = dloss_stride;
-    a.dx = dx;
-    a.dx_stride = dx_stride;
-    a.dw = dw;
-    a.dw_stride = dw_stride;
+    adacomp::VocabArgs a = adacomp::vocab_args(rows, x, x_stride, w, w_stride);
+    adacomp::set_teacher(a, k, index, index_stride, logit, logit_stride, logit_dtype, temperature);
+    adacomp::set_gradients(a, lse, dloss, dloss_stride, dx, dx_stride, dw, dw_stride);
     if (!adacomp::teacher_fits(a)) return ADACOMP_ERR_INVALID_ARG;
     return adacomp::vocab_pass(h, a, true, ws, ws_bytes, stream);
 }
